@@ -553,8 +553,8 @@ def _append_exact(s):
                 x = s["kv"][r:r + n, part].double().transpose(0, 1)
                 a = x.abs().amax(dim=(1, 2))
                 if fmt == "e4m3":
-                    part, up = torch.frexp((a / torch.full_like(a, 448.0)).clamp(min=2.0 ** -126))
-                    up = up.long() - (part == 0.5).long()  # the lowest power of two that is not below a / 448
+                    frac, up = torch.frexp((a / torch.full_like(a, 448.0)).clamp(min=2.0 ** -126))
+                    up = up.long() - (frac == 0.5).long()  # the lowest power of two that is not below a / 448
                     need = torch.where(a > 0, (up + 1023 << 52).view(torch.float64), 0.0)
                 else:
                     need = (a / torch.full_like(a, 127.0)).float().double()
