@@ -18,6 +18,9 @@ namespace {
 __device__ unsigned qg_status_word;
 std::atomic<unsigned*> g_status_ptr[64];  // filled on first use; racing threads store the same value
 
+}  // namespace
+
+namespace qg {
 unsigned* status_ptr() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
@@ -30,8 +33,9 @@ unsigned* status_ptr() {
     }
     return p;
 }
+}  // namespace qg
 
-}  // namespace
+using qg::status_ptr;
 
 // Scratch of qgemv_q4k_pass_noalloc: its per-stage completion counts.  A
 // fixed array in the library's own module, so that the entry point needs no
@@ -356,6 +360,7 @@ int qg_device_status(cudaStream_t stream) {
     if (v != 0 && cudaMemcpyToSymbol(qg_status_word, &zero, sizeof(zero)) != cudaSuccess) return qg::cuda_fail(cudaGetLastError());
     if (v & qg::kStatusTimeout) return QG_ETIMEOUT;
     if (v & qg::kStatusBounds) return QG_EBOUNDS;
+    if (v & qg::kStatusPages) return QG_EPAGES;
     return QG_OK;
 }
 
@@ -385,7 +390,8 @@ const char* qg_strerror(int status) {
         case QG_ETIMEOUT: return "a bounded wait inside a kernel gave up";
         case QG_EBOUNDS: return "an index check inside a kernel failed";
         case QG_EALIAS: return "output overlaps an input";
-        case QG_ESCRATCH: return "more stages than the fixed scratch of qgemv_q4k_pass_noalloc holds";
+        case QG_ESCRATCH: return "more stages than the fixed scratch of qgemv_q4k_pass_noalloc holds, or workspace too small";
+        case QG_EPAGES: return "too few free cache pages";
         default: return "unknown status";
     }
 }

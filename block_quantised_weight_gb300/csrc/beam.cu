@@ -1,0 +1,421 @@
+// Beam selection: the best continuations of each request over its beams and
+// the vocabulary.
+//
+// Mathematics.  score = cum[beam] + x - lse(row), lse = m + log(sum 2^((x - m)
+// log2 e)).  Within a row the order is that of the logits, so a row's part
+// only has to keep its `keep` largest logits, whatever its lse; the scores
+// are formed in 64 bits at the end, from few candidates.
+//
+// Bound.  Every logit is read once: HBM-bound for batches, latency-bound for
+// one request.  A CTA streams a part of a row: the running maximum and sum
+// per thread, and a buffer of candidates in shared memory.  A logit enters
+// the buffer when it is above a threshold that at least `keep` values reach:
+// the keep-th largest of the threads' own maxima, found by counting.  After
+// the first step few values pass, so the selection costs one comparison a
+// logit.  The last CTA of a request to arrive merges the parts; all order is
+// by (value, index), so the result does not depend on who arrives when.
+#include <atomic>
+
+#include "kv_common.cuh"
+#include "launch_common.cuh"
+#include "qgkv_launch.h"
+
+namespace qg {
+namespace {
+
+constexpr int kBeamThreads = 256;
+constexpr int kPer = 8;                            // values a thread takes in one step
+constexpr int kStep = kBeamThreads * kPer;
+constexpr int kKeepLimit = 1024;                   // buffered candidates above which the buffer is thinned
+constexpr int kCap = kKeepLimit + kStep;
+
+// Larger is better; all keys of one selection differ.
+struct Key1 {  // (logit, token): order of the logit's bits, then the lower token
+    unsigned long long a;
+    __device__ static Key1 lowest() { return {0ull}; }
+    __device__ bool operator<(const Key1& o) const { return a < o.a; }
+};
+struct Key2 {  // (score, flat index)
+    unsigned long long a, b;
+    __device__ static Key2 lowest() { return {0ull, 0ull}; }
+    __device__ bool operator<(const Key2& o) const { return a < o.a || (a == o.a && b < o.b); }
+};
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ unsigned long long ordered64(double x) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double unordered64(unsigned long long u) {
+    return __longlong_as_double(static_cast<long long>(u >> 63 ? u & 0x7FFFFFFFFFFFFFFFull : ~u));
+}
+
+// The candidates of a CTA and the threshold below which nothing is kept.
+template <class K>
+struct Pool {
+    K buf[kCap];
+    K top[kBeamThreads];
+    K floor_key;
+    int n;
+
+    __device__ void reset() {
+        if (threadIdx.x == 0) {
+            n = 0;
+            floor_key = K::lowest();
+        }
+        __syncthreads();
+    }
+    // floor_key = the keep-th largest of the threads' keys `mine`
+    __device__ void raise(K mine, int keep) {
+        top[threadIdx.x] = mine;
+        __syncthreads();
+        int above = 0;
+#pragma unroll 8
+        for (int i = 0; i < kBeamThreads; ++i)
+            above += (mine < top[i] || (i < threadIdx.x && !(top[i] < mine))) ? 1 : 0;
+        if (above == keep - 1) floor_key = mine;
+        __syncthreads();
+    }
+    __device__ void push(K k) { buf[atomicAdd(&n, 1)] = k; }
+    // Thin the buffer: every thread's share of it, its largest, the
+    // keep-th largest of those; what is below goes.
+    __device__ void thin(int keep) {
+        constexpr int kShare = kCap / kBeamThreads;
+        K mine[kShare];
+        K best = K::lowest();
+        const int have = n;
+#pragma unroll
+        for (int j = 0; j < kShare; ++j) {
+            const int i = j * kBeamThreads + threadIdx.x;
+            mine[j] = i < have ? buf[i] : K::lowest();
+            if (best < mine[j]) best = mine[j];
+        }
+        raise(best, keep);
+        if (threadIdx.x == 0) n = 0;
+        __syncthreads();
+        const K f = floor_key;
+#pragma unroll
+        for (int j = 0; j < kShare; ++j)
+            if (!(mine[j] < f) && K::lowest() < mine[j]) push(mine[j]);
+        __syncthreads();
+    }
+    // After the last push: calls f(rank, key) for the best `keep`.
+    template <class F>
+    __device__ void finish(int keep, F f) {
+        while (n > 512) {
+            const int was = n;
+            __syncthreads();
+            thin(keep);
+            if (n >= was) break;
+        }
+        const int have = n;
+        for (int i = threadIdx.x; i < have; i += kBeamThreads) {
+            const K k = buf[i];
+            int rank = 0;
+            for (int j = 0; j < have; ++j) rank += k < buf[j] ? 1 : 0;
+            if (rank < keep) f(rank, k);
+        }
+    }
+};
+
+struct BeamArgs {
+    const void* logits;
+    const float* cum;
+    int beams, keep, splits, part_keep;
+    int64_t vocab, row_stride, span;
+    unsigned long long* keys;  // [rows][splits][part_keep]
+    double* sums;              // [rows][splits]
+    float* maxima;             // [rows][splits]
+    unsigned* count;           // [requests]
+    float* scores;
+    int32_t* tokens;
+    int32_t* parents;
+};
+
+// Values at .. at + 7 of a row (at a multiple of 8), -inf outside [0, end).
+// A row may start anywhere (a vocabulary of odd size): off its 16-byte
+// boundary by `words` 32-bit words and `half` a word, it is read in the
+// aligned vectors that hold the eight values, each of which holds at least
+// one of them, and shifted into place.  Which thread sums which tokens thus
+// does not depend on the address: equal rows give equal sums.
+template <class T>
+__device__ __forceinline__ void load8(const T* p, int64_t end, int64_t at, int words, bool half, float (&x)[8]) {
+    constexpr int W = 2 * sizeof(T);  // 32-bit words of eight values
+    if (at + 8 <= end) {
+        uint32_t w[W + 4];
+        const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p + at) & ~uintptr_t(15));
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const uint4 q = ldg_stream16(v + i);
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        }
+        if (words || half) {
+            const uint4 q = ldg_stream16(v + W / 4);
+            w[W] = q.x, w[W + 1] = q.y, w[W + 2] = q.z, w[W + 3] = q.w;
+            if (words & 2)
+#pragma unroll
+                for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+            if (words & 1)
+#pragma unroll
+                for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+            if (half)
+#pragma unroll
+                for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i % W]);
+            } else {
+                const unsigned short h = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
+                x[i] = to_f32(*reinterpret_cast<const T*>(&h));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = at + i < end ? to_f32(p[at + i]) : -INFINITY;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float red_m[kBeamThreads / 32];
+    __shared__ double red_l[kBeamThreads / 32];
+    __shared__ bool last;
+    __shared__ double row_lse[QGKV_MAX_BEAMS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x / a.splits;
+    const int split = static_cast<int>(blockIdx.x - row * a.splits);
+    const T* p = static_cast<const T*>(a.logits) + row * a.row_stride;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const int words = off >> 2;
+    const bool half = (off & 2) != 0;
+    const int64_t lo = split * a.span;
+    const int64_t end = min(lo + a.span, a.vocab);
+
+    Pool<Key1>& pool = *reinterpret_cast<Pool<Key1>*>(smem);
+    pool.reset();
+    float m = -INFINITY, l = 0.f;
+    bool started = false;
+    for (int64_t at0 = lo; at0 < end; at0 += kStep) {
+        const int64_t at = at0 + tid * kPer;
+        float x[kPer];
+        load8(p, end, at, words, half, x);
+        float mx = m;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, x[i]);
+        if (mx > m) {
+            l *= exp2_fast((m - mx) * 1.4426950408889634f);
+            m = mx;
+        }
+        // a thread without a finite maximum keeps l = 0; NaN has to reach l
+        const float ref = m == -INFINITY ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s += exp2_fast((x[i] - ref) * 1.4426950408889634f);
+        l += s;
+        Key1 best = Key1::lowest();
+        Key1 key[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float v = x[i] == x[i] ? x[i] : -INFINITY;
+            const bool real = at + i < end;
+            const uint32_t token = static_cast<uint32_t>(at + i);
+            key[i].a = real ? (static_cast<unsigned long long>(ordered(v)) << 32) | (0xFFFFFFFFu - token) : 0ull;
+            if (best < key[i]) best = key[i];
+        }
+        if (!started) {
+            started = true;
+            pool.raise(best, a.keep);
+            const Key1 f = pool.floor_key;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (!(key[i] < f) && key[i].a) pool.push(key[i]);
+        } else {
+            const Key1 f = pool.floor_key;
+            if (f < best) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (f < key[i]) pool.push(key[i]);
+            }
+        }
+        __syncthreads();
+        while (pool.n > kKeepLimit) {
+            const int was = pool.n;
+            __syncthreads();
+            pool.thin(a.keep);
+            if (pool.n >= was) break;  // not reached: thinning twice leaves at most 6 * keep
+        }
+        __syncthreads();
+    }
+    // the part's maximum and sum (the sum over threads in 64 bits)
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    if (lane == 0) red_m[warp] = M;
+    __syncthreads();
+    for (int w = 0; w < kBeamThreads / 32; ++w) M = fmaxf(M, red_m[w]);
+    double L = m == -INFINITY ? static_cast<double>(l) : static_cast<double>(l) * exp2f((m - M) * 1.4426950408889634f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
+    if (lane == 0) red_l[warp] = L;
+    __syncthreads();
+    const int64_t at_part = row * a.splits + split;
+    if (tid == 0) {
+        L = 0.0;
+        for (int w = 0; w < kBeamThreads / 32; ++w) L += red_l[w];
+        a.maxima[at_part] = M;
+        a.sums[at_part] = L;
+    }
+    unsigned long long* out = a.keys + at_part * a.part_keep;
+    for (int i = tid; i < a.part_keep; i += kBeamThreads)
+        if (i >= pool.n) out[i] = 0ull;  // a part shorter than `keep`
+    pool.finish(a.part_keep, [&](int rank, Key1 k) { out[rank] = k.a; });
+
+    // ---- the request's last part merges
+    const int64_t request = row / a.beams;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const unsigned need = static_cast<unsigned>(a.beams * a.splits);
+        last = atomicAdd(a.count + request, 1u) == need - 1;
+        if (last) a.count[request] = 0u;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    const int64_t row0 = request * a.beams;
+    for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
+        float mm = -INFINITY;
+        for (int s = lane; s < a.splits; s += 32) mm = fmaxf(mm, __ldcg(a.maxima + (row0 + b) * a.splits + s));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+        double sum = 0.0;
+        for (int s = lane; s < a.splits; s += 32) {
+            const float ms = __ldcg(a.maxima + (row0 + b) * a.splits + s);
+            const double ls = __ldcg(a.sums + (row0 + b) * a.splits + s);
+            sum += ms == -INFINITY ? ls : ls * exp2f((ms - mm) * 1.4426950408889634f);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) {
+            const float cb = a.cum[row0 + b];
+            const bool good = sum > 0.0 && sum < 1e300 && mm < INFINITY && mm > -INFINITY && cb < INFINITY && cb > -INFINITY;
+            row_lse[b] = good ? static_cast<double>(mm) + log(sum) : __longlong_as_double(0x7FF8000000000000ll);
+        }
+    }
+    Pool<Key2>& merge = *reinterpret_cast<Pool<Key2>*>(smem);
+    __syncthreads();
+    merge.reset();
+    const int per_row = a.splits * a.part_keep;
+    const int total = a.beams * per_row;
+    started = false;
+    for (int at0 = 0; at0 < total; at0 += kStep) {
+        Key2 key[kPer];
+        Key2 best = Key2::lowest();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = at0 + i * kBeamThreads + tid;
+            key[i] = Key2::lowest();
+            if (e < total) {
+                const int b = e / per_row;
+                const unsigned long long k = __ldcg(a.keys + (row0 + b) * per_row + (e - b * per_row));
+                const double lse = row_lse[b];
+                double score = -INFINITY;
+                int64_t token = e - b * per_row;  // of a row that scores -inf throughout: its first tokens
+                bool real = token < a.vocab;
+                if (lse == lse) {
+                    real = k != 0ull;
+                    token = 0xFFFFFFFFu - static_cast<uint32_t>(k);
+                    score = static_cast<double>(a.cum[row0 + b]) +
+                            (static_cast<double>(unordered(static_cast<uint32_t>(k >> 32))) - lse);
+                }
+                if (real) {
+                    key[i].a = ordered64(score);
+                    key[i].b = 0x7FFFFFFFFFFFFFFFull - static_cast<unsigned long long>(b * a.vocab + token);
+                }
+            }
+            if (best < key[i]) best = key[i];
+        }
+        if (!started) {
+            started = true;
+            merge.raise(best, a.keep);
+        }
+        const Key2 f = merge.floor_key;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (!(key[i] < f) && key[i].a) merge.push(key[i]);
+        __syncthreads();
+        while (merge.n > kKeepLimit) {
+            const int was = merge.n;
+            __syncthreads();
+            merge.thin(a.keep);
+            if (merge.n >= was) break;
+        }
+        __syncthreads();
+    }
+    merge.finish(a.keep, [&](int rank, Key2 k) {
+        const int64_t flat = static_cast<int64_t>(0x7FFFFFFFFFFFFFFFull - k.b);
+        const int64_t b = flat / a.vocab;
+        const int64_t to = request * a.keep + rank;
+        a.scores[to] = static_cast<float>(unordered64(k.a));
+        a.tokens[to] = static_cast<int32_t>(flat - b * a.vocab);
+        a.parents[to] = static_cast<int32_t>(row0 + b);
+    });
+}
+
+template <class T>
+int launch_beam(BeamArgs a, int requests, cudaStream_t s) {
+    const int smem = static_cast<int>(sizeof(Pool<Key2>));
+    const int dev = current_device();
+    static std::atomic<bool> done[64];
+    if (dev < 0) return cuda_fail(cudaGetLastError());
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(qg_beam_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return cuda_fail(cudaGetLastError());
+        done[dev].store(true, std::memory_order_release);
+    }
+    qg_beam_kernel<T><<<static_cast<unsigned>(requests * a.beams * a.splits), kBeamThreads, smem, s>>>(a);
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_beam_select(const void* logits, int type, const float* cum, int requests, int beams, int64_t vocab,
+                       int64_t row_stride, int keep, float* scores, int32_t* tokens, int32_t* parents,
+                       uint8_t* workspace, cudaStream_t s) {
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return cuda_fail(cudaGetLastError());
+    BeamArgs a = {};
+    a.logits = logits, a.cum = cum, a.beams = beams, a.keep = keep, a.vocab = vocab, a.row_stride = row_stride;
+    a.scores = scores, a.tokens = tokens, a.parents = parents;
+    const int64_t rows = static_cast<int64_t>(requests) * beams;
+    // Enough parts for four CTAs an SM, each at least one step long, and no
+    // more than the partial results have room for.
+    int64_t splits = (4 * sms + rows - 1) / rows;
+    splits = std::min(splits, (vocab + kStep - 1) / kStep);
+    const int64_t room = kWsPartBytes - 64;
+    splits = std::max<int64_t>(1, std::min(splits, room / (rows * (keep * 8 + 16))));
+    a.span = ((vocab + splits - 1) / splits + kStep - 1) / kStep * kStep;
+    splits = (vocab + a.span - 1) / a.span;
+    a.splits = static_cast<int>(splits);
+    a.part_keep = static_cast<int>(std::min<int64_t>(keep, vocab));
+    if (rows * splits * (a.part_keep * 8 + 16) > room) return QG_ESCRATCH;
+    uint8_t* part = workspace + kWsPart;
+    a.keys = reinterpret_cast<unsigned long long*>(part);
+    a.sums = reinterpret_cast<double*>(part + rows * splits * a.part_keep * 8);
+    a.maxima = reinterpret_cast<float*>(a.sums + rows * splits);
+    a.count = reinterpret_cast<unsigned*>(workspace + kWsCounters) + kCntBeam;
+    if (type == QGKV_F32) return launch_beam<float>(a, requests, s);
+    if (type == QGKV_F16) return launch_beam<__half>(a, requests, s);
+    return launch_beam<__nv_bfloat16>(a, requests, s);
+}
+
+}  // namespace qg

@@ -16,6 +16,7 @@ namespace qg {
 // Device status bits (returned by qg_device_status as negative codes).
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBounds = 2u;
+constexpr unsigned kStatusPages = 4u;
 
 // A healthy bulk copy lands within microseconds.  A wait that has not seen
 // its phase complete after kWaitLimitNs of wall time gives up.

@@ -25,6 +25,7 @@ QG_ETIMEOUT = -4
 QG_EBOUNDS = -5
 QG_EALIAS = -6
 QG_ESCRATCH = -7
+QG_EPAGES = -8
 QG_MAX_M = 32
 QG_MAX_GROUP = 4
 QG_MAX_PASS_STAGES = 96
