@@ -48,17 +48,41 @@ __device__ __forceinline__ uint32_t hsub2_1152(uint32_t a) {
     return r;
 }
 
-// Four codes (one 32-bit word, lowest byte first) -> two f16x2, exact.  int8:
-// 0x6400 | (code + 128) is the f16 1024 + code + 128, from which 1152 is taken.
+// Four codes of one token (a 32-bit word) as two f16x2 operands, for a product
+// with q.  e4m3: bytes (0, 1) and (2, 3), exact.  int8: bytes (0, 2) and
+// (1, 3) as the f16 subnormals (code + 128) * 2^-24, exact, two operations a
+// pair; the sums then carry 128 * sum(q) too much (kCodeBias), which their
+// initial value takes off.
+constexpr float kCodeBias = -128.f / 16777216.f;
 template <bool INT8>
-__device__ __forceinline__ void codes4_f16(uint32_t x, uint32_t& a, uint32_t& b) {
+__device__ __forceinline__ void k_codes(uint32_t x, uint32_t& a, uint32_t& b) {
     if (INT8) {
-        const uint32_t y = x ^ 0x80808080u;
-        a = hsub2_1152(prmt(y, 0x64646464u, 0x4140u));
-        b = hsub2_1152(prmt(y, 0x64646464u, 0x4342u));
+        a = (x & 0x00FF00FFu) ^ 0x00800080u;
+        b = ((x >> 8) & 0x00FF00FFu) ^ 0x00800080u;
     } else {
         a = e4m3x2_f16x2(x & 0xFFFFu);
         b = e4m3x2_f16x2(x >> 16);
+    }
+}
+
+// Words of two tokens -> four operands (token 0, token 1), one for each byte,
+// exact.  int8: 0x6400 | (code + 128) is the f16 1152 + code.
+template <bool INT8>
+__device__ __forceinline__ void v_codes(uint32_t t0, uint32_t t1, uint32_t (&r)[4]) {
+    if (INT8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t p = prmt(t0, t1, i ? 0x7632u : 0x5410u);
+            r[2 * i] = hsub2_1152((p & 0x00FF00FFu) ^ 0x64806480u);
+            r[2 * i + 1] = hsub2_1152(((p >> 8) & 0x00FF00FFu) ^ 0x64806480u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t p = prmt(t0, t1, i ? 0x7362u : 0x5140u);
+            r[2 * i] = e4m3x2_f16x2(p & 0xFFFFu);
+            r[2 * i + 1] = e4m3x2_f16x2(p >> 16);
+        }
     }
 }
 
@@ -82,6 +106,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values held as a fragment.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -26,6 +26,11 @@ static_assert(QGKV_MAX_PAGES / kChunk <= 4096, "chunk counts exceed the workspac
 
 __device__ __forceinline__ int pages_of(int len, int log2p) { return (len + (1 << log2p) - 1) >> log2p; }
 
+// The planning results lie in the workspace, so an index from there is checked
+// like one from the caller: a workspace that was not zeroed before its first
+// use gives wrong tables and QG_EBOUNDS, never an access outside an array.
+__device__ __forceinline__ bool in_pages(int i, int64_t pages) { return i >= 0 && i < pages; }
+
 // Length of row b cut to the table (kStatusBounds where it does not fit).
 __device__ __forceinline__ int length_of(const int32_t* lens, int64_t b, int64_t width, int log2p, unsigned* status) {
     const int len = lens[b];
@@ -371,12 +376,15 @@ __global__ void __launch_bounds__(kPlanThreads) qg_compact_list_kernel(const Com
         if (q >= a.pages) break;
         if (q < n) {
             if (v[j] > 0) a.refs2[q] = v[j];
-            else a.holes[q - at] = q;
+            else if (in_pages(q - at, a.pages)) a.holes[q - at] = q;
+            else atomicOr(a.status, kStatusBounds);
         } else {
             a.refs2[q] = 0;
             if (v[j] > 0) {
-                a.movers[at - held_below] = q;
-                a.rank[q] = at - held_below;
+                const int i = at - held_below;
+                a.rank[q] = i;
+                if (in_pages(i, a.pages)) a.movers[i] = q;
+                else atomicOr(a.status, kStatusBounds);
             }
         }
         at += v[j] > 0 ? 1 : 0;
@@ -395,16 +403,22 @@ __global__ void __launch_bounds__(256) qg_compact_rows_kernel(const CompactArgs 
             int to = -1;
             if (j < held) {
                 const int id = a.table[b * a.width + j];
-                if (id >= 0 && id < a.pages && a.now[id] > 0) to = id < n ? id : a.holes[a.rank[id]];
-                else atomicOr(a.status, kStatusBounds);
+                if (in_pages(id, a.pages) && a.now[id] > 0) {
+                    if (id < n) to = id;
+                    else if (in_pages(a.rank[id], a.pages)) to = a.holes[a.rank[id]];
+                }
+                if (to < 0) atomicOr(a.status, kStatusBounds);
             }
             a.table2[b * a.width + j] = to;
         }
         if (threadIdx.x == 0) a.lens2[b] = len;
     } else {
-        for (int i = (blockIdx.x - a.batch) * blockDim.x + threadIdx.x; i < moves;
-             i += (gridDim.x - a.batch) * blockDim.x)
-            a.refs2[a.holes[i]] = a.now[a.movers[i]];
+        for (int64_t i = (blockIdx.x - a.batch) * blockDim.x + threadIdx.x; i < moves && i < a.pages;
+             i += (gridDim.x - a.batch) * blockDim.x) {
+            const int to = a.holes[i], from = a.movers[i];
+            if (in_pages(to, a.pages) && in_pages(from, a.pages)) a.refs2[to] = a.now[from];
+            else atomicOr(a.status, kStatusBounds);
+        }
     }
 }
 
