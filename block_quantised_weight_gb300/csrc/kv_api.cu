@@ -31,7 +31,7 @@ int check_cache(const qgkv_cache* c, int64_t layer) {
     if (!page_size_ok(c->page_tokens) || c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16) return QG_EINVAL;
     const int64_t bytes = static_cast<int64_t>(c->heads) * c->page_tokens * c->head_dim;
     if (c->page_stride < bytes || (c->layers > 1 && c->layer_stride < bytes)) return QG_EINVAL;
-    if (c->page_stride > (int64_t(1) << 40) || c->layer_stride > (int64_t(1) << 50) || c->layer_stride < 0)
+    if (c->page_stride >= (int64_t(1) << 40) || c->layer_stride > (int64_t(1) << 50) || c->layer_stride < 0)
         return QG_EINVAL;
     if (off16(c->k) || off16(c->v) || off4(c->k_scale) || off4(c->v_scale) || c->page_stride % 16 ||
         c->layer_stride % 16)

@@ -21,14 +21,14 @@
 // a clock and SM come in).  Both products are formed transposed, tokens by
 // heads (K q^T) and dims by heads (V^T p^T), so that the 16-row operand is the
 // codes and the 8 columns are query rows: group sizes up to 8 fill one column
-// tile, and the codes are converted once for all of them.  The fragments are
-// laid out so that codes go from global memory to registers and into the
-// tensor instruction without shared memory: the order of a head's dims is
-// free in q . k and in the rows of o, so a lane takes 16 dims of one token for
-// K and 8 or 16 dims of four tokens for V, each a whole vector load, each quad
-// or octet a whole row segment.  p leaves the first product as the transpose
-// of what the second takes; movmatrix turns it.  The loads of the next step
-// are issued as soon as the registers of the current one are consumed.
+// tile, and the codes are converted once for all of them.  Each warp streams
+// its own tokens through a ring in shared memory that TMA fills (one box of 16
+// tokens for K and for V, whatever the order of the cache; the swizzle lets
+// every read below meet each bank once), so that bytes in flight cost no
+// registers and no address arithmetic.  The order of a head's dims is free in
+// q . k and in the rows of o: a lane takes 16 dims of one token for K and 8 or
+// 16 dims of four tokens for V, whole vectors each.  p leaves the first
+// product as the transpose of what the second takes; movmatrix turns it.
 //
 // Split.  The tokens of all (sequence, head, row block) are one line of
 // 128-token tiles, cut evenly among the CTAs whatever the lengths; a CTA that
@@ -86,49 +86,85 @@ __device__ __forceinline__ int ceil_ref(float x) {
     return x == -INFINITY ? kNone : static_cast<int>(ceilf(fminf(fmaxf(x, -1.0e8f), 1.0e8f)));
 }
 
+// What the template arguments fix: DC chunks of 64 dims.
+template <int DC, int MT>
+struct Shape {
+    static constexpr int NS = DC <= 2 ? 2 : 1;       // 16-token subtiles of one warp step
+    static constexpr int RU = 8 * MT;                // query rows of a unit
+    static constexpr int DP = 64 * DC;
+    static constexpr int RB = DC == 1 ? 64 : 128;    // bytes of a box row
+    static constexpr int NB = DC == 4 ? 2 : 1;       // boxes of a token row
+    static constexpr int kBox = 16 * RB;
+    static constexpr int kSub = 2 * NB * kBox;       // K and V of a subtile
+    static constexpr int kStage = NS * kSub;
+    static constexpr int S = DC == 1 ? 3 : 2;        // stages of a warp's ring
+    static constexpr int kRing = S * kStage;         // of one warp
+    static_assert(RU * DP * 4 <= kRing, "a warp's result does not fit its ring");
+    // shared memory: rings, queries, log-sums, row data, barriers, sequences and their prefix sums
+    static constexpr int off_q(int) { return 4 * kRing; }
+    static constexpr int off_ws(int parts) { return off_q(parts) + parts * MT * 4 * DC * 32 * 8; }
+    static constexpr int off_rows(int parts) { return off_ws(parts) + 8 * RU * 4; }
+    static constexpr int off_bar(int parts) { return off_rows(parts) + RU * 16; }
+    static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
+};
+
 template <int DC, int MT, int PARTS, bool INT8, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const AttnArgs a, int grid) {
-    constexpr int NS = DC <= 2 ? 2 : 1;    // 16-token subtiles of one warp step
-    constexpr int RU = 8 * MT;             // query rows of a unit
-    constexpr int VW = DC == 1 ? 2 : 4;    // 32-bit words of one V load
-    constexpr int VL = DC == 4 ? 2 : 1;    // V loads per token row
-    constexpr int DP = 64 * DC;
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint2* qf = reinterpret_cast<uint2*>(smem);                       // [PARTS][MT][4 * DC][32]
-    float* wo = reinterpret_cast<float*>(qf + PARTS * MT * 4 * DC * 32);  // [4][RU][DP]
-    float* ws = wo + 4 * RU * DP;                                     // [4][RU] log-sums
-    float* wt = ws + 4 * RU;                                          // [RU] and scratch
-    int64_t* pre = reinterpret_cast<int64_t*>(wt + 2 * RU);           // [batch + 1]
+__global__ void __launch_bounds__(kThreads, MINB)
+qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    int grid) {
+    using F = Shape<DC, MT>;
+    constexpr int NS = F::NS, RU = F::RU, DP = F::DP, S = F::S;
+    constexpr int VW = DC == 1 ? 2 : 4;    // 32-bit words of one V read
+    constexpr int VL = F::NB;              // V reads per token row
+    extern __shared__ __align__(1024) unsigned char smem[];
+    uint2* qf = reinterpret_cast<uint2*>(smem + F::off_q(PARTS));         // [PARTS][MT][4 * DC][32]
+    float* ws = reinterpret_cast<float*>(smem + F::off_ws(PARTS));        // [4][RU] largest |q|, later log-sums
+    float* wb = ws + 4 * RU;                                              // [4][RU] sums of q
+    int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(PARTS));  // [RU] output rows, -1 past the last
+    int* limits = reinterpret_cast<int*>(orow + RU);                      // [RU] tokens that a row sees
+    int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(PARTS));  // [batch + 1]
+    int2* seqs = reinterpret_cast<int2*>(pre + a.batch + 1);              // [batch] rows, length
     __shared__ int64_t warp_sum[4];
     __shared__ int last_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const KVLayer& c = a.c;
+    // this warp's ring of stages and their barriers
+    unsigned char* ring = smem + warp * F::kRing;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + F::off_bar(PARTS)) + warp * S;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(bar + i, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    }
+    __syncwarp();
+    unsigned issued = 0, taken = 0;  // stages over the life of the kernel
 
     // ---- the line: prefix sums of the sequences' tiles
     {
         int64_t base = 0;
         for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
             const int b = b0 + tid;
-            int64_t u = 0;
+            int64_t x = 0;
             if (b < a.batch) {
                 const Seq s = sequence(a, b);
                 const int64_t blocks = (static_cast<int64_t>(s.n) * a.group + RU - 1) / RU;
-                u = blocks * c.heads * max(1, (s.len + kTile - 1) / kTile);
+                x = blocks * c.heads * max(1, (s.len + kTile - 1) / kTile);
+                seqs[b] = make_int2(s.n, s.len);
             }
-            int64_t x = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o) x += y;
             }
+            if (b0) __syncthreads();  // the earlier sums have been read
             if (lane == 31) warp_sum[warp] = x;
             __syncthreads();
             for (int w = 0; w < warp; ++w) x += warp_sum[w];
             if (b < a.batch) pre[b + 1] = base + x;
             base += warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
-            __syncthreads();
         }
         if (tid == 0) pre[0] = 0;
         __syncthreads();
@@ -148,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
         }
         // empty sequences share their successor's prefix: take the last with pre <= u that has tiles
         const int b = lo;
-        const Seq sq = sequence(a, b);
+        const Seq sq = {seqs[b].x, seqs[b].y};
+        const int64_t row0 = a.starts ? a.starts[b] : b;
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];
@@ -168,200 +205,149 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
         const int full_end = min(seen_least, tok1);  // up to here every row sees every token
 
         // ---- the stream of this warp: steps of 16 * NS tokens, 64 * NS apart.
-        // Lane i holds the page and scales of the i-th 16-token subtile.
+        // Lane i holds the page and scales of the i-th 16-token subtile, in the
+        // one or the other of two sets of 32 subtiles: the copies run ahead of
+        // the steps by a stage or two.
         constexpr int step_tok = 64 * NS;
         const int warp_tok = tok0 + warp * 16 * NS;
         const int steps = tok1 > warp_tok ? (tok1 - warp_tok + step_tok - 1) / step_tok : 0;
         const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
-        int id_c = -1;
-        float ks_c = 0.f, vs_c = 0.f;
+        int id_c[2];
+        float ks_c[2], vs_c[2];
         auto refill = [&](int batch32) {
             const int sub = batch32 * 32 + lane;
             const int tok = warp_tok + (sub / NS) * step_tok + (sub % NS) * 16;
-            id_c = -1;
-            ks_c = vs_c = 0.f;
+            int id = -1;
+            float k1 = 0.f, v1 = 0.f;
             if (tok < tok1) {
-                const int id = row_table[tok >> c.log2p];
+                id = row_table[tok >> c.log2p];
                 if (id >= 0 && id < c.pages) {
-                    id_c = id;
                     const int64_t at = static_cast<int64_t>(id) * c.heads + h;
-                    ks_c = __ldg(c.ks + at);
-                    vs_c = __ldg(c.vs + at);
+                    k1 = __ldg(c.ks + at);
+                    v1 = __ldg(c.vs + at);
                 } else {
+                    id = -1;
                     atomicOr(a.status, kStatusBounds);
                 }
             }
+            if (batch32 & 1) id_c[1] = id, ks_c[1] = k1, vs_c[1] = v1;
+            else id_c[0] = id, ks_c[0] = k1, vs_c[0] = v1;
         };
-        uint4 kr[NS][2][DC];
-        uint32_t vr[NS][4][VL][VW];
-        int nid[NS];
-        float nks[NS], nvs[NS];
-        bool nfull = false;
-        // lanes past the head's dims read its last ones: their q is 0, their columns of o are not written
-        const int klane = g * c.token_stride, vlane = 2 * t * c.token_stride;
-        const uint8_t* kbase = c.k + static_cast<int64_t>(h) * c.head_stride;
-        const uint8_t* vbase = c.v + static_cast<int64_t>(h) * c.head_stride;
-        const int pmask = (1 << c.log2p) - 1;
-        auto locate = [&](int it) {  // pages and scales of step `it`
-            if (it > 0 && (it * NS & 31) == 0) refill(it * NS >> 5);
-            const int tok = warp_tok + it * step_tok;
-            nfull = tok + 16 * NS <= full_end;
+        auto issue = [&](int it) {  // fill the next stage with step `it`
+            const int odd = (it * NS >> 5) & 1;
+            if ((it * NS & 31) == 0) refill(it * NS >> 5);
+            const int st = issued % S;
+            int id[NS];
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const int sub = it * NS + s;
-                nid[s] = __shfl_sync(~0u, id_c, sub & 31);
-                nks[s] = __shfl_sync(~0u, ks_c, sub & 31);
-                nvs[s] = __shfl_sync(~0u, vs_c, sub & 31);
-                nfull &= nid[s] >= 0;
-            }
-        };
-        auto load_k_as = [&](int it, auto all) {
+            for (int s = 0; s < NS; ++s) id[s] = __shfl_sync(~0u, odd ? id_c[1] : id_c[0], (it * NS + s) & 31);
+            if (lane == 0) {
+                unsigned bytes = 0;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const int tok = warp_tok + it * step_tok + s * 16;
-                const uint8_t* p = kbase + nid[s] * c.page_stride + ((tok & pmask) * c.token_stride + klane);
+                for (int s = 0; s < NS; ++s) bytes += id[s] >= 0 ? F::kSub : 0;
+                mbar_arrive_expect_tx(bar + st, bytes);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint8_t* pj = p + j * 8 * c.token_stride;
-                    const bool there = all || (nid[s] >= 0 && tok + j * 8 + g < tok1);
+                for (int s = 0; s < NS; ++s)
+                    if (id[s] >= 0) {
+                        const int tok = (warp_tok + it * step_tok + s * 16) & ((1 << c.log2p) - 1);
+                        unsigned char* dst = ring + st * F::kStage + s * F::kSub;
 #pragma unroll
-                    for (int cc = 0; cc < DC; ++cc) {
-                        if (!all) kr[s][j][cc] = make_uint4(0, 0, 0, 0);
-                        if (there) kr[s][j][cc] = ldg_stream16(pj + min(cc * 64 + t * 16, c.dim - 16));
-                    }
-                }
-            }
-        };
-        auto load_k = [&](int it) {
-            if (nfull) load_k_as(it, std::true_type());
-            else load_k_as(it, std::false_type());
-        };
-        auto load_v_as = [&](int it, auto all) {
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const int tok = warp_tok + it * step_tok + s * 16;
-                const uint8_t* p = vbase + nid[s] * c.page_stride + ((tok & pmask) * c.token_stride + vlane);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = (j & 1) + 8 * (j >> 1);
-                    const uint8_t* pj = p + row * c.token_stride;
-                    const bool there = all || (nid[s] >= 0 && tok + row + 2 * t < tok1);
-#pragma unroll
-                    for (int x = 0; x < VL; ++x) {
-                        if (!all)
-#pragma unroll
-                            for (int i = 0; i < VW; ++i) vr[s][j][x][i] = 0;
-                        if (there) {
-                            const uint8_t* at = pj + min(x * 128 + g * (4 * VW), c.dim - 4 * VW);
-                            if (VW == 2) {
-                                const uint2 v = ldg_stream8(at);
-                                vr[s][j][x][0] = v.x, vr[s][j][x][1] = v.y;
-                            } else {
-                                const uint4 v = ldg_stream16(at);
-                                vr[s][j][x][0] = v.x, vr[s][j][x][1] = v.y;
-                                vr[s][j][x][VW - 2] = v.z, vr[s][j][x][VW - 1] = v.w;
-                            }
+                        for (int x = 0; x < F::NB; ++x) {
+                            tma_load_4d(dst + x * F::kBox, &kmap, x * 128, tok, h, id[s], bar + st);
+                            tma_load_4d(dst + (F::NB + x) * F::kBox, &vmap, x * 128, tok, h, id[s], bar + st);
                         }
                     }
-                }
             }
+            ++issued;
+            __syncwarp();
         };
-        auto load_v = [&](int it) {
-            if (nfull) load_v_as(it, std::true_type());
-            else load_v_as(it, std::false_type());
-        };
-        if (steps > 0) {  // on their way while the queries are prepared
-            refill(0);
-            locate(0);
-            load_k(0);
-            load_v(0);
-        }
 
         // ---- queries: the column operand, scaled by a power of two per row.
-        // A lane prepares row g of each tile of 8; the scores it gets are
-        // those of rows 2t and 2t + 1, so their factors come from the lanes
-        // that prepared these.
-        float qfac[MT][2], init[MT][2];
-        int limit[MT][2];  // tokens that the rows see
-        __syncthreads();  // the previous segment's users of qf and wo are done
+        // Warp w takes the w-th four of a lane's 16 dims; a lane prepares row g
+        // of each tile of 8.
+        float4 x[MT][DC];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int r = row_first + mt * 8 + g;
-            const bool live = r < nrows;
             const int i_row = r / a.group;
-            const int64_t qat = live ? (sq.row0 + i_row) * a.q_row + (h * a.group + r - i_row * a.group) * a.q_head : 0;
-            // read twice (the second time from L1): the first codes of K and V hold the registers
-            auto get = [&](int cc, float(&x)[16]) {
-                const int d0 = cc * 64 + t * 16;
-                if (live && d0 < c.dim) {
-                    load_q16(a.q, a.type, qat + d0, x);
-                } else {
+            const int64_t qat = (row0 + i_row) * a.q_row + (h * a.group + r - i_row * a.group) * a.q_head;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-                }
-            };
-            float amax = 0.f;
-#pragma unroll 1
             for (int cc = 0; cc < DC; ++cc) {
-                float x[16];
-                get(cc, x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+                const int d0 = DC == 1 ? t * 16 : (cc >> 1) * 128 + t * 32 + (cc & 1) * 16;
+                x[mt][cc] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < nrows && d0 < c.dim) x[mt][cc] = load_q4(a.q, a.type, qat + d0 + 4 * warp);
             }
+        }
+        // the previous segment's users of the rings and of the arrays below are
+        // done; what they wrote to the rings stays ahead of the copies
+        fence_proxy_async_smem();
+        __syncthreads();
+        for (int it = 0; it < S && it < steps; ++it) issue(it);
+        if (tid < RU) {
+            const int r = row_first + tid, i_row = r / a.group;
+            orow[tid] = r < nrows ? (row0 + i_row) * a.q_heads + h * a.group + r - i_row * a.group : -1;
+            limits[tid] = r < nrows ? sq.len - sq.n + i_row + 1 : 0;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float amax = 0.f;
+#pragma unroll
+            for (int cc = 0; cc < DC; ++cc)
+                amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[mt][cc].x)), fmaxf(fabsf(x[mt][cc].y), fabsf(x[mt][cc].z))),
+                             fabsf(x[mt][cc].w));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+            if (t == 0) ws[warp * RU + mt * 8 + g] = amax;
+        }
+        __syncthreads();
+        float fac[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const float* am = ws + mt * 8 + g;
+            const float amax = fmaxf(fmaxf(am[0], am[RU]), fmaxf(am[2 * RU], am[3 * RU]));
             // 2^e with amax * 2^e in [2^14, 2^15); 1 for zero or non-finite rows
             int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
             e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-            const float fac = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) *
-                              (INT8 ? 16777216.f : 1.f);
+            fac[mt] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (INT8 ? 16777216.f : 1.f);
             f2 sum = {0.f, 0.f}, sum_lo = {0.f, 0.f};
-#pragma unroll 1
-            for (int cc = 0; cc < DC; ++cc) {
-                float x[16];
-                get(cc, x);
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    // the dims in the order that k_codes gives a word's bytes
-                    const float x0 = x[4 * w] * up, x1 = x[4 * w + (INT8 ? 2 : 1)] * up;
-                    const float x2 = x[4 * w + (INT8 ? 1 : 2)] * up, x3 = x[4 * w + 3] * up;
-                    uint2 f, fl;
-                    f.x = pack_f16x2(x0, x1);
-                    f.y = pack_f16x2(x2, x3);
-                    if (PARTS == 2) {
-                        fl.x = rest_f16x2(x0, x1, f.x);
-                        fl.y = rest_f16x2(x2, x3, f.y);
-                    }
-                    if (INT8) {
-                        fadd2(sum, h2_to_f2(f.x));
-                        fadd2(sum, h2_to_f2(f.y));
-                        if (PARTS == 2) {
-                            fadd2(sum_lo, h2_to_f2(fl.x));
-                            fadd2(sum_lo, h2_to_f2(fl.y));
-                        }
-                    }
-                    // every warp holds the same rows: each writes a quarter of the steps
-                    if (w == warp) {
-                        qf[(mt * 4 * DC + cc * 4 + w) * 32 + lane] = f;
-                        if (PARTS == 2) qf[((MT + mt) * 4 * DC + cc * 4 + w) * 32 + lane] = fl;
-                    }
+            for (int cc = 0; cc < DC; ++cc) {
+                // the dims in the order that k_codes gives a word's bytes
+                const float x0 = x[mt][cc].x * up, x1 = (INT8 ? x[mt][cc].z : x[mt][cc].y) * up;
+                const float x2 = (INT8 ? x[mt][cc].y : x[mt][cc].z) * up, x3 = x[mt][cc].w * up;
+                uint2 f;
+                f.x = pack_f16x2(x0, x1);
+                f.y = pack_f16x2(x2, x3);
+                qf[(mt * 4 * DC + cc * 4 + warp) * 32 + lane] = f;
+                if (INT8) fadd2(sum, h2_to_f2(f.x)), fadd2(sum, h2_to_f2(f.y));
+                if (PARTS == 2) {
+                    uint2 fl;
+                    fl.x = rest_f16x2(x0, x1, f.x);
+                    fl.y = rest_f16x2(x2, x3, f.y);
+                    qf[((MT + mt) * 4 * DC + cc * 4 + warp) * 32 + lane] = fl;
+                    if (INT8) fadd2(sum_lo, h2_to_f2(fl.x)), fadd2(sum_lo, h2_to_f2(fl.y));
                 }
             }
-            float bias = (sum.x + sum.y) + (sum_lo.x + sum_lo.y);
-            bias += __shfl_xor_sync(~0u, bias, 1);
-            bias += __shfl_xor_sync(~0u, bias, 2);
-            bias *= kCodeBias;
-            const int lim = live ? sq.len - sq.n + i_row + 1 : 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int src = (2 * t + i) * 4;
-                qfac[mt][i] = __shfl_sync(~0u, fac, src);
-                init[mt][i] = __shfl_sync(~0u, bias, src);
-                limit[mt][i] = __shfl_sync(~0u, lim, src);
+            if (INT8) {
+                float bias = (sum.x + sum.y) + (sum_lo.x + sum_lo.y);
+                bias += __shfl_xor_sync(~0u, bias, 1);
+                bias += __shfl_xor_sync(~0u, bias, 2);
+                if (t == 0) wb[warp * RU + mt * 8 + g] = bias;
             }
         }
         __syncthreads();
+        // the scores a lane gets are those of rows 2t and 2t + 1 of each tile
+        float qfac[MT][2], init[MT][2];
+        int limit[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = mt * 8 + 2 * t + i;
+                qfac[mt][i] = __shfl_sync(~0u, fac[mt], (2 * t + i) * 4);
+                init[mt][i] = INT8 ? (wb[r] + wb[RU + r] + wb[2 * RU + r] + wb[3 * RU + r]) * kCodeBias : 0.f;
+                limit[mt][i] = limits[r];
+            }
 
         float o[MT][4 * DC][4];
         int m[MT][2], mu[MT][2];    // references: m of the scores, mu of score + log2 vs
@@ -381,13 +367,30 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                 for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
         }
 
+        // lanes' byte offsets in a box: K rows g (+ 8), V rows 2t and 2t + 1 (+ 8), as the swizzle places them
+        int koff[2], voff[2];
+        if (DC == 1) {
+            koff[0] = koff[1] = g * 64 + ((t ^ (g >> 1)) * 16);
+            for (int i = 0; i < 2; ++i) voff[i] = (2 * t + i) * 64 + (((g >> 1) ^ t) * 16) + (g & 1) * 8;
+        } else {
+            for (int i = 0; i < 2; ++i) koff[i] = g * 128 + (((2 * t + i) ^ g) * 16);
+            for (int i = 0; i < 2; ++i) voff[i] = (2 * t + i) * 128 + ((g ^ (2 * t + i)) * 16);
+        }
         // One step; `full`: every row sees every token of it.
         auto step = [&](int it, auto full) {
             const int tok = warp_tok + it * step_tok;
+            const unsigned char* stage = ring + (taken % S) * F::kStage;
             float ks[NS], vs[NS];
             bool there[NS];
+            const int odd = (it * NS >> 5) & 1;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) ks[s] = nks[s], vs[s] = nvs[s], there[s] = nid[s] >= 0;
+            for (int s = 0; s < NS; ++s) {
+                const int from = (it * NS + s) & 31;
+                there[s] = full || __shfl_sync(~0u, odd ? id_c[1] : id_c[0], from) >= 0;
+                ks[s] = __shfl_sync(~0u, odd ? ks_c[1] : ks_c[0], from);
+                vs[s] = __shfl_sync(~0u, odd ? vs_c[1] : vs_c[0], from);
+            }
+            mbar_wait_bounded(bar + taken % S, (taken / S) & 1, a.status);
             // scores: rows are tokens g and g + 8 of a subtile, columns the query rows 2t and 2t + 1
             float sc[MT][NS][4];
 #pragma unroll
@@ -398,7 +401,13 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                     for (int i = 0; i < 4; ++i) sc[mt][s][i] = INT8 ? init[mt][i & 1] : 0.f;
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) {
-                if (DC == 4 && cc * 64 >= c.dim) break;  // the other DC hold more than 64 (DC - 1) dims
+                uint4 k4[NS][2];
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        k4[s][j] = *reinterpret_cast<const uint4*>(stage + s * F::kSub + (cc >> 1) * F::kBox +
+                                                                   j * 8 * F::RB + koff[cc & 1]);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t ka[NS][4];
@@ -406,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                     for (int s = 0; s < NS; ++s)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const uint4& k4 = kr[s][j][cc];
-                            k_codes<INT8>(w == 0 ? k4.x : w == 1 ? k4.y : w == 2 ? k4.z : k4.w, ka[s][j], ka[s][j + 2]);
+                            const uint4& q4 = k4[s][j];
+                            k_codes<INT8>(w == 0 ? q4.x : w == 1 ? q4.y : w == 2 ? q4.z : q4.w, ka[s][j], ka[s][j + 2]);
                         }
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
@@ -419,11 +428,6 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                                 mma16816(sc[mt][s], ka[s][0], ka[s][1], ka[s][2], ka[s][3], f.x, f.y);
                         }
                 }
-            }
-            const bool more = it + 1 < steps;
-            if (more) {
-                locate(it + 1);
-                load_k(it + 1);
             }
             // vs < 2^evs, the same in all lanes
             int evs[NS];
@@ -515,39 +519,53 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                     }
                 }
             }
-            if (!INT8 && !full && sq.n > 1) {
-                // A code of V that is NaN where not every row sees every token:
-                // taken out of the products and set where a row sees it.
-                uint32_t any = 0;
+            // o += V^T p^T.  Row tile 2w + i: dims with bytes 4w + 2i (rows 0-7) and 4w + 2i + 1 (rows 8-15)
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                for (int x = 0; x < VL; ++x) {
+                    uint32_t vr[4][VW];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                        for (int x = 0; x < VL; ++x)
+                    for (int j = 0; j < 4; ++j) {
+                        const unsigned char* p = stage + s * F::kSub + (F::NB + x) * F::kBox + (j >> 1) * 8 * F::RB + voff[j & 1];
+                        if (VW == 2) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(p);
+                            vr[j][0] = v.x, vr[j][1] = v.y;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p);
+                            vr[j][0] = v.x, vr[j][1] = v.y, vr[j][VW - 2] = v.z, vr[j][VW - 1] = v.w;
+                        }
+                        if (!full && (!there[s] || tok + s * 16 + 2 * t + (j & 1) + 8 * (j >> 1) >= tok1)) {
 #pragma unroll
-                            for (int i = 0; i < VW; ++i)
-                                any |= __vcmpeq4(vr[s][j][x][i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                if (__any_sync(~0u, any != 0)) {
+                            for (int w = 0; w < VW; ++w) vr[j][w] = 0;
+                        }
+                    }
+                    if (!INT8 && !full && sq.n > 1) {
+                        // A code that is NaN where not every row sees every token:
+                        // taken out of the products and set where a row sees it.
+                        uint32_t any = 0;
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const int r = row_first + mt * 8 + g;
-                        const int lim = r < nrows ? sq.len - sq.n + r / a.group + 1 : 0;
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int s = 0; s < NS; ++s) {
-                            const int first = tok + s * 16 + 2 * t;
-                            const uint32_t sees0 = (first < lim ? 0x3C00u : 0u) | (first + 1 < lim ? 0x3C000000u : 0u);
-                            const uint32_t sees1 = (first + 8 < lim ? 0x3C00u : 0u) | (first + 9 < lim ? 0x3C000000u : 0u);
+                            for (int w = 0; w < VW; ++w) any |= __vcmpeq4(vr[j][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        if (__any_sync(~0u, any != 0)) {
 #pragma unroll
-                            for (int x = 0; x < VL; ++x)
+                            for (int w = 0; w < VW; ++w) {
+                                uint32_t is[4], c01[4], c23[4];
 #pragma unroll
-                                for (int w = 0; w < VW; ++w) {
-                                    uint32_t is[4], c01[4], c23[4];
+                                for (int j = 0; j < 4; ++j) {
+                                    is[j] = __vcmpeq4(vr[j][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                    vr[j][w] &= ~is[j];
+                                    is[j] &= 0x38383838u;  // e4m3 1.0 where the code is NaN
+                                }
+                                v_codes<false>(is[0], is[1], c01);
+                                v_codes<false>(is[2], is[3], c23);
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j)  // e4m3 1.0 where the code is NaN
-                                        is[j] = __vcmpeq4(vr[s][j][x][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x38383838u;
-                                    v_codes<false>(is[0], is[1], c01);
-                                    v_codes<false>(is[2], is[3], c23);
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    const int lim = limits[mt * 8 + g];
+                                    const int at = tok + s * 16 + 2 * t;
+                                    const uint32_t sees0 = (at < lim ? 0x3C00u : 0u) | (at + 1 < lim ? 0x3C000000u : 0u);
+                                    const uint32_t sees1 = (at + 8 < lim ? 0x3C00u : 0u) | (at + 9 < lim ? 0x3C000000u : 0u);
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) {
                                         float cnt[4] = {0.f, 0.f, 0.f, 0.f};
@@ -558,29 +576,14 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                                             if (cnt[j] > 0.f) d[j] = __int_as_float(0x7FC00000);
                                     }
                                 }
+                            }
                         }
                     }
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int x = 0; x < VL; ++x)
-#pragma unroll
-                                for (int i = 0; i < VW; ++i)
-                                    vr[s][j][x][i] &= ~__vcmpeq4(vr[s][j][x][i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                }
-            }
-            // o += V^T p^T.  Row tile 2w + i: dims with bytes 4w + 2i (rows 0-7) and 4w + 2i + 1 (rows 8-15)
-#pragma unroll
-            for (int x = 0; x < VL; ++x)
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
                     for (int w = 0; w < VW; ++w) {
                         uint32_t c01[4], c23[4];
-                        v_codes<INT8>(vr[s][0][x][w], vr[s][1][x][w], c01);
-                        v_codes<INT8>(vr[s][2][x][w], vr[s][3][x][w], c23);
+                        v_codes<INT8>(vr[0][w], vr[1][w], c01);
+                        v_codes<INT8>(vr[2][w], vr[3][w], c23);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -590,10 +593,22 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                                     mma16816(o[mt][x * 2 * VW + 2 * w + i], c01[2 * i], c01[2 * i + 1], c23[2 * i],
                                              c23[2 * i + 1], pb[p][mt][s][0], pb[p][mt][s][1]);
                     }
-            if (more) load_v(it + 1);
+                }
+            ++taken;
+            __syncwarp();  // every lane has read the stage
+            if (it + S < steps) issue(it + S);
         };
+        // Steps of whole tokens for every row, while all pages are there; then the rest.
         int it = 0;
-        for (; it < steps && nfull; ++it) step(it, std::true_type());
+        const int whole_steps = full_end > warp_tok ? (full_end - warp_tok + step_tok - 16 * NS) / step_tok : 0;
+        for (; it < whole_steps; ++it) {
+            int least = 0;  // negative where a page is missing
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                least |= __shfl_sync(~0u, (it * NS >> 5) & 1 ? id_c[1] : id_c[0], (it * NS + s) & 31);
+            if (least < 0) break;
+            step(it, std::true_type());
+        }
         for (; it < steps; ++it) step(it, std::false_type());
 
         // ---- this warp's normalised result and log-sum
@@ -611,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                 const float inv = none ? 0.f : 1.f / sum;
                 const int r = mt * 8 + 2 * t + i;
                 if (g == 0) ws[warp * RU + r] = none ? -INFINITY : static_cast<float>(m[mt][i]) + log2f(sum);
-                float* dst = wo + (warp * RU + r) * DP + g * (4 * VW);
+                float* dst = reinterpret_cast<float*>(ring) + r * DP + g * (4 * VW);
 #pragma unroll
                 for (int x = 0; x < VL; ++x)
 #pragma unroll
@@ -624,35 +639,45 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
                     }
             }
         __syncthreads();
-        // ---- join the four warps; then either the output or a partial result
+        // ---- join the four warps; then either the output or a partial result.
+        // LPR lanes take a row, four dims each.
+        constexpr int LPR = DC == 1 ? 16 : 32, XV = DC == 4 ? 2 : 1;
+        const int row_lane = lane % LPR, row_of = warp * (32 / LPR) + lane / LPR;
         const bool whole = seg == tiles;
-        const int slot = u == u_begin ? 0 : 1;
-        float* part = a.part + static_cast<int64_t>(cta * 2 + slot) * kPartFloats;
-        for (int r = warp; r < RU; r += 4) {
-            const float s0 = ws[r], s1 = ws[RU + r], s2 = ws[2 * RU + r], s3 = ws[3 * RU + r];
-            const float mx = fmaxf(fmaxf(s0, s1), fmaxf(s2, s3));
+        float* part = a.part + static_cast<int64_t>(cta * 2 + (u == u_begin ? 0 : 1)) * kPartFloats;
+        constexpr int kWarpFloats = F::kRing / 4;
+        const float* wo = reinterpret_cast<const float*>(smem);  // the warps' results, kWarpFloats apart
+#pragma unroll
+        for (int r = row_of; r < RU; r += 128 / LPR) {
+            const int64_t to = orow[r];
+            if (to < 0) break;
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ws[i * RU + r];
+            const float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
             const float ref = mx == -INFINITY ? 0.f : mx;
-            const float w0 = exp2f(s0 - ref), w1 = exp2f(s1 - ref), w2 = exp2f(s2 - ref), w3 = exp2f(s3 - ref);
-            const float sum = w0 + w1 + w2 + w3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = exp2_fast(w[i] - ref);  // 0 for a warp without tokens, whose result is 0
+            const float sum = w[0] + w[1] + w[2] + w[3];
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const float ls = sum == 0.f ? -INFINITY : ref + log2f(sum);
-            const int rr = row_first + r;
-            const int64_t orow = (sq.row0 + rr / a.group) * a.q_heads + h * a.group + rr % a.group;
-            for (int d = lane; d < c.dim; d += 32) {
-                const float* p = wo + r * DP + d;
-                // a warp without tokens contributes nothing, not 0 * its contents
-                float acc = 0.f;
-                if (s0 != -INFINITY) acc += w0 * p[0];
-                if (s1 != -INFINITY) acc += w1 * p[RU * DP];
-                if (s2 != -INFINITY) acc += w2 * p[2 * RU * DP];
-                if (s3 != -INFINITY) acc += w3 * p[3 * RU * DP];
-                acc *= inv;
-                if (!whole) part[r * c.dim + d] = acc;
-                else if (rr < nrows) store_out(a.out, a.type, orow * c.dim + d, acc);
+#pragma unroll
+            for (int x2 = 0; x2 < XV; ++x2) {
+                const int d = 4 * (row_lane + 32 * x2);
+                if (d >= c.dim) break;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(wo + i * kWarpFloats + r * DP + d);
+                    acc.x += w[i] * v.x, acc.y += w[i] * v.y, acc.z += w[i] * v.z, acc.w += w[i] * v.w;
+                }
+                acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+                if (whole) store_out4(a.out, a.type, to * c.dim + d, acc);
+                else *reinterpret_cast<float4*>(part + r * c.dim + d) = acc;
             }
-            if (lane == 0) {
+            if (row_lane == 0) {
+                const float ls = sum == 0.f ? -INFINITY : ref + log2f(sum);
                 if (!whole) part[2048 + r] = ls;
-                else if (rr < nrows && a.lse) a.lse[orow] = ls * 0.69314718055994531f;
+                else if (a.lse) a.lse[to] = ls * 0.69314718055994531f;
             }
         }
         if (!whole) {
@@ -668,41 +693,57 @@ __global__ void __launch_bounds__(kThreads, MINB) qg_attn_rows_kernel(const Attn
             }
             __syncthreads();
             if (last_flag) {
-                // the CTAs' partials in the order of the line
-                auto slot_of = [&](int cc) {
-                    return a.part + static_cast<int64_t>(cc * 2 + (line.first(cc) >= span0 ? 0 : 1)) * kPartFloats;
-                };
-                for (int r = warp; r < RU; r += 4) {
-                    const int rr = row_first + r;
-                    if (rr >= nrows) break;
-                    float mx = -INFINITY;
-                    for (int i = lane; i < need; i += 32) mx = fmaxf(mx, __ldcg(slot_of(first + i) + 2048 + r));
+                // The CTAs' partials in the order of the line.  Only the first
+                // of them may hold this span in its second slot.
+                const float* p0 = a.part + static_cast<int64_t>(first * 2 + (line.first(first) < span0 ? 1 : 0)) * kPartFloats;
+                const float* p1 = a.part + static_cast<int64_t>(first) * 2 * kPartFloats;
+                auto part_of = [&](int i) { return i == 0 ? p0 : p1 + static_cast<int64_t>(i) * 2 * kPartFloats; };
+                for (int r = row_of; r < RU; r += 128 / LPR) {
+                    const int64_t to = orow[r];
+                    const bool live = to >= 0;  // the lanes of a dead row take part in the shuffles
+                    float ls0 = -INFINITY;
+                    if (live && row_lane < need) ls0 = __ldcg(part_of(row_lane) + 2048 + r);
+                    float mx = ls0;
+                    for (int i = LPR + row_lane; live && i < need; i += LPR) mx = fmaxf(mx, __ldcg(part_of(i) + 2048 + r));
 #pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+                    for (int o2 = LPR / 2; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o2));
                     const float ref = mx == -INFINITY ? 0.f : mx;
-                    float acc[2 * DC];
+                    float4 acc[XV];
 #pragma unroll
-                    for (int x = 0; x < 2 * DC; ++x) acc[x] = 0.f;
+                    for (int x2 = 0; x2 < XV; ++x2) acc[x2] = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
-#pragma unroll 4
-                    for (int i = 0; i < need; ++i) {
-                        const float* p = slot_of(first + i);
-                        const float ls = __ldcg(p + 2048 + r);
-                        const float w = exp2f(ls - ref);
+                    for (int base = 0; base < need; base += LPR) {
+                        float w = ls0;
+                        if (base) w = live && base + row_lane < need ? __ldcg(part_of(base + row_lane) + 2048 + r) : -INFINITY;
+                        w = exp2_fast(w - ref);
                         sum += w;
-                        if (ls == -INFINITY) continue;
+                        const int count = min(LPR, need - base);
+#pragma unroll 8
+                        for (int j = 0; j < count; ++j) {
+                            const float wj = __shfl_sync(~0u, w, j, LPR);
+                            const float* p = part_of(base + j) + r * c.dim;
 #pragma unroll
-                        for (int x = 0; x < 2 * DC; ++x)
-                            if (x * 32 + lane < c.dim) acc[x] += w * __ldcg(p + r * c.dim + x * 32 + lane);
+                            for (int x2 = 0; x2 < XV; ++x2) {
+                                const int d = 4 * (row_lane + 32 * x2);
+                                if (live && d < c.dim) {
+                                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + d));
+                                    acc[x2].x += wj * v.x, acc[x2].y += wj * v.y, acc[x2].z += wj * v.z, acc[x2].w += wj * v.w;
+                                }
+                            }
+                        }
                     }
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int64_t orow = (sq.row0 + rr / a.group) * a.q_heads + h * a.group + rr % a.group;
 #pragma unroll
-                    for (int x = 0; x < 2 * DC; ++x)
-                        if (x * 32 + lane < c.dim)
-                            store_out(a.out, a.type, orow * c.dim + x * 32 + lane, acc[x] * inv);
-                    if (lane == 0 && a.lse)
-                        a.lse[orow] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+                    for (int o2 = LPR / 2; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(~0u, sum, o2);
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                    for (int x2 = 0; x2 < XV; ++x2) {
+                        const int d = 4 * (row_lane + 32 * x2);
+                        if (live && d < c.dim)
+                            store_out4(a.out, a.type, to * c.dim + d,
+                                       make_float4(acc[x2].x * inv, acc[x2].y * inv, acc[x2].z * inv, acc[x2].w * inv));
+                    }
+                    if (live && row_lane == 0 && a.lse)
+                        a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
                 }
             }
         }
@@ -715,9 +756,13 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     const int dev = current_device();
     const int sms = sm_count(dev);
     if (sms <= 0) return cuda_fail(cudaGetLastError());
-    constexpr int RU = 8 * MT, DP = 64 * DC;
-    const int fixed = PARTS * MT * 4 * DC * 32 * 8 + 4 * RU * DP * 4 + 6 * RU * 4;
-    const int most = fixed + (QGKV_MAX_BATCH + 1) * 8;
+    using F = Shape<DC, MT>;
+    constexpr int fixed = F::off_pre(PARTS);
+    static_assert(F::off_rows(PARTS) % 16 == 0 && F::off_bar(PARTS) % 8 == 0 && F::off_q(PARTS) % 16 == 0, "alignment");
+    CUtensorMap kmap, vmap;
+    if (!encode_cache(&kmap, a.c, a.c.k, F::RB, 16) || !encode_cache(&vmap, a.c, a.c.v, F::RB, 16))
+        return cuda_fail(cudaGetLastError());
+    const int most = fixed + (QGKV_MAX_BATCH + 1) * 16;
     static std::atomic<bool> done[64];
     auto kern = qg_attn_rows_kernel<DC, MT, PARTS, INT8, MINB>;
     if (!done[dev].load(std::memory_order_acquire)) {
@@ -726,7 +771,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
         done[dev].store(true, std::memory_order_release);
     }
     const int grid = sms * MINB < kMaxCtas ? sms * MINB : kMaxCtas;
-    kern<<<grid, kThreads, fixed + (a.batch + 1) * 8, s>>>(a, grid);
+    kern<<<grid, kThreads, fixed + (a.batch + 1) * 16, s>>>(a, kmap, vmap, grid);
     return launch_status();
 }
 
@@ -735,12 +780,27 @@ int launch_typed(const AttnArgs& a, cudaStream_t s) {
     // 16 rows a unit where the mean sequence has more than 8 (the codes are
     // then read half as often); 256-dim heads keep 8 for their registers
     const bool wide = a.rows * a.group > 8 * static_cast<int64_t>(a.batch);
-    if (a.c.dim <= 64) return wide ? launch_one<1, 2, PARTS, INT8, 4>(a, s) : launch_one<1, 1, PARTS, INT8, 3>(a, s);
-    if (a.c.dim <= 128) return wide ? launch_one<2, 2, PARTS, INT8, 2>(a, s) : launch_one<2, 1, PARTS, INT8, 2>(a, s);
+    if (a.c.dim <= 64) return wide ? launch_one<1, 2, PARTS, INT8, 4>(a, s) : launch_one<1, 1, PARTS, INT8, 4>(a, s);
+    if (a.c.dim <= 128) return wide ? launch_one<2, 2, PARTS, INT8, 2>(a, s) : launch_one<2, 1, PARTS, INT8, 3>(a, s);
     return launch_one<4, 1, PARTS, INT8, 2>(a, s);
 }
 
 }  // namespace
+
+bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.dim), cuuint64_t(1) << c.log2p,
+                                static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t gstride[3] = {static_cast<cuuint64_t>(c.token_stride), static_cast<cuuint64_t>(c.head_stride),
+                                   static_cast<cuuint64_t>(c.page_stride)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_tokens), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), gdim, gstride, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s) {
     if (a.type == QGKV_F32) return int8 ? launch_typed<2, true>(a, s) : launch_typed<2, false>(a, s);

@@ -23,27 +23,21 @@ struct AttnArgs {
     unsigned* status;
 };
 
-// Rows start, number of rows and length of sequence b.  A length beyond the
-// table is cut to it (kStatusBounds).
+// Number of rows and length of sequence b.  A length beyond the table is cut
+// to it, rows outside the tensor are none (kStatusBounds).
 struct Seq {
-    int64_t row0;
-    int n;
-    int len;
+    int n, len;
 };
 __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
-    Seq s;
-    s.row0 = b;
-    s.n = 1;
+    Seq s = {1, a.lens[b]};
     if (a.starts) {
         const int64_t r0 = a.starts[b], r1 = a.starts[b + 1];
-        s.row0 = r0;
         s.n = static_cast<int>(r1 - r0);
         if (r0 < 0 || r1 < r0 || r1 > a.rows) {
             atomicOr(a.status, kStatusBounds);
             s.n = 0;
         }
     }
-    s.len = a.lens[b];
     const int64_t most = a.width << a.c.log2p;
     if (s.len < 0 || s.len > most) {
         atomicOr(a.status, kStatusBounds);
@@ -52,42 +46,36 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     return s;
 }
 
-__device__ __forceinline__ void store_out(void* out, int type, int64_t at, float x) {
-    if (type == QGKV_F32) static_cast<float*>(out)[at] = x;
-    else if (type == QGKV_F16) static_cast<__half*>(out)[at] = __float2half_rn(x);
-    else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
-}
-
-// 16 consecutive query values.
-__device__ __forceinline__ void load_q16(const void* q, int type, int64_t at, float (&x)[16]) {
+// Four consecutive output values.
+__device__ __forceinline__ void store_out4(void* out, int type, int64_t at, float4 x) {
     if (type == QGKV_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(q) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = p[i];
-            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-        }
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = x;
+    } else if (type == QGKV_F16) {
+        *reinterpret_cast<uint2*>(static_cast<__half*>(out) + at) = make_uint2(pack_f16x2(x.x, x.y), pack_f16x2(x.z, x.w));
     } else {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = p[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (type == QGKV_F16) {
-                    const f2 f = h2_to_f2(w[j]);
-                    x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
-                } else {
-                    x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                    x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-                }
-            }
-        }
+        uint32_t lo, hi;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x.y), "f"(x.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x.w), "f"(x.z));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint2(lo, hi);
     }
 }
 
+// Four consecutive query values.
+__device__ __forceinline__ float4 load_q4(const void* q, int type, int64_t at) {
+    if (type == QGKV_F32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+    if (type == QGKV_F16) {
+        const f2 a = h2_to_f2(v.x), b = h2_to_f2(v.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+}
+
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s);
+// K or V of one layer as [pages][heads][page_tokens][dim], boxes of box_tokens x box_bytes, swizzled so
+// that the attention's shared-memory reads meet no bank twice
+bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens);
 int launch_attn_prompt(const AttnArgs& a, bool int8, cudaStream_t s);
 
 }  // namespace qg
