@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kTile = 128;        // tokens of a tile: 4 warps x 32
 constexpr int kThreads = 128;
-constexpr int kMaxCtas = 1536;    // partial slots: 2 per CTA
+constexpr int kMaxCtas = 1824;    // partial slots: 2 per CTA
 constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its log-sums
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
@@ -698,13 +698,24 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 const float* p0 = a.part + static_cast<int64_t>(first * 2 + (line.first(first) < span0 ? 1 : 0)) * kPartFloats;
                 const float* p1 = a.part + static_cast<int64_t>(first) * 2 * kPartFloats;
                 auto part_of = [&](int i) { return i == 0 ? p0 : p1 + static_cast<int64_t>(i) * 2 * kPartFloats; };
-                for (int r = row_of; r < RU; r += 128 / LPR) {
-                    const int64_t to = orow[r];
-                    const bool live = to >= 0;  // the lanes of a dead row take part in the shuffles
-                    float ls0 = -INFINITY;
-                    if (live && row_lane < need) ls0 = __ldcg(part_of(row_lane) + 2048 + r);
-                    float mx = ls0;
-                    for (int i = LPR + row_lane; live && i < need; i += LPR) mx = fmaxf(mx, __ldcg(part_of(i) + 2048 + r));
+                // A lane's parts of the log-sums of its rows are all on their
+                // way before the first is used; then 16 parts of a row at a time.
+                constexpr int RW = RU * LPR / 128;  // rows of a lane
+                int64_t to[RW];
+                float ls0[RW];
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = row_of + i * (128 / LPR);
+                    to[i] = orow[r];  // the lanes of a dead row take part in the shuffles
+                    ls0[i] = -INFINITY;
+                    if (to[i] >= 0 && row_lane < need) ls0[i] = __ldcg(part_of(row_lane) + 2048 + r);
+                }
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = row_of + i * (128 / LPR);
+                    const bool live = to[i] >= 0;
+                    float mx = ls0[i];
+                    for (int j = LPR + row_lane; live && j < need; j += LPR) mx = fmaxf(mx, __ldcg(part_of(j) + 2048 + r));
 #pragma unroll
                     for (int o2 = LPR / 2; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o2));
                     const float ref = mx == -INFINITY ? 0.f : mx;
@@ -713,21 +724,26 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     for (int x2 = 0; x2 < XV; ++x2) acc[x2] = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
                     for (int base = 0; base < need; base += LPR) {
-                        float w = ls0;
+                        float w = ls0[i];
                         if (base) w = live && base + row_lane < need ? __ldcg(part_of(base + row_lane) + 2048 + r) : -INFINITY;
                         w = exp2_fast(w - ref);
                         sum += w;
-                        const int count = min(LPR, need - base);
-#pragma unroll 8
-                        for (int j = 0; j < count; ++j) {
-                            const float wj = __shfl_sync(~0u, w, j, LPR);
-                            const float* p = part_of(base + j) + r * c.dim;
+                        for (int j0 = 0; j0 < LPR && base + j0 < need; j0 += 16) {
 #pragma unroll
                             for (int x2 = 0; x2 < XV; ++x2) {
                                 const int d = 4 * (row_lane + 32 * x2);
-                                if (live && d < c.dim) {
-                                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + d));
-                                    acc[x2].x += wj * v.x, acc[x2].y += wj * v.y, acc[x2].z += wj * v.z, acc[x2].w += wj * v.w;
+                                float4 v[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    if (live && d < c.dim && base + j0 + j < need)
+                                        v[j] = __ldcg(reinterpret_cast<const float4*>(part_of(base + j0 + j) + r * c.dim + d));
+                                }
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    const float wj = __shfl_sync(~0u, w, j0 + j, LPR);
+                                    acc[x2].x += wj * v[j].x, acc[x2].y += wj * v[j].y;
+                                    acc[x2].z += wj * v[j].z, acc[x2].w += wj * v[j].w;
                                 }
                             }
                         }
@@ -739,11 +755,11 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     for (int x2 = 0; x2 < XV; ++x2) {
                         const int d = 4 * (row_lane + 32 * x2);
                         if (live && d < c.dim)
-                            store_out4(a.out, a.type, to * c.dim + d,
+                            store_out4(a.out, a.type, to[i] * c.dim + d,
                                        make_float4(acc[x2].x * inv, acc[x2].y * inv, acc[x2].z * inv, acc[x2].w * inv));
                     }
                     if (live && row_lane == 0 && a.lse)
-                        a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+                        a.lse[to[i]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
                 }
             }
         }
@@ -780,8 +796,8 @@ int launch_typed(const AttnArgs& a, cudaStream_t s) {
     // 16 rows a unit where the mean sequence has more than 8 (the codes are
     // then read half as often); 256-dim heads keep 8 for their registers
     const bool wide = a.rows * a.group > 8 * static_cast<int64_t>(a.batch);
-    if (a.c.dim <= 64) return wide ? launch_one<1, 2, PARTS, INT8, 4>(a, s) : launch_one<1, 1, PARTS, INT8, 4>(a, s);
-    if (a.c.dim <= 128) return wide ? launch_one<2, 2, PARTS, INT8, 2>(a, s) : launch_one<2, 1, PARTS, INT8, 3>(a, s);
+    if (a.c.dim <= 64) return wide ? launch_one<1, 2, PARTS, INT8, 3>(a, s) : launch_one<1, 1, PARTS, INT8, 3>(a, s);
+    if (a.c.dim <= 128) return wide ? launch_one<2, 2, PARTS, INT8, 2>(a, s) : launch_one<2, 1, PARTS, INT8, INT8 ? 2 : 3>(a, s);
     return launch_one<4, 1, PARTS, INT8, 2>(a, s);
 }
 
