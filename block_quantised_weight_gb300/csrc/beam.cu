@@ -7,13 +7,16 @@
 // are formed in 64 bits at the end, from few candidates.
 //
 // Bound.  Every logit is read once: HBM-bound for batches, latency-bound for
-// one request.  A CTA streams a part of a row: the running maximum and sum
-// per thread, and a buffer of candidates in shared memory.  A logit enters
-// the buffer when it is above a threshold that at least `keep` values reach:
-// the keep-th largest of the threads' own maxima, found by counting.  After
-// the first step few values pass, so the selection costs one comparison a
-// logit.  The last CTA of a request to arrive merges the parts; all order is
-// by (value, index), so the result does not depend on who arrives when.
+// one request.  A CTA streams a part of a row, the next step's values on
+// their way while one is summed: the running maximum and sum per thread, and
+// a buffer of candidates in shared memory.  A logit enters the buffer when it
+// is above a floor that at least `keep` values reach.  The floor comes from
+// the threads' own maxima: every warp sorts its 32 and takes the
+// ceil(keep / 8)-th; the least of these eight is reached at least `keep`
+// times, and about 20 of 2048 random values pass it for keep = 8.  So a value
+// costs five instructions, and a step one barrier.  The last CTA of a request
+// to arrive merges the parts; all order is by (value, index), so the result
+// does not depend on who arrives when.
 #include <atomic>
 
 #include "kv_common.cuh"
@@ -26,19 +29,25 @@ namespace {
 constexpr int kBeamThreads = 256;
 constexpr int kPer = 8;                            // values a thread takes in one step
 constexpr int kStep = kBeamThreads * kPer;
+constexpr int kWarps = kBeamThreads / 32;
 constexpr int kKeepLimit = 1024;                   // buffered candidates above which the buffer is thinned
-constexpr int kCap = kKeepLimit + kStep;
+constexpr int kMergePer = 2;                       // parts' candidates a thread takes in one step of the merge
+constexpr int kMergeStep = kBeamThreads * kMergePer;
 
 // Larger is better; all keys of one selection differ.
 struct Key1 {  // (logit, token): order of the logit's bits, then the lower token
     unsigned long long a;
     __device__ static Key1 lowest() { return {0ull}; }
     __device__ bool operator<(const Key1& o) const { return a < o.a; }
+    __device__ Key1 from(int mask) const { return {__shfl_xor_sync(~0u, a, mask)}; }
+    __device__ Key1 at(int lane) const { return {__shfl_sync(~0u, a, lane)}; }
 };
 struct Key2 {  // (score, flat index)
     unsigned long long a, b;
     __device__ static Key2 lowest() { return {0ull, 0ull}; }
     __device__ bool operator<(const Key2& o) const { return a < o.a || (a == o.a && b < o.b); }
+    __device__ Key2 from(int mask) const { return {__shfl_xor_sync(~0u, a, mask), __shfl_xor_sync(~0u, b, mask)}; }
+    __device__ Key2 at(int lane) const { return {__shfl_sync(~0u, a, lane), __shfl_sync(~0u, b, lane)}; }
 };
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -57,8 +66,9 @@ __device__ __forceinline__ double unordered64(unsigned long long u) {
 }
 
 // The candidates of a CTA and the threshold below which nothing is kept.
-template <class K>
+template <class K, int PUSHED>
 struct Pool {
+    static constexpr int kCap = kKeepLimit + PUSHED;  // PUSHED: the most that one step adds
     K buf[kCap];
     K top[kBeamThreads];
     K floor_key;
@@ -71,21 +81,47 @@ struct Pool {
         }
         __syncthreads();
     }
-    // floor_key = the keep-th largest of the threads' keys `mine`
+    // floor_key = a key that at least `keep` of the threads' keys `mine`
+    // reach (or the lowest): the least over the warps of their
+    // ceil(keep / 8)-th largest.
     __device__ void raise(K mine, int keep) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int step = size >> 1; step > 0; step >>= 1) {
+                const K other = mine.from(step);
+                // the larger goes to the lower lane where the run falls
+                const bool larger = ((lane & step) == 0) == ((lane & size) == 0);
+                if (larger ? mine < other : other < mine) mine = other;
+            }
+        const K kth = mine.at((keep + kWarps - 1) / kWarps - 1);
+        if (lane == 0) top[threadIdx.x >> 5] = kth;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            K least = top[0];
+            for (int w = 1; w < kWarps; ++w)
+                if (top[w] < least) least = top[w];
+            if (floor_key < least) floor_key = least;
+        }
+        __syncthreads();
+    }
+    // The same with the keep-th largest of all, by counting: bounds what is
+    // left by keep threads' shares whatever the order of the values.
+    __device__ void raise_exact(K mine, int keep) {
         top[threadIdx.x] = mine;
         __syncthreads();
         int above = 0;
 #pragma unroll 8
         for (int i = 0; i < kBeamThreads; ++i)
             above += (mine < top[i] || (i < threadIdx.x && !(top[i] < mine))) ? 1 : 0;
-        if (above == keep - 1) floor_key = mine;
+        if (above == keep - 1 && floor_key < mine) floor_key = mine;
         __syncthreads();
     }
     __device__ void push(K k) { buf[atomicAdd(&n, 1)] = k; }
-    // Thin the buffer: every thread's share of it, its largest, the
-    // keep-th largest of those; what is below goes.
-    __device__ void thin(int keep) {
+    // Thin the buffer: a floor from every thread's largest of its share; what
+    // is below goes.
+    __device__ void thin(int keep, bool exact) {
         constexpr int kShare = kCap / kBeamThreads;
         K mine[kShare];
         K best = K::lowest();
@@ -96,7 +132,8 @@ struct Pool {
             mine[j] = i < have ? buf[i] : K::lowest();
             if (best < mine[j]) best = mine[j];
         }
-        raise(best, keep);
+        if (exact) raise_exact(best, keep);
+        else raise(best, keep);
         if (threadIdx.x == 0) n = 0;
         __syncthreads();
         const K f = floor_key;
@@ -105,15 +142,28 @@ struct Pool {
             if (!(mine[j] < f) && K::lowest() < mine[j]) push(mine[j]);
         __syncthreads();
     }
+    // Until at most `limit` are left; the counting form where the sorted one
+    // does not get there.  Ends: 12 shares of at most 12, then 6, ... a thread.
+    __device__ void thin_to(int limit, int keep) {
+        bool exact = false;
+        while (n > limit) {
+            const int was = n;
+            __syncthreads();
+            thin(keep, exact);
+            if (exact && n >= was) break;
+            exact = true;
+        }
+        __syncthreads();
+    }
+    // After a step's pushes (one barrier): whether the buffer has to be
+    // thinned.  The last thread to push sees the whole count.
+    __device__ bool crowded() {
+        return __syncthreads_or(*reinterpret_cast<volatile int*>(&n) > kKeepLimit) != 0;
+    }
     // After the last push: calls f(rank, key) for the best `keep`.
     template <class F>
     __device__ void finish(int keep, F f) {
-        while (n > 512) {
-            const int was = n;
-            __syncthreads();
-            thin(keep);
-            if (n >= was) break;
-        }
+        thin_to(256, keep);
         const int have = n;
         for (int i = threadIdx.x; i < have; i += kBeamThreads) {
             const K k = buf[i];
@@ -184,7 +234,7 @@ __device__ __forceinline__ void load8(const T* p, int64_t end, int64_t at, int w
 }
 
 template <class T>
-__global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 4) qg_beam_kernel(const BeamArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red_m[kBeamThreads / 32];
     __shared__ double red_l[kBeamThreads / 32];
@@ -200,20 +250,23 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
     const int64_t lo = split * a.span;
     const int64_t end = min(lo + a.span, a.vocab);
 
-    Pool<Key1>& pool = *reinterpret_cast<Pool<Key1>*>(smem);
+    Pool<Key1, kStep>& pool = *reinterpret_cast<Pool<Key1, kStep>*>(smem);
     pool.reset();
-    float m = -INFINITY, l = 0.f;
-    bool started = false;
+    float m = -INFINITY, l = 0.f, floor_value = -INFINITY;
+    float next[kPer];
+    load8(p, end, lo + tid * kPer, words, half, next);
     for (int64_t at0 = lo; at0 < end; at0 += kStep) {
         const int64_t at = at0 + tid * kPer;
         float x[kPer];
-        load8(p, end, at, words, half, x);
-        float mx = m;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, x[i]);
-        if (mx > m) {
-            l *= exp2_fast((m - mx) * 1.4426950408889634f);
-            m = mx;
+        for (int i = 0; i < kPer; ++i) x[i] = next[i];
+        if (at0 + kStep < end) load8(p, end, at + kStep, words, half, next);
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+        if (top > m) {
+            l *= exp2_fast((m - top) * 1.4426950408889634f);
+            m = top;
         }
         // a thread without a finite maximum keeps l = 0; NaN has to reach l
         const float ref = m == -INFINITY ? 0.f : m;
@@ -221,39 +274,33 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) s += exp2_fast((x[i] - ref) * 1.4426950408889634f);
         l += s;
-        Key1 best = Key1::lowest();
-        Key1 key[kPer];
+        auto key = [&](int i) {
+            Key1 k = {0ull};
+            if (at + i < end && x[i] == x[i])
+                k.a = (static_cast<unsigned long long>(ordered(x[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at + i));
+            return k;
+        };
+        if (at0 == lo) {
+            Key1 best = Key1::lowest();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float v = x[i] == x[i] ? x[i] : -INFINITY;
-            const bool real = at + i < end;
-            const uint32_t token = static_cast<uint32_t>(at + i);
-            key[i].a = real ? (static_cast<unsigned long long>(ordered(v)) << 32) | (0xFFFFFFFFu - token) : 0ull;
-            if (best < key[i]) best = key[i];
-        }
-        if (!started) {
-            started = true;
+            for (int i = 0; i < kPer; ++i)
+                if (best < key(i)) best = key(i);
             pool.raise(best, a.keep);
+            floor_value = pool.floor_key.a ? unordered(static_cast<uint32_t>(pool.floor_key.a >> 32)) : -INFINITY;
+        }
+        if (top >= floor_value) {
             const Key1 f = pool.floor_key;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                if (!(key[i] < f) && key[i].a) pool.push(key[i]);
-        } else {
-            const Key1 f = pool.floor_key;
-            if (f < best) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (f < key[i]) pool.push(key[i]);
-            }
+                if (x[i] >= floor_value) {
+                    const Key1 k = key(i);
+                    if (k.a && !(k < f)) pool.push(k);
+                }
         }
-        __syncthreads();
-        while (pool.n > kKeepLimit) {
-            const int was = pool.n;
-            __syncthreads();
-            pool.thin(a.keep);
-            if (pool.n >= was) break;  // not reached: thinning twice leaves at most 6 * keep
+        if (pool.crowded()) {
+            pool.thin_to(kKeepLimit, a.keep);
+            floor_value = pool.floor_key.a ? unordered(static_cast<uint32_t>(pool.floor_key.a >> 32)) : -INFINITY;
         }
-        __syncthreads();
     }
     // the part's maximum and sum (the sum over threads in 64 bits)
     float M = m;
@@ -275,8 +322,9 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
         a.sums[at_part] = L;
     }
     unsigned long long* out = a.keys + at_part * a.part_keep;
+    pool.thin_to(256, a.part_keep);
     for (int i = tid; i < a.part_keep; i += kBeamThreads)
-        if (i >= pool.n) out[i] = 0ull;  // a part shorter than `keep`
+        if (i >= pool.n) out[i] = 0ull;  // a part with fewer
     pool.finish(a.part_keep, [&](int rank, Key1 k) { out[rank] = k.a; });
 
     // ---- the request's last part merges
@@ -311,17 +359,16 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
             row_lse[b] = good ? static_cast<double>(mm) + log(sum) : __longlong_as_double(0x7FF8000000000000ll);
         }
     }
-    Pool<Key2>& merge = *reinterpret_cast<Pool<Key2>*>(smem);
+    Pool<Key2, kMergeStep>& merge = *reinterpret_cast<Pool<Key2, kMergeStep>*>(smem);
     __syncthreads();
     merge.reset();
     const int per_row = a.splits * a.part_keep;
     const int total = a.beams * per_row;
-    started = false;
-    for (int at0 = 0; at0 < total; at0 += kStep) {
-        Key2 key[kPer];
+    for (int at0 = 0; at0 < total; at0 += kMergeStep) {
+        Key2 key[kMergePer];
         Key2 best = Key2::lowest();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < kMergePer; ++i) {
             const int e = at0 + i * kBeamThreads + tid;
             key[i] = Key2::lowest();
             if (e < total) {
@@ -344,22 +391,12 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
             }
             if (best < key[i]) best = key[i];
         }
-        if (!started) {
-            started = true;
-            merge.raise(best, a.keep);
-        }
+        if (at0 == 0) merge.raise(best, a.keep);
         const Key2 f = merge.floor_key;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kMergePer; ++i)
             if (!(key[i] < f) && key[i].a) merge.push(key[i]);
-        __syncthreads();
-        while (merge.n > kKeepLimit) {
-            const int was = merge.n;
-            __syncthreads();
-            merge.thin(a.keep);
-            if (merge.n >= was) break;
-        }
-        __syncthreads();
+        if (merge.crowded()) merge.thin_to(kKeepLimit, a.keep);
     }
     merge.finish(a.keep, [&](int rank, Key2 k) {
         const int64_t flat = static_cast<int64_t>(0x7FFFFFFFFFFFFFFFull - k.b);
@@ -373,7 +410,7 @@ __global__ void __launch_bounds__(kBeamThreads) qg_beam_kernel(const BeamArgs a)
 
 template <class T>
 int launch_beam(BeamArgs a, int requests, cudaStream_t s) {
-    const int smem = static_cast<int>(sizeof(Pool<Key2>));
+    constexpr int smem = static_cast<int>(std::max(sizeof(Pool<Key1, kStep>), sizeof(Pool<Key2, kMergeStep>)));
     const int dev = current_device();
     static std::atomic<bool> done[64];
     if (dev < 0) return cuda_fail(cudaGetLastError());
@@ -397,9 +434,9 @@ int launch_beam_select(const void* logits, int type, const float* cum, int reque
     a.logits = logits, a.cum = cum, a.beams = beams, a.keep = keep, a.vocab = vocab, a.row_stride = row_stride;
     a.scores = scores, a.tokens = tokens, a.parents = parents;
     const int64_t rows = static_cast<int64_t>(requests) * beams;
-    // Enough parts for four CTAs an SM, each at least one step long, and no
-    // more than the partial results have room for.
-    int64_t splits = (4 * sms + rows - 1) / rows;
+    // Enough parts for eight CTAs an SM (two waves of four), each at least one
+    // step long, and no more than the partial results have room for.
+    int64_t splits = (8 * sms + rows - 1) / rows;
     splits = std::min(splits, (vocab + kStep - 1) / kStep);
     const int64_t room = kWsPartBytes - 64;
     splits = std::max<int64_t>(1, std::min(splits, room / (rows * (keep * 8 + 16))));
