@@ -10,10 +10,10 @@
 // one request.  A CTA streams a part of a row, the next step's values on
 // their way while one is summed: the running maximum and sum per thread, and
 // a buffer of candidates in shared memory.  A logit enters the buffer when it
-// is above a floor that at least `keep` values reach.  The floor comes from
+// reaches a floor that at least `keep` values reach.  The floor comes from
 // the threads' own maxima: every warp sorts its 32 and takes the
 // ceil(keep / 8)-th; the least of these eight is reached at least `keep`
-// times, and about 20 of 2048 random values pass it for keep = 8.  So a value
+// times, and about 20 random values of a step pass it for keep = 8.  So a value
 // costs five instructions, and a step one barrier.  The last CTA of a request
 // to arrive merges the parts; all order is by (value, index), so the result
 // does not depend on who arrives when.
@@ -27,7 +27,7 @@ namespace qg {
 namespace {
 
 constexpr int kBeamThreads = 256;
-constexpr int kPer = 8;                            // values a thread takes in one step
+constexpr int kPer = 16;                           // values a thread takes in one step
 constexpr int kStep = kBeamThreads * kPer;
 constexpr int kWarps = kBeamThreads / 32;
 constexpr int kKeepLimit = 1024;                   // buffered candidates above which the buffer is thinned
@@ -64,6 +64,49 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 __device__ __forceinline__ double unordered64(unsigned long long u) {
     return __longlong_as_double(static_cast<long long>(u >> 63 ? u & 0x7FFFFFFFFFFFFFFFull : ~u));
 }
+
+// A value that at least `keep` of the CTA's threads' values `mine` reach: the
+// least over the warps of their ceil(keep / 8)-th largest.  scratch: 8 floats.
+__device__ __forceinline__ float floor_of(float mine, int keep, float* scratch) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int step = size >> 1; step > 0; step >>= 1) {
+            const float other = __shfl_xor_sync(~0u, mine, step);
+            // the larger goes to the lower lane where the run falls
+            mine = ((lane & step) == 0) == ((lane & size) == 0) ? fmaxf(mine, other) : fminf(mine, other);
+        }
+    const float kth = __shfl_sync(~0u, mine, (keep + kWarps - 1) / kWarps - 1);
+    if (lane == 0) scratch[threadIdx.x >> 5] = kth;
+    __syncthreads();
+    float least = scratch[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) least = fminf(least, scratch[w]);
+    return least;
+}
+
+// A sum in two floats: what rounding takes from the first is kept in the second.
+struct Sum2 {
+    float hi, lo;
+    __device__ void add(float x, float x_lo = 0.f) {
+        const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)) + x_lo;
+        hi = s;
+    }
+    __device__ void add_lanes() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float h2 = __shfl_xor_sync(~0u, hi, o), l2 = __shfl_xor_sync(~0u, lo, o);
+            // the same operands in both lanes of a pair, in the same order
+            const bool low = (threadIdx.x & o) == 0;
+            const float a = low ? hi : h2, b = low ? h2 : hi;
+            const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+            lo = (lo + l2) + __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+            hi = s;
+        }
+    }
+};
 
 // The candidates of a CTA and the threshold below which nothing is kept.
 template <class K, int PUSHED>
@@ -142,8 +185,9 @@ struct Pool {
             if (!(mine[j] < f) && K::lowest() < mine[j]) push(mine[j]);
         __syncthreads();
     }
-    // Until at most `limit` are left; the counting form where the sorted one
-    // does not get there.  Ends: 12 shares of at most 12, then 6, ... a thread.
+    // Until at most `limit` (at least 256) are left; the counting form
+    // where the sorted one does not halve the buffer.  Counting leaves at most
+    // keep threads' shares, so it gets below 2 * keep.
     __device__ void thin_to(int limit, int keep) {
         bool exact = false;
         while (n > limit) {
@@ -151,7 +195,7 @@ struct Pool {
             __syncthreads();
             thin(keep, exact);
             if (exact && n >= was) break;
-            exact = true;
+            exact = 2 * n > was;
         }
         __syncthreads();
     }
@@ -163,11 +207,16 @@ struct Pool {
     // After the last push: calls f(rank, key) for the best `keep`.
     template <class F>
     __device__ void finish(int keep, F f) {
+        if (n > 96) {  // the ranks below cost n comparisons each: one cheap pass
+            __syncthreads();
+            thin(keep, false);
+        }
         thin_to(256, keep);
         const int have = n;
         for (int i = threadIdx.x; i < have; i += kBeamThreads) {
             const K k = buf[i];
             int rank = 0;
+#pragma unroll 8
             for (int j = 0; j < have; ++j) rank += k < buf[j] ? 1 : 0;
             if (rank < keep) f(rank, k);
         }
@@ -180,87 +229,54 @@ struct BeamArgs {
     int beams, keep, splits, part_keep;
     int64_t vocab, row_stride, span;
     unsigned long long* keys;  // [rows][splits][part_keep]
-    double* sums;              // [rows][splits]
-    float* maxima;             // [rows][splits]
+    float4* parts;             // [rows][splits] maximum, sum (two floats)
     unsigned* count;           // [requests]
     float* scores;
     int32_t* tokens;
     int32_t* parents;
 };
 
-// Values at .. at + 7 of a row (at a multiple of 8), -inf outside [0, end).
-// A row may start anywhere (a vocabulary of odd size): off its 16-byte
-// boundary by `words` 32-bit words and `half` a word, it is read in the
-// aligned vectors that hold the eight values, each of which holds at least
-// one of them, and shifted into place.  Which thread sums which tokens thus
-// does not depend on the address: equal rows give equal sums.
+// A thread's values of a step: tokens at + i * kBeamThreads, -inf from `end`
+// on.  One value a load: a row may start anywhere (a vocabulary of odd size),
+// and which thread sums which tokens must not depend on the address, or equal
+// rows would get unequal sums.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, int64_t end, int64_t at, int words, bool half, float (&x)[8]) {
-    constexpr int W = 2 * sizeof(T);  // 32-bit words of eight values
-    if (at + 8 <= end) {
-        uint32_t w[W + 4];
-        const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p + at) & ~uintptr_t(15));
+__device__ __forceinline__ void load_step(const T* p, int at, int end, float (&x)[kPer]) {
+    if (at + (kPer - 1) * kBeamThreads < end) {
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-            const uint4 q = ldg_stream16(v + i);
-            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-        }
-        if (words || half) {
-            const uint4 q = ldg_stream16(v + W / 4);
-            w[W] = q.x, w[W + 1] = q.y, w[W + 2] = q.z, w[W + 3] = q.w;
-            if (words & 2)
-#pragma unroll
-                for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
-            if (words & 1)
-#pragma unroll
-                for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
-            if (half)
-#pragma unroll
-                for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (sizeof(T) == 4) {
-                x[i] = __uint_as_float(w[i % W]);
-            } else {
-                const unsigned short h = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
-                x[i] = to_f32(*reinterpret_cast<const T*>(&h));
-            }
-        }
+        for (int i = 0; i < kPer; ++i) x[i] = to_f32(__ldcs(p + at + i * kBeamThreads));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = at + i < end ? to_f32(p[at + i]) : -INFINITY;
+        for (int i = 0; i < kPer; ++i)
+            x[i] = at + i * kBeamThreads < end ? to_f32(__ldcs(p + at + i * kBeamThreads)) : -INFINITY;
     }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kBeamThreads, 4) qg_beam_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 3) qg_beam_kernel(const BeamArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float red_m[kBeamThreads / 32];
-    __shared__ double red_l[kBeamThreads / 32];
+    __shared__ float red_m[2 * kWarps];
+    __shared__ Sum2 red_l[kWarps];
     __shared__ bool last;
     __shared__ double row_lse[QGKV_MAX_BEAMS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / a.splits;
     const int split = static_cast<int>(blockIdx.x - row * a.splits);
     const T* p = static_cast<const T*>(a.logits) + row * a.row_stride;
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-    const int words = off >> 2;
-    const bool half = (off & 2) != 0;
-    const int64_t lo = split * a.span;
-    const int64_t end = min(lo + a.span, a.vocab);
+    const int lo = static_cast<int>(split * a.span), end = static_cast<int>(min(lo + a.span, a.vocab));
 
     Pool<Key1, kStep>& pool = *reinterpret_cast<Pool<Key1, kStep>*>(smem);
     pool.reset();
     float m = -INFINITY, l = 0.f, floor_value = -INFINITY;
     float next[kPer];
-    load8(p, end, lo + tid * kPer, words, half, next);
-    for (int64_t at0 = lo; at0 < end; at0 += kStep) {
-        const int64_t at = at0 + tid * kPer;
+    load_step(p, lo + tid, end, next);
+    int steps = 1;
+    for (int at0 = lo; at0 < end; at0 += kStep) {
+        const int at = at0 + tid;
         float x[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) x[i] = next[i];
-        if (at0 + kStep < end) load8(p, end, at + kStep, words, half, next);
+        if (at0 + kStep < end) load_step(p, at + kStep, end, next);
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
@@ -275,56 +291,53 @@ __global__ void __launch_bounds__(kBeamThreads, 4) qg_beam_kernel(const BeamArgs
         for (int i = 0; i < kPer; ++i) s += exp2_fast((x[i] - ref) * 1.4426950408889634f);
         l += s;
         auto key = [&](int i) {
+            const int token = at + i * kBeamThreads;
             Key1 k = {0ull};
-            if (at + i < end && x[i] == x[i])
-                k.a = (static_cast<unsigned long long>(ordered(x[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at + i));
+            if (token < end && x[i] == x[i])
+                k.a = (static_cast<unsigned long long>(ordered(x[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(token));
             return k;
         };
-        if (at0 == lo) {
-            Key1 best = Key1::lowest();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (best < key(i)) best = key(i);
-            pool.raise(best, a.keep);
-            floor_value = pool.floor_key.a ? unordered(static_cast<uint32_t>(pool.floor_key.a >> 32)) : -INFINITY;
+        // the floor from the threads' maxima so far, at steps 1, 2, 4, 8, ...
+        if ((steps & (steps - 1)) == 0) {
+            const float f = floor_of(m, a.keep, red_m + (steps & 1) * kWarps);
+            floor_value = fmaxf(floor_value, f);
         }
         if (top >= floor_value) {
-            const Key1 f = pool.floor_key;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 if (x[i] >= floor_value) {
                     const Key1 k = key(i);
-                    if (k.a && !(k < f)) pool.push(k);
+                    if (k.a) pool.push(k);
                 }
         }
+        ++steps;
         if (pool.crowded()) {
             pool.thin_to(kKeepLimit, a.keep);
-            floor_value = pool.floor_key.a ? unordered(static_cast<uint32_t>(pool.floor_key.a >> 32)) : -INFINITY;
+            if (pool.floor_key.a) floor_value = fmaxf(floor_value, unordered(static_cast<uint32_t>(pool.floor_key.a >> 32)));
         }
     }
-    // the part's maximum and sum (the sum over threads in 64 bits)
+    // the part's maximum and sum
     float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     if (lane == 0) red_m[warp] = M;
     __syncthreads();
-    for (int w = 0; w < kBeamThreads / 32; ++w) M = fmaxf(M, red_m[w]);
-    double L = m == -INFINITY ? static_cast<double>(l) : static_cast<double>(l) * exp2f((m - M) * 1.4426950408889634f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_m[w]);
+    Sum2 L = {m == -INFINITY ? l : l * exp2_fast((m - M) * 1.4426950408889634f), 0.f};
+    L.add_lanes();
     if (lane == 0) red_l[warp] = L;
     __syncthreads();
     const int64_t at_part = row * a.splits + split;
     if (tid == 0) {
-        L = 0.0;
-        for (int w = 0; w < kBeamThreads / 32; ++w) L += red_l[w];
-        a.maxima[at_part] = M;
-        a.sums[at_part] = L;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) L.add(red_l[w].hi, red_l[w].lo);
+        a.parts[at_part] = make_float4(M, L.hi, L.lo, 0.f);
     }
     unsigned long long* out = a.keys + at_part * a.part_keep;
-    pool.thin_to(256, a.part_keep);
     for (int i = tid; i < a.part_keep; i += kBeamThreads)
         if (i >= pool.n) out[i] = 0ull;  // a part with fewer
+    __syncthreads();
     pool.finish(a.part_keep, [&](int rank, Key1 k) { out[rank] = k.a; });
 
     // ---- the request's last part merges
@@ -340,23 +353,29 @@ __global__ void __launch_bounds__(kBeamThreads, 4) qg_beam_kernel(const BeamArgs
     __syncthreads();
     if (!last) return;
     const int64_t row0 = request * a.beams;
-    for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
+    for (int b = warp; b < a.beams; b += kWarps) {
+        const float4* parts = a.parts + (row0 + b) * a.splits;
         float mm = -INFINITY;
-        for (int s = lane; s < a.splits; s += 32) mm = fmaxf(mm, __ldcg(a.maxima + (row0 + b) * a.splits + s));
+        for (int s = lane; s < a.splits; s += 32) mm = fmaxf(mm, __ldcg(parts + s).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-        double sum = 0.0;
+        Sum2 sum = {0.f, 0.f};
         for (int s = lane; s < a.splits; s += 32) {
-            const float ms = __ldcg(a.maxima + (row0 + b) * a.splits + s);
-            const double ls = __ldcg(a.sums + (row0 + b) * a.splits + s);
-            sum += ms == -INFINITY ? ls : ls * exp2f((ms - mm) * 1.4426950408889634f);
+            const float4 q = __ldcg(parts + s);
+            const float w = q.x == -INFINITY ? 1.f : exp2_fast((q.x - mm) * 1.4426950408889634f);
+            sum.add(w * q.y, w * q.z);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        sum.add_lanes();
         if (lane == 0) {
             const float cb = a.cum[row0 + b];
-            const bool good = sum > 0.0 && sum < 1e300 && mm < INFINITY && mm > -INFINITY && cb < INFINITY && cb > -INFINITY;
-            row_lse[b] = good ? static_cast<double>(mm) + log(sum) : __longlong_as_double(0x7FF8000000000000ll);
+            const float total = sum.hi + sum.lo;
+            const bool good = total > 0.f && total < INFINITY && mm < INFINITY && mm > -INFINITY && cb < INFINITY && cb > -INFINITY;
+            // log(sum) = e log 2 + log(f), f in [1, 2): logf of f is right to 2^-25
+            const int e = static_cast<int>(__float_as_uint(total) >> 23) - 127;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const float f = sum.hi * down;
+            const double ln = static_cast<double>(logf(f)) + static_cast<double>(sum.lo * down / f) + e * 0.69314718055994530942;
+            row_lse[b] = good ? static_cast<double>(mm) + ln : __longlong_as_double(0x7FF8000000000000ll);
         }
     }
     Pool<Key2, kMergeStep>& merge = *reinterpret_cast<Pool<Key2, kMergeStep>*>(smem);
@@ -364,43 +383,57 @@ __global__ void __launch_bounds__(kBeamThreads, 4) qg_beam_kernel(const BeamArgs
     merge.reset();
     const int per_row = a.splits * a.part_keep;
     const int total = a.beams * per_row;
+    // Scores in 32 bits first: `keep` candidates reach the floor of their lower
+    // bounds, and only those whose upper bound reaches it are formed in 64.
+    floor_value = -INFINITY;
     for (int at0 = 0; at0 < total; at0 += kMergeStep) {
-        Key2 key[kMergePer];
-        Key2 best = Key2::lowest();
+        unsigned long long k[kMergePer];
+        float upper[kMergePer], best = -INFINITY;
+        int beam[kMergePer];
 #pragma unroll
         for (int i = 0; i < kMergePer; ++i) {
             const int e = at0 + i * kBeamThreads + tid;
-            key[i] = Key2::lowest();
+            k[i] = 0ull;
+            upper[i] = -INFINITY;
+            beam[i] = 0;
             if (e < total) {
-                const int b = e / per_row;
-                const unsigned long long k = __ldcg(a.keys + (row0 + b) * per_row + (e - b * per_row));
-                const double lse = row_lse[b];
-                double score = -INFINITY;
-                int64_t token = e - b * per_row;  // of a row that scores -inf throughout: its first tokens
-                bool real = token < a.vocab;
-                if (lse == lse) {
-                    real = k != 0ull;
-                    token = 0xFFFFFFFFu - static_cast<uint32_t>(k);
-                    score = static_cast<double>(a.cum[row0 + b]) +
-                            (static_cast<double>(unordered(static_cast<uint32_t>(k >> 32))) - lse);
-                }
-                if (real) {
-                    key[i].a = ordered64(score);
-                    key[i].b = 0x7FFFFFFFFFFFFFFFull - static_cast<unsigned long long>(b * a.vocab + token);
+                beam[i] = e / per_row;
+                k[i] = __ldcg(a.keys + (row0 + beam[i]) * per_row + (e - beam[i] * per_row));
+                if (row_lse[beam[i]] == row_lse[beam[i]] && k[i]) {
+                    const float lse = static_cast<float>(row_lse[beam[i]]), cum = a.cum[row0 + beam[i]];
+                    const float v = unordered(static_cast<uint32_t>(k[i] >> 32));
+                    const float score = cum + (v - lse);
+                    const float off = v == -INFINITY ? 0.f : (fabsf(cum) + fabsf(v) + fabsf(lse)) * 4.8e-7f;
+                    upper[i] = score + off;
+                    best = fmaxf(best, score - off);
                 }
             }
-            if (best < key[i]) best = key[i];
         }
-        if (at0 == 0) merge.raise(best, a.keep);
-        const Key2 f = merge.floor_key;
+        if (at0 == 0) floor_value = floor_of(best, a.keep, red_m);
 #pragma unroll
-        for (int i = 0; i < kMergePer; ++i)
-            if (!(key[i] < f) && key[i].a) merge.push(key[i]);
+        for (int i = 0; i < kMergePer; ++i) {
+            const int e = at0 + i * kBeamThreads + tid;
+            if (e >= total || !(upper[i] >= floor_value)) continue;
+            const double lse = row_lse[beam[i]];
+            double score = -INFINITY;
+            int64_t token = e - beam[i] * per_row;  // of a row that scores -inf throughout: its first tokens
+            bool real = token < a.vocab;
+            if (lse == lse) {
+                real = k[i] != 0ull;
+                token = 0xFFFFFFFFu - static_cast<uint32_t>(k[i]);
+                score = static_cast<double>(a.cum[row0 + beam[i]]) +
+                        (static_cast<double>(unordered(static_cast<uint32_t>(k[i] >> 32))) - lse);
+            }
+            if (real)
+                merge.push({ordered64(score),
+                            0x7FFFFFFFFFFFFFFFull - static_cast<unsigned long long>(beam[i] * a.vocab + token)});
+        }
         if (merge.crowded()) merge.thin_to(kKeepLimit, a.keep);
     }
     merge.finish(a.keep, [&](int rank, Key2 k) {
-        const int64_t flat = static_cast<int64_t>(0x7FFFFFFFFFFFFFFFull - k.b);
-        const int64_t b = flat / a.vocab;
+        const unsigned long long flat = 0x7FFFFFFFFFFFFFFFull - k.b;
+        const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+        const int64_t b = flat >> 32 ? flat / vocab : static_cast<uint32_t>(flat) / vocab;
         const int64_t to = request * a.keep + rank;
         a.scores[to] = static_cast<float>(unordered64(k.a));
         a.tokens[to] = static_cast<int32_t>(flat - b * a.vocab);
@@ -434,21 +467,20 @@ int launch_beam_select(const void* logits, int type, const float* cum, int reque
     a.logits = logits, a.cum = cum, a.beams = beams, a.keep = keep, a.vocab = vocab, a.row_stride = row_stride;
     a.scores = scores, a.tokens = tokens, a.parents = parents;
     const int64_t rows = static_cast<int64_t>(requests) * beams;
-    // Enough parts for eight CTAs an SM (two waves of four), each at least one
-    // step long, and no more than the partial results have room for.
-    int64_t splits = (8 * sms + rows - 1) / rows;
-    splits = std::min(splits, (vocab + kStep - 1) / kStep);
+    // Enough parts for the three CTAs that an SM holds (8 an SM: 83 us where 3 give 73,
+    // 384 rows of 128257 values), each at least 2048 values long, and no more than the partial results have room for.
+    int64_t splits = (3 * sms + rows - 1) / rows;
+    splits = std::min<int64_t>(splits, (vocab + 2047) / 2048);
     const int64_t room = kWsPartBytes - 64;
     splits = std::max<int64_t>(1, std::min(splits, room / (rows * (keep * 8 + 16))));
-    a.span = ((vocab + splits - 1) / splits + kStep - 1) / kStep * kStep;
+    a.span = (vocab + splits - 1) / splits;
     splits = (vocab + a.span - 1) / a.span;
     a.splits = static_cast<int>(splits);
     a.part_keep = static_cast<int>(std::min<int64_t>(keep, vocab));
     if (rows * splits * (a.part_keep * 8 + 16) > room) return QG_ESCRATCH;
     uint8_t* part = workspace + kWsPart;
-    a.keys = reinterpret_cast<unsigned long long*>(part);
-    a.sums = reinterpret_cast<double*>(part + rows * splits * a.part_keep * 8);
-    a.maxima = reinterpret_cast<float*>(a.sums + rows * splits);
+    a.parts = reinterpret_cast<float4*>(part);
+    a.keys = reinterpret_cast<unsigned long long*>(part + rows * splits * 16);
     a.count = reinterpret_cast<unsigned*>(workspace + kWsCounters) + kCntBeam;
     if (type == QGKV_F32) return launch_beam<float>(a, requests, s);
     if (type == QGKV_F16) return launch_beam<__half>(a, requests, s);
