@@ -9,7 +9,10 @@
 // bytes; for one token a sequence it is a single short dependency chain
 // (table -> scale -> codes).  One CTA takes one (block, head) of K or V: the
 // largest magnitude needs the whole block before its first code, so the
-// values are read twice, the second time from L1/L2.
+// block's values wait in registers (up to 16 vectors of 16 bytes a thread;
+// larger blocks are read a second time).  int8's quotient is formed as a
+// product, whose error is below 2^-16 of a code: only quotients that close to
+// a tie (or not finite) take the division, one in 2^14.
 #include "kv_common.cuh"
 #include "launch_common.cuh"
 #include "qgkv_launch.h"
@@ -31,15 +34,6 @@ struct AppendArgs {
     unsigned* status;
 };
 
-// 16 bytes of values -> fp32.
-template <class T>
-__device__ __forceinline__ void load_values(const T* p, float (&x)[16 / sizeof(T)]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const T* e = reinterpret_cast<const T*>(&a);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) x[i] = to_f32(e[i]);
-}
-
 // Code of y = x / scale.
 template <bool INT8>
 __device__ __forceinline__ uint32_t code_of(float y) {
@@ -50,6 +44,44 @@ __device__ __forceinline__ uint32_t code_of(float y) {
     unsigned short r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(y));
     return r & 0xFFu;
+}
+
+// Four codes of int8 by division: out of line, the way there is rare.
+__device__ __noinline__ uint32_t codes_by_division(float x0, float x1, float x2, float x3, float scale) {
+    const float x[4] = {x0, x1, x2, x3};
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool finite = fabsf(x[i]) <= 3.4028235e38f;
+        r |= code_of<true>(scale == 0.f ? (finite ? 0.f : x[i]) : __fdiv_rn(x[i], scale)) << (8 * i);
+    }
+    return r;
+}
+
+// Codes of four values.  inv: 1 / scale rounded (for e4m3 a power of two,
+// exact), 0 for a zero block.
+template <bool INT8>
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float x2, float x3, float scale, float inv) {
+    if (!INT8) {
+        if (scale == 0.f) inv = 1.f;  // zeros stay zeros, infinities and NaN keep their codes
+        unsigned short lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1 * inv), "f"(x0 * inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3 * inv), "f"(x2 * inv));
+        return lo | static_cast<uint32_t>(hi) << 16;
+    }
+    const float x[4] = {x0, x1, x2, x3};
+    uint32_t z[4];
+    bool sure = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = x[i] * inv;
+        const float big = y + 12582912.f;  // 1.5 * 2^23: the sum's low bits are y rounded to an integer
+        z[i] = __float_as_uint(big);
+        // further than 2^-15 from a tie; false for NaN and infinities
+        sure &= fabsf(fabsf(y - (big - 12582912.f)) - 0.5f) > 0x1p-15f;
+    }
+    if (!sure) return codes_by_division(x0, x1, x2, x3, scale);
+    return prmt(prmt(z[0], z[1], 0x0040u), prmt(z[2], z[3], 0x0040u), 0x5410u);
 }
 
 template <bool INT8>
@@ -63,7 +95,33 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-template <class T, bool INT8, int THREADS>
+// The running largest magnitude of pairs of 16-bit values; NaN is passed over.
+template <class T>
+struct Pair {
+    __device__ void take(uint32_t) {}
+    __device__ float largest() const { return 0.f; }
+};
+template <>
+struct Pair<__half> {
+    __half2 m = __floats2half2_rn(0.f, 0.f);
+    __device__ void take(uint32_t two) {
+        two &= 0x7FFF7FFFu;
+        m = __hmax2(m, *reinterpret_cast<__half2*>(&two));
+    }
+    __device__ float largest() const { return fmaxf(__low2float(m), __high2float(m)); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+    __device__ void take(uint32_t two) {
+        two &= 0x7FFF7FFFu;
+        m = __hmax2(m, *reinterpret_cast<__nv_bfloat162*>(&two));
+    }
+    __device__ float largest() const { return fmaxf(__low2float(m), __high2float(m)); }
+};
+
+// NV: vectors of 16 bytes that a thread holds, 0 to read the values twice.
+template <class T, bool INT8, int THREADS, int NV>
 __global__ void __launch_bounds__(THREADS) qg_append_kernel(const AppendArgs a) {
     constexpr int V = 16 / sizeof(T);
     __shared__ int found[4];
@@ -119,31 +177,71 @@ __global__ void __launch_bounds__(THREADS) qg_append_kernel(const AppendArgs a) 
         if (tid == 0) atomicOr(a.status, kStatusBounds);
         return;
     }
-    const int64_t page = a.table[b * a.width + page_at];
-    if (page < 0 || page >= c.pages) {
-        if (tid == 0) atomicOr(a.status, kStatusBounds);
-        return;
-    }
     const int off = block == 0 ? static_cast<int>(len & (page_tokens - 1)) : 0;  // tokens the block holds
     const int64_t row = r0 + (block == 0 ? 0 : (page_at << c.log2p) - len);
     const int n = static_cast<int>(min(static_cast<int64_t>(page_tokens - off), r1 - row));
 
     const T* src = static_cast<const T*>(blockIdx.z ? a.v : a.k) + row * a.row_stride + h * a.head_stride;
-    uint8_t* dst = (blockIdx.z ? c.v : c.k) + page * c.page_stride + static_cast<int64_t>(h) * c.head_stride;
-    float* scale_at = (blockIdx.z ? c.vs : c.ks) + page * c.heads + h;
     const int per = c.dim / V;  // vectors of a token
 
-    // ---- largest finite magnitude
+    // ---- the values, on their way while the page is looked up
+    const int vecs = n * per;
+    // vector tid of the block and the step to tid + THREADS
+    const int tok_first = tid / per, vec_first = tid - tok_first * per;
+    const int tok_step = THREADS / per, vec_step = THREADS - tok_step * per;
+    uint4 held[NV > 0 ? NV : 1];
+    if (NV > 0) {
+        int tok = tok_first, vec = vec_first;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            held[i] = make_uint4(0, 0, 0, 0);
+            if (tid + i * THREADS < vecs) held[i] = ldg_stream16(src + tok * a.row_stride + vec * V);
+            tok += tok_step, vec += vec_step;
+            if (vec >= per) vec -= per, ++tok;
+        }
+    }
+    const int64_t page = a.table[b * a.width + page_at];
+    if (page < 0 || page >= c.pages) {
+        if (tid == 0) atomicOr(a.status, kStatusBounds);
+        return;
+    }
+    uint8_t* dst = (blockIdx.z ? c.v : c.k) + page * c.page_stride + static_cast<int64_t>(h) * c.head_stride;
+    float* scale_at = (blockIdx.z ? c.vs : c.ks) + page * c.heads + h;
     const float old = off > 0 ? *scale_at : 0.f;
+
+    // ---- largest finite magnitude
     float amax = 0.f;
-    for (int i = tid; i < n * per; i += THREADS) {
-        const int tok = i / per, d = (i - tok * per) * V;
-        float x[V];
-        load_values(src + tok * a.row_stride + d, x);
+    auto each = [&](auto f) {  // every vector of this thread
+        if (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) f(held[i]);  // those past the last are 0
+        } else {
+            int tok = tok_first, vec = vec_first;
+            for (int i = tid; i < vecs; i += THREADS) {
+                f(*reinterpret_cast<const uint4*>(src + tok * a.row_stride + vec * V));
+                tok += tok_step, vec += vec_step;
+                if (vec >= per) vec -= per, ++tok;
+            }
+        }
+    };
+    auto largest_finite = [&](const uint4& v) {
+        const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float y = fabsf(x[j]);
+            const float y = fabsf(to_f32(e[j]));
             if (y <= 3.4028235e38f) amax = fmaxf(amax, y);
+        }
+    };
+    if (sizeof(T) == 4) {
+        each(largest_finite);
+    } else {
+        // two values an instruction; NaN is passed over, an infinity sends the thread back
+        Pair<T> m;
+        each([&](const uint4& v) { m.take(v.x), m.take(v.y), m.take(v.z), m.take(v.w); });
+        amax = m.largest();
+        if (amax == INFINITY) {
+            amax = 0.f;
+            each(largest_finite);
         }
     }
 #pragma unroll
@@ -181,35 +279,51 @@ __global__ void __launch_bounds__(THREADS) qg_append_kernel(const AppendArgs a) 
     if (tid == 0) *scale_at = scale;
 
     // ---- new codes
-    const float inv = INT8 || scale == 0.f ? 0.f : __fdiv_rn(1.f, scale);  // e4m3: a power of two, exact
-    for (int i = tid; i < n * per; i += THREADS) {
-        const int tok = i / per, d = (i - tok * per) * V;
+    const float inv = scale == 0.f ? 0.f : __fdiv_rn(1.f, scale);
+    auto write = [&](const uint4& v, int tok, int vec) {
+        const T* e = reinterpret_cast<const T*>(&v);
         float x[V];
-        load_values(src + tok * a.row_stride + d, x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = to_f32(e[j]);
         uint32_t w[V / 4];
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) {
-            w[j] = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // a zero block's codes are 0, NaN aside
-                float y = x[4 * j + q];
-                if (scale == 0.f) y = y == y && fabsf(y) <= 3.4028235e38f ? 0.f : y;
-                else y = INT8 ? __fdiv_rn(y, scale) : __fmul_rn(y, inv);
-                w[j] |= code_of<INT8>(y) << (8 * q);
-            }
-        }
-        uint8_t* p = dst + static_cast<int64_t>(off + tok) * c.token_stride + d;
+        for (int j = 0; j < V / 4; ++j)
+            w[j] = codes_of<INT8>(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3], scale, inv);
+        uint8_t* p = dst + static_cast<int64_t>(off + tok) * c.token_stride + vec * V;
         if (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
         else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[V / 4 - 1]);
+    };
+    int tok = tok_first, vec = vec_first;
+    if (NV > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (tid + i * THREADS < vecs) write(held[i], tok, vec);
+            tok += tok_step, vec += vec_step;
+            if (vec >= per) vec -= per, ++tok;
+        }
+    } else {
+        for (int i = tid; i < vecs; i += THREADS) {
+            write(*reinterpret_cast<const uint4*>(src + tok * a.row_stride + vec * V), tok, vec);
+            tok += tok_step, vec += vec_step;
+            if (vec >= per) vec -= per, ++tok;
+        }
     }
 }
 
 template <class T, bool INT8>
 void launch_typed(const AppendArgs& a, int64_t units, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(units), a.c.heads, 2);
-    if (!a.starts) qg_append_kernel<T, INT8, 32><<<grid, 32, 0, s>>>(a);
-    else qg_append_kernel<T, INT8, 128><<<grid, 128, 0, s>>>(a);
+    if (!a.starts) {  // one token: at most 64 vectors
+        qg_append_kernel<T, INT8, 32, 2><<<grid, 32, 0, s>>>(a);
+        return;
+    }
+    // vectors of a whole block over 128 threads
+    const int need = ((1 << a.c.log2p) * a.c.dim * static_cast<int>(sizeof(T)) / 16 + 127) / 128;
+    if (need <= 2) qg_append_kernel<T, INT8, 128, 2><<<grid, 128, 0, s>>>(a);
+    else if (need <= 4) qg_append_kernel<T, INT8, 128, 4><<<grid, 128, 0, s>>>(a);
+    else if (need <= 8) qg_append_kernel<T, INT8, 128, 8><<<grid, 128, 0, s>>>(a);
+    else if (need <= 16) qg_append_kernel<T, INT8, 128, 16><<<grid, 128, 0, s>>>(a);
+    else qg_append_kernel<T, INT8, 128, 0><<<grid, 128, 0, s>>>(a);
 }
 
 }  // namespace
