@@ -142,6 +142,10 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     a.part = reinterpret_cast<float*>(ws + qg::kWsPart);
     a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
     a.status = st;
+    // From 64 query rows (tokens x heads of a group) a sequence on average the
+    // tcgen05 kernel; below, and for more than 128 dims, the row kernel.
+    const bool many = rows * a.group >= 64 * static_cast<int64_t>(batch) && starts && cache->head_dim <= 128;
+    if (many) return qg::launch_attn_prompt(a, cache->format == QGKV_INT8, stream);
     return qg::launch_attn_rows(a, cache->format == QGKV_INT8, stream);
 }
 

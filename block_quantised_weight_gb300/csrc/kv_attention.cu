@@ -776,7 +776,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     constexpr int fixed = F::off_pre(PARTS);
     static_assert(F::off_rows(PARTS) % 16 == 0 && F::off_bar(PARTS) % 8 == 0 && F::off_q(PARTS) % 16 == 0, "alignment");
     CUtensorMap kmap, vmap;
-    if (!encode_cache(&kmap, a.c, a.c.k, F::RB, 16) || !encode_cache(&vmap, a.c, a.c.v, F::RB, 16))
+    if (!encode_cache(&kmap, a.c, a.c.k, F::RB, 16, true) || !encode_cache(&vmap, a.c, a.c.v, F::RB, 16, true))
         return cuda_fail(cudaGetLastError());
     const int most = fixed + (QGKV_MAX_BATCH + 1) * 16;
     static std::atomic<bool> done[64];
@@ -803,7 +803,8 @@ int launch_typed(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens) {
+bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens,
+                  bool swizzle) {
     auto encode = tensor_map_encoder();
     if (!encode) return false;
     const cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.dim), cuuint64_t(1) << c.log2p,
@@ -814,7 +815,7 @@ bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int b
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), gdim, gstride, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -73,9 +73,9 @@ __device__ __forceinline__ float4 load_q4(const void* q, int type, int64_t at) {
 }
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s);
-// K or V of one layer as [pages][heads][page_tokens][dim], boxes of box_tokens x box_bytes, swizzled so
-// that the attention's shared-memory reads meet no bank twice
-bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens);
+// K or V of one layer as [pages][heads][page_tokens][dim], boxes of box_tokens x box_bytes; `swizzle`: 64- or
+// 128-byte rows, so that reads down a column of a box meet no bank twice.  Bytes past the dims arrive as 0.
+bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens, bool swizzle);
 int launch_attn_prompt(const AttnArgs& a, bool int8, cudaStream_t s);
 
 }  // namespace qg

@@ -1,0 +1,675 @@
+// Attention of many query rows over the 8-bit paged cache (prompts and long
+// chunks) on the tcgen05 tensor cores.
+//
+// Mathematics: kv_attention.cu's.  A CTA takes ROWS = 256 query rows (tokens x
+// heads of a group) of one cache head as two tiles of 128 (fp32 queries: one
+// tile of 128, whose q and p enter as two f16 parts), and walks the keys in
+// steps of 128 tokens:
+//   S = q K^T     q, K as f16 operands in shared memory, S in tensor memory
+//   p = 2^(S * scale * ks - m),  one thread per row, written over S as f16
+//   O += p V      p from tensor memory, V^T from shared memory
+// A row's references m and u are integers that move only when a score passes
+// them by more than 2; then the thread rescales its row of O in tensor memory.
+//
+// Bound.  4 * dim flops a score, 1 exponential: for 128 dims the tensor pipe
+// and the issue slots of the softmax are near each other.  So the roles run
+// beside each other: one warp copies (TMA), four convert the 8-bit codes into
+// f16 operands (K as it lies, V transposed, so that both products take
+// K-major operands), one issues the MMAs, four a tile do the softmax.  The
+// MMAs of one tile run while the other's softmax does; the converted operands
+// serve both tiles.
+//
+// Shared memory: q 64 KB, four operand slots of 32 KB (K, V, K, V), two slots
+// of raw codes of 16 KB.  Tensor memory: S (128 columns) and O (dim columns)
+// of each tile.
+#include <atomic>
+
+#include "kv_attention.cuh"
+#include "launch_common.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kStepTokens = 128;
+constexpr int kOps = 4;       // operand slots
+constexpr int kRaws = 2;      // raw slots
+constexpr int kScales = 8;    // steps whose scales are held
+constexpr uint32_t kRow8 = 1024;  // bytes of 8 operand rows of 128 bytes
+
+template <int DP, int PARTS>
+struct PShape {
+    static constexpr int TILES = PARTS == 1 ? 2 : 1;
+    static constexpr int ROWS = 128 * TILES;
+    static constexpr int kQTile = 128 * DP * 2;
+    static constexpr int kOp = kStepTokens * DP * 2;
+    static constexpr int kRaw = kStepTokens * DP;
+    static constexpr int off_op = TILES * PARTS * kQTile;
+    static constexpr int off_raw = off_op + kOps * kOp;
+    static constexpr int off_scale = off_raw + kRaws * kRaw;
+    static constexpr int off_bar = off_scale + kScales * 8 * 16;
+    static constexpr int smem = off_bar + 256;
+    static constexpr int warps = TILES * 4 + 4 + 2;
+    static constexpr int kCols = TILES == 2 ? 512 : 256;  // tensor memory: 256 columns a tile
+    static_assert(smem <= 232448, "shared memory");
+};
+
+// K-major operand with the 128-byte swizzle: rows of 128 bytes (64 f16), 8-row
+// groups kRow8 apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    uint64_t d = (saddr >> 4) & 0x3FFFu;
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>((kRow8 >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// kind::f16, f16 operands, both K-major, fp32 sums, 128 rows x n columns.
+__host__ __device__ constexpr uint32_t f16_desc(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void arrive_on(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes; the values are there after tmem_loaded().
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&w)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+          "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]),
+          "r"(w[16]), "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]),
+          "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The line of units: for each sequence, its row blocks from the last (which
+// sees most) to the first, each for all heads.  A walker only goes forward.
+template <int ROWS>
+struct Walk {
+    int b = -1, h, row_first, nrows, seen_least, seen_most, steps;
+    Seq sq;
+    int64_t base = 0, units = 0;
+    int blocks = 0;
+    __device__ bool to(const AttnArgs& a, int64_t u) {
+        while (u >= base + units) {
+            base += units;
+            if (++b >= a.batch) return false;
+            sq = sequence(a, b);
+            blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + ROWS - 1) / ROWS);
+            units = static_cast<int64_t>(blocks) * a.c.heads;
+        }
+        const int64_t in = u - base;
+        const int back = static_cast<int>(in / a.c.heads);
+        h = static_cast<int>(in - static_cast<int64_t>(back) * a.c.heads);
+        nrows = sq.n * a.group;
+        row_first = (blocks - 1 - back) * ROWS;
+        const int i_last = (min(row_first + ROWS, nrows) - 1) / a.group;
+        seen_most = max(0, sq.len - sq.n + i_last + 1);
+        seen_least = sq.len - sq.n + row_first / a.group + 1;
+        steps = (seen_most + kStepTokens - 1) / kStepTokens;
+        return true;
+    }
+};
+
+constexpr int kNone = -(1 << 29);
+__device__ __forceinline__ float pow2i(int k) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(k, -127), 127) + 127) << 23);
+}
+__device__ __forceinline__ int ceil_ref(float x) {
+    return x == -INFINITY ? kNone : static_cast<int>(ceilf(fminf(fmaxf(x, -1.0e8f), 1.0e8f)));
+}
+
+template <int DP, int PARTS, bool INT8>
+__global__ void __launch_bounds__(PShape<DP, PARTS>::warps * 32, 1)
+qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+    using F = PShape<DP, PARTS>;
+    constexpr int TILES = F::TILES;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScales][8]: ks, vs, there, exponent of vs
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
+    uint64_t* raw_empty = raw_full + kRaws;
+    uint64_t* op_full = raw_empty + kRaws;
+    uint64_t* op_empty = op_full + kOps;
+    uint64_t* s_full = op_empty + kOps;   // [2]
+    uint64_t* p_full = s_full + 2;        // [2]
+    uint64_t* q_full = p_full + 2;        // [2]
+    uint64_t* o_done = q_full + 2;        // [2]
+    uint64_t* sc_full = o_done + 2;       // [kScales]
+    static_assert((2 * kRaws + 2 * kOps + 8 + kScales) * 8 <= 256, "barriers");
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int nan_unit[8];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const KVLayer& c = a.c;
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it; the same in all threads
+        if (tid == 0) atomicOr(a.status, kStatusBounds);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kRaws; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, 4);
+        for (int i = 0; i < kOps; ++i) mbar_init(op_full + i, 4), mbar_init(op_empty + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(q_full + i, 4);
+            mbar_init(o_done + i, 1);
+        }
+        for (int i = 0; i < kScales; ++i) mbar_init(sc_full + i, 1);
+        fence_mbar_init();
+    }
+    if (tid < 8) nan_unit[tid] = 0;
+    if (warp == F::warps - 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&tmem_slot)), "r"(F::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    Walk<F::ROWS> w;
+    // A wait that gave up ends all further waits, copies and MMAs of its
+    // thread: the kernel then runs to its end within a few wait limits.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !mbar_wait_bounded(bar, parity & 1u, a.status);
+    };
+
+    if (warp == F::warps - 2) {
+        // ---------------------------------------------------------- copies
+        int64_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
+        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
+            const int32_t* table = a.table + static_cast<int64_t>(w.b) * a.width;
+            auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
+                int id = -1;
+                f = make_float4(0.f, 0.f, 0.f, __int_as_float(kNone));
+                const int tok = j * kStepTokens + lane * 16;
+                if (lane < 8 && tok < w.seen_most) {
+                    id = table[tok >> c.log2p];
+                    if (id >= 0 && id < c.pages) {
+                        const int64_t at = static_cast<int64_t>(id) * c.heads + w.h;
+                        f.x = __ldg(c.ks + at);
+                        f.y = __ldg(c.vs + at);
+                        f.z = 1.f;
+                        if (f.y > 0.f)
+                            f.w = __int_as_float(static_cast<int>((__float_as_uint(f.y) >> 23) & 255u) - 126);
+                    } else {
+                        id = -1;
+                        atomicOr(a.status, kStatusBounds);
+                    }
+                }
+                return id;
+            };
+            float4 f;
+            int id = w.steps > 0 ? look(0, f) : -1;
+            for (int j = 0; j < w.steps; ++j, ++g) {
+                const int tok = (j * kStepTokens + lane * 16) & ((1 << c.log2p) - 1);
+                const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++o) {
+                    const int slot = static_cast<int>(o % kRaws);
+                    if (o >= kRaws) wait(raw_empty + slot, static_cast<uint32_t>(o / kRaws - 1));
+                    if (kv == 0) {
+                        if (lane < 8) scales[(g % kScales) * 8 + lane] = f;
+                        __syncwarp();
+                        if (lane == 0) arrive_on(sc_full + g % kScales);
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(raw_full + slot, valid * 16 * DP);
+                    __syncwarp();
+                    if (id >= 0 && !dead)
+                        tma_load_4d(smem + F::off_raw + slot * F::kRaw + lane * 16 * DP, kv ? &vmap : &kmap, 0, tok, w.h, id,
+                                    raw_full + slot);
+                }
+                if (j + 1 < w.steps) id = look(j + 1, f);
+            }
+        }
+    } else if (warp == F::warps - 1) {
+        // ---------------------------------------------------------- MMAs
+        int64_t o = 0;                 // operands taken
+        uint32_t ps = 0, qs = 0;       // probabilities (per tile) and queries taken
+        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
+            if (w.steps == 0) continue;
+            for (int j = 0; j <= w.steps; ++j) {
+                const int64_t ko = o + 2 * j, vo = ko - 1;  // K of step j, V of step j - 1
+                if (j < w.steps) wait(op_full + ko % kOps, static_cast<uint32_t>(ko / kOps));
+                if (j > 0) wait(op_full + vo % kOps, static_cast<uint32_t>(vo / kOps));
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    const uint32_t st = tmem + t * 256, ot = st + 128;
+                    if (j == 0) wait(q_full + t, qs);
+                    else wait(p_full + t, (ps + j - 1));
+                    fence_after();
+                    if (lane == 0 && !dead) {
+                        if (j > 0) {
+                            const uint32_t vb = smem_u32(smem + F::off_op + (vo % kOps) * F::kOp);
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                                for (int ks = 0; ks < 8; ++ks) {
+                                    const uint32_t pa = PARTS == 1 ? st + ks * 8 : st + (ks >> 2) * 64 + (ks & 3) * 8 + p * 32;
+                                    mma_ts(ot, pa, operand_desc(vb + (ks >> 2) * (DP * 128) + (ks & 3) * 32), f16_desc(DP),
+                                           j > 1 || ks > 0 || p > 0 ? 1u : 0u);
+                                }
+                            if (j == w.steps) commit_to(o_done + t);
+                        }
+                        if (j < w.steps) {
+                            const uint32_t kb = smem_u32(smem + F::off_op + (ko % kOps) * F::kOp);
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p) {
+                                const uint32_t qb = smem_u32(smem + (t * PARTS + p) * F::kQTile);
+#pragma unroll
+                                for (int ks = 0; ks < DP / 16; ++ks)
+                                    mma_ss(st, operand_desc(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                           operand_desc(kb + (ks >> 2) * 16384 + (ks & 3) * 32), f16_desc(kStepTokens),
+                                           p > 0 || ks > 0 ? 1u : 0u);
+                            }
+                            commit_to(s_full + t);
+                        }
+                        if (t == TILES - 1) {
+                            if (j > 0) commit_to(op_empty + vo % kOps);
+                            if (j < w.steps) commit_to(op_empty + ko % kOps);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            o += 2 * w.steps;
+            ps += w.steps;
+            ++qs;
+        }
+    } else if (warp >= TILES * 4) {
+        // ---------------------------------------------------------- 8 bits -> f16 operands
+        const int ct = tid - TILES * 128, cw = ct >> 5;
+        int64_t o = 0, g = 0;
+        int unit = 0;
+        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
+            for (int j = 0; j < w.steps; ++j, ++g) {
+                const int tok0 = j * kStepTokens;
+                const bool diagonal = tok0 + kStepTokens > w.seen_least;  // some row does not see all of it
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++o) {
+                    const int rs = static_cast<int>(o % kRaws), os = static_cast<int>(o % kOps);
+                    wait(raw_full + rs, static_cast<uint32_t>(o / kRaws));
+                    if (o >= kOps) wait(op_empty + os, static_cast<uint32_t>(o / kOps - 1));
+                    const unsigned char* raw = smem + F::off_raw + rs * F::kRaw;
+                    unsigned char* op = smem + F::off_op + os * F::kOp;
+                    const float4* sc = scales + (g % kScales) * 8;
+                    if (kv == 0) {
+                        constexpr int C16 = DP / 16;
+#pragma unroll 4
+                        for (int it = 0; it < C16; ++it) {
+                            const int item = it * 128 + ct, token = item / C16, c16 = item % C16;
+                            uint4 x = *reinterpret_cast<const uint4*>(raw + token * DP + c16 * 16);
+                            if (sc[token >> 4].z == 0.f) x = make_uint4(0, 0, 0, 0);
+                            uint32_t h[8];
+                            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (INT8) {  // dims in the order 0, 2, 1, 3 (q's too)
+                                    h[2 * i] = hsub2_1152((in[i] & 0x00FF00FFu) ^ 0x64806480u);
+                                    h[2 * i + 1] = hsub2_1152(((in[i] >> 8) & 0x00FF00FFu) ^ 0x64806480u);
+                                } else {
+                                    h[2 * i] = e4m3x2_f16x2(in[i] & 0xFFFFu);
+                                    h[2 * i + 1] = e4m3x2_f16x2(in[i] >> 16);
+                                }
+                            }
+                            // two 16-byte chunks; lanes of the second 64 dims store theirs in the other order
+                            const bool flip = (c16 >> 2) & 1;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const bool second = (e == 1) != flip;
+                                const int ch = 2 * c16 + (second ? 1 : 0);
+                                *reinterpret_cast<uint4*>(op + (ch >> 3) * 16384 + token * 128 + (((ch & 7) ^ (token & 7)) << 4)) =
+                                    second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                    } else {
+                        constexpr int W = DP / 4;            // words of a token
+                        constexpr int per = 32 / W;          // groups of 8 tokens a warp takes at once
+                        const int word = lane % W;
+                        bool found = false;
+#pragma unroll 1
+                        for (int it = 0; it < 4 / per; ++it) {
+                            const int t0 = ((it * 4 + cw) * per + lane / W) * 8;
+                            const int limit = sc[t0 >> 4].z == 0.f ? 0 : w.seen_most - tok0;
+                            uint32_t x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                x[i] = *reinterpret_cast<const uint32_t*>(raw + (t0 + i) * DP + word * 4);
+                                if (t0 + i >= limit) x[i] = 0;
+                            }
+                            if (!INT8 && diagonal) {
+                                // NaN codes must not meet the zeros of rows that do not see them
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint32_t is = __vcmpeq4(x[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                    found |= is != 0;
+                                    x[i] &= ~is;
+                                }
+                            }
+                            uint32_t r[4][4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v_codes<INT8>(x[2 * i], x[2 * i + 1], r[i]);
+                            // the order of a lane's four dims turns with the lane, so that eight lanes meet eight bank groups
+                            const int turn = (lane >> 1) & 3;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t s0 = turn & 1 ? r[i][1] : r[i][0], s1 = turn & 1 ? r[i][2] : r[i][1];
+                                uint32_t s2 = turn & 1 ? r[i][3] : r[i][2], s3 = turn & 1 ? r[i][0] : r[i][3];
+                                r[i][0] = turn & 2 ? s2 : s0, r[i][1] = turn & 2 ? s3 : s1;
+                                r[i][2] = turn & 2 ? s0 : s2, r[i][3] = turn & 2 ? s1 : s3;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int dim = word * 4 + ((i + turn) & 3);
+                                *reinterpret_cast<uint4*>(op + (t0 >> 6) * (DP * 128) + dim * 128 +
+                                                          ((((t0 >> 3) & 7) ^ (dim & 7)) << 4)) =
+                                    make_uint4(r[0][i], r[1][i], r[2][i], r[3][i]);
+                            }
+                        }
+                        if (found) nan_unit[unit & 7] = unit + 1;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive_on(op_full + os);
+                        arrive_on(raw_empty + rs);
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax, a thread a row
+        const int t = warp >> 2, trow = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t st = tmem + t * 256 + lanes, ot = st + 128;
+        int64_t g = 0;
+        uint32_t ss = 0, os = 0;
+        int unit = 0;
+        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
+            const int r = w.row_first + t * 128 + trow;
+            const bool live = r < w.nrows;
+            const int i_row = r / a.group;
+            const int64_t row0 = a.starts ? a.starts[w.b] : w.b;
+            const int head = w.h * a.group + r - i_row * a.group;
+            const int limit = live ? w.sq.len - w.sq.n + i_row + 1 : 0;
+            float factor = 0.f;
+            if (w.steps > 0) {
+                // ---- queries: f16 parts of q * 2^e, the sign of the scale in them
+                const int64_t qat = (row0 + i_row) * a.q_row + head * a.q_head;
+                float amax = 0.f;
+                if (live)
+                    for (int d = 0; d < c.dim; d += 4) {
+                        const float4 x = load_q4(a.q, a.type, qat + d);
+                        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+                    }
+                int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
+                e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
+                float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                if (a.scale_log2 < 0.f) up = -up;
+                unsigned char* qb = smem + t * PARTS * F::kQTile;
+#pragma unroll 2
+                for (int ch = 0; ch < DP / 8; ++ch) {
+                    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+                    if (live && ch * 8 < c.dim) {
+                        float4 x0 = load_q4(a.q, a.type, qat + ch * 8), x1 = load_q4(a.q, a.type, qat + ch * 8 + 4);
+                        if (INT8) {
+                            const float s0 = x0.y, s1 = x1.y;
+                            x0.y = x0.z, x0.z = s0, x1.y = x1.z, x1.z = s1;
+                        }
+                        hi.x = pack_f16x2(x0.x * up, x0.y * up), hi.y = pack_f16x2(x0.z * up, x0.w * up);
+                        hi.z = pack_f16x2(x1.x * up, x1.y * up), hi.w = pack_f16x2(x1.z * up, x1.w * up);
+                        if (PARTS == 2) {
+                            lo.x = rest_f16x2(x0.x * up, x0.y * up, hi.x), lo.y = rest_f16x2(x0.z * up, x0.w * up, hi.y);
+                            lo.z = rest_f16x2(x1.x * up, x1.y * up, hi.z), lo.w = rest_f16x2(x1.z * up, x1.w * up, hi.w);
+                        }
+                    }
+                    unsigned char* dst = qb + (ch >> 3) * 16384 + trow * 128 + (((ch & 7) ^ (trow & 7)) << 4);
+                    *reinterpret_cast<uint4*>(dst) = hi;
+                    if (PARTS == 2) *reinterpret_cast<uint4*>(dst + F::kQTile) = lo;
+                }
+                fence_proxy_async_smem();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_on(q_full + t);
+            }
+
+            int m = kNone, mu = kNone;
+            float l = 0.f, pk = 1.f;
+            for (int j = 0; j < w.steps; ++j, ++g, ++ss) {
+                wait(sc_full + g % kScales, static_cast<uint32_t>(g / kScales));
+                wait(s_full + t, ss);
+                fence_after();
+                const float4* sc = scales + (g % kScales) * 8;
+                const int left = limit - j * kStepTokens;  // columns that the row sees
+                const bool all = __all_sync(~0u, left >= kStepTokens);
+                uint32_t v[32];
+                // ---- largest scores, by 16 tokens
+                bool passed = false;
+                int mn = m, un = mu;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_load32(st + q * 32, v);
+                    tmem_loaded();
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const float4 f = sc[q * 2 + s];
+                        float top = -INFINITY;
+                        if (all && f.z != 0.f) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[s * 16 + i]));
+                        } else {
+                            const int seen = f.z == 0.f ? 0 : left - (q * 32 + s * 16);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i < seen) top = fmaxf(top, __uint_as_float(v[s * 16 + i]));
+                        }
+                        if (top != -INFINITY) top *= factor * f.x;
+                        const int evs = __float_as_int(f.w);
+                        passed |= top > static_cast<float>(m + 2) || top > static_cast<float>(mu + 2 - evs);
+                        const int upto = ceil_ref(top);
+                        mn = max(mn, upto);
+                        un = max(un, upto + evs);
+                    }
+                }
+                if (__any_sync(~0u, passed)) {
+                    // lanes whose references do not move multiply by 1
+                    if (!passed) mn = m, un = mu;
+                    const int k_old = min(12 + m - mu, 126), k_new = min(12 + mn - un, 126);
+                    const float os2 = pow2i((k_new - mn) - (k_old - m));
+                    l *= pow2i(m - mn);
+                    m = mn, mu = un;
+                    pk = pow2i(max(k_new, -126));
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < DP / 32; ++q) {
+                            tmem_load32(ot + q * 32, v);
+                            tmem_loaded();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * os2);
+                            tmem_store32(ot + q * 32, v);
+                        }
+                        tmem_stored();
+                    }
+                }
+                // ---- probabilities, over S
+                const float ref = static_cast<float>(m);
+                float lsum = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[32], lo[PARTS == 2 ? 32 : 1];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_load32(st + half * 64 + q * 32, v);
+                        tmem_loaded();
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int grp = half * 4 + q * 2 + s;
+                            const float4 f = sc[grp];
+                            const float fs = factor * f.x, fv = f.y * pk;
+                            const int seen = f.z == 0.f ? 0 : left - grp * 16;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float y0 = fmaf(__uint_as_float(v[s * 16 + i]), fs, -ref);
+                                float y1 = fmaf(__uint_as_float(v[s * 16 + i + 1]), fs, -ref);
+                                if (!all || f.z == 0.f) {
+                                    if (i >= seen) y0 = -INFINITY;
+                                    if (i + 1 >= seen) y1 = -INFINITY;
+                                }
+                                float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
+                                lsum += p0 + p1;
+                                p0 *= fv, p1 *= fv;
+                                const uint32_t two = pack_f16x2(p0, p1);
+                                hi[q * 16 + s * 8 + i / 2] = two;
+                                if (PARTS == 2) lo[(q * 16 + s * 8 + i / 2) % (PARTS == 2 ? 32 : 1)] = rest_f16x2(p0, p1, two);
+                            }
+                        }
+                    }
+                    if (PARTS == 1) {
+                        tmem_store32(st + half * 32, hi);
+                    } else {
+                        tmem_store32(st + half * 64, hi);
+                        tmem_store32(st + half * 64 + 32, reinterpret_cast<const uint32_t(&)[32]>(lo));
+                    }
+                }
+                l += lsum;
+                tmem_stored();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_on(p_full + t);
+            }
+
+            // ---- the row's result
+            const int64_t to = (row0 + i_row) * a.q_heads + head;
+            const bool none = l == 0.f && m == kNone;
+            const int down = none ? 0 : max(-min(12 + m - mu, 126), -252);
+            const float f1 = (none ? 0.f : 1.f / l) * pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
+            if (w.steps > 0) {
+                wait(o_done + t, os);
+                ++os;
+                fence_after();
+            }
+#pragma unroll 1
+            for (int q = 0; q < DP / 32; ++q) {
+                uint32_t v[32];
+                if (w.steps > 0) {
+                    tmem_load32(ot + q * 32, v);
+                    tmem_loaded();
+                }
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const int d = q * 32 + i;
+                        if (d >= c.dim) break;
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!none)
+                            x = make_float4(__uint_as_float(v[i]) * f1 * f2v, __uint_as_float(v[i + 1]) * f1 * f2v,
+                                            __uint_as_float(v[i + 2]) * f1 * f2v, __uint_as_float(v[i + 3]) * f1 * f2v);
+                        store_out4(a.out, a.type, to * c.dim + d, x);
+                    }
+                }
+            }
+            if (live && a.lse)
+                a.lse[to] = none ? -INFINITY : (static_cast<float>(m) + log2f(l)) * 0.69314718055994531f;
+            if (!INT8 && live && nan_unit[unit & 7] == unit + 1) {
+                // rare: NaN codes of V among tokens that not every row sees; those that this row sees
+                const int first = max(0, w.seen_least) / kStepTokens * kStepTokens;
+                for (int tok = first; tok < limit; ++tok) {
+                    const int id = a.table[static_cast<int64_t>(w.b) * a.width + (tok >> c.log2p)];
+                    if (id < 0 || id >= c.pages) continue;
+                    const uint8_t* p = c.v + id * c.page_stride + static_cast<int64_t>(w.h) * c.head_stride +
+                                       (tok & ((1 << c.log2p) - 1)) * c.token_stride;
+                    for (int d = 0; d < c.dim; ++d)
+                        if ((p[d] & 0x7F) == 0x7F) {
+                            const float nan = __int_as_float(0x7FC00000);
+                            if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
+                            else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
+                            else static_cast<__nv_bfloat16*>(a.out)[to * c.dim + d] = __float2bfloat16_rn(nan);
+                        }
+                }
+            }
+            fence_before();
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == F::warps - 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F::kCols) : "memory");
+    }
+}
+
+template <int DP, int PARTS, bool INT8>
+int launch_one(const AttnArgs& a, cudaStream_t s) {
+    using F = PShape<DP, PARTS>;
+    const int dev = current_device();
+    const int sms = sm_count(dev);
+    if (sms <= 0) return cuda_fail(cudaGetLastError());
+    CUtensorMap kmap, vmap;
+    if (!encode_cache(&kmap, a.c, a.c.k, DP, 16, false) || !encode_cache(&vmap, a.c, a.c.v, DP, 16, false))
+        return cuda_fail(cudaGetLastError());
+    static std::atomic<bool> done[64];
+    auto kern = qg_attn_prompt_kernel<DP, PARTS, INT8>;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem) != cudaSuccess)
+            return cuda_fail(cudaGetLastError());
+        done[dev].store(true, std::memory_order_release);
+    }
+    // no more CTAs than units there can be
+    const int64_t most = (a.rows * a.group / F::ROWS + a.batch) * a.c.heads;
+    const int grid = static_cast<int>(std::min<int64_t>(sms, most));
+    kern<<<grid, F::warps * 32, F::smem, s>>>(a, kmap, vmap);
+    return launch_status();
+}
+
+template <int PARTS, bool INT8>
+int launch_typed(const AttnArgs& a, cudaStream_t s) {
+    return a.c.dim <= 64 ? launch_one<64, PARTS, INT8>(a, s) : launch_one<128, PARTS, INT8>(a, s);
+}
+
+}  // namespace
+
+int launch_attn_prompt(const AttnArgs& a, bool int8, cudaStream_t s) {
+    if (a.type == QGKV_F32) return int8 ? launch_typed<2, true>(a, s) : launch_typed<2, false>(a, s);
+    return int8 ? launch_typed<1, true>(a, s) : launch_typed<1, false>(a, s);
+}
+
+}  // namespace qg

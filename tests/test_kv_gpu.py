@@ -196,6 +196,78 @@ def test_attention_rows_that_see_nothing(kv, ws):
         check_attention(kv, ws, lens, rows, 4, 2, 64, 16, "e4m3", "hnd", "f32")
 
 
+@pytest.mark.parametrize("lens, rows", [
+    ([300], [300]), ([1000, 513, 64], [257, 513, 1]), ([129, 0, 700, 128], [128, 0, 5, 128]), ([2100], [130]),
+    ([40, 50], [200, 64]), ([128, 256], [128, 256]),
+], ids=str)
+@pytest.mark.parametrize("group, dim, page, order, dtype, fmt", [
+    (1, 64, 16, "hnd", "f32", "e4m3"), (4, 128, 64, "hnd", "bf16", "e4m3"), (8, 64, 32, "nhd", "f16", "int8"),
+    (3, 128, 128, "nhd", "f32", "int8"), (12, 96, 16, "hnd", "bf16", "int8"), (2, 80, 256, "hnd", "f32", "e4m3"),
+    (5, 16, 16, "nhd", "f16", "e4m3"), (1, 128, 16, "hnd", "f16", "e4m3"),
+])
+def test_attention_prompts(kv, ws, lens, rows, group, dim, page, order, dtype, fmt):
+    """Many rows a sequence: whole blocks of rows, parts of them, rows before the first token."""
+    check_attention(kv, ws, lens, rows, 2 * group, 2, dim, page, fmt, order, dtype, seed=group)
+
+
+def test_attention_prompts_of_many_sequences(kv, ws):
+    g = np.random.default_rng(7)
+    rows = [int(x) for x in g.integers(30, 400, 60)]
+    lens = [r + int(x) for r, x in zip(rows, g.integers(0, 300, 60))]
+    check_attention(kv, ws, lens, rows, 8, 4, 64, 32, "e4m3", "hnd", "bf16", seed=60)
+
+
+def test_attention_prompt_negative_scale(kv, ws):
+    check_attention(kv, ws, [200], [150], 4, 2, 64, 16, "int8", "hnd", "f32", scale=-0.1)
+    check_attention(kv, ws, [200], [1], 4, 2, 64, 16, "int8", "hnd", "f32", scale=-0.1)
+
+
+def test_attention_prompt_masked_tokens_do_not_reach(kv, ws):
+    """NaN codes behind the length and in tokens that only later rows see; a missing page."""
+    lens, rows = [300], [140]
+    cache, table, ln = make(kv, lens, 2, 64, 16, "e4m3", "hnd", seed=3)
+    st = starts_of(rows)
+    q = torch.randn((140, 4, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
+    ref = attention_ref(cache, 0, q, table, lens, st, 0.125)
+    last = table[0, 18].long()
+    for c in (cache.k, cache.v):
+        c[0, last, :, 300 - 288:] = 0x7F
+    held = set(table[0].tolist())
+    for p in range(cache.pages):
+        if p not in held:
+            cache.k[0, p] = 0x7F
+            cache.v[0, p] = 0xFF
+    out, lse = kv.kv_attention(cache, 0, q, table, ln, starts=i32(st), return_lse=True, workspace=ws)
+    close(out, lse, ref, 300, torch.float32)
+    for tok, head, dim in ((260, 1, 5), (299, 0, 63), (130, 0, 7)):  # rows from tok - 160 on see it
+        cache.v[0, table[0, tok // 16].long(), head, tok % 16, dim] = 0x7F
+    out = kv.kv_attention(cache, 0, q, table, ln, starts=i32(st), workspace=ws)
+    want = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    want[100:, 2:, 5] = True
+    want[139:, :2, 63] = True
+    want[:, :2, 7] = True
+    assert torch.equal(torch.isnan(out), want)
+    assert ((out.double() - ref[0]).abs()[~want] <= (ref[2] * 1e-4)[~want]).all()
+    cache.k[0, table[0, 17].long(), 0, 3, 9] = 0xFF  # position 275: rows from 115 on of the first group
+    out = kv.kv_attention(cache, 0, q, table, ln, starts=i32(st), workspace=ws)
+    assert torch.isnan(out[115:, :2]).all() and torch.isfinite(out[:115, 2:, :5]).all()
+    assert not torch.isnan(out[:115, :2, 8:60]).any()
+
+
+def test_attention_prompt_bad_page_is_reported_and_masked(kv, ws):
+    lens, rows = [200], [90]
+    cache, table, ln = make(kv, lens, 2, 64, 16, "int8", "hnd", seed=4)
+    q = torch.randn((90, 4, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    for wrong in (-1, cache.pages):
+        t = table.clone()
+        t[0, 2] = wrong
+        out = kv.kv_attention(cache, 0, q, t, ln, starts=i32([0, 90]), workspace=ws)
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+        keep = [i for i in range(table.shape[1]) if i != 2]
+        ref = attention_ref(cache, 0, q, table[:, keep].contiguous(), [200 - 16], [0, 90], 0.125)
+        close(out, None, ref, 200, torch.float32)
+
+
 @pytest.mark.parametrize("batch, context", [(1, 40000), (2, 9001), (70, 300), (300, 40)])
 def test_attention_splits(kv, ws, batch, context):
     """Few long sequences (parts joined through the workspace) and many short ones."""
