@@ -3,13 +3,15 @@
 //
 // Mathematics: kv_attention.cu's.  A CTA takes ROWS = 256 query rows (tokens x
 // heads of a group) of one cache head as two tiles of 128 (fp32 queries: one
-// tile of 128, whose q and p enter as two f16 parts), and walks the keys in
+// tile of 128, whose q enters as two f16 parts), and walks the keys in
 // steps of 128 tokens:
 //   S = q K^T     q, K as f16 operands in shared memory, S in tensor memory
-//   p = 2^(S * scale * ks - m),  one thread per row, written over S as f16
+//   p = 2^(S * scale * ks + log2 vs + k - m),  one thread a row, over S as f16
 //   O += p V      p from tensor memory, V^T from shared memory
-// A row's references m and u are integers that move only when a score passes
-// them by more than 2; then the thread rescales its row of O in tensor memory.
+// with l the sum of p less its block's scale.  A row's references m and u (k =
+// 6 + m - u, 12 for two parts of p) are integers that move only when a score
+// passes them by more than 8 (2): the thread takes its 64 scores once, as if they held, and only where
+// one passes goes round again and rescales its row of O in tensor memory.
 //
 // Bound.  4 * dim flops a score, 1 exponential: for 128 dims the tensor pipe
 // and the issue slots of the softmax are near each other.  So the roles run
@@ -36,14 +38,14 @@ constexpr int kRaws = 2;      // raw slots
 constexpr int kScales = 8;    // steps whose scales are held
 constexpr uint32_t kRow8 = 1024;  // bytes of 8 operand rows of 128 bytes
 
-template <int DP, int PARTS>
+template <int DP, int QP>  // QP: f16 parts of q
 struct PShape {
-    static constexpr int TILES = PARTS == 1 ? 2 : 1;
+    static constexpr int TILES = QP == 1 ? 2 : 1;
     static constexpr int ROWS = 128 * TILES;
     static constexpr int kQTile = 128 * DP * 2;
     static constexpr int kOp = kStepTokens * DP * 2;
     static constexpr int kRaw = kStepTokens * DP;
-    static constexpr int off_op = TILES * PARTS * kQTile;
+    static constexpr int off_op = TILES * QP * kQTile;
     static constexpr int off_raw = off_op + kOps * kOp;
     static constexpr int off_scale = off_raw + kRaws * kRaw;
     static constexpr int off_bar = off_scale + kScales * 8 * 16;
@@ -155,14 +157,14 @@ __device__ __forceinline__ int ceil_ref(float x) {
     return x == -INFINITY ? kNone : static_cast<int>(ceilf(fminf(fmaxf(x, -1.0e8f), 1.0e8f)));
 }
 
-template <int DP, int PARTS, bool INT8>
-__global__ void __launch_bounds__(PShape<DP, PARTS>::warps * 32, 1)
+template <int DP, int QP, int PP, bool INT8>  // PP: f16 parts of p
+__global__ void __launch_bounds__(PShape<DP, QP>::warps * 32, 1)
 qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-    using F = PShape<DP, PARTS>;
+    using F = PShape<DP, QP>;
     constexpr int TILES = F::TILES;
     extern __shared__ __align__(1024) unsigned char smem[];
-    float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScales][8]: ks, vs, there, exponent of vs
+    float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScales][8]: ks, vs, there, log2 vs
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
     uint64_t* raw_empty = raw_full + kRaws;
     uint64_t* op_full = raw_empty + kRaws;
@@ -219,7 +221,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const int32_t* table = a.table + static_cast<int64_t>(w.b) * a.width;
             auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
                 int id = -1;
-                f = make_float4(0.f, 0.f, 0.f, __int_as_float(kNone));
+                f = make_float4(0.f, 0.f, 0.f, -INFINITY);
                 const int tok = j * kStepTokens + lane * 16;
                 if (lane < 8 && tok < w.seen_most) {
                     id = table[tok >> c.log2p];
@@ -228,8 +230,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         f.x = __ldg(c.ks + at);
                         f.y = __ldg(c.vs + at);
                         f.z = 1.f;
-                        if (f.y > 0.f)
-                            f.w = __int_as_float(static_cast<int>((__float_as_uint(f.y) >> 23) & 255u) - 126);
+                        if (f.y > 0.f) f.w = log2f(f.y);
                     } else {
                         id = -1;
                         atomicOr(a.status, kStatusBounds);
@@ -280,10 +281,10 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         if (j > 0) {
                             const uint32_t vb = smem_u32(smem + F::off_op + (vo % kOps) * F::kOp);
 #pragma unroll
-                            for (int p = 0; p < PARTS; ++p)
+                            for (int p = 0; p < PP; ++p)
 #pragma unroll
                                 for (int ks = 0; ks < 8; ++ks) {
-                                    const uint32_t pa = PARTS == 1 ? st + ks * 8 : st + (ks >> 2) * 64 + (ks & 3) * 8 + p * 32;
+                                    const uint32_t pa = PP == 1 ? st + ks * 8 : st + (ks >> 2) * 64 + (ks & 3) * 8 + p * 32;
                                     mma_ts(ot, pa, operand_desc(vb + (ks >> 2) * (DP * 128) + (ks & 3) * 32), f16_desc(DP),
                                            j > 1 || ks > 0 || p > 0 ? 1u : 0u);
                                 }
@@ -292,8 +293,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         if (j < w.steps) {
                             const uint32_t kb = smem_u32(smem + F::off_op + (ko % kOps) * F::kOp);
 #pragma unroll
-                            for (int p = 0; p < PARTS; ++p) {
-                                const uint32_t qb = smem_u32(smem + (t * PARTS + p) * F::kQTile);
+                            for (int p = 0; p < QP; ++p) {
+                                const uint32_t qb = smem_u32(smem + (t * QP + p) * F::kQTile);
 #pragma unroll
                                 for (int ks = 0; ks < DP / 16; ++ks)
                                     mma_ss(st, operand_desc(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
@@ -432,39 +433,48 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const int limit = live ? w.sq.len - w.sq.n + i_row + 1 : 0;
             float factor = 0.f;
             if (w.steps > 0) {
-                // ---- queries: f16 parts of q * 2^e, the sign of the scale in them
+                // ---- queries: f16 parts of q * 2^e, the sign of the scale in
+                // them.  A row is read twice (the second time from L1), eight
+                // vectors on their way at a time.
                 const int64_t qat = (row0 + i_row) * a.q_row + head * a.q_head;
                 float amax = 0.f;
-                if (live)
-                    for (int d = 0; d < c.dim; d += 4) {
-                        const float4 x = load_q4(a.q, a.type, qat + d);
-                        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
-                    }
+#pragma unroll 1
+                for (int d0 = 0; d0 < DP; d0 += 32) {
+                    float4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = live && d0 + 4 * i < c.dim ? load_q4(a.q, a.type, qat + d0 + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[i].x)), fmaxf(fabsf(x[i].y), fabsf(x[i].z))), fabsf(x[i].w));
+                }
                 int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
                 e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
                 float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
                 factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                 if (a.scale_log2 < 0.f) up = -up;
-                unsigned char* qb = smem + t * PARTS * F::kQTile;
-#pragma unroll 2
-                for (int ch = 0; ch < DP / 8; ++ch) {
-                    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-                    if (live && ch * 8 < c.dim) {
-                        float4 x0 = load_q4(a.q, a.type, qat + ch * 8), x1 = load_q4(a.q, a.type, qat + ch * 8 + 4);
-                        if (INT8) {
-                            const float s0 = x0.y, s1 = x1.y;
-                            x0.y = x0.z, x0.z = s0, x1.y = x1.z, x1.z = s1;
+                unsigned char* qb = smem + t * QP * F::kQTile;
+#pragma unroll 1
+                for (int d0 = 0; d0 < DP; d0 += 32) {
+                    float4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = live && d0 + 4 * i < c.dim ? load_q4(a.q, a.type, qat + d0 + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ch = d0 / 8 + i;
+                        uint32_t h[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 y = x[2 * i + k];
+                            const float y0 = y.x * up, y1 = (INT8 ? y.z : y.y) * up, y2 = (INT8 ? y.y : y.z) * up, y3 = y.w * up;
+                            h[2 * k] = pack_f16x2(y0, y1), h[2 * k + 1] = pack_f16x2(y2, y3);
+                            if (QP == 2) lo[2 * k] = rest_f16x2(y0, y1, h[2 * k]), lo[2 * k + 1] = rest_f16x2(y2, y3, h[2 * k + 1]);
                         }
-                        hi.x = pack_f16x2(x0.x * up, x0.y * up), hi.y = pack_f16x2(x0.z * up, x0.w * up);
-                        hi.z = pack_f16x2(x1.x * up, x1.y * up), hi.w = pack_f16x2(x1.z * up, x1.w * up);
-                        if (PARTS == 2) {
-                            lo.x = rest_f16x2(x0.x * up, x0.y * up, hi.x), lo.y = rest_f16x2(x0.z * up, x0.w * up, hi.y);
-                            lo.z = rest_f16x2(x1.x * up, x1.y * up, hi.z), lo.w = rest_f16x2(x1.z * up, x1.w * up, hi.w);
-                        }
+                        unsigned char* dst = qb + (ch >> 3) * 16384 + trow * 128 + (((ch & 7) ^ (trow & 7)) << 4);
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if (QP == 2) *reinterpret_cast<uint4*>(dst + F::kQTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    unsigned char* dst = qb + (ch >> 3) * 16384 + trow * 128 + (((ch & 7) ^ (trow & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = hi;
-                    if (PARTS == 2) *reinterpret_cast<uint4*>(dst + F::kQTile) = lo;
                 }
                 fence_proxy_async_smem();
                 fence_before();
@@ -472,8 +482,15 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 if (lane == 0) arrive_on(q_full + t);
             }
 
+            // References: m of the scores, mu of score + log2 vs.  What is
+            // stored of a probability is 2^(score + log2 vs + kr), at most
+            // 2^14.  One f16 part keeps its 11 bits 20 binary orders down, so
+            // references may be passed by 8 (at 2 every fourth step went
+            // round again, at 8 hardly one after a unit's first); two parts
+            // keep 2^-37 of the largest, and 2 it is.
+            constexpr int kPass = PP == 1 ? 8 : 2, kBase = 14 - kPass;
             int m = kNone, mu = kNone;
-            float l = 0.f, pk = 1.f;
+            float l = 0.f, kf = kBase, kr = kBase - static_cast<float>(kNone);
             for (int j = 0; j < w.steps; ++j, ++g, ++ss) {
                 wait(sc_full + g % kScales, static_cast<uint32_t>(g / kScales));
                 wait(s_full + t, ss);
@@ -481,96 +498,126 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const float4* sc = scales + (g % kScales) * 8;
                 const int left = limit - j * kStepTokens;  // columns that the row sees
                 const bool all = __all_sync(~0u, left >= kStepTokens);
-                uint32_t v[32];
-                // ---- largest scores, by 16 tokens
-                bool passed = false;
-                int mn = m, un = mu;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_load32(st + q * 32, v);
-                    tmem_loaded();
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const float4 f = sc[q * 2 + s];
-                        float top = -INFINITY;
-                        if (all && f.z != 0.f) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[s * 16 + i]));
-                        } else {
-                            const int seen = f.z == 0.f ? 0 : left - (q * 32 + s * 16);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i < seen) top = fmaxf(top, __uint_as_float(v[s * 16 + i]));
-                        }
-                        if (top != -INFINITY) top *= factor * f.x;
-                        const int evs = __float_as_int(f.w);
-                        passed |= top > static_cast<float>(m + 2) || top > static_cast<float>(mu + 2 - evs);
-                        const int upto = ceil_ref(top);
-                        mn = max(mn, upto);
-                        un = max(un, upto + evs);
-                    }
-                }
-                if (__any_sync(~0u, passed)) {
-                    // lanes whose references do not move multiply by 1
-                    if (!passed) mn = m, un = mu;
-                    const int k_old = min(12 + m - mu, 126), k_new = min(12 + mn - un, 126);
-                    const float os2 = pow2i((k_new - mn) - (k_old - m));
-                    l *= pow2i(m - mn);
-                    m = mn, mu = un;
-                    pk = pow2i(max(k_new, -126));
-                    if (j > 0) {
 #pragma unroll 1
-                        for (int q = 0; q < DP / 32; ++q) {
-                            tmem_load32(ot + q * 32, v);
-                            tmem_loaded();
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sh = st + half * 64;
+                    uint32_t hi[32], lo[PP == 2 ? 32 : 1];
+                    float lh;
+#pragma unroll 1
+                    for (int round = 0; round < 2; ++round) {
+                        // Optimistic: with the references as they are.  A score
+                        // that passes them by more than 2 sends the warp round again.
+                        bool passed = false;
+                        lh = 0.f;
+                        uint32_t va[32], vb[32];
+                        tmem_load32(sh, va);
+                        tmem_loaded();
+                        tmem_load32(sh + 32, vb);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * os2);
-                            tmem_store32(ot + q * 32, v);
+                        for (int q = 0; q < 2; ++q) {
+                            if (q == 1) tmem_loaded();
+                            const uint32_t(&v)[32] = q == 0 ? va : vb;
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                const int grp = half * 4 + q * 2 + s;
+                                const float4 f = sc[grp];
+                                const float lvk = f.w + kf;
+                                const bool far = lvk < -100.f;  // a block whose values count for nothing (or are 0)
+                                const float add = far ? -static_cast<float>(m) : f.w + kr;
+                                const f2 fs = {factor * f.x, factor * f.x}, c2 = {add, add};
+                                f2 y[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    y[i] = c2;
+                                    ffma2(y[i], {__uint_as_float(v[s * 16 + 2 * i]), __uint_as_float(v[s * 16 + 2 * i + 1])}, fs);
+                                }
+                                if (!all || f.z == 0.f) {
+                                    const int seen = f.z == 0.f ? 0 : left - grp * 16;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        if (2 * i >= seen) y[i].x = -INFINITY;
+                                        if (2 * i + 1 >= seen) y[i].y = -INFINITY;
+                                    }
+                                }
+                                float top = fmaxf(y[0].x, y[0].y);
+#pragma unroll
+                                for (int i = 1; i < 8; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+                                passed |= top > (far ? static_cast<float>(kPass) : fminf(14.f, lvk + kPass));
+                                f2 sum = {0.f, 0.f};
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    y[i].x = exp2_fast(y[i].x);
+                                    y[i].y = exp2_fast(y[i].y);
+                                    fadd2(sum, y[i]);
+                                    const uint32_t two = far ? 0u : pack_f16x2(y[i].x, y[i].y);
+                                    hi[q * 16 + s * 8 + i] = two;
+                                    if (PP == 2) lo[(q * 16 + s * 8 + i) % (PP == 2 ? 32 : 1)] = far ? 0u : rest_f16x2(y[i].x, y[i].y, two);
+                                }
+                                lh = fmaf(sum.x + sum.y, far ? 1.f : exp2_fast(-lvk), lh);
+                            }
+                        }
+                        if (!__any_sync(~0u, passed)) break;
+                        int mn = m, un = mu;
+                        if (round == 0) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                tmem_load32(sh + q * 32, va);
+                                tmem_loaded();
+#pragma unroll
+                                for (int s = 0; s < 2; ++s) {
+                                    const int grp = half * 4 + q * 2 + s;
+                                    const float4 f = sc[grp];
+                                    const int seen = !passed || f.z == 0.f ? 0 : left - grp * 16;
+                                    float top = -INFINITY;
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        if (i < seen) top = fmaxf(top, __uint_as_float(va[s * 16 + i]));
+                                    if (top != -INFINITY) {
+                                        top *= factor * f.x;
+                                        mn = max(mn, ceil_ref(top));
+                                        un = max(un, ceil_ref(top + f.w));
+                                    }
+                                }
+                            }
+                        }
+                        const int k_old = min(kBase + m - mu, 126), k_new = min(kBase + mn - un, 126);
+                        const float down = pow2i((k_new - mn) - (k_old - m));
+                        l *= pow2i(m - mn);
+                        m = mn, mu = un;
+                        kf = static_cast<float>(max(k_new, -126));
+                        kr = kf - static_cast<float>(m);
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int q = 0; q < DP / 32; ++q) {
+                                tmem_load32(ot + q * 32, va);
+                                tmem_loaded();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * down);
+                                tmem_store32(ot + q * 32, va);
+                            }
+                        }
+                        if (half == 1) {  // the first half's probabilities are stored already
+                            const uint32_t d2 = pack_f16x2(down, down);
+#pragma unroll 1
+                            for (int p = 0; p < PP; ++p) {
+                                tmem_load32(st + p * 32, va);
+                                tmem_loaded();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(va[i]) : "r"(va[i]), "r"(d2));
+                                tmem_store32(st + p * 32, va);
+                            }
                         }
                         tmem_stored();
                     }
-                }
-                // ---- probabilities, over S
-                const float ref = static_cast<float>(m);
-                float lsum = 0.f;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t hi[32], lo[PARTS == 2 ? 32 : 1];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        tmem_load32(st + half * 64 + q * 32, v);
-                        tmem_loaded();
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const int grp = half * 4 + q * 2 + s;
-                            const float4 f = sc[grp];
-                            const float fs = factor * f.x, fv = f.y * pk;
-                            const int seen = f.z == 0.f ? 0 : left - grp * 16;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float y0 = fmaf(__uint_as_float(v[s * 16 + i]), fs, -ref);
-                                float y1 = fmaf(__uint_as_float(v[s * 16 + i + 1]), fs, -ref);
-                                if (!all || f.z == 0.f) {
-                                    if (i >= seen) y0 = -INFINITY;
-                                    if (i + 1 >= seen) y1 = -INFINITY;
-                                }
-                                float p0 = exp2_fast(y0), p1 = exp2_fast(y1);
-                                lsum += p0 + p1;
-                                p0 *= fv, p1 *= fv;
-                                const uint32_t two = pack_f16x2(p0, p1);
-                                hi[q * 16 + s * 8 + i / 2] = two;
-                                if (PARTS == 2) lo[(q * 16 + s * 8 + i / 2) % (PARTS == 2 ? 32 : 1)] = rest_f16x2(p0, p1, two);
-                            }
-                        }
-                    }
-                    if (PARTS == 1) {
+                    l += lh;
+                    if (PP == 1) {
                         tmem_store32(st + half * 32, hi);
                     } else {
                         tmem_store32(st + half * 64, hi);
                         tmem_store32(st + half * 64 + 32, reinterpret_cast<const uint32_t(&)[32]>(lo));
                     }
                 }
-                l += lsum;
                 tmem_stored();
                 fence_before();
                 __syncwarp();
@@ -580,7 +627,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             // ---- the row's result
             const int64_t to = (row0 + i_row) * a.q_heads + head;
             const bool none = l == 0.f && m == kNone;
-            const int down = none ? 0 : max(-min(12 + m - mu, 126), -252);
+            const int down = none ? 0 : max(-min(kBase + m - mu, 126), -252);
             const float f1 = (none ? 0.f : 1.f / l) * pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
             if (w.steps > 0) {
                 wait(o_done + t, os);
@@ -637,9 +684,9 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     }
 }
 
-template <int DP, int PARTS, bool INT8>
+template <int DP, int QP, int PP, bool INT8>
 int launch_one(const AttnArgs& a, cudaStream_t s) {
-    using F = PShape<DP, PARTS>;
+    using F = PShape<DP, QP>;
     const int dev = current_device();
     const int sms = sm_count(dev);
     if (sms <= 0) return cuda_fail(cudaGetLastError());
@@ -647,7 +694,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     if (!encode_cache(&kmap, a.c, a.c.k, DP, 16, false) || !encode_cache(&vmap, a.c, a.c.v, DP, 16, false))
         return cuda_fail(cudaGetLastError());
     static std::atomic<bool> done[64];
-    auto kern = qg_attn_prompt_kernel<DP, PARTS, INT8>;
+    auto kern = qg_attn_prompt_kernel<DP, QP, PP, INT8>;
     if (!done[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem) != cudaSuccess)
             return cuda_fail(cudaGetLastError());
@@ -660,16 +707,23 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     return launch_status();
 }
 
-template <int PARTS, bool INT8>
+template <int QP, int PP, bool INT8>
 int launch_typed(const AttnArgs& a, cudaStream_t s) {
-    return a.c.dim <= 64 ? launch_one<64, PARTS, INT8>(a, s) : launch_one<128, PARTS, INT8>(a, s);
+    return a.c.dim <= 64 ? launch_one<64, QP, PP, INT8>(a, s) : launch_one<128, QP, PP, INT8>(a, s);
+}
+
+template <bool INT8>
+int launch_format(const AttnArgs& a, cudaStream_t s) {
+    if (a.type == QGKV_F32) return launch_typed<2, 2, INT8>(a, s);
+    // f16 outputs round as finely as one f16 part of p would: two
+    if (a.type == QGKV_F16) return launch_typed<1, 2, INT8>(a, s);
+    return launch_typed<1, 1, INT8>(a, s);
 }
 
 }  // namespace
 
 int launch_attn_prompt(const AttnArgs& a, bool int8, cudaStream_t s) {
-    if (a.type == QGKV_F32) return int8 ? launch_typed<2, true>(a, s) : launch_typed<2, false>(a, s);
-    return int8 ? launch_typed<1, true>(a, s) : launch_typed<1, false>(a, s);
+    return int8 ? launch_format<true>(a, s) : launch_format<false>(a, s);
 }
 
 }  // namespace qg
