@@ -264,7 +264,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         // ---- queries: the column operand, scaled by a power of two per row.
         // Warp w takes the w-th four of a lane's 16 dims; a lane prepares row g
         // of each tile of 8.
-        float4 x[MT][DC];
+        uint4 raw[MT][DC];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int r = row_first + mt * 8 + g;
@@ -273,8 +273,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) {
                 const int d0 = DC == 1 ? t * 16 : (cc >> 1) * 128 + t * 32 + (cc & 1) * 16;
-                x[mt][cc] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < nrows && d0 < c.dim) x[mt][cc] = load_q4(a.q, a.type, qat + d0 + 4 * warp);
+                raw[mt][cc] = load_q4(a.q, a.type, qat + d0 + 4 * warp, r < nrows && d0 < c.dim);
             }
         }
         // the previous segment's users of the rings and of the arrays below are
@@ -287,9 +286,12 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             orow[tid] = r < nrows ? (row0 + i_row) * a.q_heads + h * a.group + r - i_row * a.group : -1;
             limits[tid] = r < nrows ? sq.len - sq.n + i_row + 1 : 0;
         }
+        float4 x[MT][DC];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float amax = 0.f;
+#pragma unroll
+            for (int cc = 0; cc < DC; ++cc) x[mt][cc] = q4_values(raw[mt][cc], a.type);
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc)
                 amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[mt][cc].x)), fmaxf(fabsf(x[mt][cc].y), fabsf(x[mt][cc].z))),

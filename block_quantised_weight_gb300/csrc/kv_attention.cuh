@@ -60,10 +60,22 @@ __device__ __forceinline__ void store_out4(void* out, int type, int64_t at, floa
     }
 }
 
-// Four consecutive query values.
-__device__ __forceinline__ float4 load_q4(const void* q, int type, int64_t at) {
-    if (type == QGKV_F32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+// Four consecutive query values as they lie (16-bit types in x and y); to
+// values with q4_values once they are there, so that reads of several vectors
+// do not wait for one another.
+__device__ __forceinline__ uint4 load_q4(const void* q, int type, int64_t at, bool there) {
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (type == QGKV_F32) {
+        if (there) r = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(q) + at));
+    } else if (there) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+        r.x = v.x, r.y = v.y;
+    }
+    return r;
+}
+__device__ __forceinline__ float4 q4_values(uint4 v, int type) {
+    if (type == QGKV_F32)
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
     if (type == QGKV_F16) {
         const f2 a = h2_to_f2(v.x), b = h2_to_f2(v.y);
         return make_float4(a.x, a.y, b.x, b.y);

@@ -33,9 +33,9 @@ namespace qg {
 namespace {
 
 constexpr int kStepTokens = 128;
-constexpr int kOps = 4;       // operand slots
-constexpr int kRaws = 2;      // raw slots
-constexpr int kScales = 8;    // steps whose scales are held
+constexpr uint32_t kOps = 4;       // operand slots
+constexpr uint32_t kRaws = 2;      // raw slots
+constexpr uint32_t kScales = 8;    // steps whose scales are held
 constexpr uint32_t kRow8 = 1024;  // bytes of 8 operand rows of 128 bytes
 
 template <int DP, int QP>  // QP: f16 parts of q
@@ -216,7 +216,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 
     if (warp == F::warps - 2) {
         // ---------------------------------------------------------- copies
-        int64_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
+        uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
         for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
             const int32_t* table = a.table + static_cast<int64_t>(w.b) * a.width;
             auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
@@ -245,8 +245,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++o) {
-                    const int slot = static_cast<int>(o % kRaws);
-                    if (o >= kRaws) wait(raw_empty + slot, static_cast<uint32_t>(o / kRaws - 1));
+                    const int slot = o % kRaws;
+                    if (o >= kRaws) wait(raw_empty + slot, o / kRaws - 1);
                     if (kv == 0) {
                         if (lane < 8) scales[(g % kScales) * 8 + lane] = f;
                         __syncwarp();
@@ -263,14 +263,14 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         }
     } else if (warp == F::warps - 1) {
         // ---------------------------------------------------------- MMAs
-        int64_t o = 0;                 // operands taken
+        uint32_t o = 0;                // operands taken
         uint32_t ps = 0, qs = 0;       // probabilities (per tile) and queries taken
         for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
             if (w.steps == 0) continue;
             for (int j = 0; j <= w.steps; ++j) {
-                const int64_t ko = o + 2 * j, vo = ko - 1;  // K of step j, V of step j - 1
-                if (j < w.steps) wait(op_full + ko % kOps, static_cast<uint32_t>(ko / kOps));
-                if (j > 0) wait(op_full + vo % kOps, static_cast<uint32_t>(vo / kOps));
+                const uint32_t ko = o + 2 * j, vo = ko - 1;  // K of step j, V of step j - 1
+                if (j < w.steps) wait(op_full + ko % kOps, ko / kOps);
+                if (j > 0) wait(op_full + vo % kOps, vo / kOps);
 #pragma unroll
                 for (int t = 0; t < TILES; ++t) {
                     const uint32_t st = tmem + t * 256, ot = st + 128;
@@ -279,26 +279,26 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     fence_after();
                     if (lane == 0 && !dead) {
                         if (j > 0) {
-                            const uint32_t vb = smem_u32(smem + F::off_op + (vo % kOps) * F::kOp);
+                            const uint64_t vb = operand_desc(smem_u32(smem + F::off_op + (vo % kOps) * F::kOp));
 #pragma unroll
                             for (int p = 0; p < PP; ++p)
 #pragma unroll
                                 for (int ks = 0; ks < 8; ++ks) {
                                     const uint32_t pa = PP == 1 ? st + ks * 8 : st + (ks >> 2) * 64 + (ks & 3) * 8 + p * 32;
-                                    mma_ts(ot, pa, operand_desc(vb + (ks >> 2) * (DP * 128) + (ks & 3) * 32), f16_desc(DP),
+                                    mma_ts(ot, pa, vb + (((ks >> 2) * (DP * 128) + (ks & 3) * 32) >> 4), f16_desc(DP),
                                            j > 1 || ks > 0 || p > 0 ? 1u : 0u);
                                 }
                             if (j == w.steps) commit_to(o_done + t);
                         }
                         if (j < w.steps) {
-                            const uint32_t kb = smem_u32(smem + F::off_op + (ko % kOps) * F::kOp);
+                            const uint64_t kb = operand_desc(smem_u32(smem + F::off_op + (ko % kOps) * F::kOp));
 #pragma unroll
                             for (int p = 0; p < QP; ++p) {
-                                const uint32_t qb = smem_u32(smem + (t * QP + p) * F::kQTile);
+                                const uint64_t qb = operand_desc(smem_u32(smem + (t * QP + p) * F::kQTile));
 #pragma unroll
                                 for (int ks = 0; ks < DP / 16; ++ks)
-                                    mma_ss(st, operand_desc(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                           operand_desc(kb + (ks >> 2) * 16384 + (ks & 3) * 32), f16_desc(kStepTokens),
+                                    mma_ss(st, qb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                                           kb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), f16_desc(kStepTokens),
                                            p > 0 || ks > 0 ? 1u : 0u);
                             }
                             commit_to(s_full + t);
@@ -318,7 +318,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     } else if (warp >= TILES * 4) {
         // ---------------------------------------------------------- 8 bits -> f16 operands
         const int ct = tid - TILES * 128, cw = ct >> 5;
-        int64_t o = 0, g = 0;
+        uint32_t o = 0, g = 0;
         int unit = 0;
         for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
             for (int j = 0; j < w.steps; ++j, ++g) {
@@ -326,9 +326,9 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const bool diagonal = tok0 + kStepTokens > w.seen_least;  // some row does not see all of it
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++o) {
-                    const int rs = static_cast<int>(o % kRaws), os = static_cast<int>(o % kOps);
-                    wait(raw_full + rs, static_cast<uint32_t>(o / kRaws));
-                    if (o >= kOps) wait(op_empty + os, static_cast<uint32_t>(o / kOps - 1));
+                    const int rs = o % kRaws, os = o % kOps;
+                    wait(raw_full + rs, o / kRaws);
+                    if (o >= kOps) wait(op_empty + os, o / kOps - 1);
                     const unsigned char* raw = smem + F::off_raw + rs * F::kRaw;
                     unsigned char* op = smem + F::off_op + os * F::kOp;
                     const float4* sc = scales + (g % kScales) * 8;
@@ -421,8 +421,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         const int t = warp >> 2, trow = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t st = tmem + t * 256 + lanes, ot = st + 128;
-        int64_t g = 0;
-        uint32_t ss = 0, os = 0;
+        uint32_t g = 0, ss = 0, os = 0;
         int unit = 0;
         for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
             const int r = w.row_first + t * 128 + trow;
@@ -434,46 +433,45 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             float factor = 0.f;
             if (w.steps > 0) {
                 // ---- queries: f16 parts of q * 2^e, the sign of the scale in
-                // them.  A row is read twice (the second time from L1), eight
-                // vectors on their way at a time.
-                const int64_t qat = (row0 + i_row) * a.q_row + head * a.q_head;
-                float amax = 0.f;
-#pragma unroll 1
-                for (int d0 = 0; d0 < DP; d0 += 32) {
-                    float4 x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = live && d0 + 4 * i < c.dim ? load_q4(a.q, a.type, qat + d0 + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[i].x)), fmaxf(fabsf(x[i].y), fabsf(x[i].z))), fabsf(x[i].w));
-                }
-                int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
-                e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
-                float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-                factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                if (a.scale_log2 < 0.f) up = -up;
+                // them.  QL lanes read a row, four dims each; eight reads on
+                // their way at a time.
+                constexpr int QL = DP / 4, QR = 32 / QL;
+                const int64_t mine = live ? (row0 + i_row) * a.q_row + head * a.q_head : -1;
+                const int d = (lane % QL) * 4;
                 unsigned char* qb = smem + t * QP * F::kQTile;
 #pragma unroll 1
-                for (int d0 = 0; d0 < DP; d0 += 32) {
-                    float4 x[8];
+                for (int r0 = 0; r0 < 32; r0 += 8 * QR) {
+                    uint4 raw[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = live && d0 + 4 * i < c.dim ? load_q4(a.q, a.type, qat + d0 + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t at = __shfl_sync(~0u, mine, r0 + i * QR + lane / QL);
+                        raw[i] = load_q4(a.q, a.type, at + d, at >= 0 && d < c.dim);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = d0 / 8 + i;
-                        uint32_t h[4], lo[4];
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = q4_values(raw[i], a.type);
+                        const int row = r0 + i * QR + lane / QL;
+                        float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float4 y = x[2 * i + k];
-                            const float y0 = y.x * up, y1 = (INT8 ? y.z : y.y) * up, y2 = (INT8 ? y.y : y.z) * up, y3 = y.w * up;
-                            h[2 * k] = pack_f16x2(y0, y1), h[2 * k + 1] = pack_f16x2(y2, y3);
-                            if (QP == 2) lo[2 * k] = rest_f16x2(y0, y1, h[2 * k]), lo[2 * k + 1] = rest_f16x2(y2, y3, h[2 * k + 1]);
+                        for (int k = QL / 2; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
+                        int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
+                        e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
+                        float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                        const float f = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                        for (int k = 0; k < QR; ++k) {
+                            const float fk = __shfl_sync(~0u, f, k * QL);
+                            if (lane == r0 + i * QR + k) factor = fk;
                         }
-                        unsigned char* dst = qb + (ch >> 3) * 16384 + trow * 128 + (((ch & 7) ^ (trow & 7)) << 4);
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-                        if (QP == 2) *reinterpret_cast<uint4*>(dst + F::kQTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (a.scale_log2 < 0.f) up = -up;
+                        const float y0 = x.x * up, y1 = (INT8 ? x.z : x.y) * up;
+                        const float y2 = (INT8 ? x.y : x.z) * up, y3 = x.w * up;
+                        uint2 h = make_uint2(pack_f16x2(y0, y1), pack_f16x2(y2, y3));
+                        const int tr = (warp & 3) * 32 + row, ch = d >> 3;
+                        unsigned char* dst = qb + (ch >> 3) * 16384 + tr * 128 + (((ch & 7) ^ (tr & 7)) << 4) + (d & 4) * 2;
+                        *reinterpret_cast<uint2*>(dst) = h;
+                        if (QP == 2)
+                            *reinterpret_cast<uint2*>(dst + F::kQTile) = make_uint2(rest_f16x2(y0, y1, h.x), rest_f16x2(y2, y3, h.y));
                     }
                 }
                 fence_proxy_async_smem();
@@ -492,7 +490,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             int m = kNone, mu = kNone;
             float l = 0.f, kf = kBase, kr = kBase - static_cast<float>(kNone);
             for (int j = 0; j < w.steps; ++j, ++g, ++ss) {
-                wait(sc_full + g % kScales, static_cast<uint32_t>(g / kScales));
+                wait(sc_full + g % kScales, g / kScales);
                 wait(s_full + t, ss);
                 fence_after();
                 const float4* sc = scales + (g % kScales) * 8;
@@ -634,6 +632,11 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 ++os;
                 fence_after();
             }
+            // The rows go out through the tile's query memory (its MMAs are
+            // done), so that a row's 16-byte pieces leave together.
+            const int piece = a.type == QGKV_F32 ? 4 : 8;          // values of 16 bytes
+            unsigned char* stage = smem + t * QP * F::kQTile + (warp & 3) * (QP * F::kQTile / 4);
+            const int row_bytes = DP * 16 / piece;
 #pragma unroll 1
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t v[32];
@@ -641,19 +644,44 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     tmem_load32(ot + q * 32, v);
                     tmem_loaded();
                 }
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const int d = q * 32 + i;
-                        if (d >= c.dim) break;
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (!none)
-                            x = make_float4(__uint_as_float(v[i]) * f1 * f2v, __uint_as_float(v[i + 1]) * f1 * f2v,
-                                            __uint_as_float(v[i + 2]) * f1 * f2v, __uint_as_float(v[i + 3]) * f1 * f2v);
-                        store_out4(a.out, a.type, to * c.dim + d, x);
+                for (int i = 0; i < 32; ++i) v[i] = none || w.steps == 0 ? 0u : __float_as_uint(__uint_as_float(v[i]) * f1 * f2v);
+                if (a.type == QGKV_F32) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(stage + lane * row_bytes + (((q * 8 + i / 4) ^ (lane & 7)) << 4)) =
+                            make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t o4[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float lo = __uint_as_float(v[i + 2 * k]), hi = __uint_as_float(v[i + 2 * k + 1]);
+                            if (a.type == QGKV_F16) o4[k] = pack_f16x2(lo, hi);
+                            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o4[k]) : "f"(hi), "f"(lo));
+                        }
+                        *reinterpret_cast<uint4*>(stage + lane * row_bytes + (((q * 4 + i / 8) ^ (lane & 7)) << 4)) =
+                            make_uint4(o4[0], o4[1], o4[2], o4[3]);
                     }
                 }
             }
+            __syncwarp();
+            {
+                const int pieces = DP / piece, per = 32 / pieces;  // 16-byte pieces of a row, rows at once
+                const int64_t my_to = live ? to * c.dim : -1;
+#pragma unroll 4
+                for (int r0 = 0; r0 < 32; r0 += per) {
+                    const int row = r0 + lane / pieces, ch = lane % pieces;
+                    const int64_t at = __shfl_sync(~0u, my_to, row) ;
+                    if (at >= 0 && ch * piece < c.dim) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * row_bytes + ((ch ^ (row & 7)) << 4));
+                        if (a.type == QGKV_F32) *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at + ch * 4) = x;
+                        else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + ch * 8) = x;
+                    }
+                }
+            }
+            __syncwarp();  // ahead of what follows
             if (live && a.lse)
                 a.lse[to] = none ? -INFINITY : (static_cast<float>(m) + log2f(l)) * 0.69314718055994531f;
             if (!INT8 && live && nan_unit[unit & 7] == unit + 1) {
@@ -674,6 +702,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 }
             }
             fence_before();
+            // the tile's warps have left its query memory
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
         }
     }
     fence_before();
