@@ -27,6 +27,7 @@ constexpr int64_t kWsTotal = kWsPart + kWsPartBytes;
 
 // Counter words by user.
 constexpr int kCntAttn = 0;      // [kMaxAttnCtas]
+constexpr int kCntPrompt = 4096; // [2] (from the attention's counters)
 constexpr int kCntPages = 8192;  // [1]
 constexpr int kCntBeam = 8320;   // [QGKV_MAX_BATCH]
 

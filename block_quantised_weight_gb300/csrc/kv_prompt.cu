@@ -1,7 +1,7 @@
 // Attention of many query rows over the 8-bit paged cache (prompts and long
 // chunks) on the tcgen05 tensor cores.
 //
-// Mathematics: kv_attention.cu's.  A CTA takes ROWS = 256 query rows (tokens x
+// Mathematics: kv_rows.cuh's.  A CTA takes ROWS = 256 query rows (tokens x
 // heads of a group) of one cache head as two tiles of 128 (fp32 queries: one
 // tile of 128, whose q enters as two f16 parts), and walks the keys in
 // steps of 128 tokens:
@@ -35,6 +35,7 @@ namespace {
 constexpr int kStepTokens = 128;
 constexpr uint32_t kOps = 4;       // operand slots
 constexpr uint32_t kRaws = 2;      // raw slots
+constexpr uint32_t kUnits = 4;   // units handed to the roles ahead
 constexpr uint32_t kScales = 8;    // steps whose scales are held
 constexpr uint32_t kRow8 = 1024;  // bytes of 8 operand rows of 128 bytes
 
@@ -49,7 +50,7 @@ struct PShape {
     static constexpr int off_raw = off_op + kOps * kOp;
     static constexpr int off_scale = off_raw + kRaws * kRaw;
     static constexpr int off_bar = off_scale + kScales * 8 * 16;
-    static constexpr int smem = off_bar + 256;
+    static constexpr int smem = off_bar + 320;
     static constexpr int warps = TILES * 4 + 4 + 2;
     static constexpr int kCols = TILES == 2 ? 512 : 256;  // tensor memory: 256 columns a tile
     static_assert(smem <= 232448, "shared memory");
@@ -173,8 +174,12 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     uint64_t* p_full = s_full + 2;        // [2]
     uint64_t* q_full = p_full + 2;        // [2]
     uint64_t* o_done = q_full + 2;        // [2]
-    uint64_t* sc_full = o_done + 2;       // [kScales]
-    static_assert((2 * kRaws + 2 * kOps + 8 + kScales) * 8 <= 256, "barriers");
+    uint64_t* t_left = o_done + 2;        // [2]
+    uint64_t* sc_full = t_left + 2;       // [kScales]
+    uint64_t* unit_full = sc_full + kScales;
+    uint64_t* unit_empty = unit_full + kUnits;
+    static_assert((2 * kRaws + 2 * kOps + 10 + kScales + 2 * kUnits) * 8 <= 320, "barriers");
+    __shared__ volatile long long units[kUnits];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int nan_unit[8];
 
@@ -192,8 +197,10 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             mbar_init(p_full + i, 4);
             mbar_init(q_full + i, 4);
             mbar_init(o_done + i, 1);
+            mbar_init(t_left + i, 4);
         }
         for (int i = 0; i < kScales; ++i) mbar_init(sc_full + i, 1);
+        for (int i = 0; i < kUnits; ++i) mbar_init(unit_full + i, 1), mbar_init(unit_empty + i, TILES * 4 + 5);
         fence_mbar_init();
     }
     if (tid < 8) nan_unit[tid] = 0;
@@ -210,14 +217,48 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     // A wait that gave up ends all further waits, copies and MMAs of its
     // thread: the kernel then runs to its end within a few wait limits.
     bool dead = false;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead) dead = !mbar_wait_bounded(bar, parity & 1u, a.status);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // by whole warps
+        if (!dead) dead = __any_sync(~0u, !mbar_wait_bounded(bar, parity & 1u, a.status));
+    };
+    // The next unit: the copying warp takes it from a counter that all CTAs
+    // share (the longest first, so the CTAs end together) and hands it to the
+    // others; false after the last.
+    uint32_t turn = 0;
+    auto next_unit = [&]() {
+        const uint32_t slot = turn % kUnits;
+        wait(unit_full + slot, turn / kUnits);
+        const long long u = units[slot];
+        __syncwarp();
+        if (lane == 0) arrive_on(unit_empty + slot);
+        ++turn;
+        return !dead && u >= 0 && w.to(a, u);
     };
 
     if (warp == F::warps - 2) {
         // ---------------------------------------------------------- copies
         uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
-        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
+        for (;; ++turn) {
+            const uint32_t slot = turn % kUnits;
+            if (turn >= kUnits) wait(unit_empty + slot, turn / kUnits - 1);
+            long long u = 0;
+            if (lane == 0) u = atomicAdd(a.count + kCntPrompt, 1u);
+            u = __shfl_sync(~0u, u, 0);
+            const bool there = !dead && w.to(a, u);
+            if (lane == 0) {
+                units[slot] = there ? u : -1;
+                arrive_on(unit_full + slot);
+            }
+            __syncwarp();
+            if (!there) break;
+            // its queries on their way to L2
+            for (int r = w.row_first + lane; r < min(w.row_first + F::ROWS, w.nrows); r += 32) {
+                const int i_row = r / a.group;
+                const int64_t row0 = a.starts ? a.starts[w.b] : w.b;
+                const int64_t qat = (row0 + i_row) * a.q_row + (w.h * a.group + r - i_row * a.group) * a.q_head;
+                const int size = a.type == QGKV_F32 ? 4 : 2;
+                for (int at = 0; at < c.dim * size; at += 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + qat * size + at));
+            }
             const int32_t* table = a.table + static_cast<int64_t>(w.b) * a.width;
             auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
                 int id = -1;
@@ -265,7 +306,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         // ---------------------------------------------------------- MMAs
         uint32_t o = 0;                // operands taken
         uint32_t ps = 0, qs = 0;       // probabilities (per tile) and queries taken
-        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x) {
+        while (next_unit()) {
             if (w.steps == 0) continue;
             for (int j = 0; j <= w.steps; ++j) {
                 const uint32_t ko = o + 2 * j, vo = ko - 1;  // K of step j, V of step j - 1
@@ -320,7 +361,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         const int ct = tid - TILES * 128, cw = ct >> 5;
         uint32_t o = 0, g = 0;
         int unit = 0;
-        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
+        for (; next_unit(); ++unit) {
             for (int j = 0; j < w.steps; ++j, ++g) {
                 const int tok0 = j * kStepTokens;
                 const bool diagonal = tok0 + kStepTokens > w.seen_least;  // some row does not see all of it
@@ -389,17 +430,17 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
                             for (int i = 0; i < 4; ++i) v_codes<INT8>(x[2 * i], x[2 * i + 1], r[i]);
                             // the order of a lane's four dims turns with the lane, so that eight lanes meet eight bank groups
-                            const int turn = (lane >> 1) & 3;
+                            const int spin = (lane >> 1) & 3;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                uint32_t s0 = turn & 1 ? r[i][1] : r[i][0], s1 = turn & 1 ? r[i][2] : r[i][1];
-                                uint32_t s2 = turn & 1 ? r[i][3] : r[i][2], s3 = turn & 1 ? r[i][0] : r[i][3];
-                                r[i][0] = turn & 2 ? s2 : s0, r[i][1] = turn & 2 ? s3 : s1;
-                                r[i][2] = turn & 2 ? s0 : s2, r[i][3] = turn & 2 ? s1 : s3;
+                                uint32_t s0 = spin & 1 ? r[i][1] : r[i][0], s1 = spin & 1 ? r[i][2] : r[i][1];
+                                uint32_t s2 = spin & 1 ? r[i][3] : r[i][2], s3 = spin & 1 ? r[i][0] : r[i][3];
+                                r[i][0] = spin & 2 ? s2 : s0, r[i][1] = spin & 2 ? s3 : s1;
+                                r[i][2] = spin & 2 ? s0 : s2, r[i][3] = spin & 2 ? s1 : s3;
                             }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int dim = word * 4 + ((i + turn) & 3);
+                                const int dim = word * 4 + ((i + spin) & 3);
                                 *reinterpret_cast<uint4*>(op + (t0 >> 6) * (DP * 128) + dim * 128 +
                                                           ((((t0 >> 3) & 7) ^ (dim & 7)) << 4)) =
                                     make_uint4(r[0][i], r[1][i], r[2][i], r[3][i]);
@@ -423,7 +464,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         const uint32_t st = tmem + t * 256 + lanes, ot = st + 128;
         uint32_t g = 0, ss = 0, os = 0;
         int unit = 0;
-        for (int64_t u = blockIdx.x; w.to(a, u); u += gridDim.x, ++unit) {
+        for (; next_unit(); ++unit) {
             const int r = w.row_first + t * 128 + trow;
             const bool live = r < w.nrows;
             const int i_row = r / a.group;
@@ -703,11 +744,18 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             }
             fence_before();
             // the tile's warps have left its query memory
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+            __syncwarp();
+            if (lane == 0) arrive_on(t_left + t);
+            wait(t_left + t, static_cast<uint32_t>(unit));
         }
     }
     fence_before();
     __syncthreads();
+    if (tid == 0 && atomicAdd(a.count + kCntPrompt + 1, 1u) == gridDim.x - 1) {
+        // the last CTA to end leaves the counters ready for the next call
+        a.count[kCntPrompt] = 0u;
+        a.count[kCntPrompt + 1] = 0u;
+    }
     if (warp == F::warps - 1) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F::kCols) : "memory");

@@ -7,9 +7,9 @@
 //   l = sum p[t],   o = sum p[t] * vs[page] * vcode[t],   out = o / l
 // Codes are exact in f16.  q * 2^j (a power of two that brings the row's
 // largest value to [2^14, 2^15)) and p * vs * 2^k enter the products in f16:
-// 16-bit queries and their probabilities as one part (q exact, p rounded to 11
-// bits, below the rounding of the output), fp32 ones as two, hi and lo, about
-// 22 bits.  m is at least the running maximum less 2 and k is chosen by a
+// 16-bit queries enter as one part, exactly, fp32 ones as two, hi and lo, about
+// 22 bits; probabilities as one part (11 bits) where the output is bf16, else
+// as two.  m is at least the running maximum less 2 and k is chosen by a
 // bound u on s + log2 vs (k = 12 + m - u), so that what reaches o is at most
 // 2^14 and its largest part near that however the scales of the blocks
 // differ.  m and u are integers, which makes every rescaling a power of two,
@@ -36,6 +36,7 @@
 // normalised partial results in the workspace and the last to arrive at a
 // counter joins them in the order of the line (bits do not depend on the
 // order of arrival).
+#pragma once
 #include <atomic>
 #include <type_traits>
 
@@ -108,7 +109,8 @@ struct Shape {
     static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
 };
 
-template <int DC, int MT, int PARTS, bool INT8, int MINB>
+// QP, PP: f16 parts of q and of p.
+template <int DC, int MT, int QP, int PP, bool INT8, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB)
 qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     int grid) {
@@ -117,12 +119,12 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     constexpr int VW = DC == 1 ? 2 : 4;    // 32-bit words of one V read
     constexpr int VL = F::NB;              // V reads per token row
     extern __shared__ __align__(1024) unsigned char smem[];
-    uint2* qf = reinterpret_cast<uint2*>(smem + F::off_q(PARTS));         // [PARTS][MT][4 * DC][32]
-    float* ws = reinterpret_cast<float*>(smem + F::off_ws(PARTS));        // [4][RU] largest |q|, later log-sums
+    uint2* qf = reinterpret_cast<uint2*>(smem + F::off_q(QP));         // [QP][MT][4 * DC][32]
+    float* ws = reinterpret_cast<float*>(smem + F::off_ws(QP));        // [4][RU] largest |q|, later log-sums
     float* wb = ws + 4 * RU;                                              // [4][RU] sums of q
-    int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(PARTS));  // [RU] output rows, -1 past the last
+    int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(QP));  // [RU] output rows, -1 past the last
     int* limits = reinterpret_cast<int*>(orow + RU);                      // [RU] tokens that a row sees
-    int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(PARTS));  // [batch + 1]
+    int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(QP));  // [batch + 1]
     int2* seqs = reinterpret_cast<int2*>(pre + a.batch + 1);              // [batch] rows, length
     __shared__ int64_t warp_sum[4];
     __shared__ int last_flag;
@@ -132,7 +134,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     const KVLayer& c = a.c;
     // this warp's ring of stages and their barriers
     unsigned char* ring = smem + warp * F::kRing;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + F::off_bar(PARTS)) + warp * S;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + F::off_bar(QP)) + warp * S;
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
@@ -322,7 +324,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 f.y = pack_f16x2(x2, x3);
                 qf[(mt * 4 * DC + cc * 4 + warp) * 32 + lane] = f;
                 if (INT8) fadd2(sum, h2_to_f2(f.x)), fadd2(sum, h2_to_f2(f.y));
-                if (PARTS == 2) {
+                if (QP == 2) {
                     uint2 fl;
                     fl.x = rest_f16x2(x0, x1, f.x);
                     fl.y = rest_f16x2(x2, x3, f.y);
@@ -421,7 +423,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                             k_codes<INT8>(w == 0 ? q4.x : w == 1 ? q4.y : w == 2 ? q4.z : q4.w, ka[s][j], ka[s][j + 2]);
                         }
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
+                    for (int p = 0; p < QP; ++p)
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             const uint2 f = qf[((p * MT + mt) * 4 * DC + cc * 4 + w) * 32 + lane];
@@ -447,7 +449,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                             if (mine >= limit[mt][i & 1] || mine >= tok1 || !there[s]) sc[mt][s][i] = __int_as_float(kMasked);
                         }
             }
-            uint32_t pb[PARTS][MT][NS][2];
+            uint32_t pb[PP][MT][NS][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 float y[NS][4];
@@ -516,8 +518,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t hi2 = pack_f16x2(y[s][2 * j], y[s][2 * j + 1]);
                         pb[0][mt][s][j] = transpose8x8(hi2);
-                        if (PARTS == 2)
-                            pb[PARTS - 1][mt][s][j] = transpose8x8(rest_f16x2(y[s][2 * j], y[s][2 * j + 1], hi2));
+                        if (PP == 2)
+                            pb[PP - 1][mt][s][j] = transpose8x8(rest_f16x2(y[s][2 * j], y[s][2 * j + 1], hi2));
                     }
                 }
             }
@@ -591,7 +593,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                                for (int p = 0; p < PARTS; ++p)
+                                for (int p = 0; p < PP; ++p)
                                     mma16816(o[mt][x * 2 * VW + 2 * w + i], c01[2 * i], c01[2 * i + 1], c23[2 * i],
                                              c23[2 * i + 1], pb[p][mt][s][0], pb[p][mt][s][1]);
                     }
@@ -769,20 +771,20 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     }
 }
 
-template <int DC, int MT, int PARTS, bool INT8, int MINB>
+template <int DC, int MT, int QP, int PP, bool INT8, int MINB>
 int launch_one(const AttnArgs& a, cudaStream_t s) {
     const int dev = current_device();
     const int sms = sm_count(dev);
     if (sms <= 0) return cuda_fail(cudaGetLastError());
     using F = Shape<DC, MT>;
-    constexpr int fixed = F::off_pre(PARTS);
-    static_assert(F::off_rows(PARTS) % 16 == 0 && F::off_bar(PARTS) % 8 == 0 && F::off_q(PARTS) % 16 == 0, "alignment");
+    constexpr int fixed = F::off_pre(QP);
+    static_assert(F::off_rows(QP) % 16 == 0 && F::off_bar(QP) % 8 == 0 && F::off_q(QP) % 16 == 0, "alignment");
     CUtensorMap kmap, vmap;
     if (!encode_cache(&kmap, a.c, a.c.k, F::RB, 16, true) || !encode_cache(&vmap, a.c, a.c.v, F::RB, 16, true))
         return cuda_fail(cudaGetLastError());
     const int most = fixed + (QGKV_MAX_BATCH + 1) * 16;
     static std::atomic<bool> done[64];
-    auto kern = qg_attn_rows_kernel<DC, MT, PARTS, INT8, MINB>;
+    auto kern = qg_attn_rows_kernel<DC, MT, QP, PP, INT8, MINB>;
     if (!done[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
             return cuda_fail(cudaGetLastError());
@@ -793,37 +795,27 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     return launch_status();
 }
 
-template <int PARTS, bool INT8>
+template <int QP, int PP, bool INT8>
 int launch_typed(const AttnArgs& a, cudaStream_t s) {
     // 16 rows a unit where the mean sequence has more than 8 (the codes are
-    // then read half as often); 256-dim heads keep 8 for their registers
+    // then read half as often); 256-dim heads keep 8 for their registers.
+    // int8's conversions hold more registers: two CTAs an SM instead of three
+    // (attn_long 121 us for 130; e4m3's attn_batch 58 us for 56).
     const bool wide = a.rows * a.group > 8 * static_cast<int64_t>(a.batch);
-    if (a.c.dim <= 64) return wide ? launch_one<1, 2, PARTS, INT8, 3>(a, s) : launch_one<1, 1, PARTS, INT8, 3>(a, s);
-    if (a.c.dim <= 128) return wide ? launch_one<2, 2, PARTS, INT8, 2>(a, s) : launch_one<2, 1, PARTS, INT8, INT8 ? 2 : 3>(a, s);
-    return launch_one<4, 1, PARTS, INT8, 2>(a, s);
+    if (a.c.dim <= 64) return wide ? launch_one<1, 2, QP, PP, INT8, 3>(a, s) : launch_one<1, 1, QP, PP, INT8, 3>(a, s);
+    if (a.c.dim <= 128)
+        return wide ? launch_one<2, 2, QP, PP, INT8, 2>(a, s) : launch_one<2, 1, QP, PP, INT8, INT8 ? 2 : 3>(a, s);
+    return launch_one<4, 1, QP, PP, INT8, 2>(a, s);
 }
 
 }  // namespace
 
-bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens,
-                  bool swizzle) {
-    auto encode = tensor_map_encoder();
-    if (!encode) return false;
-    const cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.dim), cuuint64_t(1) << c.log2p,
-                                static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
-    const cuuint64_t gstride[3] = {static_cast<cuuint64_t>(c.token_stride), static_cast<cuuint64_t>(c.head_stride),
-                                   static_cast<cuuint64_t>(c.page_stride)};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_tokens), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), gdim, gstride, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s) {
-    if (a.type == QGKV_F32) return int8 ? launch_typed<2, true>(a, s) : launch_typed<2, false>(a, s);
-    return int8 ? launch_typed<1, true>(a, s) : launch_typed<1, false>(a, s);
+template <bool INT8>
+int launch_rows(const AttnArgs& a, cudaStream_t s) {
+    if (a.type == QGKV_F32) return launch_typed<2, 2, INT8>(a, s);
+    // f16 outputs round as finely as one f16 part of p would: two
+    if (a.type == QGKV_F16) return launch_typed<1, 2, INT8>(a, s);
+    return launch_typed<1, 1, INT8>(a, s);
 }
 
 }  // namespace qg

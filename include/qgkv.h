@@ -110,11 +110,11 @@ QG_API int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, co
  * the same type, dense, 16-byte aligned.  lse: fp32 [rows][q_heads] or null.
  * A row that sees nothing gives 0 and -inf.  Tokens a row does not see do not
  * reach it, whatever their codes.
- * Numerics: codes enter the tensor cores exactly (f16).  fp32 q and its
- * probabilities enter as the sum of two f16 parts (about 22 bits, and no
- * weight probability * scale below 2^-37 of the row's largest); 16-bit q
- * enters exactly and its probabilities rounded to f16 (11 bits, below the
- * rounding of the output).  All sums are fp32.  Repeated calls give the same bits. */
+ * Numerics: codes enter the tensor cores exactly (f16).  fp32 q enters as the
+ * sum of two f16 parts (about 22 bits), 16-bit q exactly.  Probabilities enter
+ * as two parts (and no weight probability * scale below 2^-37 of the row's
+ * largest), for bf16 q as one (11 bits, below the output's rounding).
+ * All sums are fp32.  Repeated calls give the same bits. */
 QG_API int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                           int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
                           int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,

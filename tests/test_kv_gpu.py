@@ -3,8 +3,8 @@ implementations in 64 bits.
 
 Attention tolerance.  With A = sum p |v| of an output, S the largest
 scale * sum |q k| of its row and L its tokens: q and p of fp32 queries enter as
-two f16 parts (relative 2^-22 each), 16-bit q exactly and their p as one f16
-part (2^-11), the scores' fp32 sums and scaling are off by at most
+two f16 parts (relative 2^-22 each), 16-bit q exactly, p of bf16 queries as one
+f16 part (2^-11), the scores' fp32 sums and scaling are off by at most
 4 S 2^-22 (which changes p by that factor), 2^x by 2^-22, and sums of L / 64
 steps plus joins by (16 + L / 64) 2^-22 of A; the output's own rounding adds
 eps / 2.  A weight p * scale far below the row's largest, W, is cut at f16's
@@ -157,7 +157,7 @@ def check_attention(kv, ws, lens, rows, hq, heads, dim, page, fmt, order, dtype,
     out, lse = kv.kv_attention(cache, layer, q, table, ln, starts=starts, scale=scale, return_lse=True, workspace=ws)
     again = kv.kv_attention(cache, layer, q, table, ln, starts=starts, scale=scale, workspace=ws)
     ref = attention_ref(cache, layer, q, table, lens, st, scale or 1 / math.sqrt(dim))
-    close(out, lse, ref, max(lens), DT[dtype], one_part=dtype != "f32")
+    close(out, lse, ref, max(lens), DT[dtype], one_part=dtype == "bf16")
     assert torch.equal(out, again)  # the same bits whoever joins the parts
 
 
