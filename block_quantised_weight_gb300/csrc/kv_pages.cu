@@ -23,6 +23,9 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kChunk = 4 * kPlanThreads;  // pages a CTA counts
 static_assert(QGKV_MAX_PAGES / kChunk <= 4096, "chunk counts exceed the workspace");
+// Up to this many chunks one CTA counts them all, in the launch before: about a
+// microsecond a chunk, where a launch of its own costs two and more on the host.
+constexpr int kMergeChunks = 4;
 
 __device__ __forceinline__ int pages_of(int len, int log2p) { return (len + (1 << log2p) - 1) >> log2p; }
 
@@ -113,12 +116,12 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 4;  // 16-byte vectors a thread has in flight
 constexpr int kCopyBytes = kCopyThreads * kCopyVec * 16;
 
-__global__ void __launch_bounds__(kCopyThreads) qg_copy_pages_kernel(const CopyArgs a) {
+__device__ __forceinline__ void copy_pages(const CopyArgs& a, int cta, int ctas) {
     int64_t n = a.most;
     if (a.count) n = min(n, static_cast<int64_t>(*a.count));
     const int parts = (a.bytes + kCopyBytes - 1) / kCopyBytes;
     const int64_t per = static_cast<int64_t>(a.layers) * 2 * parts;
-    for (int64_t i = blockIdx.x; i < n * per; i += gridDim.x) {
+    for (int64_t i = cta; i < n * per; i += ctas) {
         const int64_t pair = i / per;
         int r = static_cast<int>(i - pair * per);
         const int part = r % parts;
@@ -148,6 +151,10 @@ __global__ void __launch_bounds__(kCopyThreads) qg_copy_pages_kernel(const CopyA
     }
 }
 
+__global__ void __launch_bounds__(kCopyThreads) qg_copy_pages_kernel(const CopyArgs a) {
+    copy_pages(a, blockIdx.x, gridDim.x);
+}
+
 // ---------------------------------------------------------------- fork
 
 struct ForkArgs {
@@ -169,64 +176,29 @@ struct ForkArgs {
     unsigned* status;
 };
 
-// CTAs 0 .. batch-1: an old sequence's pages gain (children - 1) references.
-// The others: a new sequence's table row and length.
-__global__ void __launch_bounds__(256) qg_fork_rows_kernel(const ForkArgs a) {
-    __shared__ int children;
-    if (static_cast<int>(blockIdx.x) < a.batch) {
-        const int r = blockIdx.x;
-        if (threadIdx.x == 0) children = 0;
-        __syncthreads();
-        int mine = 0;
-        for (int i = threadIdx.x; i < a.batch2; i += blockDim.x) mine += a.parent[i] == r ? 1 : 0;
-        if (mine) atomicAdd(&children, mine);
-        __syncthreads();
-        const int change = children - 1;
-        if (change == 0) return;
-        const int n = pages_of(length_of(a.lens, r, a.width, a.log2p, a.status), a.log2p);
-        for (int j = threadIdx.x; j < n; j += blockDim.x) {
-            const int id = a.table[r * a.width + j];
-            if (id >= 0 && id < a.pages) atomicAdd(a.delta + id, change);
-            else atomicOr(a.status, kStatusBounds);
-        }
-    } else {
-        const int i = blockIdx.x - a.batch;
-        const int p = a.parent[i];
-        const bool ok = p >= 0 && p < a.batch;
-        if (!ok && threadIdx.x == 0) atomicOr(a.status, kStatusBounds);
-        const int len = ok ? length_of(a.lens, p, a.width, a.log2p, a.status) : 0;
-        const int n = pages_of(len, a.log2p);
-        for (int64_t j = threadIdx.x; j < a.width; j += blockDim.x)
-            a.table2[i * a.width + j] = j < n ? a.table[p * a.width + j] : -1;
-        if (threadIdx.x == 0) a.lens2[i] = len;
-    }
+// Pages of one chunk: refs2 = refs + delta, delta back to 0; the chunk's free pages are counted.
+__device__ __forceinline__ void fork_count(const ForkArgs& a, int chunk, int* red) {
+    const int64_t p = static_cast<int64_t>(chunk) * kChunk + threadIdx.x * 4;
+    int4 r = load4(a.refs, p, a.pages, 1);
+    const int4 d = load4(a.delta, p, a.pages, 0);
+    if (d.x | d.y | d.z | d.w) store4(a.delta, p, a.pages, make_int4(0, 0, 0, 0));
+    r.x += d.x, r.y += d.y, r.z += d.z, r.w += d.w;
+    store4(a.refs2, p, a.pages, r);
+    int before;
+    const int zeros = block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), before, red);
+    if (threadIdx.x == 0) a.chunks[chunk] = zeros;
 }
 
-// refs2 = refs + delta, delta back to 0, free pages counted by chunk; the
-// last CTA finds who needs a page of its own and hands out the free ones.
-__global__ void __launch_bounds__(kPlanThreads) qg_fork_plan_kernel(const ForkArgs a) {
-    extern __shared__ int32_t smem[];  // tail [batch2], free list [batch2]
-    __shared__ int red[32];
-    __shared__ int flag;
+// Who needs a page of its own gets the lowest free ones.  One CTA; smem: tail
+// [batch2], list [batch2].
+__device__ __forceinline__ void fork_plan(const ForkArgs& a, int32_t* smem, int* red) {
     const int tid = threadIdx.x;
-    {
-        const int64_t p = static_cast<int64_t>(blockIdx.x) * kChunk + tid * 4;
-        int4 r = load4(a.refs, p, a.pages, 1);
-        const int4 d = load4(a.delta, p, a.pages, 0);
-        if (d.x | d.y | d.z | d.w) store4(a.delta, p, a.pages, make_int4(0, 0, 0, 0));
-        r.x += d.x, r.y += d.y, r.z += d.z, r.w += d.w;
-        store4(a.refs2, p, a.pages, r);
-        int before;
-        const int zeros = block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), before, red);
-        if (tid == 0) a.chunks[blockIdx.x] = zeros;
-    }
-    if (!last_cta(a.counter, &flag)) return;
     int32_t* tail = smem;
     int32_t* list = smem + a.batch2;
     // the partly filled last page of each new sequence, -1 where it has none
     for (int i = tid; i < a.batch2; i += kPlanThreads) {
-        const int len = a.lens2[i];
-        const int id = (len & ((1 << a.log2p) - 1)) ? a.table2[i * a.width + (len >> a.log2p)] : -1;
+        const int len = __ldcg(a.lens2 + i);
+        const int id = (len & ((1 << a.log2p) - 1)) ? __ldcg(a.table2 + i * a.width + (len >> a.log2p)) : -1;
         tail[i] = id >= 0 && id < a.pages ? id : -1;
     }
     __syncthreads();
@@ -250,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) qg_fork_plan_kernel(const ForkAr
         const int sum = block_scan(copy, before, red);
         if (copy) {
             a.src[needed + before] = mine;
-            list[needed + before] = i;  // the sequence, for now
+            list[needed + before] = i;
         }
         needed += sum;
     }
@@ -283,10 +255,60 @@ __global__ void __launch_bounds__(kPlanThreads) qg_fork_plan_kernel(const ForkAr
         const int i = list[k];
         const int from = a.src[k];
         const int to = k < granted ? a.dst[k] : -1;
-        a.table2[i * a.width + (a.lens2[i] >> a.log2p)] = to;
+        a.table2[i * a.width + (__ldcg(a.lens2 + i) >> a.log2p)] = to;
         atomicSub(a.refs2 + from, 1);
         if (to >= 0) a.refs2[to] = 1;
     }
+}
+
+// CTAs 0 .. batch-1: an old sequence's pages gain (children - 1) references.
+// The others: a new sequence's table row and length.  With few pages (`merged`)
+// the last CTA to end also counts and plans, which saves a launch; with many
+// the counting is spread over CTAs of its own (qg_fork_plan_kernel).
+__global__ void __launch_bounds__(kPlanThreads) qg_fork_rows_kernel(const ForkArgs a, int merged) {
+    extern __shared__ int32_t smem[];
+    __shared__ int children;
+    __shared__ int red[32];
+    __shared__ int flag;
+    if (static_cast<int>(blockIdx.x) < a.batch) {
+        const int r = blockIdx.x;
+        if (threadIdx.x == 0) children = 0;
+        __syncthreads();
+        int mine = 0;
+        for (int i = threadIdx.x; i < a.batch2; i += blockDim.x) mine += a.parent[i] == r ? 1 : 0;
+        if (mine) atomicAdd(&children, mine);
+        __syncthreads();
+        const int change = children - 1;
+        const int n = change ? pages_of(length_of(a.lens, r, a.width, a.log2p, a.status), a.log2p) : 0;
+        for (int j = threadIdx.x; j < n; j += blockDim.x) {
+            const int id = a.table[r * a.width + j];
+            if (id >= 0 && id < a.pages) atomicAdd(a.delta + id, change);
+            else atomicOr(a.status, kStatusBounds);
+        }
+    } else {
+        const int i = blockIdx.x - a.batch;
+        const int p = a.parent[i];
+        const bool ok = p >= 0 && p < a.batch;
+        if (!ok && threadIdx.x == 0) atomicOr(a.status, kStatusBounds);
+        const int len = ok ? length_of(a.lens, p, a.width, a.log2p, a.status) : 0;
+        const int n = pages_of(len, a.log2p);
+        for (int64_t j = threadIdx.x; j < a.width; j += blockDim.x)
+            a.table2[i * a.width + j] = j < n ? a.table[p * a.width + j] : -1;
+        if (threadIdx.x == 0) a.lens2[i] = len;
+    }
+    if (!merged || !last_cta(a.counter, &flag)) return;
+    for (int ch = 0; ch * static_cast<int64_t>(kChunk) < a.pages; ++ch) fork_count(a, ch, red);
+    __syncthreads();
+    fork_plan(a, smem, red);
+}
+
+// A CTA counts a chunk; the last plans.
+__global__ void __launch_bounds__(kPlanThreads) qg_fork_plan_kernel(const ForkArgs a) {
+    extern __shared__ int32_t smem[];
+    __shared__ int red[32];
+    __shared__ int flag;
+    fork_count(a, blockIdx.x, red);
+    if (last_cta(a.counter, &flag)) fork_plan(a, smem, red);
 }
 
 // ---------------------------------------------------------------- compact
@@ -313,9 +335,9 @@ struct CompactArgs {
     unsigned* status;
 };
 
-__global__ void __launch_bounds__(256) qg_drop_rows_kernel(const CompactArgs a) {
-    const int b = blockIdx.x;
-    if (!a.drop[b]) return;
+// A dropped sequence's pages lose a reference.
+__device__ __forceinline__ void drop_row(const CompactArgs& a, int b) {
+    if (!a.drop || !a.drop[b]) return;
     const int n = pages_of(length_of(a.lens, b, a.width, a.log2p, a.status), a.log2p);
     for (int j = threadIdx.x; j < n; j += blockDim.x) {
         const int id = a.table[b * a.width + j];
@@ -324,28 +346,28 @@ __global__ void __launch_bounds__(256) qg_drop_rows_kernel(const CompactArgs a) 
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) qg_compact_count_kernel(const CompactArgs a) {
-    __shared__ int red[32];
-    __shared__ int flag;
+// Pages of one chunk: counts after the drops, delta back to 0, pages held.
+__device__ __forceinline__ void compact_count(const CompactArgs& a, int chunk, int* red) {
+    const int64_t p = static_cast<int64_t>(chunk) * kChunk + threadIdx.x * 4;
+    int4 r = load4(a.refs, p, a.pages, 0);
+    const int4 d = load4(a.delta, p, a.pages, 0);
+    if (d.x | d.y | d.z | d.w) store4(a.delta, p, a.pages, make_int4(0, 0, 0, 0));
+    r.x += d.x, r.y += d.y, r.z += d.z, r.w += d.w;
+    store4(a.now, p, a.pages, r);
+    int before;
+    const int held = block_scan((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), before, red);
+    if (threadIdx.x == 0) a.chunks[chunk] = held;
+}
+
+// One CTA: n, the pages held below each chunk, and how many of them lie below n.
+__device__ __forceinline__ void compact_total(const CompactArgs& a, int chunks, int* red) {
     const int tid = threadIdx.x;
-    {
-        const int64_t p = static_cast<int64_t>(blockIdx.x) * kChunk + tid * 4;
-        int4 r = load4(a.refs, p, a.pages, 0);
-        const int4 d = load4(a.delta, p, a.pages, 0);
-        if (d.x | d.y | d.z | d.w) store4(a.delta, p, a.pages, make_int4(0, 0, 0, 0));
-        r.x += d.x, r.y += d.y, r.z += d.z, r.w += d.w;
-        store4(a.now, p, a.pages, r);
-        int before;
-        const int held = block_scan((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), before, red);
-        if (tid == 0) a.chunks[blockIdx.x] = held;
-    }
-    if (!last_cta(a.counter, &flag)) return;
-    const int mine = tid < static_cast<int>(gridDim.x) ? __ldcg(a.chunks + tid) : 0;  // at most 256 chunks
+    const int mine = tid < chunks ? __ldcg(a.chunks + tid) : 0;  // at most 256 chunks
     int before;
     const int n = block_scan(mine, before, red);
-    if (tid < static_cast<int>(gridDim.x)) a.chunks[tid] = before;
+    if (tid < chunks) a.chunks[tid] = before;
     __syncthreads();
-    const int ch = min(n / kChunk, static_cast<int>(gridDim.x) - 1);  // the chunk that n lies in
+    const int ch = min(n / kChunk, chunks - 1);  // the chunk that n lies in
     const int64_t p = static_cast<int64_t>(ch) * kChunk + tid * 4;
     const int4 r = load4(a.now, p, a.pages, 0);
     int x;
@@ -358,17 +380,17 @@ __global__ void __launch_bounds__(kPlanThreads) qg_compact_count_kernel(const Co
         a.scalars[2] = n - held_below;
         *a.count = n;
     }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kPlanThreads) qg_compact_list_kernel(const CompactArgs a) {
-    __shared__ int red[32];
-    const int tid = threadIdx.x;
-    const int n = a.scalars[0], held_below = a.scalars[1];
-    const int64_t p = static_cast<int64_t>(blockIdx.x) * kChunk + tid * 4;
+// The holes below n and the held pages from n on, each in order.
+__device__ __forceinline__ void compact_list(const CompactArgs& a, int chunk, int* red) {
+    const int n = __ldcg(a.scalars), held_below = __ldcg(a.scalars + 1);
+    const int64_t p = static_cast<int64_t>(chunk) * kChunk + threadIdx.x * 4;
     const int4 r = load4(a.now, p, a.pages, 0);
     int at;
     block_scan((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), at, red);
-    at += a.chunks[blockIdx.x];  // held pages below p
+    at += __ldcg(a.chunks + chunk);  // held pages below p
     const int v[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -391,8 +413,37 @@ __global__ void __launch_bounds__(kPlanThreads) qg_compact_list_kernel(const Com
     }
 }
 
-// CTAs 0 .. batch-1: a table row; the others: the counts of the filled holes.
-__global__ void __launch_bounds__(256) qg_compact_rows_kernel(const CompactArgs a) {
+// Few pages: the drops, then all the counting in the last CTA to end.
+__global__ void __launch_bounds__(kPlanThreads) qg_compact_plan_kernel(const CompactArgs a) {
+    __shared__ int red[32];
+    __shared__ int flag;
+    drop_row(a, blockIdx.x);
+    if (!last_cta(a.counter, &flag)) return;
+    const int chunks = static_cast<int>((a.pages + kChunk - 1) / kChunk);
+    for (int ch = 0; ch < chunks; ++ch) compact_count(a, ch, red);
+    __syncthreads();
+    compact_total(a, chunks, red);
+    for (int ch = 0; ch < chunks; ++ch) compact_list(a, ch, red);
+}
+
+// Many pages: the same in three launches, a CTA a chunk.
+__global__ void __launch_bounds__(256) qg_drop_rows_kernel(const CompactArgs a) { drop_row(a, blockIdx.x); }
+
+__global__ void __launch_bounds__(kPlanThreads) qg_compact_count_kernel(const CompactArgs a) {
+    __shared__ int red[32];
+    __shared__ int flag;
+    compact_count(a, blockIdx.x, red);
+    if (last_cta(a.counter, &flag)) compact_total(a, gridDim.x, red);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) qg_compact_list_kernel(const CompactArgs a) {
+    __shared__ int red[32];
+    compact_list(a, blockIdx.x, red);
+}
+
+// CTAs 0 .. batch-1: a table row; then a few for the counts of the filled
+// holes; the others copy the pages.
+__global__ void __launch_bounds__(kCopyThreads) qg_compact_move_kernel(const CompactArgs a, const CopyArgs copy, int ref_ctas) {
     const int n = a.scalars[0], moves = a.scalars[2];
     if (static_cast<int>(blockIdx.x) < a.batch) {
         const int b = blockIdx.x;
@@ -412,13 +463,15 @@ __global__ void __launch_bounds__(256) qg_compact_rows_kernel(const CompactArgs 
             a.table2[b * a.width + j] = to;
         }
         if (threadIdx.x == 0) a.lens2[b] = len;
-    } else {
+    } else if (static_cast<int>(blockIdx.x) < a.batch + ref_ctas) {
         for (int64_t i = (blockIdx.x - a.batch) * blockDim.x + threadIdx.x; i < moves && i < a.pages;
-             i += (gridDim.x - a.batch) * blockDim.x) {
+             i += ref_ctas * blockDim.x) {
             const int to = a.holes[i], from = a.movers[i];
             if (in_pages(to, a.pages) && in_pages(from, a.pages)) a.refs2[to] = a.now[from];
             else atomicOr(a.status, kStatusBounds);
         }
+    } else {
+        copy_pages(copy, blockIdx.x - a.batch - ref_ctas, gridDim.x - a.batch - ref_ctas);
     }
 }
 
@@ -551,20 +604,32 @@ int plan_smem(const void* kern, int bytes, std::atomic<int>* done, int dev) {
 
 }  // namespace
 
-int launch_copy_pages(const qgkv_cache& c, const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
-                      unsigned* status, cudaStream_t s) {
-    if (most == 0) return QG_OK;
+namespace {
+CopyArgs copy_args(const qgkv_cache& c, const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
+                   unsigned* status) {
     CopyArgs a = {};
     a.base[0] = c.k, a.base[1] = c.v, a.scale[0] = c.k_scale, a.scale[1] = c.v_scale;
     a.layer_stride = c.layer_stride, a.page_stride = c.page_stride, a.pages = c.pages;
     a.layers = static_cast<int>(c.layers), a.heads = c.heads;
     a.bytes = c.heads * c.page_tokens * c.head_dim;
     a.src = src, a.dst = dst, a.count = count, a.most = most, a.status = status;
+    return a;
+}
+
+// Eight CTAs an SM, or one for each piece there can be.
+int copy_ctas(const CopyArgs& a, int sms) {
+    const int64_t items = a.most * a.layers * 2 * ((a.bytes + kCopyBytes - 1) / kCopyBytes);
+    return static_cast<int>(std::min<int64_t>(items, static_cast<int64_t>(sms) * 8));
+}
+}  // namespace
+
+int launch_copy_pages(const qgkv_cache& c, const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
+                      unsigned* status, cudaStream_t s) {
+    if (most == 0) return QG_OK;
+    const CopyArgs a = copy_args(c, src, dst, count, most, status);
     const int sms = sm_count(current_device());
     if (sms <= 0) return cuda_fail(cudaGetLastError());
-    const int64_t items = most * c.layers * 2 * ((a.bytes + kCopyBytes - 1) / kCopyBytes);
-    const int grid = static_cast<int>(std::min<int64_t>(items, static_cast<int64_t>(sms) * 8));
-    qg_copy_pages_kernel<<<grid, kCopyThreads, 0, s>>>(a);
+    qg_copy_pages_kernel<<<copy_ctas(a, sms), kCopyThreads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -574,7 +639,10 @@ int launch_fork(const qgkv_cache& c, const int32_t* table, int64_t width, const 
     const int dev = current_device();
     if (dev < 0) return cuda_fail(cudaGetLastError());
     static std::atomic<int> done[64];
-    const int rc = plan_smem(reinterpret_cast<const void*>(qg_fork_plan_kernel), QGKV_MAX_BATCH * 8, done, dev);
+    static std::atomic<int> done_rows[64];
+    int rc = plan_smem(reinterpret_cast<const void*>(qg_fork_plan_kernel), QGKV_MAX_BATCH * 8, done, dev);
+    if (rc != QG_OK) return rc;
+    rc = plan_smem(reinterpret_cast<const void*>(qg_fork_rows_kernel), QGKV_MAX_BATCH * 8, done_rows, dev);
     if (rc != QG_OK) return rc;
     ForkArgs a = {};
     a.table = table, a.lens = lens, a.parent = parent, a.refs = refs, a.width = width, a.pages = c.pages;
@@ -583,9 +651,10 @@ int launch_fork(const qgkv_cache& c, const int32_t* table, int64_t width, const 
     a.delta = at<int32_t>(ws, kWsDelta), a.chunks = at<int32_t>(ws, kWsChunks);
     a.src = at<int32_t>(ws, kWsMovers), a.dst = at<int32_t>(ws, kWsHoles);
     a.count = at<int32_t>(ws, kWsScalars), a.counter = at<unsigned>(ws, kWsCounters) + kCntPages;
-    qg_fork_rows_kernel<<<batch + batch2, 256, 0, s>>>(a);
     const int chunks = static_cast<int>((c.pages + kChunk - 1) / kChunk);
-    qg_fork_plan_kernel<<<chunks, kPlanThreads, batch2 * 8, s>>>(a);
+    const bool merged = chunks <= kMergeChunks;
+    qg_fork_rows_kernel<<<batch + batch2, merged ? kPlanThreads : 256, merged ? batch2 * 8 : 0, s>>>(a, merged);
+    if (!merged) qg_fork_plan_kernel<<<chunks, kPlanThreads, batch2 * 8, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e);
     return launch_copy_pages(c, a.src, a.dst, a.count, batch2, status, s);
@@ -602,13 +671,21 @@ int launch_compact(const qgkv_cache& c, const int32_t* table, int64_t width, con
     a.movers = at<int32_t>(ws, kWsMovers), a.rank = at<int32_t>(ws, kWsRank), a.chunks = at<int32_t>(ws, kWsChunks);
     a.scalars = at<int32_t>(ws, kWsScalars), a.counter = at<unsigned>(ws, kWsCounters) + kCntPages;
     const int chunks = static_cast<int>((c.pages + kChunk - 1) / kChunk);
-    if (drop) qg_drop_rows_kernel<<<batch, 256, 0, s>>>(a);
-    qg_compact_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
-    qg_compact_list_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
-    qg_compact_rows_kernel<<<batch + static_cast<int>((c.pages + 2047) / 2048), 256, 0, s>>>(a);
+    if (chunks <= kMergeChunks) {
+        qg_compact_plan_kernel<<<drop ? batch : 1, kPlanThreads, 0, s>>>(a);
+    } else {
+        if (drop) qg_drop_rows_kernel<<<batch, 256, 0, s>>>(a);
+        qg_compact_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
+        qg_compact_list_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_copy_pages(c, a.movers, a.holes, a.scalars + 2, c.pages, status, s);
+    const CopyArgs copy = copy_args(c, a.movers, a.holes, a.scalars + 2, c.pages, status);
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return cuda_fail(cudaGetLastError());
+    const int ref_ctas = static_cast<int>((c.pages + 4095) / 4096);
+    qg_compact_move_kernel<<<batch + ref_ctas + copy_ctas(copy, sms), kCopyThreads, 0, s>>>(a, copy, ref_ctas);
+    return launch_status();
 }
 
 int launch_reserve(int64_t pages, int page_tokens, int32_t* table, int64_t width, const int32_t* lens,

@@ -17,7 +17,6 @@ no CPU fallback; a refused call raises ``qgemv.QGError``, a wrong type or shape
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 
 import torch
@@ -78,21 +77,15 @@ def load():
     return _fns
 
 
-def _on(fn):
-    """With stream=, the call runs with that stream current: what it allocates belongs to the stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
 def _call(name, *args):
     rc = (_fns or load())[name](*args)
     if rc:
         _q._check(name, rc)
+
+
+def _other(stream):
+    """Whether a call has to be made again with `stream` current, so that what it allocates belongs to it."""
+    return stream is not None and stream != torch.cuda.current_stream()
 
 
 def _stream(t):
@@ -100,14 +93,14 @@ def _stream(t):
 
 
 def _need(t, dtype, name, shape=None):
-    """A contiguous CUDA tensor of this type (and shape, None where free)."""
+    """The address of a contiguous CUDA tensor of this type (and shape, None where free)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None:
+    if shape is not None and t.shape != shape:
         if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     return t.data_ptr()
@@ -173,6 +166,7 @@ class KVCache:
                            k.stride(0) if self.layers > 1 else dense, k.stride(1) if self.pages > 1 else dense,
                            self.heads, self.page_tokens, self.head_dim, FORMATS[fmt], ORDERS[order])
         self.ref = ctypes.addressof(self.c)
+        self.scale = 1.0 / math.sqrt(self.head_dim)
 
     @classmethod
     def allocate(cls, layers, pages, heads, page_tokens, head_dim, fmt="e4m3", order="hnd", device="cuda"):
@@ -197,10 +191,12 @@ def _ws(workspace, t):
     return w, w.ptr, w.bytes
 
 
-@_on
-def kv_append(cache, layer, k, v, table, lens, starts=None):
+def kv_append(cache, layer, k, v, table, lens, starts=None, stream=None):
     """Quantise new tokens k, v [rows, heads, head_dim] into the cache behind each
     sequence's lens[b] tokens (qgkv_append); rows by `starts`, or one a sequence."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_append(cache, layer, k, v, table, lens, starts)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
     kp, kind, rows, row, head = _rows(k, cache.heads, cache.head_dim, "k")
     vp, kind_v, rows_v, row_v, head_v = _rows(v, cache.heads, cache.head_dim, "v")
@@ -210,19 +206,21 @@ def kv_append(cache, layer, k, v, table, lens, starts=None):
           _stream(k))
 
 
-@_on
 def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None, lse=None, return_lse=False,
-                 workspace=None):
+                 workspace=None, stream=None):
     """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
     (qgkv_attention).  q [rows, q_heads, head_dim]; returns out, or (out, lse) with
     return_lse.  scale: 1 / sqrt(head_dim) where None."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_attention(cache, layer, q, table, lens, starts, scale, out, lse, return_lse, workspace)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     heads = q.shape[1]
     qp, kind, rows, row, head = _rows(q, heads, cache.head_dim, "q")
     if out is None:
-        out = torch.empty((rows, heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _need(out, q.dtype, "out", (rows, heads, cache.head_dim))
@@ -235,13 +233,16 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
         ep = None
     w, wp, wb = _ws(workspace, q)
     _call("qgkv_attention", cache.ref, layer, qp, op, ep, kind, rows, heads, row, head, tp, width, lp, sp, batch,
-          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, wp, wb, _stream(q))
+          cache.scale if scale is None else scale, wp, wb, _stream(q))
     return (out, lse) if return_lse else out
 
 
-@_on
-def kv_copy_pages(cache, src, dst, count=None):
-    """Copy pages src[i] to dst[i] (int32), codes and scales of every layer; `count` (int32 [1]) limits them on the device."""
+def kv_copy_pages(cache, src, dst, count=None, stream=None):
+    """Copy pages src[i] to dst[i] (int32), codes and scales of every layer; `count` (int32 [1])
+    limits them on the device."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_copy_pages(cache, src, dst, count)
     sp, dp = _need(src, torch.int32, "src", (None,)), _need(dst, torch.int32, "dst", tuple(src.shape))
     cp = None if count is None else _need(count, torch.int32, "count", (1,))
     _call("qgkv_copy_pages", cache.ref, sp, dp, cp, src.shape[0], _stream(src))
@@ -258,10 +259,12 @@ def _outs(table, refs, rows, out):
     return table2, lens2, refs2
 
 
-@_on
-def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None):
+def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None, stream=None):
     """New sequences that continue sequences parent[i] (qgkv_fork): whole pages shared,
     shared partly filled pages copied.  Returns (table2, lens2, refs2); `out` takes the three."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_fork(cache, table, lens, parent, refs, out, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
     pp = _need(parent, torch.int32, "parent", (None,))
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
@@ -273,10 +276,12 @@ def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None):
     return table2, lens2, refs2
 
 
-@_on
-def kv_compact(cache, table, lens, refs, drop=None, out=None, workspace=None):
+def kv_compact(cache, table, lens, refs, drop=None, out=None, workspace=None, stream=None):
     """Free the sequences marked by drop (bool or uint8 [batch]) and move the held pages to the
     lowest numbers (qgkv_compact).  Returns (table2, lens2, refs2, count of held pages [1])."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_compact(cache, table, lens, refs, drop, out, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
     dp = _mask(drop, batch)
@@ -294,10 +299,12 @@ def _mask(drop, batch):
     return _need(drop, torch.bool if drop.dtype == torch.bool else torch.uint8, "drop", (batch,))
 
 
-@_on
-def kv_reserve(cache, table, lens, refs, add=None, workspace=None):
+def kv_reserve(cache, table, lens, refs, add=None, workspace=None, stream=None):
     """Give each sequence the pages that lens[b] + add[b] tokens need (add None: one token each);
     table and refs are updated (qgkv_reserve)."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_reserve(cache, table, lens, refs, add, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
     ap = None if add is None else _need(add, torch.int32, "add", (batch,))
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
@@ -305,20 +312,24 @@ def kv_reserve(cache, table, lens, refs, add=None, workspace=None):
     _call("qgkv_reserve", cache.pages, cache.page_tokens, tp, width, lp, ap, batch, rp, wp, wb, _stream(table))
 
 
-@_on
-def kv_free(cache, table, lens, refs, drop=None):
+def kv_free(cache, table, lens, refs, drop=None, stream=None):
     """Free the sequences marked by drop (None: all): table, lens and refs are updated (qgkv_free)."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return kv_free(cache, table, lens, refs, drop)
     batch, width, tp, lp, _ = _batch(table, lens, None)
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
     _call("qgkv_free", cache.pages, cache.page_tokens, tp, width, lp, _mask(drop, batch), batch, rp,
           _stream(table))
 
 
-@_on
-def beam_select(logits, cum, keep, workspace=None):
+def beam_select(logits, cum, keep, workspace=None, stream=None):
     """The `keep` best continuations of each request (qgbeam_select): logits
     [requests * beams, vocab], cum float32 [requests, beams].  Returns scores float32, tokens
     int32 and parents int32 (row numbers), each [requests, keep]."""
+    if _other(stream):
+        with torch.cuda.stream(stream):
+            return beam_select(logits, cum, keep, workspace)
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2:
         raise TypeError("logits must be a CUDA tensor [rows, vocab]")
     kind = TYPES.get(logits.dtype)
@@ -333,7 +344,7 @@ def beam_select(logits, cum, keep, workspace=None):
         raise ValueError("a row of logits must be dense")
     scores = torch.empty((requests, keep), dtype=torch.float32, device=logits.device)
     ints = torch.empty((2, requests, keep), dtype=torch.int32, device=logits.device)
-    tokens, parents = ints[0], ints[1]
+    tokens, parents = ints.unbind(0)
     w, wp, wb = _ws(workspace, logits)
     _call("qgbeam_select", logits.data_ptr(), kind, cp, requests, beams, vocab,
           logits.stride(0) if rows > 1 else vocab, keep, scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), wp,

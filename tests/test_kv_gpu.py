@@ -615,7 +615,7 @@ def test_fork(kv, ws, lens, parent, outside):
     assert same_state(cache, moved(was, [s for s, _ in want[3]], [d for _, d in want[3]]))
 
 
-@pytest.mark.parametrize("pages", [4097, 9000])
+@pytest.mark.parametrize("pages", [4097, 9000, 17001])
 def test_fork_many(kv, ws, pages):
     """Two generations over several counting chunks; the free pages lie far apart."""
     page = 16
@@ -681,7 +681,7 @@ def compact_ref(table, lens, drop, refs, page):
     return np.where(table >= 0, to[table], -1), np.array(lens), refs2, n, src, dst
 
 
-@pytest.mark.parametrize("pages", [5, 64, 4096, 4100, 12289])
+@pytest.mark.parametrize("pages", [5, 64, 4096, 4100, 12289, 20483])
 @pytest.mark.parametrize("share", [0.0, 0.5, 1.0])
 def test_compact(kv, ws, pages, share):
     page = 16
