@@ -189,39 +189,48 @@ __device__ __forceinline__ void fork_count(const ForkArgs& a, int chunk, int* re
     if (threadIdx.x == 0) a.chunks[chunk] = zeros;
 }
 
-// Who needs a page of its own gets the lowest free ones.  One CTA; smem: tail
-// [batch2], list [batch2].
+// Who needs a page of its own gets the lowest free ones.  One CTA; smem: tail,
+// list and holders [batch2].
 __device__ __forceinline__ void fork_plan(const ForkArgs& a, int32_t* smem, int* red) {
     const int tid = threadIdx.x;
+    const int padded = (a.batch2 + 3) & ~3;
     int32_t* tail = smem;
-    int32_t* list = smem + a.batch2;
+    int32_t* list = smem + padded;
+    int32_t* holders = list + padded;  // references of the tail
+    if (tid < padded - a.batch2) tail[a.batch2 + tid] = -2;
     // the partly filled last page of each new sequence, -1 where it has none
     for (int i = tid; i < a.batch2; i += kPlanThreads) {
         const int len = __ldcg(a.lens2 + i);
         const int id = (len & ((1 << a.log2p) - 1)) ? __ldcg(a.table2 + i * a.width + (len >> a.log2p)) : -1;
-        tail[i] = id >= 0 && id < a.pages ? id : -1;
+        const bool there = id >= 0 && id < a.pages;
+        tail[i] = there ? id : -1;
+        holders[i] = there ? __ldcg(a.refs2 + id) : 0;
     }
     __syncthreads();
-    // who needs a copy, and its rank among them
+    // who needs a copy: a lower sequence has the same last page, or someone
+    // outside holds it too
+    for (int i = tid; i < a.batch2; i += kPlanThreads) {
+        const int mine = tail[i];
+        int same = 0, first = a.batch2;
+#pragma unroll 4
+        for (int j = 0; j < a.batch2; j += 4) {  // padded to whole fours
+            const int4 t = *reinterpret_cast<const int4*>(tail + j);
+            const int n = (t.x == mine) + (t.y == mine) + (t.z == mine) + (t.w == mine);
+            if (n && first == a.batch2) first = t.x == mine ? j : t.y == mine ? j + 1 : t.z == mine ? j + 2 : j + 3;
+            same += n;
+        }
+        list[i] = mine >= 0 && (first < i || holders[i] > same) ? 1 : 0;
+    }
+    __syncthreads();
+    // their ranks; the list then holds the sequences
     int needed = 0;
     for (int i0 = 0; i0 < a.batch2; i0 += kPlanThreads) {
         const int i = i0 + tid;
-        int copy = 0;
-        const int mine = i < a.batch2 ? tail[i] : -1;
-        if (mine >= 0) {
-            int same = 0;
-            bool lower = false;
-            for (int j = 0; j < a.batch2; ++j)
-                if (tail[j] == mine) {
-                    ++same;
-                    lower |= j < i;
-                }
-            copy = lower || __ldcg(a.refs2 + mine) > same;
-        }
+        const int copy = i < a.batch2 ? list[i] : 0;
         int before;
-        const int sum = block_scan(copy, before, red);
+        const int sum = block_scan(copy, before, red);  // every flag of this round has been read
         if (copy) {
-            a.src[needed + before] = mine;
+            a.src[needed + before] = tail[i];
             list[needed + before] = i;
         }
         needed += sum;
@@ -266,7 +275,7 @@ __device__ __forceinline__ void fork_plan(const ForkArgs& a, int32_t* smem, int*
 // the last CTA to end also counts and plans, which saves a launch; with many
 // the counting is spread over CTAs of its own (qg_fork_plan_kernel).
 __global__ void __launch_bounds__(kPlanThreads) qg_fork_rows_kernel(const ForkArgs a, int merged) {
-    extern __shared__ int32_t smem[];
+    extern __shared__ __align__(16) int32_t smem[];
     __shared__ int children;
     __shared__ int red[32];
     __shared__ int flag;
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) qg_fork_rows_kernel(const ForkAr
 
 // A CTA counts a chunk; the last plans.
 __global__ void __launch_bounds__(kPlanThreads) qg_fork_plan_kernel(const ForkArgs a) {
-    extern __shared__ int32_t smem[];
+    extern __shared__ __align__(16) int32_t smem[];
     __shared__ int red[32];
     __shared__ int flag;
     fork_count(a, blockIdx.x, red);
@@ -640,9 +649,9 @@ int launch_fork(const qgkv_cache& c, const int32_t* table, int64_t width, const 
     if (dev < 0) return cuda_fail(cudaGetLastError());
     static std::atomic<int> done[64];
     static std::atomic<int> done_rows[64];
-    int rc = plan_smem(reinterpret_cast<const void*>(qg_fork_plan_kernel), QGKV_MAX_BATCH * 8, done, dev);
+    int rc = plan_smem(reinterpret_cast<const void*>(qg_fork_plan_kernel), (QGKV_MAX_BATCH + 4) * 12, done, dev);
     if (rc != QG_OK) return rc;
-    rc = plan_smem(reinterpret_cast<const void*>(qg_fork_rows_kernel), QGKV_MAX_BATCH * 8, done_rows, dev);
+    rc = plan_smem(reinterpret_cast<const void*>(qg_fork_rows_kernel), (QGKV_MAX_BATCH + 4) * 12, done_rows, dev);
     if (rc != QG_OK) return rc;
     ForkArgs a = {};
     a.table = table, a.lens = lens, a.parent = parent, a.refs = refs, a.width = width, a.pages = c.pages;
@@ -653,8 +662,9 @@ int launch_fork(const qgkv_cache& c, const int32_t* table, int64_t width, const 
     a.count = at<int32_t>(ws, kWsScalars), a.counter = at<unsigned>(ws, kWsCounters) + kCntPages;
     const int chunks = static_cast<int>((c.pages + kChunk - 1) / kChunk);
     const bool merged = chunks <= kMergeChunks;
-    qg_fork_rows_kernel<<<batch + batch2, merged ? kPlanThreads : 256, merged ? batch2 * 8 : 0, s>>>(a, merged);
-    if (!merged) qg_fork_plan_kernel<<<chunks, kPlanThreads, batch2 * 8, s>>>(a);
+    const int smem = (batch2 + 4) * 12;
+    qg_fork_rows_kernel<<<batch + batch2, merged ? kPlanThreads : 256, merged ? smem : 0, s>>>(a, merged);
+    if (!merged) qg_fork_plan_kernel<<<chunks, kPlanThreads, smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e);
     return launch_copy_pages(c, a.src, a.dst, a.count, batch2, status, s);
