@@ -12,18 +12,20 @@ namespace qg {
 
 // ------------------------------------------------------------- workspace
 // Counters and kWsDelta are zero between calls (each call that uses them puts
-// the zeros back); the rest holds values only within a call.
+// the zeros back); the rest holds values only within a call, so the page
+// operations' lists and the others' partial results share it.
 constexpr int64_t kWsCounters = 0;                               // 16384 words
 constexpr int64_t kWsDelta = kWsCounters + 16384 * 4;            // per page: change of its count
-constexpr int64_t kWsRefs = kWsDelta + int64_t(QGKV_MAX_PAGES) * 4;
+constexpr int64_t kWsShared = kWsDelta + int64_t(QGKV_MAX_PAGES) * 4;
+constexpr int64_t kWsRefs = kWsShared;
 constexpr int64_t kWsHoles = kWsRefs + int64_t(QGKV_MAX_PAGES) * 4;
 constexpr int64_t kWsMovers = kWsHoles + int64_t(QGKV_MAX_PAGES) * 4;
 constexpr int64_t kWsRank = kWsMovers + int64_t(QGKV_MAX_PAGES) * 4;
 constexpr int64_t kWsChunks = kWsRank + int64_t(QGKV_MAX_PAGES) * 4;  // 4096 words
 constexpr int64_t kWsScalars = kWsChunks + 4096 * 4;                  // 256 words
-constexpr int64_t kWsPart = kWsScalars + 256 * 4;                     // partial results
-constexpr int64_t kWsPartBytes = int64_t(32) << 20;
-constexpr int64_t kWsTotal = kWsPart + kWsPartBytes;
+constexpr int64_t kWsTotal = kWsScalars + 256 * 4;
+constexpr int64_t kWsPart = kWsShared;                                // partial results
+constexpr int64_t kWsPartBytes = kWsTotal - kWsPart;
 
 // Counter words by user.
 constexpr int kCntAttn = 0;      // [kMaxAttnCtas]

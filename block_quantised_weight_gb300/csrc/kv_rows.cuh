@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kTile = 128;        // tokens of a tile: 4 warps x 32
 constexpr int kThreads = 128;
-constexpr int kMaxCtas = 1824;    // partial slots: 2 per CTA
+constexpr int kMaxCtas = 640;     // partial slots: 2 per CTA
 constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its log-sums
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
@@ -790,7 +790,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
             return cuda_fail(cudaGetLastError());
         done[dev].store(true, std::memory_order_release);
     }
-    const int grid = sms * MINB < kMaxCtas ? sms * MINB : kMaxCtas;
+    const int grid = std::min(sms * MINB, kMaxCtas);
     kern<<<grid, kThreads, fixed + (a.batch + 1) * 16, s>>>(a, kmap, vmap, grid);
     return launch_status();
 }
