@@ -6,9 +6,12 @@
 #include <cstdint>
 #include <mutex>
 
+#include "../../include/qgkv.h"
 #include "common.cuh"
 #include "gemv_kernel.cuh"
+#include "kv_common.cuh"
 #include "launch.h"
+#include "qgkv_launch.h"
 
 namespace {
 

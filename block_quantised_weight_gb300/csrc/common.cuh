@@ -16,7 +16,6 @@ namespace qg {
 // Device status bits (returned by qg_device_status as negative codes).
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBounds = 2u;
-constexpr unsigned kStatusPages = 4u;
 
 // A healthy bulk copy lands within microseconds.  A wait that has not seen
 // its phase complete after kWaitLimitNs of wall time gives up.
@@ -83,16 +82,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         " [%0], [%1, {%2, %3}], [%4], %5;"
         ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)),
           "l"(policy) : "memory");
-}
-
-// 4D tiled TMA load; x innermost, the same rule.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
 }
 
 // Fetch a tensor-map descriptor (kernel parameter space) ahead of its first use.

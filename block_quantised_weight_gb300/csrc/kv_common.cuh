@@ -10,6 +10,19 @@
 
 namespace qg {
 
+// Device status bit next to common.cuh's.
+constexpr unsigned kStatusPages = 4u;
+
+// 4D tiled TMA load; x innermost, x * element size a multiple of 16.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // ------------------------------------------------------------- workspace
 // Counters and kWsDelta are zero between calls (each call that uses them puts
 // the zeros back); the rest holds values only within a call, so the page

@@ -21,9 +21,6 @@ inline int launch_status() {
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
-// Device address of the current device's status word; null if it cannot be had.
-unsigned* status_ptr();
-
 int launch_gemv_q4k(const uint8_t* W, const float* X, float* Y, int M, int64_t N, int64_t K, cudaStream_t s,
                     unsigned* status, unsigned flags);
 int launch_gemv_iq3(const uint8_t* W, const uint8_t* grid, const float* X, float* Y, int M, int64_t N, int64_t K,

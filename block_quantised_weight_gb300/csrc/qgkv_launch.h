@@ -7,6 +7,9 @@
 
 namespace qg {
 
+// Device address of the current device's status word; null if it cannot be had.
+unsigned* status_ptr();
+
 int launch_beam_select(const void* logits, int type, const float* cum, int requests, int beams, int64_t vocab,
                        int64_t row_stride, int keep, float* scores, int32_t* tokens, int32_t* parents,
                        uint8_t* workspace, cudaStream_t s);

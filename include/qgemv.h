@@ -59,8 +59,7 @@ extern "C" {
 #define QG_ETIMEOUT (-4)  /* device: a bounded wait inside a kernel gave up */
 #define QG_EBOUNDS (-5)   /* device: an index check inside a kernel failed */
 #define QG_EALIAS (-6)    /* Y overlaps W, X or grid */
-#define QG_ESCRATCH (-7)  /* request larger than the fixed scratch of qgemv_q4k_pass_noalloc, or workspace too small */
-#define QG_EPAGES (-8)    /* device: an operation of qgkv.h found too few free pages */
+#define QG_ESCRATCH (-7)  /* request larger than the fixed scratch of qgemv_q4k_pass_noalloc */
 
 #define QG_MAX_M 32
 #define QG_MAX_GROUP 4
@@ -348,7 +347,7 @@ QG_API int qdequant_iq3xxs(const uint8_t* W, const uint8_t* grid, float* out, in
                            cudaStream_t stream);
 
 /* Synchronise `stream`, then return and clear the current device's status
- * word: QG_OK, QG_ETIMEOUT, QG_EBOUNDS or QG_EPAGES (QG_ECUDA if the sync failed). */
+ * word: QG_OK, QG_ETIMEOUT or QG_EBOUNDS (QG_ECUDA if the sync failed). */
 QG_API int qg_device_status(cudaStream_t stream);
 
 /* Test-only fault check: launches a kernel whose mbarrier wait can never

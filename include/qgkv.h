@@ -49,6 +49,8 @@
 extern "C" {
 #endif
 
+#define QG_EPAGES (-8) /* device: too few free pages */
+
 #define QGKV_E4M3 1
 #define QGKV_INT8 2
 
