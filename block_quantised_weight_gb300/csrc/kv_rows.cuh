@@ -797,11 +797,17 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
 
 template <int QP, int PP, bool INT8>
 int launch_typed(const AttnArgs& a, cudaStream_t s) {
-    // 16 rows a unit where the mean sequence has more than 8 (the codes are
-    // then read half as often); 256-dim heads keep 8 for their registers.
+    // 16 rows a unit read the codes half as often as 8 do, with more registers
+    // and so fewer CTAs; what they gain grows with what a code costs and with the
+    // rows.  8 against 16 rows a unit, us, 16 sequences of up to 4100 tokens, bf16:
+    //   int8, 128 dims: 16 rows 37.6 / 41.9, 24 rows 50.5 / 46.4, 64 rows 102 / 83.6
+    //   e4m3, 64 dims:  24 rows 27.3 / 28.4, 32 rows 33.3 / 31.5, 64 rows 52.2 / 45.4
+    //   e4m3, 128 dims: 48 rows 58.8 / 60.0, 64 rows 70.7 / 70.3, 128 rows 124 / 111
+    // 256-dim heads keep 8 for their registers.
     // int8's conversions hold more registers: two CTAs an SM instead of three
     // (attn_long 121 us for 130; e4m3's attn_batch 58 us for 56).
-    const bool wide = a.rows * a.group > 8 * static_cast<int64_t>(a.batch);
+    const int few = INT8 ? 16 : a.c.dim <= 64 ? 24 : 48;
+    const bool wide = a.rows * a.group > few * static_cast<int64_t>(a.batch);
     if (a.c.dim <= 64) return wide ? launch_one<1, 2, QP, PP, INT8, 3>(a, s) : launch_one<1, 1, QP, PP, INT8, 3>(a, s);
     if (a.c.dim <= 128)
         return wide ? launch_one<2, 2, QP, PP, INT8, 2>(a, s) : launch_one<2, 1, QP, PP, INT8, INT8 ? 2 : 3>(a, s);
