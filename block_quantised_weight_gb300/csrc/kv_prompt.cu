@@ -620,7 +620,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             }
                         }
                         const int k_old = min(kBase + m - mu, 126), k_new = min(kBase + mn - un, 126);
-                        const float down = pow2i((k_new - mn) - (k_old - m));
+                        const int order = (k_new - mn) - (k_old - m);
+                        const float down = pow2i(order);
                         l *= pow2i(m - mn);
                         m = mn, mu = un;
                         kf = static_cast<float>(max(k_new, -126));
@@ -636,14 +637,20 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             }
                         }
                         if (half == 1) {  // the first half's probabilities are stored already
-                            const uint32_t d2 = pack_f16x2(down, down);
+                            // in two factors: f16 ends at 2^-24, what is stored
+                            // may come down by 2^-39 before it rounds to 0
+                            const int e = max(order, -40);
+                            const float da = pow2i(e >> 1), db = pow2i(e - (e >> 1));
+                            const uint32_t d2a = pack_f16x2(da, da), d2b = pack_f16x2(db, db);
 #pragma unroll 1
                             for (int p = 0; p < PP; ++p) {
                                 tmem_load32(st + p * 32, va);
                                 tmem_loaded();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(va[i]) : "r"(va[i]), "r"(d2));
+                                for (int i = 0; i < 32; ++i) {
+                                    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(va[i]) : "r"(va[i]), "r"(d2a));
+                                    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(va[i]) : "r"(va[i]), "r"(d2b));
+                                }
                                 tmem_store32(st + p * 32, va);
                             }
                         }

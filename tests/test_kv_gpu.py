@@ -222,6 +222,42 @@ def test_attention_prompt_negative_scale(kv, ws):
     check_attention(kv, ws, [200], [1], 4, 2, 64, 16, "int8", "hnd", "f32", scale=-0.1)
 
 
+@pytest.mark.parametrize("dtype, orders", [("f32", 20), ("f32", 26), ("f32", 30), ("f16", 26), ("f16", 30), ("bf16", 26)])
+@pytest.mark.parametrize("at", [3, 100, 200])
+@pytest.mark.parametrize("first", [0, 64, 128, 192])
+def test_attention_prompt_one_large_score(kv, ws, dtype, orders, at, first):
+    """One token `orders` binary orders above the others, whose values are zero: what 64 of the others carry stays.
+
+    A weight is stored as p' = p * 2^11 (bf16: 2^5) or more, in f16, with two roundings of parts by up to three
+    halves of a 2^-24 step each: off by at most 3 * 2^-36 (bf16 3 * 2^-30) of the largest, for each of 64 tokens.
+    """
+    n, rows, dim = 256, 64, 64
+    e4 = lambda x: torch.tensor(float(x)).to(torch.float8_e4m3fn).view(torch.uint8).item()  # noqa: E731
+    cache = kv.KVCache.allocate(1, 20, 1, 16, dim, "e4m3", "hnd")
+    for c in (cache.k, cache.v):
+        c.zero_()
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    k = torch.zeros((n, dim), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    v[first:first + 64] = e4(1.0)
+    v[at] = 0
+    k[at, 0] = e4(orders)
+    cache.k[0, :16, 0] = k.view(16, 16, dim)
+    cache.v[0, :16, 0] = v.view(16, 16, dim)
+    q = torch.zeros((rows, 1, dim), device="cuda")
+    q[:, :, 0] = math.log(2)
+    q = q.to(DT[dtype])
+    table = i32([list(range(16))])
+    out = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=1.0, workspace=ws)
+    want, _, absum, smax, _ = attention_ref(cache, 0, q, table, [n], [0, rows], 1.0)
+    rel = 4 * smax[..., None] * 2.0 ** -22 + 20 * 2.0 ** -22 + (2.0 ** -11 if dtype == "bf16" else 0.0)
+    tol = absum * rel + 64 * 3 * 2.0 ** (-30 if dtype == "bf16" else -36)
+    tol = tol + want.abs() * (1.01 * torch.finfo(DT[dtype]).eps / 2) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), f"worst {float((err / tol).max()):.3f} of the tolerance"
+
+
 def test_attention_prompt_masked_tokens_do_not_reach(kv, ws):
     """NaN codes behind the length and in tokens that only later rows see; a missing page."""
     lens, rows = [300], [140]
