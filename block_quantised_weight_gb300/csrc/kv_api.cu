@@ -4,6 +4,7 @@
 
 #include "kv_attention.cuh"
 #include "launch.h"
+#include "launch_common.cuh"
 #include "qgkv_launch.h"
 
 namespace {
@@ -142,9 +143,18 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     a.part = reinterpret_cast<float*>(ws + qg::kWsPart);
     a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
     a.status = st;
-    // From 64 query rows (tokens x heads of a group) a sequence on average the
-    // tcgen05 kernel; below, and for more than 128 dims, the row kernel.
-    const bool many = rows * a.group >= 64 * static_cast<int64_t>(batch) && starts && cache->head_dim <= 128;
+    // The tcgen05 kernel takes as long for one query row (token x head of a
+    // group) a sequence as for 256, the row kernel's time grows with them; the
+    // first needs enough row blocks to fill the GPU without splitting keys.
+    // Row kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128:
+    //   16 sequences of up to 4100 tokens: bf16 128 rows 111 / 114, 192 rows
+    //   155 / 120; fp32 128 rows 138 / 146, 256 rows 252 / 224; f16 (two parts
+    //   of p for two tiles) 192 rows 171 / 194, 256 rows 223 / 201
+    //   one sequence of 8000, bf16: 128 rows 39 / 85, 256 rows 58 / 87; of
+    //   30000: 256 rows 209 / 110
+    const int sms = qg::sm_count(qg::current_device());
+    const int few = type == QGKV_F16 || 2 * static_cast<int64_t>(batch) * cache->heads < sms ? 256 : 128;
+    const bool many = rows * a.group >= static_cast<int64_t>(few) * batch && starts && cache->head_dim <= 128;
     if (many) return qg::launch_attn_prompt(a, cache->format == QGKV_INT8, stream);
     return qg::launch_attn_rows(a, cache->format == QGKV_INT8, stream);
 }

@@ -46,6 +46,28 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     return s;
 }
 
+// a / b for non-negative a and positive b, in 32 bits where they fit.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// A line of tiles (or steps) cut into pieces of equal size, the first `more` one longer.
+struct Line {
+    int64_t each;
+    int more, ctas;
+    __device__ Line(int64_t total, int grid) {
+        ctas = total < grid ? static_cast<int>(total) : grid;
+        each = ctas ? div64(total, ctas) : 0;
+        more = static_cast<int>(total - each * ctas);
+    }
+    __device__ int64_t first(int cta) const { return each * cta + min(cta, more); }
+    __device__ int of(int64_t tile) const {
+        const int64_t long_part = (each + 1) * more;
+        return static_cast<int>(tile < long_part ? div64(tile, each + 1) : more + div64(tile - long_part, each));
+    }
+};
+
 // Four consecutive output values.
 __device__ __forceinline__ void store_out4(void* out, int type, int64_t at, float4 x) {
     if (type == QGKV_F32) {

@@ -33,6 +33,12 @@ namespace qg {
 namespace {
 
 constexpr int kStepTokens = 128;
+constexpr int kMaxPromptCtas = 160;  // that share the line of steps: two part slots each
+// Fewer units than this many a CTA are split: 96 units 115 us whole, 65 split;
+// 192 units 178 / 160, 256 units 180 / 186, 512 units 258 / 295.
+constexpr int kSplitBelow = 2;
+static_assert(int64_t(kMaxPromptCtas) * 2 * 256 * (128 + 1) * 4 <= kWsPartBytes, "partials exceed the workspace");
+static_assert(kCntPromptParts + kMaxPromptCtas * 8 <= kCntPages, "counters overlap");
 constexpr uint32_t kOps = 4;       // operand slots
 constexpr uint32_t kRaws = 2;      // raw slots
 constexpr uint32_t kUnits = 4;   // units handed to the roles ahead
@@ -121,31 +127,92 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&w)[
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The line of units: for each sequence, its row blocks from the last (which
-// sees most) to the first, each for all heads.  A walker only goes forward.
+// A piece of work: steps j0 .. j1 - 1 of the keys of one row block and head.
+// Where that is not all its keys, the result is partial: pieces parts make
+// one, this CTA's goes to part slot `part`, `owner` is the first of their CTAs.
+struct Piece {
+    int b, h, row_first, n, len, row0, j0, j1, part, owner, pieces;  // b < 0: no more; part < 0: whole
+};
+
+// A row block's place in its sequence.
 template <int ROWS>
-struct Walk {
-    int b = -1, h, row_first, nrows, seen_least, seen_most, steps;
-    Seq sq;
-    int64_t base = 0, units = 0;
-    int blocks = 0;
-    __device__ bool to(const AttnArgs& a, int64_t u) {
-        while (u >= base + units) {
-            base += units;
-            if (++b >= a.batch) return false;
-            sq = sequence(a, b);
-            blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + ROWS - 1) / ROWS);
-            units = static_cast<int64_t>(blocks) * a.c.heads;
-        }
-        const int64_t in = u - base;
-        const int back = static_cast<int>(in / a.c.heads);
-        h = static_cast<int>(in - static_cast<int64_t>(back) * a.c.heads);
-        nrows = sq.n * a.group;
-        row_first = (blocks - 1 - back) * ROWS;
-        const int i_last = (min(row_first + ROWS, nrows) - 1) / a.group;
-        seen_most = max(0, sq.len - sq.n + i_last + 1);
-        seen_least = sq.len - sq.n + row_first / a.group + 1;
+struct Block {
+    int row_first, nrows, seen_least, seen_most, steps;
+    __device__ static int count(int n, int group) {
+        return static_cast<int>((static_cast<int64_t>(n) * group + ROWS - 1) / ROWS);
+    }
+    __device__ Block(int first, int n, int len, int group) : row_first(first) {
+        nrows = n * group;
+        const int i_last = (min(row_first + ROWS, nrows) - 1) / group;
+        seen_most = max(0, len - n + i_last + 1);
+        seen_least = len - n + row_first / group + 1;
         steps = (seen_most + kStepTokens - 1) / kStepTokens;
+    }
+};
+
+// Finds places on the line of all units (for each sequence its row blocks from
+// the last, which sees most, to the first, each for all heads), by a whole
+// warp, forward only.  STEPS: the line is measured in steps (a unit without
+// keys counts as one), else in units.
+template <int ROWS, bool STEPS>
+struct Walk {
+    int b0 = -32, n, len, row0;  // of this lane's sequence, b0 + lane
+    int64_t base = 0, chunk = 0, upto = 0;
+    __device__ static int64_t span(const AttnArgs& a, int n, int len) {
+        const int blocks = Block<ROWS>::count(n, a.group);
+        int64_t sum = blocks;
+        if (STEPS) {
+            sum = 0;
+            for (int i = 0; i < blocks; ++i) sum += max(1, Block<ROWS>(i * ROWS, n, len, a.group).steps);
+        }
+        return sum * a.c.heads;
+    }
+    // The next 32 sequences; false after the last.
+    __device__ bool more(const AttnArgs& a) {
+        const int lane = threadIdx.x & 31;
+        b0 += 32;
+        base += chunk;
+        if (b0 >= a.batch) return false;
+        n = len = row0 = 0;
+        if (b0 + lane < a.batch) {
+            const Seq sq = sequence(a, b0 + lane);
+            n = sq.n, len = sq.len, row0 = a.starts[b0 + lane];
+        }
+        upto = span(a, n, len);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += x;
+        }
+        chunk = __shfl_sync(~0u, upto, 31);
+        return true;
+    }
+    // The unit at `at`; the place in the unit in `in` (STEPS).
+    __device__ bool to(const AttnArgs& a, int64_t at, Piece& u, int64_t& in) {
+        while (at >= base + chunk)
+            if (!more(a)) return false;
+        const int which = __popc(__ballot_sync(~0u, upto <= at - base));
+        u.b = b0 + which;
+        u.n = __shfl_sync(~0u, n, which);
+        u.len = __shfl_sync(~0u, len, which);
+        u.row0 = __shfl_sync(~0u, row0, which);
+        const int64_t below = __shfl_sync(~0u, upto, which ? which - 1 : 0);
+        in = at - base - (which ? below : 0);
+        int block = Block<ROWS>::count(u.n, a.group) - 1, steps = 1;
+        if (STEPS) {
+            for (;; --block) {
+                steps = max(1, Block<ROWS>(block * ROWS, u.n, u.len, a.group).steps);
+                if (in < static_cast<int64_t>(steps) * a.c.heads) break;
+                in -= static_cast<int64_t>(steps) * a.c.heads;
+            }
+        } else {
+            const int64_t back = in / a.c.heads;
+            block -= static_cast<int>(back);
+            in -= back * a.c.heads;
+        }
+        u.row_first = block * ROWS;
+        u.h = static_cast<int>(in) / steps;
+        in -= static_cast<int64_t>(u.h) * steps;
         return true;
     }
 };
@@ -179,7 +246,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     uint64_t* unit_full = sc_full + kScales;
     uint64_t* unit_empty = unit_full + kUnits;
     static_assert((2 * kRaws + 2 * kOps + 10 + kScales + 2 * kUnits) * 8 <= 320, "barriers");
-    __shared__ volatile long long units[kUnits];
+    __shared__ Piece units[kUnits];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int nan_unit[8];
 
@@ -213,48 +280,96 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    Walk<F::ROWS> w;
     // A wait that gave up ends all further waits, copies and MMAs of its
     // thread: the kernel then runs to its end within a few wait limits.
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // by whole warps
         if (!dead) dead = __any_sync(~0u, !mbar_wait_bounded(bar, parity & 1u, a.status));
     };
-    // The next unit: the copying warp takes it from a counter that all CTAs
-    // share (the longest first, so the CTAs end together) and hands it to the
-    // others; false after the last.
+    // The next piece, as the copying warp hands it to the others; false after
+    // the last.
     uint32_t turn = 0;
+    Piece w;
     auto next_unit = [&]() {
         const uint32_t slot = turn % kUnits;
         wait(unit_full + slot, turn / kUnits);
-        const long long u = units[slot];
+        w = units[slot];
         __syncwarp();
         if (lane == 0) arrive_on(unit_empty + slot);
         ++turn;
-        return !dead && u >= 0 && w.to(a, u);
+        return !dead && w.b >= 0;
     };
 
     if (warp == F::warps - 2) {
         // ---------------------------------------------------------- copies
+        // Many units: the next one comes from a counter that all CTAs share, the
+        // longest of a sequence first, so that the CTAs end together.  Few: the
+        // line of their steps is cut evenly among the CTAs.
+        Walk<F::ROWS, false> by_unit;
+        Walk<F::ROWS, true> by_step;
+        int64_t total = 0;
+        while (by_unit.more(a)) total += by_unit.chunk;
+        const int ctas = min(static_cast<int>(gridDim.x), kMaxPromptCtas);
+        const bool split = total < static_cast<int64_t>(kSplitBelow) * ctas;
+        by_unit = Walk<F::ROWS, false>();
+        int64_t at = 0, end = 0;
+        Line line(0, 1);
+        if (split) {
+            const int64_t all = total;
+            total = 0;
+            while (by_step.more(a)) total += by_step.chunk;
+            by_step = Walk<F::ROWS, true>();
+            // A step takes 3.4 us, joining one part more about 1.9 (a unit's
+            // parts are joined by one CTA): S steps are best cut in about
+            // sqrt(1.7 S) parts.
+            const float mean = static_cast<float>(total) / static_cast<float>(max(all, static_cast<int64_t>(1)));
+            const int least = max(2, static_cast<int>(sqrtf(0.6f * mean)));
+            line = Line(total, static_cast<int>(min(static_cast<int64_t>(ctas), max(all, total / least))));
+            if (static_cast<int>(blockIdx.x) < line.ctas) at = line.first(blockIdx.x), end = line.first(blockIdx.x + 1);
+        }
         uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
         for (;; ++turn) {
             const uint32_t slot = turn % kUnits;
             if (turn >= kUnits) wait(unit_empty + slot, turn / kUnits - 1);
-            long long u = 0;
-            if (lane == 0) u = atomicAdd(a.count + kCntPrompt, 1u);
-            u = __shfl_sync(~0u, u, 0);
-            const bool there = !dead && w.to(a, u);
+            bool there = !dead;
+            int64_t in = 0;
+            w.part = -1, w.owner = 0, w.pieces = 1, w.j0 = 0;
+            if (split) {
+                there = there && at < end && by_step.to(a, at, w, in);
+            } else {
+                unsigned u = 0;
+                if (lane == 0) u = atomicAdd(a.count + kCntPrompt, 1u);
+                u = __shfl_sync(~0u, u, 0);
+                there = there && by_unit.to(a, u, w, in);
+            }
+            if (there) {
+                const int steps = Block<F::ROWS>(w.row_first, w.n, w.len, a.group).steps;
+                w.j1 = steps;
+                if (split) {
+                    const int64_t start = at - in, stop = start + max(1, steps);
+                    at = min(end, stop);
+                    if (in > 0 || at < stop) {
+                        w.j0 = static_cast<int>(in);
+                        w.j1 = static_cast<int>(at - start);
+                        w.owner = line.of(start);
+                        w.pieces = line.of(stop - 1) - w.owner + 1;
+                        w.part = 2 * blockIdx.x + (in == 0 ? 1 : 0);
+                    }
+                }
+            } else {
+                w.b = -1;
+            }
             if (lane == 0) {
-                units[slot] = there ? u : -1;
+                units[slot] = w;
                 arrive_on(unit_full + slot);
             }
             __syncwarp();
             if (!there) break;
+            const Block<F::ROWS> blk(w.row_first, w.n, w.len, a.group);
             // its queries on their way to L2
-            for (int r = w.row_first + lane; r < min(w.row_first + F::ROWS, w.nrows); r += 32) {
+            for (int r = w.row_first + lane; r < min(w.row_first + F::ROWS, blk.nrows); r += 32) {
                 const int i_row = r / a.group;
-                const int64_t row0 = a.starts ? a.starts[w.b] : w.b;
-                const int64_t qat = (row0 + i_row) * a.q_row + (w.h * a.group + r - i_row * a.group) * a.q_head;
+                const int64_t qat = (static_cast<int64_t>(w.row0) + i_row) * a.q_row + (w.h * a.group + r - i_row * a.group) * a.q_head;
                 const int size = a.type == QGKV_F32 ? 4 : 2;
                 for (int at = 0; at < c.dim * size; at += 128)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + qat * size + at));
@@ -264,7 +379,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 int id = -1;
                 f = make_float4(0.f, 0.f, 0.f, -INFINITY);
                 const int tok = j * kStepTokens + lane * 16;
-                if (lane < 8 && tok < w.seen_most) {
+                if (lane < 8 && tok < blk.seen_most) {
                     id = table[tok >> c.log2p];
                     if (id >= 0 && id < c.pages) {
                         const int64_t at = static_cast<int64_t>(id) * c.heads + w.h;
@@ -280,8 +395,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 return id;
             };
             float4 f;
-            int id = w.steps > 0 ? look(0, f) : -1;
-            for (int j = 0; j < w.steps; ++j, ++g) {
+            int id = w.j0 < w.j1 ? look(w.j0, f) : -1;
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
                 const int tok = (j * kStepTokens + lane * 16) & ((1 << c.log2p) - 1);
                 const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
 #pragma unroll
@@ -299,7 +414,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         tma_load_4d(smem + F::off_raw + slot * F::kRaw + lane * 16 * DP, kv ? &vmap : &kmap, 0, tok, w.h, id,
                                     raw_full + slot);
                 }
-                if (j + 1 < w.steps) id = look(j + 1, f);
+                if (j + 1 < w.j1) id = look(j + 1, f);
             }
         }
     } else if (warp == F::warps - 1) {
@@ -307,10 +422,11 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         uint32_t o = 0;                // operands taken
         uint32_t ps = 0, qs = 0;       // probabilities (per tile) and queries taken
         while (next_unit()) {
-            if (w.steps == 0) continue;
-            for (int j = 0; j <= w.steps; ++j) {
+            const int steps = w.j1 - w.j0;
+            if (steps == 0) continue;
+            for (int j = 0; j <= steps; ++j) {
                 const uint32_t ko = o + 2 * j, vo = ko - 1;  // K of step j, V of step j - 1
-                if (j < w.steps) wait(op_full + ko % kOps, ko / kOps);
+                if (j < steps) wait(op_full + ko % kOps, ko / kOps);
                 if (j > 0) wait(op_full + vo % kOps, vo / kOps);
 #pragma unroll
                 for (int t = 0; t < TILES; ++t) {
@@ -329,9 +445,9 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                     mma_ts(ot, pa, vb + (((ks >> 2) * (DP * 128) + (ks & 3) * 32) >> 4), f16_desc(DP),
                                            j > 1 || ks > 0 || p > 0 ? 1u : 0u);
                                 }
-                            if (j == w.steps) commit_to(o_done + t);
+                            if (j == steps) commit_to(o_done + t);
                         }
-                        if (j < w.steps) {
+                        if (j < steps) {
                             const uint64_t kb = operand_desc(smem_u32(smem + F::off_op + (ko % kOps) * F::kOp));
 #pragma unroll
                             for (int p = 0; p < QP; ++p) {
@@ -346,14 +462,14 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         }
                         if (t == TILES - 1) {
                             if (j > 0) commit_to(op_empty + vo % kOps);
-                            if (j < w.steps) commit_to(op_empty + ko % kOps);
+                            if (j < steps) commit_to(op_empty + ko % kOps);
                         }
                     }
                     __syncwarp();
                 }
             }
-            o += 2 * w.steps;
-            ps += w.steps;
+            o += 2 * steps;
+            ps += steps;
             ++qs;
         }
     } else if (warp >= TILES * 4) {
@@ -362,9 +478,10 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         uint32_t o = 0, g = 0;
         int unit = 0;
         for (; next_unit(); ++unit) {
-            for (int j = 0; j < w.steps; ++j, ++g) {
+            const Block<F::ROWS> blk(w.row_first, w.n, w.len, a.group);
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
                 const int tok0 = j * kStepTokens;
-                const bool diagonal = tok0 + kStepTokens > w.seen_least;  // some row does not see all of it
+                const bool diagonal = tok0 + kStepTokens > blk.seen_least;  // some row does not see all of it
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++o) {
                     const int rs = o % kRaws, os = o % kOps;
@@ -410,7 +527,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll 1
                         for (int it = 0; it < 4 / per; ++it) {
                             const int t0 = ((it * 4 + cw) * per + lane / W) * 8;
-                            const int limit = sc[t0 >> 4].z == 0.f ? 0 : w.seen_most - tok0;
+                            const int limit = sc[t0 >> 4].z == 0.f ? 0 : blk.seen_most - tok0;
                             uint32_t x[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
@@ -466,13 +583,14 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         int unit = 0;
         for (; next_unit(); ++unit) {
             const int r = w.row_first + t * 128 + trow;
-            const bool live = r < w.nrows;
+            const bool live = r < w.n * a.group;
             const int i_row = r / a.group;
-            const int64_t row0 = a.starts ? a.starts[w.b] : w.b;
+            const int64_t row0 = w.row0;
             const int head = w.h * a.group + r - i_row * a.group;
-            const int limit = live ? w.sq.len - w.sq.n + i_row + 1 : 0;
+            const int limit = live ? w.len - w.n + i_row + 1 : 0;
             float factor = 0.f;
-            if (w.steps > 0) {
+            const bool busy = w.j0 < w.j1;
+            if (busy) {
                 // ---- queries: f16 parts of q * 2^e, the sign of the scale in
                 // them.  QL lanes read a row, four dims each; eight reads on
                 // their way at a time.
@@ -530,7 +648,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             constexpr int kPass = PP == 1 ? 8 : 2, kBase = 14 - kPass;
             int m = kNone, mu = kNone;
             float l = 0.f, kf = kBase, kr = kBase - static_cast<float>(kNone);
-            for (int j = 0; j < w.steps; ++j, ++g, ++ss) {
+            for (int j = w.j0; j < w.j1; ++j, ++g, ++ss) {
                 wait(sc_full + g % kScales, g / kScales);
                 wait(s_full + t, ss);
                 fence_after();
@@ -626,7 +744,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         m = mn, mu = un;
                         kf = static_cast<float>(max(k_new, -126));
                         kr = kf - static_cast<float>(m);
-                        if (j > 0) {
+                        if (j > w.j0) {
 #pragma unroll 1
                             for (int q = 0; q < DP / 32; ++q) {
                                 tmem_load32(ot + q * 32, va);
@@ -675,7 +793,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const bool none = l == 0.f && m == kNone;
             const int down = none ? 0 : max(-min(kBase + m - mu, 126), -252);
             const float f1 = (none ? 0.f : 1.f / l) * pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
-            if (w.steps > 0) {
+            if (busy) {
                 wait(o_done + t, os);
                 ++os;
                 fence_after();
@@ -685,15 +803,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const int piece = a.type == QGKV_F32 ? 4 : 8;          // values of 16 bytes
             unsigned char* stage = smem + t * QP * F::kQTile + (warp & 3) * (QP * F::kQTile / 4);
             const int row_bytes = DP * 16 / piece;
-#pragma unroll 1
-            for (int q = 0; q < DP / 32; ++q) {
-                uint32_t v[32];
-                if (w.steps > 0) {
-                    tmem_load32(ot + q * 32, v);
-                    tmem_loaded();
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = none || w.steps == 0 ? 0u : __float_as_uint(__uint_as_float(v[i]) * f1 * f2v);
+            auto stage_out = [&](int q, const uint32_t(&v)[32]) {  // 32 dims of this lane's row
                 if (a.type == QGKV_F32) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
@@ -713,9 +823,97 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             make_uint4(o4[0], o4[1], o4[2], o4[3]);
                     }
                 }
+            };
+            // Partial results of this warp's rows: 32 log-sums, then pieces of 16
+            // bytes, lane by lane, so that each read and write is 512 bytes wide.
+            auto part_of = [&](int slot) {
+                return a.part + (static_cast<int64_t>(slot) * (TILES * 4) + warp) * (32 * (DP + 1));
+            };
+            float log_sum = none ? -INFINITY : static_cast<float>(m) + log2f(l);  // of base 2
+            bool ends = w.part < 0;  // this warp has the rows' result
+            float* mine_part = ends ? nullptr : part_of(w.part);
+#pragma unroll 1
+            for (int q = 0; q < DP / 32; ++q) {
+                uint32_t v[32];
+                if (busy) {
+                    tmem_load32(ot + q * 32, v);
+                    tmem_loaded();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = none || !busy ? 0u : __float_as_uint(__uint_as_float(v[i]) * f1 * f2v);
+                if (ends) {
+                    stage_out(q, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(reinterpret_cast<uint4*>(mine_part + 32 + ((q * 8 + i) * 32 + lane) * 4),
+                               make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                }
+            }
+            // Rare: NaN codes of V among tokens that not every row sees; those
+            // that this row sees, in this piece's keys.
+            auto nans = [&](auto put) {
+                if (INT8 || !live || nan_unit[unit & 7] != unit + 1) return;
+                const int from = max(max(0, w.len - w.n + w.row_first / a.group + 1) / kStepTokens, w.j0) * kStepTokens;
+                for (int tok = from; tok < min(limit, w.j1 * kStepTokens); ++tok) {
+                    const int id = a.table[static_cast<int64_t>(w.b) * a.width + (tok >> c.log2p)];
+                    if (id < 0 || id >= c.pages) continue;
+                    const uint8_t* p = c.v + id * c.page_stride + static_cast<int64_t>(w.h) * c.head_stride +
+                                       (tok & ((1 << c.log2p) - 1)) * c.token_stride;
+                    for (int d = 0; d < c.dim; ++d)
+                        if ((p[d] & 0x7F) == 0x7F) put(d, __int_as_float(0x7FC00000));
+                }
+            };
+            if (!ends) {
+                __stcg(mine_part + lane, log_sum);
+                nans([&](int d, float nan) { __stcg(mine_part + 32 + ((d >> 2) * 32 + lane) * 4 + (d & 3), nan); });
+                __threadfence();
+                __syncwarp();
+                unsigned* arrived = a.count + kCntPromptParts + w.owner * 8 + warp;
+                unsigned before = 0;
+                if (lane == 0) before = atomicAdd(arrived, 1u);
+                ends = __shfl_sync(~0u, before, 0) == static_cast<unsigned>(w.pieces - 1);
+                if (ends) {
+                    // The last to arrive joins the rows, in the order of the line.
+                    if (lane == 0) *arrived = 0u;
+                    __threadfence();
+                    auto slot_of = [&](int i) { return 2 * (w.owner + i) + (i == 0 ? 1 : 0); };
+                    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+                    for (int i = 0; i < w.pieces; ++i) top = fmaxf(top, __ldcg(part_of(slot_of(i)) + lane));
+                    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+                    for (int i = 0; i < w.pieces; ++i) sum += exp2_fast(__ldcg(part_of(slot_of(i)) + lane) - ref);
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                    for (int q = 0; q < DP / 32; ++q) {
+                        float acc[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 2
+                        for (int i = 0; i < w.pieces; ++i) {
+                            const float* p = part_of(slot_of(i));
+                            float4 x[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                x[k] = __ldcg(reinterpret_cast<const float4*>(p + 32 + ((q * 8 + k) * 32 + lane) * 4));
+                            const float f = exp2_fast(__ldcg(p + lane) - ref);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                acc[4 * k] = fmaf(f, x[k].x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, x[k].y, acc[4 * k + 1]);
+                                acc[4 * k + 2] = fmaf(f, x[k].z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, x[k].w, acc[4 * k + 3]);
+                            }
+                        }
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[i] * inv);
+                        stage_out(q, v);
+                    }
+                    log_sum = sum == 0.f ? -INFINITY : ref + log2f(sum);
+                }
             }
             __syncwarp();
-            {
+            if (ends) {
                 const int pieces = DP / piece, per = 32 / pieces;  // 16-byte pieces of a row, rows at once
                 const int64_t my_to = live ? to * c.dim : -1;
 #pragma unroll 4
@@ -728,26 +926,14 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + ch * 8) = x;
                     }
                 }
-            }
-            __syncwarp();  // ahead of what follows
-            if (live && a.lse)
-                a.lse[to] = none ? -INFINITY : (static_cast<float>(m) + log2f(l)) * 0.69314718055994531f;
-            if (!INT8 && live && nan_unit[unit & 7] == unit + 1) {
-                // rare: NaN codes of V among tokens that not every row sees; those that this row sees
-                const int first = max(0, w.seen_least) / kStepTokens * kStepTokens;
-                for (int tok = first; tok < limit; ++tok) {
-                    const int id = a.table[static_cast<int64_t>(w.b) * a.width + (tok >> c.log2p)];
-                    if (id < 0 || id >= c.pages) continue;
-                    const uint8_t* p = c.v + id * c.page_stride + static_cast<int64_t>(w.h) * c.head_stride +
-                                       (tok & ((1 << c.log2p) - 1)) * c.token_stride;
-                    for (int d = 0; d < c.dim; ++d)
-                        if ((p[d] & 0x7F) == 0x7F) {
-                            const float nan = __int_as_float(0x7FC00000);
-                            if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
-                            else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
-                            else static_cast<__nv_bfloat16*>(a.out)[to * c.dim + d] = __float2bfloat16_rn(nan);
-                        }
-                }
+                __syncwarp();  // ahead of what follows
+                if (live && a.lse) a.lse[to] = log_sum * 0.69314718055994531f;
+                if (w.part < 0)
+                    nans([&](int d, float nan) {
+                        if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
+                        else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
+                        else static_cast<__nv_bfloat16*>(a.out)[to * c.dim + d] = __float2bfloat16_rn(nan);
+                    });
             }
             fence_before();
             // the tile's warps have left its query memory
@@ -785,10 +971,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
             return cuda_fail(cudaGetLastError());
         done[dev].store(true, std::memory_order_release);
     }
-    // no more CTAs than units there can be
-    const int64_t most = (a.rows * a.group / F::ROWS + a.batch) * a.c.heads;
-    const int grid = static_cast<int>(std::min<int64_t>(sms, most));
-    kern<<<grid, F::warps * 32, F::smem, s>>>(a, kmap, vmap);
+    kern<<<sms, F::warps * 32, F::smem, s>>>(a, kmap, vmap);
     return launch_status();
 }
 

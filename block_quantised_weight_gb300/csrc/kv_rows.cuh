@@ -53,28 +53,6 @@ constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its lo
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
 
-// a / b for non-negative a and positive b, in 32 bits where they fit.
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The line of tiles cut into pieces of equal size, the first `more` one longer.
-struct Line {
-    int64_t each;
-    int more, ctas;
-    __device__ Line(int64_t total, int grid) {
-        ctas = total < grid ? static_cast<int>(total) : grid;
-        each = ctas ? div64(total, ctas) : 0;
-        more = static_cast<int>(total - each * ctas);
-    }
-    __device__ int64_t first(int cta) const { return each * cta + min(cta, more); }
-    __device__ int of(int64_t tile) const {
-        const int64_t long_part = (each + 1) * more;
-        return static_cast<int>(tile < long_part ? div64(tile, each + 1) : more + div64(tile - long_part, each));
-    }
-};
-
 constexpr int kNone = -(1 << 29);  // reference of a row that has seen nothing
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
 

@@ -217,6 +217,32 @@ def test_attention_prompts_of_many_sequences(kv, ws):
     check_attention(kv, ws, lens, rows, 8, 4, 64, 32, "e4m3", "hnd", "bf16", seed=60)
 
 
+@pytest.mark.parametrize("lens, rows", [
+    ([20011], [150]), ([9000, 40, 0, 2500, 3], [150, 200, 0, 1500, 90]), ([5000], [5000]), ([640, 700], [64, 64]),
+], ids=str)
+@pytest.mark.parametrize("heads, group, dim, page, dtype, fmt", [
+    (1, 4, 128, 64, "bf16", "e4m3"), (2, 2, 64, 16, "f32", "int8"), (3, 3, 96, 32, "f16", "e4m3"), (8, 1, 128, 128, "f32", "e4m3"),
+])
+def test_attention_prompts_of_few_blocks(kv, ws, lens, rows, heads, group, dim, page, dtype, fmt):
+    """Fewer row blocks than there is room for: their keys are split and the parts joined."""
+    check_attention(kv, ws, lens, rows, heads * group, heads, dim, page, fmt, "hnd", dtype, seed=heads)
+
+
+def test_attention_prompt_nan_codes_of_split_keys(kv, ws):
+    """NaN codes of V that only later rows see, in several parts of the keys."""
+    lens, rows = [3000], [1500]
+    cache, table, ln = make(kv, lens, 2, 64, 16, "e4m3", "hnd", seed=8)
+    q = torch.randn((1500, 4, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(9))
+    marks = ((1503, 0, 5), (2100, 1, 63), (2101, 0, 6), (2999, 1, 7), (40, 1, 9))
+    for tok, head, dim in marks:
+        cache.v[1, table[0, tok // 16].long(), head, tok % 16, dim] = 0xFF
+    out = kv.kv_attention(cache, 1, q, table, ln, starts=i32([0, 1500]), workspace=ws)
+    want = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    for tok, head, dim in marks:
+        want[max(0, tok - 1500):, 2 * head:2 * head + 2, dim] = True
+    assert torch.equal(torch.isnan(out), want)
+
+
 def test_attention_prompt_negative_scale(kv, ws):
     check_attention(kv, ws, [200], [150], 4, 2, 64, 16, "int8", "hnd", "f32", scale=-0.1)
     check_attention(kv, ws, [200], [1], 4, 2, 64, 16, "int8", "hnd", "f32", scale=-0.1)
@@ -225,7 +251,8 @@ def test_attention_prompt_negative_scale(kv, ws):
 @pytest.mark.parametrize("dtype, orders", [("f32", 20), ("f32", 26), ("f32", 30), ("f16", 26), ("f16", 30), ("bf16", 26)])
 @pytest.mark.parametrize("at", [3, 100, 200])
 @pytest.mark.parametrize("first", [0, 64, 128, 192])
-def test_attention_prompt_one_large_score(kv, ws, dtype, orders, at, first):
+@pytest.mark.parametrize("group", [1, 4])
+def test_attention_prompt_one_large_score(kv, ws, dtype, orders, at, first, group):
     """One token `orders` binary orders above the others, whose values are zero: what 64 of the others carry stays.
 
     A weight is stored as p' = p * 2^11 (bf16: 2^5) or more, in f16, with two roundings of parts by up to three
@@ -245,7 +272,7 @@ def test_attention_prompt_one_large_score(kv, ws, dtype, orders, at, first):
     k[at, 0] = e4(orders)
     cache.k[0, :16, 0] = k.view(16, 16, dim)
     cache.v[0, :16, 0] = v.view(16, 16, dim)
-    q = torch.zeros((rows, 1, dim), device="cuda")
+    q = torch.zeros((rows, group, dim), device="cuda")
     q[:, :, 0] = math.log(2)
     q = q.to(DT[dtype])
     table = i32([list(range(16))])
@@ -302,6 +329,21 @@ def test_attention_prompt_bad_page_is_reported_and_masked(kv, ws):
         keep = [i for i in range(table.shape[1]) if i != 2]
         ref = attention_ref(cache, 0, q, table[:, keep].contiguous(), [200 - 16], [0, 90], 0.125)
         close(out, None, ref, 200, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_attention_prompt_bad_page_of_many_rows(kv, ws, fmt):
+    """The same with enough rows for the prompt kernel and keys in several parts."""
+    cache, table, ln = make(kv, [700], 2, 64, 16, fmt, "hnd", seed=6)
+    q = torch.randn((300, 4, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    for wrong in (-1, cache.pages):
+        t = table.clone()
+        t[0, 2] = wrong
+        out = kv.kv_attention(cache, 0, q, t, ln, starts=i32([0, 300]), workspace=ws)
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+        keep = [i for i in range(table.shape[1]) if i != 2]
+        ref = attention_ref(cache, 0, q, table[:, keep].contiguous(), [700 - 16], [0, 300], 0.125)
+        close(out, None, ref, 700, torch.float32)
 
 
 @pytest.mark.parametrize("batch, context", [(1, 40000), (2, 9001), (70, 300), (300, 40)])
