@@ -141,6 +141,7 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     a.scale_log2 = scale * 1.4426950408889634f;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.part = reinterpret_cast<float*>(ws + qg::kWsPart);
+    a.splits = reinterpret_cast<int4*>(ws + qg::kWsSplits);
     a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
     a.status = st;
     // The tcgen05 kernel takes as long for one query row (token x head of a
@@ -150,8 +151,8 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     //   16 sequences of up to 4100 tokens: bf16 128 rows 111 / 114, 192 rows
     //   155 / 120; fp32 128 rows 138 / 146, 256 rows 252 / 224; f16 (two parts
     //   of p for two tiles) 192 rows 171 / 194, 256 rows 223 / 201
-    //   one sequence of 8000, bf16: 128 rows 39 / 85, 256 rows 58 / 87; of
-    //   30000: 256 rows 209 / 110
+    //   one sequence of 1000, bf16: 128 rows 17 / 29, 256 rows 30 / 31; of 8000:
+    //   128 rows 39 / 56, 256 rows 58 / 57; of 30000: 256 rows 209 / 89
     const int sms = qg::sm_count(qg::current_device());
     const int few = type == QGKV_F16 || 2 * static_cast<int64_t>(batch) * cache->heads < sms ? 256 : 128;
     const bool many = rows * a.group >= static_cast<int64_t>(few) * batch && starts && cache->head_dim <= 128;

@@ -19,6 +19,7 @@ struct AttnArgs {
     int64_t rows;
     float scale_log2;  // softmax scale * log2(e)
     float* part;
+    int4* splits;
     unsigned* count;
     unsigned* status;
 };

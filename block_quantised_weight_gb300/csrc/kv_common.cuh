@@ -38,13 +38,13 @@ constexpr int64_t kWsChunks = kWsRank + int64_t(QGKV_MAX_PAGES) * 4;  // 4096 wo
 constexpr int64_t kWsScalars = kWsChunks + 4096 * 4;                  // 256 words
 constexpr int64_t kWsPart = kWsShared;                                // partial results
 constexpr int64_t kWsPartBytes = int64_t(320) * 256 * 129 * 4;        // 320 of 256 rows x 128 dims and their sums
-constexpr int64_t kWsTotal = kWsPart + kWsPartBytes;
+constexpr int64_t kWsSplits = kWsPart + kWsPartBytes;                 // prompts whose keys are split: [160] x 32 bytes
+constexpr int64_t kWsTotal = kWsSplits + 160 * 32;
 static_assert(kWsScalars + 256 * 4 <= kWsTotal, "lists exceed the shared part");
 
 // Counter words by user.
 constexpr int kCntAttn = 0;      // [kMaxAttnCtas]
 constexpr int kCntPrompt = 4096; // [2] (from the attention's counters)
-constexpr int kCntPromptParts = kCntPrompt + 64;  // [kMaxPromptCtas * 8]
 constexpr int kCntPages = 8192;  // [1]
 constexpr int kCntBeam = 8320;   // [QGKV_MAX_BATCH]
 

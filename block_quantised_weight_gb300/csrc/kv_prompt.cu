@@ -15,11 +15,19 @@
 //
 // Bound.  4 * dim flops a score, 1 exponential: for 128 dims the tensor pipe
 // and the issue slots of the softmax are near each other.  So the roles run
-// beside each other: one warp copies (TMA), four convert the 8-bit codes into
+// beside each other: one warp finds the work and copies (TMA), four convert the 8-bit codes into
 // f16 operands (K as it lies, V transposed, so that both products take
 // K-major operands), one issues the MMAs, four a tile do the softmax.  The
 // MMAs of one tile run while the other's softmax does; the converted operands
-// serve both tiles.
+// serve both tiles.  Measured: prompt chunks (3 x 2048 rows behind up to 6000
+// tokens, 32 / 8 heads of 128, e4m3, bf16 q) 454 us, 677 TFLOP/s; fp32 q 1206 us,
+// fp16 q 924 us (two parts of q or p).  A step of 256 rows x 128 tokens takes
+// about 3.4 us: the MMAs alone about half of it, the softmax about as much.
+//
+// Split.  Many units (row block x head): CTAs take them from a counter.  Few: the
+// line of their steps is cut evenly, each CTA leaves at most two partial results
+// and qg_attn_join_kernel joins them in the order of the line (4 sequences of up
+// to 4100 tokens, 256 rows each: 115 us whole, 65 split).
 //
 // Shared memory: q 64 KB, four operand slots of 32 KB (K, V, K, V), two slots
 // of raw codes of 16 KB.  Tensor memory: S (128 columns) and O (dim columns)
@@ -37,8 +45,9 @@ constexpr int kMaxPromptCtas = 160;  // that share the line of steps: two part s
 // Fewer units than this many a CTA are split: 96 units 115 us whole, 65 split;
 // 192 units 178 / 160, 256 units 180 / 186, 512 units 258 / 295.
 constexpr int kSplitBelow = 2;
+constexpr int kLeastSteps = 2;  // of a CTA's share of the line (at 4, 1000 tokens x 256 rows: 37 us for 32)
 static_assert(int64_t(kMaxPromptCtas) * 2 * 256 * (128 + 1) * 4 <= kWsPartBytes, "partials exceed the workspace");
-static_assert(kCntPromptParts + kMaxPromptCtas * 8 <= kCntPages, "counters overlap");
+static_assert(kMaxPromptCtas * 32 <= kWsTotal - kWsSplits, "splits exceed the workspace");
 constexpr uint32_t kOps = 4;       // operand slots
 constexpr uint32_t kRaws = 2;      // raw slots
 constexpr uint32_t kUnits = 4;   // units handed to the roles ahead
@@ -128,10 +137,10 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&w)[
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A piece of work: steps j0 .. j1 - 1 of the keys of one row block and head.
-// Where that is not all its keys, the result is partial: pieces parts make
-// one, this CTA's goes to part slot `part`, `owner` is the first of their CTAs.
+// Where that is not all its keys, the result is partial and goes to part slot
+// `part`.
 struct Piece {
-    int b, h, row_first, n, len, row0, j0, j1, part, owner, pieces;  // b < 0: no more; part < 0: whole
+    int b, h, row_first, n, len, row0, j0, j1, part;  // b < 0: no more; part < 0: whole
 };
 
 // A row block's place in its sequence.
@@ -228,7 +237,7 @@ __device__ __forceinline__ int ceil_ref(float x) {
 template <int DP, int QP, int PP, bool INT8>  // PP: f16 parts of p
 __global__ void __launch_bounds__(PShape<DP, QP>::warps * 32, 1)
 qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap) {
+                      const __grid_constant__ CUtensorMap vmap, const bool may_split) {
     using F = PShape<DP, QP>;
     constexpr int TILES = F::TILES;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -310,21 +319,18 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         int64_t total = 0;
         while (by_unit.more(a)) total += by_unit.chunk;
         const int ctas = min(static_cast<int>(gridDim.x), kMaxPromptCtas);
-        const bool split = total < static_cast<int64_t>(kSplitBelow) * ctas;
+        const bool split = may_split && total < static_cast<int64_t>(kSplitBelow) * ctas;
         by_unit = Walk<F::ROWS, false>();
         int64_t at = 0, end = 0;
+        if (may_split && lane == 0 && static_cast<int>(blockIdx.x) < kMaxPromptCtas)
+            a.splits[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
         Line line(0, 1);
         if (split) {
             const int64_t all = total;
             total = 0;
             while (by_step.more(a)) total += by_step.chunk;
             by_step = Walk<F::ROWS, true>();
-            // A step takes 3.4 us, joining one part more about 1.9 (a unit's
-            // parts are joined by one CTA): S steps are best cut in about
-            // sqrt(1.7 S) parts.
-            const float mean = static_cast<float>(total) / static_cast<float>(max(all, static_cast<int64_t>(1)));
-            const int least = max(2, static_cast<int>(sqrtf(0.6f * mean)));
-            line = Line(total, static_cast<int>(min(static_cast<int64_t>(ctas), max(all, total / least))));
+            line = Line(total, static_cast<int>(min(static_cast<int64_t>(ctas), max(all, total / kLeastSteps))));
             if (static_cast<int>(blockIdx.x) < line.ctas) at = line.first(blockIdx.x), end = line.first(blockIdx.x + 1);
         }
         uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
@@ -333,7 +339,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             if (turn >= kUnits) wait(unit_empty + slot, turn / kUnits - 1);
             bool there = !dead;
             int64_t in = 0;
-            w.part = -1, w.owner = 0, w.pieces = 1, w.j0 = 0;
+            w.part = -1, w.j0 = 0;
             if (split) {
                 there = there && at < end && by_step.to(a, at, w, in);
             } else {
@@ -351,9 +357,12 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     if (in > 0 || at < stop) {
                         w.j0 = static_cast<int>(in);
                         w.j1 = static_cast<int>(at - start);
-                        w.owner = line.of(start);
-                        w.pieces = line.of(stop - 1) - w.owner + 1;
                         w.part = 2 * blockIdx.x + (in == 0 ? 1 : 0);
+                        if (in == 0 && lane == 0) {  // the first part: what the join has to know
+                            a.splits[2 * blockIdx.x] = make_int4(line.of(stop - 1) - static_cast<int>(blockIdx.x) + 1,
+                                                                 w.h, w.row_first, 0);
+                            a.splits[2 * blockIdx.x + 1] = make_int4(w.row0, w.n, 0, 0);
+                        }
                     }
                 }
             } else {
@@ -581,21 +590,27 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         const uint32_t st = tmem + t * 256 + lanes, ot = st + 128;
         uint32_t g = 0, ss = 0, os = 0;
         int unit = 0;
-        for (; next_unit(); ++unit) {
-            const int r = w.row_first + t * 128 + trow;
+        for (;; ++unit, ++turn) {
+            // The piece's description stays where it is and is read again after
+            // the loop over its steps, which has no registers to spare for it.
+            const uint32_t slot = turn % kUnits;
+            wait(unit_full + slot, turn / kUnits);
+            const volatile Piece& w = units[slot];
+            if (dead || w.b < 0) break;
+            const int j1 = w.j1, j0 = w.j0;
+            int r = w.row_first + t * 128 + trow;
             const bool live = r < w.n * a.group;
-            const int i_row = r / a.group;
-            const int64_t row0 = w.row0;
-            const int head = w.h * a.group + r - i_row * a.group;
-            const int limit = live ? w.len - w.n + i_row + 1 : 0;
+            const int limit = live ? w.len - w.n + r / a.group + 1 : 0;
             float factor = 0.f;
-            const bool busy = w.j0 < w.j1;
+            const bool busy = j0 < j1;
             if (busy) {
                 // ---- queries: f16 parts of q * 2^e, the sign of the scale in
                 // them.  QL lanes read a row, four dims each; eight reads on
                 // their way at a time.
                 constexpr int QL = DP / 4, QR = 32 / QL;
-                const int64_t mine = live ? (row0 + i_row) * a.q_row + head * a.q_head : -1;
+                const int i_row = r / a.group;
+                const int64_t mine = live ? (static_cast<int64_t>(w.row0) + i_row) * a.q_row +
+                                                (w.h * a.group + r - i_row * a.group) * a.q_head : -1;
                 const int d = (lane % QL) * 4;
                 unsigned char* qb = smem + t * QP * F::kQTile;
 #pragma unroll 1
@@ -648,7 +663,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             constexpr int kPass = PP == 1 ? 8 : 2, kBase = 14 - kPass;
             int m = kNone, mu = kNone;
             float l = 0.f, kf = kBase, kr = kBase - static_cast<float>(kNone);
-            for (int j = w.j0; j < w.j1; ++j, ++g, ++ss) {
+            for (int j = j0; j < j1; ++j, ++g, ++ss) {
                 wait(sc_full + g % kScales, g / kScales);
                 wait(s_full + t, ss);
                 fence_after();
@@ -744,7 +759,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         m = mn, mu = un;
                         kf = static_cast<float>(max(k_new, -126));
                         kr = kf - static_cast<float>(m);
-                        if (j > w.j0) {
+                        if (j > j0) {
 #pragma unroll 1
                             for (int q = 0; q < DP / 32; ++q) {
                                 tmem_load32(ot + q * 32, va);
@@ -789,7 +804,10 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             }
 
             // ---- the row's result
-            const int64_t to = (row0 + i_row) * a.q_heads + head;
+            r = w.row_first + t * 128 + trow;
+            const bool there = r < w.n * a.group;
+            const int i_row = r / a.group;
+            const int64_t to = (static_cast<int64_t>(w.row0) + i_row) * a.q_heads + w.h * a.group + r - i_row * a.group;
             const bool none = l == 0.f && m == kNone;
             const int down = none ? 0 : max(-min(kBase + m - mu, 126), -252);
             const float f1 = (none ? 0.f : 1.f / l) * pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
@@ -829,8 +847,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             auto part_of = [&](int slot) {
                 return a.part + (static_cast<int64_t>(slot) * (TILES * 4) + warp) * (32 * (DP + 1));
             };
-            float log_sum = none ? -INFINITY : static_cast<float>(m) + log2f(l);  // of base 2
-            bool ends = w.part < 0;  // this warp has the rows' result
+            const float log_sum = none ? -INFINITY : static_cast<float>(m) + log2f(l);  // of base 2
+            const bool ends = w.part < 0;
             float* mine_part = ends ? nullptr : part_of(w.part);
 #pragma unroll 1
             for (int q = 0; q < DP / 32; ++q) {
@@ -853,9 +871,9 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             // Rare: NaN codes of V among tokens that not every row sees; those
             // that this row sees, in this piece's keys.
             auto nans = [&](auto put) {
-                if (INT8 || !live || nan_unit[unit & 7] != unit + 1) return;
+                if (INT8 || !there || nan_unit[unit & 7] != unit + 1) return;
                 const int from = max(max(0, w.len - w.n + w.row_first / a.group + 1) / kStepTokens, w.j0) * kStepTokens;
-                for (int tok = from; tok < min(limit, w.j1 * kStepTokens); ++tok) {
+                for (int tok = from; tok < min(w.len - w.n + i_row + 1, w.j1 * kStepTokens); ++tok) {
                     const int id = a.table[static_cast<int64_t>(w.b) * a.width + (tok >> c.log2p)];
                     if (id < 0 || id >= c.pages) continue;
                     const uint8_t* p = c.v + id * c.page_stride + static_cast<int64_t>(w.h) * c.head_stride +
@@ -867,55 +885,11 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             if (!ends) {
                 __stcg(mine_part + lane, log_sum);
                 nans([&](int d, float nan) { __stcg(mine_part + 32 + ((d >> 2) * 32 + lane) * 4 + (d & 3), nan); });
-                __threadfence();
-                __syncwarp();
-                unsigned* arrived = a.count + kCntPromptParts + w.owner * 8 + warp;
-                unsigned before = 0;
-                if (lane == 0) before = atomicAdd(arrived, 1u);
-                ends = __shfl_sync(~0u, before, 0) == static_cast<unsigned>(w.pieces - 1);
-                if (ends) {
-                    // The last to arrive joins the rows, in the order of the line.
-                    if (lane == 0) *arrived = 0u;
-                    __threadfence();
-                    auto slot_of = [&](int i) { return 2 * (w.owner + i) + (i == 0 ? 1 : 0); };
-                    float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-                    for (int i = 0; i < w.pieces; ++i) top = fmaxf(top, __ldcg(part_of(slot_of(i)) + lane));
-                    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-                    for (int i = 0; i < w.pieces; ++i) sum += exp2_fast(__ldcg(part_of(slot_of(i)) + lane) - ref);
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll 1
-                    for (int q = 0; q < DP / 32; ++q) {
-                        float acc[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 2
-                        for (int i = 0; i < w.pieces; ++i) {
-                            const float* p = part_of(slot_of(i));
-                            float4 x[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                x[k] = __ldcg(reinterpret_cast<const float4*>(p + 32 + ((q * 8 + k) * 32 + lane) * 4));
-                            const float f = exp2_fast(__ldcg(p + lane) - ref);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                acc[4 * k] = fmaf(f, x[k].x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, x[k].y, acc[4 * k + 1]);
-                                acc[4 * k + 2] = fmaf(f, x[k].z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, x[k].w, acc[4 * k + 3]);
-                            }
-                        }
-                        uint32_t v[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[i] * inv);
-                        stage_out(q, v);
-                    }
-                    log_sum = sum == 0.f ? -INFINITY : ref + log2f(sum);
-                }
             }
             __syncwarp();
             if (ends) {
                 const int pieces = DP / piece, per = 32 / pieces;  // 16-byte pieces of a row, rows at once
-                const int64_t my_to = live ? to * c.dim : -1;
+                const int64_t my_to = there ? to * c.dim : -1;
 #pragma unroll 4
                 for (int r0 = 0; r0 < 32; r0 += per) {
                     const int row = r0 + lane / pieces, ch = lane % pieces;
@@ -927,18 +901,18 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     }
                 }
                 __syncwarp();  // ahead of what follows
-                if (live && a.lse) a.lse[to] = log_sum * 0.69314718055994531f;
-                if (w.part < 0)
-                    nans([&](int d, float nan) {
-                        if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
-                        else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
-                        else static_cast<__nv_bfloat16*>(a.out)[to * c.dim + d] = __float2bfloat16_rn(nan);
-                    });
+                if (there && a.lse) a.lse[to] = log_sum * 0.69314718055994531f;
+                nans([&](int d, float nan) {
+                    if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
+                    else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
+                    else static_cast<__nv_bfloat16*>(a.out)[to * c.dim + d] = __float2bfloat16_rn(nan);
+                });
             }
             fence_before();
             // the tile's warps have left its query memory
             __syncwarp();
             if (lane == 0) arrive_on(t_left + t);
+            if (lane == 0) arrive_on(unit_empty + slot);
             wait(t_left + t, static_cast<uint32_t>(unit));
         }
     }
@@ -955,6 +929,62 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     }
 }
 
+// Joins the parts of the units whose keys were split, in the order of the line:
+// a thread takes 32 dims of a row, a CTA those of a tile's 128 rows, so that
+// the parts (16 KB of them a CTA and part) come through all SMs.  In the last
+// CTA to arrive joining took about 2 us a part: one sequence of 256 query rows,
+// 8000 tokens 69 us (here 57), 30000 tokens 110 us (89).
+template <int DP, int TILES>
+__global__ void __launch_bounds__(128) qg_attn_join_kernel(const AttnArgs a) {
+    const int owner = blockIdx.x, t = blockIdx.y / (DP / 32), q = blockIdx.y % (DP / 32);
+    const int4 u0 = a.splits[2 * owner], u1 = a.splits[2 * owner + 1];
+    const int parts = u0.x, n = u1.y;
+    const int64_t row0 = u1.x;
+    if (parts <= 0) return;
+    if (owner + parts > kMaxPromptCtas || row0 < 0 || row0 + n > a.rows) {  // a workspace that was not zeroed
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusBounds);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = u0.z + t * 128 + threadIdx.x;
+    const bool live = r < n * a.group;
+    auto part_of = [&](int i) {
+        const int64_t slot = 2 * (owner + i) + (i == 0 ? 1 : 0);
+        return a.part + (slot * (TILES * 4) + t * 4 + warp) * (32 * (DP + 1));
+    };
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + lane));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float acc[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float* p = part_of(i);
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(p + 32 + ((q * 8 + k) * 32 + lane) * 4));
+        const float f = exp2_fast(__ldcg(p + lane) - ref);
+        sum += f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            acc[4 * k] = fmaf(f, x[k].x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, x[k].y, acc[4 * k + 1]);
+            acc[4 * k + 2] = fmaf(f, x[k].z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, x[k].w, acc[4 * k + 3]);
+        }
+    }
+    if (!live) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i_row = r / a.group;
+    const int64_t to = (row0 + i_row) * a.q_heads + u0.y * a.group + r - i_row * a.group;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (q * 32 + k * 4 < a.c.dim)
+            store_out4(a.out, a.type, to * a.c.dim + q * 32 + k * 4,
+                       make_float4(acc[4 * k] * inv, acc[4 * k + 1] * inv, acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    if (q == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
 template <int DP, int QP, int PP, bool INT8>
 int launch_one(const AttnArgs& a, cudaStream_t s) {
     using F = PShape<DP, QP>;
@@ -964,6 +994,9 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     CUtensorMap kmap, vmap;
     if (!encode_cache(&kmap, a.c, a.c.k, DP, 16, false) || !encode_cache(&vmap, a.c, a.c.v, DP, 16, false))
         return cuda_fail(cudaGetLastError());
+    // Rows that fill as many units as this leave none to split, and no join to launch.
+    const int ctas = std::min(sms, kMaxPromptCtas);
+    const bool split = a.rows * a.group / F::ROWS * a.c.heads < static_cast<int64_t>(kSplitBelow) * ctas;
     static std::atomic<bool> done[64];
     auto kern = qg_attn_prompt_kernel<DP, QP, PP, INT8>;
     if (!done[dev].load(std::memory_order_acquire)) {
@@ -971,7 +1004,8 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
             return cuda_fail(cudaGetLastError());
         done[dev].store(true, std::memory_order_release);
     }
-    kern<<<sms, F::warps * 32, F::smem, s>>>(a, kmap, vmap);
+    kern<<<sms, F::warps * 32, F::smem, s>>>(a, kmap, vmap, split);
+    if (split) qg_attn_join_kernel<DP, F::TILES><<<dim3(ctas, F::TILES * (DP / 32)), 128, 0, s>>>(a);
     return launch_status();
 }
 
