@@ -171,7 +171,7 @@ QG_API int qgkv_free(int64_t pages, int page_tokens, int32_t* table, int64_t tab
  * beam, as qgkv_fork takes it), each [requests][keep].  A row that holds NaN
  * or +inf, or nothing but -inf, or whose cum is NaN or +inf, scores -inf throughout.
  * QG_ESCRATCH where requests * beams * (8 * keep + 16) bytes of partial results
- * exceed the workspace's room for them (16 MB). */
+ * exceed the workspace's room for them (42 MB). */
 QG_API int qgbeam_select(const void* logits, int type, const float* cum, int requests, int beams, int64_t vocab,
                          int64_t row_stride, int keep, float* scores, int32_t* tokens, int32_t* parents,
                          void* workspace, int64_t workspace_bytes, cudaStream_t stream);
