@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kStepTokens = 128;
 constexpr int kMaxPromptCtas = 160;  // that share the line of steps: two part slots each
-// Fewer units than this many a CTA are split: 96 units 115 us whole, 65 split;
+// Fewer units than this many a CTA are split: 32 units 115 us whole, 65 split;
 // 192 units 178 / 160, 256 units 180 / 186, 512 units 258 / 295.
 constexpr int kSplitBelow = 2;
 constexpr int kLeastSteps = 2;  // of a CTA's share of the line (at 4, 1000 tokens x 256 rows: 37 us for 32)
