@@ -86,7 +86,7 @@ struct Shape {
     // shared memory: rings, queries, log-sums, row data, barriers, sequences and their prefix sums
     static constexpr int off_q(int) { return 4 * kRing; }
     static constexpr int off_ws(int parts) { return off_q(parts) + parts * MT * 4 * DC * 32 * 8; }
-    static constexpr int off_rows(int parts) { return off_ws(parts) + 8 * RU * 4; }
+    static constexpr int off_rows(int parts) { return off_ws(parts) + 4 * RU * 4; }
     static constexpr int off_bar(int parts) { return off_rows(parts) + RU * 16; }
     static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
 };
@@ -103,7 +103,6 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     extern __shared__ __align__(1024) unsigned char smem[];
     uint2* qf = reinterpret_cast<uint2*>(smem + F::off_q(QP));         // [QP][MT][4 * DC][32]
     float* ws = reinterpret_cast<float*>(smem + F::off_ws(QP));        // [4][RU] largest |q|, later log-sums
-    float* wb = ws + 4 * RU;                                              // [4][RU] sums of q
     int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(QP));  // [RU] output rows, -1 past the last
     int* limits = reinterpret_cast<int*>(orow + RU);                      // [RU] tokens that a row sees
     int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(QP));  // [batch + 1]
@@ -294,8 +293,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
             e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-            fac[mt] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (INT8 ? 16777216.f : 1.f);
-            f2 sum = {0.f, 0.f}, sum_lo = {0.f, 0.f};
+            fac[mt] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) {
                 // the dims in the order that k_codes gives a word's bytes
@@ -305,25 +303,17 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 f.x = pack_f16x2(x0, x1);
                 f.y = pack_f16x2(x2, x3);
                 qf[(mt * 4 * DC + cc * 4 + warp) * 32 + lane] = f;
-                if (INT8) fadd2(sum, h2_to_f2(f.x)), fadd2(sum, h2_to_f2(f.y));
                 if (QP == 2) {
                     uint2 fl;
                     fl.x = rest_f16x2(x0, x1, f.x);
                     fl.y = rest_f16x2(x2, x3, f.y);
                     qf[((MT + mt) * 4 * DC + cc * 4 + warp) * 32 + lane] = fl;
-                    if (INT8) fadd2(sum_lo, h2_to_f2(fl.x)), fadd2(sum_lo, h2_to_f2(fl.y));
                 }
-            }
-            if (INT8) {
-                float bias = (sum.x + sum.y) + (sum_lo.x + sum_lo.y);
-                bias += __shfl_xor_sync(~0u, bias, 1);
-                bias += __shfl_xor_sync(~0u, bias, 2);
-                if (t == 0) wb[warp * RU + mt * 8 + g] = bias;
             }
         }
         __syncthreads();
         // the scores a lane gets are those of rows 2t and 2t + 1 of each tile
-        float qfac[MT][2], init[MT][2];
+        float qfac[MT][2];
         int limit[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -331,7 +321,6 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             for (int i = 0; i < 2; ++i) {
                 const int r = mt * 8 + 2 * t + i;
                 qfac[mt][i] = __shfl_sync(~0u, fac[mt], (2 * t + i) * 4);
-                init[mt][i] = INT8 ? (wb[r] + wb[RU + r] + wb[2 * RU + r] + wb[3 * RU + r]) * kCodeBias : 0.f;
                 limit[mt][i] = limits[r];
             }
 
@@ -384,7 +373,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[mt][s][i] = INT8 ? init[mt][i & 1] : 0.f;
+                    for (int i = 0; i < 4; ++i) sc[mt][s][i] = 0.f;
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) {
                 uint4 k4[NS][2];
@@ -787,7 +776,8 @@ int launch_typed(const AttnArgs& a, cudaStream_t s) {
     //   e4m3, 128 dims: 48 rows 58.8 / 60.0, 64 rows 70.7 / 70.3, 128 rows 124 / 111
     // 256-dim heads keep 8 for their registers.
     // int8's conversions hold more registers: two CTAs an SM instead of three
-    // (attn_long 121 us for 130; e4m3's attn_batch 58 us for 56).
+    // (long documents 114 us for 118, though 48 sequences of up to 4100 tokens 64
+    // for 61; e4m3's batch 58 us for 56 with two).
     const int few = INT8 ? 16 : a.c.dim <= 64 ? 24 : 48;
     const bool wide = a.rows * a.group > few * static_cast<int64_t>(a.batch);
     if (a.c.dim <= 64) return wide ? launch_one<1, 2, QP, PP, INT8, 3>(a, s) : launch_one<1, 1, QP, PP, INT8, 3>(a, s);

@@ -190,6 +190,21 @@ def test_attention_several_rows(kv, ws, rows, dim, dtype, fmt):
     check_attention(kv, ws, lens, rows, 12, 4, dim, 32, fmt, "hnd", dtype)
 
 
+@pytest.mark.parametrize("rows", [1, 3, 40, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_int8_small_codes(kv, ws, rows, dtype):
+    """Small codes and queries of one sign: the scores are exact to their own size, not to that of 128 * sum(q)."""
+    n, dim = 700, 128
+    cache, table, ln = make(kv, [n], 2, dim, 32, "int8", "hnd", seed=21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    cache.k.copy_(torch.randint(-2, 3, cache.k.shape, device="cuda", generator=g).to(torch.int8).view(torch.uint8))
+    cache.k_scale.fill_(1.0)
+    q = (1.0 + 0.5 * torch.rand((rows, 4, dim), device="cuda", generator=g)).to(DT[dtype])
+    out, lse = kv.kv_attention(cache, 0, q, table, ln, starts=i32([0, rows]), return_lse=True, workspace=ws)
+    ref = attention_ref(cache, 0, q, table, [n], [0, rows], 1 / math.sqrt(dim))
+    close(out, lse, ref, n, DT[dtype], one_part=dtype == "bf16")
+
+
 def test_attention_rows_that_see_nothing(kv, ws):
     """More rows than tokens: the first rows' masks leave nothing; also empty sequences among full ones."""
     for lens, rows in (([2, 0, 0], [5, 3, 0]), ([0], [1]), ([0, 90, 0, 1], [1, 1, 1, 1]), ([30], [200])):
