@@ -20,8 +20,8 @@
 // K-major operands), one issues the MMAs, four a tile do the softmax.  The
 // MMAs of one tile run while the other's softmax does; the converted operands
 // serve both tiles.  Measured: prompt chunks (3 x 2048 rows behind up to 6000
-// tokens, 32 / 8 heads of 128, e4m3, bf16 q) 454 us, 677 TFLOP/s; fp32 q 1206 us,
-// fp16 q 924 us (two parts of q or p).  A step of 256 rows x 128 tokens takes
+// tokens, 32 / 8 heads of 128, e4m3, bf16 q) 452 us, 680 TFLOP/s; fp32 q 1204 us,
+// fp16 q 922 us (two parts of q or p).  A step of 256 rows x 128 tokens takes
 // about 3.4 us: the MMAs alone about half of it, the softmax about as much.
 //
 // Split.  Many units (row block x head): CTAs take them from a counter.  Few: the
@@ -447,25 +447,25 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         if (j > 0) {
                             const uint64_t vb = operand_desc(smem_u32(smem + F::off_op + (vo % kOps) * F::kOp));
 #pragma unroll
-                            for (int p = 0; p < PP; ++p)
+                            for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
                                 for (int ks = 0; ks < 8; ++ks) {
                                     const uint32_t pa = PP == 1 ? st + ks * 8 : st + (ks >> 2) * 64 + (ks & 3) * 8 + p * 32;
                                     mma_ts(ot, pa, vb + (((ks >> 2) * (DP * 128) + (ks & 3) * 32) >> 4), f16_desc(DP),
-                                           j > 1 || ks > 0 || p > 0 ? 1u : 0u);
+                                           j > 1 || ks > 0 || p < PP - 1 ? 1u : 0u);
                                 }
                             if (j == steps) commit_to(o_done + t);
                         }
                         if (j < steps) {
                             const uint64_t kb = operand_desc(smem_u32(smem + F::off_op + (ko % kOps) * F::kOp));
 #pragma unroll
-                            for (int p = 0; p < QP; ++p) {
+                            for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
                                 const uint64_t qb = operand_desc(smem_u32(smem + (t * QP + p) * F::kQTile));
 #pragma unroll
                                 for (int ks = 0; ks < DP / 16; ++ks)
                                     mma_ss(st, qb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
                                            kb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), f16_desc(kStepTokens),
-                                           p > 0 || ks > 0 ? 1u : 0u);
+                                           p < QP - 1 || ks > 0 ? 1u : 0u);
                             }
                             commit_to(s_full + t);
                         }
