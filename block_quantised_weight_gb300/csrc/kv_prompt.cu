@@ -770,6 +770,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             }
                         }
                         if (half == 1) {  // the first half's probabilities are stored already
+                            tmem_stored();  // and have arrived before they are read back
                             // in two factors: f16 ends at 2^-24, what is stored
                             // may come down by 2^-39 before it rounds to 0
                             const int e = max(order, -40);
