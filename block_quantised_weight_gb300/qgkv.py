@@ -4,7 +4,8 @@ paged key/value cache, its attention, page operations and beam selection.
 Argument marshalling only: each function checks torch CUDA tensors and calls
 the C entry point on the current torch stream (or on `stream=`).  There is
 no CPU fallback; a refused call raises ``qgemv.QGError``, a wrong type or shape
-``TypeError`` / ``ValueError``.
+``TypeError`` / ``ValueError``, and so do tensors that are not on the current
+device.
 
     cache = KVCache.allocate(layers=22, pages=4096, heads=4, page_tokens=64, head_dim=64)
     ws = KVWorkspace("cuda")
@@ -88,8 +89,15 @@ def _other(stream):
     return stream is not None and stream != torch.cuda.current_stream()
 
 
-def _stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _stream(*tensors):
+    """The current stream of the tensors' device (None is passed over).  They lie on one device and it is
+    the current one: the library launches there, on the pointers it is given."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor lies on cuda:{t.get_device()}, the current device is cuda:{device}: all "
+                             "have to be on the current device (torch.cuda.device)")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _need(t, dtype, name, shape=None):
@@ -161,6 +169,8 @@ class KVCache:
         self.heads, self.page_tokens = (a, b) if order == "hnd" else (b, a)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             _need(t, torch.float32, name, (self.layers, self.pages, self.heads))
+        if not k.get_device() == v.get_device() == k_scale.get_device() == v_scale.get_device():
+            raise ValueError("k, v and their scales must lie on one device")
         dense = a * b * self.head_dim
         self.c = QgkvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.layers, self.pages,
                            k.stride(0) if self.layers > 1 else dense, k.stride(1) if self.pages > 1 else dense,
@@ -203,7 +213,7 @@ def kv_append(cache, layer, k, v, table, lens, starts=None, stream=None):
     if (kind, rows, row, head) != (kind_v, rows_v, row_v, head_v):
         raise ValueError("k and v must have the same type, shape and strides")
     _call("qgkv_append", cache.ref, layer, kp, vp, kind, rows, row, head, tp, width, lp, sp, batch,
-          _stream(k))
+          _stream(k, v, cache.k, table, lens, starts))
 
 
 def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None, lse=None, return_lse=False,
@@ -233,7 +243,8 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
         ep = None
     w, wp, wb = _ws(workspace, q)
     _call("qgkv_attention", cache.ref, layer, qp, op, ep, kind, rows, heads, row, head, tp, width, lp, sp, batch,
-          cache.scale if scale is None else scale, wp, wb, _stream(q))
+          cache.scale if scale is None else scale, wp, wb,
+          _stream(q, cache.k, out, lse, table, lens, starts, w.buffer))
     return (out, lse) if return_lse else out
 
 
@@ -245,7 +256,7 @@ def kv_copy_pages(cache, src, dst, count=None, stream=None):
             return kv_copy_pages(cache, src, dst, count)
     sp, dp = _need(src, torch.int32, "src", (None,)), _need(dst, torch.int32, "dst", tuple(src.shape))
     cp = None if count is None else _need(count, torch.int32, "count", (1,))
-    _call("qgkv_copy_pages", cache.ref, sp, dp, cp, src.shape[0], _stream(src))
+    _call("qgkv_copy_pages", cache.ref, sp, dp, cp, src.shape[0], _stream(src, dst, count, cache.k))
 
 
 def _outs(table, refs, rows, out):
@@ -272,7 +283,7 @@ def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None, stream=N
     table2, lens2, refs2 = _outs(table, refs, rows, out)
     w, wp, wb = _ws(workspace, table)
     _call("qgkv_fork", cache.ref, tp, width, lp, batch, pp, rows, rp, table2.data_ptr(), lens2.data_ptr(),
-          refs2.data_ptr(), wp, wb, _stream(table))
+          refs2.data_ptr(), wp, wb, _stream(table, lens, parent, refs, table2, lens2, refs2, cache.k, w.buffer))
     return table2, lens2, refs2
 
 
@@ -289,7 +300,8 @@ def kv_compact(cache, table, lens, refs, drop=None, out=None, workspace=None, st
     count = torch.empty((1,), dtype=torch.int32, device=table.device)
     w, wp, wb = _ws(workspace, table)
     _call("qgkv_compact", cache.ref, tp, width, lp, batch, dp, rp, table2.data_ptr(), lens2.data_ptr(),
-          refs2.data_ptr(), count.data_ptr(), wp, wb, _stream(table))
+          refs2.data_ptr(), count.data_ptr(), wp, wb,
+          _stream(table, lens, drop, refs, table2, lens2, refs2, cache.k, w.buffer))
     return table2, lens2, refs2, count
 
 
@@ -309,7 +321,8 @@ def kv_reserve(cache, table, lens, refs, add=None, workspace=None, stream=None):
     ap = None if add is None else _need(add, torch.int32, "add", (batch,))
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
     w, wp, wb = _ws(workspace, table)
-    _call("qgkv_reserve", cache.pages, cache.page_tokens, tp, width, lp, ap, batch, rp, wp, wb, _stream(table))
+    _call("qgkv_reserve", cache.pages, cache.page_tokens, tp, width, lp, ap, batch, rp, wp, wb,
+          _stream(table, lens, add, refs, w.buffer))
 
 
 def kv_free(cache, table, lens, refs, drop=None, stream=None):
@@ -320,7 +333,7 @@ def kv_free(cache, table, lens, refs, drop=None, stream=None):
     batch, width, tp, lp, _ = _batch(table, lens, None)
     rp = _need(refs, torch.int32, "refs", (cache.pages,))
     _call("qgkv_free", cache.pages, cache.page_tokens, tp, width, lp, _mask(drop, batch), batch, rp,
-          _stream(table))
+          _stream(table, lens, drop, refs))
 
 
 def beam_select(logits, cum, keep, workspace=None, stream=None):
@@ -348,5 +361,5 @@ def beam_select(logits, cum, keep, workspace=None, stream=None):
     w, wp, wb = _ws(workspace, logits)
     _call("qgbeam_select", logits.data_ptr(), kind, cp, requests, beams, vocab,
           logits.stride(0) if rows > 1 else vocab, keep, scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), wp,
-          wb, _stream(logits))
+          wb, _stream(logits, cum, w.buffer))
     return scores, tokens, parents

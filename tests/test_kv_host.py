@@ -2,6 +2,8 @@
 import os
 import re
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "block_quantised_weight_gb300", "csrc")
 
@@ -13,3 +15,110 @@ def test_prompt_kernel_waits_for_stored_probabilities():
     at = src.index("if (half == 1) {")
     calls = re.findall(r"\b(tmem_stored|tmem_load32|tmem_store32)\(", src[at:])
     assert calls[:3] == ["tmem_stored", "tmem_load32", "tmem_store32"]
+
+
+torch = pytest.importorskip("torch")
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a CUDA device; its memory is never used."""
+
+    at = 0
+
+    @property
+    def is_cuda(self):
+        return True
+
+    def get_device(self):
+        return self.at
+
+
+def on(device, *shape, dtype=torch.int32):
+    t = torch.Tensor._make_subclass(OnDevice, torch.zeros(shape, dtype=dtype))
+    t.at = device
+    return t
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The binding with device 0 current and its calls recorded instead of made."""
+    from block_quantised_weight_gb300 import qgkv
+    made = []
+    monkeypatch.setattr(qgkv, "_call", lambda name, *args: made.append(name))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    return qgkv, made
+
+
+def cache_on(qgkv, device):
+    code = dict(dtype=torch.uint8)
+    scale = dict(dtype=torch.float32)
+    return qgkv.KVCache(on(device, 1, 3, 2, 16, 64, **code), on(device, 1, 3, 2, **scale),
+                        on(device, 1, 3, 2, 16, 64, **code), on(device, 1, 3, 2, **scale))
+
+
+class Workspace:
+    def __init__(self, device):
+        self.buffer, self.ptr, self.bytes = on(device, 8, dtype=torch.uint8), 0, 8
+
+
+# every tensor of every call: position in this list is the one that lies elsewhere
+OPERATORS = {
+    "qgkv_append": (4, lambda k, d: k.kv_append(
+        cache_on(k, d[0]), 0, on(d[1], 1, 2, 64, dtype=torch.float32), on(d[1], 1, 2, 64, dtype=torch.float32),
+        on(d[2], 1, 2), on(d[3], 1))),
+    "qgkv_attention": (8, lambda k, d: k.kv_attention(
+        cache_on(k, d[0]), 0, on(d[1], 1, 4, 64, dtype=torch.float32), on(d[2], 1, 2), on(d[3], 1), on(d[4], 2),
+        out=on(d[5], 1, 4, 64, dtype=torch.float32), lse=on(d[6], 1, 4, dtype=torch.float32), workspace=Workspace(d[7]))),
+    "qgkv_copy_pages": (4, lambda k, d: k.kv_copy_pages(cache_on(k, d[0]), on(d[1], 1), on(d[2], 1), on(d[3], 1))),
+    "qgkv_fork": (9, lambda k, d: k.kv_fork(
+        cache_on(k, d[0]), on(d[1], 1, 2), on(d[2], 1), on(d[3], 2), on(d[4], 3),
+        out=(on(d[5], 2, 2), on(d[6], 2), on(d[7], 3)), workspace=Workspace(d[8]))),
+    "qgkv_reserve": (5, lambda k, d: k.kv_reserve(
+        cache_on(k, 0), on(d[0], 1, 2), on(d[1], 1), on(d[2], 3), on(d[3], 1), workspace=Workspace(d[4]))),
+    "qgkv_free": (4, lambda k, d: k.kv_free(
+        cache_on(k, 0), on(d[0], 1, 2), on(d[1], 1), on(d[2], 3), on(d[3], 1, dtype=torch.uint8))),
+}
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_tensors_of_another_device_are_refused(calls, name):
+    """A launch goes to the current device: a pointer of another one must not reach it."""
+    qgkv, made = calls
+    count, call = OPERATORS[name]
+    call(qgkv, [0] * count)
+    assert made == [name]
+    for elsewhere in range(count):
+        with pytest.raises(ValueError, match="device"):
+            call(qgkv, [int(i == elsewhere) for i in range(count)])
+    with pytest.raises(ValueError, match="device"):
+        call(qgkv, [1] * count)
+    assert made == [name]
+
+
+def test_compaction_and_selection_of_another_device_are_refused(calls, monkeypatch):
+    """The calls that make their own outputs."""
+    qgkv, made = calls
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: on(0, *shape, dtype=dtype))
+    names = []
+    for d in ([0] * 8, *([int(i == j) for j in range(8)] for i in range(8))):
+        compact = lambda: qgkv.kv_compact(  # noqa: E731
+            cache_on(qgkv, 0), on(d[0], 1, 2), on(d[1], 1), on(d[2], 3), drop=on(d[3], 1, dtype=torch.uint8),
+            out=(on(0, 1, 2), on(0, 1), on(d[4], 3)), workspace=Workspace(0))
+        select = lambda: qgkv.beam_select(on(d[5], 2, 9, dtype=torch.float32), on(d[6], 1, 2, dtype=torch.float32), 2,  # noqa: E731
+                                          workspace=Workspace(d[7]))
+        for at, call in ((slice(0, 5), compact), (slice(5, 8), select)):
+            if any(d[at]):
+                with pytest.raises(ValueError, match="device"):
+                    call()
+            elif not any(d):
+                call()
+                names = list(made)
+    assert made == names == ["qgkv_compact", "qgbeam_select"]
+
+
+def test_cache_of_two_devices_is_refused(calls):
+    qgkv, _ = calls
+    one = cache_on(qgkv, 0)
+    with pytest.raises(ValueError, match="device"):
+        qgkv.KVCache(one.k, one.k_scale, one.v, on(1, 1, 3, 2, dtype=torch.float32))
