@@ -58,6 +58,7 @@ static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
 
 constexpr int kNone = -(1 << 29);  // reference of a row that has seen nothing
+constexpr int kMostK = 124;  // of k: p * 2^k stays finite, p being 4 at most
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
 
 // 2^k exactly; 0 below the normal range.
@@ -480,7 +481,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                             mn = max(mn, up);
                             un = max(un, up + evs[s]);
                         }
-                        const int k_old = min(12 + m[mt][i] - mu[mt][i], 126), k_new = min(12 + mn - un, 126);
+                        const int k_old = min(12 + m[mt][i] - mu[mt][i], kMostK), k_new = min(12 + mn - un, kMostK);
                         const float os = pow2i((k_new - mn) - (k_old - m[mt][i]));
                         l[mt][i] *= pow2i(m[mt][i] - mn);
 #pragma unroll
@@ -497,12 +498,13 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 }
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const float f0 = vs[s] * pk[mt][0], f1 = vs[s] * pk[mt][1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float p = exp2_fast(y[s][i]);
                         l[mt][i & 1] += p;
-                        y[s][i] = p * (i & 1 ? f1 : f0);
+                        // p first: vs * 2^k may pass the range where p is 0 (a row
+                        // that saw only small scales, and here sees nothing)
+                        y[s][i] = p * pk[mt][i & 1] * vs[s];
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -615,7 +617,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(~0u, sum, x);
                 // NaN sums stay NaN; a row that saw nothing has a sum of 0
                 const bool none = sum == 0.f && m[mt][i] == kNone;
-                const int down = none ? 0 : max(-min(12 + m[mt][i] - mu[mt][i], 126), -252);
+                const int down = none ? 0 : -min(12 + m[mt][i] - mu[mt][i], kMostK);
                 const float f1 = pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
                 const float inv = none ? 0.f : 1.f / sum;
                 const int r = mt * 8 + 2 * t + i;

@@ -48,3 +48,48 @@ def test_attention_prompt_scores_that_rise_in_every_half_step(kv, ws, dtype, gro
     q = q.to(DT[dtype])
     out, lse = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=1.0, return_lse=True, workspace=ws)
     close(out, lse, attention_ref(cache, 0, q, table, [n], [0, rows], 1.0), n, DT[dtype], one_part=dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim, fmt", [(64, "e4m3"), (64, "int8"), (128, "e4m3"), (256, "int8")])
+@pytest.mark.parametrize("rows", [2, 5, 14, 200])
+@pytest.mark.parametrize("scale", [4.0, 2.0 ** 20])
+def test_attention_large_scale_behind_a_block_of_zeros(kv, ws, dtype, dim, fmt, rows, scale):  # noqa: F811
+    """The first rows see blocks whose V scale is 0 alone, and give 0; a block of a large scale behind them,
+    which only later rows see, does not reach them."""
+    n = 16 + rows - 1
+    cache, table = ordered_cache(kv, n, 2, dim, fmt)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    for c in (cache.k, cache.v):
+        c.copy_(torch.randint(0, 100, c.shape, device="cuda", generator=g, dtype=torch.uint8))
+    cache.k_scale.fill_(0.01)
+    cache.v_scale[0, 0] = 0.0
+    cache.v_scale[0, 1:] = scale * (2.0 ** -10 if fmt == "int8" and dtype == "f16" else 1.0)
+    q = torch.randn((rows, 4, dim), device="cuda", generator=g).to(DT[dtype])
+    out, lse = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=0.1, return_lse=True, workspace=ws)
+    ref = attention_ref(cache, 0, q, table, [n], [0, rows], 0.1)
+    assert (out[0] == 0).all()
+    if dtype == "f16":  # what passes its range is infinite
+        fits = ref[0].abs() <= 65504
+        out = torch.where(fits, out, 0.0)
+        ref = (torch.where(fits, ref[0], 0.0), *ref[1:])
+    close(out, lse, ref, n, DT[dtype], one_part=dtype == "bf16")
+
+
+@pytest.mark.parametrize("rows", [1, 3, 300])
+@pytest.mark.parametrize("dim, fmt", [(64, "e4m3"), (128, "int8"), (256, "e4m3")])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_large_scale_of_low_scores(kv, ws, dtype, dim, fmt, rows):  # noqa: F811
+    """Blocks whose V scales differ by 2^120, the large one's scores 150 to 300 binary orders below: its weights are 0."""
+    n = 20 + 2 * rows
+    cache, table = ordered_cache(kv, n, 1, dim, fmt)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    cache.v.copy_(torch.randint(0, 100, cache.v.shape, device="cuda", generator=g, dtype=torch.uint8))
+    cache.k.fill_(code(-2, fmt))
+    cache.k[0, 0] = code(1, fmt)
+    cache.v_scale.fill_(2.0 ** 60)
+    cache.v_scale[0, 0] = 2.0 ** -60
+    q = (50.0 + 50.0 * torch.rand((rows, 2, dim), device="cuda", generator=g)).to(DT[dtype])
+    scale = math.log(2) / dim  # scores 50 to 100 on the first block, -200 to -100 behind it
+    out, lse = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=scale, return_lse=True, workspace=ws)
+    close(out, lse, attention_ref(cache, 0, q, table, [n], [0, rows], scale), n, DT[dtype], one_part=dtype == "bf16")
