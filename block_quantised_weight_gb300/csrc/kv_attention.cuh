@@ -69,6 +69,24 @@ struct Line {
     }
 };
 
+// References of the running softmax.  m of a row is a whole number held as a
+// float, so that it follows scores of any size, kNoRef before the row's first
+// token; d, the reference of score + log2 vs, is held less m, at least kNoOrder (no
+// value but zeros yet).
+constexpr float kNoRef = -3.402823466e38f;
+constexpr int kNoOrder = -1000;
+// From here on a score's rounding (2^-24 of it) is no small part of a binary
+// order: the scores of a warp that has met one are rounded before the reference
+// is taken off, so that equal scores get equal weights.
+constexpr float kHugeScore = 0x1p22f;
+
+// 2^k exactly; 0 below the normal range.
+__device__ __forceinline__ float pow2i(int k) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(k, -127), 127) + 127) << 23);
+}
+// A difference of binary orders (at most a few hundred) as an integer; -inf is far below all.
+__device__ __forceinline__ int order_of(float x) { return static_cast<int>(fmaxf(x, -4000.f)); }
+
 // Four consecutive output values.
 __device__ __forceinline__ void store_out4(void* out, int type, int64_t at, float4 x) {
     if (type == QGKV_F32) {

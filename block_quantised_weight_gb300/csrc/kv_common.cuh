@@ -37,7 +37,7 @@ constexpr int64_t kWsRank = kWsMovers + int64_t(QGKV_MAX_PAGES) * 4;
 constexpr int64_t kWsChunks = kWsRank + int64_t(QGKV_MAX_PAGES) * 4;  // 4096 words
 constexpr int64_t kWsScalars = kWsChunks + 4096 * 4;                  // 256 words
 constexpr int64_t kWsPart = kWsShared;                                // partial results
-constexpr int64_t kWsPartBytes = int64_t(320) * 256 * 129 * 4;        // 320 of 256 rows x 128 dims and their sums
+constexpr int64_t kWsPartBytes = int64_t(320) * 256 * 130 * 4;        // 320 of 256 rows x 128 dims, references and sums
 constexpr int64_t kWsSplits = kWsPart + kWsPartBytes;                 // prompts whose keys are split: [160] x 32 bytes
 constexpr int64_t kWsTotal = kWsSplits + 160 * 32;
 static_assert(kWsScalars + 256 * 4 <= kWsTotal, "lists exceed the shared part");

@@ -46,7 +46,7 @@ constexpr int kMaxPromptCtas = 160;  // that share the line of steps: two part s
 // 192 units 178 / 160, 256 units 180 / 186, 512 units 258 / 295.
 constexpr int kSplitBelow = 2;
 constexpr int kLeastSteps = 2;  // of a CTA's share of the line (at 4, 1000 tokens x 256 rows: 37 us for 32)
-static_assert(int64_t(kMaxPromptCtas) * 2 * 256 * (128 + 1) * 4 <= kWsPartBytes, "partials exceed the workspace");
+static_assert(int64_t(kMaxPromptCtas) * 2 * 256 * (128 + 2) * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxPromptCtas * 32 <= kWsTotal - kWsSplits, "splits exceed the workspace");
 constexpr uint32_t kOps = 4;       // operand slots
 constexpr uint32_t kRaws = 2;      // raw slots
@@ -225,14 +225,6 @@ struct Walk {
         return true;
     }
 };
-
-constexpr int kNone = -(1 << 29);
-__device__ __forceinline__ float pow2i(int k) {
-    return __uint_as_float(static_cast<uint32_t>(min(max(k, -127), 127) + 127) << 23);
-}
-__device__ __forceinline__ int ceil_ref(float x) {
-    return x == -INFINITY ? kNone : static_cast<int>(ceilf(fminf(fmaxf(x, -1.0e8f), 1.0e8f)));
-}
 
 template <int DP, int QP, int PP, bool INT8>  // PP: f16 parts of p
 __global__ void __launch_bounds__(PShape<DP, QP>::warps * 32, 1)
@@ -654,15 +646,16 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 if (lane == 0) arrive_on(q_full + t);
             }
 
-            // References: m of the scores, mu of score + log2 vs.  What is
+            // References: m of the scores, d + m of score + log2 vs.  What is
             // stored of a probability is 2^(score + log2 vs + kr), at most
             // 2^14.  One f16 part keeps its 11 bits 20 binary orders down, so
             // references may be passed by 8 (at 2 every fourth step went
             // round again, at 8 hardly one after a unit's first); two parts
             // keep 2^-37 of the largest, and 2 it is.
             constexpr int kPass = PP == 1 ? 8 : 2, kBase = 14 - kPass;
-            int m = kNone, mu = kNone;
-            float l = 0.f, kf = kBase, kr = kBase - static_cast<float>(kNone);
+            float m = kNoRef, l = 0.f, kf = kBase, kr = kBase - kNoRef;
+            int d = kNoOrder;
+            bool huge = false;  // of the warp: scores are first put into tensor memory less m
             for (int j = j0; j < j1; ++j, ++g, ++ss) {
                 wait(sc_full + g % kScales, g / kScales);
                 wait(s_full + t, ss);
@@ -676,10 +669,11 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     uint32_t hi[32], lo[PP == 2 ? 32 : 1];
                     float lh;
 #pragma unroll 1
-                    for (int round = 0; round < 2; ++round) {
+                    for (int round = 0;; ++round) {
                         // Optimistic: with the references as they are.  A score
-                        // that passes them by more than 2 sends the warp round again.
-                        bool passed = false;
+                        // that passes them by more than kPass sends the warp round
+                        // again, once: then none does.
+                        bool passed = huge && round == 0;
                         lh = 0.f;
                         uint32_t va[32], vb[32];
                         tmem_load32(sh, va);
@@ -695,8 +689,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 const float4 f = sc[grp];
                                 const float lvk = f.w + kf;
                                 const bool far = lvk < -100.f;  // a block whose values count for nothing (or are 0)
-                                const float add = far ? -static_cast<float>(m) : f.w + kr;
-                                const f2 fs = {factor * f.x, factor * f.x}, c2 = {add, add};
+                                const float add = far ? kr - kf : f.w + kr, fx = huge ? 1.f : factor * f.x;
+                                const f2 fs = {fx, fx}, c2 = {add, add};
                                 f2 y[8];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
@@ -728,37 +722,39 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 lh = fmaf(sum.x + sum.y, far ? 1.f : exp2_fast(-lvk), lh);
                             }
                         }
-                        if (!__any_sync(~0u, passed)) break;
-                        int mn = m, un = mu;
-                        if (round == 0) {
+                        if (round == 1 || !__any_sync(~0u, passed)) break;
+                        float mn = m, tops[4];
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                tmem_load32(sh + q * 32, va);
-                                tmem_loaded();
+                        for (int q = 0; q < 2; ++q) {
+                            tmem_load32(sh + q * 32, va);
+                            tmem_loaded();
 #pragma unroll
-                                for (int s = 0; s < 2; ++s) {
-                                    const int grp = half * 4 + q * 2 + s;
-                                    const float4 f = sc[grp];
-                                    const int seen = !passed || f.z == 0.f ? 0 : left - grp * 16;
-                                    float top = -INFINITY;
+                            for (int s = 0; s < 2; ++s) {
+                                const int grp = half * 4 + q * 2 + s;
+                                const float4 f = sc[grp];
+                                const int seen = !passed || f.z == 0.f ? 0 : left - grp * 16;
+                                float top = -INFINITY;
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        if (i < seen) top = fmaxf(top, __uint_as_float(va[s * 16 + i]));
-                                    if (top != -INFINITY) {
-                                        top *= factor * f.x;
-                                        mn = max(mn, ceil_ref(top));
-                                        un = max(un, ceil_ref(top + f.w));
-                                    }
-                                }
+                                for (int i = 0; i < 16; ++i)
+                                    if (i < seen) top = fmaxf(top, __uint_as_float(va[s * 16 + i]));
+                                if (top != -INFINITY) top = __fmul_rn(top, factor * f.x);
+                                tops[q * 2 + s] = top;
+                                mn = fmaxf(mn, ceilf(top));
                             }
                         }
-                        const int k_old = min(kBase + m - mu, 126), k_new = min(kBase + mn - un, 126);
-                        const int order = (k_new - mn) - (k_old - m);
+                        const int up = order_of(m - mn);
+                        int dn = max(d + up, kNoOrder);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            dn = max(dn, order_of(ceilf(tops[s] - mn + sc[half * 4 + s].w)));
+                        const int k_old = min(kBase - d, 126), k_new = min(kBase - dn, 126);
+                        const int order = k_new - k_old + up;
                         const float down = pow2i(order);
-                        l *= pow2i(m - mn);
-                        m = mn, mu = un;
+                        l *= pow2i(up);
+                        m = mn, d = dn;
+                        huge = __any_sync(~0u, huge || (m > kNoRef && fabsf(m) >= kHugeScore));
                         kf = static_cast<float>(max(k_new, -126));
-                        kr = kf - static_cast<float>(m);
+                        kr = huge ? kf : kf - m;
                         if (j > j0) {
 #pragma unroll 1
                             for (int q = 0; q < DP / 32; ++q) {
@@ -788,6 +784,18 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 tmem_store32(st + p * 32, va);
                             }
                         }
+                        if (huge) {
+#pragma unroll 1
+                            for (int q = 0; q < 2; ++q) {
+                                tmem_load32(sh + q * 32, va);
+                                tmem_loaded();
+                                const float f0 = factor * sc[half * 4 + q * 2].x, f1 = factor * sc[half * 4 + q * 2 + 1].x;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    va[i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(va[i]), i < 16 ? f0 : f1), m));
+                                tmem_store32(sh + q * 32, va);
+                            }
+                        }
                         tmem_stored();
                     }
                     l += lh;
@@ -809,8 +817,8 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const bool there = r < w.n * a.group;
             const int i_row = r / a.group;
             const int64_t to = (static_cast<int64_t>(w.row0) + i_row) * a.q_heads + w.h * a.group + r - i_row * a.group;
-            const bool none = l == 0.f && m == kNone;
-            const int down = none ? 0 : max(-min(kBase + m - mu, 126), -252);
+            const bool none = l == 0.f && m == kNoRef;
+            const int down = none ? 0 : -min(kBase - d, 126);
             const float f1 = (none ? 0.f : 1.f / l) * pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
             if (busy) {
                 wait(o_done + t, os);
@@ -843,12 +851,12 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     }
                 }
             };
-            // Partial results of this warp's rows: 32 log-sums, then pieces of 16
-            // bytes, lane by lane, so that each read and write is 512 bytes wide.
+            // Partial results of this warp's rows: 32 references and 32 sums, then
+            // pieces of 16 bytes, lane by lane, so that each read and write is 512
+            // bytes wide.
             auto part_of = [&](int slot) {
-                return a.part + (static_cast<int64_t>(slot) * (TILES * 4) + warp) * (32 * (DP + 1));
+                return a.part + (static_cast<int64_t>(slot) * (TILES * 4) + warp) * (32 * (DP + 2));
             };
-            const float log_sum = none ? -INFINITY : static_cast<float>(m) + log2f(l);  // of base 2
             const bool ends = w.part < 0;
             float* mine_part = ends ? nullptr : part_of(w.part);
 #pragma unroll 1
@@ -865,7 +873,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        __stcg(reinterpret_cast<uint4*>(mine_part + 32 + ((q * 8 + i) * 32 + lane) * 4),
+                        __stcg(reinterpret_cast<uint4*>(mine_part + 64 + ((q * 8 + i) * 32 + lane) * 4),
                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                 }
             }
@@ -884,8 +892,9 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 }
             };
             if (!ends) {
-                __stcg(mine_part + lane, log_sum);
-                nans([&](int d, float nan) { __stcg(mine_part + 32 + ((d >> 2) * 32 + lane) * 4 + (d & 3), nan); });
+                __stcg(mine_part + lane, none ? -INFINITY : m);
+                __stcg(mine_part + 32 + lane, l);
+                nans([&](int d, float nan) { __stcg(mine_part + 64 + ((d >> 2) * 32 + lane) * 4 + (d & 3), nan); });
             }
             __syncwarp();
             if (ends) {
@@ -902,7 +911,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     }
                 }
                 __syncwarp();  // ahead of what follows
-                if (there && a.lse) a.lse[to] = log_sum * 0.69314718055994531f;
+                if (there && a.lse) a.lse[to] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 nans([&](int d, float nan) {
                     if (a.type == QGKV_F32) static_cast<float*>(a.out)[to * c.dim + d] = nan;
                     else if (a.type == QGKV_F16) static_cast<__half*>(a.out)[to * c.dim + d] = __float2half_rn(nan);
@@ -951,7 +960,7 @@ __global__ void __launch_bounds__(128) qg_attn_join_kernel(const AttnArgs a) {
     const bool live = r < n * a.group;
     auto part_of = [&](int i) {
         const int64_t slot = 2 * (owner + i) + (i == 0 ? 1 : 0);
-        return a.part + (slot * (TILES * 4) + t * 4 + warp) * (32 * (DP + 1));
+        return a.part + (slot * (TILES * 4) + t * 4 + warp) * (32 * (DP + 2));
     };
     float top = -INFINITY, sum = 0.f;
 #pragma unroll 8
@@ -965,8 +974,8 @@ __global__ void __launch_bounds__(128) qg_attn_join_kernel(const AttnArgs a) {
         const float* p = part_of(i);
         float4 x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(p + 32 + ((q * 8 + k) * 32 + lane) * 4));
-        const float f = exp2_fast(__ldcg(p + lane) - ref);
+        for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(p + 64 + ((q * 8 + k) * 32 + lane) * 4));
+        const float f = exp2_fast(__ldcg(p + lane) - ref) * __ldcg(p + 32 + lane);
         sum += f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

@@ -12,9 +12,10 @@
 // as two.  m is at least the running maximum less 2 and k is chosen by a
 // bound u on s + log2 vs (k = 12 + m - u), so that what reaches o is at most
 // 2^14 and its largest part near that however the scales of the blocks
-// differ.  m and u are integers, which makes every rescaling a power of two,
+// differ.  m and u are whole numbers, which makes every rescaling a power of two,
 // and they move only when a score passes them by more than 2: a step costs one
-// vote instead of a reduction over its tokens.
+// vote instead of a reduction over its tokens.  (Scores from 2^22 on cost the
+// reduction in every step.)
 //
 // Bound.  Decode reads every code once for 4 * group flops a byte: HBM-bound
 // on the stream of codes if few instructions are spent on each (about 23 bytes
@@ -53,22 +54,12 @@ namespace {
 constexpr int kTile = 128;        // tokens of a tile: 4 warps x 32
 constexpr int kThreads = 128;
 constexpr int kMaxCtas = 640;     // partial slots: 2 per CTA
-constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its log-sums
+constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its references and sums
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
 
-constexpr int kNone = -(1 << 29);  // reference of a row that has seen nothing
 constexpr int kMostK = 124;  // of k: p * 2^k stays finite, p being 4 at most
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
-
-// 2^k exactly; 0 below the normal range.
-__device__ __forceinline__ float pow2i(int k) {
-    return __uint_as_float(static_cast<uint32_t>(min(max(k, -127), 127) + 127) << 23);
-}
-// The least integer >= x as a reference; kNone for -inf.
-__device__ __forceinline__ int ceil_ref(float x) {
-    return x == -INFINITY ? kNone : static_cast<int>(ceilf(fminf(fmaxf(x, -1.0e8f), 1.0e8f)));
-}
 
 // What the template arguments fix: DC chunks of 64 dims.
 template <int DC, int MT>
@@ -84,10 +75,10 @@ struct Shape {
     static constexpr int S = DC == 1 ? 3 : 2;        // stages of a warp's ring
     static constexpr int kRing = S * kStage;         // of one warp
     static_assert(RU * DP * 4 <= kRing, "a warp's result does not fit its ring");
-    // shared memory: rings, queries, log-sums, row data, barriers, sequences and their prefix sums
+    // shared memory: rings, queries, references and sums, row data, barriers, sequences and their prefix sums
     static constexpr int off_q(int) { return 4 * kRing; }
     static constexpr int off_ws(int parts) { return off_q(parts) + parts * MT * 4 * DC * 32 * 8; }
-    static constexpr int off_rows(int parts) { return off_ws(parts) + 4 * RU * 4; }
+    static constexpr int off_rows(int parts) { return off_ws(parts) + 2 * 4 * RU * 4; }
     static constexpr int off_bar(int parts) { return off_rows(parts) + RU * 16; }
     static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
 };
@@ -103,7 +94,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     constexpr int VL = F::NB;              // V reads per token row
     extern __shared__ __align__(1024) unsigned char smem[];
     uint2* qf = reinterpret_cast<uint2*>(smem + F::off_q(QP));         // [QP][MT][4 * DC][32]
-    float* ws = reinterpret_cast<float*>(smem + F::off_ws(QP));        // [4][RU] largest |q|, later log-sums
+    float* ws = reinterpret_cast<float*>(smem + F::off_ws(QP));        // [4][RU] largest |q|, later references
+    float* wl = ws + 4 * RU;                                             // [4][RU] sums
     int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(QP));  // [RU] output rows, -1 past the last
     int* limits = reinterpret_cast<int*>(orow + RU);                      // [RU] tokens that a row sees
     int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(QP));  // [batch + 1]
@@ -326,14 +318,15 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             }
 
         float o[MT][4 * DC][4];
-        int m[MT][2], mu[MT][2];    // references: m of the scores, mu of score + log2 vs
-        float ref[MT][2], pk[MT][2], l[MT][2];
+        float m[MT][2], pk[MT][2], l[MT][2];  // references of the scores, 2^k, sums
+        int d[MT][2];                         // references of score + log2 vs, less m
+        bool huge = false;                    // the same in all lanes
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[mt][i] = mu[mt][i] = kNone;
-                ref[mt][i] = static_cast<float>(kNone);
+                m[mt][i] = kNoRef;
+                d[mt][i] = kNoOrder;
                 pk[mt][i] = 1.f;
                 l[mt][i] = 0.f;
             }
@@ -428,7 +421,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             int evs[NS];
 #pragma unroll
             for (int s = 0; s < NS; ++s)
-                evs[s] = vs[s] > 0.f ? static_cast<int>((__float_as_uint(vs[s]) >> 23) & 255u) - 126 : kNone;
+                evs[s] = vs[s] > 0.f ? static_cast<int>((__float_as_uint(vs[s]) >> 23) & 255u) - 126 : kNoOrder;
             if (!full) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -444,57 +437,64 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 float y[NS][4];
-                auto relative = [&]() {  // scores less their reference
+                auto relative = [&](auto rounded) {  // scores less their reference
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
                         const float f0 = qfac[mt][0] * ks[s], f1 = qfac[mt][1] * ks[s];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            y[s][i] = fmaf(sc[mt][s][i], i & 1 ? f1 : f0, -ref[mt][i & 1]);
+                            const float f = i & 1 ? f1 : f0;
+                            y[s][i] = rounded && huge ? __fsub_rn(__fmul_rn(sc[mt][s][i], f), m[mt][i & 1])
+                                                      : fmaf(sc[mt][s][i], f, -m[mt][i & 1]);
                             if (!full && __float_as_int(sc[mt][s][i]) == kMasked) y[s][i] = -INFINITY;
                         }
                     }
                 };
-                relative();
-                bool passed = false;
+                relative(std::false_type());
+                bool passed = huge;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int s = 0; s < NS; ++s) {
                         const float top = fmaxf(y[s][i], y[s][i + 2]);
-                        passed |= top > fminf(2.f, static_cast<float>(2 - (evs[s] + m[mt][i] - mu[mt][i])));
+                        passed |= top > fminf(2.f, static_cast<float>(2 - (evs[s] - d[mt][i])));
                     }
                 if (__any_sync(~0u, passed)) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        int mn = m[mt][i], un = mu[mt][i];
+                        float mn = m[mt][i], tops[NS];
 #pragma unroll
                         for (int s = 0; s < NS; ++s) {
                             const float f = qfac[mt][i] * ks[s];
                             float top = -INFINITY;
 #pragma unroll
                             for (int j = i; j < 4; j += 2)
-                                if (full || __float_as_int(sc[mt][s][j]) != kMasked) top = fmaxf(top, sc[mt][s][j] * f);
+                                if (full || __float_as_int(sc[mt][s][j]) != kMasked)
+                                    top = fmaxf(top, __fmul_rn(sc[mt][s][j], f));
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                            const int up = ceil_ref(top);
-                            mn = max(mn, up);
-                            un = max(un, up + evs[s]);
+                            tops[s] = ceilf(top);
+                            mn = fmaxf(mn, tops[s]);
                         }
-                        const int k_old = min(12 + m[mt][i] - mu[mt][i], kMostK), k_new = min(12 + mn - un, kMostK);
-                        const float os = pow2i((k_new - mn) - (k_old - m[mt][i]));
-                        l[mt][i] *= pow2i(m[mt][i] - mn);
+                        const int down = order_of(m[mt][i] - mn);
+                        int dn = max(d[mt][i] + down, kNoOrder);
+#pragma unroll
+                        for (int s = 0; s < NS; ++s) dn = max(dn, order_of(tops[s] - mn) + evs[s]);
+                        const int k_old = min(12 - d[mt][i], kMostK), k_new = min(12 - dn, kMostK);
+                        const float os = pow2i(k_new - k_old + down);
+                        l[mt][i] *= pow2i(down);
 #pragma unroll
                         for (int j = 0; j < 4 * DC; ++j) {
                             o[mt][j][i] *= os;
                             o[mt][j][i + 2] *= os;
                         }
                         m[mt][i] = mn;
-                        mu[mt][i] = un;
-                        ref[mt][i] = static_cast<float>(mn);
+                        d[mt][i] = dn;
                         pk[mt][i] = pow2i(max(k_new, -126));
+                        huge |= mn > kNoRef && fabsf(mn) >= kHugeScore;
                     }
-                    relative();
+                    huge = __any_sync(~0u, huge);
+                    relative(std::true_type());
                 }
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
@@ -607,7 +607,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         }
         for (; it < steps; ++it) step(it, std::false_type());
 
-        // ---- this warp's normalised result and log-sum
+        // ---- this warp's normalised result, its reference and sum
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -616,12 +616,12 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(~0u, sum, x);
                 // NaN sums stay NaN; a row that saw nothing has a sum of 0
-                const bool none = sum == 0.f && m[mt][i] == kNone;
-                const int down = none ? 0 : -min(12 + m[mt][i] - mu[mt][i], kMostK);
+                const bool none = sum == 0.f && m[mt][i] == kNoRef;
+                const int down = none ? 0 : -min(12 - d[mt][i], kMostK);
                 const float f1 = pow2i(down >> 1), f2v = pow2i(down - (down >> 1));
                 const float inv = none ? 0.f : 1.f / sum;
                 const int r = mt * 8 + 2 * t + i;
-                if (g == 0) ws[warp * RU + r] = none ? -INFINITY : static_cast<float>(m[mt][i]) + log2f(sum);
+                if (g == 0) ws[warp * RU + r] = none ? -INFINITY : m[mt][i], wl[warp * RU + r] = sum;
                 float* dst = reinterpret_cast<float*>(ring) + r * DP + g * (4 * VW);
 #pragma unroll
                 for (int x = 0; x < VL; ++x)
@@ -653,7 +653,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             const float mx = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
             const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = exp2_fast(w[i] - ref);  // 0 for a warp without tokens, whose result is 0
+            for (int i = 0; i < 4; ++i) w[i] = exp2_fast(w[i] - ref) * wl[i * RU + r];  // 0 for a warp without tokens, whose result is 0
             const float sum = w[0] + w[1] + w[2] + w[3];
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -671,9 +671,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 else *reinterpret_cast<float4*>(part + r * c.dim + d) = acc;
             }
             if (row_lane == 0) {
-                const float ls = sum == 0.f ? -INFINITY : ref + log2f(sum);
-                if (!whole) part[2048 + r] = ls;
-                else if (a.lse) a.lse[to] = ls * 0.69314718055994531f;
+                if (!whole) part[2048 + r] = mx, part[2048 + 16 + r] = sum;
+                else if (a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
             }
         }
         if (!whole) {
@@ -694,23 +693,26 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 const float* p0 = a.part + static_cast<int64_t>(first * 2 + (line.first(first) < span0 ? 1 : 0)) * kPartFloats;
                 const float* p1 = a.part + static_cast<int64_t>(first) * 2 * kPartFloats;
                 auto part_of = [&](int i) { return i == 0 ? p0 : p1 + static_cast<int64_t>(i) * 2 * kPartFloats; };
-                // A lane's parts of the log-sums of its rows are all on their
-                // way before the first is used; then 16 parts of a row at a time.
+                // A lane's parts of the references and sums of its rows are all on
+                // their way before the first is used; then 16 parts of a row at a time.
                 constexpr int RW = RU * LPR / 128;  // rows of a lane
                 int64_t to[RW];
-                float ls0[RW];
+                float m0[RW], l0[RW];
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
                     const int r = row_of + i * (128 / LPR);
                     to[i] = orow[r];  // the lanes of a dead row take part in the shuffles
-                    ls0[i] = -INFINITY;
-                    if (to[i] >= 0 && row_lane < need) ls0[i] = __ldcg(part_of(row_lane) + 2048 + r);
+                    m0[i] = -INFINITY, l0[i] = 0.f;
+                    if (to[i] >= 0 && row_lane < need) {
+                        m0[i] = __ldcg(part_of(row_lane) + 2048 + r);
+                        l0[i] = __ldcg(part_of(row_lane) + 2048 + 16 + r);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
                     const int r = row_of + i * (128 / LPR);
                     const bool live = to[i] >= 0;
-                    float mx = ls0[i];
+                    float mx = m0[i];
                     for (int j = LPR + row_lane; live && j < need; j += LPR) mx = fmaxf(mx, __ldcg(part_of(j) + 2048 + r));
 #pragma unroll
                     for (int o2 = LPR / 2; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o2));
@@ -720,9 +722,13 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     for (int x2 = 0; x2 < XV; ++x2) acc[x2] = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
                     for (int base = 0; base < need; base += LPR) {
-                        float w = ls0[i];
-                        if (base) w = live && base + row_lane < need ? __ldcg(part_of(base + row_lane) + 2048 + r) : -INFINITY;
-                        w = exp2_fast(w - ref);
+                        float w = m0[i], lw = l0[i];
+                        if (base) {
+                            const bool held = live && base + row_lane < need;
+                            w = held ? __ldcg(part_of(base + row_lane) + 2048 + r) : -INFINITY;
+                            lw = held ? __ldcg(part_of(base + row_lane) + 2048 + 16 + r) : 0.f;
+                        }
+                        w = exp2_fast(w - ref) * lw;
                         sum += w;
                         for (int j0 = 0; j0 < LPR && base + j0 < need; j0 += 16) {
 #pragma unroll

@@ -116,7 +116,8 @@ QG_API int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, co
  * sum of two f16 parts (about 22 bits), 16-bit q exactly.  Probabilities enter
  * as two parts (and no weight probability * scale below 2^-37 of the row's
  * largest), for bf16 q as one (11 bits, below the output's rounding).
- * All sums are fp32.  Repeated calls give the same bits. */
+ * All sums are fp32.  Scores may have any size that fp32 holds; a row with one
+ * beyond it is NaN.  Repeated calls give the same bits. */
 QG_API int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                           int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
                           int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv_gpu import (DT, attention_ref, close, i32, kv, status_clean, ws)  # noqa: E402, F401
+from test_kv_gpu import (DT, attention_ref, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,38 @@ def test_attention_large_scale_of_low_scores(kv, ws, dtype, dim, fmt, rows):  # 
     scale = math.log(2) / dim  # scores 50 to 100 on the first block, -200 to -100 behind it
     out, lse = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=scale, return_lse=True, workspace=ws)
     close(out, lse, attention_ref(cache, 0, q, table, [n], [0, rows], scale), n, DT[dtype], one_part=dtype == "bf16")
+
+
+@pytest.mark.parametrize("unit", [18, 24, 30, 60, 120])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n, rows", [(1, 1), (3000, 1), (700, 3), (40, 40), (700, 300), (3000, 260)])
+@pytest.mark.parametrize("dim, fmt, dtype", [(64, "e4m3", "f32"), (128, "int8", "bf16"), (128, "e4m3", "f16"), (256, "e4m3", "bf16")])
+def test_attention_scores_of_any_size(kv, ws, unit, sign, n, rows, dim, fmt, dtype):  # noqa: F811
+    """Scores that are whole multiples, up to 8, of 2^unit: all weight is on the tokens of the largest, in equal
+    shares, over blocks whose V scales differ, warps, CTAs and parts.  The scores are exact, so their term of the
+    tolerance falls away.  With sign -1 all are at -2^unit or below."""
+    cache, table = ordered_cache(kv, n, 1, dim, fmt)
+    g = torch.Generator(device="cuda").manual_seed(unit)
+    what = torch.randint(-8, 9, (n,), generator=torch.Generator().manual_seed(n)).tolist()
+    if sign < 0:
+        what = [abs(x) + 1 for x in what]  # times a q of -1
+    k = torch.zeros((cache.pages * 16, dim), dtype=torch.uint8)
+    k[:n, 1] = torch.tensor([code(x, fmt) for x in what], dtype=torch.uint8)
+    cache.k[0, :, 0] = k.view(-1, 16, dim).cuda()
+    cache.v.copy_(torch.randint(0, 100, cache.v.shape, device="cuda", generator=g, dtype=torch.uint8))
+    cache.v_scale.copy_(torch.exp2(torch.randint(-6, 7, cache.v_scale.shape, device="cuda", generator=g).float()))
+    q = torch.zeros((rows, 2, dim), device="cuda")
+    q[:, :, 1] = sign
+    q = q.to(DT[dtype])
+    scale = 2.0 ** unit
+    out, lse = kv.kv_attention(cache, 0, q, table, i32([n]), starts=i32([0, rows]), scale=scale, return_lse=True, workspace=ws)
+    # equal shares of the largest (64-bit scores of this size do not hold the logarithm of their number)
+    x = sign * torch.tensor(what, dtype=torch.float64, device="cuda").expand(rows, n)
+    seen = torch.arange(n, device="cuda")[None, :] <= n - rows + torch.arange(rows, device="cuda")[:, None]
+    x = torch.where(seen, x, -math.inf)
+    top = x.amax(1, keepdim=True)
+    p = (x == top).double() / (x == top).sum(1, keepdim=True)
+    want = (p @ gather(cache, 0, table, 0, n, "v")[:, 0])[:, None].expand(rows, 2, dim)  # no value is negative
+    wl = (top * scale + torch.log((x == top).sum(1, keepdim=True))).expand(rows, 2)
+    zero = torch.zeros_like(wl)
+    close(out, lse, (want, wl, want, zero, zero), n, DT[dtype], one_part=dtype == "bf16")
