@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kBeamThreads, 3) qg_beam_kernel(const BeamArgs
             const int token = at + i * kBeamThreads;
             Key1 k = {0ull};
             if (token < end && x[i] == x[i])
-                k.a = (static_cast<unsigned long long>(ordered(x[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(token));
+                // + 0: the two zeros are equal, and rank by their tokens
+                k.a = (static_cast<unsigned long long>(ordered(x[i] + 0.f)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(token));
             return k;
         };
         // the floor from the threads' maxima so far, at steps 1, 2, 4, 8, ...

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv_gpu import (DT, attention_ref, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
+from test_kv_gpu import (DT, attention_ref, check_beam, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,15 @@ def test_attention_scores_of_any_size(kv, ws, unit, sign, n, rows, dim, fmt, dty
     wl = (top * scale + torch.log((x == top).sum(1, keepdim=True))).expand(rows, 2)
     zero = torch.zeros_like(wl)
     close(out, lse, (want, wl, want, zero, zero), n, DT[dtype], one_part=dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [9, 700, 32001])
+def test_beam_zeros_of_both_signs_are_equal(kv, ws, dtype, vocab):  # noqa: F811
+    """-0.0 and +0.0 score the same: the lowest (beam, token) comes first, whatever the signs."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    sign = torch.randint(0, 2, (4, vocab), device="cuda", generator=g).float() * 2 - 1
+    for x in (sign * 0.0, torch.where(torch.arange(vocab, device="cuda") % 3 == 0, -1.0, sign * 0.0)):
+        x[:, 0] = -0.0
+        for keep in (1, 2, min(8, 2 * vocab)):
+            check_beam(kv, ws, x.to(DT[dtype]), torch.zeros((2, 2), device="cuda"), keep)
