@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kBeamThreads, 3) qg_beam_kernel(const BeamArgs
 #pragma unroll
         for (int i = 0; i < kMergePer; ++i) {
             const int e = at0 + i * kBeamThreads + tid;
-            if (e >= total || !(upper[i] >= floor_value)) continue;
+            // a bound that is NaN (sums beyond fp32: -inf + inf) excludes nothing
+            if (e >= total || upper[i] < floor_value) continue;
             const double lse = row_lse[beam[i]];
             double score = -INFINITY;
             int64_t token = e - beam[i] * per_row;  // of a row that scores -inf throughout: its first tokens

@@ -2,11 +2,12 @@
 ends of their ranges.  Helpers and tolerances are test_kv_gpu's."""
 import math
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_kv_gpu import (DT, attention_ref, check_beam, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
+from test_kv_gpu import (DT, attention_ref, beam_ref, check_beam, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +141,23 @@ def test_beam_zeros_of_both_signs_are_equal(kv, ws, dtype, vocab):  # noqa: F811
         x[:, 0] = -0.0
         for keep in (1, 2, min(8, 2 * vocab)):
             check_beam(kv, ws, x.to(DT[dtype]), torch.zeros((2, 2), device="cuda"), keep)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_beam_scores_below_the_range_are_ranked(kv, ws, dtype):  # noqa: F811
+    """Masked by the type's lowest value on a beam that is masked the same way: the scores are -inf in fp32,
+    and still come in the order of their 64-bit values, all `keep` of them."""
+    low = torch.finfo(DT[dtype]).min
+    for vocab, keep in ((8, 24), (40, 120), (300, 128), (300, 3)):
+        x = torch.randn((3, vocab), device="cuda", generator=torch.Generator(device="cuda").manual_seed(vocab))
+        x[0, 2:] = low
+        x[1, 3:] = low
+        x[2] = low
+        x = x.to(DT[dtype])
+        cum = torch.tensor([[torch.finfo(torch.float32).min, -3.0, torch.finfo(torch.float32).min]], device="cuda")
+        s, t, p = kv.beam_select(x, cum, keep, workspace=ws)
+        want, wt, wp = beam_ref(x, cum, keep)
+        assert np.array_equal(t.cpu().numpy(), wt) and np.array_equal(p.cpu().numpy(), wp)
+        with np.errstate(over="ignore"):
+            want = want.astype(np.float32)
+        assert np.array_equal(np.isinf(want), np.isinf(s.cpu().numpy())) and (s[0, :-1] >= s[0, 1:]).all()
