@@ -501,7 +501,7 @@ struct ReserveArgs {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveArgs a) {
-    extern __shared__ int32_t pre[];  // [batch + 1] pages given to the sequences before
+    extern __shared__ uint32_t pre[];  // [batch + 1] pages given to the sequences before, modulo 2^32
     __shared__ int red[32];
     __shared__ int flag;
     const int tid = threadIdx.x;
@@ -513,7 +513,9 @@ __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveA
         if (tid == 0) a.chunks[blockIdx.x] = zeros;
     }
     if (!last_cta(a.counter, &flag)) return;
-    int base = 0;
+    // Up to 4096 sequences may ask for up to 2^20 pages each: their sum takes 33
+    // bits (that of the 1024 of one round 30).
+    int64_t base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int need = 0;
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveA
         }
         int before;
         const int sum = block_scan(need, before, red);
-        if (b < a.batch) pre[b + 1] = base + before + need;
+        if (b < a.batch) pre[b + 1] = static_cast<uint32_t>(base) + before + need;
         base += sum;
     }
     if (tid == 0) pre[0] = 0;
@@ -535,9 +537,10 @@ __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveA
     __syncthreads();
     if (base > avail) {  // one after the other: who does not fit gets none
         if (tid == 0) {
-            int given = 0, was = 0;
+            int given = 0;
+            uint32_t was = 0;
             for (int b = 0; b < a.batch; ++b) {
-                const int need = pre[b + 1] - was;
+                const int need = static_cast<int>(pre[b + 1] - was);
                 was = pre[b + 1];
                 if (given + need <= avail) given += need;
                 pre[b + 1] = given;
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveA
         }
         __syncthreads();
     }
-    const int needed = pre[a.batch];
+    const int needed = static_cast<int>(pre[a.batch]);  // at most avail from here on
     int given = 0;
     for (int ch = 0; given < needed && ch < static_cast<int>(gridDim.x); ++ch) {
         const int in_chunk = __ldcg(a.chunks + ch);
@@ -564,10 +567,10 @@ __global__ void __launch_bounds__(kPlanThreads) qg_reserve_kernel(const ReserveA
                     int lo = 0, hi = a.batch;  // the sequence whose share `at` lies in
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) >> 1;
-                        if (pre[mid] <= at) lo = mid; else hi = mid;
+                        if (pre[mid] <= static_cast<uint32_t>(at)) lo = mid; else hi = mid;
                     }
                     const int len = length_of(a.lens, lo, a.width, a.log2p, a.status);
-                    a.table[lo * a.width + pages_of(len, a.log2p) + (at - pre[lo])] = static_cast<int32_t>(p + j);
+                    a.table[lo * a.width + pages_of(len, a.log2p) + (at - static_cast<int>(pre[lo]))] = static_cast<int32_t>(p + j);
                     a.refs[p + j] = 1;
                 }
                 ++at;

@@ -7,6 +7,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from block_quantised_weight_gb300 import qgemv  # noqa: E402
 from test_kv_gpu import (DT, attention_ref, beam_ref, check_beam, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
@@ -161,3 +162,27 @@ def test_beam_scores_below_the_range_are_ranked(kv, ws, dtype):  # noqa: F811
         with np.errstate(over="ignore"):
             want = want.astype(np.float32)
         assert np.array_equal(np.isinf(want), np.isinf(s.cpu().numpy())) and (s[0, :-1] >= s[0, 1:]).all()
+
+
+@pytest.mark.parametrize("batch", [2049, 4096])
+def test_reserve_of_more_pages_than_32_bits_count(kv, ws, batch):  # noqa: F811
+    """Sequences that together ask for 2^31 pages and more: too few, and those that fit get theirs."""
+    page, width, pages = 16, 1 << 20, 5000
+    if torch.cuda.mem_get_info()[0] < batch * width * 4 + (1 << 30):
+        pytest.skip("not enough device memory")
+    table = torch.empty((batch, width), dtype=torch.int32, device="cuda")
+    table[:, :4] = -1
+    add = torch.full((batch,), width * page, dtype=torch.int32, device="cuda")
+    small = [3, 1024, batch - 1]
+    add[small] = i32([3 * page, 1, page + 1])
+    cache = kv.KVCache.allocate(1, pages, 1, page, 16)
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    free = [2, 4095, 4096, 4500, 4999]
+    refs[free] = 0
+    kv.kv_reserve(cache, table, torch.zeros_like(add), refs, add=add, workspace=ws)
+    assert qgemv.qg_device_status() == qgemv.QG_EPAGES
+    assert table[3, :4].tolist() == [2, 4095, 4096, -1] and table[1024, :2].tolist() == [4500, -1]
+    assert (table[batch - 1, :2] == -1).all() and refs.tolist().count(0) == 1
+    others = torch.ones(batch, dtype=torch.bool, device="cuda")
+    others[[3, 1024]] = False
+    assert (table[others, :4] == -1).all()
