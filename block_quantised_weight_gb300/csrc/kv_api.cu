@@ -53,10 +53,11 @@ int check_workspace(const void* ws, int64_t bytes) {
     return QG_OK;
 }
 
-// Rows of `heads` x dim values: strides that hold them, in whole 16 bytes.
+// Rows of `heads` x dim values: strides that hold them, in whole 16 bytes.  No
+// rows need no memory (an empty tensor's address is null).
 int check_rows(const void* p, int type, int64_t rows, int heads, int dim, int64_t row_stride, int64_t head_stride) {
     const int size = type_bytes(type);
-    if (!p || !size || rows < 0 || rows > kMost) return QG_EINVAL;
+    if ((!p && rows) || !size || rows < 0 || rows > kMost) return QG_EINVAL;
     if (row_stride < dim || head_stride < dim || row_stride > kMost || head_stride > kMost) return QG_EINVAL;
     if (off16(p) || row_stride * size % 16 || head_stride * size % 16) return QG_EALIGN;
     (void)heads;
@@ -119,7 +120,7 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     if (rc != QG_OK) return rc;
     if ((rc = check_batch(table, table_width, lens, batch)) != QG_OK) return rc;
     if (q_heads < 1 || q_heads % cache->heads || q_heads > 65536) return QG_EINVAL;
-    if (!out || !(scale > -3.0e38f && scale < 3.0e38f)) return QG_EINVAL;
+    if ((!out && rows) || !(scale > -3.0e38f && scale < 3.0e38f)) return QG_EINVAL;
     if ((rc = check_rows(q, type, rows, q_heads, cache->head_dim, row_stride, head_stride)) != QG_OK) return rc;
     if (!starts && rows != batch) return QG_EINVAL;
     if (off16(out) || off4(lse) || off4(starts)) return QG_EALIGN;
@@ -164,8 +165,9 @@ int qgkv_copy_pages(const qgkv_cache* cache, const int32_t* src, const int32_t* 
                     int64_t most, cudaStream_t stream) {
     const int rc = check_cache(cache, 0);
     if (rc != QG_OK) return rc;
-    if (!src || !dst || most < 0 || most > QGKV_MAX_PAGES) return QG_EINVAL;
+    if (most < 0 || most > QGKV_MAX_PAGES || (most && (!src || !dst))) return QG_EINVAL;
     if (off4(src) || off4(dst) || off4(count)) return QG_EALIGN;
+    if (most == 0) return QG_OK;
     unsigned* st = qg::status_ptr();
     if (!st) return qg::cuda_fail(cudaGetLastError());
     return qg::launch_copy_pages(*cache, src, dst, count, most, st, stream);

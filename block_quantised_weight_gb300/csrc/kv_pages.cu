@@ -639,7 +639,6 @@ int copy_ctas(const CopyArgs& a, int sms) {
 
 int launch_copy_pages(const qgkv_cache& c, const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
                       unsigned* status, cudaStream_t s) {
-    if (most == 0) return QG_OK;
     const CopyArgs a = copy_args(c, src, dst, count, most, status);
     const int sms = sm_count(current_device());
     if (sms <= 0) return cuda_fail(cudaGetLastError());

@@ -186,3 +186,15 @@ def test_reserve_of_more_pages_than_32_bits_count(kv, ws, batch):  # noqa: F811
     others = torch.ones(batch, dtype=torch.bool, device="cuda")
     others[[3, 1024]] = False
     assert (table[others, :4] == -1).all()
+
+
+def test_empty_tensors(kv, ws):  # noqa: F811
+    cache, table = ordered_cache(kv, 40, 2, 64, "e4m3")
+    none = torch.empty((0, 2, 64), device="cuda")
+    was = [x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    kv.kv_append(cache, 0, none, none, table, i32([40]), starts=i32([0, 0]))
+    out, lse = kv.kv_attention(cache, 0, torch.empty((0, 4, 64), device="cuda"), table, i32([40]), starts=i32([0, 0]),
+                               return_lse=True, workspace=ws)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    kv.kv_copy_pages(cache, i32([]), i32([]))
+    assert all(torch.equal(a, b) for a, b in zip(was, (cache.k, cache.v, cache.k_scale, cache.v_scale)))

@@ -122,3 +122,25 @@ def test_cache_of_two_devices_is_refused(calls):
     one = cache_on(qgkv, 0)
     with pytest.raises(ValueError, match="device"):
         qgkv.KVCache(one.k, one.k_scale, one.v, on(1, 1, 3, 2, dtype=torch.float32))
+
+
+def test_no_rows_and_no_pages_are_no_error():
+    """An empty tensor's address is null: nothing to do, on the host already."""
+    import ctypes
+    from block_quantised_weight_gb300 import build, qgemv, qgkv
+    build.build()
+    base = 0x100000
+    c = qgkv.QgkvCache(base, base + (1 << 28), base + (2 << 28), base + (3 << 28), 2, 64, 64 * 4096, 4096, 4, 16, 64, 1, 0)
+    table, lens, starts, ws = (base + (4 << 28) + (i << 20) for i in range(4))
+    f, ref = qgkv.load(), ctypes.addressof(c)
+    for k in (None, base + (5 << 28)):
+        assert f["qgkv_append"](ref, 0, k, k, 0, 0, 256, 64, table, 8, lens, starts, 3, None) == qgemv.QG_OK
+        assert f["qgkv_attention"](ref, 0, k, k, None, 2, 0, 32, 2048, 64, table, 8, lens, starts, 3, 0.1, ws, 1 << 30,
+                                   None) == qgemv.QG_OK
+        assert f["qgkv_copy_pages"](ref, k, k, None, 0, None) == qgemv.QG_OK
+    # with rows, or with what is wrong anyway, they stay errors
+    assert f["qgkv_append"](ref, 0, None, base, 0, 1, 256, 64, table, 8, lens, starts, 3, None) == qgemv.QG_EINVAL
+    assert f["qgkv_attention"](ref, 0, base, None, None, 2, 1, 32, 2048, 64, table, 8, lens, starts, 3, 0.1, ws, 1 << 30,
+                               None) == qgemv.QG_EINVAL
+    assert f["qgkv_append"](ref, 0, None, None, 9, 0, 256, 64, table, 8, lens, starts, 3, None) == qgemv.QG_EINVAL
+    assert f["qgkv_copy_pages"](ref, None, None, None, -1, None) == qgemv.QG_EINVAL
