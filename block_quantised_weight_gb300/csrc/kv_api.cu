@@ -123,6 +123,8 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     if ((!out && rows) || !(scale > -3.0e38f && scale < 3.0e38f)) return QG_EINVAL;
     if ((rc = check_rows(q, type, rows, q_heads, cache->head_dim, row_stride, head_stride)) != QG_OK) return rc;
     if (!starts && rows != batch) return QG_EINVAL;
+    // the kernels count the query rows of a cache head (tokens x heads of a group) in 32 bits
+    if (rows * (q_heads / cache->heads) > kMost - 512) return QG_EINVAL;
     if (off16(out) || off4(lse) || off4(starts)) return QG_EALIGN;
     if ((rc = check_workspace(workspace, workspace_bytes)) != QG_OK) return rc;
     if (rows == 0) return QG_OK;

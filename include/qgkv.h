@@ -105,7 +105,8 @@ QG_API int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, co
 /* Attention of `rows` query rows over the cache.  Sequence b holds lens[b]
  * tokens, its own rows' tokens included; row i of its n rows sees the first
  * lens[b] - n + i + 1 of them (causal at the end of the sequence).  Query
- * head j reads cache head j / (q_heads / heads).
+ * head j reads cache head j / (q_heads / heads); rows * (q_heads / heads) is at
+ * most 2^31 - 512.
  *   out = softmax(scale * q k^T) v,   lse = log(sum(exp(scale * q k^T)))
  * q: rows of [q_heads][head_dim] values of `type`, row_stride and head_stride
  * elements apart (multiples of 16 bytes).  out: [rows][q_heads][head_dim] of

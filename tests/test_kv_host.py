@@ -144,3 +144,20 @@ def test_no_rows_and_no_pages_are_no_error():
                                None) == qgemv.QG_EINVAL
     assert f["qgkv_append"](ref, 0, None, None, 9, 0, 256, 64, table, 8, lens, starts, 3, None) == qgemv.QG_EINVAL
     assert f["qgkv_copy_pages"](ref, None, None, None, -1, None) == qgemv.QG_EINVAL
+
+
+def test_attention_rows_beyond_32_bits_are_refused():
+    """The query rows of a cache head are counted in 32 bits on the device."""
+    import ctypes
+    from block_quantised_weight_gb300 import build, qgemv, qgkv
+    build.build()
+    base = 0x100000
+    c = qgkv.QgkvCache(base, base + (1 << 28), base + (2 << 28), base + (3 << 28), 1, 64, 64 * 4096, 4096, 1, 64, 16, 1, 0)
+    table, lens, starts, ws = (base + (4 << 28) + (i << 20) for i in range(4))
+    far = 1 << 45
+    attention = lambda rows, heads: qgkv.load()["qgkv_attention"](  # noqa: E731
+        ctypes.addressof(c), 0, far, 2 * far, None, 2, rows, heads, 16 * heads, 16, table, 8, lens, starts, 3, 0.1, ws,
+        1 << 30, None)
+    assert attention(1 << 20, 1 << 11) == qgemv.QG_EINVAL
+    assert attention((1 << 31) - 511, 1) == qgemv.QG_EINVAL
+    assert attention(1 << 30, 65536) == qgemv.QG_EINVAL
