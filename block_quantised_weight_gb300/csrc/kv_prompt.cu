@@ -326,6 +326,7 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             if (static_cast<int>(blockIdx.x) < line.ctas) at = line.first(blockIdx.x), end = line.first(blockIdx.x + 1);
         }
         uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
+        uint32_t sent = 0;      // raw tiles whose copies were issued
         for (;; ++turn) {
             const uint32_t slot = turn % kUnits;
             if (turn >= kUnits) wait(unit_empty + slot, turn / kUnits - 1);
@@ -414,10 +415,14 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     if (id >= 0 && !dead)
                         tma_load_4d(smem + F::off_raw + slot * F::kRaw + lane * 16 * DP, kv ? &vmap : &kmap, 0, tok, w.h, id,
                                     raw_full + slot);
+                    if (!dead) sent = o + 1;
                 }
                 if (j + 1 < w.j1) id = look(j + 1, f);
             }
         }
+        if (dead)  // the copies in flight: shared memory is theirs until they land
+            for (uint32_t x = sent > kRaws ? sent - kRaws : 0; x < sent; ++x)
+                (void)mbar_wait_bounded(raw_full + x % kRaws, (x / kRaws) & 1u, a.status);
     } else if (warp == F::warps - 1) {
         // ---------------------------------------------------------- MMAs
         uint32_t o = 0;                // operands taken

@@ -117,6 +117,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     }
     __syncwarp();
     unsigned issued = 0, taken = 0;  // stages over the life of the kernel
+    bool dead = false;  // a wait of this lane gave up: none follows, and no copy if it is lane 0, which issues them
 
     // ---- the line: prefix sums of the sequences' tiles
     {
@@ -216,7 +217,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             int id[NS];
 #pragma unroll
             for (int s = 0; s < NS; ++s) id[s] = __shfl_sync(~0u, odd ? id_c[1] : id_c[0], (it * NS + s) & 31);
-            if (lane == 0) {
+            if (lane == 0 && !dead) {
                 unsigned bytes = 0;
 #pragma unroll
                 for (int s = 0; s < NS; ++s) bytes += id[s] >= 0 ? F::kSub : 0;
@@ -359,7 +360,12 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 ks[s] = __shfl_sync(~0u, odd ? ks_c[1] : ks_c[0], from);
                 vs[s] = __shfl_sync(~0u, odd ? vs_c[1] : vs_c[0], from);
             }
-            mbar_wait_bounded(bar + taken % S, (taken / S) & 1, a.status);
+            if (!mbar_try_wait(bar + taken % S, (taken / S) & 1) && !dead &&
+                !mbar_wait_bounded(bar + taken % S, (taken / S) & 1, a.status)) {
+                dead = true;
+                for (unsigned x = taken; lane == 0 && x != issued; ++x)  // the copies in flight, once more
+                    (void)mbar_wait_bounded(bar + x % S, (x / S) & 1, a.status);
+            }
             // scores: rows are tokens g and g + 8 of a subtile, columns the query rows 2t and 2t + 1
             float sc[MT][NS][4];
 #pragma unroll

@@ -161,3 +161,13 @@ def test_attention_rows_beyond_32_bits_are_refused():
     assert attention(1 << 20, 1 << 11) == qgemv.QG_EINVAL
     assert attention((1 << 31) - 511, 1) == qgemv.QG_EINVAL
     assert attention(1 << 30, 65536) == qgemv.QG_EINVAL
+
+
+def test_no_verdict_of_a_bounded_wait_is_dropped():
+    """A wait that gave up ends its warp's further waits and copies (a wait that drains copies in flight says
+    that it has no use for the verdict)."""
+    for name in ("kv_rows.cuh", "kv_prompt.cu"):
+        src = open(os.path.join(CSRC, name)).read()
+        assert "mbar_wait_bounded(" in src
+        assert not re.search(r"^\s*mbar_wait_bounded\(", src, flags=re.M), name
+        assert not re.search(r"[;{}]\s*mbar_wait_bounded\(", src), name
