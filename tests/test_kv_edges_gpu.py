@@ -8,7 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from block_quantised_weight_gb300 import qgemv  # noqa: E402
-from test_kv_gpu import (DT, attention_ref, beam_ref, check_beam, close, gather, i32, kv, status_clean, ws)  # noqa: E402, F401
+from test_kv_gpu import (DT, append_ref, attention_ref, beam_ref, check_beam, close, counts, filled, fork_ref, gather,  # noqa: E402, F401
+                         i32, kv, make, starts_of, status_clean, values, ws)
 
 pytestmark = pytest.mark.gpu
 
@@ -198,3 +199,153 @@ def test_empty_tensors(kv, ws):  # noqa: F811
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
     kv.kv_copy_pages(cache, i32([]), i32([]))
     assert all(torch.equal(a, b) for a, b in zip(was, (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+
+
+def check_append(cache, layer, k, v, table, lens, rows):
+    """Appends and compares codes and scales of every page with test_kv_gpu's block by block reference."""
+    from block_quantised_weight_gb300 import qgkv
+    fmt, page, heads = cache.fmt, cache.page_tokens, cache.heads
+    st = starts_of(rows)
+    before = [(values(c.clone(), fmt).cpu().numpy(), s.cpu().numpy().copy()) for c, s in
+              ((cache.k, cache.k_scale), (cache.v, cache.v_scale))]
+    qgkv.kv_append(cache, layer, k, v, table, i32(lens), starts=None if all(r == 1 for r in rows) else i32(st))
+    ids = table.cpu().numpy()
+    for (codes, scale), c, s, x in zip(before, (cache.k, cache.v), (cache.k_scale, cache.v_scale), (k, v)):
+        x = x.float().cpu().numpy().astype(np.float64)
+        view = codes[layer] if cache.order == "hnd" else codes[layer].transpose(0, 2, 1, 3)
+        for b in range(len(lens)):
+            at, end = lens[b], lens[b] + rows[b]
+            while at < end:
+                pid, off = int(ids[b, at // page]), at % page
+                n = min(page - off, end - at)
+                r = st[b] + at - lens[b]
+                for h in range(heads):
+                    view[pid, h], scale[layer, pid, h] = append_ref(view[pid, h], scale[layer, pid, h], off, x[r:r + n, h], fmt)
+                at += n
+        assert np.array_equal(s.cpu().numpy(), scale)
+        assert np.array_equal(values(c, fmt).cpu().numpy(), codes)
+
+
+def new_rows(rows, heads, dim, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((rows, 2, heads, dim), device="cuda", generator=g)
+    x = (x * torch.exp2(torch.randint(-6, 6, (rows, 2, heads, 1), device="cuda", generator=g).float())).to(DT[dtype])
+    return x[:, 0], x[:, 1]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("page, dim", [(32, 64), (64, 64), (64, 128), (128, 128), (256, 80), (256, 256)])
+def test_append_blocks_of_every_size(kv, fmt, dtype, page, dim):  # noqa: F811
+    """Blocks of 2 to 64 vectors a thread: held in registers, or read twice; a partly filled first page."""
+    lens, rows = [page // 3, 0, 2 * page - 1], [page + 5, 2 * page, 3]
+    cache, table, _ = make(kv, [a + b for a, b in zip(lens, rows)], 2, dim, page, fmt, "nhd" if dim == 80 else "hnd", seed=page)
+    k, v = new_rows(sum(rows), 2, dim, dtype, dim)
+    check_append(cache, 1, k, v, table, lens, rows)
+
+
+@pytest.mark.parametrize("batch", [33, 70, 300])
+def test_append_ragged_batch(kv, batch):  # noqa: F811
+    """More sequences than a warp looks through at once, empty ones among them."""
+    g = np.random.default_rng(batch)
+    rows = [int(x) for x in g.integers(0, 40, batch) * (g.random(batch) < 0.6)]
+    lens = [int(x) for x in g.integers(0, 60, batch)]
+    cache, table, _ = make(kv, [a + b for a, b in zip(lens, rows)], 1, 64, 16, "int8", "hnd", seed=batch)
+    k, v = new_rows(sum(rows), 1, 64, "bf16", batch)
+    check_append(cache, 0, k, v, table, lens, rows)
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_largest_batch(kv, ws, rows):  # noqa: F811
+    """4096 sequences: attention, append, fork, reserve and free of as many as a call takes."""
+    batch, page, heads, dim = 4096, 16, 1, 64
+    g = np.random.default_rng(rows)
+    lens = [int(x) for x in g.integers(rows, 40, batch)]
+    cache, table, ln = make(kv, [n + rows for n in lens], heads, dim, page, "e4m3", "hnd", seed=rows, layers=1, width=4)
+    starts = None if rows == 1 else i32(starts_of([rows] * batch))
+    k, v = new_rows(rows * batch, heads, dim, "f32", rows)
+    kv.kv_append(cache, 0, k, v, table, i32(lens), starts=starts)
+    held = [n + rows for n in lens]
+    q = torch.randn((rows * batch, 2, dim), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    out, lse = kv.kv_attention(cache, 0, q, table, i32(held), starts=starts, return_lse=True, workspace=ws)
+    some = list(range(0, batch, 97)) + [batch - 1]
+    at = torch.tensor([[b * rows + i for i in range(rows)] for b in some], device="cuda").flatten()
+    ref = attention_ref(cache, 0, q[at], table[some], [held[b] for b in some], starts_of([rows] * len(some)), 1 / 8)
+    close(out[at], lse[at], ref, 64, torch.float32)
+
+    ids, pages = table.cpu().numpy(), cache.pages + 4096
+    pool = filled(kv, 1, pages, 1, page, 16)
+    refs = counts(ids, held, page, pages)
+    parent = [int(x) for x in g.integers(0, batch, batch)]
+    want = fork_ref(ids, held, parent, refs, page)
+    t2, l2, r2 = kv.kv_fork(pool, table, i32(held), i32(parent), i32(refs.tolist()), workspace=ws)
+    assert want[4] == 0 and np.array_equal(t2.cpu().numpy(), want[0]) and np.array_equal(r2.cpu().numpy(), want[2])
+    want_table, want_refs = want[0].copy(), want[2].copy()
+    free = [p for p in range(pages) if want_refs[p] == 0]
+    for b in range(batch):
+        if want[1][b] % page == 0 and want[1][b] // page < 4:
+            want_table[b, want[1][b] // page] = free.pop(0)
+            want_refs[want_table[b, want[1][b] // page]] = 1
+    full = [b for b in range(batch) if want[1][b] == 4 * page]
+    kv.kv_reserve(pool, t2, l2, r2, workspace=ws)
+    assert qgemv.qg_device_status() == (qgemv.QG_EBOUNDS if full else qgemv.QG_OK)
+    assert np.array_equal(t2.cpu().numpy(), want_table) and np.array_equal(r2.cpu().numpy(), want_refs)
+    kv.kv_free(pool, table, i32(held), i32(refs.tolist()))
+    assert (table == -1).all()
+
+
+def test_graph_replay_of_every_operator(kv):  # noqa: F811
+    """One graph of a decode step's operators, replayed on other values, against the same calls made directly; on a
+    stream of its own throughout."""
+    page, pages, layers, heads, dim, beams, vocab = 16, 200, 2, 2, 64, 4, 3001
+    side, ws = torch.cuda.Stream(), kv.KVWorkspace("cuda")  # noqa: F811
+    table = torch.full((beams, 12), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(beams, dtype=torch.int32, device="cuda"), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    cache = filled(kv, layers, pages, heads, page, dim)
+    starts = i32([0, 40, 80, 200, 360])
+    k, v = new_rows(360, heads, dim, "bf16", 3)
+    q = torch.randn((360, 4, dim), device="cuda").bfloat16()
+    logits, cum = torch.randn((beams, vocab), device="cuda"), torch.zeros((1, beams), device="cuda")
+    fixed = (cache.k, cache.v, cache.k_scale, cache.v_scale, table, lens, refs)
+    first = [x.clone() for x in fixed]
+
+    def step():
+        new = starts[1:] - starts[:-1]
+        kv.kv_reserve(cache, table, lens, refs, add=new, workspace=ws)
+        for layer in range(layers):
+            kv.kv_append(cache, layer, k, v, table, lens, starts=starts)
+        lens.add_(new)
+        a = kv.kv_attention(cache, 1, q, table, lens, starts=starts, workspace=ws)
+        s, t, p = kv.beam_select(logits, cum, beams, workspace=ws)
+        t2, l2, r2 = kv.kv_fork(cache, table, lens, p.view(-1), refs, workspace=ws)
+        drop = p.view(-1) % 2 == 0
+        t3, l3, r3, n = kv.kv_compact(cache, t2, l2, r2, drop=drop, workspace=ws)
+        kv.kv_copy_pages(cache, n + 1, n + 2, count=torch.ones_like(n))
+        kv.kv_free(cache, t3, l3, r3)
+        return a, s, t, p, t2, l2, r2, t3, l3, r3, n
+
+    def restore(i):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        for x, y in zip(fixed, first):
+            x.copy_(y)
+        logits.copy_(torch.randn(logits.shape, device="cuda", generator=g))
+        q.copy_(torch.randn(q.shape, device="cuda", generator=g))
+        k.copy_(torch.randn(k.shape, device="cuda", generator=g))
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = []
+        for i in range(3):
+            restore(i)
+            want.append([x.clone() for x in (*step(), *fixed)])
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = step()
+        for i in (2, 0, 1):
+            restore(i)
+            graph.replay()
+            for a, b in zip((*outs, *fixed), want[i]):
+                assert torch.equal(a, b)
+    side.synchronize()
+    assert (want[0][3] != want[1][3]).any() or (want[0][2] != want[1][2]).any()
