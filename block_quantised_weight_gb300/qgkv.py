@@ -5,7 +5,8 @@ Argument marshalling only: each function checks torch CUDA tensors and calls
 the C entry point on the current torch stream (or on `stream=`).  There is
 no CPU fallback; a refused call raises ``qgemv.QGError``, a wrong type or shape
 ``TypeError`` / ``ValueError``, and so do tensors that are not on the current
-device.
+device.  Tensors given to a call with `stream=` are recorded on that stream; the
+caller orders the streams.
 
     cache = KVCache.allocate(layers=22, pages=4096, heads=4, page_tokens=64, head_dim=64)
     ws = KVWorkspace("cuda")
@@ -84,9 +85,22 @@ def _call(name, *args):
         _q._check(name, rc)
 
 
-def _other(stream):
-    """Whether a call has to be made again with `stream` current, so that what it allocates belongs to it."""
-    return stream is not None and stream != torch.cuda.current_stream()
+def _other(stream, *tensors):
+    """Whether a call has to be made again with `stream` current, so that what it allocates belongs to it.
+    What it is given (None, caches and workspaces too) is lent to that stream: memory of a tensor that the
+    caller drops after the call is not used again before the stream is done with it."""
+    if stream is None or stream == torch.cuda.current_stream():
+        return False
+    for t in tensors:
+        if isinstance(t, KVCache):
+            _other(stream, t.k, t.k_scale, t.v, t.v_scale)
+        elif isinstance(t, KVWorkspace):
+            t.buffer.record_stream(stream)
+        elif isinstance(t, (tuple, list)):
+            _other(stream, *t)
+        elif isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return True
 
 
 def _stream(*tensors):
@@ -204,7 +218,7 @@ def _ws(workspace, t):
 def kv_append(cache, layer, k, v, table, lens, starts=None, stream=None):
     """Quantise new tokens k, v [rows, heads, head_dim] into the cache behind each
     sequence's lens[b] tokens (qgkv_append); rows by `starts`, or one a sequence."""
-    if _other(stream):
+    if _other(stream, cache, k, v, table, lens, starts):
         with torch.cuda.stream(stream):
             return kv_append(cache, layer, k, v, table, lens, starts)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
@@ -221,7 +235,7 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
     """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
     (qgkv_attention).  q [rows, q_heads, head_dim]; returns out, or (out, lse) with
     return_lse.  scale: 1 / sqrt(head_dim) where None."""
-    if _other(stream):
+    if _other(stream, cache, q, table, lens, starts, out, lse, workspace):
         with torch.cuda.stream(stream):
             return kv_attention(cache, layer, q, table, lens, starts, scale, out, lse, return_lse, workspace)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
@@ -251,7 +265,7 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
 def kv_copy_pages(cache, src, dst, count=None, stream=None):
     """Copy pages src[i] to dst[i] (int32), codes and scales of every layer; `count` (int32 [1])
     limits them on the device."""
-    if _other(stream):
+    if _other(stream, cache, src, dst, count):
         with torch.cuda.stream(stream):
             return kv_copy_pages(cache, src, dst, count)
     sp, dp = _need(src, torch.int32, "src", (None,)), _need(dst, torch.int32, "dst", tuple(src.shape))
@@ -273,7 +287,7 @@ def _outs(table, refs, rows, out):
 def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None, stream=None):
     """New sequences that continue sequences parent[i] (qgkv_fork): whole pages shared,
     shared partly filled pages copied.  Returns (table2, lens2, refs2); `out` takes the three."""
-    if _other(stream):
+    if _other(stream, cache, table, lens, parent, refs, out, workspace):
         with torch.cuda.stream(stream):
             return kv_fork(cache, table, lens, parent, refs, out, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
@@ -290,7 +304,7 @@ def kv_fork(cache, table, lens, parent, refs, out=None, workspace=None, stream=N
 def kv_compact(cache, table, lens, refs, drop=None, out=None, workspace=None, stream=None):
     """Free the sequences marked by drop (bool or uint8 [batch]) and move the held pages to the
     lowest numbers (qgkv_compact).  Returns (table2, lens2, refs2, count of held pages [1])."""
-    if _other(stream):
+    if _other(stream, cache, table, lens, refs, drop, out, workspace):
         with torch.cuda.stream(stream):
             return kv_compact(cache, table, lens, refs, drop, out, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
@@ -314,7 +328,7 @@ def _mask(drop, batch):
 def kv_reserve(cache, table, lens, refs, add=None, workspace=None, stream=None):
     """Give each sequence the pages that lens[b] + add[b] tokens need (add None: one token each);
     table and refs are updated (qgkv_reserve)."""
-    if _other(stream):
+    if _other(stream, cache, table, lens, refs, add, workspace):
         with torch.cuda.stream(stream):
             return kv_reserve(cache, table, lens, refs, add, workspace)
     batch, width, tp, lp, _ = _batch(table, lens, None)
@@ -327,7 +341,7 @@ def kv_reserve(cache, table, lens, refs, add=None, workspace=None, stream=None):
 
 def kv_free(cache, table, lens, refs, drop=None, stream=None):
     """Free the sequences marked by drop (None: all): table, lens and refs are updated (qgkv_free)."""
-    if _other(stream):
+    if _other(stream, cache, table, lens, refs, drop):
         with torch.cuda.stream(stream):
             return kv_free(cache, table, lens, refs, drop)
     batch, width, tp, lp, _ = _batch(table, lens, None)
@@ -340,7 +354,7 @@ def beam_select(logits, cum, keep, workspace=None, stream=None):
     """The `keep` best continuations of each request (qgbeam_select): logits
     [requests * beams, vocab], cum float32 [requests, beams].  Returns scores float32, tokens
     int32 and parents int32 (row numbers), each [requests, keep]."""
-    if _other(stream):
+    if _other(stream, logits, cum, workspace):
         with torch.cuda.stream(stream):
             return beam_select(logits, cum, keep, workspace)
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2:

@@ -349,3 +349,34 @@ def test_graph_replay_of_every_operator(kv):  # noqa: F811
                 assert torch.equal(a, b)
     side.synchronize()
     assert (want[0][3] != want[1][3]).any() or (want[0][2] != want[1][2]).any()
+
+
+def test_tensors_dropped_after_a_call_on_another_stream(kv):  # noqa: F811
+    """The caller's tables are dropped while the stream of the call is still busy with what came before; their
+    memory, free for its own stream, is not overwritten before the call has read it."""
+    page, pages, batch = 16, 400, 30
+    g = np.random.default_rng(4)
+    lens = [int(x) for x in g.integers(1, 100, batch)]
+    cache = filled(kv, 1, pages, 1, page, 16)
+    ids = np.full((batch, 8), -1, np.int32)
+    at, perm = 0, g.permutation(pages)
+    for b, n in enumerate(lens):
+        need = (n + page - 1) // page
+        ids[b, :need] = perm[at:at + need]
+        at += need
+    refs = counts(ids, lens, page, pages)
+    parent = [int(x) for x in g.integers(0, batch, 40)]
+    want = fork_ref(ids, lens, parent, refs, page)
+    side, own = torch.cuda.Stream(), kv.KVWorkspace("cuda")
+    given = [i32(x) for x in (ids.tolist(), lens, parent, refs.tolist())]
+    sizes = [t.shape for t in given]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # about 50 ms
+    outs = kv.kv_fork(cache, *given, workspace=own, stream=side)
+    del given
+    taken = [torch.zeros(s, dtype=torch.int32, device="cuda") for s in sizes for _ in range(3)]
+    side.synchronize()
+    for a, b in zip(outs, want):
+        assert np.array_equal(a.cpu().numpy(), b)
+    assert len(taken) == 12

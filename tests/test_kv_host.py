@@ -171,3 +171,64 @@ def test_no_verdict_of_a_bounded_wait_is_dropped():
         assert "mbar_wait_bounded(" in src
         assert not re.search(r"^\s*mbar_wait_bounded\(", src, flags=re.M), name
         assert not re.search(r"[;{}]\s*mbar_wait_bounded\(", src), name
+
+
+STREAMED = {
+    "kv_append": lambda k, t: k.kv_append(t(cache_on(k, 0)), 0, t(on(0, 1, 2, 64, dtype=torch.float32)),
+                                          t(on(0, 1, 2, 64, dtype=torch.float32)), t(on(0, 1, 2)), t(on(0, 1)),
+                                          starts=t(on(0, 2)), stream="side"),
+    "kv_attention": lambda k, t: k.kv_attention(
+        t(cache_on(k, 0)), 0, t(on(0, 1, 4, 64, dtype=torch.float32)), t(on(0, 1, 2)), t(on(0, 1)), starts=t(on(0, 2)),
+        out=t(on(0, 1, 4, 64, dtype=torch.float32)), lse=t(on(0, 1, 4, dtype=torch.float32)), workspace=t(Space(k)),
+        stream="side"),
+    "kv_copy_pages": lambda k, t: k.kv_copy_pages(t(cache_on(k, 0)), t(on(0, 1)), t(on(0, 1)), t(on(0, 1)), stream="side"),
+    "kv_fork": lambda k, t: k.kv_fork(t(cache_on(k, 0)), t(on(0, 1, 2)), t(on(0, 1)), t(on(0, 2)), t(on(0, 3)),
+                                      out=(t(on(0, 2, 2)), t(on(0, 2)), t(on(0, 3))), workspace=t(Space(k)), stream="side"),
+    "kv_compact": lambda k, t: k.kv_compact(
+        t(cache_on(k, 0)), t(on(0, 1, 2)), t(on(0, 1)), t(on(0, 3)), drop=t(on(0, 1, dtype=torch.uint8)),
+        out=(t(on(0, 1, 2)), t(on(0, 1)), t(on(0, 3))), workspace=t(Space(k)), stream="side"),
+    "kv_reserve": lambda k, t: k.kv_reserve(cache_on(k, 0), t(on(0, 1, 2)), t(on(0, 1)), t(on(0, 3)), add=t(on(0, 1)),
+                                            workspace=t(Space(k)), stream="side"),
+    "kv_free": lambda k, t: k.kv_free(cache_on(k, 0), t(on(0, 1, 2)), t(on(0, 1)), t(on(0, 3)),
+                                      drop=t(on(0, 1, dtype=torch.uint8)), stream="side"),
+    "beam_select": lambda k, t: k.beam_select(t(on(0, 2, 9, dtype=torch.float32)), t(on(0, 1, 2, dtype=torch.float32)), 2,
+                                              workspace=t(Space(k)), stream="side"),
+}
+
+
+def Space(qgkv):
+    w = qgkv.KVWorkspace.__new__(qgkv.KVWorkspace)
+    w.buffer, w.ptr, w.bytes = on(0, 8, dtype=torch.uint8), 0, 8
+    return w
+
+
+@pytest.mark.parametrize("name", STREAMED)
+def test_tensors_are_lent_to_the_stream_of_a_call(calls, monkeypatch, name):
+    """A caller may drop a tensor right after a call on another stream (`table, lens, refs = kv_fork(...)`): its
+    memory must not be used again before that stream is done."""
+    import contextlib
+    qgkv, made = calls
+    lent, current = [], ["main"]
+
+    @contextlib.contextmanager
+    def enter(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(OnDevice, "record_stream", lambda self, stream: lent.append((self.data_ptr(), stream)), raising=False)
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: on(0, *shape, dtype=dtype))
+    given = []
+
+    def take(x):
+        if isinstance(x, qgkv.KVCache):
+            given.extend((x.k, x.k_scale, x.v, x.v_scale))
+        else:
+            given.append(getattr(x, "buffer", x))
+        return x
+
+    STREAMED[name](qgkv, take)
+    assert len(made) == 1 and current == ["main"]
+    assert {(t.data_ptr(), "side") for t in given} <= set(lent)
