@@ -148,14 +148,22 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
     a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
     a.status = st;
     // The tcgen05 kernel takes as long for one query row (token x head of a
-    // group) a sequence as for 256, the row kernel's time grows with them; the
-    // first needs enough row blocks to fill the GPU without splitting keys.
-    // Row kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128:
-    //   16 sequences of up to 4100 tokens: bf16 128 rows 111 / 114, 192 rows
-    //   155 / 120; fp32 128 rows 138 / 146, 256 rows 252 / 224; f16 (two parts
-    //   of p for two tiles) 192 rows 171 / 194, 256 rows 223 / 201
-    //   one sequence of 1000, bf16: 128 rows 17 / 29, 256 rows 30 / 31; of 8000:
-    //   128 rows 39 / 56, 256 rows 58 / 57; of 30000: 256 rows 209 / 89
+    // group) a sequence as for 256, the row kernel's time grows with them.  Row
+    // kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128, by query rows a
+    // sequence (the same for each of a call):
+    //   16 sequences of up to 4100 tokens: bf16 96 rows 128 / 113, 128 rows 161 /
+    //   113, 256 rows 297 / 121; fp32 64 rows 111 / 141, 128 rows 198 / 144, 256
+    //   rows 368 / 255; f16 (two parts of p for two tiles) 128 rows 175 / 177, 256
+    //   rows 326 / 187
+    //   48 of up to 1000: bf16 64 rows 122 / 98, 128 rows 223 / 101; f16 128 rows
+    //   238 / 166
+    //   few row blocks, whose keys are split, bf16: 4 of up to 4100: 128 rows 56 /
+    //   56, 256 rows 92 / 59; one of 1000: 128 rows 18 / 30, 256 rows 27 / 31; of
+    //   8000: 128 rows 40 / 60, 256 rows 59 / 61; of 30000: 128 rows 93 / 90, 256
+    //   rows 161 / 95
+    // The border is late for f16 batches and for few but long sequences, by up to
+    // 1.4 times.  The mean over a call decides for all of it: a prompt among many
+    // single tokens goes the way of the single tokens, or they its.
     const int sms = qg::sm_count(qg::current_device());
     const int few = type == QGKV_F16 || 2 * static_cast<int64_t>(batch) * cache->heads < sms ? 256 : 128;
     const bool many = rows * a.group >= static_cast<int64_t>(few) * batch && starts && cache->head_dim <= 128;

@@ -12,9 +12,11 @@
 // block's values wait in registers (up to 16 vectors of 16 bytes a thread;
 // larger blocks are read a second time).  int8's quotient is formed as a
 // product, whose error is below 2^-16 of a code: only quotients that close to
-// a tie (or not finite) take the division, one in 2^14.  Measured: 5 prompts, 4001
-// rows of 8 heads of 128, bf16: int8 28.7 us (3.2 TB/s), e4m3 24.1 us; issue-bound,
-// 18 instructions a value (256 threads a CTA: 29.7 us).  48 single tokens: 2.4 us.
+// a tie (or not finite) take the division, one in 2^14.  Measured: 5 prompts of
+// up to 4001 rows, 14801 in all, 8 heads of 128, bf16: int8 28.7 us (3.2 TB/s),
+// e4m3 21.7 us; int8 by 18 instructions a value (256 threads a CTA: 29.7 us),
+// both by one chain a CTA (lengths, values, maximum, codes) with nothing of
+// its next block on the way.  48 single tokens: 2.4 us.
 #include "kv_common.cuh"
 #include "launch_common.cuh"
 #include "qgkv_launch.h"

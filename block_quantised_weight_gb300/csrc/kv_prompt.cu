@@ -9,7 +9,7 @@
 //   p = 2^(S * scale * ks + log2 vs + k - m),  one thread a row, over S as f16
 //   O += p V      p from tensor memory, V^T from shared memory
 // with l the sum of p less its block's scale.  A row's references m and u (k =
-// 6 + m - u, 12 for two parts of p) are integers that move only when a score
+// 6 + m - u, 12 for two parts of p) are whole numbers that move only when a score
 // passes them by more than 8 (2): the thread takes its 64 scores once, as if they held, and only where
 // one passes goes round again and rescales its row of O in tensor memory.
 //
@@ -19,9 +19,11 @@
 // f16 operands (K as it lies, V transposed, so that both products take
 // K-major operands), one issues the MMAs, four a tile do the softmax.  The
 // MMAs of one tile run while the other's softmax does; the converted operands
-// serve both tiles.  Measured: prompt chunks (3 x 2048 rows behind up to 6000
-// tokens, 32 / 8 heads of 128, e4m3, bf16 q) 452 us, 680 TFLOP/s; fp32 q 1204 us,
-// fp16 q 922 us (two parts of q or p).  A step of 256 rows x 128 tokens takes
+// serve both tiles.  Measured: prompt chunks (4812 rows in three, the longest of
+// 2048, behind up to 6000 tokens, 32 / 8 heads of 128, e4m3, bf16 q) 427-455 us,
+// 675-720 TFLOP/s (int8 457); fp32 q 1176 us (two parts of q and p: one tile, so
+// products and softmax take turns), fp16 q 840 us (two parts of p, which spill
+// 216 bytes a thread; bf16's kernel 56).  A step of 256 rows x 128 tokens takes
 // about 3.4 us: the MMAs alone about half of it, the softmax about as much.
 //
 // Split.  Many units (row block x head): CTAs take them from a counter.  Few: the
@@ -653,10 +655,11 @@ qg_attn_prompt_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 
             // References: m of the scores, d + m of score + log2 vs.  What is
             // stored of a probability is 2^(score + log2 vs + kr), at most
-            // 2^14.  One f16 part keeps its 11 bits 20 binary orders down, so
+            // 2^14, the largest at least 2^(kBase - 1).  One f16 part keeps its
+            // 11 bits 19 binary orders or more below that, so
             // references may be passed by 8 (at 2 every fourth step went
             // round again, at 8 hardly one after a unit's first); two parts
-            // keep 2^-37 of the largest, and 2 it is.
+            // keep about 2^-35 of the largest, and 2 it is.
             constexpr int kPass = PP == 1 ? 8 : 2, kBase = 14 - kPass;
             float m = kNoRef, l = 0.f, kf = kBase, kr = kBase - kNoRef;
             int d = kNoOrder;

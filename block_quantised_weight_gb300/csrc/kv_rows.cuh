@@ -7,19 +7,22 @@
 //   l = sum p[t],   o = sum p[t] * vs[page] * vcode[t],   out = o / l
 // Codes are exact in f16.  q * 2^j (a power of two that brings the row's
 // largest value to [2^14, 2^15)) and p * vs * 2^k enter the products in f16:
-// 16-bit queries enter as one part, exactly, fp32 ones as two, hi and lo, about
-// 22 bits; probabilities as one part (11 bits) where the output is bf16, else
-// as two.  m is at least the running maximum less 2 and k is chosen by a
-// bound u on s + log2 vs (k = 12 + m - u), so that what reaches o is at most
-// 2^14 and its largest part near that however the scales of the blocks
-// differ.  m and u are whole numbers, which makes every rescaling a power of two,
+// 16-bit queries enter as one part, exactly (to 2^-39 of the row's largest), fp32
+// ones as two, hi and lo, about 22 bits; probabilities as one part (11 bits)
+// where the output is bf16, else as two.  m is at least the running maximum less
+// 2 and k is chosen by a bound u on s + log2 vs (k = 12 + m - u), so that what
+// reaches o is at most 2^14 and its largest part at least 2^10 (u takes the next
+// whole orders of s and of vs) however the scales of the blocks differ: half a
+// step of f16 there, 2^-25, is 2^-35 of the largest.  m and u are whole numbers, which makes every rescaling a power of two,
 // and they move only when a score passes them by more than 2: a step costs one
 // vote instead of a reduction over its tokens.  (Scores from 2^22 on cost the
 // reduction in every step.)
 //
 // Bound.  Decode reads every code once for 4 * group flops a byte: HBM-bound
 // on the stream of codes if few instructions are spent on each (about 23 bytes
-// a clock and SM come in).  Both products are formed transposed, tokens by
+// a clock and SM come in).  Short of that the batch below is bound by latency:
+// twelve warps an SM, by their registers, keep 39 % of the issue slots and 62 %
+// of DRAM busy.  Both products are formed transposed, tokens by
 // heads (K q^T) and dims by heads (V^T p^T), so that the 16-row operand is the
 // codes and the 8 columns are query rows: group sizes up to 8 fill one column
 // tile, and the codes are converted once for all of them.  Each warp streams
@@ -31,9 +34,10 @@
 // 16 dims of four tokens for V, whole vectors each.  p leaves the first
 // product as the transpose of what the second takes; movmatrix turns it.
 //
-// Measured: 48 sequences of up to 4100 tokens, 32 / 8 heads of 128, e4m3: 54.9 us,
-// 5.0 TB/s; 3 of up to 131072, int8: 114 us, 5.5 TB/s; one of 777
-// tokens, 32 / 4 heads of 64: 8.2 us, all of it latency.
+// Measured: 48 sequences of up to 4100 tokens, 32 / 8 heads of 128, e4m3: 55-56 us,
+// 5.0 TB/s (fp32 q 58, fp16 57; heads of 256 dims 57); 3 of up to 131072, int8:
+// 114-121 us, 5.2-5.5 TB/s; one of 777 tokens, 32 / 4 heads of 64: 8.2 us, all of
+// it latency.
 //
 // Split.  The tokens of all (sequence, head, row block) are one line of
 // 128-token tiles, cut evenly among the CTAs whatever the lengths; a CTA that

@@ -149,7 +149,11 @@ def _rows(t, heads, dim, name):
 
 
 class KVWorkspace:
-    """Device workspace of the operators; one serves one stream (calls that may overlap need one each)."""
+    """Device workspace of the operators; one serves one stream (calls that may overlap need one each).
+
+    A call without one (``workspace=None``) allocates and clears its own, 47 MB of memory traffic and a launch
+    more: give every call of a decode loop the same one.
+    """
 
     def __init__(self, device="cuda"):
         self.bytes = int(load()["qgkv_workspace_bytes"]())
@@ -211,6 +215,7 @@ def _batch(table, lens, starts):
 
 
 def _ws(workspace, t):
+    """The workspace of a call; where None is given, a cleared one for this call alone."""
     w = KVWorkspace(t.device) if workspace is None else workspace
     return w, w.ptr, w.bytes
 
@@ -327,7 +332,8 @@ def _mask(drop, batch):
 
 def kv_reserve(cache, table, lens, refs, add=None, workspace=None, stream=None):
     """Give each sequence the pages that lens[b] + add[b] tokens need (add None: one token each);
-    table and refs are updated (qgkv_reserve)."""
+    table and refs are updated (qgkv_reserve).  Raise lens once the tokens are stored, before any
+    fork, compaction or free: pages beyond lens do not count for these."""
     if _other(stream, cache, table, lens, refs, add, workspace):
         with torch.cuda.stream(stream):
             return kv_reserve(cache, table, lens, refs, add, workspace)

@@ -114,9 +114,11 @@ QG_API int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, co
  * A row that sees nothing gives 0 and -inf.  Tokens a row does not see do not
  * reach it, whatever their codes.
  * Numerics: codes enter the tensor cores exactly (f16).  fp32 q enters as the
- * sum of two f16 parts (about 22 bits), 16-bit q exactly.  Probabilities enter
- * as two parts (and no weight probability * scale below 2^-37 of the row's
- * largest), for bf16 q as one (11 bits, below the output's rounding).
+ * sum of two f16 parts (about 22 bits), 16-bit q exactly, both to 2^-39 of the
+ * row's largest.  Weights (probability * scale of V) enter as two f16 parts, 22
+ * bits, for bf16 q as one, 11 bits (below the output's rounding); and to within
+ * 2^-34 of the row's largest weight, for bf16 q in calls of many rows a sequence
+ * 2^-28: smaller ones are lost.
  * All sums are fp32.  Scores may have any size that fp32 holds; a row with one
  * beyond it is NaN.  Repeated calls give the same bits. */
 QG_API int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
@@ -154,7 +156,10 @@ QG_API int qgkv_compact(const qgkv_cache* cache, const int32_t* table, int64_t t
 
 /* Give sequence b the pages that lens[b] + add[b] tokens need beyond those of
  * lens[b] (add null: one token each), the lowest free ones in the order of
- * the sequences; table and refs are updated, lens is left to the caller.  A
+ * the sequences; table and refs are updated, lens is left to the caller, who
+ * raises it once the tokens are stored: until then a second call gives other
+ * pages for the same places, and a fork, compaction or free passes these by; the
+ * pages of before stay held and no table has them.  A
  * sequence for which too few are left gets none (QG_EPAGES). */
 QG_API int qgkv_reserve(int64_t pages, int page_tokens, int32_t* table, int64_t table_width, const int32_t* lens,
                         const int32_t* add, int batch, int32_t* refs, void* workspace, int64_t workspace_bytes,

@@ -380,3 +380,24 @@ def test_tensors_dropped_after_a_call_on_another_stream(kv):  # noqa: F811
     for a, b in zip(outs, want):
         assert np.array_equal(a.cpu().numpy(), b)
     assert len(taken) == 12
+
+
+@pytest.mark.parametrize("rows", [1, 7, 40, 300])
+@pytest.mark.parametrize("fmt, dim, group", [("e4m3", 64, 2), ("int8", 128, 7), ("int8", 96, 4), ("e4m3", 256, 3)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_attention_small_weights_beside_large_ones(kv, ws, rows, fmt, dim, group, dtype):  # noqa: F811
+    """Sharp rows whose largest weights meet codes of zero in half of the dims: what is left there are weights far
+    below the largest, W.
+
+    A part's largest stored weight is 2^10 at least (k = 12, less the next whole order of the score and of the scale;
+    prompts of bf16 queries 2^5), storing it takes half a step of f16, 2^-25, and a rescaling of what is stored two
+    more for each of two parts: below 2^-34 W each (2^-28 W)."""
+    n = 200 + rows
+    cache, table, ln = make(kv, [n], 2, dim, 16, fmt, "hnd", seed=rows + dim)
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    cache.v[torch.rand(cache.v.shape, device="cuda", generator=g) < 0.5] = 0
+    q = torch.randn((rows, 2 * group, dim), device="cuda", generator=g).to(DT[dtype])
+    out, lse = kv.kv_attention(cache, 1, q, table, ln, starts=i32([0, rows]), scale=0.7, return_lse=True, workspace=ws)
+    want, wl, absum, smax, floor = attention_ref(cache, 1, q, table, [n], [0, rows], 0.7)
+    prompt = dtype == "bf16" and dim <= 128 and rows > 100
+    close(out, lse, (want, wl, absum, smax, floor * 2.0 ** (10 if prompt else 4)), n, DT[dtype], one_part=dtype == "bf16")
