@@ -370,6 +370,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 for (unsigned x = taken; lane == 0 && x != issued; ++x)  // the copies in flight, once more
                     (void)mbar_wait_bounded(bar + x % S, (x / S) & 1, a.status);
             }
+            __syncwarp();  // lanes leave the wait one by one; the products below take whole warps
             // scores: rows are tokens g and g + 8 of a subtile, columns the query rows 2t and 2t + 1
             float sc[MT][NS][4];
 #pragma unroll
