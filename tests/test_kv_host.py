@@ -232,3 +232,17 @@ def test_tensors_are_lent_to_the_stream_of_a_call(calls, monkeypatch, name):
     STREAMED[name](qgkv, take)
     assert len(made) == 1 and current == ["main"]
     assert {(t.data_ptr(), "side") for t in given} <= set(lent)
+
+
+def test_row_kernel_joins_its_warp_after_a_wait():
+    """mma and movmatrix take whole warps; lanes leave a bounded wait one by one."""
+    src = open(os.path.join(CSRC, "kv_rows.cuh")).read()
+    at = src.index("if (!mbar_try_wait(bar + taken % S")
+    body = re.sub(r"//[^\n]*", "", src[at:])
+    depth, end = 0, 0
+    for end, ch in enumerate(body):  # the end of the wait's block
+        depth += {"{": 1, "}": -1}.get(ch, 0)
+        if ch == "}" and depth == 0:
+            break
+    assert body[end + 1:].lstrip().startswith("__syncwarp();")
+    assert "mma16816" not in body[:end]
