@@ -112,6 +112,51 @@ int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, const voi
                              batch, st, stream);
 }
 
+int qgkv_append_rotary(const qgkv_cache* cache, int64_t layer, const void* q, const void* k, const void* v, int type,
+                       int64_t rows, int q_heads, int64_t q_row, int64_t q_head, int64_t kv_row, int64_t kv_head,
+                       const float* rope, int64_t positions, int turned, int pairs, void* q_out, const int32_t* table,
+                       int64_t table_width, const int32_t* lens, const int32_t* starts, int batch,
+                       cudaStream_t stream) {
+    int rc = check_cache(cache, layer);
+    if (rc != QG_OK) return rc;
+    if ((rc = check_batch(table, table_width, lens, batch)) != QG_OK) return rc;
+    const int dim = cache->head_dim;
+    if (!rope || positions < 1 || positions > kMost || turned < 16 || turned > dim || turned % 16) return QG_EINVAL;
+    if (pairs != QGKV_INTERLEAVED && pairs != QGKV_HALVES) return QG_EINVAL;
+    if ((rc = check_rows(k, type, rows, cache->heads, dim, kv_row, kv_head)) != QG_OK) return rc;
+    if ((rc = check_rows(v, type, rows, cache->heads, dim, kv_row, kv_head)) != QG_OK) return rc;
+    if (q) {
+        if (q_heads < 1 || q_heads > 65536 || (!q_out && rows)) return QG_EINVAL;
+        if ((rc = check_rows(q, type, rows, q_heads, dim, q_row, q_head)) != QG_OK) return rc;
+    }
+    if (!starts && rows != batch) return QG_EINVAL;
+    if (off4(starts) || off16(rope) || (q && off16(q_out))) return QG_EALIGN;
+    if (rows == 0) return QG_OK;
+    const int64_t size = type_bytes(type), held = cache_bytes(cache);
+    const int64_t kv_in = ((rows - 1) * kv_row + (cache->heads - 1) * kv_head + dim) * size;
+    const int64_t angles = positions * turned * 4, numbers = batch * table_width * 4;
+    const Piece ins[] = {{k, kv_in}, {v, kv_in}, {rope, angles}, {table, numbers}, {lens, batch * int64_t(4)},
+                         {starts, starts ? (batch + 1) * int64_t(4) : 0}};
+    const Piece codes[] = {{cache->k, held}, {cache->v, held}};
+    for (const Piece& c : codes)
+        for (const Piece& in : ins)
+            if (in.p && meets(c.p, c.bytes, in.p, in.bytes)) return QG_EALIAS;
+    if (q) {
+        const int64_t q_in = ((rows - 1) * q_row + (q_heads - 1) * q_head + dim) * size;
+        const Piece out = {q_out, rows * q_heads * dim * size};
+        if (any_meet(&out, 1, ins, 6) || any_meet(&out, 1, codes, 2) || meets(q, q_in, cache->k, held) ||
+            meets(q, q_in, cache->v, held))
+            return QG_EALIAS;
+        const bool itself = q_out == q && (q_head == dim || q_heads == 1) && (q_row == q_heads * int64_t(dim) || rows == 1);
+        if (!itself && meets(q_out, out.bytes, q, q_in)) return QG_EALIAS;
+    }
+    unsigned* st = qg::status_ptr();
+    if (!st) return qg::cuda_fail(cudaGetLastError());
+    return qg::launch_append_rotary(*cache, layer, q, k, v, type, rows, q_heads, q_row, q_head, kv_row, kv_head, rope,
+                                    positions, turned, pairs, q_out, table, table_width, lens, starts, batch, st,
+                                    stream);
+}
+
 int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                    int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
                    int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,
@@ -270,6 +315,50 @@ int qgbeam_select(const void* logits, int type, const float* cum, int requests, 
     if (!qg::status_ptr()) return qg::cuda_fail(cudaGetLastError());
     return qg::launch_beam_select(logits, type, cum, requests, beams, vocab, row_stride, keep, scores, tokens, parents,
                                   static_cast<uint8_t*>(workspace), stream);
+}
+
+int qglogits_adjust(const void* logits, int type, int64_t rows, int64_t vocab, int64_t row_stride, void* out,
+                    int out_type, int64_t out_stride, const int32_t* history, int64_t width, const int32_t* lens,
+                    const int32_t* prompt_lens, const float* repetition, const float* presence, const float* frequency,
+                    const int32_t* bias_tokens, const float* bias, int biases, const float* temperature,
+                    const uint32_t* mask, int64_t mask_words, int masks, const int32_t* mask_rows,
+                    cudaStream_t stream) {
+    const int64_t size = type_bytes(type), out_size = type_bytes(out_type);
+    if (!size || !(out_type == type || out_type == QGKV_F32)) return QG_EINVAL;
+    if (rows < 0 || rows > QGKV_MAX_BATCH * QGKV_MAX_BEAMS || vocab < 1 || vocab >= kMost - 4096) return QG_EINVAL;
+    if (rows && (!logits || !out)) return QG_EINVAL;
+    if (row_stride < vocab || row_stride > kMost || out_stride < vocab || out_stride > kMost) return QG_EINVAL;
+    if (rows == 0) return QG_OK;
+    if (history) {
+        if (!lens || width < 1 || width > QGKV_MAX_HISTORY) return QG_EINVAL;
+    } else if (lens || prompt_lens || repetition || presence || frequency) {
+        return QG_EINVAL;
+    }
+    if (biases < 0 || biases > QGKV_MAX_BIASES || (biases && (!bias_tokens || !bias)) || (!biases && (bias_tokens || bias)))
+        return QG_EINVAL;
+    if (mask) {
+        if (masks < 1 || mask_words < (vocab + 31) / 32 || mask_words > kMost || (!mask_rows && masks < rows)) return QG_EINVAL;
+    } else if (mask_rows) {
+        return QG_EINVAL;
+    }
+    if ((reinterpret_cast<uintptr_t>(logits) & static_cast<uintptr_t>(size - 1)) ||
+        (reinterpret_cast<uintptr_t>(out) & static_cast<uintptr_t>(out_size - 1)) || off4(history) || off4(lens) ||
+        off4(prompt_lens) || off4(repetition) || off4(presence) || off4(frequency) || off4(bias_tokens) || off4(bias) ||
+        off4(temperature) || off4(mask) || off4(mask_rows))
+        return QG_EALIGN;
+    const int64_t words = rows * 4;
+    const Piece ins[] = {{history, rows * width * 4}, {lens, words}, {prompt_lens, words}, {repetition, words},
+                         {presence, words}, {frequency, words}, {bias_tokens, words * biases}, {bias, words * biases},
+                         {temperature, words}, {mask, masks * mask_words * 4}, {mask_rows, words}};
+    const Piece to = {out, ((rows - 1) * out_stride + vocab) * out_size};
+    if (any_meet(&to, 1, ins, 11)) return QG_EALIAS;
+    const bool itself = out == logits && out_type == type && (out_stride == row_stride || rows == 1);
+    if (!itself && meets(out, to.bytes, logits, ((rows - 1) * row_stride + vocab) * size)) return QG_EALIAS;
+    unsigned* st = qg::status_ptr();
+    if (!st) return qg::cuda_fail(cudaGetLastError());
+    return qg::launch_logits_adjust(logits, type, rows, vocab, row_stride, out, out_type, out_stride, history, width,
+                                    lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias, biases,
+                                    temperature, mask, mask_words, masks, mask_rows, st, stream);
 }
 
 }  // extern "C"

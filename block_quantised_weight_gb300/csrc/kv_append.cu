@@ -17,7 +17,7 @@
 // e4m3 21.7 us; int8 by 18 instructions a value (256 threads a CTA: 29.7 us),
 // both by one chain a CTA (lengths, values, maximum, codes) with nothing of
 // its next block on the way.  48 single tokens: 2.4 us.
-#include "kv_common.cuh"
+#include "kv_quant.cuh"
 #include "launch_common.cuh"
 #include "qgkv_launch.h"
 
@@ -37,67 +37,6 @@ struct AppendArgs {
     int64_t rows;
     unsigned* status;
 };
-
-// Code of y = x / scale.
-template <bool INT8>
-__device__ __forceinline__ uint32_t code_of(float y) {
-    if (INT8) {
-        if (!(y == y)) return 0u;
-        return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(y, -127.f), 127.f))) & 0xFFu;
-    }
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(y));
-    return r & 0xFFu;
-}
-
-// Four codes of int8 by division: out of line, the way there is rare.
-__device__ __noinline__ uint32_t codes_by_division(float x0, float x1, float x2, float x3, float scale) {
-    const float x[4] = {x0, x1, x2, x3};
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool finite = fabsf(x[i]) <= 3.4028235e38f;
-        r |= code_of<true>(scale == 0.f ? (finite ? 0.f : x[i]) : __fdiv_rn(x[i], scale)) << (8 * i);
-    }
-    return r;
-}
-
-// Codes of four values.  inv: 1 / scale rounded (for e4m3 a power of two,
-// exact), 0 for a zero block.
-template <bool INT8>
-__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float x2, float x3, float scale, float inv) {
-    if (!INT8) {
-        if (scale == 0.f) inv = 1.f;  // zeros stay zeros, infinities and NaN keep their codes
-        unsigned short lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1 * inv), "f"(x0 * inv));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3 * inv), "f"(x2 * inv));
-        return lo | static_cast<uint32_t>(hi) << 16;
-    }
-    const float x[4] = {x0, x1, x2, x3};
-    uint32_t z[4];
-    bool sure = true;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = x[i] * inv;
-        const float big = y + 12582912.f;  // 1.5 * 2^23: the sum's low bits are y rounded to an integer
-        z[i] = __float_as_uint(big);
-        // further than 2^-15 from a tie; false for NaN and infinities
-        sure &= fabsf(fabsf(y - (big - 12582912.f)) - 0.5f) > 0x1p-15f;
-    }
-    if (!sure) return codes_by_division(x0, x1, x2, x3, scale);
-    return prmt(prmt(z[0], z[1], 0x0040u), prmt(z[2], z[3], 0x0040u), 0x5410u);
-}
-
-template <bool INT8>
-__device__ __forceinline__ float scale_for(float amax) {
-    if (INT8) return __fdiv_rn(amax, 127.f);
-    if (!(amax > 0.f)) return 0.f;
-    // smallest e >= -126 with amax <= 1.75 * 2^(8 + e)
-    const uint32_t u = __float_as_uint(amax);
-    int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    e = max(e, -126);
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
 
 // The running largest magnitude of pairs of 16-bit values; NaN is passed over.
 template <class T>
@@ -265,19 +204,7 @@ __global__ void __launch_bounds__(THREADS) qg_append_kernel(const AppendArgs a) 
         for (int i = tid; i < off * words; i += THREADS) {
             const int tok = i / words;
             uint32_t* p = reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(tok) * c.token_stride) + (i - tok * words);
-            const uint32_t x = *p;
-            uint32_t r = 0;
-            if (INT8) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    r |= code_of<true>(__fmul_rn(static_cast<float>(static_cast<signed char>(x >> (8 * j))), f))
-                         << (8 * j);
-            } else {
-                const f2 lo = h2_to_f2(e4m3x2_f16x2(x & 0xFFFFu)), hi = h2_to_f2(e4m3x2_f16x2(x >> 16));
-                r = code_of<false>(__fmul_rn(lo.x, f)) | code_of<false>(__fmul_rn(lo.y, f)) << 8 |
-                    code_of<false>(__fmul_rn(hi.x, f)) << 16 | code_of<false>(__fmul_rn(hi.y, f)) << 24;
-            }
-            *p = r;
+            *p = rescaled<INT8>(*p, f);
         }
     }
     if (tid == 0) *scale_at = scale;

@@ -33,12 +33,15 @@ QGKV_MAX_BATCH = 4096
 QGKV_MAX_PAGES = 1 << 20
 QGKV_MAX_BEAMS = 64
 QGKV_MAX_KEEP = 128
+QGKV_MAX_HISTORY = (1 << 20) - 1
+QGKV_MAX_BIASES = 2047
 FORMATS = {"e4m3": QGKV_E4M3, "int8": QGKV_INT8}
 ORDERS = {"hnd": QGKV_HND, "nhd": QGKV_NHD}
+PAIRS = {"interleaved": 0, "halves": 1}
 TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 EXPORTS = ("qgkv_workspace_bytes", "qgkv_append", "qgkv_attention", "qgkv_copy_pages", "qgkv_fork", "qgkv_compact",
-           "qgkv_reserve", "qgkv_free", "qgbeam_select")
+           "qgkv_reserve", "qgkv_free", "qgbeam_select", "qgkv_append_rotary", "qglogits_adjust")
 
 
 class QgkvCache(ctypes.Structure):
@@ -67,6 +70,10 @@ def load():
         "qgkv_compact": [vp, vp, i64, vp, ci, vp, vp, vp, vp, vp, vp, vp, i64, vp],
         "qgkv_reserve": [i64, ci, vp, i64, vp, vp, ci, vp, vp, i64, vp],
         "qgkv_free": [i64, ci, vp, i64, vp, vp, ci, vp, vp],
+        "qgkv_append_rotary": [vp, i64, vp, vp, vp, ci, i64, ci, i64, i64, i64, i64, vp, i64, ci, ci, vp, vp, i64, vp, vp,
+                               ci, vp],
+        "qglogits_adjust": [vp, ci, i64, i64, i64, vp, ci, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, ci, vp, vp, i64, ci,
+                            vp, vp],
         "qgbeam_select": [vp, ci, vp, ci, ci, i64, i64, ci, vp, vp, vp, vp, i64, vp],
     }
     got = {}
@@ -235,6 +242,53 @@ def kv_append(cache, layer, k, v, table, lens, starts=None, stream=None):
           _stream(k, v, cache.k, table, lens, starts))
 
 
+def rotary_table(positions, turned, base=10000.0, device="cuda"):
+    """The table that kv_append_rotary takes, float32 [positions, turned]: for each position
+    turned / 2 cosines, then as many sines, of position * base ** (-2 j / turned), angles in 64 bits."""
+    half = turned // 2
+    freq = float(base) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat((torch.cos(angle), torch.sin(angle)), dim=1).float()
+
+
+def kv_append_rotary(cache, layer, q, k, v, rope, table, lens, starts=None, pairs="interleaved", out=None, stream=None):
+    """kv_append of keys turned to their positions, lens[b] + i for row i of sequence b, and the queries
+    of the same rows turned alike (qgkv_append_rotary).  q [rows, q_heads, head_dim] or None, k, v [rows,
+    heads, head_dim]; rope float32 [positions, turned], as rotary_table makes it; pairs "interleaved" or
+    "halves".  Returns the turned queries (`out`, which may be q where q is contiguous), None without q."""
+    if _other(stream, cache, q, k, v, rope, table, lens, starts, out):
+        with torch.cuda.stream(stream):
+            return kv_append_rotary(cache, layer, q, k, v, rope, table, lens, starts, pairs, out)
+    if pairs not in PAIRS:
+        raise ValueError(f"pairs must be one of {sorted(PAIRS)}, got {pairs!r}")
+    batch, width, tp, lp, sp = _batch(table, lens, starts)
+    kp, kind, rows, row, head = _rows(k, cache.heads, cache.head_dim, "k")
+    vp, kind_v, rows_v, row_v, head_v = _rows(v, cache.heads, cache.head_dim, "v")
+    if (kind, rows, row, head) != (kind_v, rows_v, row_v, head_v):
+        raise ValueError("k and v must have the same type, shape and strides")
+    rp = _need(rope, torch.float32, "rope", (None, None))
+    qp = op = None
+    q_heads = q_row = q_head = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [rows, q_heads, head_dim]")
+        q_heads = q.shape[1]
+        qp, kind_q, rows_q, q_row, q_head = _rows(q, q_heads, cache.head_dim, "q")
+        if (kind_q, rows_q) != (kind, rows):
+            raise ValueError("q must have the type and the rows of k and v")
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            op = out.data_ptr()
+        else:
+            op = _need(out, q.dtype, "out", (rows, q_heads, cache.head_dim))
+    elif out is not None:
+        raise ValueError("out is for the turned queries, there is no q")
+    _call("qgkv_append_rotary", cache.ref, layer, qp, kp, vp, kind, rows, q_heads, q_row, q_head, row, head, rp,
+          rope.shape[0], rope.shape[1], PAIRS[pairs], op, tp, width, lp, sp, batch,
+          _stream(q, k, v, cache.k, rope, out, table, lens, starts))
+    return out
+
+
 def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None, lse=None, return_lse=False,
                  workspace=None, stream=None):
     """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
@@ -383,3 +437,66 @@ def beam_select(logits, cum, keep, workspace=None, stream=None):
           logits.stride(0) if rows > 1 else vocab, keep, scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), wp,
           wb, _stream(logits, cum, w.buffer))
     return scores, tokens, parents
+
+
+def adjust_logits(logits, history=None, lens=None, prompt_lens=None, repetition=None, presence=None, frequency=None,
+                  bias_tokens=None, bias=None, temperature=None, mask=None, mask_rows=None, out=None, stream=None):
+    """Penalties for tokens that have come before, listed biases, temperature and a grammar's mask, in
+    this order (qglogits_adjust).  logits [rows, vocab]; history int32 [rows, width] of which lens int32
+    [rows] tokens count, the first prompt_lens of them given and not produced; repetition, presence,
+    frequency, temperature float32 [rows]; bias_tokens int32 and bias float32 [rows, biases], places
+    without one -1; mask int32 [masks, words], bit t % 32 of word t // 32 is 1 where token t is allowed, one
+    a row or named by mask_rows int32 [rows] (-1: none).  Returns `out` (of the logits' type or float32;
+    logits itself works in place), a new tensor of the logits' type where None."""
+    if _other(stream, logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias, temperature,
+              mask, mask_rows, out):
+        with torch.cuda.stream(stream):
+            return adjust_logits(logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias,
+                                 temperature, mask, mask_rows, out)
+    kind, rows, vocab, row = _logits(logits, "logits")
+    if out is None:
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    out_kind, out_rows, out_vocab, out_row = (kind, rows, vocab, row) if out is logits else _logits(out, "out")
+    if (out_rows, out_vocab) != (rows, vocab):
+        raise ValueError(f"out has shape {tuple(out.shape)}, not {(rows, vocab)}")
+
+    def each(t, name, dtype=torch.float32):
+        return None if t is None else _need(t, dtype, name, (rows,))
+
+    i32 = torch.int32
+    hp = width = tp = bp = mp = None
+    past = [each(lens, "lens", i32), each(prompt_lens, "prompt_lens", i32), each(repetition, "repetition"),
+            each(presence, "presence"), each(frequency, "frequency")]
+    if history is not None:
+        hp, width = _need(history, i32, "history", (rows, None)), history.shape[1]
+        if width == 0:  # nothing has come yet
+            hp, past = None, [None] * 5
+    biases = 0
+    if bias_tokens is not None and bias is not None:
+        tp, biases = _need(bias_tokens, i32, "bias_tokens", (rows, None)), bias_tokens.shape[1]
+        bp = _need(bias, torch.float32, "bias", (rows, biases))
+        if biases == 0:
+            tp = bp = None
+    elif bias_tokens is not None or bias is not None:
+        raise ValueError("bias_tokens and bias belong together")
+    masks = words = 0
+    if mask is not None:
+        mp, (masks, words) = _need(mask, i32, "mask", (None, None)), mask.shape
+    _call("qglogits_adjust", logits.data_ptr(), kind, rows, vocab, row, out.data_ptr(), out_kind, out_row, hp, width or 0,
+          *past, tp, bp, biases, each(temperature, "temperature"), mp, words, masks, each(mask_rows, "mask_rows", i32),
+          _stream(logits, out, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias,
+                  temperature, mask, mask_rows))
+    return out
+
+
+def _logits(t, name):
+    """(type, rows, vocab, row stride) of a [rows, vocab] tensor with dense rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise TypeError(f"{name} must be a CUDA tensor [rows, vocab]")
+    kind = TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"a row of {name} must be dense")
+    return kind, rows, vocab, t.stride(0) if rows > 1 else vocab

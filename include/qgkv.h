@@ -62,10 +62,16 @@ extern "C" {
 #define QGKV_F16 1
 #define QGKV_BF16 2
 
+/* Pairs of values that a rotation turns into one another. */
+#define QGKV_INTERLEAVED 0 /* (0, 1), (2, 3), ... */
+#define QGKV_HALVES 1      /* (0, R/2), (1, R/2 + 1), ... */
+
 #define QGKV_MAX_BATCH 4096       /* sequences of one call */
 #define QGKV_MAX_PAGES (1 << 20)  /* pages of one cache */
 #define QGKV_MAX_BEAMS 64         /* beams of one request */
 #define QGKV_MAX_KEEP 128         /* continuations selected per request */
+#define QGKV_MAX_HISTORY ((1 << 20) - 1) /* tokens of a row's history */
+#define QGKV_MAX_BIASES 2047      /* biases listed for a row */
 
 typedef struct qgkv_cache {
     uint8_t* k;
@@ -101,6 +107,25 @@ QG_API int64_t qgkv_workspace_bytes(void);
 QG_API int qgkv_append(const qgkv_cache* cache, int64_t layer, const void* k, const void* v, int type, int64_t rows,
                        int64_t row_stride, int64_t head_stride, const int32_t* table, int64_t table_width,
                        const int32_t* lens, const int32_t* starts, int batch, cudaStream_t stream);
+
+/* qgkv_append of keys that are first turned to their positions, with the
+ * queries of the same tokens.  Row i of sequence b has position p = lens[b] + i;
+ * rope, fp32 [positions][turned], holds for each position turned / 2 cosines and
+ * then as many sines.  Pair j (a, b) of a head's first `turned` values (a multiple
+ * of 16 up to head_dim; `pairs` says which values are a pair) becomes
+ *   fl32(fl32(a c) - fl32(b s)),  fl32(fl32(a s) + fl32(b c)),
+ * c = rope[p][j], s = rope[p][turned / 2 + j]; the other values stay.  The turned
+ * keys are quantised as they are, without a rounding to `type`.  k, v: as for
+ * qgkv_append.  q: rows of [q_heads][head_dim] values, q_row and q_head elements
+ * apart (multiples of 16 bytes), or null; q_out: [rows][q_heads][head_dim] of the
+ * same type, dense, 16-byte aligned; it may be q where q is dense.  Rows that no
+ * sequence has are left as they are.  Where p is outside the table (QG_EBOUNDS)
+ * the token is not stored and its turned queries are NaN. */
+QG_API int qgkv_append_rotary(const qgkv_cache* cache, int64_t layer, const void* q, const void* k, const void* v,
+                              int type, int64_t rows, int q_heads, int64_t q_row, int64_t q_head, int64_t kv_row,
+                              int64_t kv_head, const float* rope, int64_t positions, int turned, int pairs,
+                              void* q_out, const int32_t* table, int64_t table_width, const int32_t* lens,
+                              const int32_t* starts, int batch, cudaStream_t stream);
 
 /* Attention of `rows` query rows over the cache.  Sequence b holds lens[b]
  * tokens, its own rows' tokens included; row i of its n rows sees the first
@@ -182,6 +207,33 @@ QG_API int qgkv_free(int64_t pages, int page_tokens, int32_t* table, int64_t tab
 QG_API int qgbeam_select(const void* logits, int type, const float* cum, int requests, int beams, int64_t vocab,
                          int64_t row_stride, int keep, float* scores, int32_t* tokens, int32_t* parents,
                          void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* Adjust `rows` rows of `vocab` logits (row_stride elements apart) before a
+ * selection.  For token t of row r, with its logit x in fp32 and every operation
+ * rounded to fp32, in this order and each where its argument is not null:
+ *   history   int32 [rows][width], the row's first lens[r] tokens, of which the
+ *             first prompt_lens[r] (null: none) were given and the others
+ *             produced:
+ *     x = x > 0 ? x / repetition[r] : x * repetition[r]  if t is in it;
+ *     x = x - frequency[r] * n;  x = x - presence[r]     if t was produced n > 0 times;
+ *   bias      x = x + bias[r][i] for the last i with bias_tokens[r][i] = t
+ *             (int32 and fp32 [rows][biases]);
+ *   temperature  x = x / temperature[r];
+ *   mask      x = -inf if bit t % 32 of word t / 32 of the row's mask is 0.  mask:
+ *             `masks` rows of `mask_words` words, at least ceil(vocab / 32);
+ *             mask_rows, int32 [rows], names the mask of each row, -1 for none
+ *             (null: row r has mask r, and masks is at least rows).
+ * Tokens outside [0, vocab) in history and bias_tokens are passed over.  out: of
+ * `type` or fp32, rows out_stride elements apart; it may be `logits` itself (of
+ * the same type and stride), and then, without a temperature, only the logits that
+ * change are touched.  A length outside [0, width] is cut to it, and a mask
+ * number outside [-1, masks) counts as -1 (QG_EBOUNDS). */
+QG_API int qglogits_adjust(const void* logits, int type, int64_t rows, int64_t vocab, int64_t row_stride, void* out,
+                           int out_type, int64_t out_stride, const int32_t* history, int64_t width,
+                           const int32_t* lens, const int32_t* prompt_lens, const float* repetition,
+                           const float* presence, const float* frequency, const int32_t* bias_tokens,
+                           const float* bias, int biases, const float* temperature, const uint32_t* mask,
+                           int64_t mask_words, int masks, const int32_t* mask_rows, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
