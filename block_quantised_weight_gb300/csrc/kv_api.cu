@@ -84,6 +84,74 @@ int64_t cache_bytes(const qgkv_cache* c) {
            static_cast<int64_t>(c->heads) * c->page_tokens * c->head_dim;
 }
 
+// The checks of both attentions; fills `a`.  *done: there is nothing to launch.
+int prepare_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
+                      int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
+                      int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,
+                      void* workspace, int64_t workspace_bytes, Piece plan, qg::AttnArgs& a, bool* done) {
+    *done = true;
+    int rc = check_cache(cache, layer);
+    if (rc != QG_OK) return rc;
+    if ((rc = check_batch(table, table_width, lens, batch)) != QG_OK) return rc;
+    if (q_heads < 1 || q_heads % cache->heads || q_heads > 65536) return QG_EINVAL;
+    if ((!out && rows) || !(scale > -3.0e38f && scale < 3.0e38f)) return QG_EINVAL;
+    if ((rc = check_rows(q, type, rows, q_heads, cache->head_dim, row_stride, head_stride)) != QG_OK) return rc;
+    if (!starts && rows != batch) return QG_EINVAL;
+    // the kernels count the query rows of a cache head (tokens x heads of a group) in 32 bits
+    if (rows * (q_heads / cache->heads) > kMost - 512) return QG_EINVAL;
+    if (off16(out) || off4(lse) || off4(starts)) return QG_EALIGN;
+    if ((rc = check_workspace(workspace, workspace_bytes)) != QG_OK) return rc;
+    if (rows == 0) return QG_OK;
+    const int64_t size = type_bytes(type);
+    const int64_t in = ((rows - 1) * row_stride + (q_heads - 1) * head_stride + cache->head_dim) * size;
+    const int64_t written = rows * q_heads * cache->head_dim * size, held = cache_bytes(cache);
+    if (meets(out, written, q, in) || meets(out, written, cache->k, held) || meets(out, written, cache->v, held) ||
+        (lse && (meets(lse, rows * q_heads * 4, out, written) || meets(lse, rows * q_heads * 4, q, in))))
+        return QG_EALIAS;
+    if (plan.p && (meets(out, written, plan.p, plan.bytes) || (lse && meets(lse, rows * q_heads * 4, plan.p, plan.bytes))))
+        return QG_EALIAS;
+    unsigned* st = qg::status_ptr();
+    if (!st) return qg::cuda_fail(cudaGetLastError());
+    a = {};
+    a.c = qg::layer_of(*cache, layer);
+    a.q = q, a.out = out, a.lse = lse, a.q_row = row_stride, a.q_head = head_stride, a.type = type;
+    a.q_heads = q_heads, a.group = q_heads / cache->heads;
+    a.table = table, a.width = table_width, a.lens = lens, a.starts = starts, a.batch = batch, a.rows = rows;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.part = reinterpret_cast<float*>(ws + qg::kWsPart);
+    a.splits = reinterpret_cast<int4*>(ws + qg::kWsSplits);
+    a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
+    a.status = st;
+    *done = false;
+    return QG_OK;
+}
+
+int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
+    // The tcgen05 kernel takes as long for one query row (token x head of a
+    // group) a sequence as for 256, the row kernel's time grows with them.  Row
+    // kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128, by query rows a
+    // sequence (the same for each of a call):
+    //   16 sequences of up to 4100 tokens: bf16 96 rows 128 / 113, 128 rows 161 /
+    //   113, 256 rows 297 / 121; fp32 64 rows 111 / 141, 128 rows 198 / 144, 256
+    //   rows 368 / 255; f16 (two parts of p for two tiles) 128 rows 175 / 177, 256
+    //   rows 326 / 187
+    //   48 of up to 1000: bf16 64 rows 122 / 98, 128 rows 223 / 101; f16 128 rows
+    //   238 / 166
+    //   few row blocks, whose keys are split, bf16: 4 of up to 4100: 128 rows 56 /
+    //   56, 256 rows 92 / 59; one of 1000: 128 rows 18 / 30, 256 rows 27 / 31; of
+    //   8000: 128 rows 40 / 60, 256 rows 59 / 61; of 30000: 128 rows 93 / 90, 256
+    //   rows 161 / 95
+    // The border is late for f16 batches and for few but long sequences, by up to
+    // 1.4 times.  The mean over a call decides for all of it: a prompt among many
+    // single tokens goes the way of the single tokens, or they its.
+    const int sms = qg::sm_count(qg::current_device());
+    const int few = a.type == QGKV_F16 || 2 * static_cast<int64_t>(a.batch) * a.c.heads < sms ? 256 : 128;
+    const bool many = a.rows * a.group >= static_cast<int64_t>(few) * a.batch && a.starts && a.c.dim <= 128;
+    if (many) return qg::launch_attn_prompt(a, int8, stream);
+    return qg::launch_attn_rows(a, int8, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -161,59 +229,55 @@ int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q, void* 
                    int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
                    int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,
                    void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
-    int rc = check_cache(cache, layer);
+    qg::AttnArgs a;
+    bool done;
+    const int rc = prepare_attention(cache, layer, q, out, lse, type, rows, q_heads, row_stride, head_stride, table,
+                                     table_width, lens, starts, batch, scale, workspace, workspace_bytes, {nullptr, 0},
+                                     a, &done);
+    return rc != QG_OK || done ? rc : launch_attention(a, cache->format == QGKV_INT8, stream);
+}
+
+int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int64_t table_width, const int32_t* lens,
+               const int32_t* starts, int64_t rows, int batch, const int32_t* groups, int ngroups, int32_t* plan,
+               cudaStream_t stream) {
+    const int rc = check_batch(table, table_width, lens, batch);
     if (rc != QG_OK) return rc;
-    if ((rc = check_batch(table, table_width, lens, batch)) != QG_OK) return rc;
-    if (q_heads < 1 || q_heads % cache->heads || q_heads > 65536) return QG_EINVAL;
-    if ((!out && rows) || !(scale > -3.0e38f && scale < 3.0e38f)) return QG_EINVAL;
-    if ((rc = check_rows(q, type, rows, q_heads, cache->head_dim, row_stride, head_stride)) != QG_OK) return rc;
-    if (!starts && rows != batch) return QG_EINVAL;
-    // the kernels count the query rows of a cache head (tokens x heads of a group) in 32 bits
-    if (rows * (q_heads / cache->heads) > kMost - 512) return QG_EINVAL;
-    if (off16(out) || off4(lse) || off4(starts)) return QG_EALIGN;
-    if ((rc = check_workspace(workspace, workspace_bytes)) != QG_OK) return rc;
-    if (rows == 0) return QG_OK;
-    const int64_t size = type_bytes(type);
-    const int64_t in = ((rows - 1) * row_stride + (q_heads - 1) * head_stride + cache->head_dim) * size;
-    const int64_t written = rows * q_heads * cache->head_dim * size, held = cache_bytes(cache);
-    if (meets(out, written, q, in) || meets(out, written, cache->k, held) || meets(out, written, cache->v, held) ||
-        (lse && (meets(lse, rows * q_heads * 4, out, written) || meets(lse, rows * q_heads * 4, q, in))))
-        return QG_EALIAS;
+    if (pages < 1 || pages > QGKV_MAX_PAGES || !page_size_ok(page_tokens) || rows < 0 || rows > kMost) return QG_EINVAL;
+    if (!groups || ngroups < 1 || ngroups > QGKV_MAX_BATCH || !plan || (!starts && rows != batch)) return QG_EINVAL;
+    if (table_width * page_tokens > kMost - page_tokens) return QG_EINVAL;  // tokens are counted in 32 bits
+    if (off4(starts) || off4(groups) || off16(plan)) return QG_EALIGN;
+    const Piece ins[] = {{table, batch * table_width * 4}, {lens, batch * 4}, {starts, (batch + 1) * 4},
+                         {groups, (ngroups + 1) * 4}};
+    const Piece to = {plan, (4 * ngroups + batch) * 4};
+    if (any_meet(&to, 1, ins, 4)) return QG_EALIAS;
     unsigned* st = qg::status_ptr();
     if (!st) return qg::cuda_fail(cudaGetLastError());
-    qg::AttnArgs a = {};
-    a.c = qg::layer_of(*cache, layer);
-    a.q = q, a.out = out, a.lse = lse, a.q_row = row_stride, a.q_head = head_stride, a.type = type;
-    a.q_heads = q_heads, a.group = q_heads / cache->heads;
-    a.table = table, a.width = table_width, a.lens = lens, a.starts = starts, a.batch = batch, a.rows = rows;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.part = reinterpret_cast<float*>(ws + qg::kWsPart);
-    a.splits = reinterpret_cast<int4*>(ws + qg::kWsSplits);
-    a.count = reinterpret_cast<unsigned*>(ws + qg::kWsCounters) + qg::kCntAttn;
-    a.status = st;
-    // The tcgen05 kernel takes as long for one query row (token x head of a
-    // group) a sequence as for 256, the row kernel's time grows with them.  Row
-    // kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128, by query rows a
-    // sequence (the same for each of a call):
-    //   16 sequences of up to 4100 tokens: bf16 96 rows 128 / 113, 128 rows 161 /
-    //   113, 256 rows 297 / 121; fp32 64 rows 111 / 141, 128 rows 198 / 144, 256
-    //   rows 368 / 255; f16 (two parts of p for two tiles) 128 rows 175 / 177, 256
-    //   rows 326 / 187
-    //   48 of up to 1000: bf16 64 rows 122 / 98, 128 rows 223 / 101; f16 128 rows
-    //   238 / 166
-    //   few row blocks, whose keys are split, bf16: 4 of up to 4100: 128 rows 56 /
-    //   56, 256 rows 92 / 59; one of 1000: 128 rows 18 / 30, 256 rows 27 / 31; of
-    //   8000: 128 rows 40 / 60, 256 rows 59 / 61; of 30000: 128 rows 93 / 90, 256
-    //   rows 161 / 95
-    // The border is late for f16 batches and for few but long sequences, by up to
-    // 1.4 times.  The mean over a call decides for all of it: a prompt among many
-    // single tokens goes the way of the single tokens, or they its.
-    const int sms = qg::sm_count(qg::current_device());
-    const int few = type == QGKV_F16 || 2 * static_cast<int64_t>(batch) * cache->heads < sms ? 256 : 128;
-    const bool many = rows * a.group >= static_cast<int64_t>(few) * batch && starts && cache->head_dim <= 128;
-    if (many) return qg::launch_attn_prompt(a, cache->format == QGKV_INT8, stream);
-    return qg::launch_attn_rows(a, cache->format == QGKV_INT8, stream);
+    return qg::launch_share(pages, page_tokens, table, table_width, lens, starts, rows, batch, groups, ngroups, plan, st,
+                            stream);
+}
+
+int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
+                          int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride, const int32_t* table,
+                          int64_t table_width, const int32_t* lens, const int32_t* starts, int batch,
+                          const int32_t* plan, int ngroups, float scale, void* workspace, int64_t workspace_bytes,
+                          cudaStream_t stream) {
+    if (!plan || ngroups < 1 || ngroups > QGKV_MAX_BATCH) return QG_EINVAL;
+    if (off16(plan)) return QG_EALIGN;
+    qg::AttnArgs a;
+    bool done;
+    const int rc = prepare_attention(cache, layer, q, out, lse, type, rows, q_heads, row_stride, head_stride, table,
+                                     table_width, lens, starts, batch, scale, workspace, workspace_bytes,
+                                     {plan, (4 * int64_t(ngroups) + batch) * 4}, a, &done);
+    if (rc != QG_OK || done) return rc;
+    const int64_t values = rows * q_heads * cache->head_dim;
+    const int64_t kept = qg::shared_bytes(rows, q_heads, cache->head_dim);
+    if (2 * kept > qg::kWsSplits - qg::kWsOwn) return launch_attention(a, cache->format == QGKV_INT8, stream);
+    a.groups = reinterpret_cast<const int4*>(plan);
+    a.skip = plan + 4 * int64_t(ngroups);
+    a.sequences = batch;
+    a.own = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + qg::kWsOwn);
+    a.own_ml = reinterpret_cast<float2*>(a.own + values);
+    return qg::launch_attn_shared(a, ngroups, cache->format == QGKV_INT8, stream);
 }
 
 int qgkv_copy_pages(const qgkv_cache* cache, const int32_t* src, const int32_t* dst, const int32_t* count,

@@ -22,6 +22,14 @@ struct AttnArgs {
     int4* splits;
     unsigned* count;
     unsigned* status;
+    // A shared prefix (launch_attn_shared): the plan's groups and tokens, the
+    // results of the prefix and of what is behind it, and which of the two this is.
+    const int4* groups;
+    const int32_t* skip;
+    float* own;      // [rows][q_heads][dim], normalised
+    float2* own_ml;  // [rows][q_heads] reference and sum
+    bool prefix;     // batch counts groups
+    int sequences;   // of the call
 };
 
 // Number of rows and length of sequence b.  A length beyond the table is cut
@@ -45,6 +53,48 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
         s.len = s.len < 0 ? 0 : static_cast<int>(most);
     }
     return s;
+}
+
+// What a sequence reads behind a shared prefix, or the prefix itself for all rows of
+// its group: rows from row0 on, tokens from page column `col` of a table row on.
+// An entry of the plan that does not fit the call counts as nothing shared
+// (kStatusBounds).
+struct SharedSeq {
+    Seq s;
+    int64_t row0;
+    int table_row, col;
+    bool partial;
+};
+__device__ __forceinline__ SharedSeq shared_sequence(const AttnArgs& a, int b) {
+    SharedSeq r = {};
+    if (a.prefix) {
+        const int4 g = a.groups[b];  // first row, rows, tokens, first sequence
+        const int64_t most = a.width << a.c.log2p;
+        bool good = g.x >= 0 && g.y >= 0 && static_cast<int64_t>(g.x) + g.y <= a.rows && g.z >= 0 && g.z <= most &&
+                    (g.z & ((1 << a.c.log2p) - 1)) == 0 && (g.z == 0 || (g.w >= 0 && g.w < a.sequences));
+        if (!good) atomicOr(a.status, kStatusBounds);
+        if (good && g.z > 0) {
+            r.s = {g.y, g.z};
+            r.row0 = g.x;
+            r.table_row = g.w;
+        }
+        r.partial = true;
+        return r;
+    }
+    r.s = sequence(a, b);
+    r.row0 = a.starts ? a.starts[b] : b;
+    r.table_row = b;
+    const int skip = a.skip[b];
+    if (skip != 0 && r.s.n > 0) {
+        if (skip < 0 || skip > r.s.len - r.s.n + 1 || (skip & ((1 << a.c.log2p) - 1))) {
+            atomicOr(a.status, kStatusBounds);
+        } else {
+            r.s.len -= skip;
+            r.col = skip >> a.c.log2p;
+            r.partial = true;
+        }
+    }
+    return r;
 }
 
 // a / b for non-negative a and positive b, in 32 bits where they fit.
@@ -126,6 +176,11 @@ __device__ __forceinline__ float4 q4_values(uint4 v, int type) {
 }
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s);
+// Bytes of a result kept for a join: rows x q_heads of dim values, reference and sum.
+inline int64_t shared_bytes(int64_t rows, int q_heads, int dim) {
+    return ((rows * q_heads * (dim * int64_t(4) + 8)) + 255) / 256 * 256;
+}
+int launch_attn_shared(const AttnArgs& a, int groups, bool int8, cudaStream_t s);
 // K or V of one layer as [pages][heads][page_tokens][dim], boxes of box_tokens x box_bytes; `swizzle`: 64- or
 // 128-byte rows, so that reads down a column of a box meet no bank twice.  Bytes past the dims arrive as 0.
 bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens, bool swizzle);

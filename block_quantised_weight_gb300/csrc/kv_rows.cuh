@@ -61,6 +61,7 @@ constexpr int kMaxCtas = 640;     // partial slots: 2 per CTA
 constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its references and sums
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
+static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsOwn - kWsPart, "partials meet the results kept for a join");
 
 constexpr int kMostK = 124;  // of k: p * 2^k stays finite, p being 4 at most
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
@@ -87,8 +88,9 @@ struct Shape {
     static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
 };
 
-// QP, PP: f16 parts of q and of p.
-template <int DC, int MT, int QP, int PP, bool INT8, int MINB>
+// QP, PP: f16 parts of q and of p.  SHARED: a prefix or what is behind it
+// (shared_sequence), whose results are kept for a join.
+template <int DC, int MT, int QP, int PP, bool INT8, int MINB, bool SHARED>
 __global__ void __launch_bounds__(kThreads, MINB)
 qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     int grid) {
@@ -130,7 +132,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             const int b = b0 + tid;
             int64_t x = 0;
             if (b < a.batch) {
-                const Seq s = sequence(a, b);
+                const Seq s = SHARED ? shared_sequence(a, b).s : sequence(a, b);
                 const int64_t blocks = (static_cast<int64_t>(s.n) * a.group + RU - 1) / RU;
                 x = blocks * c.heads * max(1, (s.len + kTile - 1) / kTile);
                 seqs[b] = make_int2(s.n, s.len);
@@ -166,7 +168,16 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         // empty sequences share their successor's prefix: take the last with pre <= u that has tiles
         const int b = lo;
         const Seq sq = {seqs[b].x, seqs[b].y};
-        const int64_t row0 = a.starts ? a.starts[b] : b;
+        int64_t row0 = a.starts ? a.starts[b] : b;
+        const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
+        bool causal = true, partial = false;  // partial: the result is kept for a join
+        if (SHARED) {
+            const SharedSeq sh = shared_sequence(a, b);
+            row0 = sh.row0, partial = sh.partial, causal = !a.prefix;
+            row_table = a.table + sh.table_row * a.width + sh.col;
+        }
+        // tokens that row i of the sequence sees
+        auto sees = [&](int i) { return !SHARED || causal ? sq.len - sq.n + i + 1 : sq.len; };
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];
@@ -179,8 +190,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         const int row_first = rb * RU;
         // tokens that the block's last row sees
         const int i_last = min(row_first + RU, nrows) - 1;
-        const int seen_most = sq.len - sq.n + i_last / a.group + 1;
-        const int seen_least = sq.len - sq.n + row_first / a.group + 1;
+        const int seen_most = sees(i_last / a.group);
+        const int seen_least = sees(row_first / a.group);
         const int tok0 = tile0 * kTile;
         const int tok1 = min((tile0 + seg) * kTile, seen_most);
         const int full_end = min(seen_least, tok1);  // up to here every row sees every token
@@ -192,7 +203,6 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         constexpr int step_tok = 64 * NS;
         const int warp_tok = tok0 + warp * 16 * NS;
         const int steps = tok1 > warp_tok ? (tok1 - warp_tok + step_tok - 1) / step_tok : 0;
-        const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
         int id_c[2];
         float ks_c[2], vs_c[2];
         auto refill = [&](int batch32) {
@@ -265,7 +275,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         if (tid < RU) {
             const int r = row_first + tid, i_row = r / a.group;
             orow[tid] = r < nrows ? (row0 + i_row) * a.q_heads + h * a.group + r - i_row * a.group : -1;
-            limits[tid] = r < nrows ? sq.len - sq.n + i_row + 1 : 0;
+            limits[tid] = r < nrows ? sees(i_row) : 0;
         }
         float4 x[MT][DC];
 #pragma unroll
@@ -678,11 +688,13 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     acc.x += w[i] * v.x, acc.y += w[i] * v.y, acc.z += w[i] * v.z, acc.w += w[i] * v.w;
                 }
                 acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-                if (whole) store_out4(a.out, a.type, to * c.dim + d, acc);
+                if (SHARED && whole && partial) store_out4(a.own, QGKV_F32, to * c.dim + d, acc);
+                else if (whole) store_out4(a.out, a.type, to * c.dim + d, acc);
                 else *reinterpret_cast<float4*>(part + r * c.dim + d) = acc;
             }
             if (row_lane == 0) {
                 if (!whole) part[2048 + r] = mx, part[2048 + 16 + r] = sum;
+                else if (SHARED && partial) a.own_ml[to] = make_float2(mx, sum);
                 else if (a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
             }
         }
@@ -768,10 +780,13 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                     for (int x2 = 0; x2 < XV; ++x2) {
                         const int d = 4 * (row_lane + 32 * x2);
                         if (live && d < c.dim)
-                            store_out4(a.out, a.type, to[i] * c.dim + d,
+                            store_out4(SHARED && partial ? a.own : a.out, SHARED && partial ? QGKV_F32 : a.type,
+                                       to[i] * c.dim + d,
                                        make_float4(acc[x2].x * inv, acc[x2].y * inv, acc[x2].z * inv, acc[x2].w * inv));
                     }
-                    if (live && row_lane == 0 && a.lse)
+                    if (SHARED && partial) {
+                        if (live && row_lane == 0) a.own_ml[to[i]] = make_float2(mx, sum);
+                    } else if (live && row_lane == 0 && a.lse)
                         a.lse[to[i]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
                 }
             }
@@ -780,7 +795,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     }
 }
 
-template <int DC, int MT, int QP, int PP, bool INT8, int MINB>
+template <int DC, int MT, int QP, int PP, bool INT8, int MINB, bool SHARED>
 int launch_one(const AttnArgs& a, cudaStream_t s) {
     const int dev = current_device();
     const int sms = sm_count(dev);
@@ -793,7 +808,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
         return cuda_fail(cudaGetLastError());
     const int most = fixed + (QGKV_MAX_BATCH + 1) * 16;
     static std::atomic<bool> done[64];
-    auto kern = qg_attn_rows_kernel<DC, MT, QP, PP, INT8, MINB>;
+    auto kern = qg_attn_rows_kernel<DC, MT, QP, PP, INT8, MINB, SHARED>;
     if (!done[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
             return cuda_fail(cudaGetLastError());
@@ -804,7 +819,7 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
     return launch_status();
 }
 
-template <int QP, int PP, bool INT8>
+template <int QP, int PP, bool INT8, bool SHARED>
 int launch_typed(const AttnArgs& a, cudaStream_t s) {
     // 16 rows a unit read the codes half as often as 8 do, with more registers
     // and so fewer CTAs; what they gain grows with what a code costs and with the
@@ -818,20 +833,20 @@ int launch_typed(const AttnArgs& a, cudaStream_t s) {
     // for 61; e4m3's batch 58 us for 56 with two).
     const int few = INT8 ? 16 : a.c.dim <= 64 ? 24 : 48;
     const bool wide = a.rows * a.group > few * static_cast<int64_t>(a.batch);
-    if (a.c.dim <= 64) return wide ? launch_one<1, 2, QP, PP, INT8, 3>(a, s) : launch_one<1, 1, QP, PP, INT8, 3>(a, s);
+    if (a.c.dim <= 64) return wide ? launch_one<1, 2, QP, PP, INT8, 3, SHARED>(a, s) : launch_one<1, 1, QP, PP, INT8, 3, SHARED>(a, s);
     if (a.c.dim <= 128)
-        return wide ? launch_one<2, 2, QP, PP, INT8, 2>(a, s) : launch_one<2, 1, QP, PP, INT8, INT8 ? 2 : 3>(a, s);
-    return launch_one<4, 1, QP, PP, INT8, 2>(a, s);
+        return wide ? launch_one<2, 2, QP, PP, INT8, 2, SHARED>(a, s) : launch_one<2, 1, QP, PP, INT8, INT8 ? 2 : 3, SHARED>(a, s);
+    return launch_one<4, 1, QP, PP, INT8, 2, SHARED>(a, s);
 }
 
 }  // namespace
 
-template <bool INT8>
+template <bool INT8, bool SHARED>
 int launch_rows(const AttnArgs& a, cudaStream_t s) {
-    if (a.type == QGKV_F32) return launch_typed<2, 2, INT8>(a, s);
+    if (a.type == QGKV_F32) return launch_typed<2, 2, INT8, SHARED>(a, s);
     // f16 outputs round as finely as one f16 part of p would: two
-    if (a.type == QGKV_F16) return launch_typed<1, 2, INT8>(a, s);
-    return launch_typed<1, 1, INT8>(a, s);
+    if (a.type == QGKV_F16) return launch_typed<1, 2, INT8, SHARED>(a, s);
+    return launch_typed<1, 1, INT8, SHARED>(a, s);
 }
 
 }  // namespace qg

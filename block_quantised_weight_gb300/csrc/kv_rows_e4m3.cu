@@ -3,8 +3,8 @@
 
 namespace qg {
 
-template int launch_rows<false>(const AttnArgs&, cudaStream_t);
-extern template int launch_rows<true>(const AttnArgs&, cudaStream_t);
+template int launch_rows<false, false>(const AttnArgs&, cudaStream_t);
+extern template int launch_rows<true, false>(const AttnArgs&, cudaStream_t);
 
 bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens,
                   bool swizzle) {
@@ -23,7 +23,7 @@ bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int b
 }
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s) {
-    return int8 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
+    return int8 ? launch_rows<true, false>(a, s) : launch_rows<false, false>(a, s);
 }
 
 }  // namespace qg

@@ -3,6 +3,6 @@
 
 namespace qg {
 
-template int launch_rows<true>(const AttnArgs&, cudaStream_t);
+template int launch_rows<true, false>(const AttnArgs&, cudaStream_t);
 
 }  // namespace qg

@@ -24,6 +24,10 @@ int launch_append_rotary(const qgkv_cache& c, int64_t layer, const void* q, cons
                          int64_t width, const int32_t* lens, const int32_t* starts, int batch, unsigned* status,
                          cudaStream_t s);
 
+int launch_share(int64_t pages, int page_tokens, const int32_t* table, int64_t width, const int32_t* lens,
+                 const int32_t* starts, int64_t rows, int batch, const int32_t* groups, int ngroups, int32_t* plan,
+                 unsigned* status, cudaStream_t s);
+
 int launch_logits_adjust(const void* logits, int type, int64_t rows, int64_t vocab, int64_t row_stride, void* out,
                          int out_type, int64_t out_stride, const int32_t* history, int64_t width, const int32_t* lens,
                          const int32_t* prompt_lens, const float* repetition, const float* presence,

@@ -41,7 +41,8 @@ PAIRS = {"interleaved": 0, "halves": 1}
 TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 EXPORTS = ("qgkv_workspace_bytes", "qgkv_append", "qgkv_attention", "qgkv_copy_pages", "qgkv_fork", "qgkv_compact",
-           "qgkv_reserve", "qgkv_free", "qgbeam_select", "qgkv_append_rotary", "qglogits_adjust")
+           "qgkv_reserve", "qgkv_free", "qgbeam_select", "qgkv_append_rotary", "qglogits_adjust", "qgkv_share",
+           "qgkv_attention_shared")
 
 
 class QgkvCache(ctypes.Structure):
@@ -65,6 +66,8 @@ def load():
         "qgkv_workspace_bytes": [],
         "qgkv_append": [vp, i64, vp, vp, ci, i64, i64, i64, vp, i64, vp, vp, ci, vp],
         "qgkv_attention": [vp, i64, vp, vp, vp, ci, i64, ci, i64, i64, vp, i64, vp, vp, ci, cf, vp, i64, vp],
+        "qgkv_attention_shared": [vp, i64, vp, vp, vp, ci, i64, ci, i64, i64, vp, i64, vp, vp, ci, vp, ci, cf, vp, i64, vp],
+        "qgkv_share": [i64, ci, vp, i64, vp, vp, i64, ci, vp, ci, vp, vp],
         "qgkv_copy_pages": [vp, vp, vp, vp, i64, vp],
         "qgkv_fork": [vp, vp, i64, vp, ci, vp, ci, vp, vp, vp, vp, vp, i64, vp],
         "qgkv_compact": [vp, vp, i64, vp, ci, vp, vp, vp, vp, vp, vp, vp, i64, vp],
@@ -289,15 +292,8 @@ def kv_append_rotary(cache, layer, q, k, v, rope, table, lens, starts=None, pair
     return out
 
 
-def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None, lse=None, return_lse=False,
-                 workspace=None, stream=None):
-    """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
-    (qgkv_attention).  q [rows, q_heads, head_dim]; returns out, or (out, lse) with
-    return_lse.  scale: 1 / sqrt(head_dim) where None."""
-    if _other(stream, cache, q, table, lens, starts, out, lse, workspace):
-        with torch.cuda.stream(stream):
-            return kv_attention(cache, layer, q, table, lens, starts, scale, out, lse, return_lse, workspace)
-    batch, width, tp, lp, sp = _batch(table, lens, starts)
+def _queries(cache, q, out, lse, return_lse):
+    """(rows, q_heads, the C call's arguments for q, out, lse) of an attention, with the outputs made where None."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     heads = q.shape[1]
@@ -314,10 +310,68 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
         ep = lse.data_ptr()
     else:
         ep = None
+    return out, lse, (qp, op, ep, kind, rows, heads, row, head)
+
+
+def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None, lse=None, return_lse=False,
+                 workspace=None, stream=None):
+    """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
+    (qgkv_attention).  q [rows, q_heads, head_dim]; returns out, or (out, lse) with
+    return_lse.  scale: 1 / sqrt(head_dim) where None."""
+    if _other(stream, cache, q, table, lens, starts, out, lse, workspace):
+        with torch.cuda.stream(stream):
+            return kv_attention(cache, layer, q, table, lens, starts, scale, out, lse, return_lse, workspace)
+    batch, width, tp, lp, sp = _batch(table, lens, starts)
+    out, lse, args = _queries(cache, q, out, lse, return_lse)
     w, wp, wb = _ws(workspace, q)
-    _call("qgkv_attention", cache.ref, layer, qp, op, ep, kind, rows, heads, row, head, tp, width, lp, sp, batch,
+    _call("qgkv_attention", cache.ref, layer, *args, tp, width, lp, sp, batch,
           cache.scale if scale is None else scale, wp, wb,
           _stream(q, cache.k, out, lse, table, lens, starts, w.buffer))
+    return (out, lse) if return_lse else out
+
+
+def kv_share(cache, table, lens, groups, starts=None, rows=None, out=None, stream=None):
+    """What the sequences of each group have in common, for kv_attention_shared (qgkv_share): sequences
+    groups[g] .. groups[g + 1] - 1 (int32 [n + 1]) are group g, lens counts the step's tokens already.  Returns
+    the plan, int32 [4 n + batch]: (first row, rows, tokens shared, first sequence) of each group, then the
+    tokens that each sequence shares.  It is read and made on the device, once for all layers of a step.
+    rows: the number of query rows; where None, and with starts, rows outside the queries are first found by
+    the attention."""
+    if _other(stream, cache, table, lens, groups, starts, out):
+        with torch.cuda.stream(stream):
+            return kv_share(cache, table, lens, groups, starts, rows, out)
+    batch, width, tp, lp, sp = _batch(table, lens, starts)
+    gp = _need(groups, torch.int32, "groups", (None,))
+    n = groups.shape[0] - 1
+    if n < 1:
+        raise ValueError("groups must be [number of groups + 1]")
+    if out is None:
+        out = torch.empty((4 * n + batch,), dtype=torch.int32, device=table.device)
+    op = _need(out, torch.int32, "out", (4 * n + batch,))
+    if rows is None:
+        rows = batch if starts is None else (1 << 31) - 1
+    _call("qgkv_share", cache.pages, cache.page_tokens, tp, width, lp, sp, rows, batch, gp, n, op,
+          _stream(table, lens, groups, starts, out, cache.k))
+    return out
+
+
+def kv_attention_shared(cache, layer, q, table, lens, plan, starts=None, scale=None, out=None, lse=None,
+                        return_lse=False, workspace=None, stream=None):
+    """kv_attention of a batch whose groups share pages, which are read once for all rows of a group
+    (qgkv_attention_shared).  plan: what kv_share gave for the same table, lens and starts."""
+    if _other(stream, cache, q, table, lens, plan, starts, out, lse, workspace):
+        with torch.cuda.stream(stream):
+            return kv_attention_shared(cache, layer, q, table, lens, plan, starts, scale, out, lse, return_lse, workspace)
+    batch, width, tp, lp, sp = _batch(table, lens, starts)
+    pp = _need(plan, torch.int32, "plan", (None,))
+    groups = (plan.shape[0] - batch) // 4
+    if groups < 1 or 4 * groups + batch != plan.shape[0]:
+        raise ValueError(f"plan has {plan.shape[0]} entries, not 4 * groups + batch")
+    out, lse, args = _queries(cache, q, out, lse, return_lse)
+    w, wp, wb = _ws(workspace, q)
+    _call("qgkv_attention_shared", cache.ref, layer, *args, tp, width, lp, sp, batch, pp, groups,
+          cache.scale if scale is None else scale, wp, wb,
+          _stream(q, cache.k, out, lse, table, lens, starts, plan, w.buffer))
     return (out, lse) if return_lse else out
 
 

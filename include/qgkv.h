@@ -151,6 +151,34 @@ QG_API int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q,
                           int64_t table_width, const int32_t* lens, const int32_t* starts, int batch, float scale,
                           void* workspace, int64_t workspace_bytes, cudaStream_t stream);
 
+/* What sequences have in common, for qgkv_attention_shared.  Sequences
+ * groups[g] .. groups[g+1]-1 (int32 [ngroups + 1], rising, within the batch) are
+ * group g.  The tokens that a group shares are those of the first columns in
+ * which all its sequences hold the same pages, as far as every row of it sees
+ * them, in whole pages; 0 where fewer than two of its sequences have rows (those
+ * without rows take no part).  table, lens, starts and rows: as for the attention.
+ * plan, int32 [4 * ngroups + batch], gets for each group (first row, rows, tokens
+ * shared, first sequence) and then for each sequence the tokens that it shares.
+ * One plan serves all layers of a step.  Borders that do not rise or leave the
+ * batch: nothing is shared (QG_EBOUNDS). */
+QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int64_t table_width, const int32_t* lens,
+                      const int32_t* starts, int64_t rows, int batch, const int32_t* groups, int ngroups,
+                      int32_t* plan, cudaStream_t stream);
+
+/* qgkv_attention of a batch whose groups share tokens: the pages shared are read
+ * once for all rows of a group, and the results joined with those of the tokens
+ * behind them.  plan: what qgkv_share wrote for the same table, lens and starts;
+ * an entry that does not fit them counts as nothing shared (QG_EBOUNDS, and the
+ * rows of its group are not valid).  Everything else, numerics included, is as for
+ * qgkv_attention.  Where sharing would gain nothing (few tokens, many rows a
+ * sequence) or the results to join exceed the workspace, each sequence reads
+ * all its tokens itself. */
+QG_API int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
+                                 int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride,
+                                 const int32_t* table, int64_t table_width, const int32_t* lens,
+                                 const int32_t* starts, int batch, const int32_t* plan, int ngroups, float scale,
+                                 void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
 /* Copy pages src[i] to dst[i], 0 <= i < n, codes and scales of every layer.
  * n is *count (device) where count is not null, at most `most` either way.
  * No destination may be a source or another destination. */

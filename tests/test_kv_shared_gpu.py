@@ -1,0 +1,397 @@
+"""GPU tests of kv_share and kv_attention_shared against a plain implementation in 64
+bits that knows nothing of the sharing.
+
+Tolerance: test_kv_gpu's, which counts (16 + L / 64) 2^-22 of A for sums of L / 64
+steps and their joins.  The prefix's parts and the tokens behind it are joined once
+more, each weight by an exponential (2^-22), two products, a sum and a quotient
+(2^-24 each): 2 * 2^-22, which 512 tokens more in L cover; and for bf16 queries
+weights down to 2^-28 of the row's largest count, as in calls of many rows.
+"""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from block_quantised_weight_gb300 import qgemv  # noqa: E402
+from test_kv_gpu import DT, attention_ref, close, i32, kv, make, starts_of, status_clean, ws  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+def shared_table(kv, shape, heads, dim, page, fmt, order, seed=0, layers=2):  # noqa: F811
+    """shape: for each group (tokens of the prefix, tokens of each sequence behind it).  Whole pages of a prefix are the
+    first sequence's.  Returns cache, table, lens (list), borders of the groups."""
+    lens = [p + t for p, tails in shape for t in tails]
+    cache, table, _ = make(kv, lens, heads, dim, page, fmt, order, seed=seed, layers=layers)
+    ids, at, borders = table.cpu().numpy(), 0, [0]
+    for p, tails in shape:
+        for i in range(len(tails)):
+            ids[at + i, :p // page] = ids[at, :p // page]
+        at += len(tails)
+        borders.append(at)
+    return cache, i32(ids.tolist()), lens, borders
+
+
+def plan_ref(ids, lens, starts, borders, page, pages):
+    """The plan by its definition, one column after the other."""
+    head, skip = [], [0] * len(lens)
+    for g0, g1 in zip(borders, borders[1:]):
+        busy = [b for b in range(g0, g1) if starts[b + 1] > starts[b]]
+        tokens = 0
+        if len(busy) > 1:
+            most = min(max(0, lens[b] - (starts[b + 1] - starts[b]) + 1) for b in busy) // page
+            while tokens < most and len({ids[b][tokens] for b in busy}) == 1 and 0 <= ids[busy[0]][tokens] < pages:
+                tokens += 1
+        head += [starts[g0], starts[g1] - starts[g0], tokens * page, busy[0] if busy else g0]
+        for b in busy:
+            skip[b] = tokens * page
+    return head + skip
+
+
+def check(kv, ws, shape, group, heads, dim, page, fmt, order, dtype, rows=None, seed=0, scale=None, out=False):  # noqa: F811
+    cache, table, lens, borders = shared_table(kv, shape, heads, dim, page, fmt, order, seed)
+    rows = [1] * len(lens) if rows is None else rows
+    st = starts_of(rows)
+    starts = None if all(r == 1 for r in rows) else i32(st)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    q = torch.randn((st[-1], group * heads, dim), device="cuda", generator=g).to(DT[dtype])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=starts)
+    assert plan.tolist() == plan_ref(table.tolist(), lens, st, borders, page, cache.pages)
+    got, lse = kv.kv_attention_shared(cache, 1, q, table, i32(lens), plan, starts=starts, scale=scale, return_lse=True, workspace=ws)
+    ref = attention_ref(cache, 1, q, table, lens, st, 1 / math.sqrt(dim) if scale is None else scale)
+    one_part = dtype == "bf16"
+    if one_part:
+        ref = (*ref[:4], ref[4] * 2.0 ** 10)
+    close(got, lse, ref, max(lens) + 512, DT[dtype], one_part=one_part)
+    return cache, table, lens, borders, q, plan, got, lse
+
+
+@pytest.mark.parametrize("fmt, order", [("e4m3", "hnd"), ("int8", "nhd")])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [[(16, [1, 1])], [(15, [3, 4])], [(100, [1, 30, 17])], [(1000, [5] * 7)],
+                                   [(129, [1, 2]), (0, [9, 9]), (64, [40])], [(2000, [300, 1, 77, 16])]], ids=str)
+def test_shared(kv, ws, shape, fmt, order, dtype):  # noqa: F811
+    check(kv, ws, shape, 4, 2, 64, 16, fmt, order, dtype, seed=len(shape))
+
+
+@pytest.mark.parametrize("dtype, fmt", [("f32", "int8"), ("f16", "e4m3"), ("bf16", "e4m3"), ("bf16", "int8")])
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 128, 144, 256])
+@pytest.mark.parametrize("group", [1, 3, 8, 17])
+def test_shared_heads_and_dims(kv, ws, dim, group, dtype, fmt):  # noqa: F811
+    check(kv, ws, [(300, [20, 1, 45, 9, 33]), (150, [3, 70])], group, 2, dim, 16, fmt, "hnd", dtype, seed=dim + group)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("order", ["hnd", "nhd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_pages(kv, ws, page, order, dtype):  # noqa: F811
+    check(kv, ws, [(700, [1, 20, 300]), (513, [2, 2])], 4, 3, 128, page, "e4m3", order, dtype, seed=page)
+
+
+@pytest.mark.parametrize("members", [2, 8, 15, 33, 70])
+@pytest.mark.parametrize("dtype, dim", [("bf16", 128), ("f32", 64), ("f16", 128), ("bf16", 256), ("f32", 128), ("f16", 64)])
+def test_shared_by_many(kv, ws, members, dtype, dim):  # noqa: F811
+    """Row counts on both sides of each block of query rows."""
+    check(kv, ws, [(900, [1 + 7 * i % 50 for i in range(members)])], 4, 2, dim, 32, "e4m3", "hnd", dtype, seed=members)
+
+
+@pytest.mark.parametrize("members, groups", [(2, 40), (5, 9), (64, 3)])
+def test_shared_by_many_groups(kv, ws, members, groups):  # noqa: F811
+    g = np.random.default_rng(groups)
+    shape = [(int(g.integers(0, 500)), [int(x) for x in g.integers(1, 90, members)]) for _ in range(groups)]
+    check(kv, ws, shape, 4, 1, 64, 16, "int8", "hnd", "bf16", seed=members)
+    check(kv, ws, shape, 2, 2, 128, 16, "e4m3", "nhd", "f32", seed=members)
+
+
+@pytest.mark.parametrize("prefix, members, heads", [(40000, 3, 1), (9001, 9, 2), (20000, 20, 1)])
+@pytest.mark.parametrize("dtype, dim", [("bf16", 128), ("f32", 64), ("f16", 256)])
+def test_shared_long(kv, ws, prefix, members, heads, dtype, dim):  # noqa: F811
+    """Prefixes whose keys are cut among many CTAs."""
+    check(kv, ws, [(prefix, [33 * (i + 1) for i in range(members)])], 4, heads, dim, 64, "e4m3", "hnd", dtype, seed=prefix)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [[2, 5, 1, 1, 3], [1, 0, 9, 0, 8], [0, 0, 4, 1, 1], [40, 1, 2, 60, 1]], ids=str)
+def test_shared_several_rows(kv, ws, rows, dtype):  # noqa: F811
+    """Rows of a chunk, sequences without rows, rows that see less than the sequences have in common."""
+    check(kv, ws, [(200, [2, 30, 9]), (100, [70, 4])], 4, 2, 64, 16, "e4m3", "hnd", dtype, rows=rows, seed=sum(rows))
+
+
+def test_shared_tails_of_nothing(kv, ws):  # noqa: F811
+    """Sequences that end with the prefix: the last row sees all of it and the first one token less."""
+    check(kv, ws, [(64, [0, 0, 0]), (128, [0, 5])], 2, 2, 64, 16, "e4m3", "hnd", "f32")
+    check(kv, ws, [(64, [0, 0, 0]), (128, [0, 5])], 2, 2, 64, 16, "int8", "hnd", "bf16", rows=[1, 2, 1, 17, 1])
+
+
+def test_sequences_of_no_group(kv, ws):  # noqa: F811
+    """Borders that leave sequences at both ends out."""
+    cache, table, lens, _ = shared_table(kv, [(0, [40]), (80, [3, 9, 1]), (96, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    q = torch.randn((6, 8, 64), device="cuda")
+    for borders in ([1, 4], [1, 3], [0, 0, 1, 1, 4, 4], [6, 6]):
+        plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+        assert plan.tolist() == plan_ref(table.tolist(), lens, list(range(7)), borders, 16, cache.pages)
+        out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+        close(out, lse, attention_ref(cache, 0, q, table, lens, list(range(7)), 1 / 8), max(lens) + 512, torch.float32)
+
+
+def test_share_of_bad_inputs(kv, ws):  # noqa: F811
+    cache, table, lens, borders = shared_table(kv, [(80, [3, 9, 1]), (96, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    for bad in ([0, 4, 2], [-1, 3, 5], [0, 3, 6], [5, 3, 5]):
+        plan = kv.kv_share(cache, table, i32(lens), i32(bad))
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS and (plan == 0).all()
+    # page numbers outside the cache are no common pages, from the first of them on
+    ids = table.clone()
+    ids[:3, 2] = cache.pages
+    ids[3:, 0] = -1
+    plan = kv.kv_share(cache, ids, i32(lens), i32(borders)).tolist()
+    assert [plan[2], plan[6]] == [32, 0] and plan[8:] == [32, 32, 32, 0, 0]
+    # lengths beyond the table, rows that are none
+    plan = kv.kv_share(cache, table, i32([83, 5000, 81, 101, 101]), i32(borders)).tolist()
+    assert plan[2] == 0 and plan[6] == 96
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=i32([0, 1, 0, 2, 3, 4])).tolist()
+    assert plan[2] == 0 and plan[6] == 96
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=i32([0, 1, 2, 3, 4, 9]), rows=5).tolist()
+    assert plan[2] == 80 and plan[6] == 0
+
+
+def test_shared_bad_plans_are_reported(kv, ws):  # noqa: F811
+    """Entries that do not fit the call reach nothing outside it; the groups that fit are right."""
+    cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    q = torch.randn((5, 8, 64), device="cuda")
+    good = kv.kv_share(cache, table, i32(lens), i32(borders))
+    ref = attention_ref(cache, 0, q, table, lens, list(range(6)), 1 / 8)
+    for at, value in ((0, -1), (0, 4), (1, 9), (1, -2), (2, -16), (2, 1 << 30), (2, 7), (3, 5), (3, -1), (8, -16), (9, 1 << 20), (10, 7)):
+        plan = good.clone()
+        plan[at] = value
+        out = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS, (at, value)
+        close(out[3:], None, tuple(x[3:] for x in ref), max(lens) + 512, torch.float32)
+
+
+def test_shared_bad_pages_are_reported_and_masked(kv, ws):  # noqa: F811
+    """A plan made before its pages were lost: they count as masked in all rows."""
+    cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1])], 2, 64, 16, "e4m3", "hnd")
+    q = torch.randn((3, 8, 64), device="cuda")
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    for bad in (-1, cache.pages):
+        ids = table.clone()
+        ids[:, 5] = bad
+        ids[1, 20] = bad  # the page behind the prefix
+        out, lse = kv.kv_attention_shared(cache, 0, q, ids, i32(lens), plan, return_lse=True, workspace=ws)
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+        keep = [c for c in range(21) if c != 5]
+        for b in range(3):  # the same tokens in a table without the lost pages
+            cols = [c for c in keep if not (b == 1 and c == 20)]
+            n = len(cols) * 16 - (16 - lens[b] % 16) % 16 if cols[-1] == 20 else len(cols) * 16
+            ref = attention_ref(cache, 0, q[b:b + 1], table[b:b + 1, cols], [n], [0, 1], 1 / 8)
+            close(out[b:b + 1], lse[b:b + 1], ref, max(lens) + 512, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_shared_masked_tokens_do_not_reach(kv, ws, dtype, dim):  # noqa: F811
+    """NaN codes in pages that no row sees, behind every sequence's end and in the part of a page behind it."""
+    cache, table, lens, borders = shared_table(kv, [(330, [3, 9, 1, 20])], 2, dim, 16, "e4m3", "hnd")
+    q = torch.randn((4, 8, dim), device="cuda").to(DT[dtype])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    want = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    held = torch.zeros((cache.pages, 16), dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        for t in range(n):
+            held[table[b, t // 16], t % 16] = True
+    for c in (cache.k, cache.v):
+        c[0].masked_fill_(~held[:, None, :, None], 0x7F)
+    free = ~held.any(1)
+    cache.k_scale[0, free] = math.nan
+    cache.v_scale[0, free] = math.inf
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("where", [5, 321, 330])
+def test_shared_nan_codes_that_rows_see(kv, ws, dtype, where):  # noqa: F811
+    """A NaN code of V in the prefix reaches its dim of every row of its head; behind it, of the row that holds it."""
+    cache, table, lens, borders = shared_table(kv, [(320, [30, 40])], 2, 64, 16, "e4m3", "hnd")
+    q = torch.randn((2, 8, 64), device="cuda").to(DT[dtype])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    want = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
+    cache.v[0, table[1, where // 16], 1, where % 16, 37] = 0x7F
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
+    nan = torch.isnan(got)
+    expect = torch.zeros_like(nan)
+    expect[:2 if where < 320 else 0, 4:, 37] = True
+    expect[1, 4:, 37] = True
+    assert torch.equal(nan, expect)
+    assert torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("unit", [18, 24, 60, 120])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dim, fmt, dtype", [(64, "e4m3", "f32"), (128, "int8", "bf16"), (128, "e4m3", "f16"), (256, "e4m3", "bf16")])
+@pytest.mark.parametrize("members, n", [(2, 700), (40, 3000)])
+def test_shared_scores_of_any_size(kv, ws, unit, sign, dim, fmt, dtype, members, n):  # noqa: F811
+    """Scores that are whole multiples, up to 8, of 2^unit, in the prefix and behind it: all weight is on the tokens of
+    the largest, in equal shares, over blocks whose V scales differ."""
+    from test_kv_edges_gpu import code
+    cache, table, lens, borders = shared_table(kv, [(n, [1 + i % 20 for i in range(members)])], 1, dim, 16, fmt, "hnd")
+    cpu = torch.Generator().manual_seed(unit + n)
+    g = torch.Generator(device="cuda").manual_seed(unit)
+    what = torch.randint(-8, 9, (cache.pages, 16), generator=cpu)
+    if sign < 0:
+        what = what.abs() + 1
+    by_value = {x: code(x, fmt) for x in range(-9, 10)}
+    cache.k.zero_()
+    cache.k_scale.fill_(1.0)
+    cache.k[0, :, 0, :, 1] = torch.tensor([[by_value[int(x)] for x in row] for row in what], dtype=torch.uint8, device="cuda")
+    cache.v.copy_(torch.randint(0, 100, cache.v.shape, device="cuda", generator=g, dtype=torch.uint8))
+    cache.v_scale.copy_(torch.exp2(torch.randint(-6, 7, cache.v_scale.shape, device="cuda", generator=g).float()))
+    q = torch.zeros((members, 2, dim), device="cuda")
+    q[:, :, 1] = sign
+    q = q.to(DT[dtype])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, scale=2.0 ** unit, return_lse=True, workspace=ws)
+    from test_kv_gpu import gather
+    for b in range(members):
+        x = sign * torch.cat([what[p] for p in table[b, :(lens[b] + 15) // 16].tolist()])[:lens[b]].double().cuda()
+        p = (x == x.max()).double()
+        want = (p / p.sum()) @ gather(cache, 0, table, b, lens[b], "v")[:, 0]  # no value is negative
+        eps = torch.finfo(DT[dtype]).eps / 2 + (2.0 ** -11 if dtype == "bf16" else 0.0) + (40 + lens[b] / 64) * 2.0 ** -22
+        assert ((out[b].double() - want).abs() <= want * eps * 1.01 + 1e-30).all()
+        top = x.max().item() * 2.0 ** unit
+        assert ((lse[b].double() - top).abs() <= math.log(lens[b]) + 1e-4 + abs(top) * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim, members", [(64, 3), (128, 40), (256, 5)])
+def test_shared_scales_of_all_sizes(kv, ws, dtype, dim, members):  # noqa: F811
+    """V scales 2^-40 to 2^-4 by page, some zero; K scales zero in some pages; rows whose weight is on small ones."""
+    cache, table, lens, borders = shared_table(kv, [(500, [1 + 3 * i % 40 for i in range(members)])], 2, dim, 16, "e4m3", "hnd")
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    cache.v_scale.copy_(torch.exp2(torch.randint(-40, -3, cache.v_scale.shape, device="cuda", generator=g).float()))
+    cache.v_scale[0, ::7] = 0.0
+    cache.k_scale[0, ::11] = 0.0
+    cache.v_scale[0, table[0, 3]] = 0.0
+    q = torch.randn((members, 8, dim), device="cuda", generator=g).to(DT[dtype])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    ref = attention_ref(cache, 0, q, table, lens, list(range(members + 1)), 1 / math.sqrt(dim))
+    close(out, lse, (*ref[:4], ref[4] * 2.0 ** (10 if dtype == "bf16" else 4)), max(lens) + 512, DT[dtype], one_part=dtype == "bf16")
+
+
+def test_shared_prefix_below_and_above_the_rest(kv, ws):  # noqa: F811
+    """The prefix's scores lie 300 binary orders below those behind it, or above: one part's weight is 0."""
+    from test_kv_edges_gpu import code
+    for up in (True, False):
+        cache, table, lens, borders = shared_table(kv, [(640, [3, 30, 17])], 1, 64, 16, "e4m3", "hnd")
+        cache.k.fill_(code(1 if up else -2, "e4m3"))
+        cache.k[:, table[0, :40].long()] = code(-2 if up else 1, "e4m3")
+        cache.k_scale.fill_(1.0)
+        q = torch.full((3, 2, 64), 100.0, device="cuda")
+        plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+        out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, scale=math.log(2) / 64, return_lse=True, workspace=ws)
+        close(out, lse, attention_ref(cache, 0, q, table, lens, [0, 1, 2, 3], math.log(2) / 64), 1200, torch.float32)
+
+
+def test_shared_non_finite_queries(kv, ws):  # noqa: F811
+    """A query row with NaN gives NaN; the other rows of its block are as without it."""
+    cache, table, lens, borders = shared_table(kv, [(500, [3, 30, 17, 8, 9])], 2, 128, 16, "e4m3", "hnd")
+    q = torch.randn((5, 8, 128), device="cuda").bfloat16()
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    want = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
+    q[2, 3, 70] = math.nan
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
+    assert torch.isnan(got[2, 3]).all()
+    got[2, 3] = want[2, 3]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_strided_queries_and_outputs(kv, ws, dtype):  # noqa: F811
+    cache, table, lens, borders = shared_table(kv, [(500, [3, 30, 17, 8, 9])], 2, 64, 16, "e4m3", "hnd")
+    wide = torch.randn((5, 20, 64), device="cuda").to(DT[dtype])
+    q = wide[:, 5:13]
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    out, lse = torch.empty((5, 8, 64), device="cuda", dtype=DT[dtype]), torch.empty((5, 8), device="cuda")
+    want = kv.kv_attention_shared(cache, 0, q.contiguous(), table, i32(lens), plan, return_lse=True, workspace=ws)
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, out=out, lse=lse, workspace=ws)
+    assert got is out and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan), want[0])  # a workspace of its own
+
+
+def test_shared_rows_behind_the_last_are_left(kv, ws):  # noqa: F811
+    cache, table, lens, borders = shared_table(kv, [(500, [30, 30])], 2, 64, 16, "e4m3", "hnd")
+    q = torch.randn((9, 8, 64), device="cuda")
+    starts = i32([0, 2, 5])
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=starts)
+    out = torch.full((9, 8, 64), 3.0, device="cuda")
+    kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, starts=starts, out=out, workspace=ws)
+    assert (out[5:] == 3.0).all() and not (out[:5] == 3.0).any()
+
+
+def test_shared_repeats_bit_for_bit_and_alternates(kv, ws):  # noqa: F811
+    """The same bits again, with other calls of the same workspace between."""
+    cache, table, lens, borders = shared_table(kv, [(3000, [3, 30, 17, 8] * 12)], 2, 128, 16, "e4m3", "hnd")
+    q = torch.randn((48, 8, 128), device="cuda").bfloat16()
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    first = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    for _ in range(5):
+        other = kv.kv_attention(cache, 0, q, table, i32(lens), return_lse=True, workspace=ws)
+        again = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    # two roundings of bf16, and what each of the two may be off by before them
+    assert ((other[0].double() - first[0].double()).abs() <= 2.0 ** -7 * first[0].double().abs() + 2.0 ** -9 * first[0].abs().max()).all()
+
+
+def test_shared_in_a_graph_and_on_a_stream(kv):  # noqa: F811
+    """A captured plan and attention, replayed with other lengths, tables and queries, against direct calls."""
+    side, own = torch.cuda.Stream(), kv.KVWorkspace("cuda")
+    cache, table, lens, borders = shared_table(kv, [(600, [70, 60, 80]), (320, [50, 50])], 2, 64, 16, "e4m3", "hnd")
+    q, ln, gr = torch.randn((5, 8, 64), device="cuda"), i32(lens), i32(borders)
+
+    def step():
+        plan = kv.kv_share(cache, table, ln, gr)
+        return plan, kv.kv_attention_shared(cache, 0, q, table, ln, plan, workspace=own)
+
+    step()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        plan, out = step()
+    torch.cuda.current_stream().wait_stream(side)
+    first = table.clone()
+    for i, cut in enumerate((0, 37, 4)):
+        table.copy_(first)
+        table[1, cut:] = table[1, cut:].roll(1)  # less in common
+        ln.copy_(i32([n - 9 * i for n in lens]))
+        q.normal_()
+        graph.replay()
+        want_plan = kv.kv_share(cache, table, ln, gr)
+        want = kv.kv_attention_shared(cache, 0, q, table, ln, want_plan)
+        assert torch.equal(plan, want_plan) and torch.equal(out, want)
+        other = kv.kv_attention_shared(cache, 0, q, table, ln, plan, stream=side, workspace=own)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(other, want)
+    # the roll brought a place without a page among those of sequence 1
+    assert (table[1, :-(-int(ln[1]) // 16)] < 0).any() and qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+
+
+def test_shared_results_beyond_the_workspace(kv, ws):  # noqa: F811
+    """More rows than the workspace holds results for."""
+    batch = 1500
+    cache, table, lens, borders = shared_table(kv, [(320, [1 + i % 30 for i in range(batch)])], 1, 128, 16, "e4m3", "hnd", layers=1)
+    q = torch.randn((batch, 32, 128), device="cuda").bfloat16()
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    some = list(range(0, batch, 97)) + [batch - 1]
+    ref = attention_ref(cache, 0, q[some], table[some], [lens[b] for b in some], list(range(len(some) + 1)), 128 ** -0.5)
+    close(out[some], lse[some], (*ref[:4], ref[4] * 2.0 ** 10), 900, torch.bfloat16, one_part=True)
+
+
+def test_shared_largest_batch(kv, ws):  # noqa: F811
+    """4096 sequences in 1365 groups and one left over."""
+    shape = [(40, [1 + i % 7, 2, 3]) for i in range(1365)] + [(0, [5])]
+    check(kv, ws, shape, 2, 1, 64, 16, "e4m3", "hnd", "f32")

@@ -1,5 +1,5 @@
 """Host checks (no GPU) of the entry points around a decode step: refusals of the
-append with rotation and of the logits adjustment, devices and streams of their
+append with rotation, the shared prefix and the logits adjustment, devices and streams of their
 bindings.  Pointers are never dereferenced, validation fails first."""
 import ctypes
 
@@ -68,8 +68,60 @@ def test_logits_of_no_rows_is_no_error(kv):  # noqa: F811
     assert logits(kv, rows=0, x=None, out=None) == qgemv.QG_OK
 
 
+def share(kv, **change):  # noqa: F811
+    a = dict(pages=64, page_tokens=16, table=at(0), width=8, lens=at(1), starts=None, rows=3, batch=3, groups=at(2), n=2,
+             plan=at(3))
+    a.update(change)
+    return kv.load()["qgkv_share"](*a.values(), None)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(pages=0), E), (dict(page_tokens=24), E), (dict(table=None), E), (dict(lens=None), E), (dict(width=0), E),
+    (dict(rows=2), E), (dict(rows=-1, starts=at(4)), E), (dict(batch=4097), E), (dict(groups=None), E), (dict(n=0), E),
+    (dict(n=4097), E), (dict(plan=None), E), (dict(page_tokens=256, width=1 << 23), E), (dict(groups=at(2) + 1), G), (dict(plan=at(3) + 4), G),
+    (dict(starts=at(4) + 2), G), (dict(plan=at(0)), L), (dict(plan=at(1)), L), (dict(plan=at(2)), L),
+    (dict(plan=at(4), starts=at(4)), L),
+])
+def test_share_refusals(kv, change, code):  # noqa: F811
+    assert share(kv, **change) == code
+
+
+def shared(kv, c=None, **change):  # noqa: F811
+    a = dict(layer=0, q=at(0), out=at(1), lse=at(2), type=0, rows=3, q_heads=32, row=32 * 64, head=64, table=at(3),
+             width=8, lens=at(4), starts=None, batch=3, plan=at(6), n=2, scale=0.125, ws=at(16), wb=1 << 30)
+    a.update(change)
+    c = cache(kv) if c is None else c
+    return kv.load()["qgkv_attention_shared"](ctypes.addressof(c), *a.values(), None)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(layer=2), E), (dict(q=None), E), (dict(out=None), E), (dict(type=3), E), (dict(q_heads=30), E), (dict(rows=4), E),
+    (dict(batch=0), E), (dict(width=0), E), (dict(plan=None), E), (dict(n=0), E), (dict(n=4097), E), (dict(ws=None), E),
+    (dict(scale=float("nan")), E), (dict(q=at(0) + 4), G), (dict(plan=at(6) + 4), G), (dict(ws=at(16) + 128), G),
+    (dict(wb=1 << 20), qgemv.QG_ESCRATCH), (dict(out=at(0) + 64), L), (dict(out=A + 64), L), (dict(lse=at(1) + 64), L),
+    (dict(out=at(6)), L), (dict(lse=at(6)), L),
+])
+def test_attention_shared_refusals(kv, change, code):  # noqa: F811
+    assert shared(kv, **change) == code
+
+
+def test_attention_shared_of_no_rows_is_no_error(kv):  # noqa: F811
+    assert shared(kv, rows=0, starts=at(5), q=None, out=None, lse=None) == qgemv.QG_OK
+
+
+def Space(qgkv, take, device):
+    w = qgkv.KVWorkspace.__new__(qgkv.KVWorkspace)
+    w.buffer, w.ptr, w.bytes = take(on(device, 8, dtype=torch.uint8)), 0, 8
+    return w
+
+
 # every tensor of every call: position in this list is the one that lies elsewhere
 OPERATORS = {
+    "qgkv_share": (6, lambda k, d, t: k.kv_share(t(cache_on(k, d[0])), t(on(d[1], 2, 2)), t(on(d[2], 2)), t(on(d[3], 2)),
+                                                 starts=t(on(d[4], 3)), out=t(on(d[5], 6)))),
+    "qgkv_attention_shared": (9, lambda k, d, t: k.kv_attention_shared(
+        t(cache_on(k, d[0])), 0, t(on(d[1], 2, 4, 64, **F32)), t(on(d[2], 2, 2)), t(on(d[3], 2)), t(on(d[4], 6)),
+        starts=t(on(d[5], 3)), out=t(on(d[6], 2, 4, 64, **F32)), lse=t(on(d[7], 2, 4, **F32)), workspace=Space(k, t, d[8]))),
     "qgkv_append_rotary": (7, lambda k, d, t: k.kv_append_rotary(
         t(cache_on(k, d[0])), 0, t(on(d[1], 1, 4, 64, **F32)), t(on(d[2], 1, 2, 64, **F32)), t(on(d[2], 1, 2, 64, **F32)),
         t(on(d[3], 9, 64, **F32)), t(on(d[4], 1, 2)), t(on(d[5], 1)), out=t(on(d[6], 1, 4, 64, **F32)))),
@@ -115,7 +167,7 @@ def test_tensors_are_lent_to_the_stream_of_a_call(calls, monkeypatch, name):  # 
     count, call = OPERATORS[name]
 
     class Streamed:
-        KVCache = qgkv.KVCache
+        KVCache, KVWorkspace = qgkv.KVCache, qgkv.KVWorkspace
 
         def __getattr__(self, f):
             return lambda *a, **b: getattr(qgkv, f)(*a, **b, stream="side")
@@ -146,4 +198,14 @@ def test_binding_refusals(calls):  # noqa: F811
                 dict(presence=on(0, 2)), dict(out=on(0, 2, 9))):
         with pytest.raises(TypeError):
             qgkv.adjust_logits(x, **bad)
+    plan = lambda n: qgkv.kv_attention_shared(c, 0, q, table, lens, on(0, n))  # noqa: E731
+    for n in (0, 1, 4, 6):
+        with pytest.raises(ValueError):
+            plan(n)
+    with pytest.raises(ValueError):
+        qgkv.kv_share(c, table, lens, on(0, 1))
+    with pytest.raises(ValueError):
+        qgkv.kv_share(c, table, lens, on(0, 2), out=on(0, 6))
+    with pytest.raises(TypeError):
+        qgkv.kv_share(c, table, lens, on(0, 2, dtype=torch.int64))
     assert not made
