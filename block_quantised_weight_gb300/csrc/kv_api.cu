@@ -269,15 +269,17 @@ int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q,
                                      table_width, lens, starts, batch, scale, workspace, workspace_bytes,
                                      {plan, (4 * int64_t(ngroups) + batch) * 4}, a, &done);
     if (rc != QG_OK || done) return rc;
-    const int64_t values = rows * q_heads * cache->head_dim;
-    const int64_t kept = qg::shared_bytes(rows, q_heads, cache->head_dim);
-    if (2 * kept > qg::kWsSplits - qg::kWsOwn) return launch_attention(a, cache->format == QGKV_INT8, stream);
+    const bool int8 = cache->format == QGKV_INT8;
+    if (qg::own_bytes(rows, q_heads, cache->head_dim) > qg::kWsSplits - qg::kWsOwn) return launch_attention(a, int8, stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.groups = reinterpret_cast<const int4*>(plan);
     a.skip = plan + 4 * int64_t(ngroups);
-    a.sequences = batch;
-    a.own = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + qg::kWsOwn);
-    a.own_ml = reinterpret_cast<float2*>(a.own + values);
-    return qg::launch_attn_shared(a, ngroups, cache->format == QGKV_INT8, stream);
+    a.ngroups = ngroups;
+    a.own_ml = reinterpret_cast<float4*>(ws + qg::kWsOwn);
+    a.own = reinterpret_cast<float*>(a.own_ml + rows * q_heads);
+    a.slots = reinterpret_cast<float*>(ws + qg::kWsSlots);
+    const int launched = qg::launch_attn_prefix(a, int8, stream);
+    return launched != QG_OK ? launched : qg::launch_attn_rows_shared(a, int8, stream);
 }
 
 int qgkv_copy_pages(const qgkv_cache* cache, const int32_t* src, const int32_t* dst, const int32_t* count,

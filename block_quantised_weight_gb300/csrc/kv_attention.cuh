@@ -22,14 +22,14 @@ struct AttnArgs {
     int4* splits;
     unsigned* count;
     unsigned* status;
-    // A shared prefix (launch_attn_shared): the plan's groups and tokens, the
-    // results of the prefix and of what is behind it, and which of the two this is.
+    // A shared prefix: the plan's groups and tokens, and the prefix's results (kv_prefix.cu)
     const int4* groups;
     const int32_t* skip;
-    float* own;      // [rows][q_heads][dim], normalised
-    float2* own_ml;  // [rows][q_heads] reference and sum
-    bool prefix;     // batch counts groups
-    int sequences;   // of the call
+    int ngroups;
+    float* own;      // [rows][q_heads][dim], normalised, of a row's first piece
+    float4* own_ml;  // [rows][q_heads] its reference and sum, the CTA of the next, their number and row
+    float* slots;    // [CTA][slot_rows][slot_dims], then [slot_rows] references and sums, of further pieces
+    int slot_rows, slot_dims;
 };
 
 // Number of rows and length of sequence b.  A length beyond the table is cut
@@ -55,46 +55,29 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     return s;
 }
 
-// What a sequence reads behind a shared prefix, or the prefix itself for all rows of
-// its group: rows from row0 on, tokens from page column `col` of a table row on.
-// An entry of the plan that does not fit the call counts as nothing shared
-// (kStatusBounds).
-struct SharedSeq {
-    Seq s;
-    int64_t row0;
-    int table_row, col;
-    bool partial;
+// Entries of a plan that do not fit the call count as nothing shared (kStatusBounds).
+// A group: n rows from row0 on, whose tokens a table row has.
+struct SharedGroup {
+    int row0, n, tokens, table_row;
 };
-__device__ __forceinline__ SharedSeq shared_sequence(const AttnArgs& a, int b) {
-    SharedSeq r = {};
-    if (a.prefix) {
-        const int4 g = a.groups[b];  // first row, rows, tokens, first sequence
-        const int64_t most = a.width << a.c.log2p;
-        bool good = g.x >= 0 && g.y >= 0 && static_cast<int64_t>(g.x) + g.y <= a.rows && g.z >= 0 && g.z <= most &&
-                    (g.z & ((1 << a.c.log2p) - 1)) == 0 && (g.z == 0 || (g.w >= 0 && g.w < a.sequences));
-        if (!good) atomicOr(a.status, kStatusBounds);
-        if (good && g.z > 0) {
-            r.s = {g.y, g.z};
-            r.row0 = g.x;
-            r.table_row = g.w;
-        }
-        r.partial = true;
-        return r;
-    }
-    r.s = sequence(a, b);
-    r.row0 = a.starts ? a.starts[b] : b;
-    r.table_row = b;
+__device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int b) {
+    const int4 g = a.groups[b];  // first row, rows, tokens, first sequence
+    const bool good = g.x >= 0 && g.y >= 0 && static_cast<int64_t>(g.x) + g.y <= a.rows && g.z >= 0 &&
+                      g.z <= a.width << a.c.log2p && (g.z & ((1 << a.c.log2p) - 1)) == 0 &&
+                      (g.z == 0 || (g.w >= 0 && g.w < a.batch));
+    if (!good) atomicOr(a.status, kStatusBounds);
+    return good && g.y > 0 && g.z > 0 ? SharedGroup{g.x, g.y, g.z, g.w} : SharedGroup{0, 0, 0, 0};
+}
+// What a sequence reads behind the tokens that it shares: less of its length, later columns of its table.
+__device__ __forceinline__ int shared_columns(const AttnArgs& a, int b, Seq& s) {
     const int skip = a.skip[b];
-    if (skip != 0 && r.s.n > 0) {
-        if (skip < 0 || skip > r.s.len - r.s.n + 1 || (skip & ((1 << a.c.log2p) - 1))) {
-            atomicOr(a.status, kStatusBounds);
-        } else {
-            r.s.len -= skip;
-            r.col = skip >> a.c.log2p;
-            r.partial = true;
-        }
+    if (skip == 0 || s.n == 0) return 0;
+    if (skip < 0 || skip > s.len - s.n + 1 || (skip & ((1 << a.c.log2p) - 1))) {
+        atomicOr(a.status, kStatusBounds);
+        return 0;
     }
-    return r;
+    s.len -= skip;
+    return skip >> a.c.log2p;
 }
 
 // a / b for non-negative a and positive b, in 32 bits where they fit.
@@ -124,6 +107,7 @@ struct Line {
 // token; d, the reference of score + log2 vs, is held less m, at least kNoOrder (no
 // value but zeros yet).
 constexpr float kNoRef = -3.402823466e38f;
+constexpr int kMostK = 124;  // of k: p * 2^k stays finite, p being 4 at most
 constexpr int kNoOrder = -1000;
 // From here on a score's rounding (2^-24 of it) is no small part of a binary
 // order: the scores of a warp that has met one are rounded before the reference
@@ -176,11 +160,17 @@ __device__ __forceinline__ float4 q4_values(uint4 v, int type) {
 }
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s);
-// Bytes of a result kept for a join: rows x q_heads of dim values, reference and sum.
-inline int64_t shared_bytes(int64_t rows, int q_heads, int dim) {
-    return ((rows * q_heads * (dim * int64_t(4) + 8)) + 255) / 256 * 256;
+int launch_attn_rows_shared(const AttnArgs& a, bool int8, cudaStream_t s);
+// Query rows of a unit of the prefix: as many as shared memory holds operands for.
+constexpr int kMaxPrefixCtas = 160;
+__host__ __device__ constexpr int prefix_rows(int dp, int q_parts, int p_parts) {
+    return dp == 256 ? 32 : q_parts * p_parts == 1 ? 128 : 64;
 }
-int launch_attn_shared(const AttnArgs& a, int groups, bool int8, cudaStream_t s);
+static_assert(int64_t(kMaxPrefixCtas) * 128 * (128 + 2) * 4 <= kWsOwn - kWsSlots &&
+              int64_t(kMaxPrefixCtas) * 32 * (256 + 2) * 4 <= kWsOwn - kWsSlots, "slots exceed the workspace");
+// Bytes of the results kept for each of `rows` rows.
+inline int64_t own_bytes(int64_t rows, int q_heads, int dim) { return rows * q_heads * (dim * int64_t(4) + 16); }
+int launch_attn_prefix(AttnArgs& a, bool int8, cudaStream_t s);
 // K or V of one layer as [pages][heads][page_tokens][dim], boxes of box_tokens x box_bytes; `swizzle`: 64- or
 // 128-byte rows, so that reads down a column of a box meet no bank twice.  Bytes past the dims arrive as 0.
 bool encode_cache(CUtensorMap* map, const KVLayer& c, const uint8_t* base, int box_bytes, int box_tokens, bool swizzle);

@@ -1,0 +1,756 @@
+// Attention over a prefix that sequences share: all rows of a group over the
+// same tokens, each read once, on the tcgen05 tensor cores.
+//
+// Mathematics: kv_rows.cuh's, with both products transposed.  A CTA takes up to NMAX
+// query rows (tokens x heads of a group, a multiple of 32) of one cache head and
+// walks the keys in steps of 128:
+//   S^T = K q^T     128 keys x rows, in tensor memory
+//   p = 2^(S f - m), f = scale * ks,   z = p * vs * 2^k as f16, in shared memory
+//   O^T += V^T z    dims x rows, in tensor memory
+// A group has as many rows as its sequences have heads and tokens, from 8 to
+// hundreds, the keys are always many: with the keys on the 128 rows of the MMA its
+// columns follow the number of rows, and neither operand of the cache has to be
+// transposed: both are converted as they lie, K K-major, V M-major.  A thread has one
+// key: its scales are scalars of the thread, and what belongs to a query row (factor,
+// references) comes from shared memory, four at a time.  References are whole
+// numbers, shared by the four warps of a half of the columns, and move only when a z
+// would pass 2^15 or a p 2^20; 16 columns at a time are tried as if they held, one
+// vote of the four warps decides.
+//
+// Bound.  For up to 128 rows the codes' stream (32 KB a step and SM at 128 dims) takes as long as the
+// exponentials of 128 rows (16 a clock and SM); short calls are bound by the chain
+// plan -> table -> codes -> first step, and by the parts that are left to join.
+//
+// Split.  The steps of all (group, head, row block) are one line, cut evenly among
+// the CTAs.  A piece that begins a unit leaves its result for each row, the
+// others in a slot of their CTA; the row kernel adds them to what lies behind the
+// prefix (own_ml of a row names the CTA of the first further piece and their number).
+//
+// Roles: eight warps for the softmax (two halves of the columns), four convert
+// the codes, one copies, one issues the MMAs.
+#pragma once
+#include <atomic>
+
+#include "kv_attention.cuh"
+#include "kv_tc.cuh"
+#include "launch_common.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kLeastSteps = 2;      // of a CTA's share of the line
+constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
+constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kPrefixThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
+
+template <int DP, int QP, int PP>
+struct XShape {
+    static constexpr int NMAX = prefix_rows(DP, QP, PP);
+    static constexpr int NP = NMAX < 64 ? 64 : NMAX;  // columns of the second product: whole swizzle atoms
+    static constexpr int NH = NMAX / 2;               // columns of a softmax half
+    static constexpr int DA = DP == 256 ? 2 : 1;      // accumulators of 128 dims
+    static constexpr int kQPart = NMAX * DP * 2;
+    static constexpr int kPPart = kKeys * NP * 2;
+    static constexpr int kOp = kKeys * DP * 2;
+    static constexpr int RW = DP < 128 ? DP : 128;    // bytes of a raw row
+    static constexpr int RT = DP / RW;                // raw tiles of an operand
+    static constexpr int kRaw = kKeys * RW;
+    static constexpr uint32_t kOps = DP == 256 ? 2 : DP == 128 ? 3 : 4;
+    static constexpr int off_p = QP * kQPart;
+    static constexpr int off_op = off_p + PP * kPPart;
+    static constexpr int off_raw = off_op + static_cast<int>(kOps) * kOp;
+    static constexpr int kExtra = 12 * 1024;          // what stands behind the raw slots
+    static constexpr int kFit = (232448 - kExtra - off_raw) / kRaw;
+    static constexpr uint32_t kRaws = kFit < 8 ? kFit : 8;
+    static_assert(kFit >= 1, "shared memory");
+    static constexpr int off_scale = off_raw + static_cast<int>(kRaws) * kRaw;
+    static constexpr int off_cols = off_scale + static_cast<int>(kScaleSteps) * 8 * 16;
+    static constexpr int off_bar = off_cols + NMAX * (9 * 4 + 4 * 4 + 8);
+    static constexpr int smem = off_bar + 512;
+    static_assert(smem <= 232448 && off_cols % 16 == 0 && off_bar % 8 == 0, "shared memory");
+};
+
+struct PrefixPiece {
+    int row0, nrows, h, row_first, nc, table_row, j0, j1;
+    int slot;   // -1: begins its unit
+    int extra;  // further pieces of a unit that this one begins
+    int tokens; // of the prefix; < 0: no more pieces
+};
+
+// Rows of the blocks that nrows query rows are cut into.
+template <int NMAX>
+__device__ __forceinline__ int block_rows(int nrows, int* blocks) {
+    const int n = (nrows + NMAX - 1) / NMAX;
+    const int per = n ? ((nrows + n - 1) / n + 31) / 32 * 32 : 32;
+    *blocks = (nrows + per - 1) / per;
+    return per;
+}
+
+// Finds places on the line of all groups (heads, then row blocks, then steps), by a whole warp, forward only.
+template <int NMAX>
+struct GroupWalk {
+    int b0 = -32;
+    SharedGroup g;  // of this lane's group, b0 + lane
+    int64_t base = 0, chunk = 0, upto = 0;
+    __device__ bool more(const AttnArgs& a) {
+        const int lane = threadIdx.x & 31;
+        b0 += 32;
+        base += chunk;
+        if (b0 >= a.ngroups) return false;
+        g = SharedGroup{};
+        if (b0 + lane < a.ngroups) g = shared_group(a, b0 + lane);
+        int blocks = 0;
+        if (g.tokens) block_rows<NMAX>(g.n * a.group, &blocks);
+        upto = static_cast<int64_t>(blocks) * a.c.heads * ((static_cast<int64_t>(g.tokens) + kKeys - 1) / kKeys);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += x;
+        }
+        chunk = __shfl_sync(~0u, upto, 31);
+        return true;
+    }
+    // The unit at `at`, its steps, and the place in it.
+    __device__ bool to(const AttnArgs& a, int64_t at, PrefixPiece& u, int& steps, int64_t& in) {
+        while (at >= base + chunk)
+            if (!more(a)) return false;
+        const int which = __popc(__ballot_sync(~0u, upto <= at - base));
+        u.row0 = __shfl_sync(~0u, g.row0, which);
+        u.nrows = __shfl_sync(~0u, g.n, which) * a.group;
+        u.tokens = __shfl_sync(~0u, g.tokens, which);
+        u.table_row = __shfl_sync(~0u, g.table_row, which);
+        const int64_t below = __shfl_sync(~0u, upto, which ? which - 1 : 0);
+        in = at - base - (which ? below : 0);
+        steps = static_cast<int>((static_cast<int64_t>(u.tokens) + kKeys - 1) / kKeys);
+        int blocks;
+        const int per = block_rows<NMAX>(u.nrows, &blocks);
+        const int64_t unit = div64(in, steps);
+        in -= unit * steps;
+        u.h = static_cast<int>(div64(unit, blocks));
+        u.row_first = static_cast<int>(unit - static_cast<int64_t>(u.h) * blocks) * per;
+        u.nc = min(per, (u.nrows - u.row_first + 31) / 32 * 32);
+        return true;
+    }
+};
+
+__device__ __forceinline__ void sync_warps(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Whether any of the barrier's threads says so.
+__device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"(static_cast<uint32_t>(mine)), "r"(id), "r"(threads) : "memory");
+    return r != 0;
+}
+
+// Order of floats as integers, and back.
+__device__ __forceinline__ int as_order(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_order(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ uint32_t hmax2_of(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Column sums over the 32 lanes: lane i gets the sum of column i.
+__device__ __forceinline__ float add_columns(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float give = lane & w ? v[i] : v[i + w], keep = lane & w ? v[i + w] : v[i];
+            v[i] = keep + __shfl_xor_sync(~0u, give, w);
+        }
+    return v[0];
+}
+
+template <int DP, int QP, int PP, bool INT8>
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using F = XShape<DP, QP, PP>;
+    constexpr int NMAX = F::NMAX, NH = F::NH;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScaleSteps][8]: ks, vs, there
+    // of each column (query row): factor of its scores, less its reference, 2^k; two factors; references
+    float* fac = reinterpret_cast<float*>(smem + F::off_cols);
+    float* nm = fac + NMAX;
+    float* pk = nm + NMAX;
+    float* mul1 = pk + NMAX;
+    float* mul2 = mul1 + NMAX;
+    float* ref = mul2 + NMAX;
+    int* refd = reinterpret_cast<int*>(ref + NMAX);
+    int* top = refd + NMAX;
+    int* topd = top + NMAX;
+    float* sums = reinterpret_cast<float*>(topd + NMAX);              // [4][NMAX]
+    int64_t* orow = reinterpret_cast<int64_t*>(sums + 4 * NMAX);      // output rows, -1 past the last
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
+    uint64_t* raw_empty = raw_full + F::kRaws;
+    uint64_t* op_full = raw_empty + F::kRaws;
+    uint64_t* op_empty = op_full + F::kOps;
+    uint64_t* s_full = op_empty + F::kOps;  // [2]
+    uint64_t* p_full = s_full + 2;
+    uint64_t* pv_done = p_full + 1;
+    uint64_t* q_full = pv_done + 1;
+    uint64_t* sc_full = q_full + 1;         // [kScaleSteps]
+    uint64_t* unit_full = sc_full + kScaleSteps;
+    uint64_t* unit_empty = unit_full + kUnitsAhead;
+    static_assert((2 * F::kRaws + 2 * F::kOps + 5 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
+    __shared__ PrefixPiece units[kUnitsAhead];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int huge_half[2];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const KVLayer& c = a.c;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it; the same in all threads
+        if (tid == 0) atomicOr(a.status, kStatusBounds);
+        return;
+    }
+    if (tid == 0) {
+        for (uint32_t i = 0; i < F::kRaws; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, kConvertWarps);
+        for (uint32_t i = 0; i < F::kOps; ++i) mbar_init(op_full + i, kConvertWarps), mbar_init(op_empty + i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
+        mbar_init(p_full, kSoftmaxWarps);
+        mbar_init(pv_done, 1);
+        mbar_init(q_full, kSoftmaxWarps);
+        for (uint32_t i = 0; i < kScaleSteps; ++i) mbar_init(sc_full + i, 1);
+        for (uint32_t i = 0; i < kUnitsAhead; ++i)
+            mbar_init(unit_full + i, 1), mbar_init(unit_empty + i, kSoftmaxWarps + kConvertWarps + 1);
+        fence_mbar_init();
+    }
+    if (warp == kSoftmaxWarps + kConvertWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t o_at = tmem + 256;  // S^T: two buffers of 128 columns; O^T: F::DA of F::NP
+    // A wait that gave up ends all further waits, copies and MMAs of its warp:
+    // the kernel then runs to its end within a few wait limits.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // by whole warps
+        if (!dead) dead = __any_sync(~0u, !mbar_wait_bounded(bar, parity & 1u, a.status));
+    };
+    // The next piece, as the copying warp hands it to the others; false after the last.
+    uint32_t turn = 0;
+    PrefixPiece w;
+    auto next_unit = [&]() {
+        const uint32_t slot = turn % kUnitsAhead;
+        wait(unit_full + slot, turn / kUnitsAhead);
+        w = units[slot];
+        __syncwarp();
+        if (lane == 0) arrive_on(unit_empty + slot);
+        ++turn;
+        return !dead && w.tokens >= 0;
+    };
+
+    if (warp == kSoftmaxWarps + kConvertWarps) {
+        // ---------------------------------------------------------- copies
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        GroupWalk<NMAX> walk;
+        int64_t total = 0;
+        while (walk.more(a)) total += walk.chunk;
+        walk = GroupWalk<NMAX>();
+        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / kLeastSteps));
+        const Line line(total, static_cast<int>(ctas));
+        int64_t at = 0, end = 0;
+        if (static_cast<int>(blockIdx.x) < line.ctas) at = line.first(blockIdx.x), end = line.first(blockIdx.x + 1);
+        uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
+        uint32_t sent = 0;      // raw tiles whose copies were issued
+        for (;; ++turn) {
+            const uint32_t slot = turn % kUnitsAhead;
+            if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
+            int steps = 0;
+            int64_t in = 0;
+            const bool there = !dead && at < end && walk.to(a, at, w, steps, in);
+            if (there) {
+                const int64_t start = at - in, stop = start + steps;
+                at = min(end, stop);
+                w.j0 = static_cast<int>(in);
+                w.j1 = static_cast<int>(at - start);
+                w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
+                w.extra = in == 0 ? line.of(stop - 1) - static_cast<int>(blockIdx.x) : 0;
+            } else {
+                w.tokens = -1;
+            }
+            if (lane == 0) {
+                units[slot] = w;
+                arrive_on(unit_full + slot);
+            }
+            __syncwarp();
+            if (!there) break;
+            const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
+            auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
+                int id = -1;
+                f = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
+                if (lane < 8 && tok < w.tokens) {
+                    id = table[tok >> c.log2p];
+                    if (id >= 0 && id < c.pages) {
+                        const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
+                        f.x = __ldg(c.ks + s);
+                        f.y = __ldg(c.vs + s);
+                        f.z = 1.f;
+                    } else {
+                        id = -1;
+                        atomicOr(a.status, kStatusBounds);
+                    }
+                }
+                return id;
+            };
+            float4 f;
+            int id = look(w.j0, f);
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
+                const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
+                if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
+                __syncwarp();
+                if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
+#pragma unroll
+                for (int t = 0; t < 2 * F::RT; ++t, ++o) {
+                    const uint32_t slot = o % F::kRaws;
+                    if (o >= F::kRaws) wait(raw_empty + slot, o / F::kRaws - 1);
+                    if (lane == 0) mbar_arrive_expect_tx(raw_full + slot, valid * 16 * F::RW);
+                    __syncwarp();
+                    if (id >= 0 && !dead)
+                        tma_load_4d(smem + F::off_raw + slot * F::kRaw + lane * 16 * F::RW, t < F::RT ? &kmap : &vmap,
+                                    (t % F::RT) * F::RW, tok, w.h, id, raw_full + slot);
+                    if (!dead) sent = o + 1;
+                }
+                if (j + 1 < w.j1) id = look(j + 1, f);
+            }
+        }
+        if (dead)  // the copies in flight: shared memory is theirs until they land
+            for (uint32_t x = sent > F::kRaws ? sent - F::kRaws : 0; x < sent; ++x)
+                (void)mbar_wait_bounded(raw_full + x % F::kRaws, (x / F::kRaws) & 1u, a.status);
+    } else if (warp == kSoftmaxWarps + kConvertWarps + 1) {
+        // ---------------------------------------------------------- MMAs
+        uint32_t o = 0, g = 0, qs = 0;  // operands, steps and queries taken
+        while (next_unit()) {
+            const int steps = w.j1 - w.j0;
+            const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn((w.nc + 63) / 64 * 64);
+            wait(q_full, qs);
+            for (int j = 0; j <= steps; ++j) {
+                if (j < steps) {
+                    const uint32_t ko = o + 2 * j, st = tmem + ((g + j) & 1) * 128;
+                    wait(op_full + ko % F::kOps, ko / F::kOps);
+                    fence_after();
+                    if (lane == 0 && !dead) {
+                        const uint64_t kb = operand_desc(smem_u32(smem + F::off_op + (ko % F::kOps) * F::kOp));
+#pragma unroll
+                        for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
+                            const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
+#pragma unroll
+                            for (int ks = 0; ks < DP / 16; ++ks)
+                                mma_ss(st, kb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                                       qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
+                                       p < QP - 1 || ks > 0 ? 1u : 0u);
+                        }
+                        commit_to(s_full + ((g + j) & 1));
+                        commit_to(op_empty + ko % F::kOps);
+                    }
+                    __syncwarp();
+                }
+                if (j > 0) {
+                    const uint32_t vo = o + 2 * j - 1;
+                    wait(op_full + vo % F::kOps, vo / F::kOps);
+                    wait(p_full, g + j - 1);
+                    fence_after();
+                    if (lane == 0 && !dead) {
+#pragma unroll
+                        for (int acc = 0; acc < F::DA; ++acc) {
+                            const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + (vo % F::kOps) * F::kOp + acc * 32768), 16384);
+#pragma unroll
+                            for (int p = PP - 1; p >= 0; --p) {
+                                const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + p * F::kPPart), 16384);
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / 16; ++ks)
+                                    mma_ss(o_at + acc * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
+                                           j > 1 || ks > 0 || p < PP - 1 ? 1u : 0u);
+                            }
+                        }
+                        commit_to(pv_done);
+                        commit_to(op_empty + vo % F::kOps);
+                    }
+                    __syncwarp();
+                }
+            }
+            o += 2 * steps;
+            g += steps;
+            ++qs;
+        }
+    } else if (warp >= kSoftmaxWarps) {
+        // ---------------------------------------------------------- 8 bits -> f16 operands
+        const int ct = tid - kSoftmaxWarps * 32;
+        uint32_t o = 0, r = 0, g = 0;  // operands, raw tiles and steps
+        while (next_unit()) {
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                const float4* sc = scales + (g % kScaleSteps) * 8;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++o) {
+                    const uint32_t os = o % F::kOps;
+                    if (o >= F::kOps) wait(op_empty + os, o / F::kOps - 1);
+                    unsigned char* op = smem + F::off_op + os * F::kOp;
+#pragma unroll
+                    for (int t = 0; t < F::RT; ++t, ++r) {
+                        const uint32_t rs = r % F::kRaws;
+                        wait(raw_full + rs, r / F::kRaws);
+                        const unsigned char* raw = smem + F::off_raw + rs * F::kRaw;
+                        constexpr int C16 = F::RW / 16;
+#pragma unroll 4
+                        for (int it = 0; it < C16; ++it) {
+                            const int item = it * 128 + ct, token = item / C16, c16 = item % C16;
+                            uint4 x = *reinterpret_cast<const uint4*>(raw + token * F::RW + c16 * 16);
+                            if (sc[token >> 4].z == 0.f) x = make_uint4(0, 0, 0, 0);
+                            uint32_t h[8];
+                            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) k_codes<INT8>(in[i], h[2 * i], h[2 * i + 1]);
+                            // two 16-byte chunks; lanes of the second 64 dims store theirs in the other order
+                            const bool flip = (c16 >> 2) & 1;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const bool second = (e == 1) != flip;
+                                const int ch = t * (F::RW / 8) + 2 * c16 + (second ? 1 : 0);
+                                *reinterpret_cast<uint4*>(op + (ch >> 3) * 16384 + token * 128 + (((ch & 7) ^ (token & 7)) << 4)) =
+                                    second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) arrive_on(raw_empty + rs);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_on(op_full + os);
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax, a thread a key and half of the columns
+        const int half = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wid = 2 + half;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t g = 0;
+        for (;; ++turn) {
+            const uint32_t slot = turn % kUnitsAhead;
+            wait(unit_full + slot, turn / kUnitsAhead);
+            // All warps go on or none: they meet at barriers below, whether their waits gave up or not.
+            if (any_of(1, kSoftmaxWarps * 32, dead || units[slot].tokens < 0)) break;
+            const volatile PrefixPiece& w = units[slot];
+            const int nc = w.nc, nh = nc / 2, c0 = half * nh, j0 = w.j0, j1 = w.j1;
+            {
+                // ---- queries: f16 parts of q * 2^e for the rows of this warp, and what belongs to each row
+                constexpr int QL = DP / 4 < 32 ? DP / 4 : 32, VL = DP / 4 / QL, QR = 32 / QL;  // lanes a row, vectors a lane
+                const int r_first = warp * (nc / 8), h = w.h, nrows = w.nrows, row_first = w.row_first;
+                const int64_t row0 = w.row0;
+                constexpr int NB = VL == 2 ? 2 : 4;  // reads on their way at a time
+#pragma unroll 1
+                for (int r0 = 0; r0 < nc / 8; r0 += NB * QR) {
+                    uint4 raw[NB][VL];
+                    int64_t to[NB];
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const int in = r0 + i * QR + lane / QL;
+                        const int r = row_first + r_first + in;
+                        const bool live = in < nc / 8 && r < nrows;
+                        const int i_row = r / a.group, hq = h * a.group + r - i_row * a.group;
+                        to[i] = live ? (row0 + i_row) * a.q_heads + hq : -1;
+                        const int64_t qat = (row0 + i_row) * a.q_row + hq * a.q_head;
+#pragma unroll
+                        for (int v = 0; v < VL; ++v) {
+                            const int d = (v * QL + lane % QL) * 4;
+                            raw[i][v] = load_q4(a.q, a.type, qat + d, live && d < c.dim);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const int in = r0 + i * QR + lane / QL;
+                        if (r0 + i * QR >= nc / 8) break;
+                        float amax = 0.f;
+                        float4 x[VL];
+#pragma unroll
+                        for (int v = 0; v < VL; ++v) {
+                            x[v] = q4_values(raw[i][v], a.type);
+                            amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[v].x)), fmaxf(fabsf(x[v].y), fabsf(x[v].z))), fabsf(x[v].w));
+                        }
+#pragma unroll
+                        for (int k = QL / 2; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
+                        // 2^e with amax * 2^e in [2^14, 2^15); 1 for zero or non-finite rows
+                        int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
+                        e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
+                        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                        if (in < nc / 8) {
+                            const int col = r_first + in;
+                            if (lane % QL == 0) {
+                                fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                                nm[col] = -kNoRef, pk[col] = 1.f, ref[col] = kNoRef, refd[col] = kNoOrder;
+                                top[col] = as_order(-INFINITY), topd[col] = kNoOrder;
+                                orow[col] = to[i];
+                            }
+#pragma unroll
+                            for (int v = 0; v < VL; ++v) {
+                                const int d = (v * QL + lane % QL) * 4, ch = d >> 3;
+                                // the dims in the order that k_codes gives a word's bytes
+                                const float y0 = x[v].x * up, y1 = (INT8 ? x[v].z : x[v].y) * up;
+                                const float y2 = (INT8 ? x[v].y : x[v].z) * up, y3 = x[v].w * up;
+                                const uint2 hi = make_uint2(pack_f16x2(y0, y1), pack_f16x2(y2, y3));
+                                unsigned char* dst = smem + (ch >> 3) * (NMAX * 128) + col * 128 + (((ch & 7) ^ (col & 7)) << 4) + (d & 4) * 2;
+                                *reinterpret_cast<uint2*>(dst) = hi;
+                                if (QP == 2)
+                                    *reinterpret_cast<uint2*>(dst + F::kQPart) = make_uint2(rest_f16x2(y0, y1, hi.x), rest_f16x2(y2, y3, hi.y));
+                            }
+                        }
+                    }
+                }
+                if (lane == 0 && quarter == 0) huge_half[half] = 0;
+                fence_proxy_async_smem();
+                sync_warps(1, kSoftmaxWarps * 32);
+                if (lane == 0) arrive_on(q_full);
+            }
+            float l[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) l[i] = 0.f;
+
+            for (int j = j0; j < j1; ++j, ++g) {
+                wait(sc_full + g % kScaleSteps, g / kScaleSteps);
+                wait(s_full + (g & 1), g >> 1);
+                fence_after();
+                const float4 mine = scales[(g % kScaleSteps) * 8 + (key >> 4)];
+                const float ks = mine.x, vs = mine.y;
+                const bool there = mine.z != 0.f, whole = __all_sync(~0u, there);
+                // vs < 2^evs
+                const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
+                const uint32_t st = tmem + (g & 1) * 128 + lanes;
+                unsigned char* prow = smem + F::off_p + key * 128;
+#pragma unroll
+                for (int cc = 0; cc < NH / 16; ++cc) {
+                    if (cc * 16 >= nh) break;
+                    const int cb = c0 + cc * 16;
+                    float p[16];
+                    uint32_t z[8], zl[PP == 2 ? 8 : 1];
+                    uint32_t s[16];
+                    // Probabilities of 16 columns under the references as they are; whether one passes them.
+                    auto attempt = [&](bool rounded) {
+                        tmem_load16(st + cb, s);
+                        tmem_loaded();
+                        float high = -INFINITY;
+                        uint32_t most = 0u;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 fa = *reinterpret_cast<const float4*>(fac + cb + 4 * q);
+                            const float4 na = *reinterpret_cast<const float4*>(nm + cb + 4 * q);
+                            const float4 ka = *reinterpret_cast<const float4*>(pk + cb + 4 * q);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int i = 2 * q + u;
+                                const f2 fq = fmul2(u ? f2{fa.z, fa.w} : f2{fa.x, fa.y}, f2{ks, ks});
+                                const f2 sv = {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])};
+                                f2 y = u ? f2{na.z, na.w} : f2{na.x, na.y};
+                                if (rounded) {
+                                    y.x = __fadd_rn(__fmul_rn(sv.x, fq.x), y.x);
+                                    y.y = __fadd_rn(__fmul_rn(sv.y, fq.y), y.y);
+                                } else {
+                                    ffma2(y, sv, fq);
+                                }
+                                if (!whole && !there) y.x = y.y = -INFINITY;
+                                high = fmaxf(high, fmaxf(y.x, y.y));
+                                const f2 e = {exp2_fast(y.x), exp2_fast(y.y)};
+                                p[2 * i] = e.x, p[2 * i + 1] = e.y;
+                                // p first: vs * 2^k may pass the range where p is 0
+                                const f2 zz = fmul2(fmul2(e, u ? f2{ka.z, ka.w} : f2{ka.x, ka.y}), f2{vs, vs});
+                                z[i] = pack_f16x2(zz.x, zz.y);
+                                if (PP == 2) zl[i % (PP == 2 ? 8 : 1)] = rest_f16x2(zz.x, zz.y, z[i]);
+                                most = hmax2_of(most, z[i]);
+                            }
+                        }
+                        return high > 20.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
+                    };
+                    bool huge = huge_half[half] != 0;
+                    bool passed = true;
+                    if (!huge) passed = any_of(wid, 128, attempt(false));
+                    if (cc == 0 && g > 0) wait(pv_done, g - 1);  // z and O are this step's now
+                    if (passed) {
+                        // ---- new references of these columns (row kernel's), by all four warps
+                        fence_after();
+                        tmem_load16(st + cb, s);
+                        tmem_loaded();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float score = __fmul_rn(__uint_as_float(s[i]), fac[cb + i] * ks);
+                            p[i] = there && score == score ? ceilf(score) : -INFINITY;
+                            const int best = __reduce_max_sync(~0u, as_order(p[i]));
+                            if (lane == 0) atomicMax(top + cb + i, best);
+                        }
+                        sync_warps(wid, 128);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float mn = fmaxf(ref[cb + i], from_order(top[cb + i]));
+                            const int best = __reduce_max_sync(~0u, order_of(p[i] - mn) + evs);
+                            if (lane == 0) atomicMax(topd + cb + i, best);
+                        }
+                        sync_warps(wid, 128);
+                        if (quarter == 0 && lane < 16) {
+                            const int col = cb + lane;
+                            const float m = ref[col], mn = fmaxf(m, from_order(top[col]));
+                            const int down = order_of(m - mn), d = refd[col];
+                            const int dn = max(max(d + down, kNoOrder), topd[col]);
+                            const int k_old = min(12 - d, kMostK), k_new = min(12 - dn, kMostK);
+                            mul1[col] = pow2i(k_new - k_old + down);
+                            mul2[col] = pow2i(down);
+                            ref[col] = mn, nm[col] = -mn, refd[col] = dn;
+                            pk[col] = pow2i(max(k_new, -126));
+                            top[col] = as_order(-INFINITY), topd[col] = kNoOrder;
+                            if (mn > kNoRef && fabsf(mn) >= kHugeScore) huge_half[half] = 1;
+                        }
+                        sync_warps(wid, 128);
+                        huge = huge_half[half] != 0;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) l[cc * 16 + i] *= mul2[cb + i];
+                        if (j > j0) {
+#pragma unroll
+                            for (int acc = 0; acc < F::DA; ++acc) {
+                                tmem_load16(o_at + acc * F::NP + lanes + cb, s);
+                                tmem_loaded();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * mul1[cb + i]);
+                                tmem_store16(o_at + acc * F::NP + lanes + cb, s);
+                            }
+                            tmem_stored();
+                        }
+                        (void)attempt(huge);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) l[cc * 16 + i] += p[i];
+                    unsigned char* dst = prow + (cb >> 6) * 16384;
+                    const int ch = (cb & 63) >> 3;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        unsigned char* at = dst + (((ch + u) ^ (key & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]);
+                        if (PP == 2)
+                            *reinterpret_cast<uint4*>(at + F::kPPart) =
+                                make_uint4(zl[(4 * u) % (PP == 2 ? 8 : 1)], zl[(4 * u + 1) % (PP == 2 ? 8 : 1)],
+                                           zl[(4 * u + 2) % (PP == 2 ? 8 : 1)], zl[(4 * u + 3) % (PP == 2 ? 8 : 1)]);
+                    }
+                }
+                fence_proxy_async_smem();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_on(p_full);
+            }
+
+            // ---- the rows' sums, then their results
+#pragma unroll
+            for (int x = 0; x < (NH + 31) / 32; ++x) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = x * 32 + i < NH && x * 32 + i < nh ? l[(x * 32 + i) % NH] : 0.f;
+                const float sum = add_columns(v);
+                if (x * 32 + lane < nh) sums[quarter * NMAX + c0 + x * 32 + lane] = sum;
+            }
+            sync_warps(wid, 128);
+            float* part = a.slots + static_cast<int64_t>(w.slot < 0 ? 0 : w.slot) * (NMAX * (DP + 2));
+            const bool begins = w.slot < 0;
+            if (key < nh) {
+                const int col = c0 + key;
+                const float sum = (sums[col] + sums[NMAX + col]) + (sums[2 * NMAX + col] + sums[3 * NMAX + col]);
+                // NaN sums stay NaN; a row that saw nothing has a sum of 0
+                const bool none = sum == 0.f && ref[col] == kNoRef;
+                const int down = none ? 0 : -min(12 - refd[col], kMostK);
+                mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down >> 1);
+                mul2[col] = pow2i(down - (down >> 1));
+                const float m = none ? -INFINITY : ref[col];
+                if (begins) {
+                    if (orow[col] >= 0)
+                        a.own_ml[orow[col]] = make_float4(m, sum, __int_as_float(static_cast<int>(blockIdx.x) + 1),
+                                                          __int_as_float(w.extra | col << 16));
+                } else {
+                    *reinterpret_cast<float2*>(part + NMAX * DP + 2 * col) = make_float2(m, sum);
+                }
+            }
+            wait(pv_done, g - 1);
+            fence_after();
+            sync_warps(wid, 128);
+            const int place = INT8 ? (lane & ~3) | ((lane & 1) << 1 | (lane & 2) >> 1) : lane;  // dims as k_codes orders them
+#pragma unroll
+            for (int acc = 0; acc < F::DA; ++acc) {
+                const int d = acc * 128 + quarter * 32 + place;
+                for (int cb = c0; cb < c0 + nh; cb += 16) {
+                    uint32_t v[16];
+                    tmem_load16(o_at + acc * F::NP + lanes + cb, v);
+                    tmem_loaded();
+                    if (d < c.dim) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __uint_as_float(v[i]) * mul1[cb + i] * mul2[cb + i];
+                            const int64_t to = orow[cb + i];
+                            if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = mul1[cb + i] == 0.f ? 0.f : x;
+                        }
+                    }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_on(unit_empty + slot);
+            sync_warps(1, kSoftmaxWarps * 32);  // all have left the columns' data
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kSoftmaxWarps + kConvertWarps + 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <int DP, int QP, int PP, bool INT8>
+int launch_one(AttnArgs& a, cudaStream_t s) {
+    using F = XShape<DP, QP, PP>;
+    const int dev = current_device();
+    const int sms = sm_count(dev);
+    if (sms <= 0) return cuda_fail(cudaGetLastError());
+    CUtensorMap kmap, vmap;
+    if (!encode_cache(&kmap, a.c, a.c.k, F::RW, 16, false) || !encode_cache(&vmap, a.c, a.c.v, F::RW, 16, false))
+        return cuda_fail(cudaGetLastError());
+    static std::atomic<bool> done[64];
+    auto kern = qg_attn_prefix_kernel<DP, QP, PP, INT8>;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem) != cudaSuccess)
+            return cuda_fail(cudaGetLastError());
+        done[dev].store(true, std::memory_order_release);
+    }
+    a.slot_rows = F::NMAX, a.slot_dims = DP;
+    kern<<<std::min(sms, kMaxPrefixCtas), kPrefixThreads, F::smem, s>>>(a, kmap, vmap);
+    return launch_status();
+}
+
+template <int QP, int PP, bool INT8>
+int launch_typed(AttnArgs& a, cudaStream_t s) {
+    if (a.c.dim <= 64) return launch_one<64, QP, PP, INT8>(a, s);
+    return a.c.dim <= 128 ? launch_one<128, QP, PP, INT8>(a, s) : launch_one<256, QP, PP, INT8>(a, s);
+}
+
+}  // namespace
+
+template <bool INT8>
+int launch_prefix(AttnArgs& a, cudaStream_t s) {
+    if (a.type == QGKV_F32) return launch_typed<2, 2, INT8>(a, s);
+    // f16 outputs round as finely as one f16 part of p would: two
+    if (a.type == QGKV_F16) return launch_typed<1, 2, INT8>(a, s);
+    return launch_typed<1, 1, INT8>(a, s);
+}
+
+}  // namespace qg

@@ -61,9 +61,8 @@ constexpr int kMaxCtas = 640;     // partial slots: 2 per CTA
 constexpr int kPartFloats = 2048 + 32;  // rows * dims of a partial, then its references and sums
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials exceed the workspace");
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
-static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsOwn - kWsPart, "partials meet the results kept for a join");
+static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsSlots - kWsPart, "partials meet a prefix's results");
 
-constexpr int kMostK = 124;  // of k: p * 2^k stays finite, p being 4 at most
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
 
 // What the template arguments fix: DC chunks of 64 dims.
@@ -88,8 +87,54 @@ struct Shape {
     static constexpr int off_pre(int parts) { return off_bar(parts) + 4 * S * 8; }
 };
 
-// QP, PP: f16 parts of q and of p.  SHARED: a prefix or what is behind it
-// (shared_sequence), whose results are kept for a join.
+// Adds a prefix's results to those of a row's own tokens: `top` its reference
+// (-inf: no token), `sum` and the normalised dims of this lane.  The launch that wrote
+// them has ended (griddepcontrol.wait).
+template <int XV>
+__device__ __forceinline__ void join_prefix(const AttnArgs& a, int64_t to, int row_lane, float& top, float& sum, float4 (&acc)[XV]) {
+    grid_dependency_wait();
+    const float4 first = __ldcg(a.own_ml + to);
+    const int cta = __float_as_int(first.z), row = __float_as_int(first.w) >> 16;
+    int more = __float_as_int(first.w) & 0xFFFF;
+    if (cta < 1 || more > kMaxPrefixCtas - cta || row < 0 || row >= a.slot_rows) {  // no plan of this call
+        if (more) atomicOr(a.status, kStatusBounds);
+        more = 0;
+    }
+    const int64_t stride = static_cast<int64_t>(a.slot_rows) * (a.slot_dims + 2);
+    const float* parts = a.slots + (more ? cta * stride + static_cast<int64_t>(row) * a.slot_dims : 0);
+    const float2* ml = reinterpret_cast<const float2*>(a.slots + (more ? cta * stride + static_cast<int64_t>(a.slot_rows) * a.slot_dims : 0)) + row;
+    float best = fmaxf(top, first.x);
+#pragma unroll 8
+    for (int i = 0; i < more; ++i) best = fmaxf(best, __ldcg(ml + i * (stride / 2)).x);
+    const float ref = best == -INFINITY ? 0.f : best;
+    const float mine = exp2_fast(top - ref) * sum;
+    float total = mine;
+    float4 o[XV];
+#pragma unroll
+    for (int x = 0; x < XV; ++x)
+        o[x] = make_float4(mine * acc[x].x, mine * acc[x].y, mine * acc[x].z, mine * acc[x].w);
+    auto add = [&](float2 p, const float* from) {
+        const float w = exp2_fast(p.x - ref) * p.y;
+        total += w;
+#pragma unroll
+        for (int x = 0; x < XV; ++x) {
+            const int d = 4 * (row_lane + 32 * x);
+            if (d >= a.c.dim) break;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + d));
+            o[x].x += w * v.x, o[x].y += w * v.y, o[x].z += w * v.z, o[x].w += w * v.w;
+        }
+    };
+    add(make_float2(first.x, first.y), a.own + to * a.c.dim);
+#pragma unroll 4
+    for (int i = 0; i < more; ++i) add(__ldcg(ml + i * (stride / 2)), parts + i * stride);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int x = 0; x < XV; ++x) acc[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
+    top = best, sum = total;
+}
+
+// QP, PP: f16 parts of q and of p.  SHARED: a sequence's tokens behind those that
+// its group shares; the prefix's results, of the launch before, are joined at the end.
 template <int DC, int MT, int QP, int PP, bool INT8, int MINB, bool SHARED>
 __global__ void __launch_bounds__(kThreads, MINB)
 qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -132,7 +177,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             const int b = b0 + tid;
             int64_t x = 0;
             if (b < a.batch) {
-                const Seq s = SHARED ? shared_sequence(a, b).s : sequence(a, b);
+                Seq s = sequence(a, b);
+                if (SHARED) shared_columns(a, b, s);
                 const int64_t blocks = (static_cast<int64_t>(s.n) * a.group + RU - 1) / RU;
                 x = blocks * c.heads * max(1, (s.len + kTile - 1) / kTile);
                 seqs[b] = make_int2(s.n, s.len);
@@ -154,7 +200,10 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     }
     const Line line(pre[a.batch], grid);
     const int cta = blockIdx.x;
-    if (cta >= line.ctas) return;
+    if (cta >= line.ctas) {
+        if (SHARED) grid_dependency_wait();
+        return;
+    }
     const int64_t u_begin = line.first(cta), u_end = line.first(cta + 1);
 
     int64_t u = u_begin;
@@ -168,16 +217,14 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         // empty sequences share their successor's prefix: take the last with pre <= u that has tiles
         const int b = lo;
         const Seq sq = {seqs[b].x, seqs[b].y};
-        int64_t row0 = a.starts ? a.starts[b] : b;
+        const int64_t row0 = a.starts ? a.starts[b] : b;
         const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
-        bool causal = true, partial = false;  // partial: the result is kept for a join
+        bool behind = false;  // a prefix
         if (SHARED) {
-            const SharedSeq sh = shared_sequence(a, b);
-            row0 = sh.row0, partial = sh.partial, causal = !a.prefix;
-            row_table = a.table + sh.table_row * a.width + sh.col;
+            const int skip = a.skip[b];
+            behind = skip > 0 && a.lens[b] - skip == sq.len;
+            if (behind) row_table += skip >> c.log2p;
         }
-        // tokens that row i of the sequence sees
-        auto sees = [&](int i) { return !SHARED || causal ? sq.len - sq.n + i + 1 : sq.len; };
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];
@@ -190,8 +237,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         const int row_first = rb * RU;
         // tokens that the block's last row sees
         const int i_last = min(row_first + RU, nrows) - 1;
-        const int seen_most = sees(i_last / a.group);
-        const int seen_least = sees(row_first / a.group);
+        const int seen_most = sq.len - sq.n + i_last / a.group + 1;
+        const int seen_least = sq.len - sq.n + row_first / a.group + 1;
         const int tok0 = tile0 * kTile;
         const int tok1 = min((tile0 + seg) * kTile, seen_most);
         const int full_end = min(seen_least, tok1);  // up to here every row sees every token
@@ -275,7 +322,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         if (tid < RU) {
             const int r = row_first + tid, i_row = r / a.group;
             orow[tid] = r < nrows ? (row0 + i_row) * a.q_heads + h * a.group + r - i_row * a.group : -1;
-            limits[tid] = r < nrows ? sees(i_row) : 0;
+            limits[tid] = r < nrows ? sq.len - sq.n + i_row + 1 : 0;
         }
         float4 x[MT][DC];
 #pragma unroll
@@ -675,27 +722,32 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
             const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = exp2_fast(w[i] - ref) * wl[i * RU + r];  // 0 for a warp without tokens, whose result is 0
-            const float sum = w[0] + w[1] + w[2] + w[3];
+            float sum = w[0] + w[1] + w[2] + w[3], top = mx;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float4 acc[XV];
+#pragma unroll
+            for (int x2 = 0; x2 < XV; ++x2) {
+                const int d = 4 * (row_lane + 32 * x2);
+                acc[x2] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (d >= c.dim) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(wo + i * kWarpFloats + r * DP + d);
+                    acc[x2].x += w[i] * v.x, acc[x2].y += w[i] * v.y, acc[x2].z += w[i] * v.z, acc[x2].w += w[i] * v.w;
+                }
+                acc[x2].x *= inv, acc[x2].y *= inv, acc[x2].z *= inv, acc[x2].w *= inv;
+            }
+            if (SHARED && whole && behind) join_prefix<XV>(a, to, row_lane, top, sum, acc);
 #pragma unroll
             for (int x2 = 0; x2 < XV; ++x2) {
                 const int d = 4 * (row_lane + 32 * x2);
                 if (d >= c.dim) break;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(wo + i * kWarpFloats + r * DP + d);
-                    acc.x += w[i] * v.x, acc.y += w[i] * v.y, acc.z += w[i] * v.z, acc.w += w[i] * v.w;
-                }
-                acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-                if (SHARED && whole && partial) store_out4(a.own, QGKV_F32, to * c.dim + d, acc);
-                else if (whole) store_out4(a.out, a.type, to * c.dim + d, acc);
-                else *reinterpret_cast<float4*>(part + r * c.dim + d) = acc;
+                if (whole) store_out4(a.out, a.type, to * c.dim + d, acc[x2]);
+                else *reinterpret_cast<float4*>(part + r * c.dim + d) = acc[x2];
             }
             if (row_lane == 0) {
                 if (!whole) part[2048 + r] = mx, part[2048 + 16 + r] = sum;
-                else if (SHARED && partial) a.own_ml[to] = make_float2(mx, sum);
-                else if (a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+                else if (a.lse) a.lse[to] = sum == 0.f ? -INFINITY : ((SHARED && top != -INFINITY ? top : ref) + log2f(sum)) * 0.69314718055994531f;
             }
         }
         if (!whole) {
@@ -776,23 +828,25 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
                     for (int o2 = LPR / 2; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(~0u, sum, o2);
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    float join_top = mx;
+#pragma unroll
+                    for (int x2 = 0; x2 < XV; ++x2)
+                        acc[x2].x *= inv, acc[x2].y *= inv, acc[x2].z *= inv, acc[x2].w *= inv;
+                    if (SHARED && behind && live) join_prefix<XV>(a, to[i], row_lane, join_top, sum, acc);
 #pragma unroll
                     for (int x2 = 0; x2 < XV; ++x2) {
                         const int d = 4 * (row_lane + 32 * x2);
-                        if (live && d < c.dim)
-                            store_out4(SHARED && partial ? a.own : a.out, SHARED && partial ? QGKV_F32 : a.type,
-                                       to[i] * c.dim + d,
-                                       make_float4(acc[x2].x * inv, acc[x2].y * inv, acc[x2].z * inv, acc[x2].w * inv));
+                        if (live && d < c.dim) store_out4(a.out, a.type, to[i] * c.dim + d, acc[x2]);
                     }
-                    if (SHARED && partial) {
-                        if (live && row_lane == 0) a.own_ml[to[i]] = make_float2(mx, sum);
-                    } else if (live && row_lane == 0 && a.lse)
-                        a.lse[to[i]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+                    if (live && row_lane == 0 && a.lse)
+                        a.lse[to[i]] = sum == 0.f ? -INFINITY
+                                                  : ((SHARED && join_top != -INFINITY ? join_top : ref) + log2f(sum)) * 0.69314718055994531f;
                 }
             }
         }
         u += seg;
     }
+    if (SHARED) grid_dependency_wait();  // no launch behind this one meets the one before
 }
 
 template <int DC, int MT, int QP, int PP, bool INT8, int MINB, bool SHARED>
@@ -815,7 +869,23 @@ int launch_one(const AttnArgs& a, cudaStream_t s) {
         done[dev].store(true, std::memory_order_release);
     }
     const int grid = std::min(sms * MINB, kMaxCtas);
-    kern<<<grid, kThreads, fixed + (a.batch + 1) * 16, s>>>(a, kmap, vmap, grid);
+    const int bytes = fixed + (a.batch + 1) * 16;
+    if (!SHARED) {
+        kern<<<grid, kThreads, bytes, s>>>(a, kmap, vmap, grid);
+        return launch_status();
+    }
+    // beside the launch of the prefix, as its CTAs end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a, kmap, vmap, grid) != cudaSuccess) return cuda_fail(cudaGetLastError());
     return launch_status();
 }
 

@@ -1,4 +1,4 @@
-// The row kernel for a shared prefix and what is behind it, e4m3 codes; the launcher for both formats.
+// The row kernel for what is behind a shared prefix, e4m3 codes; the launcher for both formats.
 #include "kv_rows.cuh"
 
 namespace qg {

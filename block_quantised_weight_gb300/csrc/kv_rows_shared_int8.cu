@@ -1,4 +1,4 @@
-// The row kernel for a shared prefix and what is behind it, int8 codes.
+// The row kernel for what is behind a shared prefix, int8 codes.
 #include "kv_rows.cuh"
 
 namespace qg {
