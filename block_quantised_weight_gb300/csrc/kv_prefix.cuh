@@ -13,9 +13,12 @@
 // transposed: both are converted as they lie, K K-major, V M-major.  A thread has one
 // key: its scales are scalars of the thread, and what belongs to a query row (factor,
 // references) comes from shared memory, four at a time.  References are whole
-// numbers, shared by the four warps of a half of the columns, and move only when a z
-// would pass 2^15 or a p 2^20; 16 columns at a time are tried as if they held, one
-// vote of the four warps decides.
+// numbers, shared by the four warps of a half of the columns; they are set in a piece's
+// first step, so that z is at most 2^6 (k = 6 less the order of p * vs), and move
+// only when a z would pass 2^15 or a p 2^20: 16 columns at a time are tried as
+// if they held, one vote of the four warps decides.  Two parts of z: the second is 2^11
+// times what the first leaves, with sums of its own, so that small weights keep their
+// bits down to 2^-40 of a row's largest (one part: 2^-29).
 //
 // Bound.  For up to 128 rows the codes' stream (32 KB a step and SM at 128 dims) takes as long as the
 // exponentials of 128 rows (16 a clock and SM); short calls are bound by the chain
@@ -42,6 +45,7 @@ constexpr int kKeys = 128;
 constexpr int kLeastSteps = 2;      // of a CTA's share of the line
 constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
 constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
+constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kPrefixThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 
@@ -67,8 +71,9 @@ struct XShape {
     static_assert(kFit >= 1, "shared memory");
     static constexpr int off_scale = off_raw + static_cast<int>(kRaws) * kRaw;
     static constexpr int off_cols = off_scale + static_cast<int>(kScaleSteps) * 8 * 16;
-    static constexpr int off_bar = off_cols + NMAX * (9 * 4 + 4 * 4 + 8);
+    static constexpr int off_bar = off_cols + NMAX * (7 * 4 + 8 * 4 + 8);
     static constexpr int smem = off_bar + 512;
+    static_assert(PP * DA * NP <= 256, "tensor memory");
     static_assert(smem <= 232448 && off_cols % 16 == 0 && off_bar % 8 == 0, "shared memory");
 };
 
@@ -148,13 +153,6 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
     return r != 0;
 }
 
-// Order of floats as integers, and back.
-__device__ __forceinline__ int as_order(float x) {
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float from_order(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
-
 __device__ __forceinline__ uint32_t hmax2_of(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -174,6 +172,19 @@ __device__ __forceinline__ float add_columns(float (&v)[32]) {
     return v[0];
 }
 
+// Largest of each of 16 columns over the 32 lanes: lanes i and i + 16 get that of column i.
+__device__ __forceinline__ float max_columns(float (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float give = lane & w ? v[i] : v[i + w], keep = lane & w ? v[i + w] : v[i];
+            v[i] = fmaxf(keep, __shfl_xor_sync(~0u, give, w));
+        }
+    return fmaxf(v[0], __shfl_xor_sync(~0u, v[0], 16));
+}
+
 template <int DP, int QP, int PP, bool INT8>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
 qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -189,10 +200,9 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     float* mul2 = mul1 + NMAX;
     float* ref = mul2 + NMAX;
     int* refd = reinterpret_cast<int*>(ref + NMAX);
-    int* top = refd + NMAX;
-    int* topd = top + NMAX;
-    float* sums = reinterpret_cast<float*>(topd + NMAX);              // [4][NMAX]
-    int64_t* orow = reinterpret_cast<int64_t*>(sums + 4 * NMAX);      // output rows, -1 past the last
+    float* tops = reinterpret_cast<float*>(refd + NMAX);  // [4][NMAX] by warp: largest scores, later sums
+    float* tops_v = tops + 4 * NMAX;                      // [4][NMAX] with the orders of vs
+    int64_t* orow = reinterpret_cast<int64_t*>(tops_v + 4 * NMAX);  // output rows, -1 past the last
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
     uint64_t* raw_empty = raw_full + F::kRaws;
     uint64_t* op_full = raw_empty + F::kRaws;
@@ -237,7 +247,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t o_at = tmem + 256;  // S^T: two buffers of 128 columns; O^T: F::DA of F::NP
+    const uint32_t o_at = tmem + 256;  // S^T: two buffers of 128 columns; O^T: F::DA of F::NP for each part of z
     // A wait that gave up ends all further waits, copies and MMAs of its warp:
     // the kernel then runs to its end within a few wait limits.
     bool dead = false;
@@ -379,8 +389,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + p * F::kPPart), 16384);
 #pragma unroll
                                 for (int ks = 0; ks < kKeys / 16; ++ks)
-                                    mma_ss(o_at + acc * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
-                                           j > 1 || ks > 0 || p < PP - 1 ? 1u : 0u);
+                                    mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
+                                           j > 1 || ks > 0 ? 1u : 0u);
                             }
                         }
                         commit_to(pv_done);
@@ -497,7 +507,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             if (lane % QL == 0) {
                                 fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                                 nm[col] = -kNoRef, pk[col] = 1.f, ref[col] = kNoRef, refd[col] = kNoOrder;
-                                top[col] = as_order(-INFINITY), topd[col] = kNoOrder;
                                 orow[col] = to[i];
                             }
 #pragma unroll
@@ -535,6 +544,59 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
                 const uint32_t st = tmem + (g & 1) * 128 + lanes;
                 unsigned char* prow = smem + F::off_p + key * 128;
+                // Partial maxima of 16 columns from cb on: the scores', rounded up to whole orders, and with those of
+                // vs; `base` 0, or the references that are taken off first (huge scores, whose sums with an order do
+                // not hold it).
+                auto maxima = [&](int cb, bool based) {
+                    uint32_t s[16];
+                    float t[16], u[16];
+                    tmem_load16(st + cb, s);
+                    tmem_loaded();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float score = __fmul_rn(__uint_as_float(s[i]), fac[cb + i] * ks);
+                        t[i] = there && score == score ? ceilf(score) : -INFINITY;
+                        u[i] = fmaxf(t[i] - (based ? ref[cb + i] : 0.f), -INFINITY) + static_cast<float>(evs);
+                    }
+                    const float a = max_columns(t), b = max_columns(u);
+                    if (lane < 16) {
+                        if (!based) tops[quarter * NMAX + cb + lane] = a;
+                        tops_v[quarter * NMAX + cb + lane] = b;
+                    }
+                };
+                auto largest = [&](const float* of, int col) {
+                    return fmaxf(fmaxf(of[col], of[NMAX + col]), fmaxf(of[2 * NMAX + col], of[3 * NMAX + col]));
+                };
+                auto references = [&](int cb, int n) {  // new ones for n columns, by all four warps
+                    for (int x = cb; x < cb + n; x += 16) maxima(x, false);
+                    sync_warps(wid, 128);
+                    const int col = cb + key;
+                    int down = 0;
+                    if (key < n) {
+                        const float m = ref[col], mn = fmaxf(m, largest(tops, col));
+                        down = order_of(m - mn);
+                        ref[col] = mn, nm[col] = -mn;
+                        if (mn > kNoRef && fabsf(mn) >= kHugeScore) huge_half[half] = 1;
+                    }
+                    sync_warps(wid, 128);
+                    const bool huge = huge_half[half] != 0;
+                    if (huge) {
+                        for (int x = cb; x < cb + n; x += 16) maxima(x, true);
+                        sync_warps(wid, 128);
+                    }
+                    if (key < n) {
+                        const int d = refd[col];
+                        const float high = largest(tops_v, col);
+                        const int dn = max(max(d + down, kNoOrder), order_of(huge ? high : high - ref[col]));
+                        const int k_old = min(kBase - d, kMostK), k_new = min(kBase - dn, kMostK);
+                        mul1[col] = pow2i(k_new - k_old + down);
+                        mul2[col] = pow2i(down);
+                        refd[col] = dn;
+                        pk[col] = pow2i(max(k_new, -126));
+                    }
+                    sync_warps(wid, 128);
+                };
+                if (j == j0) references(c0, nh);
 #pragma unroll
                 for (int cc = 0; cc < NH / 16; ++cc) {
                     if (cc * 16 >= nh) break;
@@ -572,7 +634,10 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 // p first: vs * 2^k may pass the range where p is 0
                                 const f2 zz = fmul2(fmul2(e, u ? f2{ka.z, ka.w} : f2{ka.x, ka.y}), f2{vs, vs});
                                 z[i] = pack_f16x2(zz.x, zz.y);
-                                if (PP == 2) zl[i % (PP == 2 ? 8 : 1)] = rest_f16x2(zz.x, zz.y, z[i]);
+                                if (PP == 2) {  // 2^11 times what the first part leaves
+                                    const f2 hi = h2_to_f2(z[i]);
+                                    zl[i % (PP == 2 ? 8 : 1)] = pack_f16x2((zz.x - hi.x) * 2048.f, (zz.y - hi.y) * 2048.f);
+                                }
                                 most = hmax2_of(most, z[i]);
                             }
                         }
@@ -583,45 +648,14 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     if (!huge) passed = any_of(wid, 128, attempt(false));
                     if (cc == 0 && g > 0) wait(pv_done, g - 1);  // z and O are this step's now
                     if (passed) {
-                        // ---- new references of these columns (row kernel's), by all four warps
                         fence_after();
-                        tmem_load16(st + cb, s);
-                        tmem_loaded();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float score = __fmul_rn(__uint_as_float(s[i]), fac[cb + i] * ks);
-                            p[i] = there && score == score ? ceilf(score) : -INFINITY;
-                            const int best = __reduce_max_sync(~0u, as_order(p[i]));
-                            if (lane == 0) atomicMax(top + cb + i, best);
-                        }
-                        sync_warps(wid, 128);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float mn = fmaxf(ref[cb + i], from_order(top[cb + i]));
-                            const int best = __reduce_max_sync(~0u, order_of(p[i] - mn) + evs);
-                            if (lane == 0) atomicMax(topd + cb + i, best);
-                        }
-                        sync_warps(wid, 128);
-                        if (quarter == 0 && lane < 16) {
-                            const int col = cb + lane;
-                            const float m = ref[col], mn = fmaxf(m, from_order(top[col]));
-                            const int down = order_of(m - mn), d = refd[col];
-                            const int dn = max(max(d + down, kNoOrder), topd[col]);
-                            const int k_old = min(12 - d, kMostK), k_new = min(12 - dn, kMostK);
-                            mul1[col] = pow2i(k_new - k_old + down);
-                            mul2[col] = pow2i(down);
-                            ref[col] = mn, nm[col] = -mn, refd[col] = dn;
-                            pk[col] = pow2i(max(k_new, -126));
-                            top[col] = as_order(-INFINITY), topd[col] = kNoOrder;
-                            if (mn > kNoRef && fabsf(mn) >= kHugeScore) huge_half[half] = 1;
-                        }
-                        sync_warps(wid, 128);
+                        references(cb, 16);
                         huge = huge_half[half] != 0;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) l[cc * 16 + i] *= mul2[cb + i];
                         if (j > j0) {
 #pragma unroll
-                            for (int acc = 0; acc < F::DA; ++acc) {
+                            for (int acc = 0; acc < PP * F::DA; ++acc) {
                                 tmem_load16(o_at + acc * F::NP + lanes + cb, s);
                                 tmem_loaded();
 #pragma unroll
@@ -659,17 +693,17 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = x * 32 + i < NH && x * 32 + i < nh ? l[(x * 32 + i) % NH] : 0.f;
                 const float sum = add_columns(v);
-                if (x * 32 + lane < nh) sums[quarter * NMAX + c0 + x * 32 + lane] = sum;
+                if (x * 32 + lane < nh) tops[quarter * NMAX + c0 + x * 32 + lane] = sum;
             }
             sync_warps(wid, 128);
             float* part = a.slots + static_cast<int64_t>(w.slot < 0 ? 0 : w.slot) * (NMAX * (DP + 2));
             const bool begins = w.slot < 0;
             if (key < nh) {
                 const int col = c0 + key;
-                const float sum = (sums[col] + sums[NMAX + col]) + (sums[2 * NMAX + col] + sums[3 * NMAX + col]);
+                const float sum = (tops[col] + tops[NMAX + col]) + (tops[2 * NMAX + col] + tops[3 * NMAX + col]);
                 // NaN sums stay NaN; a row that saw nothing has a sum of 0
                 const bool none = sum == 0.f && ref[col] == kNoRef;
-                const int down = none ? 0 : -min(12 - refd[col], kMostK);
+                const int down = none ? 0 : -min(kBase - refd[col], kMostK);
                 mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down >> 1);
                 mul2[col] = pow2i(down - (down >> 1));
                 const float m = none ? -INFINITY : ref[col];
@@ -689,13 +723,16 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             for (int acc = 0; acc < F::DA; ++acc) {
                 const int d = acc * 128 + quarter * 32 + place;
                 for (int cb = c0; cb < c0 + nh; cb += 16) {
-                    uint32_t v[16];
+                    uint32_t v[16], vl[16];
                     tmem_load16(o_at + acc * F::NP + lanes + cb, v);
+                    if (PP == 2) tmem_load16(o_at + (F::DA + acc) * F::NP + lanes + cb, vl);
                     tmem_loaded();
                     if (d < c.dim) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float x = __uint_as_float(v[i]) * mul1[cb + i] * mul2[cb + i];
+                            float x = __uint_as_float(v[i]);
+                            if (PP == 2) x = fmaf(__uint_as_float(vl[i]), 0x1p-11f, x);
+                            x = x * mul1[cb + i] * mul2[cb + i];
                             const int64_t to = orow[cb + i];
                             if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = mul1[cb + i] == 0.f ? 0.f : x;
                         }

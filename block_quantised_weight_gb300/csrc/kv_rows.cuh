@@ -63,6 +63,7 @@ static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsPartBytes, "partials
 static_assert(kMaxCtas <= kCntPages, "counters overlap");
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsSlots - kWsPart, "partials meet a prefix's results");
 
+constexpr int kUncut = 6;    // tiles that the longest sequence may be above a CTA's share and stay whole
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
 
 // What the template arguments fix: DC chunks of 64 dims.
@@ -205,6 +206,15 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         return;
     }
     const int64_t u_begin = line.first(cta), u_end = line.first(cta + 1);
+    // Behind a prefix sequences are short, and beginning and joining a piece costs as
+    // much as some tiles: where the longest is hardly longer than a CTA's share,
+    // none is cut, and a CTA takes those whose first tile lies in its share.
+    bool uncut = false;
+    if (SHARED) {
+        int longest = 0;
+        for (int b = tid; b < a.batch; b += kThreads) longest = max(longest, seqs[b].y);
+        uncut = __syncthreads_or((longest + kTile - 1) / kTile > line.each + kUncut) == 0;
+    }
 
     int64_t u = u_begin;
     while (u < u_end) {
@@ -230,9 +240,13 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         const int64_t in = u - pre[b];
         const int hb = static_cast<int>(div64(in, tiles));
         const int tile0 = static_cast<int>(in - static_cast<int64_t>(hb) * tiles);
+        if (SHARED && uncut && tile0) {  // another CTA's
+            u += tiles - tile0;
+            continue;
+        }
         const int h = hb / blocks, rb = hb - h * blocks;
         const int64_t span0 = u - tile0;
-        const int seg = static_cast<int>(min(static_cast<int64_t>(tiles - tile0), u_end - u));
+        const int seg = SHARED && uncut ? tiles : static_cast<int>(min(static_cast<int64_t>(tiles - tile0), u_end - u));
         const int nrows = sq.n * a.group;
         const int row_first = rb * RU;
         // tokens that the block's last row sees
