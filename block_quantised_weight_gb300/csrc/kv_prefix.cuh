@@ -2,7 +2,7 @@
 // same tokens, each read once, on the tcgen05 tensor cores.
 //
 // Mathematics: kv_rows.cuh's, with both products transposed.  A CTA takes up to NMAX
-// query rows (tokens x heads of a group, a multiple of 32) of one cache head and
+// query rows (tokens x heads of a group, a multiple of 16) of one cache head and
 // walks the keys in steps of 128:
 //   S^T = K q^T     128 keys x rows, in tensor memory
 //   p = 2^(S f - m), f = scale * ks,   z = p * vs * 2^k as f16, in shared memory
@@ -13,7 +13,7 @@
 // transposed: both are converted as they lie, K K-major, V M-major.  A thread has one
 // key: its scales are scalars of the thread, and what belongs to a query row (factor,
 // references) comes from shared memory, four at a time.  References are whole
-// numbers, shared by the four warps of a half of the columns; they are set in a piece's
+// numbers, shared by the four warps that hold the keys; they are set in a piece's
 // first step, so that z is at most 2^6 (k = 6 less the order of p * vs), and move
 // only when a z would pass 2^15 or a p 2^20: 16 columns at a time are tried as
 // if they held, one vote of the four warps decides.  Two parts of z: the second is 2^11
@@ -29,8 +29,8 @@
 // others in a slot of their CTA; the row kernel adds them to what lies behind the
 // prefix (own_ml of a row names the CTA of the first further piece and their number).
 //
-// Roles: eight warps for the softmax (two halves of the columns), four convert
-// the codes, one copies, one issues the MMAs.
+// Roles: sixteen warps for the softmax (a set of four has the keys and every fourth 16
+// columns), four convert the codes, one copies, one issues the MMAs.
 #pragma once
 #include <atomic>
 
@@ -46,14 +46,15 @@ constexpr int kLeastSteps = 2;      // of a CTA's share of the line
 constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
 constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
 constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kSets = 4;             // of four softmax warps: 16 columns in every 64 each
+constexpr int kSoftmaxWarps = 4 * kSets, kConvertWarps = 4;
 constexpr int kPrefixThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
 
 template <int DP, int QP, int PP>
 struct XShape {
     static constexpr int NMAX = prefix_rows(DP, QP, PP);
     static constexpr int NP = NMAX < 64 ? 64 : NMAX;  // columns of the second product: whole swizzle atoms
-    static constexpr int NH = NMAX / 2;               // columns of a softmax half
+    static constexpr int NC = (NMAX + 16 * kSets - 1) / (16 * kSets);  // times 16 columns of a set
     static constexpr int DA = DP == 256 ? 2 : 1;      // accumulators of 128 dims
     static constexpr int kQPart = NMAX * DP * 2;
     static constexpr int kPPart = kKeys * NP * 2;
@@ -71,7 +72,7 @@ struct XShape {
     static_assert(kFit >= 1, "shared memory");
     static constexpr int off_scale = off_raw + static_cast<int>(kRaws) * kRaw;
     static constexpr int off_cols = off_scale + static_cast<int>(kScaleSteps) * 8 * 16;
-    static constexpr int off_bar = off_cols + NMAX * (7 * 4 + 8 * 4 + 8);
+    static constexpr int off_bar = off_cols + NMAX * (7 * 4 + 8 * 4 + 8);  // Columns
     static constexpr int smem = off_bar + 512;
     static_assert(PP * DA * NP <= 256, "tensor memory");
     static_assert(smem <= 232448 && off_cols % 16 == 0 && off_bar % 8 == 0, "shared memory");
@@ -88,7 +89,7 @@ struct PrefixPiece {
 template <int NMAX>
 __device__ __forceinline__ int block_rows(int nrows, int* blocks) {
     const int n = (nrows + NMAX - 1) / NMAX;
-    const int per = n ? ((nrows + n - 1) / n + 31) / 32 * 32 : 32;
+    const int per = n ? ((nrows + n - 1) / n + 15) / 16 * 16 : 16;
     *blocks = (nrows + per - 1) / per;
     return per;
 }
@@ -135,7 +136,7 @@ struct GroupWalk {
         in -= unit * steps;
         u.h = static_cast<int>(div64(unit, blocks));
         u.row_first = static_cast<int>(unit - static_cast<int64_t>(u.h) * blocks) * per;
-        u.nc = min(per, (u.nrows - u.row_first + 31) / 32 * 32);
+        u.nc = min(per, (u.nrows - u.row_first + 15) / 16 * 16);
         return true;
     }
 };
@@ -185,24 +186,91 @@ __device__ __forceinline__ float max_columns(float (&v)[16]) {
     return fmaxf(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
+// What belongs to the columns (query rows) of a unit, in shared memory.
+template <int NMAX>
+struct Columns {
+    float fac[NMAX];               // factor of the scores
+    float nm[NMAX], pk[NMAX];      // less the reference, 2^k
+    float mul1[NMAX], mul2[NMAX];  // two factors
+    float ref[NMAX];
+    int refd[NMAX];
+    float tops[4][NMAX];           // by warp of a set: largest scores, later sums
+    float tops_v[4][NMAX];         // with the orders of vs
+    int64_t orow[NMAX];            // output rows, -1 past the last
+};
+
+// New references of the 16 columns from cb on, by the four warps of a set: mul1 is what the sums
+// of z, mul2 what those of p are to be multiplied by.  evs: the order of the key's vs.  Out of line: the
+// way there is rare but in a piece's first step.
+template <int NMAX>
+__device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
+                                            int evs, int barrier) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, key = threadIdx.x & 127;
+    // Largest scores, rounded up to whole orders, and with the orders of vs; `based`: the references are taken
+    // off first (huge scores, whose sums with an order do not hold it).
+    auto maxima = [&](bool based) {
+        uint32_t s[16];
+        float t[16];
+        tmem_load16(scores + cb, s);
+        tmem_loaded();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float score = __fmul_rn(__uint_as_float(s[i]), cols.fac[cb + i] * ks);
+            t[i] = there && score == score ? ceilf(score) : -INFINITY;
+        }
+        if (!based) {
+            float u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = t[i];
+            const float top = max_columns(u);
+            if (lane < 16) cols.tops[quarter][cb + lane] = top;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            t[i] = fmaxf(based ? t[i] - cols.ref[cb + i] : t[i], -INFINITY) + static_cast<float>(evs);
+        const float top = max_columns(t);
+        if (lane < 16) cols.tops_v[quarter][cb + lane] = top;
+    };
+    auto largest = [](const float (&of)[4][NMAX], int col) {
+        return fmaxf(fmaxf(of[0][col], of[1][col]), fmaxf(of[2][col], of[3][col]));
+    };
+    maxima(false);
+    sync_warps(barrier, 128);
+    const int col = cb + key;
+    int down = 0;
+    if (key < 16) {
+        const float m = cols.ref[col], mn = fmaxf(m, largest(cols.tops, col));
+        down = order_of(m - mn);
+        cols.ref[col] = mn, cols.nm[col] = -mn;
+        if (mn > kNoRef && fabsf(mn) >= kHugeScore) *huge_at = 1;
+    }
+    sync_warps(barrier, 128);
+    const bool huge = *reinterpret_cast<volatile int*>(huge_at) != 0;
+    if (huge) {
+        maxima(true);
+        sync_warps(barrier, 128);
+    }
+    if (key < 16) {
+        const int d = cols.refd[col];
+        const float high = largest(cols.tops_v, col);
+        const int dn = max(max(d + down, kNoOrder), order_of(huge ? high : high - cols.ref[col]));
+        const int k_old = min(kBase - d, kMostK), k_new = min(kBase - dn, kMostK);
+        cols.mul1[col] = pow2i(k_new - k_old + down);
+        cols.mul2[col] = pow2i(down);
+        cols.refd[col] = dn;
+        cols.pk[col] = pow2i(max(k_new, -126));
+    }
+    sync_warps(barrier, 128);
+}
+
 template <int DP, int QP, int PP, bool INT8>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
 qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using F = XShape<DP, QP, PP>;
-    constexpr int NMAX = F::NMAX, NH = F::NH;
+    constexpr int NMAX = F::NMAX;
     extern __shared__ __align__(1024) unsigned char smem[];
     float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScaleSteps][8]: ks, vs, there
-    // of each column (query row): factor of its scores, less its reference, 2^k; two factors; references
-    float* fac = reinterpret_cast<float*>(smem + F::off_cols);
-    float* nm = fac + NMAX;
-    float* pk = nm + NMAX;
-    float* mul1 = pk + NMAX;
-    float* mul2 = mul1 + NMAX;
-    float* ref = mul2 + NMAX;
-    int* refd = reinterpret_cast<int*>(ref + NMAX);
-    float* tops = reinterpret_cast<float*>(refd + NMAX);  // [4][NMAX] by warp: largest scores, later sums
-    float* tops_v = tops + 4 * NMAX;                      // [4][NMAX] with the orders of vs
-    int64_t* orow = reinterpret_cast<int64_t*>(tops_v + 4 * NMAX);  // output rows, -1 past the last
+    Columns<NMAX>& cols = *reinterpret_cast<Columns<NMAX>*>(smem + F::off_cols);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
     uint64_t* raw_empty = raw_full + F::kRaws;
     uint64_t* op_full = raw_empty + F::kRaws;
@@ -217,7 +285,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     static_assert((2 * F::kRaws + 2 * F::kOps + 5 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
     __shared__ PrefixPiece units[kUnitsAhead];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int huge_half[2];
+    __shared__ int huge_set[kSets];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KVLayer& c = a.c;
@@ -242,6 +310,19 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // the copying warp measures the line meanwhile
+    GroupWalk<NMAX> walk;
+    int64_t total = 0;
+    if (warp == kSoftmaxWarps + kConvertWarps) {
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        walk.more(a);
+        total = walk.chunk;
+        if (a.ngroups > 32) {
+            GroupWalk<NMAX> rest = walk;
+            while (rest.more(a)) total += rest.chunk;
+        }
     }
     fence_before();
     __syncthreads();
@@ -269,12 +350,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 
     if (warp == kSoftmaxWarps + kConvertWarps) {
         // ---------------------------------------------------------- copies
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
-        GroupWalk<NMAX> walk;
-        int64_t total = 0;
-        while (walk.more(a)) total += walk.chunk;
-        walk = GroupWalk<NMAX>();
         const int64_t ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / kLeastSteps));
         const Line line(total, static_cast<int>(ctas));
         int64_t at = 0, end = 0;
@@ -410,6 +485,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         while (next_unit()) {
             for (int j = w.j0; j < w.j1; ++j, ++g) {
                 const float4* sc = scales + (g % kScaleSteps) * 8;
+                wait(sc_full + g % kScaleSteps, g / kScaleSteps);
+                const bool whole = __all_sync(~0u, sc[lane & 7].z != 0.f);  // no page is missing
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++o) {
                     const uint32_t os = o % F::kOps;
@@ -421,13 +498,16 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         wait(raw_full + rs, r / F::kRaws);
                         const unsigned char* raw = smem + F::off_raw + rs * F::kRaw;
                         constexpr int C16 = F::RW / 16;
-#pragma unroll 4
+                        uint4 x[C16];
+#pragma unroll
+                        for (int it = 0; it < C16; ++it)
+                            x[it] = *reinterpret_cast<const uint4*>(raw + (it * 128 + ct) * 16);
+#pragma unroll
                         for (int it = 0; it < C16; ++it) {
                             const int item = it * 128 + ct, token = item / C16, c16 = item % C16;
-                            uint4 x = *reinterpret_cast<const uint4*>(raw + token * F::RW + c16 * 16);
-                            if (sc[token >> 4].z == 0.f) x = make_uint4(0, 0, 0, 0);
+                            if (!whole && sc[token >> 4].z == 0.f) x[it] = make_uint4(0, 0, 0, 0);
                             uint32_t h[8];
-                            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                            const uint32_t in[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) k_codes<INT8>(in[i], h[2 * i], h[2 * i + 1]);
                             // two 16-byte chunks; lanes of the second 64 dims store theirs in the other order
@@ -450,8 +530,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             }
         }
     } else {
-        // ---------------------------------------------------------- softmax, a thread a key and half of the columns
-        const int half = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wid = 2 + half;
+        // ---------------------------------------------------------- softmax, a thread a key and a set's columns
+        const int set = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wid = 2 + set;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t g = 0;
         for (;; ++turn) {
@@ -460,78 +540,76 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             // All warps go on or none: they meet at barriers below, whether their waits gave up or not.
             if (any_of(1, kSoftmaxWarps * 32, dead || units[slot].tokens < 0)) break;
             const volatile PrefixPiece& w = units[slot];
-            const int nc = w.nc, nh = nc / 2, c0 = half * nh, j0 = w.j0, j1 = w.j1;
+            const int nc = w.nc, j0 = w.j0, j1 = w.j1;
             {
                 // ---- queries: f16 parts of q * 2^e for the rows of this warp, and what belongs to each row
                 constexpr int QL = DP / 4 < 32 ? DP / 4 : 32, VL = DP / 4 / QL, QR = 32 / QL;  // lanes a row, vectors a lane
-                const int r_first = warp * (nc / 8), h = w.h, nrows = w.nrows, row_first = w.row_first;
+                constexpr int NB = NMAX / kSoftmaxWarps / QR;  // all reads on their way at once
+                const int each = nc / kSoftmaxWarps, h = w.h, nrows = w.nrows, row_first = w.row_first;
                 const int64_t row0 = w.row0;
-                constexpr int NB = VL == 2 ? 2 : 4;  // reads on their way at a time
-#pragma unroll 1
-                for (int r0 = 0; r0 < nc / 8; r0 += NB * QR) {
-                    uint4 raw[NB][VL];
-                    int64_t to[NB];
+                uint4 raw[NB][VL];
+                int64_t to[NB];
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const int in = r0 + i * QR + lane / QL;
-                        const int r = row_first + r_first + in;
-                        const bool live = in < nc / 8 && r < nrows;
-                        const int i_row = r / a.group, hq = h * a.group + r - i_row * a.group;
-                        to[i] = live ? (row0 + i_row) * a.q_heads + hq : -1;
-                        const int64_t qat = (row0 + i_row) * a.q_row + hq * a.q_head;
+                for (int i = 0; i < NB; ++i) {
+                    const int in = i * QR + lane / QL;
+                    const int r = row_first + warp * each + in;
+                    const bool live = in < each && r < nrows;
+                    const int i_row = r / a.group, hq = h * a.group + r - i_row * a.group;
+                    to[i] = live ? (row0 + i_row) * a.q_heads + hq : -1;
+                    const int64_t qat = (row0 + i_row) * a.q_row + hq * a.q_head;
 #pragma unroll
-                        for (int v = 0; v < VL; ++v) {
-                            const int d = (v * QL + lane % QL) * 4;
-                            raw[i][v] = load_q4(a.q, a.type, qat + d, live && d < c.dim);
-                        }
+                    for (int v = 0; v < VL; ++v) {
+                        const int d = (v * QL + lane % QL) * 4;
+                        raw[i][v] = load_q4(a.q, a.type, qat + d, live && d < c.dim);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (i * QR >= each) break;
+                    const int in = i * QR + lane / QL, col = warp * each + in;
+                    float amax = 0.f;
+                    float4 x[VL];
+#pragma unroll
+                    for (int v = 0; v < VL; ++v) {
+                        x[v] = q4_values(raw[i][v], a.type);
+                        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[v].x)), fmaxf(fabsf(x[v].y), fabsf(x[v].z))), fabsf(x[v].w));
                     }
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const int in = r0 + i * QR + lane / QL;
-                        if (r0 + i * QR >= nc / 8) break;
-                        float amax = 0.f;
-                        float4 x[VL];
-#pragma unroll
-                        for (int v = 0; v < VL; ++v) {
-                            x[v] = q4_values(raw[i][v], a.type);
-                            amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x[v].x)), fmaxf(fabsf(x[v].y), fabsf(x[v].z))), fabsf(x[v].w));
+                    for (int k = QL / 2; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
+                    // 2^e with amax * 2^e in [2^14, 2^15); 1 for zero or non-finite rows
+                    int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
+                    e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
+                    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                    if (in < each) {
+                        if (lane % QL == 0) {
+                            cols.fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                            cols.ref[col] = kNoRef, cols.refd[col] = kNoOrder;
+                            cols.orow[col] = to[i];
                         }
 #pragma unroll
-                        for (int k = QL / 2; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
-                        // 2^e with amax * 2^e in [2^14, 2^15); 1 for zero or non-finite rows
-                        int e = 141 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
-                        e = amax > 0.f && amax <= 3.4028235e38f ? min(e, 120) : 0;
-                        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-                        if (in < nc / 8) {
-                            const int col = r_first + in;
-                            if (lane % QL == 0) {
-                                fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                                nm[col] = -kNoRef, pk[col] = 1.f, ref[col] = kNoRef, refd[col] = kNoOrder;
-                                orow[col] = to[i];
-                            }
-#pragma unroll
-                            for (int v = 0; v < VL; ++v) {
-                                const int d = (v * QL + lane % QL) * 4, ch = d >> 3;
-                                // the dims in the order that k_codes gives a word's bytes
-                                const float y0 = x[v].x * up, y1 = (INT8 ? x[v].z : x[v].y) * up;
-                                const float y2 = (INT8 ? x[v].y : x[v].z) * up, y3 = x[v].w * up;
-                                const uint2 hi = make_uint2(pack_f16x2(y0, y1), pack_f16x2(y2, y3));
-                                unsigned char* dst = smem + (ch >> 3) * (NMAX * 128) + col * 128 + (((ch & 7) ^ (col & 7)) << 4) + (d & 4) * 2;
-                                *reinterpret_cast<uint2*>(dst) = hi;
-                                if (QP == 2)
-                                    *reinterpret_cast<uint2*>(dst + F::kQPart) = make_uint2(rest_f16x2(y0, y1, hi.x), rest_f16x2(y2, y3, hi.y));
-                            }
+                        for (int v = 0; v < VL; ++v) {
+                            const int d = (v * QL + lane % QL) * 4, ch = d >> 3;
+                            // the dims in the order that k_codes gives a word's bytes
+                            const float y0 = x[v].x * up, y1 = (INT8 ? x[v].z : x[v].y) * up;
+                            const float y2 = (INT8 ? x[v].y : x[v].z) * up, y3 = x[v].w * up;
+                            const uint2 hi = make_uint2(pack_f16x2(y0, y1), pack_f16x2(y2, y3));
+                            unsigned char* dst = smem + (ch >> 3) * (NMAX * 128) + col * 128 + (((ch & 7) ^ (col & 7)) << 4) + (d & 4) * 2;
+                            *reinterpret_cast<uint2*>(dst) = hi;
+                            if (QP == 2)
+                                *reinterpret_cast<uint2*>(dst + F::kQPart) = make_uint2(rest_f16x2(y0, y1, hi.x), rest_f16x2(y2, y3, hi.y));
                         }
                     }
                 }
-                if (lane == 0 && quarter == 0) huge_half[half] = 0;
+                if (lane == 0 && quarter == 0) huge_set[set] = 0;
                 fence_proxy_async_smem();
                 sync_warps(1, kSoftmaxWarps * 32);
                 if (lane == 0) arrive_on(q_full);
             }
-            float l[NH];
+            f2 l[F::NC][8];  // sums of p by column pairs
 #pragma unroll
-            for (int i = 0; i < NH; ++i) l[i] = 0.f;
+            for (int cc = 0; cc < F::NC; ++cc)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) l[cc][i] = {0.f, 0.f};
 
             for (int j = j0; j < j1; ++j, ++g) {
                 wait(sc_full + g % kScaleSteps, g / kScaleSteps);
@@ -540,99 +618,43 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const float4 mine = scales[(g % kScaleSteps) * 8 + (key >> 4)];
                 const float ks = mine.x, vs = mine.y;
                 const bool there = mine.z != 0.f, whole = __all_sync(~0u, there);
-                // vs < 2^evs
-                const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
                 const uint32_t st = tmem + (g & 1) * 128 + lanes;
-                unsigned char* prow = smem + F::off_p + key * 128;
-                // Partial maxima of 16 columns from cb on: the scores', rounded up to whole orders, and with those of
-                // vs; `base` 0, or the references that are taken off first (huge scores, whose sums with an order do
-                // not hold it).
-                auto maxima = [&](int cb, bool based) {
-                    uint32_t s[16];
-                    float t[16], u[16];
-                    tmem_load16(st + cb, s);
-                    tmem_loaded();
+                bool mine_now = false;  // z and O are this step's
+                auto take = [&]() {
+                    if (!mine_now && g > 0) wait(pv_done, g - 1);
+                    mine_now = true;
+                };
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float score = __fmul_rn(__uint_as_float(s[i]), fac[cb + i] * ks);
-                        t[i] = there && score == score ? ceilf(score) : -INFINITY;
-                        u[i] = fmaxf(t[i] - (based ? ref[cb + i] : 0.f), -INFINITY) + static_cast<float>(evs);
-                    }
-                    const float a = max_columns(t), b = max_columns(u);
-                    if (lane < 16) {
-                        if (!based) tops[quarter * NMAX + cb + lane] = a;
-                        tops_v[quarter * NMAX + cb + lane] = b;
-                    }
-                };
-                auto largest = [&](const float* of, int col) {
-                    return fmaxf(fmaxf(of[col], of[NMAX + col]), fmaxf(of[2 * NMAX + col], of[3 * NMAX + col]));
-                };
-                auto references = [&](int cb, int n) {  // new ones for n columns, by all four warps
-                    for (int x = cb; x < cb + n; x += 16) maxima(x, false);
-                    sync_warps(wid, 128);
-                    const int col = cb + key;
-                    int down = 0;
-                    if (key < n) {
-                        const float m = ref[col], mn = fmaxf(m, largest(tops, col));
-                        down = order_of(m - mn);
-                        ref[col] = mn, nm[col] = -mn;
-                        if (mn > kNoRef && fabsf(mn) >= kHugeScore) huge_half[half] = 1;
-                    }
-                    sync_warps(wid, 128);
-                    const bool huge = huge_half[half] != 0;
-                    if (huge) {
-                        for (int x = cb; x < cb + n; x += 16) maxima(x, true);
-                        sync_warps(wid, 128);
-                    }
-                    if (key < n) {
-                        const int d = refd[col];
-                        const float high = largest(tops_v, col);
-                        const int dn = max(max(d + down, kNoOrder), order_of(huge ? high : high - ref[col]));
-                        const int k_old = min(kBase - d, kMostK), k_new = min(kBase - dn, kMostK);
-                        mul1[col] = pow2i(k_new - k_old + down);
-                        mul2[col] = pow2i(down);
-                        refd[col] = dn;
-                        pk[col] = pow2i(max(k_new, -126));
-                    }
-                    sync_warps(wid, 128);
-                };
-                if (j == j0) references(c0, nh);
-#pragma unroll
-                for (int cc = 0; cc < NH / 16; ++cc) {
-                    if (cc * 16 >= nh) break;
-                    const int cb = c0 + cc * 16;
-                    float p[16];
+                for (int cc = 0; cc < F::NC; ++cc) {
+                    const int cb = (cc * kSets + set) * 16;
+                    if (cb >= nc) break;
+                    f2 p[8];
                     uint32_t z[8], zl[PP == 2 ? 8 : 1];
                     uint32_t s[16];
                     // Probabilities of 16 columns under the references as they are; whether one passes them.
-                    auto attempt = [&](bool rounded) {
+                    auto attempt = [&](auto rounded) {
                         tmem_load16(st + cb, s);
                         tmem_loaded();
                         float high = -INFINITY;
                         uint32_t most = 0u;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float4 fa = *reinterpret_cast<const float4*>(fac + cb + 4 * q);
-                            const float4 na = *reinterpret_cast<const float4*>(nm + cb + 4 * q);
-                            const float4 ka = *reinterpret_cast<const float4*>(pk + cb + 4 * q);
+                            const float4 fa = *reinterpret_cast<const float4*>(cols.fac + cb + 4 * q);
+                            const float4 na = *reinterpret_cast<const float4*>(cols.nm + cb + 4 * q);
+                            const float4 ka = *reinterpret_cast<const float4*>(cols.pk + cb + 4 * q);
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int i = 2 * q + u;
                                 const f2 fq = fmul2(u ? f2{fa.z, fa.w} : f2{fa.x, fa.y}, f2{ks, ks});
                                 const f2 sv = {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])};
                                 f2 y = u ? f2{na.z, na.w} : f2{na.x, na.y};
-                                if (rounded) {
-                                    y.x = __fadd_rn(__fmul_rn(sv.x, fq.x), y.x);
-                                    y.y = __fadd_rn(__fmul_rn(sv.y, fq.y), y.y);
-                                } else {
-                                    ffma2(y, sv, fq);
-                                }
+                                if (rounded) fadd2(y, fmul2(sv, fq));
+                                else ffma2(y, sv, fq);
                                 if (!whole && !there) y.x = y.y = -INFINITY;
                                 high = fmaxf(high, fmaxf(y.x, y.y));
-                                const f2 e = {exp2_fast(y.x), exp2_fast(y.y)};
-                                p[2 * i] = e.x, p[2 * i + 1] = e.y;
+                                p[i] = {exp2_fast(y.x), exp2_fast(y.y)};
                                 // p first: vs * 2^k may pass the range where p is 0
-                                const f2 zz = fmul2(fmul2(e, u ? f2{ka.z, ka.w} : f2{ka.x, ka.y}), f2{vs, vs});
+                                const f2 zz = fmul2(fmul2(p[i], u ? f2{ka.z, ka.w} : f2{ka.x, ka.y}), f2{vs, vs});
                                 z[i] = pack_f16x2(zz.x, zz.y);
                                 if (PP == 2) {  // 2^11 times what the first part leaves
                                     const f2 hi = h2_to_f2(z[i]);
@@ -643,32 +665,37 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         }
                         return high > 20.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
                     };
-                    bool huge = huge_half[half] != 0;
-                    bool passed = true;
-                    if (!huge) passed = any_of(wid, 128, attempt(false));
-                    if (cc == 0 && g > 0) wait(pv_done, g - 1);  // z and O are this step's now
-                    if (passed) {
-                        fence_after();
-                        references(cb, 16);
-                        huge = huge_half[half] != 0;
+                    for (int round = j == j0 ? 1 : 0;; round = 1) {
+                        bool huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
+                        if (round == 1) {
+                            fence_after();
+                            // vs < 2^evs
+                            const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
+                            new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
+                            huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
+                            if (j > j0) {
+                                take();
+                                fence_after();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) l[cc * 16 + i] *= mul2[cb + i];
-                        if (j > j0) {
+                                for (int i = 0; i < 8; ++i) l[cc][i] = fmul2(l[cc][i], *reinterpret_cast<const f2*>(cols.mul2 + cb + 2 * i));
 #pragma unroll
-                            for (int acc = 0; acc < PP * F::DA; ++acc) {
-                                tmem_load16(o_at + acc * F::NP + lanes + cb, s);
-                                tmem_loaded();
+                                for (int acc = 0; acc < PP * F::DA; ++acc) {
+                                    tmem_load16(o_at + acc * F::NP + lanes + cb, s);
+                                    tmem_loaded();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * mul1[cb + i]);
-                                tmem_store16(o_at + acc * F::NP + lanes + cb, s);
+                                    for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * cols.mul1[cb + i]);
+                                    tmem_store16(o_at + acc * F::NP + lanes + cb, s);
+                                }
+                                tmem_stored();
                             }
-                            tmem_stored();
                         }
-                        (void)attempt(huge);
+                        const bool passed = huge ? attempt(std::true_type()) : attempt(std::false_type());
+                        if (round == 1 || !any_of(wid, 128, passed || huge)) break;
                     }
+                    take();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) l[cc * 16 + i] += p[i];
-                    unsigned char* dst = prow + (cb >> 6) * 16384;
+                    for (int i = 0; i < 8; ++i) fadd2(l[cc][i], p[i]);
+                    unsigned char* dst = smem + F::off_p + key * 128 + (cb >> 6) * 16384;
                     const int ch = (cb & 63) >> 3;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -680,6 +707,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                            zl[(4 * u + 2) % (PP == 2 ? 8 : 1)], zl[(4 * u + 3) % (PP == 2 ? 8 : 1)]);
                     }
                 }
+                take();
                 fence_proxy_async_smem();
                 fence_before();
                 __syncwarp();
@@ -687,30 +715,35 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             }
 
             // ---- the rows' sums, then their results
-#pragma unroll
-            for (int x = 0; x < (NH + 31) / 32; ++x) {
+            {
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = x * 32 + i < NH && x * 32 + i < nh ? l[(x * 32 + i) % NH] : 0.f;
+                for (int i = 0; i < 32; ++i) {
+                    const int cc = i / 16, pair = (i % 16) / 2;
+                    v[i] = 0.f;
+                    if (cc < F::NC && (cc * kSets + set) * 16 < nc) v[i] = i & 1 ? l[cc % F::NC][pair].y : l[cc % F::NC][pair].x;
+                }
                 const float sum = add_columns(v);
-                if (x * 32 + lane < nh) tops[quarter * NMAX + c0 + x * 32 + lane] = sum;
+                const int col = ((lane >> 4) * kSets + set) * 16 + (lane & 15);
+                if (lane < 16 * F::NC && col < nc) cols.tops[quarter][col] = sum;
             }
             sync_warps(wid, 128);
             float* part = a.slots + static_cast<int64_t>(w.slot < 0 ? 0 : w.slot) * (NMAX * (DP + 2));
             const bool begins = w.slot < 0;
-            if (key < nh) {
-                const int col = c0 + key;
-                const float sum = (tops[col] + tops[NMAX + col]) + (tops[2 * NMAX + col] + tops[3 * NMAX + col]);
+            const int mine = ((key >> 4) * kSets + set) * 16 + (key & 15);  // this thread's column
+            if (key < 16 * F::NC && mine < nc) {
+                const int col = mine;
+                const float sum = (cols.tops[0][col] + cols.tops[1][col]) + (cols.tops[2][col] + cols.tops[3][col]);
                 // NaN sums stay NaN; a row that saw nothing has a sum of 0
-                const bool none = sum == 0.f && ref[col] == kNoRef;
-                const int down = none ? 0 : -min(kBase - refd[col], kMostK);
-                mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down >> 1);
-                mul2[col] = pow2i(down - (down >> 1));
-                const float m = none ? -INFINITY : ref[col];
+                const bool none = sum == 0.f && cols.ref[col] == kNoRef;
+                const int down = none ? 0 : -min(kBase - cols.refd[col], kMostK);
+                cols.mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down >> 1);
+                cols.mul2[col] = pow2i(down - (down >> 1));
+                const float m = none ? -INFINITY : cols.ref[col];
                 if (begins) {
-                    if (orow[col] >= 0)
-                        a.own_ml[orow[col]] = make_float4(m, sum, __int_as_float(static_cast<int>(blockIdx.x) + 1),
-                                                          __int_as_float(w.extra | col << 16));
+                    if (cols.orow[col] >= 0)
+                        a.own_ml[cols.orow[col]] = make_float4(m, sum, __int_as_float(static_cast<int>(blockIdx.x) + 1),
+                                                               __int_as_float(w.extra | col << 16));
                 } else {
                     *reinterpret_cast<float2*>(part + NMAX * DP + 2 * col) = make_float2(m, sum);
                 }
@@ -719,25 +752,25 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             fence_after();
             sync_warps(wid, 128);
             const int place = INT8 ? (lane & ~3) | ((lane & 1) << 1 | (lane & 2) >> 1) : lane;  // dims as k_codes orders them
+#pragma unroll 1
+            for (int x = 0; x < F::DA * F::NC; ++x) {
+                const int acc = x / F::NC, cb = (x % F::NC * kSets + set) * 16, d = acc * 128 + quarter * 32 + place;
+                if (cb >= nc || acc * 128 + quarter * 32 >= c.dim) continue;
+                uint32_t v[16], vl[16];
+                tmem_load16(o_at + acc * F::NP + lanes + cb, v);
+                if (PP == 2) tmem_load16(o_at + (F::DA + acc) * F::NP + lanes + cb, vl);
+                tmem_loaded();
+                if (d < c.dim) {
 #pragma unroll
-            for (int acc = 0; acc < F::DA; ++acc) {
-                const int d = acc * 128 + quarter * 32 + place;
-                for (int cb = c0; cb < c0 + nh; cb += 16) {
-                    uint32_t v[16], vl[16];
-                    tmem_load16(o_at + acc * F::NP + lanes + cb, v);
-                    if (PP == 2) tmem_load16(o_at + (F::DA + acc) * F::NP + lanes + cb, vl);
-                    tmem_loaded();
-                    if (d < c.dim) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float x = __uint_as_float(v[i]);
-                            if (PP == 2) x = fmaf(__uint_as_float(vl[i]), 0x1p-11f, x);
-                            x = x * mul1[cb + i] * mul2[cb + i];
-                            const int64_t to = orow[cb + i];
-                            if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = mul1[cb + i] == 0.f ? 0.f : x;
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        float x = __uint_as_float(v[i]);
+                        if (PP == 2) x = fmaf(__uint_as_float(vl[i]), 0x1p-11f, x);
+                        x = x * cols.mul1[cb + i] * cols.mul2[cb + i];
+                        const int64_t to = cols.orow[cb + i];
+                        if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = cols.mul1[cb + i] == 0.f ? 0.f : x;
                     }
                 }
+                __syncwarp();
             }
             fence_before();
             __syncwarp();
