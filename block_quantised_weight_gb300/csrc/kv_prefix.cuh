@@ -24,7 +24,9 @@
 // exponentials of 128 rows (16 a clock and SM); short calls are bound by the chain
 // plan -> table -> codes -> first step, and by the parts that are left to join.
 //
-// Split.  The steps of all (group, head, row block) are one line, cut evenly among
+// Split.  Each unit (group, head, row block) is cut into as many parts as its steps are a
+// share of all CTAs' (a piece costs as much as some steps before its first and behind
+// its last, so a CTA gets one), and the parts are one line, cut evenly among
 // the CTAs.  A piece that begins a unit leaves its result for each row, the
 // others in a slot of their CTA; the row kernel adds them to what lies behind the
 // prefix (own_ml of a row names the CTA of the first further piece and their number).
@@ -42,9 +44,10 @@ namespace qg {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kLeastSteps = 2;      // of a CTA's share of the line
+constexpr int kLeastSteps = 2;      // of a part
 constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
 constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
+constexpr int64_t kPrefetchBytes = int64_t(64) << 20;  // half of L2
 constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
 constexpr int kSets = 4;             // of four softmax warps: 16 columns in every 64 each
 constexpr int kSoftmaxWarps = 4 * kSets, kConvertWarps = 4;
@@ -85,59 +88,76 @@ struct PrefixPiece {
     int tokens; // of the prefix; < 0: no more pieces
 };
 
-// Rows of the blocks that nrows query rows are cut into.
+// A group's units (heads x row blocks), each cut into `parts` parts of nearly equal length.
+struct Units {
+    int n, steps, parts, per, blocks;  // per: rows of a block
+};
 template <int NMAX>
-__device__ __forceinline__ int block_rows(int nrows, int* blocks) {
-    const int n = (nrows + NMAX - 1) / NMAX;
-    const int per = n ? ((nrows + n - 1) / n + 15) / 16 * 16 : 16;
-    *blocks = (nrows + per - 1) / per;
-    return per;
+__device__ __forceinline__ Units units_of(const AttnArgs& a, const SharedGroup& g) {
+    Units u = {};
+    if (g.tokens == 0) return u;
+    const unsigned rows = static_cast<unsigned>(g.n) * a.group, most = (rows + NMAX - 1) / NMAX;
+    u.per = ((rows + most - 1) / most + 15) / 16 * 16;
+    u.blocks = (rows + u.per - 1) / u.per;
+    u.n = u.blocks * a.c.heads;
+    u.steps = static_cast<int>((static_cast<unsigned>(g.tokens) + kKeys - 1) / kKeys);
+    return u;
 }
 
-// Finds places on the line of all groups (heads, then row blocks, then steps), by a whole warp, forward only.
+// The line of all parts.  A lane has every 32nd group; a part is found by a whole warp, forward only.
 template <int NMAX>
-struct GroupWalk {
+struct PartWalk {
     int b0 = -32;
-    SharedGroup g;  // of this lane's group, b0 + lane
-    int64_t base = 0, chunk = 0, upto = 0;
-    __device__ bool more(const AttnArgs& a) {
-        const int lane = threadIdx.x & 31;
-        b0 += 32;
-        base += chunk;
-        if (b0 >= a.ngroups) return false;
+    SharedGroup g;
+    Units u;
+    float steps;                       // of all units
+    int base = 0, chunk = 0, upto = 0; // parts
+    __device__ void load(const AttnArgs& a, int from) {
+        b0 = from;
         g = SharedGroup{};
-        if (b0 + lane < a.ngroups) g = shared_group(a, b0 + lane);
-        int blocks = 0;
-        if (g.tokens) block_rows<NMAX>(g.n * a.group, &blocks);
-        upto = static_cast<int64_t>(blocks) * a.c.heads * ((static_cast<int64_t>(g.tokens) + kKeys - 1) / kKeys);
+        if (b0 + (threadIdx.x & 31) < a.ngroups) g = shared_group(a, b0 + (threadIdx.x & 31));
+        u = units_of<NMAX>(a, g);
+    }
+    // Steps of the 32 groups loaded.  Every CTA gets the same value from the same operations.
+    __device__ float sum_steps() const {
+        float s = static_cast<float>(u.n) * static_cast<float>(u.steps);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        return s;
+    }
+    // As many parts a unit as its share of the CTAs, at least one, none shorter than kLeastSteps.
+    __device__ void cut(int ctas) {
+        u.parts = 0;
+        if (u.n) u.parts = max(1, min(static_cast<int>(static_cast<float>(u.steps) * static_cast<float>(ctas) / steps), u.steps / kLeastSteps));
+        upto = u.n * u.parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, upto, o);
-            if (lane >= o) upto += x;
+            const int x = __shfl_up_sync(~0u, upto, o);
+            if (static_cast<int>(threadIdx.x & 31) >= o) upto += x;
         }
         chunk = __shfl_sync(~0u, upto, 31);
-        return true;
     }
-    // The unit at `at`, its steps, and the place in it.
-    __device__ bool to(const AttnArgs& a, int64_t at, PrefixPiece& u, int& steps, int64_t& in) {
-        while (at >= base + chunk)
-            if (!more(a)) return false;
-        const int which = __popc(__ballot_sync(~0u, upto <= at - base));
-        u.row0 = __shfl_sync(~0u, g.row0, which);
-        u.nrows = __shfl_sync(~0u, g.n, which) * a.group;
-        u.tokens = __shfl_sync(~0u, g.tokens, which);
-        u.table_row = __shfl_sync(~0u, g.table_row, which);
-        const int64_t below = __shfl_sync(~0u, upto, which ? which - 1 : 0);
+    // The unit of part `at`, its steps and parts, and which of them it is.
+    __device__ void to(const AttnArgs& a, int at, int ctas, PrefixPiece& w, int& steps_of, int& parts, int& in) {
+        while (at >= base + chunk && b0 + 32 < a.ngroups) {
+            base += chunk;
+            load(a, b0 + 32);
+            cut(ctas);
+        }
+        const int which = min(31, __popc(__ballot_sync(~0u, upto <= at - base)));
+        w.row0 = __shfl_sync(~0u, g.row0, which);
+        w.nrows = __shfl_sync(~0u, g.n, which) * a.group;
+        w.tokens = __shfl_sync(~0u, g.tokens, which);
+        w.table_row = __shfl_sync(~0u, g.table_row, which);
+        const int per = __shfl_sync(~0u, u.per, which), blocks = __shfl_sync(~0u, u.blocks, which);
+        steps_of = __shfl_sync(~0u, u.steps, which), parts = __shfl_sync(~0u, u.parts, which);
+        const int below = __shfl_sync(~0u, upto, which ? which - 1 : 0);
         in = at - base - (which ? below : 0);
-        steps = static_cast<int>((static_cast<int64_t>(u.tokens) + kKeys - 1) / kKeys);
-        int blocks;
-        const int per = block_rows<NMAX>(u.nrows, &blocks);
-        const int64_t unit = div64(in, steps);
-        in -= unit * steps;
-        u.h = static_cast<int>(div64(unit, blocks));
-        u.row_first = static_cast<int>(unit - static_cast<int64_t>(u.h) * blocks) * per;
-        u.nc = min(per, (u.nrows - u.row_first + 15) / 16 * 16);
-        return true;
+        const int unit = in / parts;
+        in -= unit * parts;
+        w.h = unit / blocks;
+        w.row_first = (unit - w.h * blocks) * per;
+        w.nc = min(per, (w.nrows - w.row_first + 15) / 16 * 16);
     }
 };
 
@@ -199,9 +219,51 @@ struct Columns {
     int64_t orow[NMAX];            // output rows, -1 past the last
 };
 
+// The first references of 4 of the 16 columns from cb on, by each warp of a set from its own 32
+// keys: a lower bound of the largest, which 2^9 above the first z leaves room for.
+template <int NMAX>
+__device__ __forceinline__ void first_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
+                                                 int evs, int barrier) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    uint32_t s[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]) : "r"(scores + cb + quarter * 4));
+    tmem_loaded();
+    float top[4], high[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float score = __fmul_rn(__uint_as_float(s[i]), cols.fac[cb + quarter * 4 + i] * ks);
+        top[i] = there && score == score ? ceilf(score) : -INFINITY;
+        high[i] = top[i] + static_cast<float>(evs);
+    }
+    // lane l gets column l & 3
+#pragma unroll
+    for (int w = 2; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float gt = lane & w ? top[i] : top[i + w], gh = lane & w ? high[i] : high[i + w];
+            top[i] = fmaxf(lane & w ? top[i + w] : top[i], __shfl_xor_sync(~0u, gt, w));
+            high[i] = fmaxf(lane & w ? high[i + w] : high[i], __shfl_xor_sync(~0u, gh, w));
+        }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], o));
+        high[0] = fmaxf(high[0], __shfl_xor_sync(~0u, high[0], o));
+    }
+    if (lane < 4) {
+        const int col = cb + quarter * 4 + lane;
+        const float mn = fmaxf(kNoRef, top[0]);
+        const int dn = max(kNoOrder, order_of(high[0] - mn));
+        cols.ref[col] = mn, cols.nm[col] = -mn, cols.refd[col] = dn;
+        cols.pk[col] = pow2i(max(min(kBase - dn, kMostK), -126));
+        if (mn > kNoRef && fabsf(mn) >= kHugeScore) *reinterpret_cast<volatile int*>(huge_at) = 1;
+    }
+    sync_warps(barrier, 128);
+}
+
 // New references of the 16 columns from cb on, by the four warps of a set: mul1 is what the sums
 // of z, mul2 what those of p are to be multiplied by.  evs: the order of the key's vs.  Out of line: the
-// way there is rare but in a piece's first step.
+// way there is rare.
 template <int NMAX>
 __device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
                                             int evs, int barrier) {
@@ -312,16 +374,26 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // the copying warp measures the line meanwhile
-    GroupWalk<NMAX> walk;
-    int64_t total = 0;
+    PartWalk<NMAX> walk;
+    int total = 0;
     if (warp == kSoftmaxWarps + kConvertWarps) {
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
-        walk.more(a);
+        walk.load(a, 0);
+        walk.steps = walk.sum_steps();
+        for (int b = 32; b < a.ngroups; b += 32) {
+            PartWalk<NMAX> next;
+            next.load(a, b);
+            walk.steps += next.sum_steps();
+        }
+        walk.cut(gridDim.x);
         total = walk.chunk;
-        if (a.ngroups > 32) {
-            GroupWalk<NMAX> rest = walk;
-            while (rest.more(a)) total += rest.chunk;
+        for (int b = 32; b < a.ngroups; b += 32) {
+            PartWalk<NMAX> next;
+            next.load(a, b);
+            next.steps = walk.steps;
+            next.cut(gridDim.x);
+            total += next.chunk;
         }
     }
     fence_before();
@@ -350,25 +422,25 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 
     if (warp == kSoftmaxWarps + kConvertWarps) {
         // ---------------------------------------------------------- copies
-        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / kLeastSteps));
-        const Line line(total, static_cast<int>(ctas));
-        int64_t at = 0, end = 0;
-        if (static_cast<int>(blockIdx.x) < line.ctas) at = line.first(blockIdx.x), end = line.first(blockIdx.x + 1);
+        const Line line(total, gridDim.x);
+        int at = 0, end = 0;
+        if (static_cast<int>(blockIdx.x) < line.ctas)
+            at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
         uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
         uint32_t sent = 0;      // raw tiles whose copies were issued
         for (;; ++turn) {
             const uint32_t slot = turn % kUnitsAhead;
             if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
-            int steps = 0;
-            int64_t in = 0;
-            const bool there = !dead && at < end && walk.to(a, at, w, steps, in);
+            const bool there = !dead && at < end;
             if (there) {
-                const int64_t start = at - in, stop = start + steps;
-                at = min(end, stop);
-                w.j0 = static_cast<int>(in);
-                w.j1 = static_cast<int>(at - start);
+                int steps, parts, in;
+                walk.to(a, at, gridDim.x, w, steps, parts, in);
+                const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
+                w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
+                w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
                 w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
-                w.extra = in == 0 ? line.of(stop - 1) - static_cast<int>(blockIdx.x) : 0;
+                w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
+                at += last - in;
             } else {
                 w.tokens = -1;
             }
@@ -424,6 +496,23 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 (void)mbar_wait_bounded(raw_full + x % F::kRaws, (x / F::kRaws) & 1u, a.status);
     } else if (warp == kSoftmaxWarps + kConvertWarps + 1) {
         // ---------------------------------------------------------- MMAs
+        // What the sequences hold behind the prefix comes to L2 meanwhile, for the launch behind this one, as far
+        // as L2 keeps it: a lane a page.
+        const uint32_t page_bytes = static_cast<uint32_t>(c.heads * c.dim) << c.log2p;
+        int64_t room = kPrefetchBytes / (2 * static_cast<int64_t>(page_bytes) * gridDim.x);
+        for (int b = blockIdx.x; b < a.batch && room > 0; b += gridDim.x) {
+            const int64_t len = min(static_cast<int64_t>(max(a.lens[b], 0)), a.width << c.log2p);
+            const int64_t from = max(a.skip[b], 0) >> c.log2p;
+            const int64_t pages = min((len + (1 << c.log2p) - 1) >> c.log2p, from + room);
+            for (int64_t x = from + lane; x < pages; x += 32) {
+                const int id = a.table[b * a.width + x];
+                if (id < 0 || id >= c.pages) continue;
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.k + id * c.page_stride), "r"(page_bytes) : "memory");
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.v + id * c.page_stride), "r"(page_bytes) : "memory");
+            }
+            room -= max(int64_t(0), pages - from);
+        }
+        __syncwarp();
         uint32_t o = 0, g = 0, qs = 0;  // operands, steps and queries taken
         while (next_unit()) {
             const int steps = w.j1 - w.j0;
@@ -548,19 +637,23 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const int each = nc / kSoftmaxWarps, h = w.h, nrows = w.nrows, row_first = w.row_first;
                 const int64_t row0 = w.row0;
                 uint4 raw[NB][VL];
-                int64_t to[NB];
+                int64_t mine = -1, my_to = -1;  // lane i: of row i
+                {
+                    const int r = row_first + warp * each + lane;
+                    if (lane < each && r < nrows) {
+                        const int i_row = static_cast<unsigned>(r) / static_cast<unsigned>(a.group), hq = h * a.group + r - i_row * a.group;
+                        my_to = (row0 + i_row) * a.q_heads + hq;
+                        mine = (row0 + i_row) * a.q_row + hq * a.q_head;
+                    }
+                    if (lane < each) cols.orow[warp * each + lane] = my_to;
+                }
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    const int in = i * QR + lane / QL;
-                    const int r = row_first + warp * each + in;
-                    const bool live = in < each && r < nrows;
-                    const int i_row = r / a.group, hq = h * a.group + r - i_row * a.group;
-                    to[i] = live ? (row0 + i_row) * a.q_heads + hq : -1;
-                    const int64_t qat = (row0 + i_row) * a.q_row + hq * a.q_head;
+                    const int64_t qat = __shfl_sync(~0u, mine, i * QR + lane / QL);
 #pragma unroll
                     for (int v = 0; v < VL; ++v) {
                         const int d = (v * QL + lane % QL) * 4;
-                        raw[i][v] = load_q4(a.q, a.type, qat + d, live && d < c.dim);
+                        raw[i][v] = load_q4(a.q, a.type, qat + d, qat >= 0 && d < c.dim);
                     }
                 }
 #pragma unroll
@@ -583,8 +676,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     if (in < each) {
                         if (lane % QL == 0) {
                             cols.fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                            cols.ref[col] = kNoRef, cols.refd[col] = kNoOrder;
-                            cols.orow[col] = to[i];
                         }
 #pragma unroll
                         for (int v = 0; v < VL; ++v) {
@@ -665,12 +756,13 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         }
                         return high > 20.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
                     };
-                    for (int round = j == j0 ? 1 : 0;; round = 1) {
+                    // vs < 2^evs
+                    const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
+                    if (j == j0) first_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
+                    for (int round = 0;; round = 1) {
                         bool huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
                         if (round == 1) {
                             fence_after();
-                            // vs < 2^evs
-                            const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
                             new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
                             huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
                             if (j > j0) {

@@ -105,29 +105,51 @@ __device__ __forceinline__ void join_prefix(const AttnArgs& a, int64_t to, int r
     const float* parts = a.slots + (more ? cta * stride + static_cast<int64_t>(row) * a.slot_dims : 0);
     const float2* ml = reinterpret_cast<const float2*>(a.slots + (more ? cta * stride + static_cast<int64_t>(a.slot_rows) * a.slot_dims : 0)) + row;
     float best = fmaxf(top, first.x);
-#pragma unroll 8
-    for (int i = 0; i < more; ++i) best = fmaxf(best, __ldcg(ml + i * (stride / 2)).x);
-    const float ref = best == -INFINITY ? 0.f : best;
-    const float mine = exp2_fast(top - ref) * sum;
-    float total = mine;
+    float ref = best == -INFINITY ? 0.f : best;
+    const float mine = exp2_fast(top - ref) * sum, theirs = exp2_fast(first.x - ref) * first.y;
+    float total = mine + theirs;
     float4 o[XV];
 #pragma unroll
-    for (int x = 0; x < XV; ++x)
-        o[x] = make_float4(mine * acc[x].x, mine * acc[x].y, mine * acc[x].z, mine * acc[x].w);
-    auto add = [&](float2 p, const float* from) {
-        const float w = exp2_fast(p.x - ref) * p.y;
-        total += w;
+    for (int x = 0; x < XV; ++x) {
+        const int d = 4 * (row_lane + 32 * x);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (d < a.c.dim) v = __ldcg(reinterpret_cast<const float4*>(a.own + to * a.c.dim + d));
+        o[x] = make_float4(mine * acc[x].x + theirs * v.x, mine * acc[x].y + theirs * v.y, mine * acc[x].z + theirs * v.z,
+                           mine * acc[x].w + theirs * v.w);
+    }
+    // further parts, as many at once as their reads fit
+    constexpr int N = 8 / XV;
+    for (int i0 = 0; i0 < more; i0 += N) {
+        float2 p[N];
+        float4 v[N][XV];
 #pragma unroll
-        for (int x = 0; x < XV; ++x) {
-            const int d = 4 * (row_lane + 32 * x);
-            if (d >= a.c.dim) break;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + d));
-            o[x].x += w * v.x, o[x].y += w * v.y, o[x].z += w * v.z, o[x].w += w * v.w;
+        for (int i = 0; i < N; ++i) {
+            p[i] = make_float2(-INFINITY, 0.f);
+            if (i0 + i < more) p[i] = __ldcg(ml + (i0 + i) * (stride / 2));
+#pragma unroll
+            for (int x = 0; x < XV; ++x) {
+                const int d = 4 * (row_lane + 32 * x);
+                v[i][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < more && d < a.c.dim) v[i][x] = __ldcg(reinterpret_cast<const float4*>(parts + (i0 + i) * stride + d));
+            }
         }
-    };
-    add(make_float2(first.x, first.y), a.own + to * a.c.dim);
-#pragma unroll 4
-    for (int i = 0; i < more; ++i) add(__ldcg(ml + i * (stride / 2)), parts + i * stride);
+        float high = best;
+#pragma unroll
+        for (int i = 0; i < N; ++i) high = fmaxf(high, p[i].x);
+        const float to_ref = high == -INFINITY ? 0.f : high, down = exp2_fast(ref - to_ref);
+        best = high, ref = to_ref;
+        total *= down;
+#pragma unroll
+        for (int x = 0; x < XV; ++x) o[x].x *= down, o[x].y *= down, o[x].z *= down, o[x].w *= down;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float w = exp2_fast(p[i].x - ref) * p[i].y;
+            total += w;
+#pragma unroll
+            for (int x = 0; x < XV; ++x)
+                o[x].x += w * v[i][x].x, o[x].y += w * v[i][x].y, o[x].z += w * v[i][x].z, o[x].w += w * v[i][x].w;
+        }
+    }
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
     for (int x = 0; x < XV; ++x) acc[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
