@@ -10,7 +10,7 @@
 // A group has as many rows as its sequences have heads and tokens, from 8 to
 // hundreds, the keys are always many: with the keys on the 128 rows of the MMA its
 // columns follow the number of rows, and neither operand of the cache has to be
-// transposed: both are converted as they lie, K K-major, V M-major.  A thread has one
+// transposed: K goes to tensor memory key by key, V to shared memory as it lies (M-major).  A thread has one
 // key: its scales are scalars of the thread, and what belongs to a query row (factor,
 // references) comes from shared memory, four at a time.  References are whole
 // numbers, shared by the four warps that hold the keys; they are set in a piece's
@@ -24,15 +24,14 @@
 // exponentials of 128 rows (16 a clock and SM); short calls are bound by the chain
 // plan -> table -> codes -> first step, and by the parts that are left to join.
 //
-// Split.  Each unit (group, head, row block) is cut into as many parts as its steps are a
-// share of all CTAs' (a piece costs as much as some steps before its first and behind
-// its last, so a CTA gets one), and the parts are one line, cut evenly among
-// the CTAs.  A piece that begins a unit leaves its result for each row, the
+// Split.  Each unit (group, head, row block) is cut into parts, as long as lets every CTA
+// have one (a piece costs as much as some steps before its first and behind its
+// last), and the parts are one line, cut evenly among the CTAs.  A piece that begins a unit leaves its result for each row, the
 // others in a slot of their CTA; the row kernel adds them to what lies behind the
 // prefix (own_ml of a row names the CTA of the first further piece and their number).
 //
 // Roles: sixteen warps for the softmax (a set of four has the keys and every fourth 16
-// columns), four convert the codes, one copies, one issues the MMAs.
+// columns), four convert K, four V, one copies, one issues the MMAs.
 #pragma once
 #include <atomic>
 
@@ -50,8 +49,13 @@ constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
 constexpr int64_t kPrefetchBytes = int64_t(64) << 20;  // half of L2
 constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
 constexpr int kSets = 4;             // of four softmax warps: 16 columns in every 64 each
-constexpr int kSoftmaxWarps = 4 * kSets, kConvertWarps = 4;
-constexpr int kPrefixThreads = (kSoftmaxWarps + kConvertWarps + 2) * 32;
+// warps by role: the softmax, then four that convert K, four that convert V, one that copies, one that issues the MMAs
+constexpr int kSoftmaxWarps = 4 * kSets, kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4, kCopyWarp = kValueWarp + 4;
+constexpr int kMmaWarp = kCopyWarp + 1, kPrefixThreads = (kCopyWarp + 4) * 32;  // two of the last four do nothing
+// Registers of a thread by role, from those that the block is launched with: their sum over its warpgroups is the same.
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 88, kConvertRegs = 48, kOtherRegs = 56;
+static_assert(kPrefixThreads == 7 * 128 && kPrefixThreads * kLaunchRegs <= 65536 &&
+              4 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs <= 7 * kLaunchRegs, "registers");
 
 template <int DP, int QP, int PP>
 struct XShape {
@@ -61,23 +65,28 @@ struct XShape {
     static constexpr int DA = DP == 256 ? 2 : 1;      // accumulators of 128 dims
     static constexpr int kQPart = NMAX * DP * 2;
     static constexpr int kPPart = kKeys * NP * 2;
-    static constexpr int kOp = kKeys * DP * 2;
+    static constexpr int kOp = kKeys * DP * 2;        // V as f16
     static constexpr int RW = DP < 128 ? DP : 128;    // bytes of a raw row
     static constexpr int RT = DP / RW;                // raw tiles of an operand
     static constexpr int kRaw = kKeys * RW;
-    static constexpr uint32_t kOps = DP == 256 ? 2 : DP == 128 ? 3 : 4;
+    static constexpr uint32_t kOps = DP == 256 ? 1 : 2;
     static constexpr int off_p = QP * kQPart;
     static constexpr int off_op = off_p + PP * kPPart;
     static constexpr int off_raw = off_op + static_cast<int>(kOps) * kOp;
     static constexpr int kExtra = 12 * 1024;          // what stands behind the raw slots
     static constexpr int kFit = (232448 - kExtra - off_raw) / kRaw;
-    static constexpr uint32_t kRaws = kFit < 8 ? kFit : 8;
-    static_assert(kFit >= 1, "shared memory");
+    static constexpr uint32_t kRaws = kFit < 8 ? kFit : 8;          // of K, then of V
+    static constexpr uint32_t kRawK = (kRaws + 1) / 2, kRawV = kRaws / 2;
+    static_assert(kRawV >= RT && kRawV >= 1, "shared memory");
+    static_assert(kOps + kRawV / RT < kScaleSteps, "scales are written while they are read");
+    // tensor memory: S^T twice, O^T (DA of NP for each part of z), K as f16 once or twice
+    static constexpr int o_at = 2 * NMAX, k_at = o_at + PP * DA * NP;
+    static constexpr uint32_t KB = (512 - k_at) / (DP / 2) >= 2 ? 2 : 1;
+    static_assert(k_at + static_cast<int>(KB) * DP / 2 <= 512, "tensor memory");
     static constexpr int off_scale = off_raw + static_cast<int>(kRaws) * kRaw;
     static constexpr int off_cols = off_scale + static_cast<int>(kScaleSteps) * 8 * 16;
     static constexpr int off_bar = off_cols + NMAX * (7 * 4 + 8 * 4 + 8);  // Columns
     static constexpr int smem = off_bar + 512;
-    static_assert(PP * DA * NP <= 256, "tensor memory");
     static_assert(smem <= 232448 && off_cols % 16 == 0 && off_bar % 8 == 0, "shared memory");
 };
 
@@ -110,7 +119,7 @@ struct PartWalk {
     int b0 = -32;
     SharedGroup g;
     Units u;
-    float steps;                       // of all units
+    float steps, longest;              // of all units; of a part
     int base = 0, chunk = 0, upto = 0; // parts
     __device__ void load(const AttnArgs& a, int from) {
         b0 = from;
@@ -125,10 +134,23 @@ struct PartWalk {
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
         return s;
     }
-    // As many parts a unit as its share of the CTAs, at least one, none shorter than kLeastSteps.
-    __device__ void cut(int ctas) {
-        u.parts = 0;
-        if (u.n) u.parts = max(1, min(static_cast<int>(static_cast<float>(u.steps) * static_cast<float>(ctas) / steps), u.steps / kLeastSteps));
+    // Parts of at most `longest` steps, none shorter than kLeastSteps.
+    __device__ int parts_of(float longest) const {
+        return u.n ? max(1, min(static_cast<int>(ceilf(static_cast<float>(u.steps) / longest)), u.steps / kLeastSteps)) : 0;
+    }
+    // Sets the length of the parts: where all units have a CTA of their own, the shortest (by eighths of the mean
+    // share) with no more parts than CTAs; else a quarter of the share.
+    __device__ void plan(const AttnArgs& a, int ctas) {
+        const float share = steps / static_cast<float>(ctas);
+        longest = fmaxf(1.f, 0.25f * share);
+        if (a.ngroups > 32 || __reduce_add_sync(~0u, u.n) > ctas) return;
+        for (int i = 8; i < 32; ++i) {
+            longest = fmaxf(1.f, share * static_cast<float>(i) * 0.125f);
+            if (__reduce_add_sync(~0u, u.n * parts_of(longest)) <= ctas) return;
+        }
+    }
+    __device__ void cut() {
+        u.parts = parts_of(longest);
         upto = u.n * u.parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -138,11 +160,11 @@ struct PartWalk {
         chunk = __shfl_sync(~0u, upto, 31);
     }
     // The unit of part `at`, its steps and parts, and which of them it is.
-    __device__ void to(const AttnArgs& a, int at, int ctas, PrefixPiece& w, int& steps_of, int& parts, int& in) {
+    __device__ void to(const AttnArgs& a, int at, PrefixPiece& w, int& steps_of, int& parts, int& in) {
         while (at >= base + chunk && b0 + 32 < a.ngroups) {
             base += chunk;
             load(a, b0 + 32);
-            cut(ctas);
+            cut();
         }
         const int which = min(31, __popc(__ballot_sync(~0u, upto <= at - base)));
         w.row0 = __shfl_sync(~0u, g.row0, which);
@@ -160,6 +182,11 @@ struct PartWalk {
         w.nc = min(per, (w.nrows - w.row_first + 15) / 16 * 16);
     }
 };
+
+template <int REGS>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 
 __device__ __forceinline__ void sync_warps(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -333,18 +360,22 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     extern __shared__ __align__(1024) unsigned char smem[];
     float4* scales = reinterpret_cast<float4*>(smem + F::off_scale);  // [kScaleSteps][8]: ks, vs, there
     Columns<NMAX>& cols = *reinterpret_cast<Columns<NMAX>*>(smem + F::off_cols);
-    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
-    uint64_t* raw_empty = raw_full + F::kRaws;
-    uint64_t* op_full = raw_empty + F::kRaws;
-    uint64_t* op_empty = op_full + F::kOps;
-    uint64_t* s_full = op_empty + F::kOps;  // [2]
+    uint64_t* kraw_full = reinterpret_cast<uint64_t*>(smem + F::off_bar);
+    uint64_t* kraw_empty = kraw_full + F::kRawK;
+    uint64_t* vraw_full = kraw_empty + F::kRawK;
+    uint64_t* vraw_empty = vraw_full + F::kRawV;
+    uint64_t* k_full = vraw_empty + F::kRawV;
+    uint64_t* k_empty = k_full + F::KB;
+    uint64_t* v_full = k_empty + F::KB;
+    uint64_t* v_empty = v_full + F::kOps;
+    uint64_t* s_full = v_empty + F::kOps;   // [2]
     uint64_t* p_full = s_full + 2;
     uint64_t* pv_done = p_full + 1;
     uint64_t* q_full = pv_done + 1;
     uint64_t* sc_full = q_full + 1;         // [kScaleSteps]
     uint64_t* unit_full = sc_full + kScaleSteps;
     uint64_t* unit_empty = unit_full + kUnitsAhead;
-    static_assert((2 * F::kRaws + 2 * F::kOps + 5 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
+    static_assert((2 * F::kRaws + 2 * F::KB + 2 * F::kOps + 5 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
     __shared__ PrefixPiece units[kUnitsAhead];
     __shared__ uint32_t tmem_slot;
     __shared__ int huge_set[kSets];
@@ -357,18 +388,20 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         return;
     }
     if (tid == 0) {
-        for (uint32_t i = 0; i < F::kRaws; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, kConvertWarps);
-        for (uint32_t i = 0; i < F::kOps; ++i) mbar_init(op_full + i, kConvertWarps), mbar_init(op_empty + i, 1);
+        for (uint32_t i = 0; i < F::kRawK; ++i) mbar_init(kraw_full + i, 1), mbar_init(kraw_empty + i, 4);
+        for (uint32_t i = 0; i < F::kRawV; ++i) mbar_init(vraw_full + i, 1), mbar_init(vraw_empty + i, 4);
+        for (uint32_t i = 0; i < F::KB; ++i) mbar_init(k_full + i, 4), mbar_init(k_empty + i, 1);
+        for (uint32_t i = 0; i < F::kOps; ++i) mbar_init(v_full + i, 4), mbar_init(v_empty + i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
         mbar_init(p_full, kSoftmaxWarps);
         mbar_init(pv_done, 1);
         mbar_init(q_full, kSoftmaxWarps);
         for (uint32_t i = 0; i < kScaleSteps; ++i) mbar_init(sc_full + i, 1);
         for (uint32_t i = 0; i < kUnitsAhead; ++i)
-            mbar_init(unit_full + i, 1), mbar_init(unit_empty + i, kSoftmaxWarps + kConvertWarps + 1);
+            mbar_init(unit_full + i, 1), mbar_init(unit_empty + i, kSoftmaxWarps + 8 + 1);
         fence_mbar_init();
     }
-    if (warp == kSoftmaxWarps + kConvertWarps + 1) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -376,7 +409,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     // the copying warp measures the line meanwhile
     PartWalk<NMAX> walk;
     int total = 0;
-    if (warp == kSoftmaxWarps + kConvertWarps) {
+    if (warp == kCopyWarp) {
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
         walk.load(a, 0);
@@ -386,13 +419,14 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             next.load(a, b);
             walk.steps += next.sum_steps();
         }
-        walk.cut(gridDim.x);
+        walk.plan(a, gridDim.x);
+        walk.cut();
         total = walk.chunk;
         for (int b = 32; b < a.ngroups; b += 32) {
             PartWalk<NMAX> next;
             next.load(a, b);
-            next.steps = walk.steps;
-            next.cut(gridDim.x);
+            next.longest = walk.longest;
+            next.cut();
             total += next.chunk;
         }
     }
@@ -400,7 +434,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t o_at = tmem + 256;  // S^T: two buffers of 128 columns; O^T: F::DA of F::NP for each part of z
+    const uint32_t o_at = tmem + F::o_at;
     // A wait that gave up ends all further waits, copies and MMAs of its warp:
     // the kernel then runs to its end within a few wait limits.
     bool dead = false;
@@ -420,180 +454,189 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         return !dead && w.tokens >= 0;
     };
 
-    if (warp == kSoftmaxWarps + kConvertWarps) {
-        // ---------------------------------------------------------- copies
-        const Line line(total, gridDim.x);
-        int at = 0, end = 0;
-        if (static_cast<int>(blockIdx.x) < line.ctas)
-            at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
-        uint32_t o = 0, g = 0;  // raw tiles and steps over the life of the kernel
-        uint32_t sent = 0;      // raw tiles whose copies were issued
-        for (;; ++turn) {
-            const uint32_t slot = turn % kUnitsAhead;
-            if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
-            const bool there = !dead && at < end;
-            if (there) {
-                int steps, parts, in;
-                walk.to(a, at, gridDim.x, w, steps, parts, in);
-                const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
-                w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
-                w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
-                w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
-                w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
-                at += last - in;
-            } else {
-                w.tokens = -1;
+    // a warpgroup's warps give or take registers by one instruction
+    if (warp >= kCopyWarp) {
+        give_registers<kOtherRegs>();
+        if (warp == kCopyWarp) {
+            // ---------------------------------------------------------- copies
+            const Line line(total, gridDim.x);
+            int at = 0, end = 0;
+            if (static_cast<int>(blockIdx.x) < line.ctas)
+                at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
+            uint32_t o = 0, g = 0;  // raw tiles of K, and of V, and steps over the life of the kernel
+            uint32_t sent_k = 0, sent_v = 0;  // raw tiles whose copies were issued
+            auto copy = [&](bool v, int tile, int tok, int id, unsigned valid, uint32_t n) {
+                const uint32_t slots = v ? F::kRawV : F::kRawK, slot = n % slots;
+                uint64_t* full = (v ? vraw_full : kraw_full) + slot;
+                if (n >= slots) wait((v ? vraw_empty : kraw_empty) + slot, n / slots - 1);
+                if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
+                __syncwarp();
+                if (id >= 0 && !dead)
+                    tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + lane * 16 * F::RW, v ? &vmap : &kmap,
+                                tile * F::RW, tok, w.h, id, full);
+                if (!dead) (v ? sent_v : sent_k) = n + 1;
+            };
+            for (;; ++turn) {
+                const uint32_t slot = turn % kUnitsAhead;
+                if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
+                const bool there = !dead && at < end;
+                if (there) {
+                    int steps, parts, in;
+                    walk.to(a, at, w, steps, parts, in);
+                    const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
+                    w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
+                    w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
+                    w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
+                    w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
+                    at += last - in;
+                } else {
+                    w.tokens = -1;
+                }
+                if (lane == 0) {
+                    units[slot] = w;
+                    arrive_on(unit_full + slot);
+                }
+                __syncwarp();
+                if (!there) break;
+                const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
+                auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
+                    int id = -1;
+                    f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
+                    if (lane < 8 && tok < w.tokens) {
+                        id = table[tok >> c.log2p];
+                        if (id >= 0 && id < c.pages) {
+                            const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
+                            f.x = __ldg(c.ks + s);
+                            f.y = __ldg(c.vs + s);
+                            f.z = 1.f;
+                        } else {
+                            id = -1;
+                            atomicOr(a.status, kStatusBounds);
+                        }
+                    }
+                    return id;
+                };
+                float4 f;
+                int id = look(w.j0, f);
+                for (int j = w.j0; j < w.j1; ++j, ++g) {
+                    const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
+                    const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
+                    if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
+                    __syncwarp();
+                    if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
+                    for (int t = 0; t < F::RT; ++t) copy(false, t, tok, id, valid, o + t);
+                    for (int t = 0; t < F::RT; ++t) copy(true, t, tok, id, valid, o + t);
+                    o += F::RT;
+                    if (j + 1 < w.j1) id = look(j + 1, f);
+                }
             }
-            if (lane == 0) {
-                units[slot] = w;
-                arrive_on(unit_full + slot);
+            if (dead) {  // the copies in flight: shared memory is theirs until they land
+                for (uint32_t x = sent_k > F::kRawK ? sent_k - F::kRawK : 0; x < sent_k; ++x)
+                    (void)mbar_wait_bounded(kraw_full + x % F::kRawK, (x / F::kRawK) & 1u, a.status);
+                for (uint32_t x = sent_v > F::kRawV ? sent_v - F::kRawV : 0; x < sent_v; ++x)
+                    (void)mbar_wait_bounded(vraw_full + x % F::kRawV, (x / F::kRawV) & 1u, a.status);
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------- MMAs
+            // What the sequences hold behind the prefix comes to L2 meanwhile, for the launch behind this one, as far
+            // as L2 keeps it: a lane a page.
+            const uint32_t page_bytes = static_cast<uint32_t>(c.heads * c.dim) << c.log2p;
+            int64_t room = kPrefetchBytes / (2 * static_cast<int64_t>(page_bytes) * gridDim.x);
+            for (int b = blockIdx.x; b < a.batch && room > 0; b += gridDim.x) {
+                const int64_t len = min(static_cast<int64_t>(max(a.lens[b], 0)), a.width << c.log2p);
+                const int64_t from = max(a.skip[b], 0) >> c.log2p;
+                const int64_t pages = min((len + (1 << c.log2p) - 1) >> c.log2p, from + room);
+                for (int64_t x = from + lane; x < pages; x += 32) {
+                    const int id = a.table[b * a.width + x];
+                    if (id < 0 || id >= c.pages) continue;
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.k + id * c.page_stride), "r"(page_bytes) : "memory");
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.v + id * c.page_stride), "r"(page_bytes) : "memory");
+                }
+                room -= max(int64_t(0), pages - from);
             }
             __syncwarp();
-            if (!there) break;
-            const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
-            auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
-                int id = -1;
-                f = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
-                if (lane < 8 && tok < w.tokens) {
-                    id = table[tok >> c.log2p];
-                    if (id >= 0 && id < c.pages) {
-                        const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
-                        f.x = __ldg(c.ks + s);
-                        f.y = __ldg(c.vs + s);
-                        f.z = 1.f;
-                    } else {
-                        id = -1;
-                        atomicOr(a.status, kStatusBounds);
-                    }
-                }
-                return id;
-            };
-            float4 f;
-            int id = look(w.j0, f);
-            for (int j = w.j0; j < w.j1; ++j, ++g) {
-                const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
-                const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
-                if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
-                __syncwarp();
-                if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
+            uint32_t g = 0, qs = 0;  // steps and queries taken
+            while (next_unit()) {
+                const int steps = w.j1 - w.j0;
+                const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn((w.nc + 63) / 64 * 64);
+                wait(q_full, qs);
+                for (int j = 0; j <= steps; ++j) {
+                    if (j < steps) {
+                        const uint32_t n = g + j, kb = n % F::KB, st = tmem + (n & 1) * NMAX;
+                        wait(k_full + kb, n / F::KB);
+                        fence_after();
+                        if (lane == 0 && !dead) {
+                            const uint32_t ka = tmem + F::k_at + kb * (DP / 2);
 #pragma unroll
-                for (int t = 0; t < 2 * F::RT; ++t, ++o) {
-                    const uint32_t slot = o % F::kRaws;
-                    if (o >= F::kRaws) wait(raw_empty + slot, o / F::kRaws - 1);
-                    if (lane == 0) mbar_arrive_expect_tx(raw_full + slot, valid * 16 * F::RW);
-                    __syncwarp();
-                    if (id >= 0 && !dead)
-                        tma_load_4d(smem + F::off_raw + slot * F::kRaw + lane * 16 * F::RW, t < F::RT ? &kmap : &vmap,
-                                    (t % F::RT) * F::RW, tok, w.h, id, raw_full + slot);
-                    if (!dead) sent = o + 1;
-                }
-                if (j + 1 < w.j1) id = look(j + 1, f);
-            }
-        }
-        if (dead)  // the copies in flight: shared memory is theirs until they land
-            for (uint32_t x = sent > F::kRaws ? sent - F::kRaws : 0; x < sent; ++x)
-                (void)mbar_wait_bounded(raw_full + x % F::kRaws, (x / F::kRaws) & 1u, a.status);
-    } else if (warp == kSoftmaxWarps + kConvertWarps + 1) {
-        // ---------------------------------------------------------- MMAs
-        // What the sequences hold behind the prefix comes to L2 meanwhile, for the launch behind this one, as far
-        // as L2 keeps it: a lane a page.
-        const uint32_t page_bytes = static_cast<uint32_t>(c.heads * c.dim) << c.log2p;
-        int64_t room = kPrefetchBytes / (2 * static_cast<int64_t>(page_bytes) * gridDim.x);
-        for (int b = blockIdx.x; b < a.batch && room > 0; b += gridDim.x) {
-            const int64_t len = min(static_cast<int64_t>(max(a.lens[b], 0)), a.width << c.log2p);
-            const int64_t from = max(a.skip[b], 0) >> c.log2p;
-            const int64_t pages = min((len + (1 << c.log2p) - 1) >> c.log2p, from + room);
-            for (int64_t x = from + lane; x < pages; x += 32) {
-                const int id = a.table[b * a.width + x];
-                if (id < 0 || id >= c.pages) continue;
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.k + id * c.page_stride), "r"(page_bytes) : "memory");
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.v + id * c.page_stride), "r"(page_bytes) : "memory");
-            }
-            room -= max(int64_t(0), pages - from);
-        }
-        __syncwarp();
-        uint32_t o = 0, g = 0, qs = 0;  // operands, steps and queries taken
-        while (next_unit()) {
-            const int steps = w.j1 - w.j0;
-            const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn((w.nc + 63) / 64 * 64);
-            wait(q_full, qs);
-            for (int j = 0; j <= steps; ++j) {
-                if (j < steps) {
-                    const uint32_t ko = o + 2 * j, st = tmem + ((g + j) & 1) * 128;
-                    wait(op_full + ko % F::kOps, ko / F::kOps);
-                    fence_after();
-                    if (lane == 0 && !dead) {
-                        const uint64_t kb = operand_desc(smem_u32(smem + F::off_op + (ko % F::kOps) * F::kOp));
+                            for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
+                                const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
 #pragma unroll
-                        for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
-                            const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
-#pragma unroll
-                            for (int ks = 0; ks < DP / 16; ++ks)
-                                mma_ss(st, kb + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                                       qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
-                                       p < QP - 1 || ks > 0 ? 1u : 0u);
-                        }
-                        commit_to(s_full + ((g + j) & 1));
-                        commit_to(op_empty + ko % F::kOps);
-                    }
-                    __syncwarp();
-                }
-                if (j > 0) {
-                    const uint32_t vo = o + 2 * j - 1;
-                    wait(op_full + vo % F::kOps, vo / F::kOps);
-                    wait(p_full, g + j - 1);
-                    fence_after();
-                    if (lane == 0 && !dead) {
-#pragma unroll
-                        for (int acc = 0; acc < F::DA; ++acc) {
-                            const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + (vo % F::kOps) * F::kOp + acc * 32768), 16384);
-#pragma unroll
-                            for (int p = PP - 1; p >= 0; --p) {
-                                const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + p * F::kPPart), 16384);
-#pragma unroll
-                                for (int ks = 0; ks < kKeys / 16; ++ks)
-                                    mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
-                                           j > 1 || ks > 0 ? 1u : 0u);
+                                for (int ks = 0; ks < DP / 16; ++ks)
+                                    mma_ts(st, ka + ks * 8, qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
+                                           p < QP - 1 || ks > 0 ? 1u : 0u);
                             }
+                            commit_to(s_full + (n & 1));
+                            commit_to(k_empty + kb);
                         }
-                        commit_to(pv_done);
-                        commit_to(op_empty + vo % F::kOps);
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (j > 0) {
+                        const uint32_t n = g + j - 1, os = n % F::kOps;
+                        wait(v_full + os, n / F::kOps);
+                        wait(p_full, n);
+                        fence_after();
+                        if (lane == 0 && !dead) {
+#pragma unroll
+                            for (int acc = 0; acc < F::DA; ++acc) {
+                                const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + os * F::kOp + acc * 32768), 16384);
+#pragma unroll
+                                for (int p = PP - 1; p >= 0; --p) {
+                                    const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + p * F::kPPart), 16384);
+#pragma unroll
+                                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                                        mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
+                                               j > 1 || ks > 0 ? 1u : 0u);
+                                }
+                            }
+                            commit_to(pv_done);
+                            commit_to(v_empty + os);
+                        }
+                        __syncwarp();
+                    }
                 }
+                g += steps;
+                ++qs;
             }
-            o += 2 * steps;
-            g += steps;
-            ++qs;
         }
-    } else if (warp >= kSoftmaxWarps) {
-        // ---------------------------------------------------------- 8 bits -> f16 operands
-        const int ct = tid - kSoftmaxWarps * 32;
-        uint32_t o = 0, r = 0, g = 0;  // operands, raw tiles and steps
+    } else if (warp >= kValueWarp) {
+        // ---------------------------------------------------------- V: 8 bits -> f16 in shared memory, as it lies
+        give_registers<kConvertRegs>();
+        const int ct = tid - kValueWarp * 32;
+        uint32_t r = 0, g = 0;  // raw tiles and steps
         while (next_unit()) {
             for (int j = w.j0; j < w.j1; ++j, ++g) {
                 const float4* sc = scales + (g % kScaleSteps) * 8;
                 wait(sc_full + g % kScaleSteps, g / kScaleSteps);
                 const bool whole = __all_sync(~0u, sc[lane & 7].z != 0.f);  // no page is missing
+                const uint32_t os = g % F::kOps;
+                unsigned char* op = smem + F::off_op + os * F::kOp;
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++o) {
-                    const uint32_t os = o % F::kOps;
-                    if (o >= F::kOps) wait(op_empty + os, o / F::kOps - 1);
-                    unsigned char* op = smem + F::off_op + os * F::kOp;
+                for (int t = 0; t < F::RT; ++t, ++r) {
+                    const uint32_t rs = r % F::kRawV;
+                    wait(vraw_full + rs, r / F::kRawV);
+                    if (t == 0 && g >= F::kOps) wait(v_empty + os, g / F::kOps - 1);
+                    const unsigned char* raw = smem + F::off_raw + (F::kRawK + rs) * F::kRaw;
+                    constexpr int C16 = F::RW / 16;
 #pragma unroll
-                    for (int t = 0; t < F::RT; ++t, ++r) {
-                        const uint32_t rs = r % F::kRaws;
-                        wait(raw_full + rs, r / F::kRaws);
-                        const unsigned char* raw = smem + F::off_raw + rs * F::kRaw;
-                        constexpr int C16 = F::RW / 16;
-                        uint4 x[C16];
+                    for (int i0 = 0; i0 < C16; i0 += 4) {
+                        uint4 x[4];
 #pragma unroll
-                        for (int it = 0; it < C16; ++it)
-                            x[it] = *reinterpret_cast<const uint4*>(raw + (it * 128 + ct) * 16);
+                        for (int it = 0; it < 4; ++it)
+                            x[it] = *reinterpret_cast<const uint4*>(raw + ((i0 + it) * 128 + ct) * 16);
 #pragma unroll
-                        for (int it = 0; it < C16; ++it) {
-                            const int item = it * 128 + ct, token = item / C16, c16 = item % C16;
+                        for (int it = 0; it < 4; ++it) {
+                            const int item = (i0 + it) * 128 + ct, token = item / C16, c16 = item % C16;
                             if (!whole && sc[token >> 4].z == 0.f) x[it] = make_uint4(0, 0, 0, 0);
                             uint32_t h[8];
                             const uint32_t in[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
@@ -609,17 +652,66 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                     second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0) arrive_on(raw_empty + rs);
                     }
-                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_on(op_full + os);
+                    if (lane == 0) arrive_on(vraw_empty + rs);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_on(v_full + os);
+            }
+        }
+    } else if (warp >= kKeyWarp) {
+        // ---------------------------------------------------------- K: 8 bits -> f16 in tensor memory, a thread a key
+        give_registers<kConvertRegs>();
+        const int key = tid - kKeyWarp * 32;
+        const int turn16 = F::RW == 64 ? (key >> 1) & 3 : key & 7;  // the copy's swizzle: no two of eight rows in a bank
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t r = 0, g = 0;  // raw tiles and steps
+        while (next_unit()) {
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                wait(sc_full + g % kScaleSteps, g / kScaleSteps);
+                const bool there = scales[(g % kScaleSteps) * 8 + (key >> 4)].z != 0.f;
+                const uint32_t kb = g % F::KB;
+#pragma unroll 1
+                for (int t = 0; t < F::RT; ++t, ++r) {
+                    const uint32_t rs = r % F::kRawK;
+                    wait(kraw_full + rs, r / F::kRawK);
+                    if (t == 0 && g >= F::KB) {
+                        wait(k_empty + kb, g / F::KB - 1);
+                        fence_after();
+                    }
+                    const unsigned char* raw = smem + F::off_raw + rs * F::kRaw + key * F::RW;
+#pragma unroll
+                    for (int c = 0; c < F::RW / 32; ++c) {
+                        uint4 x[2];
+                        uint32_t h[16];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            x[i] = *reinterpret_cast<const uint4*>(raw + (((c * 2 + i) ^ turn16) << 4));
+                            if (!there) x[i] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            k_codes<INT8>(x[i].x, h[8 * i], h[8 * i + 1]);
+                            k_codes<INT8>(x[i].y, h[8 * i + 2], h[8 * i + 3]);
+                            k_codes<INT8>(x[i].z, h[8 * i + 4], h[8 * i + 5]);
+                            k_codes<INT8>(x[i].w, h[8 * i + 6], h[8 * i + 7]);
+                        }
+                        tmem_store16(tmem + F::k_at + kb * (DP / 2) + lanes + t * (F::RW / 2) + c * 16, h);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive_on(kraw_empty + rs);
+                }
+                tmem_stored();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_on(k_full + kb);
             }
         }
     } else {
         // ---------------------------------------------------------- softmax, a thread a key and a set's columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int set = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wid = 2 + set;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t g = 0;
@@ -709,7 +801,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 const float4 mine = scales[(g % kScaleSteps) * 8 + (key >> 4)];
                 const float ks = mine.x, vs = mine.y;
                 const bool there = mine.z != 0.f, whole = __all_sync(~0u, there);
-                const uint32_t st = tmem + (g & 1) * 128 + lanes;
+                const uint32_t st = tmem + (g & 1) * NMAX + lanes;
                 bool mine_now = false;  // z and O are this step's
                 auto take = [&]() {
                     if (!mine_now && g > 0) wait(pv_done, g - 1);
@@ -872,7 +964,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     }
     fence_before();
     __syncthreads();
-    if (warp == kSoftmaxWarps + kConvertWarps + 1) {
+    if (warp == kMmaWarp) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
@@ -885,7 +977,7 @@ int launch_one(AttnArgs& a, cudaStream_t s) {
     const int sms = sm_count(dev);
     if (sms <= 0) return cuda_fail(cudaGetLastError());
     CUtensorMap kmap, vmap;
-    if (!encode_cache(&kmap, a.c, a.c.k, F::RW, 16, false) || !encode_cache(&vmap, a.c, a.c.v, F::RW, 16, false))
+    if (!encode_cache(&kmap, a.c, a.c.k, F::RW, 16, true) || !encode_cache(&vmap, a.c, a.c.v, F::RW, 16, false))
         return cuda_fail(cudaGetLastError());
     static std::atomic<bool> done[64];
     auto kern = qg_attn_prefix_kernel<DP, QP, PP, INT8>;
