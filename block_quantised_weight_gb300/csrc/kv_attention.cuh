@@ -161,12 +161,10 @@ __device__ __forceinline__ float4 q4_values(uint4 v, int type) {
 
 int launch_attn_rows(const AttnArgs& a, bool int8, cudaStream_t s);
 int launch_attn_rows_shared(const AttnArgs& a, bool int8, cudaStream_t s);
-// Query rows of a unit of the prefix: as many as shared memory holds operands for.
+// Query rows of a unit of the prefix (kv_prefix.cuh).
 constexpr int kMaxPrefixCtas = 160;
-__host__ __device__ constexpr int prefix_rows(int dp, int q_parts, int p_parts) {
-    return dp == 256 ? 32 : q_parts * p_parts == 1 ? 128 : 64;
-}
-static_assert(int64_t(kMaxPrefixCtas) * 128 * (128 + 2) * 4 <= kWsOwn - kWsSlots &&
+__host__ __device__ constexpr int prefix_rows(int dp) { return dp == 256 ? 32 : 64; }
+static_assert(int64_t(kMaxPrefixCtas) * 64 * (128 + 2) * 4 <= kWsOwn - kWsSlots &&
               int64_t(kMaxPrefixCtas) * 32 * (256 + 2) * 4 <= kWsOwn - kWsSlots, "slots exceed the workspace");
 // Bytes of the results kept for each of `rows` rows.
 inline int64_t own_bytes(int64_t rows, int q_heads, int dim) { return rows * q_heads * (dim * int64_t(4) + 16); }

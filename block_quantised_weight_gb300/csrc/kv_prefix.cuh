@@ -1,37 +1,40 @@
 // Attention over a prefix that sequences share: all rows of a group over the
 // same tokens, each read once, on the tcgen05 tensor cores.
 //
-// Mathematics: kv_rows.cuh's, with both products transposed.  A CTA takes up to NMAX
+// Mathematics: kv_rows.cuh's, with both products transposed.  A CTA takes up to 64 (32 from 129 dims on)
 // query rows (tokens x heads of a group, a multiple of 16) of one cache head and
 // walks the keys in steps of 128:
 //   S^T = K q^T     128 keys x rows, in tensor memory
-//   p = 2^(S f - m), f = scale * ks,   z = p * vs * 2^k as f16, in shared memory
-//   O^T += V^T z    dims x rows, in tensor memory
+//   e = 2^(S f - m + k), f = scale * ks,   z = e * vs as f16, in shared memory
+//   O^T += V^T z    dims x rows, in tensor memory,   l += e
 // A group has as many rows as its sequences have heads and tokens, from 8 to
 // hundreds, the keys are always many: with the keys on the 128 rows of the MMA its
 // columns follow the number of rows, and neither operand of the cache has to be
-// transposed: K goes to tensor memory key by key, V to shared memory as it lies (M-major).  A thread has one
-// key: its scales are scalars of the thread, and what belongs to a query row (factor,
-// references) comes from shared memory, four at a time.  References are whole
-// numbers, shared by the four warps that hold the keys; they are set in a piece's
-// first step, so that z is at most 2^6 (k = 6 less the order of p * vs), and move
-// only when a z would pass 2^15 or a p 2^20: 16 columns at a time are tried as
-// if they held, one vote of the four warps decides.  Two parts of z: the second is 2^11
-// times what the first leaves, with sums of its own, so that small weights keep their
-// bits down to 2^-40 of a row's largest (one part: 2^-29).
+// transposed: K goes to tensor memory key by key, V to shared memory as it lies (M-major).
+// A thread has one key and 16 columns: the key's scales are scalars of the thread, and what
+// belongs to a query row (factor, references) comes from shared memory, four at a
+// time.  References are whole numbers, shared by the four warps that hold the
+// keys; they are set in a piece's first step, so that z is at most 2^6 (k = 6 less
+// the order of p * vs), and move only when a z would pass 2^15: 16 columns are tried
+// as if they held, one vote of the four warps decides.  Scores from 2^22 on, and scales
+// whose k fp32 sums would not hold, take a slower way.  Two parts of z: the second is
+// 2^11 times what the first leaves, with sums of its own, so that small weights keep
+// their bits down to 2^-40 of a row's largest (one part: 2^-29).
 //
-// Bound.  For up to 128 rows the codes' stream (32 KB a step and SM at 128 dims) takes as long as the
-// exponentials of 128 rows (16 a clock and SM); short calls are bound by the chain
+// Bound.  For few rows the stream of codes; for 64 a step's traffic of shared memory: the
+// copies, reading and writing of the codes and both products' operands move 190 KB a step at
+// 128 dims, 1500 clocks, and the warps' waits for one another.  Short calls are bound by the chain
 // plan -> table -> codes -> first step, and by the parts that are left to join.
 //
 // Split.  Each unit (group, head, row block) is cut into parts, as long as lets every CTA
 // have one (a piece costs as much as some steps before its first and behind its
-// last), and the parts are one line, cut evenly among the CTAs.  A piece that begins a unit leaves its result for each row, the
-// others in a slot of their CTA; the row kernel adds them to what lies behind the
-// prefix (own_ml of a row names the CTA of the first further piece and their number).
+// last), and the parts are one line, cut evenly among the CTAs.  A piece that begins a unit
+// leaves its result for each row, the others in a slot of their CTA; the row
+// kernel adds them to what lies behind the prefix (own_ml of a row names the CTA of
+// the first further piece and their number).
 //
-// Roles: sixteen warps for the softmax (a set of four has the keys and every fourth 16
-// columns), four convert K, four V, one copies, one issues the MMAs.
+// Roles: sixteen warps for the softmax (a set of four has the keys, and 16 columns),
+// four convert K, four V, one copies, one issues the MMAs.
 #pragma once
 #include <atomic>
 
@@ -48,20 +51,16 @@ constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
 constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
 constexpr int64_t kPrefetchBytes = int64_t(64) << 20;  // half of L2
 constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
-constexpr int kSets = 4;             // of four softmax warps: 16 columns in every 64 each
+constexpr int kSets = 4;             // of four softmax warps, 16 columns each
 // warps by role: the softmax, then four that convert K, four that convert V, one that copies, one that issues the MMAs
 constexpr int kSoftmaxWarps = 4 * kSets, kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4, kCopyWarp = kValueWarp + 4;
-constexpr int kMmaWarp = kCopyWarp + 1, kPrefixThreads = (kCopyWarp + 4) * 32;  // two of the last four do nothing
-// Registers of a thread by role, from those that the block is launched with: their sum over its warpgroups is the same.
-constexpr int kLaunchRegs = 72, kSoftmaxRegs = 88, kConvertRegs = 48, kOtherRegs = 56;
-static_assert(kPrefixThreads == 7 * 128 && kPrefixThreads * kLaunchRegs <= 65536 &&
-              4 * kSoftmaxRegs + 2 * kConvertRegs + kOtherRegs <= 7 * kLaunchRegs, "registers");
+constexpr int kMmaWarp = kCopyWarp + 1, kPrefixThreads = (kMmaWarp + 1) * 32;
 
 template <int DP, int QP, int PP>
 struct XShape {
-    static constexpr int NMAX = prefix_rows(DP, QP, PP);
-    static constexpr int NP = NMAX < 64 ? 64 : NMAX;  // columns of the second product: whole swizzle atoms
-    static constexpr int NC = (NMAX + 16 * kSets - 1) / (16 * kSets);  // times 16 columns of a set
+    static constexpr int NMAX = prefix_rows(DP);
+    static constexpr int NP = 64;                     // columns of the second product: a whole swizzle atom
+    static constexpr int PB = PP == 1 || DP == 64 ? 2 : 1;  // buffers of z, as shared memory has room
     static constexpr int DA = DP == 256 ? 2 : 1;      // accumulators of 128 dims
     static constexpr int kQPart = NMAX * DP * 2;
     static constexpr int kPPart = kKeys * NP * 2;
@@ -71,7 +70,7 @@ struct XShape {
     static constexpr int kRaw = kKeys * RW;
     static constexpr uint32_t kOps = DP == 256 ? 1 : 2;
     static constexpr int off_p = QP * kQPart;
-    static constexpr int off_op = off_p + PP * kPPart;
+    static constexpr int off_op = off_p + PB * PP * kPPart;
     static constexpr int off_raw = off_op + static_cast<int>(kOps) * kOp;
     static constexpr int kExtra = 12 * 1024;          // what stands behind the raw slots
     static constexpr int kFit = (232448 - kExtra - off_raw) / kRaw;
@@ -183,11 +182,6 @@ struct PartWalk {
     }
 };
 
-template <int REGS>
-__device__ __forceinline__ void give_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-
 __device__ __forceinline__ void sync_warps(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -207,17 +201,17 @@ __device__ __forceinline__ uint32_t hmax2_of(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Column sums over the 32 lanes: lane i gets the sum of column i.
-__device__ __forceinline__ float add_columns(float (&v)[32]) {
+// Sum of each of 16 columns over the 32 lanes: lanes i and i + 16 get that of column i.
+__device__ __forceinline__ float add_columns(float (&v)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1)
+    for (int w = 8; w > 0; w >>= 1)
 #pragma unroll
         for (int i = 0; i < w; ++i) {
             const float give = lane & w ? v[i] : v[i + w], keep = lane & w ? v[i + w] : v[i];
             v[i] = keep + __shfl_xor_sync(~0u, give, w);
         }
-    return v[0];
+    return v[0] + __shfl_xor_sync(~0u, v[0], 16);
 }
 
 // Largest of each of 16 columns over the 32 lanes: lanes i and i + 16 get that of column i.
@@ -233,11 +227,15 @@ __device__ __forceinline__ float max_columns(float (&v)[16]) {
     return fmaxf(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
+// The order k of z, and what of it the sums of e = p 2^ke take: as much as leaves them in fp32's range.
+__device__ __forceinline__ int order_z(int d) { return min(kBase - d, kMostK); }
+__device__ __forceinline__ int order_e(int k) { return min(max(k, -60), 90); }
+
 // What belongs to the columns (query rows) of a unit, in shared memory.
 template <int NMAX>
 struct Columns {
     float fac[NMAX];               // factor of the scores
-    float nm[NMAX], pk[NMAX];      // less the reference, 2^k
+    float nm[NMAX], pk[NMAX];      // ke less the reference, 2^(k - ke)
     float mul1[NMAX], mul2[NMAX];  // two factors
     float ref[NMAX];
     int refd[NMAX];
@@ -281,15 +279,16 @@ __device__ __forceinline__ void first_references(Columns<NMAX>& cols, int* huge_
         const int col = cb + quarter * 4 + lane;
         const float mn = fmaxf(kNoRef, top[0]);
         const int dn = max(kNoOrder, order_of(high[0] - mn));
-        cols.ref[col] = mn, cols.nm[col] = -mn, cols.refd[col] = dn;
-        cols.pk[col] = pow2i(max(min(kBase - dn, kMostK), -126));
-        if (mn > kNoRef && fabsf(mn) >= kHugeScore) *reinterpret_cast<volatile int*>(huge_at) = 1;
+        const int k = order_z(dn), ke = order_e(k);
+        cols.ref[col] = mn, cols.refd[col] = dn;
+        cols.nm[col] = static_cast<float>(ke) - mn, cols.pk[col] = pow2i(k - ke);
+        if ((k != ke && dn > kNoOrder) || (mn > kNoRef && fabsf(mn) >= kHugeScore)) *reinterpret_cast<volatile int*>(huge_at) = 1;
     }
     sync_warps(barrier, 128);
 }
 
 // New references of the 16 columns from cb on, by the four warps of a set: mul1 is what the sums
-// of z, mul2 what those of p are to be multiplied by.  evs: the order of the key's vs.  Out of line: the
+// of z, mul2 what those of e are to be multiplied by.  evs: the order of the key's vs.  Out of line: the
 // way there is rare.
 template <int NMAX>
 __device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
@@ -330,7 +329,7 @@ __device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, u
     if (key < 16) {
         const float m = cols.ref[col], mn = fmaxf(m, largest(cols.tops, col));
         down = order_of(m - mn);
-        cols.ref[col] = mn, cols.nm[col] = -mn;
+        cols.ref[col] = mn;
         if (mn > kNoRef && fabsf(mn) >= kHugeScore) *huge_at = 1;
     }
     sync_warps(barrier, 128);
@@ -343,11 +342,12 @@ __device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, u
         const int d = cols.refd[col];
         const float high = largest(cols.tops_v, col);
         const int dn = max(max(d + down, kNoOrder), order_of(huge ? high : high - cols.ref[col]));
-        const int k_old = min(kBase - d, kMostK), k_new = min(kBase - dn, kMostK);
+        const int k_old = order_z(d), k_new = order_z(dn), e_new = order_e(k_new);
         cols.mul1[col] = pow2i(k_new - k_old + down);
-        cols.mul2[col] = pow2i(down);
+        cols.mul2[col] = pow2i(e_new - order_e(k_old) + down);
         cols.refd[col] = dn;
-        cols.pk[col] = pow2i(max(k_new, -126));
+        cols.nm[col] = static_cast<float>(e_new) - cols.ref[col], cols.pk[col] = pow2i(k_new - e_new);
+        if (k_new != e_new && dn > kNoOrder) *huge_at = 1;  // and more than zeros have come
     }
     sync_warps(barrier, 128);
 }
@@ -369,13 +369,13 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     uint64_t* v_full = k_empty + F::KB;
     uint64_t* v_empty = v_full + F::kOps;
     uint64_t* s_full = v_empty + F::kOps;   // [2]
-    uint64_t* p_full = s_full + 2;
-    uint64_t* pv_done = p_full + 1;
-    uint64_t* q_full = pv_done + 1;
+    uint64_t* p_full = s_full + 2;          // [2]
+    uint64_t* pv_done = p_full + 2;         // [2]
+    uint64_t* q_full = pv_done + 2;
     uint64_t* sc_full = q_full + 1;         // [kScaleSteps]
     uint64_t* unit_full = sc_full + kScaleSteps;
     uint64_t* unit_empty = unit_full + kUnitsAhead;
-    static_assert((2 * F::kRaws + 2 * F::KB + 2 * F::kOps + 5 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
+    static_assert((2 * F::kRaws + 2 * F::KB + 2 * F::kOps + 7 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
     __shared__ PrefixPiece units[kUnitsAhead];
     __shared__ uint32_t tmem_slot;
     __shared__ int huge_set[kSets];
@@ -393,8 +393,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         for (uint32_t i = 0; i < F::KB; ++i) mbar_init(k_full + i, 4), mbar_init(k_empty + i, 1);
         for (uint32_t i = 0; i < F::kOps; ++i) mbar_init(v_full + i, 4), mbar_init(v_empty + i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
-        mbar_init(p_full, kSoftmaxWarps);
-        mbar_init(pv_done, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(p_full + i, kSoftmaxWarps), mbar_init(pv_done + i, 1);
         mbar_init(q_full, kSoftmaxWarps);
         for (uint32_t i = 0; i < kScaleSteps; ++i) mbar_init(sc_full + i, 1);
         for (uint32_t i = 0; i < kUnitsAhead; ++i)
@@ -454,164 +453,159 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         return !dead && w.tokens >= 0;
     };
 
-    // a warpgroup's warps give or take registers by one instruction
-    if (warp >= kCopyWarp) {
-        give_registers<kOtherRegs>();
-        if (warp == kCopyWarp) {
-            // ---------------------------------------------------------- copies
-            const Line line(total, gridDim.x);
-            int at = 0, end = 0;
-            if (static_cast<int>(blockIdx.x) < line.ctas)
-                at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
-            uint32_t o = 0, g = 0;  // raw tiles of K, and of V, and steps over the life of the kernel
-            uint32_t sent_k = 0, sent_v = 0;  // raw tiles whose copies were issued
-            auto copy = [&](bool v, int tile, int tok, int id, unsigned valid, uint32_t n) {
-                const uint32_t slots = v ? F::kRawV : F::kRawK, slot = n % slots;
-                uint64_t* full = (v ? vraw_full : kraw_full) + slot;
-                if (n >= slots) wait((v ? vraw_empty : kraw_empty) + slot, n / slots - 1);
-                if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
-                __syncwarp();
-                if (id >= 0 && !dead)
-                    tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + lane * 16 * F::RW, v ? &vmap : &kmap,
-                                tile * F::RW, tok, w.h, id, full);
-                if (!dead) (v ? sent_v : sent_k) = n + 1;
-            };
-            for (;; ++turn) {
-                const uint32_t slot = turn % kUnitsAhead;
-                if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
-                const bool there = !dead && at < end;
-                if (there) {
-                    int steps, parts, in;
-                    walk.to(a, at, w, steps, parts, in);
-                    const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
-                    w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
-                    w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
-                    w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
-                    w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
-                    at += last - in;
-                } else {
-                    w.tokens = -1;
-                }
-                if (lane == 0) {
-                    units[slot] = w;
-                    arrive_on(unit_full + slot);
-                }
-                __syncwarp();
-                if (!there) break;
-                const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
-                auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
-                    int id = -1;
-                    f = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
-                    if (lane < 8 && tok < w.tokens) {
-                        id = table[tok >> c.log2p];
-                        if (id >= 0 && id < c.pages) {
-                            const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
-                            f.x = __ldg(c.ks + s);
-                            f.y = __ldg(c.vs + s);
-                            f.z = 1.f;
-                        } else {
-                            id = -1;
-                            atomicOr(a.status, kStatusBounds);
-                        }
-                    }
-                    return id;
-                };
-                float4 f;
-                int id = look(w.j0, f);
-                for (int j = w.j0; j < w.j1; ++j, ++g) {
-                    const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
-                    const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
-                    if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
-                    __syncwarp();
-                    if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
-                    for (int t = 0; t < F::RT; ++t) copy(false, t, tok, id, valid, o + t);
-                    for (int t = 0; t < F::RT; ++t) copy(true, t, tok, id, valid, o + t);
-                    o += F::RT;
-                    if (j + 1 < w.j1) id = look(j + 1, f);
-                }
+    if (warp == kCopyWarp) {
+        // ---------------------------------------------------------- copies
+        const Line line(total, gridDim.x);
+        int at = 0, end = 0;
+        if (static_cast<int>(blockIdx.x) < line.ctas)
+            at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
+        uint32_t o = 0, g = 0;  // raw tiles of K, and of V, and steps over the life of the kernel
+        uint32_t sent_k = 0, sent_v = 0;  // raw tiles whose copies were issued
+        auto copy = [&](bool v, int tile, int tok, int id, unsigned valid, uint32_t n) {
+            const uint32_t slots = v ? F::kRawV : F::kRawK, slot = n % slots;
+            uint64_t* full = (v ? vraw_full : kraw_full) + slot;
+            if (n >= slots) wait((v ? vraw_empty : kraw_empty) + slot, n / slots - 1);
+            if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
+            __syncwarp();
+            if (id >= 0 && !dead)
+                tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + lane * 16 * F::RW, v ? &vmap : &kmap,
+                            tile * F::RW, tok, w.h, id, full);
+            if (!dead) (v ? sent_v : sent_k) = n + 1;
+        };
+        for (;; ++turn) {
+            const uint32_t slot = turn % kUnitsAhead;
+            if (turn >= kUnitsAhead) wait(unit_empty + slot, turn / kUnitsAhead - 1);
+            const bool there = !dead && at < end;
+            if (there) {
+                int steps, parts, in;
+                walk.to(a, at, w, steps, parts, in);
+                const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
+                w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
+                w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
+                w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
+                w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
+                at += last - in;
+            } else {
+                w.tokens = -1;
             }
-            if (dead) {  // the copies in flight: shared memory is theirs until they land
-                for (uint32_t x = sent_k > F::kRawK ? sent_k - F::kRawK : 0; x < sent_k; ++x)
-                    (void)mbar_wait_bounded(kraw_full + x % F::kRawK, (x / F::kRawK) & 1u, a.status);
-                for (uint32_t x = sent_v > F::kRawV ? sent_v - F::kRawV : 0; x < sent_v; ++x)
-                    (void)mbar_wait_bounded(vraw_full + x % F::kRawV, (x / F::kRawV) & 1u, a.status);
-            }
-        } else if (warp == kMmaWarp) {
-            // ---------------------------------------------------------- MMAs
-            // What the sequences hold behind the prefix comes to L2 meanwhile, for the launch behind this one, as far
-            // as L2 keeps it: a lane a page.
-            const uint32_t page_bytes = static_cast<uint32_t>(c.heads * c.dim) << c.log2p;
-            int64_t room = kPrefetchBytes / (2 * static_cast<int64_t>(page_bytes) * gridDim.x);
-            for (int b = blockIdx.x; b < a.batch && room > 0; b += gridDim.x) {
-                const int64_t len = min(static_cast<int64_t>(max(a.lens[b], 0)), a.width << c.log2p);
-                const int64_t from = max(a.skip[b], 0) >> c.log2p;
-                const int64_t pages = min((len + (1 << c.log2p) - 1) >> c.log2p, from + room);
-                for (int64_t x = from + lane; x < pages; x += 32) {
-                    const int id = a.table[b * a.width + x];
-                    if (id < 0 || id >= c.pages) continue;
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.k + id * c.page_stride), "r"(page_bytes) : "memory");
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.v + id * c.page_stride), "r"(page_bytes) : "memory");
-                }
-                room -= max(int64_t(0), pages - from);
+            if (lane == 0) {
+                units[slot] = w;
+                arrive_on(unit_full + slot);
             }
             __syncwarp();
-            uint32_t g = 0, qs = 0;  // steps and queries taken
-            while (next_unit()) {
-                const int steps = w.j1 - w.j0;
-                const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn((w.nc + 63) / 64 * 64);
-                wait(q_full, qs);
-                for (int j = 0; j <= steps; ++j) {
-                    if (j < steps) {
-                        const uint32_t n = g + j, kb = n % F::KB, st = tmem + (n & 1) * NMAX;
-                        wait(k_full + kb, n / F::KB);
-                        fence_after();
-                        if (lane == 0 && !dead) {
-                            const uint32_t ka = tmem + F::k_at + kb * (DP / 2);
-#pragma unroll
-                            for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
-                                const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
-#pragma unroll
-                                for (int ks = 0; ks < DP / 16; ++ks)
-                                    mma_ts(st, ka + ks * 8, qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
-                                           p < QP - 1 || ks > 0 ? 1u : 0u);
-                            }
-                            commit_to(s_full + (n & 1));
-                            commit_to(k_empty + kb);
-                        }
-                        __syncwarp();
-                    }
-                    if (j > 0) {
-                        const uint32_t n = g + j - 1, os = n % F::kOps;
-                        wait(v_full + os, n / F::kOps);
-                        wait(p_full, n);
-                        fence_after();
-                        if (lane == 0 && !dead) {
-#pragma unroll
-                            for (int acc = 0; acc < F::DA; ++acc) {
-                                const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + os * F::kOp + acc * 32768), 16384);
-#pragma unroll
-                                for (int p = PP - 1; p >= 0; --p) {
-                                    const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + p * F::kPPart), 16384);
-#pragma unroll
-                                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                                        mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
-                                               j > 1 || ks > 0 ? 1u : 0u);
-                                }
-                            }
-                            commit_to(pv_done);
-                            commit_to(v_empty + os);
-                        }
-                        __syncwarp();
+            if (!there) break;
+            const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
+            auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
+                int id = -1;
+                f = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
+                if (lane < 8 && tok < w.tokens) {
+                    id = table[tok >> c.log2p];
+                    if (id >= 0 && id < c.pages) {
+                        const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
+                        f.x = __ldg(c.ks + s);
+                        f.y = __ldg(c.vs + s);
+                        f.z = 1.f;
+                    } else {
+                        id = -1;
+                        atomicOr(a.status, kStatusBounds);
                     }
                 }
-                g += steps;
-                ++qs;
+                return id;
+            };
+            float4 f;
+            int id = look(w.j0, f);
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
+                const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
+                if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
+                __syncwarp();
+                if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
+                for (int t = 0; t < F::RT; ++t) copy(false, t, tok, id, valid, o + t);
+                for (int t = 0; t < F::RT; ++t) copy(true, t, tok, id, valid, o + t);
+                o += F::RT;
+                if (j + 1 < w.j1) id = look(j + 1, f);
             }
+        }
+        if (dead) {  // the copies in flight: shared memory is theirs until they land
+            for (uint32_t x = sent_k > F::kRawK ? sent_k - F::kRawK : 0; x < sent_k; ++x)
+                (void)mbar_wait_bounded(kraw_full + x % F::kRawK, (x / F::kRawK) & 1u, a.status);
+            for (uint32_t x = sent_v > F::kRawV ? sent_v - F::kRawV : 0; x < sent_v; ++x)
+                (void)mbar_wait_bounded(vraw_full + x % F::kRawV, (x / F::kRawV) & 1u, a.status);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMAs
+        // What the sequences hold behind the prefix comes to L2 meanwhile, for the launch behind this one, as far
+        // as L2 keeps it: a lane a page.
+        const uint32_t page_bytes = static_cast<uint32_t>(c.heads * c.dim) << c.log2p;
+        int64_t room = kPrefetchBytes / (2 * static_cast<int64_t>(page_bytes) * gridDim.x);
+        for (int b = blockIdx.x; b < a.batch && room > 0; b += gridDim.x) {
+            const int64_t len = min(static_cast<int64_t>(max(a.lens[b], 0)), a.width << c.log2p);
+            const int64_t from = max(a.skip[b], 0) >> c.log2p;
+            const int64_t pages = min((len + (1 << c.log2p) - 1) >> c.log2p, from + room);
+            for (int64_t x = from + lane; x < pages; x += 32) {
+                const int id = a.table[b * a.width + x];
+                if (id < 0 || id >= c.pages) continue;
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.k + id * c.page_stride), "r"(page_bytes) : "memory");
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.v + id * c.page_stride), "r"(page_bytes) : "memory");
+            }
+            room -= max(int64_t(0), pages - from);
+        }
+        __syncwarp();
+        uint32_t g = 0, qs = 0;  // steps and queries taken
+        while (next_unit()) {
+            const int steps = w.j1 - w.j0;
+            const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn(F::NP);
+            wait(q_full, qs);
+            for (int j = 0; j <= steps; ++j) {
+                if (j < steps) {
+                    const uint32_t n = g + j, kb = n % F::KB, st = tmem + (n & 1) * NMAX;
+                    wait(k_full + kb, n / F::KB);
+                    fence_after();
+                    if (lane == 0 && !dead) {
+                        const uint32_t ka = tmem + F::k_at + kb * (DP / 2);
+#pragma unroll
+                        for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
+                            const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
+#pragma unroll
+                            for (int ks = 0; ks < DP / 16; ++ks)
+                                mma_ts(st, ka + ks * 8, qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
+                                       p < QP - 1 || ks > 0 ? 1u : 0u);
+                        }
+                        commit_to(s_full + (n & 1));
+                        commit_to(k_empty + kb);
+                    }
+                    __syncwarp();
+                }
+                if (j > 0) {
+                    const uint32_t n = g + j - 1, os = n % F::kOps;
+                    wait(v_full + os, n / F::kOps);
+                    wait(p_full + (n & 1), n >> 1);
+                    fence_after();
+                    if (lane == 0 && !dead) {
+#pragma unroll
+                        for (int acc = 0; acc < F::DA; ++acc) {
+                            const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + os * F::kOp + acc * 32768), 16384);
+#pragma unroll
+                            for (int p = PP - 1; p >= 0; --p) {
+                                const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + ((n % F::PB) * PP + p) * F::kPPart), 16384);
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / 16; ++ks)
+                                    mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
+                                           j > 1 || ks > 0 ? 1u : 0u);
+                            }
+                        }
+                        commit_to(pv_done + (n & 1));
+                        commit_to(v_empty + os);
+                    }
+                    __syncwarp();
+                }
+            }
+            g += steps;
+            ++qs;
         }
     } else if (warp >= kValueWarp) {
         // ---------------------------------------------------------- V: 8 bits -> f16 in shared memory, as it lies
-        give_registers<kConvertRegs>();
         const int ct = tid - kValueWarp * 32;
         uint32_t r = 0, g = 0;  // raw tiles and steps
         while (next_unit()) {
@@ -663,7 +657,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         }
     } else if (warp >= kKeyWarp) {
         // ---------------------------------------------------------- K: 8 bits -> f16 in tensor memory, a thread a key
-        give_registers<kConvertRegs>();
         const int key = tid - kKeyWarp * 32;
         const int turn16 = F::RW == 64 ? (key >> 1) & 3 : key & 7;  // the copy's swizzle: no two of eight rows in a bank
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -711,7 +704,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         }
     } else {
         // ---------------------------------------------------------- softmax, a thread a key and a set's columns
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int set = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wid = 2 + set;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t g = 0;
@@ -788,34 +780,31 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 sync_warps(1, kSoftmaxWarps * 32);
                 if (lane == 0) arrive_on(q_full);
             }
-            f2 l[F::NC][8];  // sums of p by column pairs
+            f2 l[8];  // sums of e by column pairs
 #pragma unroll
-            for (int cc = 0; cc < F::NC; ++cc)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) l[cc][i] = {0.f, 0.f};
+            for (int i = 0; i < 8; ++i) l[i] = {0.f, 0.f};
+            const int cb = set * 16;
+            const bool busy = cb < nc;  // this set has columns
 
             for (int j = j0; j < j1; ++j, ++g) {
                 wait(sc_full + g % kScaleSteps, g / kScaleSteps);
                 wait(s_full + (g & 1), g >> 1);
                 fence_after();
-                const float4 mine = scales[(g % kScaleSteps) * 8 + (key >> 4)];
-                const float ks = mine.x, vs = mine.y;
-                const bool there = mine.z != 0.f, whole = __all_sync(~0u, there);
-                const uint32_t st = tmem + (g & 1) * NMAX + lanes;
-                bool mine_now = false;  // z and O are this step's
-                auto take = [&]() {
-                    if (!mine_now && g > 0) wait(pv_done, g - 1);
-                    mine_now = true;
-                };
-#pragma unroll
-                for (int cc = 0; cc < F::NC; ++cc) {
-                    const int cb = (cc * kSets + set) * 16;
-                    if (cb >= nc) break;
-                    f2 p[8];
+                if (busy) {
+                    const float4 page = scales[(g % kScaleSteps) * 8 + (key >> 4)];
+                    const float ks = page.x, vs = page.y;
+                    const bool there = page.z != 0.f;
+                    // vs < 2^evs
+                    const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
+                    // pages there whose vs shows in z when e would leave its range
+                    const bool plain = __all_sync(~0u, there && evs > -90);
+                    const uint32_t st = tmem + (g & 1) * NMAX + lanes;
+                    f2 e[8];
                     uint32_t z[8], zl[PP == 2 ? 8 : 1];
                     uint32_t s[16];
-                    // Probabilities of 16 columns under the references as they are; whether one passes them.
-                    auto attempt = [&](auto rounded) {
+                    // e = p 2^k and z = e vs of the 16 columns under the references as they are; whether one passes
+                    // them.  `any`: scores of any size and any k.
+                    auto attempt = [&](auto any) {
                         tmem_load16(st + cb, s);
                         tmem_loaded();
                         float high = -INFINITY;
@@ -823,21 +812,30 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float4 fa = *reinterpret_cast<const float4*>(cols.fac + cb + 4 * q);
-                            const float4 na = *reinterpret_cast<const float4*>(cols.nm + cb + 4 * q);
-                            const float4 ka = *reinterpret_cast<const float4*>(cols.pk + cb + 4 * q);
+                            const float4 na = *reinterpret_cast<const float4*>((any ? cols.ref : cols.nm) + cb + 4 * q);
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int i = 2 * q + u;
                                 const f2 fq = fmul2(u ? f2{fa.z, fa.w} : f2{fa.x, fa.y}, f2{ks, ks});
                                 const f2 sv = {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])};
                                 f2 y = u ? f2{na.z, na.w} : f2{na.x, na.y};
-                                if (rounded) fadd2(y, fmul2(sv, fq));
-                                else ffma2(y, sv, fq);
-                                if (!whole && !there) y.x = y.y = -INFINITY;
-                                high = fmaxf(high, fmaxf(y.x, y.y));
-                                p[i] = {exp2_fast(y.x), exp2_fast(y.y)};
-                                // p first: vs * 2^k may pass the range where p is 0
-                                const f2 zz = fmul2(fmul2(p[i], u ? f2{ka.z, ka.w} : f2{ka.x, ka.y}), f2{vs, vs});
+                                f2 pk = {1.f, 1.f};
+                                if (any) {  // the score rounded, its reference off, then ke
+                                    const f2 t = fmul2(sv, fq);
+                                    const int k0 = order_e(order_z(cols.refd[cb + 2 * i])), k1 = order_e(order_z(cols.refd[cb + 2 * i + 1]));
+                                    y.x = __fadd_rn(__fsub_rn(t.x, y.x), static_cast<float>(k0));
+                                    y.y = __fadd_rn(__fsub_rn(t.y, y.y), static_cast<float>(k1));
+                                    pk = *reinterpret_cast<const f2*>(cols.pk + cb + 2 * i);
+                                } else {
+                                    ffma2(y, sv, fq);
+                                }
+                                if (any || !plain) {
+                                    if (!there) y.x = y.y = -INFINITY;
+                                    high = fmaxf(high, fmaxf(y.x, y.y));
+                                }
+                                e[i] = {exp2_fast(y.x), exp2_fast(y.y)};
+                                f2 zz = fmul2(e[i], f2{vs, vs});
+                                if (any) zz = fmul2(fmul2(e[i], pk), f2{vs, vs});  // e first: vs * 2^k may pass the range where e is 0
                                 z[i] = pack_f16x2(zz.x, zz.y);
                                 if (PP == 2) {  // 2^11 times what the first part leaves
                                     const f2 hi = h2_to_f2(z[i]);
@@ -846,10 +844,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 most = hmax2_of(most, z[i]);
                             }
                         }
-                        return high > 20.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
+                        return high > 105.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
                     };
-                    // vs < 2^evs
-                    const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
                     if (j == j0) first_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
                     for (int round = 0;; round = 1) {
                         bool huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
@@ -858,11 +854,11 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
                             huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
                             if (j > j0) {
-                                take();
+                                wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // O stands still
                                 fence_after();
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) l[cc][i] = fmul2(l[cc][i], *reinterpret_cast<const f2*>(cols.mul2 + cb + 2 * i));
-#pragma unroll
+                                for (int i = 0; i < 8; ++i) l[i] = fmul2(l[i], *reinterpret_cast<const f2*>(cols.mul2 + cb + 2 * i));
+#pragma unroll 1
                                 for (int acc = 0; acc < PP * F::DA; ++acc) {
                                     tmem_load16(o_at + acc * F::NP + lanes + cb, s);
                                     tmem_loaded();
@@ -876,11 +872,11 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         const bool passed = huge ? attempt(std::true_type()) : attempt(std::false_type());
                         if (round == 1 || !any_of(wid, 128, passed || huge)) break;
                     }
-                    take();
+                    if (g >= static_cast<uint32_t>(F::PB)) wait(pv_done + ((g - F::PB) & 1), (g - F::PB) >> 1);  // z's buffer is free
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fadd2(l[cc][i], p[i]);
-                    unsigned char* dst = smem + F::off_p + key * 128 + (cb >> 6) * 16384;
-                    const int ch = (cb & 63) >> 3;
+                    for (int i = 0; i < 8; ++i) fadd2(l[i], e[i]);
+                    unsigned char* dst = smem + F::off_p + (g % F::PB) * PP * F::kPPart + key * 128;
+                    const int ch = cb >> 3;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         unsigned char* at = dst + (((ch + u) ^ (key & 7)) << 4);
@@ -890,56 +886,49 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                                 make_uint4(zl[(4 * u) % (PP == 2 ? 8 : 1)], zl[(4 * u + 1) % (PP == 2 ? 8 : 1)],
                                            zl[(4 * u + 2) % (PP == 2 ? 8 : 1)], zl[(4 * u + 3) % (PP == 2 ? 8 : 1)]);
                     }
+                    fence_proxy_async_smem();
+                    fence_before();
                 }
-                take();
-                fence_proxy_async_smem();
-                fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_on(p_full);
+                if (lane == 0) arrive_on(p_full + (g & 1));
             }
 
             // ---- the rows' sums, then their results
-            {
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int cc = i / 16, pair = (i % 16) / 2;
-                    v[i] = 0.f;
-                    if (cc < F::NC && (cc * kSets + set) * 16 < nc) v[i] = i & 1 ? l[cc % F::NC][pair].y : l[cc % F::NC][pair].x;
-                }
-                const float sum = add_columns(v);
-                const int col = ((lane >> 4) * kSets + set) * 16 + (lane & 15);
-                if (lane < 16 * F::NC && col < nc) cols.tops[quarter][col] = sum;
-            }
-            sync_warps(wid, 128);
             float* part = a.slots + static_cast<int64_t>(w.slot < 0 ? 0 : w.slot) * (NMAX * (DP + 2));
             const bool begins = w.slot < 0;
-            const int mine = ((key >> 4) * kSets + set) * 16 + (key & 15);  // this thread's column
-            if (key < 16 * F::NC && mine < nc) {
-                const int col = mine;
-                const float sum = (cols.tops[0][col] + cols.tops[1][col]) + (cols.tops[2][col] + cols.tops[3][col]);
-                // NaN sums stay NaN; a row that saw nothing has a sum of 0
-                const bool none = sum == 0.f && cols.ref[col] == kNoRef;
-                const int down = none ? 0 : -min(kBase - cols.refd[col], kMostK);
-                cols.mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down >> 1);
-                cols.mul2[col] = pow2i(down - (down >> 1));
-                const float m = none ? -INFINITY : cols.ref[col];
-                if (begins) {
-                    if (cols.orow[col] >= 0)
-                        a.own_ml[cols.orow[col]] = make_float4(m, sum, __int_as_float(static_cast<int>(blockIdx.x) + 1),
-                                                               __int_as_float(w.extra | col << 16));
-                } else {
-                    *reinterpret_cast<float2*>(part + NMAX * DP + 2 * col) = make_float2(m, sum);
+            if (busy) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[2 * i] = l[i].x, v[2 * i + 1] = l[i].y;
+                const float sum = add_columns(v);
+                if (lane < 16) cols.tops[quarter][cb + lane] = sum;
+                sync_warps(wid, 128);
+                if (key < 16) {
+                    const int col = cb + key;
+                    const float sum = (cols.tops[0][col] + cols.tops[1][col]) + (cols.tops[2][col] + cols.tops[3][col]);
+                    // NaN sums stay NaN; a row that saw nothing has a sum of 0
+                    const bool none = sum == 0.f && cols.ref[col] == kNoRef;
+                    const int k = order_z(cols.refd[col]), ke = order_e(k), down = none ? 0 : ke - k;
+                    cols.mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down);  // 2^-k of z's sums by 2^-ke of e's
+                    const float m = none ? -INFINITY : cols.ref[col];
+                    const float total = none ? 0.f : sum * pow2i(-ke);
+                    if (begins) {
+                        if (cols.orow[col] >= 0)
+                            a.own_ml[cols.orow[col]] = make_float4(m, total, __int_as_float(static_cast<int>(blockIdx.x) + 1),
+                                                                   __int_as_float(w.extra | col << 16));
+                    } else {
+                        *reinterpret_cast<float2*>(part + NMAX * DP + 2 * col) = make_float2(m, total);
+                    }
                 }
             }
-            wait(pv_done, g - 1);
+            wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);
             fence_after();
             sync_warps(wid, 128);
             const int place = INT8 ? (lane & ~3) | ((lane & 1) << 1 | (lane & 2) >> 1) : lane;  // dims as k_codes orders them
 #pragma unroll 1
-            for (int x = 0; x < F::DA * F::NC; ++x) {
-                const int acc = x / F::NC, cb = (x % F::NC * kSets + set) * 16, d = acc * 128 + quarter * 32 + place;
-                if (cb >= nc || acc * 128 + quarter * 32 >= c.dim) continue;
+            for (int acc = 0; busy && acc < F::DA; ++acc) {
+                const int d = acc * 128 + quarter * 32 + place;
+                if (acc * 128 + quarter * 32 >= c.dim) break;
                 uint32_t v[16], vl[16];
                 tmem_load16(o_at + acc * F::NP + lanes + cb, v);
                 if (PP == 2) tmem_load16(o_at + (F::DA + acc) * F::NP + lanes + cb, vl);
@@ -949,9 +938,9 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     for (int i = 0; i < 16; ++i) {
                         float x = __uint_as_float(v[i]);
                         if (PP == 2) x = fmaf(__uint_as_float(vl[i]), 0x1p-11f, x);
-                        x = x * cols.mul1[cb + i] * cols.mul2[cb + i];
+                        const float f = cols.mul1[cb + i];
                         const int64_t to = cols.orow[cb + i];
-                        if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = cols.mul1[cb + i] == 0.f ? 0.f : x;
+                        if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = f == 0.f ? 0.f : x * f;
                     }
                 }
                 __syncwarp();
