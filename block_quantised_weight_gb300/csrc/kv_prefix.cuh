@@ -468,7 +468,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
             __syncwarp();
             if (id >= 0 && !dead)
-                tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + lane * 16 * F::RW, v ? &vmap : &kmap,
+                tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + (lane & 7) * 16 * F::RW, v ? &vmap : &kmap,
                             tile * F::RW, tok, w.h, id, full);
             if (!dead) (v ? sent_v : sent_k) = n + 1;
         };
@@ -495,36 +495,47 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             __syncwarp();
             if (!there) break;
             const int32_t* table = a.table + static_cast<int64_t>(w.table_row) * a.width;
-            auto look = [&](int j, float4& f) {  // page of this lane's 16 tokens of step j (lanes 0-7)
-                int id = -1;
-                f = make_float4(0.f, 0.f, 0.f, 0.f);
+            // Lane i has the page and scales of the i-th 16 tokens of four steps; those of the next four are on
+            // their way meanwhile.
+            const int64_t last_tok = min(static_cast<int64_t>(w.tokens), static_cast<int64_t>(w.j1) * kKeys);
+            auto pages = [&](int j) {
                 const int64_t tok = static_cast<int64_t>(j) * kKeys + lane * 16;
-                if (lane < 8 && tok < w.tokens) {
-                    id = table[tok >> c.log2p];
-                    if (id >= 0 && id < c.pages) {
-                        const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
-                        f.x = __ldg(c.ks + s);
-                        f.y = __ldg(c.vs + s);
-                        f.z = 1.f;
-                    } else {
+                int id = -1;
+                if (tok < last_tok) {
+                    id = __ldg(table + (tok >> c.log2p));
+                    if (id < 0 || id >= c.pages) {
                         id = -1;
                         atomicOr(a.status, kStatusBounds);
                     }
                 }
                 return id;
             };
-            float4 f;
-            int id = look(w.j0, f);
+            auto page_scales = [&](int id) {
+                float2 f = make_float2(0.f, 0.f);
+                if (id >= 0) {
+                    const int64_t s = static_cast<int64_t>(id) * c.heads + w.h;
+                    f = make_float2(__ldg(c.ks + s), __ldg(c.vs + s));
+                }
+                return f;
+            };
+            int id = pages(w.j0), id_next = -1;
+            float2 f = page_scales(id), f_next = f;
             for (int j = w.j0; j < w.j1; ++j, ++g) {
-                const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + lane * 16) & ((1 << c.log2p) - 1));
-                const unsigned valid = __popc(__ballot_sync(~0u, id >= 0));
-                if (lane < 8) scales[(g % kScaleSteps) * 8 + lane] = f;
+                const int r = (j - w.j0) & 3;
+                if (r == 0) {
+                    if (j > w.j0) id = id_next, f = f_next;
+                    id_next = pages(j + 4);
+                }
+                if (r == 2) f_next = page_scales(id_next);
+                const bool mine = (lane >> 3) == r;
+                const int tok = static_cast<int>((static_cast<int64_t>(j) * kKeys + (lane & 7) * 16) & ((1 << c.log2p) - 1));
+                const unsigned valid = __popc(__ballot_sync(~0u, mine && id >= 0));
+                for (int t = 0; t < F::RT; ++t) copy(false, t, tok, mine ? id : -1, valid, o + t);
+                if (mine) scales[(g % kScaleSteps) * 8 + (lane & 7)] = make_float4(f.x, f.y, id >= 0 ? 1.f : 0.f, 0.f);
                 __syncwarp();
                 if (lane == 0) arrive_on(sc_full + g % kScaleSteps);
-                for (int t = 0; t < F::RT; ++t) copy(false, t, tok, id, valid, o + t);
-                for (int t = 0; t < F::RT; ++t) copy(true, t, tok, id, valid, o + t);
+                for (int t = 0; t < F::RT; ++t) copy(true, t, tok, mine ? id : -1, valid, o + t);
                 o += F::RT;
-                if (j + 1 < w.j1) id = look(j + 1, f);
             }
         }
         if (dead) {  // the copies in flight: shared memory is theirs until they land
