@@ -16,8 +16,8 @@
 // time.  References are whole numbers, shared by the four warps that hold the
 // keys; they are set in a piece's first step, so that z is at most 2^6 (k = 6 less
 // the order of p * vs), and move only when a z would pass 2^15: 16 columns are tried
-// as if they held, one vote of the four warps decides.  Scores from 2^22 on, and scales
-// whose k fp32 sums would not hold, take a slower way.  Two parts of z: the second is
+// as if they held, one vote of the four warps decides.  Scores from 2^22 on take a
+// slower way.  Two parts of z: the second is
 // 2^11 times what the first leaves, with sums of its own, so that small weights keep
 // their bits down to 2^-40 of a row's largest (one part: 2^-29).
 //
@@ -50,6 +50,7 @@ constexpr int kLeastSteps = 2;      // of a part
 constexpr uint32_t kUnitsAhead = 2; // pieces handed to the roles ahead
 constexpr uint32_t kScaleSteps = 8; // steps whose scales are held
 constexpr int64_t kPrefetchBytes = int64_t(64) << 20;  // half of L2
+constexpr int kMostE = 90;
 constexpr int kBase = 6;             // of k: z is at most 2^6 under new references, and may grow to 2^15
 constexpr int kSets = 4;             // of four softmax warps, 16 columns each
 // warps by role: the softmax, then four that convert K, four that convert V, one that copies, one that issues the MMAs
@@ -227,16 +228,16 @@ __device__ __forceinline__ float max_columns(float (&v)[16]) {
     return fmaxf(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
-// The order k of z, and what of it the sums of e = p 2^ke take: as much as leaves them in fp32's range.
-__device__ __forceinline__ int order_z(int d) { return min(kBase - d, kMostK); }
-__device__ __forceinline__ int order_e(int k) { return min(max(k, -60), 90); }
+// The order k of z: at most kMostE, as the sums of e = p 2^k have to stay in fp32's range.
+__device__ __forceinline__ int order_z(int d) { return min(kBase - d, kMostE); }
 
 // What belongs to the columns (query rows) of a unit, in shared memory.
 template <int NMAX>
 struct Columns {
     float fac[NMAX];               // factor of the scores
-    float nm[NMAX], pk[NMAX];      // ke less the reference, 2^(k - ke)
-    float mul1[NMAX], mul2[NMAX];  // two factors
+    float nm[NMAX];                // k less the reference
+    float one[NMAX], k[NMAX];      // the same of scores that were settled (huge ones)
+    float mul[NMAX];               // a factor
     float ref[NMAX];
     int refd[NMAX];
     float tops[4][NMAX];           // by warp of a set: largest scores, later sums
@@ -247,7 +248,7 @@ struct Columns {
 // The first references of 4 of the 16 columns from cb on, by each warp of a set from its own 32
 // keys: a lower bound of the largest, which 2^9 above the first z leaves room for.
 template <int NMAX>
-__device__ __forceinline__ void first_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
+__device__ __noinline__ bool first_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
                                                  int evs, int barrier) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     uint32_t s[4];
@@ -279,20 +280,20 @@ __device__ __forceinline__ void first_references(Columns<NMAX>& cols, int* huge_
         const int col = cb + quarter * 4 + lane;
         const float mn = fmaxf(kNoRef, top[0]);
         const int dn = max(kNoOrder, order_of(high[0] - mn));
-        const int k = order_z(dn), ke = order_e(k);
         cols.ref[col] = mn, cols.refd[col] = dn;
-        cols.nm[col] = static_cast<float>(ke) - mn, cols.pk[col] = pow2i(k - ke);
-        if ((k != ke && dn > kNoOrder) || (mn > kNoRef && fabsf(mn) >= kHugeScore)) *reinterpret_cast<volatile int*>(huge_at) = 1;
+        cols.nm[col] = static_cast<float>(order_z(dn)) - mn;
+        if (mn > kNoRef && fabsf(mn) >= kHugeScore) *reinterpret_cast<volatile int*>(huge_at) = 1;
     }
     sync_warps(barrier, 128);
+    return *reinterpret_cast<volatile int*>(huge_at) != 0;  // the same in all four
 }
 
-// New references of the 16 columns from cb on, by the four warps of a set: mul1 is what the sums
-// of z, mul2 what those of e are to be multiplied by.  evs: the order of the key's vs.  Out of line: the
-// way there is rare.
+// New references of the 16 columns from cb on, by the four warps of a set; mul is what the sums of e
+// and z are to be multiplied by, and those of z are (n accumulators of 64 columns at `sums`).  evs: the order of the key's
+// vs.  Huge scores are settled: rounded, and less their references in tensor memory.  Returns whether they are.
 template <int NMAX>
-__device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
-                                            int evs, int barrier) {
+__device__ __noinline__ bool new_references(Columns<NMAX>& cols, int* huge_at, uint32_t scores, int cb, bool there, float ks,
+                                            int evs, int barrier, uint32_t sums, int n) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, key = threadIdx.x & 127;
     // Largest scores, rounded up to whole orders, and with the orders of vs; `based`: the references are taken
     // off first (huge scores, whose sums with an order do not hold it).
@@ -342,14 +343,35 @@ __device__ __noinline__ void new_references(Columns<NMAX>& cols, int* huge_at, u
         const int d = cols.refd[col];
         const float high = largest(cols.tops_v, col);
         const int dn = max(max(d + down, kNoOrder), order_of(huge ? high : high - cols.ref[col]));
-        const int k_old = order_z(d), k_new = order_z(dn), e_new = order_e(k_new);
-        cols.mul1[col] = pow2i(k_new - k_old + down);
-        cols.mul2[col] = pow2i(e_new - order_e(k_old) + down);
+        cols.mul[col] = pow2i(order_z(dn) - order_z(d) + down);
         cols.refd[col] = dn;
-        cols.nm[col] = static_cast<float>(e_new) - cols.ref[col], cols.pk[col] = pow2i(k_new - e_new);
-        if (k_new != e_new && dn > kNoOrder) *huge_at = 1;  // and more than zeros have come
+        cols.k[col] = static_cast<float>(order_z(dn)), cols.nm[col] = cols.k[col] - cols.ref[col];
     }
     sync_warps(barrier, 128);
+    uint32_t s[16];
+    for (int x = 0; x < n; ++x) {
+        tmem_load16(sums + x * 64 + cb, s);
+        tmem_loaded();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * cols.mul[cb + i]);
+        tmem_store16(sums + x * 64 + cb, s);
+    }
+    if (huge) {
+        tmem_load16(scores + cb, s);
+        tmem_loaded();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            s[i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(s[i]), cols.fac[cb + i] * ks), cols.ref[cb + i]));
+        tmem_store16(scores + cb, s);
+    }
+    tmem_stored();
+    return huge;
+}
+
+// The rest of a wait whose phase had not ended at first: out of line, as most code that a step does not
+// run, for the warps' different roles leave the instruction caches little room.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, unsigned* status) {
+    return __any_sync(~0u, !mbar_wait_bounded(bar, parity, status));
 }
 
 template <int DP, int QP, int PP, bool INT8>
@@ -438,7 +460,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     // the kernel then runs to its end within a few wait limits.
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // by whole warps
-        if (!dead) dead = __any_sync(~0u, !mbar_wait_bounded(bar, parity & 1u, a.status));
+        if (!dead && !__all_sync(~0u, mbar_try_wait(bar, parity & 1u))) dead = wait_on(bar, parity & 1u, a.status);
     };
     // The next piece, as the copying warp hands it to the others; false after the last.
     uint32_t turn = 0;
@@ -461,13 +483,14 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             at = static_cast<int>(line.first(blockIdx.x)), end = static_cast<int>(line.first(blockIdx.x + 1));
         uint32_t o = 0, g = 0;  // raw tiles of K, and of V, and steps over the life of the kernel
         uint32_t sent_k = 0, sent_v = 0;  // raw tiles whose copies were issued
+        const int box = min(kKeys, 1 << c.log2p);  // tokens of a copy: a page's, as far as they are one step's
         auto copy = [&](bool v, int tile, int tok, int id, unsigned valid, uint32_t n) {
             const uint32_t slots = v ? F::kRawV : F::kRawK, slot = n % slots;
             uint64_t* full = (v ? vraw_full : kraw_full) + slot;
             if (n >= slots) wait((v ? vraw_empty : kraw_empty) + slot, n / slots - 1);
             if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
             __syncwarp();
-            if (id >= 0 && !dead)
+            if (id >= 0 && (lane & 7) * 16 % box == 0 && !dead)
                 tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + (lane & 7) * 16 * F::RW, v ? &vmap : &kmap,
                             tile * F::RW, tok, w.h, id, full);
             if (!dead) (v ? sent_v : sent_k) = n + 1;
@@ -617,7 +640,14 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         }
     } else if (warp >= kValueWarp) {
         // ---------------------------------------------------------- V: 8 bits -> f16 in shared memory, as it lies
-        const int ct = tid - kValueWarp * 32;
+        // A warp has 64 of the dims and a part of the tokens, a lane 16 dims of every eighth token: its places in the
+        // swizzled rows are then the same for all of them, and the 32 lanes meet every bank equally often.
+        constexpr int DB = F::RW / 64, WT = kKeys * DB / 4;  // blocks of 64 dims of a raw tile, tokens of a warp
+        const int vw = warp - kValueWarp, block = vw % DB, c16 = block * 4 + (lane & 3), t7 = lane >> 2;
+        const int token0 = vw / DB * WT + t7;
+        const int from = token0 * F::RW + ((F::RW == 64 ? c16 ^ (t7 >> 1) : c16 ^ t7) << 4);
+        const int to0 = block * 16384 + token0 * 128 + (((2 * (lane & 3)) ^ t7) << 4);
+        const int to1 = block * 16384 + token0 * 128 + (((2 * (lane & 3) + 1) ^ t7) << 4);
         uint32_t r = 0, g = 0;  // raw tiles and steps
         while (next_unit()) {
             for (int j = w.j0; j < w.j1; ++j, ++g) {
@@ -625,37 +655,32 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 wait(sc_full + g % kScaleSteps, g / kScaleSteps);
                 const bool whole = __all_sync(~0u, sc[lane & 7].z != 0.f);  // no page is missing
                 const uint32_t os = g % F::kOps;
-                unsigned char* op = smem + F::off_op + os * F::kOp;
 #pragma unroll 1
                 for (int t = 0; t < F::RT; ++t, ++r) {
                     const uint32_t rs = r % F::kRawV;
                     wait(vraw_full + rs, r / F::kRawV);
                     if (t == 0 && g >= F::kOps) wait(v_empty + os, g / F::kOps - 1);
-                    const unsigned char* raw = smem + F::off_raw + (F::kRawK + rs) * F::kRaw;
-                    constexpr int C16 = F::RW / 16;
+                    const unsigned char* raw = smem + F::off_raw + (F::kRawK + rs) * F::kRaw + from;
+                    unsigned char* op = smem + F::off_op + os * F::kOp + t * 32768;
 #pragma unroll
-                    for (int i0 = 0; i0 < C16; i0 += 4) {
+                    for (int i0 = 0; i0 < WT / 8; i0 += 4) {
                         uint4 x[4];
 #pragma unroll
-                        for (int it = 0; it < 4; ++it)
-                            x[it] = *reinterpret_cast<const uint4*>(raw + ((i0 + it) * 128 + ct) * 16);
+                        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + (i0 + i) * 8 * F::RW);
+                        if (!whole) {
 #pragma unroll
-                        for (int it = 0; it < 4; ++it) {
-                            const int item = (i0 + it) * 128 + ct, token = item / C16, c16 = item % C16;
-                            if (!whole && sc[token >> 4].z == 0.f) x[it] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 4; ++i)
+                                if (sc[(token0 + (i0 + i) * 8) >> 4].z == 0.f) x[i] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
                             uint32_t h[8];
-                            const uint32_t in[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) k_codes<INT8>(in[i], h[2 * i], h[2 * i + 1]);
-                            // two 16-byte chunks; lanes of the second 64 dims store theirs in the other order
-                            const bool flip = (c16 >> 2) & 1;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const bool second = (e == 1) != flip;
-                                const int ch = t * (F::RW / 8) + 2 * c16 + (second ? 1 : 0);
-                                *reinterpret_cast<uint4*>(op + (ch >> 3) * 16384 + token * 128 + (((ch & 7) ^ (token & 7)) << 4)) =
-                                    second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-                            }
+                            k_codes<INT8>(x[i].x, h[0], h[1]);
+                            k_codes<INT8>(x[i].y, h[2], h[3]);
+                            k_codes<INT8>(x[i].z, h[4], h[5]);
+                            k_codes<INT8>(x[i].w, h[6], h[7]);
+                            *reinterpret_cast<uint4*>(op + to0 + (i0 + i) * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(op + to1 + (i0 + i) * 1024) = make_uint4(h[4], h[5], h[6], h[7]);
                         }
                     }
                     __syncwarp();
@@ -675,7 +700,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         while (next_unit()) {
             for (int j = w.j0; j < w.j1; ++j, ++g) {
                 wait(sc_full + g % kScaleSteps, g / kScaleSteps);
-                const bool there = scales[(g % kScaleSteps) * 8 + (key >> 4)].z != 0.f;
+                const bool there = scales[(g % kScaleSteps) * 8 + (key >> 4)].z != 0.f, whole = __all_sync(~0u, there);
                 const uint32_t kb = g % F::KB;
 #pragma unroll 1
                 for (int t = 0; t < F::RT; ++t, ++r) {
@@ -691,9 +716,11 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         uint4 x[2];
                         uint32_t h[16];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            x[i] = *reinterpret_cast<const uint4*>(raw + (((c * 2 + i) ^ turn16) << 4));
-                            if (!there) x[i] = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + ((c * 2 + i) * 16 ^ turn16 * 16));
+                        if (!whole) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!there) x[i] = make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -771,6 +798,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     if (in < each) {
                         if (lane % QL == 0) {
                             cols.fac[col] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                            cols.one[col] = 1.f;
                         }
 #pragma unroll
                         for (int v = 0; v < VL; ++v) {
@@ -797,12 +825,19 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const int cb = set * 16;
             const bool busy = cb < nc;  // this set has columns
 
+            bool huge = false;              // the set's scores are
+            float4 page = make_float4(0.f, 0.f, 0.f, 0.f);  // of this step, read a step ahead
+            auto next_page = [&](uint32_t n) {
+                wait(sc_full + n % kScaleSteps, n / kScaleSteps);
+                return scales[(n % kScaleSteps) * 8 + (key >> 4)];
+            };
+            if (busy) page = next_page(g);
+
             for (int j = j0; j < j1; ++j, ++g) {
-                wait(sc_full + g % kScaleSteps, g / kScaleSteps);
+                // Its MMAs are behind those of step g - 2, whose z's buffer is free then where there are two.
                 wait(s_full + (g & 1), g >> 1);
                 fence_after();
                 if (busy) {
-                    const float4 page = scales[(g % kScaleSteps) * 8 + (key >> 4)];
                     const float ks = page.x, vs = page.y;
                     const bool there = page.z != 0.f;
                     // vs < 2^evs
@@ -813,77 +848,64 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     f2 e[8];
                     uint32_t z[8], zl[PP == 2 ? 8 : 1];
                     uint32_t s[16];
-                    // e = p 2^k and z = e vs of the 16 columns under the references as they are; whether one passes
-                    // them.  `any`: scores of any size and any k.
-                    auto attempt = [&](auto any) {
+                    // e = p 2^k and z = e vs of the 16 columns under the references as they are; whether one passes them.
+                    bool settled = false;
+                    auto attempt = [&]() {
                         tmem_load16(st + cb, s);
                         tmem_loaded();
                         float high = -INFINITY;
                         uint32_t most = 0u;
+                        const float* fac = (settled ? cols.one : cols.fac) + cb;
+                        const float* nm = (settled ? cols.k : cols.nm) + cb;
+                        const float by = settled ? 1.f : ks;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float4 fa = *reinterpret_cast<const float4*>(cols.fac + cb + 4 * q);
-                            const float4 na = *reinterpret_cast<const float4*>((any ? cols.ref : cols.nm) + cb + 4 * q);
+                            const float4 fa = *reinterpret_cast<const float4*>(fac + 4 * q);
+                            const float4 na = *reinterpret_cast<const float4*>(nm + 4 * q);
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int i = 2 * q + u;
-                                const f2 fq = fmul2(u ? f2{fa.z, fa.w} : f2{fa.x, fa.y}, f2{ks, ks});
-                                const f2 sv = {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])};
-                                f2 y = u ? f2{na.z, na.w} : f2{na.x, na.y};
-                                f2 pk = {1.f, 1.f};
-                                if (any) {  // the score rounded, its reference off, then ke
-                                    const f2 t = fmul2(sv, fq);
-                                    const int k0 = order_e(order_z(cols.refd[cb + 2 * i])), k1 = order_e(order_z(cols.refd[cb + 2 * i + 1]));
-                                    y.x = __fadd_rn(__fsub_rn(t.x, y.x), static_cast<float>(k0));
-                                    y.y = __fadd_rn(__fsub_rn(t.y, y.y), static_cast<float>(k1));
-                                    pk = *reinterpret_cast<const f2*>(cols.pk + cb + 2 * i);
-                                } else {
-                                    ffma2(y, sv, fq);
-                                }
-                                if (any || !plain) {
-                                    if (!there) y.x = y.y = -INFINITY;
-                                    high = fmaxf(high, fmaxf(y.x, y.y));
-                                }
-                                e[i] = {exp2_fast(y.x), exp2_fast(y.y)};
-                                f2 zz = fmul2(e[i], f2{vs, vs});
-                                if (any) zz = fmul2(fmul2(e[i], pk), f2{vs, vs});  // e first: vs * 2^k may pass the range where e is 0
-                                z[i] = pack_f16x2(zz.x, zz.y);
-                                if (PP == 2) {  // 2^11 times what the first part leaves
-                                    const f2 hi = h2_to_f2(z[i]);
-                                    zl[i % (PP == 2 ? 8 : 1)] = pack_f16x2((zz.x - hi.x) * 2048.f, (zz.y - hi.y) * 2048.f);
-                                }
-                                most = hmax2_of(most, z[i]);
+                                const f2 fq = fmul2(u ? f2{fa.z, fa.w} : f2{fa.x, fa.y}, f2{by, by});
+                                e[i] = u ? f2{na.z, na.w} : f2{na.x, na.y};
+                                ffma2(e[i], {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])}, fq);
                             }
+                        }
+                        if (!plain) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                if (!there) e[i].x = e[i].y = -INFINITY;
+                                high = fmaxf(high, fmaxf(e[i].x, e[i].y));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            e[i] = {exp2_fast(e[i].x), exp2_fast(e[i].y)};
+                            const f2 zz = fmul2(e[i], f2{vs, vs});
+                            z[i] = pack_f16x2(zz.x, zz.y);
+                            if (PP == 2) {  // 2^11 times what the first part leaves
+                                const f2 hi = h2_to_f2(z[i]);
+                                zl[i % (PP == 2 ? 8 : 1)] = pack_f16x2((zz.x - hi.x) * 2048.f, (zz.y - hi.y) * 2048.f);
+                            }
+                            most = hmax2_of(most, z[i]);
                         }
                         return high > 105.f || (most & 0xFFFFu) > 0x7800u || (most >> 16) > 0x7800u;  // f16's 2^15
                     };
-                    if (j == j0) first_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
-                    for (int round = 0;; round = 1) {
-                        bool huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
-                        if (round == 1) {
-                            fence_after();
-                            new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
-                            huge = *reinterpret_cast<volatile int*>(huge_set + set) != 0;
-                            if (j > j0) {
-                                wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // O stands still
-                                fence_after();
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) l[i] = fmul2(l[i], *reinterpret_cast<const f2*>(cols.mul2 + cb + 2 * i));
+                    if (j == j0) huge = first_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid);
 #pragma unroll 1
-                                for (int acc = 0; acc < PP * F::DA; ++acc) {
-                                    tmem_load16(o_at + acc * F::NP + lanes + cb, s);
-                                    tmem_loaded();
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * cols.mul1[cb + i]);
-                                    tmem_store16(o_at + acc * F::NP + lanes + cb, s);
-                                }
-                                tmem_stored();
-                            }
-                        }
-                        const bool passed = huge ? attempt(std::true_type()) : attempt(std::false_type());
+                    for (int round = 0;; round = 1) {
+                        const bool passed = attempt();
                         if (round == 1 || !any_of(wid, 128, passed || huge)) break;
+                        if (j > j0) wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // O stands still
+                        fence_after();
+                        settled = huge = new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid, o_at + lanes,
+                                                       j > j0 ? PP * F::DA : 0);
+                        if (j > j0) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) l[i] = fmul2(l[i], *reinterpret_cast<const f2*>(cols.mul + cb + 2 * i));
+                        }
                     }
-                    if (g >= static_cast<uint32_t>(F::PB)) wait(pv_done + ((g - F::PB) & 1), (g - F::PB) >> 1);  // z's buffer is free
+                    if (j + 1 < j1) page = next_page(g + 1);
+                    if (F::PB == 1 && g > 0) wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // z's buffer is free
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fadd2(l[i], e[i]);
                     unsigned char* dst = smem + F::off_p + (g % F::PB) * PP * F::kPPart + key * 128;
@@ -919,10 +941,9 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     const float sum = (cols.tops[0][col] + cols.tops[1][col]) + (cols.tops[2][col] + cols.tops[3][col]);
                     // NaN sums stay NaN; a row that saw nothing has a sum of 0
                     const bool none = sum == 0.f && cols.ref[col] == kNoRef;
-                    const int k = order_z(cols.refd[col]), ke = order_e(k), down = none ? 0 : ke - k;
-                    cols.mul1[col] = (none ? 0.f : 1.f / sum) * pow2i(down);  // 2^-k of z's sums by 2^-ke of e's
+                    cols.mul[col] = none ? 0.f : 1.f / sum;
                     const float m = none ? -INFINITY : cols.ref[col];
-                    const float total = none ? 0.f : sum * pow2i(-ke);
+                    const float total = none ? 0.f : sum * pow2i(-order_z(cols.refd[col]));
                     if (begins) {
                         if (cols.orow[col] >= 0)
                             a.own_ml[cols.orow[col]] = make_float4(m, total, __int_as_float(static_cast<int>(blockIdx.x) + 1),
@@ -949,7 +970,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     for (int i = 0; i < 16; ++i) {
                         float x = __uint_as_float(v[i]);
                         if (PP == 2) x = fmaf(__uint_as_float(vl[i]), 0x1p-11f, x);
-                        const float f = cols.mul1[cb + i];
+                        const float f = cols.mul[cb + i];
                         const int64_t to = cols.orow[cb + i];
                         if (to >= 0) (begins ? a.own + to * c.dim : part + (cb + i) * DP)[d] = f == 0.f ? 0.f : x * f;
                     }
@@ -976,8 +997,9 @@ int launch_one(AttnArgs& a, cudaStream_t s) {
     const int dev = current_device();
     const int sms = sm_count(dev);
     if (sms <= 0) return cuda_fail(cudaGetLastError());
+    const int box = std::min(kKeys, 1 << a.c.log2p);
     CUtensorMap kmap, vmap;
-    if (!encode_cache(&kmap, a.c, a.c.k, F::RW, 16, true) || !encode_cache(&vmap, a.c, a.c.v, F::RW, 16, false))
+    if (!encode_cache(&kmap, a.c, a.c.k, F::RW, box, true) || !encode_cache(&vmap, a.c, a.c.v, F::RW, box, true))
         return cuda_fail(cudaGetLastError());
     static std::atomic<bool> done[64];
     auto kern = qg_attn_prefix_kernel<DP, QP, PP, INT8>;
