@@ -61,7 +61,9 @@ template <int DP, int QP, int PP>
 struct XShape {
     static constexpr int NMAX = prefix_rows(DP);
     static constexpr int NP = 64;                     // columns of the second product: a whole swizzle atom
-    static constexpr int PB = PP == 1 || DP == 64 ? 2 : 1;  // buffers of z, as shared memory has room
+    // Buffers of S^T, and of z, as shared memory has room: with three the sets of warps drift apart, and one's
+    // waits are the others' time.
+    static constexpr uint32_t SB = PP == 1 || DP == 64 ? 3 : 2, PB = SB == 3 ? 3 : 1;
     static constexpr int DA = DP == 256 ? 2 : 1;      // accumulators of 128 dims
     static constexpr int kQPart = NMAX * DP * 2;
     static constexpr int kPPart = kKeys * NP * 2;
@@ -71,7 +73,7 @@ struct XShape {
     static constexpr int kRaw = kKeys * RW;
     static constexpr uint32_t kOps = DP == 256 ? 1 : 2;
     static constexpr int off_p = QP * kQPart;
-    static constexpr int off_op = off_p + PB * PP * kPPart;
+    static constexpr int off_op = off_p + static_cast<int>(PB) * PP * kPPart;
     static constexpr int off_raw = off_op + static_cast<int>(kOps) * kOp;
     static constexpr int kExtra = 12 * 1024;          // what stands behind the raw slots
     static constexpr int kFit = (232448 - kExtra - off_raw) / kRaw;
@@ -79,8 +81,8 @@ struct XShape {
     static constexpr uint32_t kRawK = (kRaws + 1) / 2, kRawV = kRaws / 2;
     static_assert(kRawV >= RT && kRawV >= 1, "shared memory");
     static_assert(kOps + kRawV / RT < kScaleSteps, "scales are written while they are read");
-    // tensor memory: S^T twice, O^T (DA of NP for each part of z), K as f16 once or twice
-    static constexpr int o_at = 2 * NMAX, k_at = o_at + PP * DA * NP;
+    // tensor memory: S^T, O^T (DA of NP for each part of z), K as f16 once or twice
+    static constexpr int o_at = static_cast<int>(SB) * NMAX, k_at = o_at + PP * DA * NP;
     static constexpr uint32_t KB = (512 - k_at) / (DP / 2) >= 2 ? 2 : 1;
     static_assert(k_at + static_cast<int>(KB) * DP / 2 <= 512, "tensor memory");
     static constexpr int off_scale = off_raw + static_cast<int>(kRaws) * kRaw;
@@ -193,6 +195,13 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
         "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r) : "r"(static_cast<uint32_t>(mine)), "r"(id), "r"(threads) : "memory");
+    return r != 0;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
 
@@ -390,14 +399,14 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
     uint64_t* k_empty = k_full + F::KB;
     uint64_t* v_full = k_empty + F::KB;
     uint64_t* v_empty = v_full + F::kOps;
-    uint64_t* s_full = v_empty + F::kOps;   // [2]
-    uint64_t* p_full = s_full + 2;          // [2]
-    uint64_t* pv_done = p_full + 2;         // [2]
-    uint64_t* q_full = pv_done + 2;
+    uint64_t* s_full = v_empty + F::kOps;   // [SB]
+    uint64_t* p_full = s_full + F::SB;      // [SB]
+    uint64_t* pv_done = p_full + F::SB;     // [SB]
+    uint64_t* q_full = pv_done + F::SB;
     uint64_t* sc_full = q_full + 1;         // [kScaleSteps]
     uint64_t* unit_full = sc_full + kScaleSteps;
     uint64_t* unit_empty = unit_full + kUnitsAhead;
-    static_assert((2 * F::kRaws + 2 * F::KB + 2 * F::kOps + 7 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
+    static_assert((2 * F::kRaws + 2 * F::KB + 2 * F::kOps + 3 * F::SB + 1 + kScaleSteps + 2 * kUnitsAhead) * 8 <= 512, "barriers");
     __shared__ PrefixPiece units[kUnitsAhead];
     __shared__ uint32_t tmem_slot;
     __shared__ int huge_set[kSets];
@@ -414,8 +423,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
         for (uint32_t i = 0; i < F::kRawV; ++i) mbar_init(vraw_full + i, 1), mbar_init(vraw_empty + i, 4);
         for (uint32_t i = 0; i < F::KB; ++i) mbar_init(k_full + i, 4), mbar_init(k_empty + i, 1);
         for (uint32_t i = 0; i < F::kOps; ++i) mbar_init(v_full + i, 4), mbar_init(v_empty + i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(p_full + i, kSoftmaxWarps), mbar_init(pv_done + i, 1);
+        for (uint32_t i = 0; i < F::SB; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, kSoftmaxWarps), mbar_init(pv_done + i, 1);
         mbar_init(q_full, kSoftmaxWarps);
         for (uint32_t i = 0; i < kScaleSteps; ++i) mbar_init(sc_full + i, 1);
         for (uint32_t i = 0; i < kUnitsAhead; ++i)
@@ -586,50 +594,54 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             room -= max(int64_t(0), pages - from);
         }
         __syncwarp();
+        // All that the MMAs take is uniform, and so known to be, and one lane is elected: then their operands need no
+        // moves between register files, which made an MMA's issue 120 clocks (16 a step: 3000 clocks a step, all of it).
         uint32_t g = 0, qs = 0;  // steps and queries taken
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0), sm = __shfl_sync(~0u, smem_u32(smem), 0);
         while (next_unit()) {
-            const int steps = w.j1 - w.j0;
-            const uint32_t sdesc = f16_desc(w.nc), pdesc = f16_desc_mn(F::NP);
+            const int steps = __shfl_sync(~0u, w.j1 - w.j0, 0);
+            const uint32_t sdesc = f16_desc(__shfl_sync(~0u, w.nc, 0)), pdesc = f16_desc_mn(F::NP);
+            constexpr int kLag = F::SB - 1;  // steps that the second products are behind the first
             wait(q_full, qs);
-            for (int j = 0; j <= steps; ++j) {
+            for (int j = 0; j < steps + kLag; ++j) {
                 if (j < steps) {
-                    const uint32_t n = g + j, kb = n % F::KB, st = tmem + (n & 1) * NMAX;
+                    const uint32_t n = g + j, kb = n % F::KB, st = tm + n % F::SB * NMAX;
                     wait(k_full + kb, n / F::KB);
                     fence_after();
-                    if (lane == 0 && !dead) {
-                        const uint32_t ka = tmem + F::k_at + kb * (DP / 2);
+                    if (!dead && elect_one()) {
+                        const uint32_t ka = tm + F::k_at + kb * (DP / 2);
 #pragma unroll
                         for (int p = QP - 1; p >= 0; --p) {  // the small parts first: half the roundings at full size
-                            const uint64_t qb = operand_desc(smem_u32(smem + p * F::kQPart));
+                            const uint64_t qb = operand_desc(sm + p * F::kQPart);
 #pragma unroll
                             for (int ks = 0; ks < DP / 16; ++ks)
                                 mma_ts(st, ka + ks * 8, qb + (((ks >> 2) * (NMAX * 128) + (ks & 3) * 32) >> 4), sdesc,
                                        p < QP - 1 || ks > 0 ? 1u : 0u);
                         }
-                        commit_to(s_full + (n & 1));
+                        commit_to(s_full + n % F::SB);
                         commit_to(k_empty + kb);
                     }
                     __syncwarp();
                 }
-                if (j > 0) {
-                    const uint32_t n = g + j - 1, os = n % F::kOps;
+                if (j >= kLag) {
+                    const uint32_t n = g + j - kLag, os = n % F::kOps;
                     wait(v_full + os, n / F::kOps);
-                    wait(p_full + (n & 1), n >> 1);
+                    wait(p_full + n % F::SB, n / F::SB);
                     fence_after();
-                    if (lane == 0 && !dead) {
+                    if (!dead && elect_one()) {
 #pragma unroll
                         for (int acc = 0; acc < F::DA; ++acc) {
-                            const uint64_t vb = operand_desc_mn(smem_u32(smem + F::off_op + os * F::kOp + acc * 32768), 16384);
+                            const uint64_t vb = operand_desc_mn(sm + F::off_op + os * F::kOp + acc * 32768, 16384);
 #pragma unroll
                             for (int p = PP - 1; p >= 0; --p) {
-                                const uint64_t pb = operand_desc_mn(smem_u32(smem + F::off_p + ((n % F::PB) * PP + p) * F::kPPart), 16384);
+                                const uint64_t pb = operand_desc_mn(sm + F::off_p + ((n % F::PB) * PP + p) * F::kPPart, 16384);
 #pragma unroll
                                 for (int ks = 0; ks < kKeys / 16; ++ks)
-                                    mma_ss(o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4), pdesc,
-                                           j > 1 || ks > 0 ? 1u : 0u);
+                                    mma_ss(tm + F::o_at + (p * F::DA + acc) * F::NP, vb + ((ks * 2048) >> 4), pb + ((ks * 2048) >> 4),
+                                           pdesc, j > kLag || ks > 0 ? 1u : 0u);
                             }
                         }
-                        commit_to(pv_done + (n & 1));
+                        commit_to(pv_done + n % F::SB);
                         commit_to(v_empty + os);
                     }
                     __syncwarp();
@@ -834,8 +846,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             if (busy) page = next_page(g);
 
             for (int j = j0; j < j1; ++j, ++g) {
-                // Its MMAs are behind those of step g - 2, whose z's buffer is free then where there are two.
-                wait(s_full + (g & 1), g >> 1);
+                // Its MMAs are behind the second products of step g - 3, whose z's buffer is free then where there are three.
+                wait(s_full + g % F::SB, g / F::SB);
                 fence_after();
                 if (busy) {
                     const float ks = page.x, vs = page.y;
@@ -844,7 +856,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     const int evs = vs > 0.f ? static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 126 : kNoOrder;
                     // pages there whose vs shows in z when e would leave its range
                     const bool plain = __all_sync(~0u, there && evs > -90);
-                    const uint32_t st = tmem + (g & 1) * NMAX + lanes;
+                    const uint32_t st = tmem + g % F::SB * NMAX + lanes;
                     f2 e[8];
                     uint32_t z[8], zl[PP == 2 ? 8 : 1];
                     uint32_t s[16];
@@ -895,7 +907,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     for (int round = 0;; round = 1) {
                         const bool passed = attempt();
                         if (round == 1 || !any_of(wid, 128, passed || huge)) break;
-                        if (j > j0) wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // O stands still
+                        if (j > j0) wait(pv_done + (g - 1) % F::SB, (g - 1) / F::SB);  // O stands still
                         fence_after();
                         settled = huge = new_references<NMAX>(cols, huge_set + set, st, cb, there, ks, evs, wid, o_at + lanes,
                                                        j > j0 ? PP * F::DA : 0);
@@ -905,7 +917,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         }
                     }
                     if (j + 1 < j1) page = next_page(g + 1);
-                    if (F::PB == 1 && g > 0) wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);  // z's buffer is free
+                    if (F::PB == 1 && g > 0) wait(pv_done + (g - 1) % F::SB, (g - 1) / F::SB);  // z's buffer is free
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fadd2(l[i], e[i]);
                     unsigned char* dst = smem + F::off_p + (g % F::PB) * PP * F::kPPart + key * 128;
@@ -923,7 +935,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) arrive_on(p_full + (g & 1));
+                if (lane == 0) arrive_on(p_full + g % F::SB);
             }
 
             // ---- the rows' sums, then their results
@@ -953,7 +965,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     }
                 }
             }
-            wait(pv_done + ((g - 1) & 1), (g - 1) >> 1);
+            wait(pv_done + (g - 1) % F::SB, (g - 1) / F::SB);
             fence_after();
             sync_warps(wid, 128);
             const int place = INT8 ? (lane & ~3) | ((lane & 1) << 1 | (lane & 2) >> 1) : lane;  // dims as k_codes orders them
