@@ -79,7 +79,8 @@ struct XShape {
     static constexpr int kFit = (232448 - kExtra - off_raw) / kRaw;
     static constexpr uint32_t kRaws = kFit < 8 ? kFit : 8;          // of K, then of V
     static constexpr uint32_t kRawK = (kRaws + 1) / 2, kRawV = kRaws / 2;
-    static_assert(kRawV >= RT && kRawV >= 1, "shared memory");
+    // a ring holds a step, whose scales are posted behind its copies of K
+    static_assert(kRawV >= RT && kRawK >= RT, "shared memory");
     static_assert(kOps + kRawV / RT < kScaleSteps, "scales are written while they are read");
     // tensor memory: S^T, O^T (DA of NP for each part of z), K as f16 once or twice
     static constexpr int o_at = static_cast<int>(SB) * NMAX, k_at = o_at + PP * DA * NP;
@@ -496,12 +497,13 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const uint32_t slots = v ? F::kRawV : F::kRawK, slot = n % slots;
             uint64_t* full = (v ? vraw_full : kraw_full) + slot;
             if (n >= slots) wait((v ? vraw_empty : kraw_empty) + slot, n / slots - 1);
+            if (dead) return;  // no arrival at a barrier whose bytes may be outstanding
             if (lane == 0) mbar_arrive_expect_tx(full, valid * 16 * F::RW);
             __syncwarp();
-            if (id >= 0 && (lane & 7) * 16 % box == 0 && !dead)
+            if (id >= 0 && (lane & 7) * 16 % box == 0)
                 tma_load_4d(smem + F::off_raw + (slot + (v ? F::kRawK : 0)) * F::kRaw + (lane & 7) * 16 * F::RW, v ? &vmap : &kmap,
                             tile * F::RW, tok, w.h, id, full);
-            if (!dead) (v ? sent_v : sent_k) = n + 1;
+            (v ? sent_v : sent_k) = n + 1;
         };
         for (;; ++turn) {
             const uint32_t slot = turn % kUnitsAhead;
@@ -696,7 +698,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) arrive_on(vraw_empty + rs);
+                    if (lane == 0 && !dead) arrive_on(vraw_empty + rs);  // a slot goes back only when its copy has landed
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -744,7 +746,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                         tmem_store16(tmem + F::k_at + kb * (DP / 2) + lanes + t * (F::RW / 2) + c * 16, h);
                     }
                     __syncwarp();
-                    if (lane == 0) arrive_on(kraw_empty + rs);
+                    if (lane == 0 && !dead) arrive_on(kraw_empty + rs);
                 }
                 tmem_stored();
                 fence_before();
@@ -837,19 +839,20 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
             const int cb = set * 16;
             const bool busy = cb < nc;  // this set has columns
 
-            bool huge = false;              // the set's scores are
+            bool huge = false, next_ready = false;  // the set's scores are; the next step's scales are there
             float4 page = make_float4(0.f, 0.f, 0.f, 0.f);  // of this step, read a step ahead
-            auto next_page = [&](uint32_t n) {
-                wait(sc_full + n % kScaleSteps, n / kScaleSteps);
+            auto next_page = [&](uint32_t n, bool ready) {
+                if (!ready) wait(sc_full + n % kScaleSteps, n / kScaleSteps);
                 return scales[(n % kScaleSteps) * 8 + (key >> 4)];
             };
-            if (busy) page = next_page(g);
+            if (busy) page = next_page(g, false);
 
             for (int j = j0; j < j1; ++j, ++g) {
                 // Its MMAs are behind the second products of step g - 3, whose z's buffer is free then where there are three.
                 wait(s_full + g % F::SB, g / F::SB);
                 fence_after();
                 if (busy) {
+                    next_ready = j + 1 < j1 && __all_sync(~0u, mbar_try_wait(sc_full + (g + 1) % kScaleSteps, ((g + 1) / kScaleSteps) & 1u));
                     const float ks = page.x, vs = page.y;
                     const bool there = page.z != 0.f;
                     // vs < 2^evs
@@ -916,7 +919,6 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                             for (int i = 0; i < 8; ++i) l[i] = fmul2(l[i], *reinterpret_cast<const f2*>(cols.mul + cb + 2 * i));
                         }
                     }
-                    if (j + 1 < j1) page = next_page(g + 1);
                     if (F::PB == 1 && g > 0) wait(pv_done + (g - 1) % F::SB, (g - 1) / F::SB);  // z's buffer is free
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fadd2(l[i], e[i]);
@@ -936,6 +938,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 }
                 __syncwarp();
                 if (lane == 0) arrive_on(p_full + g % F::SB);
+                if (busy && j + 1 < j1) page = next_page(g + 1, next_ready);
             }
 
             // ---- the rows' sums, then their results

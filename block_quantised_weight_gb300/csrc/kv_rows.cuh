@@ -193,8 +193,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     unsigned issued = 0, taken = 0;  // stages over the life of the kernel
     bool dead = false;  // a wait of this lane gave up: none follows, and no copy if it is lane 0, which issues them
 
-    // ---- the line: prefix sums of the sequences' tiles
-    {
+    // ---- the line: prefix sums of the sequences' tiles (`whole`: of their blocks for all heads)
+    auto measure = [&](bool whole) {
         int64_t base = 0;
         for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
             const int b = b0 + tid;
@@ -203,7 +203,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 Seq s = sequence(a, b);
                 if (SHARED) shared_columns(a, b, s);
                 const int64_t blocks = (static_cast<int64_t>(s.n) * a.group + RU - 1) / RU;
-                x = blocks * c.heads * max(1, (s.len + kTile - 1) / kTile);
+                x = blocks * c.heads * (whole ? 1 : max(1, (s.len + kTile - 1) / kTile));
                 seqs[b] = make_int2(s.n, s.len);
             }
 #pragma unroll
@@ -220,23 +220,28 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         }
         if (tid == 0) pre[0] = 0;
         __syncthreads();
-    }
-    const Line line(pre[a.batch], grid);
+    };
+    measure(false);
+    Line line(pre[a.batch], grid);
     const int cta = blockIdx.x;
-    if (cta >= line.ctas) {
-        if (SHARED) grid_dependency_wait();
-        return;
-    }
-    const int64_t u_begin = line.first(cta), u_end = line.first(cta + 1);
     // Behind a prefix sequences are short, and beginning and joining a piece costs as
     // much as some tiles: where the longest is hardly longer than a CTA's share,
-    // none is cut, and a CTA takes those whose first tile lies in its share.
+    // none is cut, and the line counts them whole.
     bool uncut = false;
     if (SHARED) {
         int longest = 0;
         for (int b = tid; b < a.batch; b += kThreads) longest = max(longest, seqs[b].y);
         uncut = __syncthreads_or((longest + kTile - 1) / kTile > line.each + kUncut) == 0;
+        if (uncut) {
+            measure(true);
+            line = Line(pre[a.batch], grid);
+        }
     }
+    if (cta >= line.ctas) {
+        if (SHARED) grid_dependency_wait();
+        return;
+    }
+    const int64_t u_begin = line.first(cta), u_end = line.first(cta + 1);
 
     int64_t u = u_begin;
     while (u < u_end) {
@@ -260,12 +265,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];
-        const int hb = static_cast<int>(div64(in, tiles));
-        const int tile0 = static_cast<int>(in - static_cast<int64_t>(hb) * tiles);
-        if (SHARED && uncut && tile0) {  // another CTA's
-            u += tiles - tile0;
-            continue;
-        }
+        const int hb = static_cast<int>(SHARED && uncut ? in : div64(in, tiles));
+        const int tile0 = SHARED && uncut ? 0 : static_cast<int>(in - static_cast<int64_t>(hb) * tiles);
         const int h = hb / blocks, rb = hb - h * blocks;
         const int64_t span0 = u - tile0;
         const int seg = SHARED && uncut ? tiles : static_cast<int>(min(static_cast<int64_t>(tiles - tile0), u_end - u));
@@ -880,7 +881,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 }
             }
         }
-        u += seg;
+        u += SHARED && uncut ? 1 : seg;
     }
     if (SHARED) grid_dependency_wait();  // no launch behind this one meets the one before
 }
