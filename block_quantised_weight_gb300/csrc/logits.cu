@@ -14,6 +14,14 @@
 // of arrival does not show.  In place and without a temperature only what changes
 // is touched.
 //
+// Measured (GB300, bytes read and written at the copy rate in brackets): 384 x
+// 128257 fp32, histories of up to 4096, 113 us (59), 105 without most of the
+// histories and 107 without the division; 96 x 50257 in bf16 12.2 us (2.9); one
+// row 3.6 us.  What is left beyond HBM is the row of steps of a CTA (table,
+// histories, stream, listed tokens) that 8 CTAs an SM overlap: spans of 2048 or
+// 512 threads took 150 us, the stream's loads in registers ahead of the
+// histories 200, 6 CTAs an SM 116 to 122.
+//
 #include <algorithm>
 
 #include "kv_common.cuh"
@@ -24,7 +32,6 @@ namespace qg {
 namespace {
 
 constexpr int kThreadsL = 256;
-constexpr int kPerL = 8;           // logits of a thread on their way at once
 constexpr int kMostSpan = 4096;    // tokens of a CTA: a table of 16 KB, a list of 8
 // A token's word: how often it was produced, whether it came at all, and the
 // place in the list, counted from 1, of the last bias for it.
@@ -60,8 +67,8 @@ __device__ __forceinline__ void store_as(__half* p, float x) { *p = __float2half
 __device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // x / t for many x, correctly rounded: from the rounded reciprocal of t, two remainders each exact in one fma
-// (Markstein, IBM J. Res. Dev. 34, 1990).  Operands whose quotients, products or remainders could leave
-// fp32's normal range, zeros, infinities and NaN take the division itself.
+// (Markstein, IBM J. Res. Dev. 34, 1990), where no quotient, product or remainder leaves fp32's normal range;
+// other operands (zeros, infinities, far ends) take the division itself.
 struct Divisor {
     float t, r;
     bool near_one;
@@ -69,17 +76,54 @@ struct Divisor {
         t = by, r = __frcp_rn(by);
         near_one = fabsf(by) >= 0x1p-40f && fabsf(by) <= 0x1p40f;
     }
-    __device__ __forceinline__ float of(float x) const {
-        const float ax = fabsf(x);
-        if (!(near_one && ax >= 0x1p-60f && ax <= 0x1p60f)) return __fdiv_rn(x, t);
-        float q = __fmul_rn(x, r);
-        q = __fmaf_rn(__fmaf_rn(-q, t, x), r, q);
-        return __fmaf_rn(__fmaf_rn(-q, t, x), r, q);
+    template <int N>
+    __device__ __forceinline__ void divide(float (&x)[N]) const {
+        float most = 0.f, least = INFINITY;  // NaN is passed over: it stays NaN either way
+#pragma unroll
+        for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(x[i])), least = fminf(least, fabsf(x[i]));
+        if (near_one && least >= 0x1p-60f && most <= 0x1p60f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float q = __fmul_rn(x[i], r);
+                q = __fmaf_rn(__fmaf_rn(-q, t, x[i]), r, q);
+                x[i] = __fmaf_rn(__fmaf_rn(-q, t, x[i]), r, q);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                float y = 0.f;
+#pragma unroll
+                for (int k = 0; k < N; ++k) y = k == i ? x[k] : y;
+                y = __fdiv_rn(y, t);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[k] = k == i ? y : x[k];
+            }
+        }
     }
 };
 
+// 16 bytes of values, and N values stored in whole 16 bytes.
+template <class T, int N>
+__device__ __forceinline__ void values_of(const uint4& u, float (&x)[N]) {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+}
+template <int N>
+__device__ __forceinline__ void store_all(float* p, const float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+}
+template <class O, int N>
+__device__ __forceinline__ void store_all(O* p, const float (&x)[N]) {
+    O e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) store_as(e + i, x[i]);
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(e));
+}
+
 template <class T, class O, bool TABLE>
-__global__ void __launch_bounds__(kThreadsL) qg_logits_kernel(const LogitArgs a) {
+__global__ void __launch_bounds__(kThreadsL, 8) qg_logits_kernel(const LogitArgs a) {
     extern __shared__ __align__(16) unsigned table[];              // [span], then
     uint16_t* listed = reinterpret_cast<uint16_t*>(table + a.span);  // [span] tokens with a word
     __shared__ int count;
@@ -89,7 +133,13 @@ __global__ void __launch_bounds__(kThreadsL) qg_logits_kernel(const LogitArgs a)
     const int n = static_cast<int>(min(static_cast<int64_t>(a.span), a.vocab - lo));
     const T* x = static_cast<const T*>(a.x) + row * a.x_row + lo;
     O* out = static_cast<O*>(a.out) + row * a.out_row + lo;
-    const bool heat = a.temperature != nullptr;
+    const bool heat = a.temperature != nullptr, all = !a.in_place || heat;  // not all: others than the listed stay but for the mask
+    if (TABLE && all && tid == 0) {  // the span comes to L2 while the table is filled
+        const uintptr_t from = (reinterpret_cast<uintptr_t>(x) + 15) & ~uintptr_t(15);
+        const uintptr_t to = reinterpret_cast<uintptr_t>(x + n) & ~uintptr_t(15);
+        if (to > from)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(to - from)) : "memory");
+    }
     const Divisor temperature(heat ? a.temperature[row] : 1.f);
     const uint32_t* mask = nullptr;
     if (a.mask) {
@@ -154,29 +204,52 @@ __global__ void __launch_bounds__(kThreadsL) qg_logits_kernel(const LogitArgs a)
         }
         __syncthreads();  // all have read their logits before they are written in place
     }
-    const bool all = !a.in_place || heat;  // else the others stay but for the mask
-    if (all || mask) {
-        int at = tid;
-        for (; at + (kPerL - 1) * kThreadsL < n; at += kThreadsL * kPerL) {
-            float v[kPerL];
-            uint32_t bits[kPerL];
+    auto shown = [&](int t) { return !mask || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u); };
+    auto one = [&](int t) {
+        const bool hidden = !shown(t);
+        if (!all && !hidden) return;
+        float y[1] = {hidden ? 0.f : to_f32(x[t])};
+        if (heat && !hidden) temperature.divide(y);
+        store_as(out + t, hidden ? -INFINITY : y[0]);
+    };
+    // Whole 16 bytes where input and output meet their borders at the same tokens (a vocabulary of odd size
+    // shifts both alike), the few before and behind them one by one.
+    constexpr int V = 16 / sizeof(T);
+    const int head = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T));
+    if (all && n >= 2 * V && (reinterpret_cast<uintptr_t>(out + head) & 15) == 0) {
+        const int vectors = (n - head) / V, rest = head + vectors * V;
+        const int last_word = (n - 1) >> 5;
+        constexpr int U = 2;  // vectors on their way at once
+        for (int v0 = tid; v0 < vectors; v0 += U * kThreadsL) {
+            uint4 u[U];
+            uint32_t bits[U];
 #pragma unroll
-            for (int i = 0; i < kPerL; ++i) {
-                if (all) v[i] = to_f32(x[at + i * kThreadsL]);
-                if (mask) bits[i] = __ldg(mask + ((at + i * kThreadsL) >> 5)) >> (at & 31);
+            for (int i = 0; i < U; ++i) {
+                const int v = v0 + i * kThreadsL, t = head + v * V;
+                if (v < vectors) {
+                    u[i] = __ldcs(reinterpret_cast<const uint4*>(x + t));
+                    if (mask) bits[i] = __funnelshift_r(__ldg(mask + (t >> 5)), __ldg(mask + min((t >> 5) + 1, last_word)), t & 31);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < kPerL; ++i) {
-                if (heat) v[i] = temperature.of(v[i]);
-                const bool hidden = mask && !(bits[i] & 1u);
-                if (all || hidden) store_as(out + at + i * kThreadsL, hidden ? -INFINITY : v[i]);
+            for (int i = 0; i < U; ++i) {
+                const int v = v0 + i * kThreadsL, t = head + v * V;
+                if (v >= vectors) break;
+                float y[V];
+                values_of<T>(u[i], y);
+                if (heat) temperature.divide(y);
+                if (mask) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (!(bits[i] >> k & 1u)) y[k] = -INFINITY;
+                }
+                store_all(out + t, y);
             }
         }
-        for (; at < n; at += kThreadsL) {
-            const bool hidden = mask && !((__ldg(mask + (at >> 5)) >> (at & 31)) & 1u);
-            if (hidden) store_as(out + at, -INFINITY);
-            else if (all) store_as(out + at, heat ? temperature.of(to_f32(x[at])) : to_f32(x[at]));
-        }
+        if (tid < head) one(tid);
+        if (rest + tid < n) one(rest + tid);
+    } else if (all || mask) {
+        for (int t = tid; t < n; t += kThreadsL) one(t);
     }
     if (TABLE) {
         __syncthreads();  // behind the stream's writes
