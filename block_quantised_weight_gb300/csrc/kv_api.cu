@@ -127,7 +127,7 @@ int prepare_attention(const qgkv_cache* cache, int64_t layer, const void* q, voi
     return QG_OK;
 }
 
-int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
+bool many_rows(const qg::AttnArgs& a) {
     // The tcgen05 kernel takes as long for one query row (token x head of a
     // group) a sequence as for 256, the row kernel's time grows with them.  Row
     // kernel / tcgen05 kernel, us, e4m3, 32 / 8 heads of 128, by query rows a
@@ -147,9 +147,24 @@ int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
     // single tokens goes the way of the single tokens, or they its.
     const int sms = qg::sm_count(qg::current_device());
     const int few = a.type == QGKV_F16 || 2 * static_cast<int64_t>(a.batch) * a.c.heads < sms ? 256 : 128;
-    const bool many = a.rows * a.group >= static_cast<int64_t>(few) * a.batch && a.starts && a.c.dim <= 128;
-    if (many) return qg::launch_attn_prompt(a, int8, stream);
-    return qg::launch_attn_rows(a, int8, stream);
+    return a.rows * a.group >= static_cast<int64_t>(few) * a.batch && a.starts && a.c.dim <= 128;
+}
+
+int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
+    return many_rows(a) ? qg::launch_attn_prompt(a, int8, stream) : qg::launch_attn_rows(a, int8, stream);
+}
+
+// The most bytes of pages that a plan can save, by the table's width, have to be
+// worth a second kernel and the join.  Shared / each for itself, us:
+//   4 beams of 820 tokens, 4 heads of 64 (1.3 MB): 13.6 / 8.2
+//   4 of 1080, 8 heads of 128 (6.7 MB): 15.0 / 10.8;  8 groups of 4 of 1060, 4 heads of 64 (17 MB): 15.7 / 14.2
+//   4 of 4160, 8 heads of 128 (26 MB): 16.3 / 18.2;  48 of 1320 (130 MB): 26 / 27;  48 of 8800 (850 MB): 42 / 97
+// Widths are all that the host knows: behind a table much wider than its
+// sequences a small plan is followed all the same.
+constexpr double kLeastSaved = 16 << 20;
+bool worth_sharing(const qg::AttnArgs& a) {
+    const double most = 2.0 * (a.batch - 1) * a.width * (int64_t(1) << a.c.log2p) * a.c.heads * a.c.dim;
+    return most >= kLeastSaved && !many_rows(a);
 }
 
 }  // namespace
@@ -270,7 +285,8 @@ int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q,
                                      {plan, (4 * int64_t(ngroups) + batch) * 4}, a, &done);
     if (rc != QG_OK || done) return rc;
     const bool int8 = cache->format == QGKV_INT8;
-    if (qg::own_bytes(rows, q_heads, cache->head_dim) > qg::kWsSplits - qg::kWsOwn) return launch_attention(a, int8, stream);
+    if (!worth_sharing(a) || qg::own_bytes(rows, q_heads, cache->head_dim) > qg::kWsSplits - qg::kWsOwn)
+        return launch_attention(a, int8, stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.groups = reinterpret_cast<const int4*>(plan);
     a.skip = plan + 4 * int64_t(ngroups);

@@ -169,10 +169,14 @@ QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int6
  * once for all rows of a group, and the results joined with those of the tokens
  * behind them.  plan: what qgkv_share wrote for the same table, lens and starts;
  * an entry that does not fit them counts as nothing shared (QG_EBOUNDS, and the
- * rows of its group are not valid).  Everything else, numerics included, is as for
- * qgkv_attention.  Where sharing would gain nothing (few tokens, many rows a
- * sequence) or the results to join exceed the workspace, each sequence reads
- * all its tokens itself. */
+ * rows of its group are not valid).  Results are those of qgkv_attention to within
+ * its numerics, but for what small weights and scales of V keep among the tokens
+ * shared: bf16 q to within 2^-28 of the row's largest weight, other types 2^-39; full
+ * precision for scales of V of 2^-80 to 2^90 (qgkv_append writes none outside for
+ * values of 2^-70 to 2^97).  Where sharing gains nothing each sequence reads all its
+ * tokens itself and the plan is not read: the table's width times its sequences come
+ * to less than 16 MB of pages, many rows a sequence, or more results to join than the
+ * workspace holds.  The choice depends on the call's sizes alone. */
 QG_API int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                                  int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride,
                                  const int32_t* table, int64_t table_width, const int32_t* lens,

@@ -22,11 +22,20 @@ from test_kv_gpu import DT, attention_ref, close, i32, kv, make, starts_of, stat
 pytestmark = pytest.mark.gpu
 
 
-def shared_table(kv, shape, heads, dim, page, fmt, order, seed=0, layers=2):  # noqa: F811
+LEAST = 16 << 20  # bytes of pages that a table has to have room for, beyond one sequence's, to be shared
+
+
+def least_width(batch, heads, dim, page):
+    return -(-LEAST // (2 * (batch - 1) * heads * dim * page))
+
+
+def shared_table(kv, shape, heads, dim, page, fmt, order, seed=0, layers=2, wide=True):  # noqa: F811
     """shape: for each group (tokens of the prefix, tokens of each sequence behind it).  Whole pages of a prefix are the
-    first sequence's.  Returns cache, table, lens (list), borders of the groups."""
+    first sequence's.  wide: the table has columns enough for its pages to be shared, however few are held.  Returns
+    cache, table, lens (list), borders of the groups."""
     lens = [p + t for p, tails in shape for t in tails]
-    cache, table, _ = make(kv, lens, heads, dim, page, fmt, order, seed=seed, layers=layers)
+    width = max(*(-(-n // page) for n in lens), least_width(len(lens), heads, dim, page)) if wide else None
+    cache, table, _ = make(kv, lens, heads, dim, page, fmt, order, seed=seed, layers=layers, width=width)
     ids, at, borders = table.cpu().numpy(), 0, [0]
     for p, tails in shape:
         for i in range(len(tails)):
@@ -141,7 +150,7 @@ def test_sequences_of_no_group(kv, ws):  # noqa: F811
 
 
 def test_share_of_bad_inputs(kv, ws):  # noqa: F811
-    cache, table, lens, borders = shared_table(kv, [(80, [3, 9, 1]), (96, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    cache, table, lens, borders = shared_table(kv, [(80, [3, 9, 1]), (96, [5, 5])], 2, 64, 16, "e4m3", "hnd", wide=False)
     for bad in ([0, 4, 2], [-1, 3, 5], [0, 3, 6], [5, 3, 5]):
         plan = kv.kv_share(cache, table, i32(lens), i32(bad))
         assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS and (plan == 0).all()
@@ -393,6 +402,39 @@ def test_shared_results_beyond_the_workspace(kv, ws):  # noqa: F811
     some = list(range(0, batch, 97)) + [batch - 1]
     ref = attention_ref(cache, 0, q[some], table[some], [lens[b] for b in some], list(range(len(some) + 1)), 128 ** -0.5)
     close(out[some], lse[some], small(ref, "bf16"), 900, torch.bfloat16, one_part=True)
+
+
+def test_shared_from_a_width_on(kv, ws):  # noqa: F811
+    """On both sides of the least width: below it kv_attention's bits, whatever the plan; from it on the plan is read."""
+    cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    q, least = torch.randn((5, 8, 64), device="cuda"), least_width(5, 2, 64, 16)
+    assert table.shape[1] == least
+    ref = attention_ref(cache, 0, q, table, lens, list(range(6)), 1 / 8)
+    for width in (least - 1, least):
+        ids = table[:, :width].contiguous()
+        plan = kv.kv_share(cache, ids, i32(lens), i32(borders))
+        got = kv.kv_attention_shared(cache, 0, q, ids, i32(lens), plan, return_lse=True, workspace=ws)
+        plain = kv.kv_attention(cache, 0, q, ids, i32(lens), return_lse=True, workspace=ws)
+        close(*got, ref, max(lens) + 512, torch.float32)
+        if width < least:
+            assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+        plan[2] = 7
+        kv.kv_attention_shared(cache, 0, q, ids, i32(lens), plan, workspace=ws)
+        assert qgemv.qg_device_status() == (qgemv.QG_OK if width < least else qgemv.QG_EBOUNDS)
+
+
+@pytest.mark.parametrize("rows, shared", [(31, True), (32, False)])
+def test_shared_up_to_many_rows(kv, ws, rows, shared):  # noqa: F811
+    """128 query rows a sequence of 80 go to the kernel of prompts, which shares nothing."""
+    lens = [200 + i for i in range(80)]
+    cache, table, _, borders = shared_table(kv, [(160, [n - 160 for n in lens])], 1, 64, 16, "e4m3", "hnd")
+    st = [rows * i for i in range(81)]
+    q = torch.randn((st[-1], 4, 64), device="cuda").bfloat16()
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=i32(st))
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, starts=i32(st), return_lse=True, workspace=ws)
+    plain = kv.kv_attention(cache, 0, q, table, i32(lens), starts=i32(st), return_lse=True, workspace=ws)
+    assert torch.equal(got[1], plain[1]) != shared
+    close(*got, small(attention_ref(cache, 0, q, table, lens, st, 1 / 8), "bf16"), max(lens) + 512, torch.bfloat16, one_part=True)
 
 
 def test_shared_largest_batch(kv, ws):  # noqa: F811
