@@ -1,5 +1,6 @@
 """ctypes binding of the decode-state operators (include/qgkv.h): the 8-bit
-paged key/value cache, its attention, page operations and beam selection.
+paged key/value cache, its attention, page operations, the adjustment of logits and
+beam selection.
 
 Argument marshalling only: each function checks torch CUDA tensors and calls
 the C entry point on the current torch stream (or on `stream=`).  There is
@@ -11,8 +12,11 @@ caller orders the streams.
     cache = KVCache.allocate(layers=22, pages=4096, heads=4, page_tokens=64, head_dim=64)
     ws = KVWorkspace("cuda")
     kv_reserve(cache, table, lens, refs, workspace=ws)       # pages for one token each
-    kv_append(cache, layer, k, v, table, lens)               # then lens += 1
+    q = kv_append_rotary(cache, layer, q, k, v, rope, table, lens)  # or kv_append; then lens += 1
     out = kv_attention(cache, layer, q, table, lens, workspace=ws)
+    plan = kv_share(cache, table, lens, groups)              # once a step: what its sequences have in common
+    out = kv_attention_shared(cache, layer, q, table, lens, plan, workspace=ws)
+    logits = adjust_logits(logits, history, history_lens, repetition=penalty, mask=allowed)
     scores, tokens, parents = beam_select(logits, cum, keep, workspace=ws)
     table, lens, refs = kv_fork(cache, table, lens, parents.view(-1), refs, workspace=ws)
 """

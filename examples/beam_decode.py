@@ -2,12 +2,12 @@
 
 A TinyLlama-shaped decoder (RMSNorm, rotary positions, grouped-query attention,
 SwiGLU) with synthetic Q4_K weights: the linear layers are the fused GEMVs of
-``qgemv``, everything between them that a decode keeps is ``qgkv`` - the cache's
-append and attention, the selection over beams and vocabulary, and the fork of
-the beams' pages.  torch holds the memory and does the rotary positions and the
-embedding lookup.
+``qgemv``, everything between them is ``qgkv`` - the rotary positions with the
+cache's append, the attention with the pages that beams share read once, penalties and
+masks of the logits, the selection over beams and vocabulary, and the fork of
+the beams' pages.  torch holds the memory and does the embedding lookup.
 
-    python examples/beam_decode.py [--layers 22] [--steps 32] [--beams 4]
+    python examples/beam_decode.py [--layers 22] [--steps 32] [--beams 4] [--repetition 1.1] [--prompt 21]
 """
 from __future__ import annotations
 
@@ -47,32 +47,24 @@ class Model:
         self.cache = qgkv.KVCache.allocate(layers, pages, kv_heads, page_tokens, self.dim, fmt, device=device)
         self.refs = torch.zeros(pages, dtype=torch.int32, device=device)
         self.workspace = qgkv.KVWorkspace(device)
-        self.freq = 10000.0 ** (-torch.arange(0, self.dim, 2, device=device, dtype=torch.float64) / self.dim)
+        self.rope = qgkv.rotary_table(pages * page_tokens, self.dim, device=device)
 
-    def rotate(self, x, pos):
-        """Rotary positions (angles in 64 bits) of x [rows, heads, dim]."""
-        angle = pos.double()[:, None] * self.freq
-        cos, sin = torch.cos(angle).float()[:, None], torch.sin(angle).float()[:, None]
-        a, b = x[..., 0::2], x[..., 1::2]
-        return torch.stack((a * cos - b * sin, a * sin + b * cos), dim=-1).flatten(-2)
-
-    def step(self, tokens, table, lens, starts=None):
+    def step(self, tokens, table, lens, starts=None, groups=None):
         """Logits of `tokens` (at most four rows), which go behind each sequence's lens[b]
-        tokens: one a sequence, or by `starts`.  The pages must be reserved."""
+        tokens: one a sequence, or by `starts`.  The pages must be reserved.  groups: borders of
+        sequences that share pages."""
         rows = tokens.shape[0]
         x = self.embedding[tokens.long()].contiguous()
-        if starts is None:
-            new, pos = 1, lens
-        else:
-            new = starts[1:] - starts[:-1]
-            pos = lens.repeat_interleave(new) + torch.arange(rows, device=self.device) - starts[:-1].repeat_interleave(new)
-        held = (lens + new).int()
+        held = (lens + (1 if starts is None else starts[1:] - starts[:-1])).int()
+        plan = None if groups is None else qgkv.kv_share(self.cache, table, held, groups, starts=starts)
         for i, w in enumerate(self.layers):
             q, k, v = qgemv.qgemv_q4k_fused_group([w["q"], w["k"], w["v"]], x, norm_weight=w["norm1"], eps=self.eps)
-            q = self.rotate(q.view(rows, self.q_heads, self.dim), pos)
-            k = self.rotate(k.view(rows, self.kv_heads, self.dim), pos)
-            qgkv.kv_append(self.cache, i, k, v.view(rows, self.kv_heads, self.dim), table, lens, starts=starts)
-            a = qgkv.kv_attention(self.cache, i, q, table, held, starts=starts, workspace=self.workspace)
+            q, k, v = (t.view(rows, -1, self.dim) for t in (q, k, v))
+            q = qgkv.kv_append_rotary(self.cache, i, q, k, v, self.rope, table, lens, starts=starts)
+            if plan is None:
+                a = qgkv.kv_attention(self.cache, i, q, table, held, starts=starts, workspace=self.workspace)
+            else:
+                a = qgkv.kv_attention_shared(self.cache, i, q, table, held, plan, starts=starts, workspace=self.workspace)
             x = qgemv.qgemv_q4k_fused(w["o"], a.view(rows, self.hidden), residual=x)
             gate, up = qgemv.qgemv_q4k_fused_group([w["gate"], w["up"]], x, norm_weight=w["norm2"], eps=self.eps)
             x = qgemv.qgemv_q4k_fused(w["down"], gate, up=up, residual=x)
@@ -90,16 +82,32 @@ class Model:
         return logits[-1:]
 
 
-def beam_search(model, prompt, beams=4, steps=16):
-    """(scores, tokens) of the best `beams` continuations of `prompt` by `steps` tokens."""
+def beam_search(model, prompt, beams=4, steps=16, repetition=1.0, banned=()):
+    """(scores, tokens) of the best `beams` continuations of `prompt` by `steps` tokens.  repetition: the penalty of
+    tokens that came before, the prompt's among them; banned: tokens that are not produced."""
     dev, ws = model.device, model.workspace
     width = (len(prompt) + steps + model.cache.page_tokens) // model.cache.page_tokens + 1
     table = torch.full((1, width), -1, dtype=torch.int32, device=dev)
     lens = torch.zeros(1, dtype=torch.int32, device=dev)
     logits = model.prefill(prompt, table, lens)
     cum = torch.zeros((1, 1), device=dev)
+    before = torch.tensor([prompt], dtype=torch.int32, device=dev)
     history = torch.empty((1, 0), dtype=torch.int32, device=dev)
+    groups = torch.tensor([0, beams], dtype=torch.int32, device=dev)
+    mask = None
+    if len(banned):
+        allowed = torch.ones((1, -(-model.vocab // 32) * 32), dtype=torch.int64, device=dev)
+        allowed[0, list(banned)] = 0
+        bits = (allowed.view(1, -1, 32) << torch.arange(32, device=dev)).sum(-1)
+        mask = torch.where(bits >= 1 << 31, bits - (1 << 32), bits).int()
     for _ in range(steps):
+        if repetition != 1.0 or mask is not None:
+            n = logits.shape[0]
+            said = torch.cat((before.expand(n, -1), history), dim=1)
+            logits = qgkv.adjust_logits(
+                logits, history=said, lens=torch.full((n,), said.shape[1], dtype=torch.int32, device=dev),
+                repetition=torch.full((n,), repetition, device=dev), mask=mask,
+                mask_rows=None if mask is None else torch.zeros(n, dtype=torch.int32, device=dev))
         scores, tokens, parents = qgkv.beam_select(logits, cum, beams, workspace=ws)
         # the beams continue their parents: pages are shared, the partly filled last one is copied
         table, lens, model.refs = qgkv.kv_fork(model.cache, table, lens, parents.view(-1), model.refs, workspace=ws)
@@ -108,7 +116,7 @@ def beam_search(model, prompt, beams=4, steps=16):
         if history.shape[1] == steps:
             break
         qgkv.kv_reserve(model.cache, table, lens, model.refs, workspace=ws)
-        logits = model.step(tokens.view(-1), table, lens)
+        logits = model.step(tokens.view(-1), table, lens, groups=groups)
         lens += 1
     qgkv.kv_free(model.cache, table, lens, model.refs)
     if qgemv.qg_device_status() != qgemv.QG_OK:
@@ -121,14 +129,16 @@ def main():
     p.add_argument("--layers", type=int, default=22)
     p.add_argument("--steps", type=int, default=32)
     p.add_argument("--beams", type=int, default=4, choices=range(1, 5))
+    p.add_argument("--repetition", type=float, default=1.0)
+    p.add_argument("--prompt", type=int, default=21, help="tokens of the prompt")
     p.add_argument("--fmt", default="e4m3", choices=sorted(qgkv.FORMATS))
     a = p.parse_args()
-    model = Model(layers=a.layers, fmt=a.fmt)
-    prompt = [(7 * i * i + 3) % model.vocab for i in range(21)]
-    beam_search(model, prompt, a.beams, 2)  # first use
+    model = Model(layers=a.layers, fmt=a.fmt, pages=512 + a.prompt // 16)
+    prompt = [(7 * i * i + 3) % model.vocab for i in range(a.prompt)]
+    beam_search(model, prompt, a.beams, 2, a.repetition)  # first use
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
-    scores, tokens = beam_search(model, prompt, a.beams, a.steps)
+    scores, tokens = beam_search(model, prompt, a.beams, a.steps, a.repetition)
     end.record()
     torch.cuda.synchronize()
     for s, t in zip(scores.tolist(), tokens.tolist()):
