@@ -9,20 +9,23 @@
 // vocabulary in two parts.  It gathers those tokens of its span from the whole
 // history and list of the row, in a table in shared memory with a word a token (how
 // often it came, which bias is its last), lists each once, and works out their
-// logits; then it streams the span with a division and the mask alone, and writes the
-// listed ones over it.  The table's atomics are integer additions and maxima: the order
+// logits; and it streams the span with a division and the mask alone, the listed ones written
+// over it.  The table's atomics are integer additions and maxima: the order
 // of arrival does not show.  In place and without a temperature only what changes
 // is touched.
 //
+// Out of place the stream may come first, and it overlaps the history's reading by other warps; only the listed tokens
+// wait for both.  In place their logits are read, and kept, before the stream writes them.
+//
 // Measured (GB300, bytes read and written at the copy rate in brackets): 384 x
-// 128257 fp32, histories of up to 4096, 113 us (59), 105 without most of the
-// histories and 107 without the division; 96 x 50257 in bf16 12.2 us (2.9); one
-// row 3.6 us.  What is left beyond HBM is the row of steps of a CTA (table,
-// histories, stream, listed tokens) that 8 CTAs an SM overlap: spans of 2048 or
-// 512 threads took 150 us, the stream's loads in registers ahead of the
-// histories 200, 6 CTAs an SM 116 to 122.
+// 128257 fp32, histories of up to 2500, 96 us (59), 68 of them for the stream alone, 80 without
+// the histories; 96 x 50257 in bf16 11.5 us (2.9), 4 x 32000 3.3 us: launch and the chain
+// lengths -> history -> marks -> listed logits.  Steps with a barrier behind each and
+// loads in their place took 113 us, without the prefetch of the span to L2 119; spans
+// of 2048 or 512 threads 150, the stream's loads in registers ahead of the histories 200, 6 CTAs an SM 108.
 //
 #include <algorithm>
+#include <cmath>
 
 #include "kv_common.cuh"
 #include "launch_common.cuh"
@@ -32,7 +35,8 @@ namespace qg {
 namespace {
 
 constexpr int kThreadsL = 256;
-constexpr int kMostSpan = 4096;    // tokens of a CTA: a table of 16 KB, a list of 8
+constexpr int kLeastSpan = 1024, kMostSpan = 4096;  // tokens of a CTA: a table and a list of 6 bytes each, of 8 CTAs an SM
+constexpr int kCtasL = 8;
 // A token's word: how often it was produced, whether it came at all, and the
 // place in the list, counted from 1, of the last bias for it.
 constexpr unsigned kCame = 1u << 20;
@@ -65,6 +69,15 @@ struct LogitArgs {
 __device__ __forceinline__ void store_as(float* p, float x) { __stcs(p, x); }
 __device__ __forceinline__ void store_as(__half* p, float x) { *p = __float2half_rn(x); }
 __device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// An addition in shared memory that each lane makes by itself: few lanes come here at once, and joining them
+// first costs more than it saves.
+__device__ __forceinline__ unsigned add_shared(unsigned* p, unsigned x) {
+    unsigned was;
+    asm volatile("atom.shared.add.u32 %0, [%1], %2;"
+                 : "=r"(was) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(x) : "memory");
+    return was;
+}
 
 // x / t for many x, correctly rounded: from the rounded reciprocal of t, two remainders each exact in one fma
 // (Markstein, IBM J. Res. Dev. 34, 1990), where no quotient, product or remainder leaves fp32's normal range;
@@ -123,10 +136,10 @@ __device__ __forceinline__ void store_all(O* p, const float (&x)[N]) {
 }
 
 template <class T, class O, bool TABLE>
-__global__ void __launch_bounds__(kThreadsL, 8) qg_logits_kernel(const LogitArgs a) {
+__global__ void __launch_bounds__(kThreadsL, kCtasL) qg_logits_kernel(const LogitArgs a) {
     extern __shared__ __align__(16) unsigned table[];              // [span], then
     uint16_t* listed = reinterpret_cast<uint16_t*>(table + a.span);  // [span] tokens with a word
-    __shared__ int count;
+    __shared__ unsigned count;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / a.chunks;
     const int64_t lo = (blockIdx.x - row * a.chunks) * static_cast<int64_t>(a.span);
@@ -140,6 +153,26 @@ __global__ void __launch_bounds__(kThreadsL, 8) qg_logits_kernel(const LogitArgs
         if (to > from)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(to - from)) : "memory");
     }
+    // What the steps below need comes on its way together: lengths and the first biases, then the first of the history.
+    int len = 0, made_from = 0;  // tokens of the history, the first that was produced
+    float rho = 1.f, presence = 0.f, frequency = 0.f;
+    int32_t biased = -1;
+    const int32_t* past = nullptr;
+    const int32_t* bias_at = nullptr;
+    if (TABLE) {
+        if (a.bias_tokens) {
+            bias_at = a.bias_tokens + row * a.biases;
+            if (tid < a.biases) biased = __ldg(bias_at + tid);
+        }
+        if (a.history) {
+            past = a.history + row * a.width;
+            len = a.lens[row];
+            if (a.prompt_lens) made_from = a.prompt_lens[row];
+            if (a.repetition) rho = a.repetition[row];
+            if (a.presence) presence = a.presence[row];
+            if (a.frequency) frequency = a.frequency[row];
+        }
+    }
     const Divisor temperature(heat ? a.temperature[row] : 1.f);
     const uint32_t* mask = nullptr;
     if (a.mask) {
@@ -150,59 +183,76 @@ __global__ void __launch_bounds__(kThreadsL, 8) qg_logits_kernel(const LogitArgs
     if (TABLE) {
         for (int i = tid; i < a.span / 4; i += kThreadsL) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
         if (tid == 0) count = 0;
-        __syncthreads();
-        auto first = [&](unsigned was, int t) {
-            if (was == 0u) listed[atomicAdd(&count, 1)] = static_cast<uint16_t>(t);
+        if (len < 0 || len > a.width) {
+            if (tid == 0) atomicOr(a.status, kStatusBounds);
+            len = len < 0 ? 0 : static_cast<int>(a.width);
+        }
+        constexpr int kMarks = 8;
+        int32_t token[kMarks];
+        auto tokens_from = [&](int i0) {  // on their way at once
+#pragma unroll
+            for (int u = 0; u < kMarks; ++u) token[u] = i0 + u * kThreadsL < len ? __ldg(past + i0 + u * kThreadsL) : -1;
         };
-        if (a.bias_tokens) {
-            const int32_t* at = a.bias_tokens + row * a.biases;
-            for (int i = tid; i < a.biases; i += kThreadsL) {
-                const int64_t t = at[i] - lo;
-                if (t >= 0 && t < n) first(atomicMax(table + t, static_cast<unsigned>(i + 1) << kBiasShift), static_cast<int>(t));
-            }
-            __syncthreads();
+        tokens_from(tid);
+        __syncthreads();
+        const int32_t lo32 = static_cast<int32_t>(lo);
+        int t;
+        auto within = [&](int32_t x) {  // a token of the span, at t
+            t = static_cast<int>(static_cast<unsigned>(x) - static_cast<unsigned>(lo32));
+            return x >= lo32 && t < n;
+        };
+        auto first = [&](unsigned was) {
+            if (was == 0u) listed[add_shared(&count, 1u)] = static_cast<uint16_t>(t);
+        };
+        for (int i = tid; i < a.biases; i += kThreadsL) {
+            if (i != tid) biased = __ldg(bias_at + i);
+            if (!within(biased)) continue;
+            unsigned was = table[t], seen;  // the last of the list counts, whatever the history adds meanwhile
+            do {
+                seen = was;
+                was = atomicCAS(table + t, seen, (seen & (2 * kCame - 1)) | max(seen >> kBiasShift, static_cast<unsigned>(i + 1)) << kBiasShift);
+            } while (was != seen);
+            first(was);
         }
-        if (a.history) {
-            int64_t len = a.lens[row];
-            const int64_t prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
-            if (len < 0 || len > a.width) {
-                if (tid == 0) atomicOr(a.status, kStatusBounds);
-                len = len < 0 ? 0 : a.width;
-            }
-            const int32_t* at = a.history + row * a.width;
-            for (int i0 = tid; i0 < len; i0 += 4 * kThreadsL) {
-                int32_t token[4];  // on their way at once
+        // Few of a row's tokens lie in the span: a thread marks which of its next eight do, and a warp goes
+        // through the few marks of its lanes together.
+        for (int i0 = tid; i0 < len; i0 += kMarks * kThreadsL) {
+            if (i0 != tid) tokens_from(i0);
+            unsigned marks = 0;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) token[u] = i0 + u * kThreadsL < len ? __ldg(at + i0 + u * kThreadsL) : -1;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int64_t t = token[u] - lo;
-                    if (token[u] < 0 || t < 0 || t >= n) continue;
-                    first(i0 + u * kThreadsL >= prompt ? atomicAdd(table + t, 1u) : atomicOr(table + t, kCame), static_cast<int>(t));
-                }
+            for (int u = 0; u < kMarks; ++u) marks |= within(token[u]) ? 1u << u : 0u;
+            while (marks) {
+                const int i = i0 + (__ffs(marks) - 1) * kThreadsL;
+                marks &= marks - 1;
+                within(__ldg(past + i));
+                first(i >= made_from ? add_shared(table + t, 1u) : atomicOr(table + t, kCame));
             }
+        }
+    }
+    // A listed token's logit.
+    auto adjusted = [&](int t) {
+        const unsigned word = table[t], times = word & (kCame - 1), with = word >> kBiasShift;
+        float y = to_f32(x[t]);
+        const float bias = with ? __ldg(a.bias + row * a.biases + with - 1) : 0.f;
+        const uint32_t allowed = mask ? __ldg(mask + (t >> 5)) : ~0u;  // on its way with the others
+        if (word & (2 * kCame - 1)) {  // in the history
+            if (a.repetition) y = y > 0.f ? __fdiv_rn(y, rho) : __fmul_rn(y, rho);
+            if (times) {
+                if (a.frequency) y = __fsub_rn(y, __fmul_rn(frequency, static_cast<float>(times)));
+                if (a.presence) y = __fsub_rn(y, presence);
+            }
+        }
+        if (with) y = __fadd_rn(y, bias);
+        if (heat) y = __fdiv_rn(y, temperature.t);
+        return allowed >> (t & 31) & 1u ? y : -INFINITY;
+    };
+    if (TABLE && a.in_place) {  // the listed tokens' logits are read before the stream writes them
+        __syncthreads();
+        for (unsigned i = tid; i < count; i += kThreadsL) {
+            const int t = listed[i];
+            table[t] = __float_as_uint(adjusted(t));
         }
         __syncthreads();
-        const float rho = a.repetition ? a.repetition[row] : 1.f;
-        const float presence = a.presence ? a.presence[row] : 0.f, frequency = a.frequency ? a.frequency[row] : 0.f;
-        const int have = count;
-        for (int i = tid; i < have; i += kThreadsL) {  // each token once: its word becomes its logit
-            const int t = listed[i];
-            const unsigned word = table[t], times = word & (kCame - 1), with = word >> kBiasShift;
-            float y = to_f32(x[t]);
-            if (word & (2 * kCame - 1)) {  // in the history
-                if (a.repetition) y = y > 0.f ? __fdiv_rn(y, rho) : __fmul_rn(y, rho);
-                if (times) {
-                    if (a.frequency) y = __fsub_rn(y, __fmul_rn(frequency, static_cast<float>(times)));
-                    if (a.presence) y = __fsub_rn(y, presence);
-                }
-            }
-            if (with) y = __fadd_rn(y, a.bias[row * a.biases + with - 1]);
-            if (heat) y = __fdiv_rn(y, temperature.t);
-            if (mask && !((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u)) y = -INFINITY;
-            table[t] = __float_as_uint(y);
-        }
-        __syncthreads();  // all have read their logits before they are written in place
     }
     auto shown = [&](int t) { return !mask || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u); };
     auto one = [&](int t) {
@@ -252,10 +302,10 @@ __global__ void __launch_bounds__(kThreadsL, 8) qg_logits_kernel(const LogitArgs
         for (int t = tid; t < n; t += kThreadsL) one(t);
     }
     if (TABLE) {
-        __syncthreads();  // behind the stream's writes
-        for (int i = tid; i < count; i += kThreadsL) {
+        __syncthreads();  // behind the marks and the stream's writes
+        for (unsigned i = tid; i < count; i += kThreadsL) {
             const int t = listed[i];
-            store_as(out + t, __uint_as_float(table[t]));
+            store_as(out + t, a.in_place ? __uint_as_float(table[t]) : adjusted(t));
         }
     }
 }
@@ -286,11 +336,22 @@ int launch_logits_adjust(const void* logits, int type, int64_t rows, int64_t voc
     a.temperature = temperature, a.mask = mask, a.mask_row = mask_words, a.masks = masks, a.mask_rows = mask_rows;
     a.in_place = logits == out;
     a.status = status;
-    // Spans long enough that reading the history again for each costs little,
-    // short enough that few rows keep every SM busy.
-    int64_t span = rows * vocab / (4 * static_cast<int64_t>(sms));
-    span = std::min<int64_t>(std::max<int64_t>(span, 1024), kMostSpan) / 1024 * 1024;
-    int64_t chunks = (vocab + span - 1) / span;
+    // Spans long enough that reading the history again for each costs little, short enough that few rows keep every SM
+    // busy: the least waves x (a span and what a CTA costs beside it, as much as some 2000 tokens).  Many waves
+    // count whole, for the last takes as long with few CTAs (384 x 128257: 34 spans, 10.7 waves, 95 us, 32 spans, 10.1
+    // waves, 99); few overlap, and half a wave stands for their latencies (96 x 50257: 13 spans, 1.03 waves, 11.5 us,
+    // 25 spans 14.1; 4 x 32000: spans of 1024 tokens 3.3 us, of 4096 4.0).
+    const double slots = static_cast<double>(kCtasL) * sms;
+    const int64_t fewest = (vocab + kMostSpan - 1) / kMostSpan, most = (vocab + kLeastSpan - 1) / kLeastSpan;
+    int64_t span = 0;
+    double best = INFINITY;
+    for (int64_t n = fewest; n <= most; n += std::max<int64_t>(1, fewest / 16)) {
+        const int64_t of = ((vocab + n - 1) / n + 31) / 32 * 32;
+        const double waves = static_cast<double>(rows * n) / slots;
+        const double cost = ((waves > 4 ? std::ceil(waves) : waves) + 0.5) * static_cast<double>(of + 2048);
+        if (cost < best) best = cost, span = of;
+    }
+    const int64_t chunks = (vocab + span - 1) / span;
     if (rows * chunks > INT32_MAX) return QG_EINVAL;
     a.span = static_cast<int>(span), a.chunks = static_cast<int>(chunks);
     if (type == QGKV_F32) return launch_typed<float, float>(a, rows, s);
