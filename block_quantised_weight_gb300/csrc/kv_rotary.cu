@@ -15,6 +15,11 @@
 // sines.  A CTA takes a block (the tokens of a page) of one head of K or V, whose
 // turned values wait in registers for the block's scale; or the block's rows of
 // several query heads, cosines and sines read once for them.
+//
+// Measured (GB300; bytes at the copy rate in brackets): 5 prompts of up to 4001 rows, 32 / 8
+// heads of 128, bf16, 62 us (50), fp32 104; 48 single tokens 2.7 us, launch and chain.
+// Five CTAs of 128 threads an SM (102 registers): with four the prompts took 63
+// to 69 us, six spill into the L1 (74).  Loads of 4 heads on their way: 2 took 76 us, 8 72.
 #include "kv_quant.cuh"
 #include "launch_common.cuh"
 #include "qgkv_launch.h"
@@ -113,7 +118,7 @@ __device__ __forceinline__ uint4 to_raw(const float (&x)[V]) {
 
 // ITEMS: items that a thread holds, 0 to read and turn the values twice.
 template <class T, bool INT8, int THREADS, int ITEMS>
-__global__ void __launch_bounds__(THREADS) qg_append_rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 1) qg_append_rotary_kernel(const RotaryArgs a) {
     constexpr int V = 16 / sizeof(T);
     __shared__ int found[2];
     __shared__ float red[THREADS / 32];
@@ -390,9 +395,13 @@ __global__ void __launch_bounds__(THREADS) qg_append_rotary_kernel(const RotaryA
 
 template <class T, bool INT8>
 void launch_typed(RotaryArgs a, int64_t units, cudaStream_t s) {
-    // A CTA's query heads: eight where they are many blocks, so that a block of 64
-    // tokens of 128 dims is 64 KB or more of work with one reading of the angles.
-    a.q_chunk = 8;
+    // A CTA's query heads, for which each block's angles are read once: sixteen, fewer where that leaves SMs idle.
+    // 16 / 8 / 4 / 2 heads a CTA, us: 5 prompts of up to 4001 rows, 32 heads of 128, bf16: 61.6 / 64.8 / 66.6 / 74.4;
+    // 400 single tokens, 32 heads of 64, fp32: 5.5 / 5.6 / 6.3 / 8.0; 8 chunks of up to 300 rows, 12 heads of 96, fp16:
+    // 11.1 / 8.7 / 6.7 / 8.4; 7 of up to 131 rows: 9.3 / 7.1 / 5.2 / 5.1.
+    a.q_chunk = 16;
+    const int64_t busy = sm_count(current_device());
+    while (a.q_chunk > 2 && units * ((a.q_heads + a.q_chunk - 1) / a.q_chunk) < busy) a.q_chunk /= 2;
     a.q_chunks = a.q ? (a.q_heads + a.q_chunk - 1) / a.q_chunk : 0;
     const dim3 grid(static_cast<unsigned>(units), a.q_chunks + 2 * a.c.heads);
     constexpr int held = 64 / (2 * (16 / sizeof(T)));  // items whose values take 64 registers
