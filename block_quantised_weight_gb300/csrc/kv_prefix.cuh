@@ -513,8 +513,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 int steps, parts, in;
                 walk.to(a, at, w, steps, parts, in);
                 const int last = min(end - at, parts - in) + in;  // parts of one unit are one piece
-                w.j0 = static_cast<int>(static_cast<int64_t>(steps) * in / parts);
-                w.j1 = static_cast<int>(static_cast<int64_t>(steps) * last / parts);
+                w.j0 = static_cast<int>(div64(static_cast<int64_t>(steps) * in, parts));
+                w.j1 = static_cast<int>(div64(static_cast<int64_t>(steps) * last, parts));
                 w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
                 w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
                 at += last - in;

@@ -175,6 +175,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(QP));  // [batch + 1]
     int2* seqs = reinterpret_cast<int2*>(pre + a.batch + 1);              // [batch] rows, length
     __shared__ int64_t warp_sum[4];
+    __shared__ int warp_most[4];
     __shared__ int last_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,17 +195,23 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     bool dead = false;  // a wait of this lane gave up: none follows, and no copy if it is lane 0, which issues them
 
     // ---- the line: prefix sums of the sequences' tiles (`whole`: of their blocks for all heads)
-    auto measure = [&](bool whole) {
+    auto units_of = [&](int2 q, bool whole) {  // rows, length
+        const int64_t blocks = (static_cast<int64_t>(q.x) * a.group + RU - 1) / RU;
+        return blocks * c.heads * (whole ? 1 : max(1, (q.y + kTile - 1) / kTile));
+    };
+    auto read = [&](int b) {
+        Seq s = sequence(a, b);
+        if (SHARED) shared_columns(a, b, s);
+        return make_int2(s.n, s.len);
+    };
+    auto measure = [&](bool known, bool whole) {
         int64_t base = 0;
         for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
             const int b = b0 + tid;
             int64_t x = 0;
             if (b < a.batch) {
-                Seq s = sequence(a, b);
-                if (SHARED) shared_columns(a, b, s);
-                const int64_t blocks = (static_cast<int64_t>(s.n) * a.group + RU - 1) / RU;
-                x = blocks * c.heads * (whole ? 1 : max(1, (s.len + kTile - 1) / kTile));
-                seqs[b] = make_int2(s.n, s.len);
+                if (!known) seqs[b] = read(b);
+                x = units_of(seqs[b], whole);
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -221,22 +228,33 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         if (tid == 0) pre[0] = 0;
         __syncthreads();
     };
-    measure(false);
-    Line line(pre[a.batch], grid);
-    const int cta = blockIdx.x;
     // Behind a prefix sequences are short, and beginning and joining a piece costs as
     // much as some tiles: where the longest is hardly longer than a CTA's share,
     // none is cut, and the line counts them whole.
     bool uncut = false;
     if (SHARED) {
+        int64_t sum = 0;
         int longest = 0;
-        for (int b = tid; b < a.batch; b += kThreads) longest = max(longest, seqs[b].y);
-        uncut = __syncthreads_or((longest + kTile - 1) / kTile > line.each + kUncut) == 0;
-        if (uncut) {
-            measure(true);
-            line = Line(pre[a.batch], grid);
+#pragma unroll 4
+        for (int b = tid; b < a.batch; b += kThreads) {
+            const int2 q = read(b);
+            seqs[b] = q;
+            sum += units_of(q, false);
+            longest = max(longest, q.y);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        longest = __reduce_max_sync(~0u, longest);
+        if (lane == 0) warp_sum[warp] = sum, warp_most[warp] = longest;
+        __syncthreads();
+        const Line cut(warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3], grid);
+        longest = max(max(warp_most[0], warp_most[1]), max(warp_most[2], warp_most[3]));
+        uncut = (longest + kTile - 1) / kTile <= cut.each + kUncut;
+        __syncthreads();  // the sums have been read
     }
+    measure(SHARED, uncut);
+    const Line line(pre[a.batch], grid);
+    const int cta = blockIdx.x;
     if (cta >= line.ctas) {
         if (SHARED) grid_dependency_wait();
         return;
