@@ -141,15 +141,16 @@ struct PartWalk {
     __device__ int parts_of(float longest) const {
         return u.n ? max(1, min(static_cast<int>(ceilf(static_cast<float>(u.steps) / longest)), u.steps / kLeastSteps)) : 0;
     }
-    // Sets the length of the parts: where all units have a CTA of their own, the shortest (by eighths of the mean
-    // share) with no more parts than CTAs; else a quarter of the share.
+    // Sets the length of the parts: where all units have a CTA of their own, the shortest (by whole steps, long
+    // ones by sixteenths of the mean share) with no more parts than CTAs; else a quarter of the share.
     __device__ void plan(const AttnArgs& a, int ctas) {
         const float share = steps / static_cast<float>(ctas);
         longest = fmaxf(1.f, 0.25f * share);
         if (a.ngroups > 32 || __reduce_add_sync(~0u, u.n) > ctas) return;
-        for (int i = 8; i < 32; ++i) {
-            longest = fmaxf(1.f, share * static_cast<float>(i) * 0.125f);
-            if (__reduce_add_sync(~0u, u.n * parts_of(longest)) <= ctas) return;
+        const float finer = fmaxf(1.f, floorf(share * 0.0625f));
+        for (float x = fmaxf(1.f, ceilf(share)); x < 4.f * share + 1.f; x += finer) {
+            longest = x;
+            if (__reduce_add_sync(~0u, u.n * parts_of(x)) <= ctas) return;
         }
     }
     __device__ void cut() {
