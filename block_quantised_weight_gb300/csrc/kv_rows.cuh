@@ -230,7 +230,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     };
     // Behind a prefix sequences are short, and beginning and joining a piece costs as
     // much as some tiles: where the longest is hardly longer than a CTA's share,
-    // none is cut, and the line counts them whole.
+    // none is cut, and the line counts them whole (48 sequences of up to 600 tokens
+    // behind 8200: 42 us for 46 cut, 192 of up to 300 behind 24 prefixes 52 for 62).
     bool uncut = false;
     if (SHARED) {
         int64_t sum = 0;

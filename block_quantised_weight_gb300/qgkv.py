@@ -149,17 +149,19 @@ def _rows(t, heads, dim, name):
     kind = TYPES.get(t.dtype)
     if kind is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not (rows, {heads}, {dim})")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not (rows, {heads}, {dim})")
     row, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: a head's values must be dense")
     # strides of a dimension of one element carry no meaning
-    if t.shape[1] == 1:
+    rows = shape[0]
+    if heads == 1:
         head = dim
-    if t.shape[0] == 1:
+    if rows == 1:
         row = heads * head
-    return t.data_ptr(), kind, t.shape[0], row, head
+    return t.data_ptr(), kind, rows, row, head
 
 
 class KVWorkspace:
@@ -263,7 +265,7 @@ def kv_append_rotary(cache, layer, q, k, v, rope, table, lens, starts=None, pair
     of the same rows turned alike (qgkv_append_rotary).  q [rows, q_heads, head_dim] or None, k, v [rows,
     heads, head_dim]; rope float32 [positions, turned], as rotary_table makes it; pairs "interleaved" or
     "halves".  Returns the turned queries (`out`, which may be q where q is contiguous), None without q."""
-    if _other(stream, cache, q, k, v, rope, table, lens, starts, out):
+    if stream is not None and _other(stream, cache, q, k, v, rope, table, lens, starts, out):
         with torch.cuda.stream(stream):
             return kv_append_rotary(cache, layer, q, k, v, rope, table, lens, starts, pairs, out)
     if pairs not in PAIRS:
@@ -322,7 +324,7 @@ def kv_attention(cache, layer, q, table, lens, starts=None, scale=None, out=None
     """softmax(scale * q k^T) v over each sequence's lens[b] tokens, causal at their end
     (qgkv_attention).  q [rows, q_heads, head_dim]; returns out, or (out, lse) with
     return_lse.  scale: 1 / sqrt(head_dim) where None."""
-    if _other(stream, cache, q, table, lens, starts, out, lse, workspace):
+    if stream is not None and _other(stream, cache, q, table, lens, starts, out, lse, workspace):
         with torch.cuda.stream(stream):
             return kv_attention(cache, layer, q, table, lens, starts, scale, out, lse, return_lse, workspace)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
@@ -341,7 +343,7 @@ def kv_share(cache, table, lens, groups, starts=None, rows=None, out=None, strea
     tokens that each sequence shares.  It is read and made on the device, once for all layers of a step.
     rows: the number of query rows; where None, and with starts, rows outside the queries are first found by
     the attention."""
-    if _other(stream, cache, table, lens, groups, starts, out):
+    if stream is not None and _other(stream, cache, table, lens, groups, starts, out):
         with torch.cuda.stream(stream):
             return kv_share(cache, table, lens, groups, starts, rows, out)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
@@ -363,7 +365,7 @@ def kv_attention_shared(cache, layer, q, table, lens, plan, starts=None, scale=N
                         return_lse=False, workspace=None, stream=None):
     """kv_attention of a batch whose groups share pages, which are read once for all rows of a group
     (qgkv_attention_shared).  plan: what kv_share gave for the same table, lens and starts."""
-    if _other(stream, cache, q, table, lens, plan, starts, out, lse, workspace):
+    if stream is not None and _other(stream, cache, q, table, lens, plan, starts, out, lse, workspace):
         with torch.cuda.stream(stream):
             return kv_attention_shared(cache, layer, q, table, lens, plan, starts, scale, out, lse, return_lse, workspace)
     batch, width, tp, lp, sp = _batch(table, lens, starts)
@@ -506,8 +508,8 @@ def adjust_logits(logits, history=None, lens=None, prompt_lens=None, repetition=
     without one -1; mask int32 [masks, words], bit t % 32 of word t // 32 is 1 where token t is allowed, one
     a row or named by mask_rows int32 [rows] (-1: none).  Returns `out` (of the logits' type or float32;
     logits itself works in place), a new tensor of the logits' type where None."""
-    if _other(stream, logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias, temperature,
-              mask, mask_rows, out):
+    if stream is not None and _other(stream, logits, history, lens, prompt_lens, repetition, presence, frequency,
+                                     bias_tokens, bias, temperature, mask, mask_rows, out):
         with torch.cuda.stream(stream):
             return adjust_logits(logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias,
                                  temperature, mask, mask_rows, out)
@@ -518,21 +520,21 @@ def adjust_logits(logits, history=None, lens=None, prompt_lens=None, repetition=
     if (out_rows, out_vocab) != (rows, vocab):
         raise ValueError(f"out has shape {tuple(out.shape)}, not {(rows, vocab)}")
 
-    def each(t, name, dtype=torch.float32):
-        return None if t is None else _need(t, dtype, name, (rows,))
-
-    i32 = torch.int32
+    i32, f32, each = torch.int32, torch.float32, (rows,)
     hp = width = tp = bp = mp = None
-    past = [each(lens, "lens", i32), each(prompt_lens, "prompt_lens", i32), each(repetition, "repetition"),
-            each(presence, "presence"), each(frequency, "frequency")]
+    past = (None if lens is None else _need(lens, i32, "lens", each),
+            None if prompt_lens is None else _need(prompt_lens, i32, "prompt_lens", each),
+            None if repetition is None else _need(repetition, f32, "repetition", each),
+            None if presence is None else _need(presence, f32, "presence", each),
+            None if frequency is None else _need(frequency, f32, "frequency", each))
     if history is not None:
         hp, width = _need(history, i32, "history", (rows, None)), history.shape[1]
         if width == 0:  # nothing has come yet
-            hp, past = None, [None] * 5
+            hp, past = None, (None,) * 5
     biases = 0
     if bias_tokens is not None and bias is not None:
         tp, biases = _need(bias_tokens, i32, "bias_tokens", (rows, None)), bias_tokens.shape[1]
-        bp = _need(bias, torch.float32, "bias", (rows, biases))
+        bp = _need(bias, f32, "bias", (rows, biases))
         if biases == 0:
             tp = bp = None
     elif bias_tokens is not None or bias is not None:
@@ -541,7 +543,8 @@ def adjust_logits(logits, history=None, lens=None, prompt_lens=None, repetition=
     if mask is not None:
         mp, (masks, words) = _need(mask, i32, "mask", (None, None)), mask.shape
     _call("qglogits_adjust", logits.data_ptr(), kind, rows, vocab, row, out.data_ptr(), out_kind, out_row, hp, width or 0,
-          *past, tp, bp, biases, each(temperature, "temperature"), mp, words, masks, each(mask_rows, "mask_rows", i32),
+          *past, tp, bp, biases, None if temperature is None else _need(temperature, f32, "temperature", each), mp, words,
+          masks, None if mask_rows is None else _need(mask_rows, i32, "mask_rows", each),
           _stream(logits, out, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias,
                   temperature, mask, mask_rows))
     return out

@@ -188,3 +188,67 @@ def test_beam_decode_step_over_shared_pages(kv):  # noqa: F811
         together = model.step(tokens, table, lens, groups=i32([0, 4]))
         assert ((apart - together).abs() <= 0.05).all()
         lens += 1
+
+
+def test_pages_behind_32_bits(kv):  # noqa: F811
+    """The same appends and attention on the first pages of a small cache and on the last of one of more than 2^32 bytes."""
+    heads, page, dim, pages = 8, 256, 256, 8300
+    assert pages * heads * page * dim > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rope, n = kv.rotary_table(1024, 256), [600, 3, 5]
+    q, k, v = (torch.randn((sum(n), h, dim), device="cuda", generator=g).bfloat16() for h in (32, heads, heads))
+    rows = torch.randn((2, 32, dim), device="cuda", generator=g).bfloat16()
+    got = []
+    for held, first in ((8, 0), (pages, pages - 8)):
+        cache = kv.KVCache.allocate(1, held, heads, page, dim)
+        table = torch.full((2, least_width(2, heads, dim, page)), -1, dtype=torch.int32, device="cuda")
+        table[:, :2] = i32([first + 7, first + 1])
+        table[:, 2] = i32([first + 4, first + 2])
+        turn = kv.kv_append_rotary(cache, 0, q[:600], k[:600], v[:600], rope, table[:1], i32([0]), starts=i32([0, 600]))
+        kv.kv_copy_pages(cache, i32([first + 4]), i32([first + 2]))
+        kv.kv_append_rotary(cache, 0, q[600:], k[600:], v[600:], rope, table, i32([600, 600]), starts=i32([0, 3, 8]))
+        lens = i32([603, 605])
+        plan = kv.kv_share(cache, table, lens, i32([0, 2]))
+        assert plan[2] == 512
+        out = kv.kv_attention_shared(cache, 0, rows, table, lens, plan, return_lse=True)
+        got.append((turn, *out, cache.k[0, first:first + 8].clone(), cache.v[0, first:first + 8].clone(),
+                    cache.k_scale[0, first:first + 8].clone(), cache.v_scale[0, first:first + 8].clone()))
+        close(*out, small(attention_ref(cache, 0, rows, table, [603, 605], [0, 1, 2], dim ** -0.5), "bf16"), 605 + 512,
+              torch.bfloat16, one_part=True)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_logits_behind_32_bits(kv):  # noqa: F811
+    """The last rows of more than 2^31 logits (and 2^32 bytes) against the same rows by themselves."""
+    rows, vocab, some = 16800, 128001, 5
+    assert rows * vocab > 1 << 31
+    x = torch.zeros((rows, vocab), dtype=torch.float16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x[-some:] = torch.randn((some, vocab), device="cuda", generator=g).half()
+    a = dict(history=torch.randint(0, vocab, (rows, 40), device="cuda", generator=g).int(), lens=i32([40] * rows),
+             frequency=torch.rand(rows, device="cuda", generator=g), temperature=0.5 + torch.rand(rows, device="cuda", generator=g))
+    got = kv.adjust_logits(x, **a)
+    want = kv.adjust_logits(x[-some:].contiguous(), **{n: t[-some:].contiguous() for n, t in a.items()})
+    assert torch.equal(got[-some:], want)
+    assert torch.equal(kv.adjust_logits(x, **a, out=x)[-some:], want)
+
+
+def test_shared_attention_on_two_streams_at_once(kv):  # noqa: F811
+    """Calls that may overlap, each with a workspace of its own, have the bits of calls by themselves."""
+    from test_kv_shared_gpu import shared_table
+    cases, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for i, dtype in enumerate(("f32", "bf16")):
+        cache, table, lens, borders = shared_table(kv, [(2000, [40 + 9 * j for j in range(12)])], 2, 128, 16, "e4m3", "hnd", seed=i)
+        q = torch.randn((12, 8, 128), device="cuda").to(DT[dtype])
+        w, ln = kv.KVWorkspace("cuda"), i32(lens)
+        plan = kv.kv_share(cache, table, ln, i32(borders))
+        cases.append((cache, q, table, ln, plan, w, kv.kv_attention_shared(cache, 0, q, table, ln, plan, workspace=w)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (cache, q, table, ln, plan, w, _) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(kv.kv_attention_shared(cache, 0, q, table, ln, plan, workspace=w))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, cases[i][-1]) for x in got[i])
