@@ -18,11 +18,13 @@
 // wait for both.  In place their logits are read, and kept, before the stream writes them.
 //
 // Measured (GB300, bytes read and written at the copy rate in brackets): 384 x
-// 128257 fp32, histories of up to 2500, 96 us (59), 68 of them for the stream alone, 80 without
-// the histories; 96 x 50257 in bf16 11.5 us (2.9), 4 x 32000 3.3 us: launch and the chain
-// lengths -> history -> marks -> listed logits.  Steps with a barrier behind each and
-// loads in their place took 113 us, without the prefetch of the span to L2 119; spans
-// of 2048 or 512 threads 150, the stream's loads in registers ahead of the histories 200, 6 CTAs an SM 108.
+// 128257 fp32, histories of up to 2500, 89 us (59); 96 x 50257 in bf16 10.9 us (2.9), 4 x
+// 32000 3.2 us: launch and the chain lengths -> history -> marks -> listed logits.  The largest
+// is bound by issue: 80 % of its slots, half of the instructions the stream's (a division is ten
+// of them, in pairs five), a quarter the history's, which every CTA of a row reads.
+// Slower, of the time then: a barrier behind each step and loads in their place 18 %, no prefetch of the span to L2
+// 19 %, two vectors of a thread on their way at once 5 %, spans of 2048 or 512 threads 35 %, 6 CTAs an SM 8 %, the
+// stream's loads in registers ahead of the histories twice the time.
 //
 #include <algorithm>
 #include <cmath>
@@ -91,15 +93,24 @@ struct Divisor {
     }
     template <int N>
     __device__ __forceinline__ void divide(float (&x)[N]) const {
+        static_assert(N % 2 == 0, "pairs");
         float most = 0.f, least = INFINITY;  // NaN is passed over: it stays NaN either way
 #pragma unroll
-        for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(x[i])), least = fminf(least, fabsf(x[i]));
+        for (int i = 0; i < N; i += 2) {
+            asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(x[i]), "f"(x[i + 1]));
+            asm("min.abs.f32 %0, %0, %1, %2;" : "+f"(least) : "f"(x[i]), "f"(x[i + 1]));
+        }
         if (near_one && least >= 0x1p-60f && most <= 0x1p60f) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float q = __fmul_rn(x[i], r);
-                q = __fmaf_rn(__fmaf_rn(-q, t, x[i]), r, q);
-                x[i] = __fmaf_rn(__fmaf_rn(-q, t, x[i]), r, q);
+            for (int i = 0; i < N; i += 2) {
+                f2 q = fmul2(f2{x[i], x[i + 1]}, f2{r, r});
+#pragma unroll
+                for (int again = 0; again < 2; ++again) {
+                    f2 rest = {x[i], x[i + 1]};
+                    ffma2(rest, q, f2{-t, -t});
+                    ffma2(q, rest, f2{r, r});
+                }
+                x[i] = q.x, x[i + 1] = q.y;
             }
         } else {
 #pragma unroll 1
@@ -258,9 +269,9 @@ __global__ void __launch_bounds__(kThreadsL, kCtasL) qg_logits_kernel(const Logi
     auto one = [&](int t) {
         const bool hidden = !shown(t);
         if (!all && !hidden) return;
-        float y[1] = {hidden ? 0.f : to_f32(x[t])};
-        if (heat && !hidden) temperature.divide(y);
-        store_as(out + t, hidden ? -INFINITY : y[0]);
+        float y = hidden ? -INFINITY : to_f32(x[t]);
+        if (heat && !hidden) y = __fdiv_rn(y, temperature.t);
+        store_as(out + t, y);
     };
     // Whole 16 bytes where input and output meet their borders at the same tokens (a vocabulary of odd size
     // shifts both alike), the few before and behind them one by one.
@@ -269,32 +280,17 @@ __global__ void __launch_bounds__(kThreadsL, kCtasL) qg_logits_kernel(const Logi
     if (all && n >= 2 * V && (reinterpret_cast<uintptr_t>(out + head) & 15) == 0) {
         const int vectors = (n - head) / V, rest = head + vectors * V;
         const int last_word = (n - 1) >> 5;
-        constexpr int U = 2;  // vectors on their way at once
-        for (int v0 = tid; v0 < vectors; v0 += U * kThreadsL) {
-            uint4 u[U];
-            uint32_t bits[U];
+        for (int v = tid; v < vectors; v += kThreadsL) {  // their latency is the other warps' time: 64 an SM
+            const int t = head + v * V;
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(x + t));
+            const uint32_t bits = mask ? __funnelshift_r(__ldg(mask + (t >> 5)), __ldg(mask + min((t >> 5) + 1, last_word)), t & 31) : ~0u;
+            float y[V];
+            values_of<T>(u, y);
+            if (heat) temperature.divide(y);
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int v = v0 + i * kThreadsL, t = head + v * V;
-                if (v < vectors) {
-                    u[i] = __ldcs(reinterpret_cast<const uint4*>(x + t));
-                    if (mask) bits[i] = __funnelshift_r(__ldg(mask + (t >> 5)), __ldg(mask + min((t >> 5) + 1, last_word)), t & 31);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int v = v0 + i * kThreadsL, t = head + v * V;
-                if (v >= vectors) break;
-                float y[V];
-                values_of<T>(u[i], y);
-                if (heat) temperature.divide(y);
-                if (mask) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        if (!(bits[i] >> k & 1u)) y[k] = -INFINITY;
-                }
-                store_all(out + t, y);
-            }
+            for (int k = 0; k < V; ++k)
+                if (!(bits >> k & 1u)) y[k] = -INFINITY;
+            store_all(out + t, y);
         }
         if (tid < head) one(tid);
         if (rest + tid < n) one(rest + tid);
@@ -338,9 +334,9 @@ int launch_logits_adjust(const void* logits, int type, int64_t rows, int64_t voc
     a.status = status;
     // Spans long enough that reading the history again for each costs little, short enough that few rows keep every SM
     // busy: the least waves x (a span and what a CTA costs beside it, as much as some 2000 tokens).  Many waves
-    // count whole, for the last takes as long with few CTAs (384 x 128257: 34 spans, 10.7 waves, 95 us, 32 spans, 10.1
-    // waves, 99); few overlap, and half a wave stands for their latencies (96 x 50257: 13 spans, 1.03 waves, 11.5 us,
-    // 25 spans 14.1; 4 x 32000: spans of 1024 tokens 3.3 us, of 4096 4.0).
+    // count whole, for the last takes as long with few CTAs (384 x 128257: 34 spans, 10.7 waves, 90 us, 32 spans, 10.1
+    // waves, 92); few overlap, and half a wave stands for their latencies (96 x 50257: 13 spans, 1.03 waves, 10.9 us,
+    // 25 spans 13.3; 4 x 32000: spans of 1024 tokens 3.1 us, of 4096 4.0).
     const double slots = static_cast<double>(kCtasL) * sms;
     const int64_t fewest = (vocab + kMostSpan - 1) / kMostSpan, most = (vocab + kLeastSpan - 1) / kLeastSpan;
     int64_t span = 0;
