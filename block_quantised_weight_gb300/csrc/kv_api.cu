@@ -160,9 +160,14 @@ int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
 //   4 of 1080, 8 heads of 128 (6.7 MB): 15.0 / 10.8;  8 groups of 4 of 1060, 4 heads of 64 (17 MB): 15.7 / 14.2
 //   4 of 4160, 8 heads of 128 (26 MB): 16.3 / 18.2;  48 of 1320 (130 MB): 26 / 27;  48 of 8800 (850 MB): 42 / 97
 // Widths are all that the host knows: behind a table much wider than its
-// sequences a small plan is followed all the same.
+// sequences a small plan is followed all the same.  Nor does the prefix kernel read as
+// fast as the row kernel, for a step takes it as long for few rows as for 64: with 16 groups
+// behind up to 6000 tokens, bf16, of 2 / 3 / 4 / 6 sequences, shared 57 / 57 / 65 / 70, each for itself 35 / 47 / 58 /
+// 81 (8 heads of 64), 67 / 69 / 78 / 85 and 47 / 63 / 77 / 109 (of 128), 77 / 78 / 81 / 94 and 51 / 66 / 84 / 116 (4 of 256).
 constexpr double kLeastSaved = 16 << 20;
-bool worth_sharing(const qg::AttnArgs& a) {
+constexpr int kLeastMembers = 4;  // sequences of a call to each group
+bool worth_sharing(const qg::AttnArgs& a, int ngroups) {
+    if (a.batch < static_cast<int64_t>(kLeastMembers) * ngroups) return false;
     const double most = 2.0 * (a.batch - 1) * a.width * (int64_t(1) << a.c.log2p) * a.c.heads * a.c.dim;
     return most >= kLeastSaved && !many_rows(a);
 }
@@ -285,7 +290,7 @@ int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q,
                                      {plan, (4 * int64_t(ngroups) + batch) * 4}, a, &done);
     if (rc != QG_OK || done) return rc;
     const bool int8 = cache->format == QGKV_INT8;
-    if (!worth_sharing(a) || qg::own_bytes(rows, q_heads, cache->head_dim) > qg::kWsSplits - qg::kWsOwn)
+    if (!worth_sharing(a, ngroups) || qg::own_bytes(rows, q_heads, cache->head_dim) > qg::kWsSplits - qg::kWsOwn)
         return launch_attention(a, int8, stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.groups = reinterpret_cast<const int4*>(plan);

@@ -22,7 +22,7 @@ struct AttnArgs {
     int4* splits;
     unsigned* count;
     unsigned* status;
-    // A shared prefix: the plan's groups and tokens, and the prefix's results (kv_prefix.cu)
+    // A shared prefix: the plan's groups and tokens, and the prefix's results (kv_prefix.cuh)
     const int4* groups;
     const int32_t* skip;
     int ngroups;

@@ -175,8 +175,8 @@ QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int6
  * precision for scales of V of 2^-80 to 2^90 (qgkv_append writes none outside for
  * values of 2^-70 to 2^97).  Where sharing gains nothing each sequence reads all its
  * tokens itself and the plan is not read: the table's width times its sequences come
- * to less than 16 MB of pages, many rows a sequence, or more results to join than the
- * workspace holds.  The choice depends on the call's sizes alone. */
+ * to less than 16 MB of pages, fewer than four sequences of the batch to a group,
+ * many rows a sequence, or more results to join than the workspace holds.  The choice depends on the call's sizes alone. */
 QG_API int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                                  int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride,
                                  const int32_t* table, int64_t table_width, const int32_t* lens,

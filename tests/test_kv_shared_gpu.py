@@ -29,11 +29,16 @@ def least_width(batch, heads, dim, page):
     return -(-LEAST // (2 * (batch - 1) * heads * dim * page))
 
 
+MEMBERS = 4        # sequences that a batch has to have for each group
+
+
 def shared_table(kv, shape, heads, dim, page, fmt, order, seed=0, layers=2, wide=True):  # noqa: F811
     """shape: for each group (tokens of the prefix, tokens of each sequence behind it).  Whole pages of a prefix are the
-    first sequence's.  wide: the table has columns enough for its pages to be shared, however few are held.  Returns
+    first sequence's.  wide: the table has columns enough for its pages to be shared, however few are held, and sequences
+    of five tokens and no group behind the others, as many as the groups are too small by.  Returns
     cache, table, lens (list), borders of the groups."""
     lens = [p + t for p, tails in shape for t in tails]
+    lens += [5] * max(0, MEMBERS * len(shape) - len(lens)) if wide else []
     width = max(*(-(-n // page) for n in lens), least_width(len(lens), heads, dim, page)) if wide else None
     cache, table, _ = make(kv, lens, heads, dim, page, fmt, order, seed=seed, layers=layers, width=width)
     ids, at, borders = table.cpu().numpy(), 0, [0]
@@ -68,7 +73,7 @@ def plan_ref(ids, lens, starts, borders, page, pages):
 
 def check(kv, ws, shape, group, heads, dim, page, fmt, order, dtype, rows=None, seed=0, scale=None, out=False):  # noqa: F811
     cache, table, lens, borders = shared_table(kv, shape, heads, dim, page, fmt, order, seed)
-    rows = [1] * len(lens) if rows is None else rows
+    rows = [1] * len(lens) if rows is None else rows + [1] * (len(lens) - len(rows))
     st = starts_of(rows)
     starts = None if all(r == 1 for r in rows) else i32(st)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
@@ -141,12 +146,13 @@ def test_shared_tails_of_nothing(kv, ws):  # noqa: F811
 def test_sequences_of_no_group(kv, ws):  # noqa: F811
     """Borders that leave sequences at both ends out."""
     cache, table, lens, _ = shared_table(kv, [(0, [40]), (80, [3, 9, 1]), (96, [5, 5])], 2, 64, 16, "e4m3", "hnd")
-    q = torch.randn((6, 8, 64), device="cuda")
-    for borders in ([1, 4], [1, 3], [0, 0, 1, 1, 4, 4], [6, 6]):
+    n = len(lens)
+    q = torch.randn((n, 8, 64), device="cuda")
+    for borders in ([1, 4], [1, 3], [0, 0, 1, 4], [0, 0, 1, 1, 4, 4], [6, 6]):
         plan = kv.kv_share(cache, table, i32(lens), i32(borders))
-        assert plan.tolist() == plan_ref(table.tolist(), lens, list(range(7)), borders, 16, cache.pages)
+        assert plan.tolist() == plan_ref(table.tolist(), lens, list(range(n + 1)), borders, 16, cache.pages)
         out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
-        close(out, lse, attention_ref(cache, 0, q, table, lens, list(range(7)), 1 / 8), max(lens) + 512, torch.float32)
+        close(out, lse, attention_ref(cache, 0, q, table, lens, list(range(n + 1)), 1 / 8), max(lens) + 512, torch.float32)
 
 
 def test_share_of_bad_inputs(kv, ws):  # noqa: F811
@@ -172,10 +178,10 @@ def test_share_of_bad_inputs(kv, ws):  # noqa: F811
 def test_shared_bad_plans_are_reported(kv, ws):  # noqa: F811
     """Entries that do not fit the call reach nothing outside it; the groups that fit are right."""
     cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
-    q = torch.randn((5, 8, 64), device="cuda")
+    q = torch.randn((8, 8, 64), device="cuda")
     good = kv.kv_share(cache, table, i32(lens), i32(borders))
-    ref = attention_ref(cache, 0, q, table, lens, list(range(6)), 1 / 8)
-    for at, value in ((0, -1), (0, 4), (1, 9), (1, -2), (2, -16), (2, 1 << 30), (2, 7), (3, 5), (3, -1), (8, -16), (9, 1 << 20), (10, 7)):
+    ref = attention_ref(cache, 0, q, table, lens, list(range(9)), 1 / 8)
+    for at, value in ((0, -1), (0, 6), (1, 9), (1, -2), (2, -16), (2, 1 << 30), (2, 7), (3, 8), (3, -1), (8, -16), (9, 1 << 20), (10, 7)):
         plan = good.clone()
         plan[at] = value
         out = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
@@ -186,7 +192,7 @@ def test_shared_bad_plans_are_reported(kv, ws):  # noqa: F811
 def test_shared_bad_pages_are_reported_and_masked(kv, ws):  # noqa: F811
     """A plan made before its pages were lost: they count as masked in all rows."""
     cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1])], 2, 64, 16, "e4m3", "hnd")
-    q = torch.randn((3, 8, 64), device="cuda")
+    q = torch.randn((4, 8, 64), device="cuda")
     plan = kv.kv_share(cache, table, i32(lens), i32(borders))
     for bad in (-1, cache.pages):
         ids = table.clone()
@@ -229,7 +235,7 @@ def test_shared_masked_tokens_do_not_reach(kv, ws, dtype, dim):  # noqa: F811
 def test_shared_nan_codes_that_rows_see(kv, ws, dtype, where):  # noqa: F811
     """A NaN code of V in the prefix reaches its dim of every row of its head; behind it, of the row that holds it."""
     cache, table, lens, borders = shared_table(kv, [(320, [30, 40])], 2, 64, 16, "e4m3", "hnd")
-    q = torch.randn((2, 8, 64), device="cuda").to(DT[dtype])
+    q = torch.randn((4, 8, 64), device="cuda").to(DT[dtype])
     plan = kv.kv_share(cache, table, i32(lens), i32(borders))
     want = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, workspace=ws)
     cache.v[0, table[1, where // 16], 1, where % 16, 37] = 0x7F
@@ -262,7 +268,7 @@ def test_shared_scores_of_any_size(kv, ws, unit, sign, dim, fmt, dtype, members,
     cache.k[0, :, 0, :, 1] = torch.tensor([[by_value[int(x)] for x in row] for row in what], dtype=torch.uint8, device="cuda")
     cache.v.copy_(torch.randint(0, 100, cache.v.shape, device="cuda", generator=g, dtype=torch.uint8))
     cache.v_scale.copy_(torch.exp2(torch.randint(-6, 7, cache.v_scale.shape, device="cuda", generator=g).float()))
-    q = torch.zeros((members, 2, dim), device="cuda")
+    q = torch.zeros((len(lens), 2, dim), device="cuda")
     q[:, :, 1] = sign
     q = q.to(DT[dtype])
     plan = kv.kv_share(cache, table, i32(lens), i32(borders))
@@ -288,10 +294,10 @@ def test_shared_scales_of_all_sizes(kv, ws, dtype, dim, members):  # noqa: F811
     cache.v_scale[0, ::7] = 0.0
     cache.k_scale[0, ::11] = 0.0
     cache.v_scale[0, table[0, 3]] = 0.0
-    q = torch.randn((members, 8, dim), device="cuda", generator=g).to(DT[dtype])
+    q = torch.randn((len(lens), 8, dim), device="cuda", generator=g).to(DT[dtype])
     plan = kv.kv_share(cache, table, i32(lens), i32(borders))
     out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
-    ref = attention_ref(cache, 0, q, table, lens, list(range(members + 1)), 1 / math.sqrt(dim))
+    ref = attention_ref(cache, 0, q, table, lens, list(range(len(lens) + 1)), 1 / math.sqrt(dim))
     close(out, lse, small((*ref[:4], ref[4] * 2.0 ** 4), dtype), max(lens) + 512, DT[dtype], one_part=dtype == "bf16")
 
 
@@ -303,10 +309,10 @@ def test_shared_prefix_below_and_above_the_rest(kv, ws):  # noqa: F811
         cache.k.fill_(code(1 if up else -2, "e4m3"))
         cache.k[:, table[0, :40].long()] = code(-2 if up else 1, "e4m3")
         cache.k_scale.fill_(1.0)
-        q = torch.full((3, 2, 64), 100.0, device="cuda")
+        q = torch.full((4, 2, 64), 100.0, device="cuda")
         plan = kv.kv_share(cache, table, i32(lens), i32(borders))
         out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, scale=math.log(2) / 64, return_lse=True, workspace=ws)
-        close(out, lse, attention_ref(cache, 0, q, table, lens, [0, 1, 2, 3], math.log(2) / 64), 1200, torch.float32)
+        close(out, lse, attention_ref(cache, 0, q, table, lens, [0, 1, 2, 3, 4], math.log(2) / 64), 1200, torch.float32)
 
 
 def test_shared_non_finite_queries(kv, ws):  # noqa: F811
@@ -337,12 +343,12 @@ def test_shared_strided_queries_and_outputs(kv, ws, dtype):  # noqa: F811
 
 def test_shared_rows_behind_the_last_are_left(kv, ws):  # noqa: F811
     cache, table, lens, borders = shared_table(kv, [(500, [30, 30])], 2, 64, 16, "e4m3", "hnd")
-    q = torch.randn((9, 8, 64), device="cuda")
-    starts = i32([0, 2, 5])
+    q = torch.randn((11, 8, 64), device="cuda")
+    starts = i32([0, 2, 5, 6, 7])
     plan = kv.kv_share(cache, table, i32(lens), i32(borders), starts=starts)
-    out = torch.full((9, 8, 64), 3.0, device="cuda")
+    out = torch.full((11, 8, 64), 3.0, device="cuda")
     kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, starts=starts, out=out, workspace=ws)
-    assert (out[5:] == 3.0).all() and not (out[:5] == 3.0).any()
+    assert (out[7:] == 3.0).all() and not (out[:7] == 3.0).any()
 
 
 def test_shared_repeats_bit_for_bit_and_alternates(kv, ws):  # noqa: F811
@@ -363,7 +369,7 @@ def test_shared_in_a_graph_and_on_a_stream(kv):  # noqa: F811
     """A captured plan and attention, replayed with other lengths, tables and queries, against direct calls."""
     side, own = torch.cuda.Stream(), kv.KVWorkspace("cuda")
     cache, table, lens, borders = shared_table(kv, [(600, [70, 60, 80]), (320, [50, 50])], 2, 64, 16, "e4m3", "hnd")
-    q, ln, gr = torch.randn((5, 8, 64), device="cuda"), i32(lens), i32(borders)
+    q, ln, gr = torch.randn((len(lens), 8, 64), device="cuda"), i32(lens), i32(borders)
 
     def step():
         plan = kv.kv_share(cache, table, ln, gr)
@@ -379,7 +385,7 @@ def test_shared_in_a_graph_and_on_a_stream(kv):  # noqa: F811
     for i, cut in enumerate((0, 37, 4)):
         table.copy_(first)
         table[1, cut:] = table[1, cut:].roll(1)  # less in common
-        ln.copy_(i32([n - 9 * i for n in lens]))
+        ln.copy_(i32([n - 9 * i if n > 5 else n for n in lens]))
         q.normal_()
         graph.replay()
         want_plan = kv.kv_share(cache, table, ln, gr)
@@ -407,9 +413,9 @@ def test_shared_results_beyond_the_workspace(kv, ws):  # noqa: F811
 def test_shared_from_a_width_on(kv, ws):  # noqa: F811
     """On both sides of the least width: below it kv_attention's bits, whatever the plan; from it on the plan is read."""
     cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
-    q, least = torch.randn((5, 8, 64), device="cuda"), least_width(5, 2, 64, 16)
+    q, least = torch.randn((8, 8, 64), device="cuda"), least_width(8, 2, 64, 16)
     assert table.shape[1] == least
-    ref = attention_ref(cache, 0, q, table, lens, list(range(6)), 1 / 8)
+    ref = attention_ref(cache, 0, q, table, lens, list(range(9)), 1 / 8)
     for width in (least - 1, least):
         ids = table[:, :width].contiguous()
         plan = kv.kv_share(cache, ids, i32(lens), i32(borders))
@@ -421,6 +427,21 @@ def test_shared_from_a_width_on(kv, ws):  # noqa: F811
         plan[2] = 7
         kv.kv_attention_shared(cache, 0, q, ids, i32(lens), plan, workspace=ws)
         assert qgemv.qg_device_status() == (qgemv.QG_OK if width < least else qgemv.QG_EBOUNDS)
+
+
+@pytest.mark.parametrize("members, shared", [(3, False), (4, True)])
+def test_shared_from_four_sequences_a_group_on(kv, ws, members, shared):  # noqa: F811
+    lens = [200 + i for i in range(3 * members)]
+    cache, table, _ = make(kv, lens, 2, 64, 16, "e4m3", "hnd", width=least_width(len(lens), 2, 64, 16))
+    for i in range(0, len(lens), members):
+        table[i:i + members, :10] = table[i, :10].clone()
+    q = torch.randn((len(lens), 8, 64), device="cuda")
+    plan = kv.kv_share(cache, table, i32(lens), i32([0, members, 2 * members, 3 * members]))
+    assert plan[2:12:4].tolist() == [160] * 3
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    plain = kv.kv_attention(cache, 0, q, table, i32(lens), return_lse=True, workspace=ws)
+    assert torch.equal(got[1], plain[1]) != shared
+    close(*got, attention_ref(cache, 0, q, table, lens, list(range(len(lens) + 1)), 1 / 8), max(lens) + 512, torch.float32)
 
 
 @pytest.mark.parametrize("rows, shared", [(31, True), (32, False)])
@@ -438,6 +459,6 @@ def test_shared_up_to_many_rows(kv, ws, rows, shared):  # noqa: F811
 
 
 def test_shared_largest_batch(kv, ws):  # noqa: F811
-    """4096 sequences in 1365 groups and one left over."""
-    shape = [(40, [1 + i % 7, 2, 3]) for i in range(1365)] + [(0, [5])]
+    """4096 sequences in 1024 groups."""
+    shape = [(40, [1 + i % 7, 2, 3, 6]) for i in range(1023)] + [(0, [5, 4, 5, 1])]
     check(kv, ws, shape, 2, 1, 64, 16, "e4m3", "hnd", "f32")

@@ -197,23 +197,23 @@ def test_pages_behind_32_bits(kv):  # noqa: F811
     g = torch.Generator(device="cuda").manual_seed(5)
     rope, n = kv.rotary_table(1024, 256), [600, 3, 5]
     q, k, v = (torch.randn((sum(n), h, dim), device="cuda", generator=g).bfloat16() for h in (32, heads, heads))
-    rows = torch.randn((2, 32, dim), device="cuda", generator=g).bfloat16()
+    rows = torch.randn((4, 32, dim), device="cuda", generator=g).bfloat16()
     got = []
     for held, first in ((8, 0), (pages, pages - 8)):
         cache = kv.KVCache.allocate(1, held, heads, page, dim)
-        table = torch.full((2, least_width(2, heads, dim, page)), -1, dtype=torch.int32, device="cuda")
-        table[:, :2] = i32([first + 7, first + 1])
-        table[:, 2] = i32([first + 4, first + 2])
+        table = torch.full((4, least_width(4, heads, dim, page)), -1, dtype=torch.int32, device="cuda")
+        table[:2, :2] = i32([first + 7, first + 1])
+        table[:2, 2] = i32([first + 4, first + 2])  # two sequences of no group see nothing
         turn = kv.kv_append_rotary(cache, 0, q[:600], k[:600], v[:600], rope, table[:1], i32([0]), starts=i32([0, 600]))
         kv.kv_copy_pages(cache, i32([first + 4]), i32([first + 2]))
-        kv.kv_append_rotary(cache, 0, q[600:], k[600:], v[600:], rope, table, i32([600, 600]), starts=i32([0, 3, 8]))
-        lens = i32([603, 605])
+        kv.kv_append_rotary(cache, 0, q[600:], k[600:], v[600:], rope, table[:2], i32([600, 600]), starts=i32([0, 3, 8]))
+        lens = i32([603, 605, 0, 0])
         plan = kv.kv_share(cache, table, lens, i32([0, 2]))
         assert plan[2] == 512
         out = kv.kv_attention_shared(cache, 0, rows, table, lens, plan, return_lse=True)
         got.append((turn, *out, cache.k[0, first:first + 8].clone(), cache.v[0, first:first + 8].clone(),
                     cache.k_scale[0, first:first + 8].clone(), cache.v_scale[0, first:first + 8].clone()))
-        close(*out, small(attention_ref(cache, 0, rows, table, [603, 605], [0, 1, 2], dim ** -0.5), "bf16"), 605 + 512,
+        close(*out, small(attention_ref(cache, 0, rows, table, [603, 605, 0, 0], [0, 1, 2, 3, 4], dim ** -0.5), "bf16"), 605 + 512,
               torch.bfloat16, one_part=True)
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
