@@ -68,16 +68,19 @@ __device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int b) {
     if (!good) atomicOr(a.status, kStatusBounds);
     return good && g.y > 0 && g.z > 0 ? SharedGroup{g.x, g.y, g.z, g.w} : SharedGroup{0, 0, 0, 0};
 }
-// What a sequence reads behind the tokens that it shares: less of its length, later columns of its table.
+// Whole columns of its table that a sequence of n rows and len tokens (cut to the table) shares by a plan's entry
+// `skip`, which its first row sees; -1 where the entry does not fit it.
+__host__ __device__ constexpr int columns_shared(int skip, int n, int len, int log2p) {
+    return skip == 0 || n == 0 ? 0 : skip < 0 || skip > len - n + 1 || (skip & ((1 << log2p) - 1)) ? -1 : skip >> log2p;
+}
+// What sequence b reads behind the tokens that it shares: less of its length, the columns of its table behind those
+// returned.  An entry that does not fit is as none (kStatusBounds).
 __device__ __forceinline__ int shared_columns(const AttnArgs& a, int b, Seq& s) {
-    const int skip = a.skip[b];
-    if (skip == 0 || s.n == 0) return 0;
-    if (skip < 0 || skip > s.len - s.n + 1 || (skip & ((1 << a.c.log2p) - 1))) {
-        atomicOr(a.status, kStatusBounds);
-        return 0;
-    }
-    s.len -= skip;
-    return skip >> a.c.log2p;
+    const int columns = columns_shared(a.skip[b], s.n, s.len, a.c.log2p);
+    if (columns < 0) atomicOr(a.status, kStatusBounds);
+    if (columns <= 0) return 0;
+    s.len -= columns << a.c.log2p;
+    return columns;
 }
 
 // a / b for non-negative a and positive b, in 32 bits where they fit.

@@ -64,6 +64,7 @@ static_assert(kMaxCtas <= kCntPages, "counters overlap");
 static_assert(int64_t(kMaxCtas) * 2 * kPartFloats * 4 <= kWsSlots - kWsPart, "partials meet a prefix's results");
 
 constexpr int kUncut = 6;    // tiles that the longest sequence may be above a CTA's share and stay whole
+constexpr int kBehind = INT_MIN;  // bit of a sequence's number of rows: it lies behind a prefix
 constexpr int kMasked = 0x7FABCDEF;  // a NaN that no arithmetic gives: the score of a token that a row does not see
 
 // What the template arguments fix: DC chunks of 64 dims.
@@ -173,7 +174,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     int64_t* orow = reinterpret_cast<int64_t*>(smem + F::off_rows(QP));  // [RU] output rows, -1 past the last
     int* limits = reinterpret_cast<int*>(orow + RU);                      // [RU] tokens that a row sees
     int64_t* pre = reinterpret_cast<int64_t*>(smem + F::off_pre(QP));  // [batch + 1]
-    int2* seqs = reinterpret_cast<int2*>(pre + a.batch + 1);              // [batch] rows, length
+    int2* seqs = reinterpret_cast<int2*>(pre + a.batch + 1);              // [batch] rows (SHARED: with kBehind), length
     __shared__ int64_t warp_sum[4];
     __shared__ int warp_most[4];
     __shared__ int last_flag;
@@ -195,13 +196,14 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
     bool dead = false;  // a wait of this lane gave up: none follows, and no copy if it is lane 0, which issues them
 
     // ---- the line: prefix sums of the sequences' tiles (`whole`: of their blocks for all heads)
-    auto units_of = [&](int2 q, bool whole) {  // rows, length
-        const int64_t blocks = (static_cast<int64_t>(q.x) * a.group + RU - 1) / RU;
+    auto rows_of = [](int2 q) { return SHARED ? q.x & ~kBehind : q.x; };
+    auto units_of = [&](int2 q, bool whole) {
+        const int64_t blocks = (static_cast<int64_t>(rows_of(q)) * a.group + RU - 1) / RU;
         return blocks * c.heads * (whole ? 1 : max(1, (q.y + kTile - 1) / kTile));
     };
     auto read = [&](int b) {
         Seq s = sequence(a, b);
-        if (SHARED) shared_columns(a, b, s);
+        if (SHARED && shared_columns(a, b, s) > 0) s.n |= kBehind;
         return make_int2(s.n, s.len);
     };
     auto measure = [&](bool known, bool whole) {
@@ -272,15 +274,11 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         }
         // empty sequences share their successor's prefix: take the last with pre <= u that has tiles
         const int b = lo;
-        const Seq sq = {seqs[b].x, seqs[b].y};
+        const Seq sq = {rows_of(seqs[b]), seqs[b].y};
         const int64_t row0 = a.starts ? a.starts[b] : b;
         const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
-        bool behind = false;  // a prefix
-        if (SHARED) {
-            const int skip = a.skip[b];
-            behind = skip > 0 && a.lens[b] - skip == sq.len;
-            if (behind) row_table += skip >> c.log2p;
-        }
+        const bool behind = SHARED && seqs[b].x < 0;  // as read() found: it has left the columns shared out of the length
+        if (behind) row_table += a.skip[b] >> c.log2p;
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];

@@ -189,6 +189,44 @@ def test_shared_bad_plans_are_reported(kv, ws):  # noqa: F811
         close(out[3:], None, tuple(x[3:] for x in ref), max(lens) + 512, torch.float32)
 
 
+def beyond_the_table(kv):  # noqa: F811
+    """A batch whose second sequence has a page in every column; its lengths as they are, and with that one the table's."""
+    cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    width = table.shape[1]
+    table[1, 20:] = torch.arange(width - 20, device="cuda").int() % cache.pages
+    return cache, table, lens, borders, 16 * width, [*lens[:1], 16 * width, *lens[2:]]
+
+
+def test_shared_length_beyond_the_table(kv, ws):  # noqa: F811
+    """It counts as the table, and the tokens shared are read once: by the prefix, not again and not instead of others."""
+    cache, table, lens, borders, most, held = beyond_the_table(kv)
+    q = torch.randn((8, 8, 64), device="cuda")
+    plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+    ref = attention_ref(cache, 0, q, table, held, list(range(9)), 1 / 8)
+    for more in (1, 16, 320, 5 * most):
+        beyond = list(lens)
+        beyond[1] = most + more
+        out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(beyond), plan, return_lse=True, workspace=ws)
+        assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+        close(out, lse, ref, most + 512, torch.float32)
+
+
+def test_shared_length_and_plan_beyond_the_table(kv, ws):  # noqa: F811
+    """An entry beyond the table too, by as much as the length among them: it counts as nothing shared."""
+    cache, table, lens, borders, most, held = beyond_the_table(kv)
+    q = torch.randn((8, 8, 64), device="cuda")
+    good = kv.kv_share(cache, table, i32(lens), i32(borders))
+    ref = attention_ref(cache, 0, q, table, held, list(range(9)), 1 / 8)
+    for skip in (most + 16, 2 * most, 1 << 20):
+        for more in (skip, skip + 16, skip - 16):
+            beyond, plan = list(lens), good.clone()
+            beyond[1] = most + more
+            plan[9] = skip
+            out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(beyond), plan, return_lse=True, workspace=ws)
+            assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+            close(out, lse, ref, most + 512, torch.float32)
+
+
 def test_shared_bad_pages_are_reported_and_masked(kv, ws):  # noqa: F811
     """A plan made before its pages were lost: they count as masked in all rows."""
     cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1])], 2, 64, 16, "e4m3", "hnd")
