@@ -27,7 +27,7 @@ struct AttnArgs {
     const int32_t* skip;
     int ngroups;
     float* own;      // [rows][q_heads][dim], normalised, of a row's first piece
-    float4* own_ml;  // [rows][q_heads] its reference and sum, the CTA of the next, their number and row
+    float4* own_ml;  // [rows][q_heads] its reference and sum, the CTA of the next and their row, their number and its group
     float* slots;    // [CTA][slot_rows][slot_dims], then [slot_rows] references and sums, of further pieces
     int slot_rows, slot_dims;
 };
@@ -56,15 +56,18 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
 }
 
 // Entries of a plan that do not fit the call count as nothing shared (kStatusBounds).
-// A group: n rows from row0 on, whose tokens a table row has.
+// A group: n rows from row0 on, whose tokens a table row has.  Groups' rows rise: one that begins among those of
+// the group before counts as nothing shared, so that two groups never write the results of one row.
 struct SharedGroup {
     int row0, n, tokens, table_row;
 };
-__device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int b) {
-    const int4 g = a.groups[b];  // first row, rows, tokens, first sequence
-    const bool good = g.x >= 0 && g.y >= 0 && static_cast<int64_t>(g.x) + g.y <= a.rows && g.z >= 0 &&
-                      g.z <= a.width << a.c.log2p && (g.z & ((1 << a.c.log2p) - 1)) == 0 &&
-                      (g.z == 0 || (g.w >= 0 && g.w < a.batch));
+__device__ __forceinline__ bool group_fits(const AttnArgs& a, int4 g) {  // first row, rows, tokens, first sequence
+    return g.x >= 0 && g.y >= 0 && static_cast<int64_t>(g.x) + g.y <= a.rows && g.z >= 0 && g.z <= a.width << a.c.log2p &&
+           (g.z & ((1 << a.c.log2p) - 1)) == 0 && (g.z == 0 || (g.w >= 0 && g.w < a.batch));
+}
+__device__ __forceinline__ int4 group_before(const AttnArgs& a, int b) { return b > 0 ? a.groups[b - 1] : make_int4(0, 0, 0, 0); }
+__device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int4 g, int4 before) {
+    const bool good = group_fits(a, g) && (g.y == 0 || !group_fits(a, before) || g.x >= before.x + before.y);
     if (!good) atomicOr(a.status, kStatusBounds);
     return good && g.y > 0 && g.z > 0 ? SharedGroup{g.x, g.y, g.z, g.w} : SharedGroup{0, 0, 0, 0};
 }

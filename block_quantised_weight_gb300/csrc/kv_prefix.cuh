@@ -36,7 +36,7 @@
 // have one (a piece costs as much as some steps before its first and behind its
 // last), and the parts are one line, cut evenly among the CTAs.  A piece that begins a unit
 // leaves its result for each row, the others in a slot of their CTA; the row
-// kernel adds them to what lies behind the prefix (own_ml of a row names the CTA of
+// kernel adds them to what lies behind the prefix (own_ml of a row names its group, the CTA of
 // the first further piece and their number).
 //
 // Roles: sixteen warps for the softmax (a set of four has the keys, and 16 columns),
@@ -102,7 +102,7 @@ struct XShape {
 struct PrefixPiece {
     int row0, nrows, h, row_first, nc, table_row, j0, j1;
     int slot;   // -1: begins its unit
-    int extra;  // further pieces of a unit that this one begins
+    int extra;  // further pieces of a unit that this one begins, its group << 16
     int tokens; // of the prefix; < 0: no more pieces
 };
 
@@ -133,7 +133,8 @@ struct PartWalk {
     __device__ void load(const AttnArgs& a, int from) {
         b0 = from;
         g = SharedGroup{};
-        if (b0 + (threadIdx.x & 31) < a.ngroups) g = shared_group(a, b0 + (threadIdx.x & 31));
+        const int b = b0 + static_cast<int>(threadIdx.x & 31);
+        if (b < a.ngroups) g = shared_group(a, a.groups[b], group_before(a, b));
         u = units_of<NMAX>(a, g);
     }
     // Steps of the 32 groups loaded.  Every CTA gets the same value from the same operations.
@@ -181,6 +182,7 @@ struct PartWalk {
         w.nrows = __shfl_sync(~0u, g.n, which) * a.group;
         w.tokens = __shfl_sync(~0u, g.tokens, which);
         w.table_row = __shfl_sync(~0u, g.table_row, which);
+        w.extra = b0 + which << 16;
         const int per = __shfl_sync(~0u, u.per, which), blocks = __shfl_sync(~0u, u.blocks, which);
         steps_of = __shfl_sync(~0u, u.steps, which), parts = __shfl_sync(~0u, u.parts, which);
         const int below = __shfl_sync(~0u, upto, which ? which - 1 : 0);
@@ -523,7 +525,7 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                 w.j0 = static_cast<int>(div64(static_cast<int64_t>(steps) * in, parts));
                 w.j1 = static_cast<int>(div64(static_cast<int64_t>(steps) * last, parts));
                 w.slot = in == 0 ? -1 : static_cast<int>(blockIdx.x);
-                w.extra = in == 0 ? line.of(at + parts - 1) - static_cast<int>(blockIdx.x) : 0;
+                if (in == 0) w.extra |= line.of(at + parts - 1) - static_cast<int>(blockIdx.x);
                 at += last - in;
             } else {
                 w.tokens = -1;
@@ -968,8 +970,8 @@ qg_attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap
                     const float total = none ? 0.f : sum * pow2i(-order_z(cols.refd[col]));
                     if (begins) {
                         if (cols.orow[col] >= 0)
-                            a.own_ml[cols.orow[col]] = make_float4(m, total, __int_as_float(static_cast<int>(blockIdx.x) + 1),
-                                                                   __int_as_float(w.extra | col << 16));
+                            a.own_ml[cols.orow[col]] = make_float4(m, total, __int_as_float((static_cast<int>(blockIdx.x) + 1) | col << 16),
+                                                                   __int_as_float(w.extra));
                     } else {
                         *reinterpret_cast<float2*>(part + NMAX * DP + 2 * col) = make_float2(m, total);
                     }

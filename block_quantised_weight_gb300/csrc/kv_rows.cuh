@@ -91,17 +91,19 @@ struct Shape {
 
 // Adds a prefix's results to those of a row's own tokens: `top` its reference
 // (-inf: no token), `sum` and the normalised dims of this lane.  The launch that wrote
-// them has ended (griddepcontrol.wait).
+// them has ended (griddepcontrol.wait).  They are that launch's where the group that they name has this row
+// and the `skip` tokens of its sequence, for the launch writes every row of such a group; where a plan's entries
+// disagree they can be those of a call before (kStatusBounds).
 template <int XV>
-__device__ __forceinline__ void join_prefix(const AttnArgs& a, int64_t to, int row_lane, float& top, float& sum, float4 (&acc)[XV]) {
+__device__ __forceinline__ void join_prefix(const AttnArgs& a, int64_t to, int skip, int row_lane, float& top, float& sum, float4 (&acc)[XV]) {
     grid_dependency_wait();
     const float4 first = __ldcg(a.own_ml + to);
-    const int cta = __float_as_int(first.z), row = __float_as_int(first.w) >> 16;
+    const int cta = __float_as_int(first.z) & 0xFFFF, row = __float_as_int(first.z) >> 16;
+    const int group = __float_as_int(first.w) >> 16;
     int more = __float_as_int(first.w) & 0xFFFF;
-    if (cta < 1 || more > kMaxPrefixCtas - cta || row < 0 || row >= a.slot_rows) {  // no plan of this call
-        if (more) atomicOr(a.status, kStatusBounds);
-        more = 0;
-    }
+    bool good = cta >= 1 && more <= kMaxPrefixCtas - cta && row >= 0 && row < a.slot_rows && group >= 0 && group < a.ngroups;
+    if (!good) more = 0;
+    const int4 entry = a.groups[good ? group : 0], before = group_before(a, good ? group : 0);
     const int64_t stride = static_cast<int64_t>(a.slot_rows) * (a.slot_dims + 2);
     const float* parts = a.slots + (more ? cta * stride + static_cast<int64_t>(row) * a.slot_dims : 0);
     const float2* ml = reinterpret_cast<const float2*>(a.slots + (more ? cta * stride + static_cast<int64_t>(a.slot_rows) * a.slot_dims : 0)) + row;
@@ -118,6 +120,10 @@ __device__ __forceinline__ void join_prefix(const AttnArgs& a, int64_t to, int r
         o[x] = make_float4(mine * acc[x].x + theirs * v.x, mine * acc[x].y + theirs * v.y, mine * acc[x].z + theirs * v.z,
                            mine * acc[x].w + theirs * v.w);
     }
+    const SharedGroup g = shared_group(a, entry, before);
+    const int64_t in = to - static_cast<int64_t>(g.row0) * a.q_heads;
+    good = good && g.tokens == skip && in >= 0 && in < static_cast<int64_t>(g.n) * a.q_heads;
+    if (!good && row_lane == 0) atomicOr(a.status, kStatusBounds);
     // further parts, as many at once as their reads fit
     constexpr int N = 8 / XV;
     for (int i0 = 0; i0 < more; i0 += N) {
@@ -277,8 +283,8 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
         const Seq sq = {rows_of(seqs[b]), seqs[b].y};
         const int64_t row0 = a.starts ? a.starts[b] : b;
         const int32_t* row_table = a.table + static_cast<int64_t>(b) * a.width;
-        const bool behind = SHARED && seqs[b].x < 0;  // as read() found: it has left the columns shared out of the length
-        if (behind) row_table += a.skip[b] >> c.log2p;
+        const int skip = SHARED && seqs[b].x < 0 ? a.skip[b] : 0;  // as read() found: it has left them out of the length
+        if (SHARED) row_table += skip >> c.log2p;
         const int tiles = max(1, (sq.len + kTile - 1) / kTile);
         const int blocks = static_cast<int>((static_cast<int64_t>(sq.n) * a.group + RU - 1) / RU);
         const int64_t in = u - pre[b];
@@ -791,7 +797,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
                 }
                 acc[x2].x *= inv, acc[x2].y *= inv, acc[x2].z *= inv, acc[x2].w *= inv;
             }
-            if (SHARED && whole && behind) join_prefix<XV>(a, to, row_lane, top, sum, acc);
+            if (SHARED && whole && skip) join_prefix<XV>(a, to, skip, row_lane, top, sum, acc);
 #pragma unroll
             for (int x2 = 0; x2 < XV; ++x2) {
                 const int d = 4 * (row_lane + 32 * x2);
@@ -886,7 +892,7 @@ qg_attn_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, 
 #pragma unroll
                     for (int x2 = 0; x2 < XV; ++x2)
                         acc[x2].x *= inv, acc[x2].y *= inv, acc[x2].z *= inv, acc[x2].w *= inv;
-                    if (SHARED && behind && live) join_prefix<XV>(a, to[i], row_lane, join_top, sum, acc);
+                    if (SHARED && skip && live) join_prefix<XV>(a, to[i], skip, row_lane, join_top, sum, acc);
 #pragma unroll
                     for (int x2 = 0; x2 < XV; ++x2) {
                         const int d = 4 * (row_lane + 32 * x2);

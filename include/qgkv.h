@@ -167,10 +167,12 @@ QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int6
 
 /* qgkv_attention of a batch whose groups share tokens: the pages shared are read
  * once for all rows of a group, and the results joined with those of the tokens
- * behind them.  plan: what qgkv_share wrote for the same table, lens and starts;
- * an entry that does not fit them counts as nothing shared (QG_EBOUNDS, and the
- * rows of its group are not valid).  Results are those of qgkv_attention to within
- * its numerics, but for what small weights and scales of V keep among the tokens
+ * behind them.  plan: what qgkv_share wrote for the same table, lens and starts.
+ * QG_EBOUNDS reports entries out of range, groups that begin among the rows of the
+ * one before, and sequences that share tokens without a group of their rows that
+ * shares as many; the rows of such groups and sequences are not valid.  That a
+ * group's sequences still hold the same pages is not looked at again.  Results are
+ * those of qgkv_attention to within its numerics, but for what small weights and scales of V keep among the tokens
  * shared: bf16 q to within 2^-28 of the row's largest weight, other types 2^-39; full
  * precision for scales of V of 2^-80 to 2^90 (qgkv_append writes none outside for
  * values of 2^-70 to 2^97).  Where sharing gains nothing each sequence reads all its

@@ -189,6 +189,32 @@ def test_shared_bad_plans_are_reported(kv, ws):  # noqa: F811
         close(out[3:], None, tuple(x[3:] for x in ref), max(lens) + 512, torch.float32)
 
 
+@pytest.mark.parametrize("change, wrong", [({1: 2}, [2]), ({1: 0}, [0, 1, 2]), ({0: 1, 1: 2}, [0]), ({2: 304}, [0, 1, 2]), ({2: 0}, [0, 1, 2]),
+                                           ({8: 304}, [0]), ({9: 16, 10: 160}, [1, 2]), ({0: 3, 1: 2}, [0, 1, 2, 3, 4]), ({1: 5}, [3, 4]),
+                                           ({4: 0, 5: 5}, [3, 4]), ({5: 1}, [4]), ({13: 16}, [5])], ids=str)
+def test_shared_plans_that_disagree_are_reported(kv, ws, change, wrong):  # noqa: F811
+    """Entries in range of which groups and sequences say different things, behind a call that left results for every
+    row of them: rows whose entries agree are right."""
+    cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
+    lens[5:], n = [40] * 3, len(lens)  # sequences of no group, which could share two pages
+    table[5:, :3] = table[0, :3]
+    q = torch.randn((n, 8, 64), device="cuda")
+    good = kv.kv_share(cache, table, i32(lens), i32(borders))
+    assert good.tolist() == [0, 3, 320, 0, 3, 2, 400, 3, 320, 320, 320, 400, 400, 0, 0, 0]
+    others = kv.kv_share(cache, table, i32(lens), i32([5, 8]))
+    assert others.tolist() == [5, 3, 32, 5] + [0] * 5 + [32] * 3
+    for plan in (others, good):
+        kv.kv_attention_shared(cache, 1, q, table, i32(lens), plan, workspace=ws)
+    assert qgemv.qg_device_status() == qgemv.QG_OK
+    plan, right = good.clone(), [b for b in range(n) if b not in wrong]
+    for at, value in change.items():
+        plan[at] = value
+    out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    assert qgemv.qg_device_status() == qgemv.QG_EBOUNDS
+    ref = attention_ref(cache, 0, q, table, lens, list(range(n + 1)), 1 / 8)
+    close(out[right], lse[right], tuple(x[right] for x in ref), max(lens) + 512, torch.float32)
+
+
 def beyond_the_table(kv):  # noqa: F811
     """A batch whose second sequence has a page in every column; its lengths as they are, and with that one the table's."""
     cache, table, lens, borders = shared_table(kv, [(320, [3, 9, 1]), (400, [5, 5])], 2, 64, 16, "e4m3", "hnd")
