@@ -114,6 +114,33 @@ def test_append_rotary_query_heads(kv, q_heads):  # noqa: F811
     check(kv, [5, 0], [3, 20], q_heads, 1, 64, 64, 16, "e4m3", "hnd", "f32", "interleaved")
 
 
+@pytest.mark.parametrize("q_heads", [7, 17, 40])
+@pytest.mark.parametrize("dtype, dim, part", [("bf16", 128, 128), ("f32", 64, 48), ("f16", 96, 32)])
+def test_append_rotary_query_heads_of_many_tokens(kv, q_heads, dtype, dim, part):  # noqa: F811
+    """Blocks on both sides of a CTA for each SM at 2, 4, 8 and 16 heads a CTA, the last of them with fewer heads; more
+    heads than a thread has on their way at once."""
+    for n in (20, 40, 170):
+        check(kv, [3 + i % 40 for i in range(n)], [1] * n, q_heads, 1, dim, part, 16, "e4m3", "hnd", dtype, "halves", seed=n)
+    for n in (7, 18, 90):
+        check(kv, [3 + i % 40 for i in range(n)], [2 + i % 19 for i in range(n)], q_heads, 1, dim, part, 16, "int8", "nhd", dtype,
+              "interleaved", seed=n)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("q_heads", [17, 40])
+def test_append_rotary_of_many_tokens_in_place(kv, q_heads, rows):  # noqa: F811
+    n = 170
+    lens, st = [i % 50 for i in range(n)], [rows * i for i in range(n + 1)]
+    cache, table, _ = make(kv, [x + rows for x in lens], 1, 128, 16, "e4m3", "hnd")
+    q, k, v = parts(st[-1], q_heads, 1, 128, "bf16")
+    q, rope = q.contiguous(), kv.rotary_table(64, 128)
+    pos = torch.cat([torch.arange(x, x + rows) for x in lens]).cuda()
+    want = turned(q, rope, pos, "halves").to(q.dtype)
+    starts = None if rows == 1 else i32(st)
+    assert kv.kv_append_rotary(cache, 0, q, k, v, rope, table, i32(lens), starts=starts, pairs="halves", out=q) is q
+    assert torch.equal(q, want)
+
+
 def test_append_rotary_of_many_sequences(kv):  # noqa: F811
     g = np.random.default_rng(3)
     rows = [int(x) for x in g.integers(0, 40, 75) * (g.random(75) < 0.6)]
