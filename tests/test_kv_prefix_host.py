@@ -47,3 +47,12 @@ def test_copies_in_flight_are_waited_for():
     at = src.index("if (dead) {")
     for ring in ("kraw_full", "vraw_full"):
         assert f"(void)mbar_wait_bounded({ring}" in src[at:at + 900]
+
+
+def test_the_checks_above_find_what_they_check():
+    """Each of the searches above meets the sources' calls: a renamed helper is not passed over."""
+    src = source("kv_prefix.cuh")
+    assert len(re.findall(r"[^;{}]*\bmbar_wait_bounded\([^;]*;", src)) == 3
+    assert len(re.findall(r"[^;{}]*\bwait_on\([^;{]*[;{]", src)) == 2
+    assert src.count("mbar_arrive_expect_tx") == 1
+    assert src.count("mbar_try_wait") == 2  # tried once each: in wait() and ahead of a step
