@@ -365,6 +365,25 @@ def test_shared_scales_of_all_sizes(kv, ws, dtype, dim, members):  # noqa: F811
     close(out, lse, small((*ref[:4], ref[4] * 2.0 ** 4), dtype), max(lens) + 512, DT[dtype], one_part=dtype == "bf16")
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim, members", [(64, 3), (128, 40), (256, 5)])
+def test_shared_scales_of_all_sizes_to_the_stated_cut(kv, ws, dtype, dim, members, fmt):  # noqa: F811
+    """As above, to the cut of small weights that the module's tolerance counts and no more."""
+    for seed in range(4):
+        cache, table, lens, borders = shared_table(kv, [(500, [1 + 3 * i % 40 for i in range(members)])], 2, dim, 16, fmt, "hnd", seed=seed)
+        g = torch.Generator(device="cuda").manual_seed(dim + seed)
+        cache.v_scale.copy_(torch.exp2(torch.randint(-40, -3, cache.v_scale.shape, device="cuda", generator=g).float()))
+        cache.v_scale[0, ::7] = 0.0
+        cache.k_scale[0, ::11] = 0.0
+        cache.v_scale[0, table[0, 3]] = 0.0
+        q = torch.randn((len(lens), 8, dim), device="cuda", generator=g).to(DT[dtype])
+        plan = kv.kv_share(cache, table, i32(lens), i32(borders))
+        out, lse = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+        ref = attention_ref(cache, 0, q, table, lens, list(range(len(lens) + 1)), 1 / math.sqrt(dim))
+        close(out, lse, small(ref, dtype), max(lens) + 512, DT[dtype], one_part=dtype == "bf16")
+
+
 def test_shared_prefix_below_and_above_the_rest(kv, ws):  # noqa: F811
     """The prefix's scores lie 300 binary orders below those behind it, or above: one part's weight is 0."""
     from test_kv_edges_gpu import code
