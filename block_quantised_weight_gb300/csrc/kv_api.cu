@@ -154,13 +154,15 @@ int launch_attention(const qg::AttnArgs& a, bool int8, cudaStream_t stream) {
     return many_rows(a) ? qg::launch_attn_prompt(a, int8, stream) : qg::launch_attn_rows(a, int8, stream);
 }
 
-// The most bytes of pages that a plan can save, by the table's width, have to be
-// worth a second kernel and the join.  Shared / each for itself, us:
+// The pages that sequences read beside the first, at most by the table's width, have to be
+// worth a second kernel and the join (more than a plan saves where there are several groups, each of which
+// reads its prefix once).  Shared / each for itself, us:
 //   4 beams of 820 tokens, 4 heads of 64 (1.3 MB): 13.6 / 8.2
 //   4 of 1080, 8 heads of 128 (6.7 MB): 15.0 / 10.8;  8 groups of 4 of 1060, 4 heads of 64 (17 MB): 15.7 / 14.2
 //   4 of 4160, 8 heads of 128 (26 MB): 16.3 / 18.2;  48 of 1320 (130 MB): 26 / 27;  48 of 8800 (850 MB): 42 / 97
 // Widths are all that the host knows: behind a table much wider than its
-// sequences a small plan is followed all the same.  Nor does the prefix kernel read as
+// sequences a small plan is followed all the same.  And of the groups it knows their number: one large group
+// beside many of one sequence does not share (the header says how to pass them).  Nor does the prefix kernel read as
 // fast as the row kernel, for a step takes it as long for few rows as for 64: with 16 groups
 // behind up to 6000 tokens, bf16, of 2 / 3 / 4 / 6 sequences, shared 57 / 57 / 65 / 70, each for itself 35 / 47 / 58 /
 // 81 (8 heads of 64), 67 / 69 / 78 / 85 and 47 / 63 / 77 / 109 (of 128), 77 / 78 / 81 / 94 and 51 / 66 / 84 / 116 (4 of 256).

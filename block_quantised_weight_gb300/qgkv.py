@@ -342,7 +342,11 @@ def kv_share(cache, table, lens, groups, starts=None, rows=None, out=None, strea
     the plan, int32 [4 n + batch]: (first row, rows, tokens shared, first sequence) of each group, then the
     tokens that each sequence shares.  It is read and made on the device, once for all layers of a step.
     rows: the number of query rows; where None, and with starts, rows outside the queries are first found by
-    the attention."""
+    the attention.
+
+    A group shares what all its sequences have in common, so a short one, or one that left the prompt, sets it for
+    the others.  A batch of fewer than four sequences to a group shares nothing: leave sequences of their own before
+    the first border or behind the last, not as groups of one."""
     if stream is not None and _other(stream, cache, table, lens, groups, starts, out):
         with torch.cuda.stream(stream):
             return kv_share(cache, table, lens, groups, starts, rows, out)

@@ -160,7 +160,11 @@ QG_API int qgkv_attention(const qgkv_cache* cache, int64_t layer, const void* q,
  * plan, int32 [4 * ngroups + batch], gets for each group (first row, rows, tokens
  * shared, first sequence) and then for each sequence the tokens that it shares.
  * One plan serves all layers of a step.  Borders that do not rise or leave the
- * batch: nothing is shared (QG_EBOUNDS). */
+ * batch: nothing is shared (QG_EBOUNDS).
+ * A group shares what all its sequences with rows have in common: a short one, or
+ * one that has left the prompt, sets it for all.  Sequences that share nothing are
+ * best left before the first border or behind the last: as groups of their own, or
+ * spread among others, they count against sharing (qgkv_attention_shared). */
 QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int64_t table_width, const int32_t* lens,
                       const int32_t* starts, int64_t rows, int batch, const int32_t* groups, int ngroups,
                       int32_t* plan, cudaStream_t stream);
@@ -175,10 +179,13 @@ QG_API int qgkv_share(int64_t pages, int page_tokens, const int32_t* table, int6
  * those of qgkv_attention to within its numerics, but for what small weights and scales of V keep among the tokens
  * shared: bf16 q to within 2^-28 of the row's largest weight, other types 2^-39; full
  * precision for scales of V of 2^-80 to 2^90 (qgkv_append writes none outside for
- * values of 2^-70 to 2^97).  Where sharing gains nothing each sequence reads all its
- * tokens itself and the plan is not read: the table's width times its sequences come
- * to less than 16 MB of pages, fewer than four sequences of the batch to a group,
- * many rows a sequence, or more results to join than the workspace holds.  The choice depends on the call's sizes alone. */
+ * values of 2^-70 to 2^97).
+ * The sizes of a call alone decide whether it shares; where it does not, each
+ * sequence reads all its tokens itself and the plan is not read.  It does not where
+ * the columns of all sequences but one come to less than 16 MB of pages, where the
+ * batch has fewer than four sequences for each of ngroups (a group of one counts as
+ * a group), where sequences have many rows, or where there are more results to join
+ * than the workspace holds. */
 QG_API int qgkv_attention_shared(const qgkv_cache* cache, int64_t layer, const void* q, void* out, float* lse, int type,
                                  int64_t rows, int q_heads, int64_t row_stride, int64_t head_stride,
                                  const int32_t* table, int64_t table_width, const int32_t* lens,

@@ -527,6 +527,23 @@ def test_shared_from_four_sequences_a_group_on(kv, ws, members, shared):  # noqa
     close(*got, attention_ref(cache, 0, q, table, lens, list(range(len(lens) + 1)), 1 / 8), max(lens) + 512, torch.float32)
 
 
+@pytest.mark.parametrize("alone", ["in groups", "behind the groups"])
+def test_shared_beside_sequences_that_share_nothing(kv, ws, alone):  # noqa: F811
+    """Twelve sequences behind a prompt and five of their own: with a group for each of the five the call has too few
+    sequences a group to share; where the borders leave them out it shares."""
+    lens = [643 + i for i in range(12)] + [50 + i for i in range(5)]
+    n = len(lens)
+    cache, table, _ = make(kv, lens, 2, 64, 16, "e4m3", "hnd", width=least_width(n, 2, 64, 16))
+    table[:12, :40] = table[0, :40].clone()
+    q = torch.randn((n, 8, 64), device="cuda")
+    plan = kv.kv_share(cache, table, i32(lens), i32([0, 12, 13, 14, 15, 16, 17] if alone == "in groups" else [0, 12]))
+    assert plan[2] == 640
+    got = kv.kv_attention_shared(cache, 0, q, table, i32(lens), plan, return_lse=True, workspace=ws)
+    plain = kv.kv_attention(cache, 0, q, table, i32(lens), return_lse=True, workspace=ws)
+    assert torch.equal(got[1], plain[1]) == (alone == "in groups")
+    close(*got, attention_ref(cache, 0, q, table, lens, list(range(n + 1)), 1 / 8), max(lens) + 512, torch.float32)
+
+
 @pytest.mark.parametrize("rows, shared", [(31, True), (32, False)])
 def test_shared_up_to_many_rows(kv, ws, rows, shared):  # noqa: F811
     """128 query rows a sequence of 80 go to the kernel of prompts, which shares nothing."""
