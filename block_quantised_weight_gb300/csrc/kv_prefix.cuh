@@ -21,14 +21,16 @@
 // 2^11 times what the first leaves, with sums of its own, so that small weights keep
 // their bits down to 2^-40 of a row's largest (one part: 2^-29).
 //
-// Bound.  For few rows the stream of codes; for 64 a step's traffic of shared memory: the
-// copies, reading and writing of the codes and both products' operands move 190 KB a step at
-// 128 dims, 1500 clocks, and the warps' waits for one another.  Short calls are bound by the chain
+// Bound.  The chain of a step's softmax (scores out of tensor memory, the vote, weights to shared memory): 2000 of 2800
+// clocks at 64 rows of 128 dims, in a profile with the tensor pipe busy for 11 % of the time, DRAM for 14 % and 41 % of
+// the issue slots.  Copies, codes and both products' operands move 190 KB of shared memory a step, 1500 clocks by
+// its width, beside it.  Steps of fewer rows take as long.  832 threads leave 72 registers, at which all forms spill: 24 to
+// 72 bytes of stores a thread up to 128 dims, 72 (bf16 q) to 528 (fp32) above.  Short calls are bound by the chain
 // plan -> table -> codes -> first step, and by the parts that are left to join.
 //
 // Measured (GB300, us a layer with the rows behind the prefix; each for itself in brackets): 48 sequences of 600
-// tokens behind 8200, 32 / 8 heads of 128, e4m3: bf16 42 (98), fp16 44 (106), fp32 46 (113), int8 codes 55 (149); 8 of
-// them 21 (28), 128 of them 101 (237); 32 behind two prefixes of 65536, int8: 106 (576).  About 6 us to a CTA's first
+// tokens behind 8200, 32 / 8 heads of 128, e4m3: bf16 43 (97), fp16 45 (105), fp32 47 (113), int8 codes 55 (149); 8 of
+// them 20 (28), 128 of them 101 (237); 32 behind two prefixes of 65536, int8: 103 (575).  About 6 us to a CTA's first
 // step, 1.5 a step of 64 rows, 2 behind the last.  With K as f16 in shared memory and eight softmax
 // warps the first of them took 51 where it then took 46.
 //

@@ -253,8 +253,8 @@ QG_API int qgbeam_select(const void* logits, int type, const float* cum, int req
  * selection.  For token t of row r, with its logit x in fp32 and every operation
  * rounded to fp32, in this order and each where its argument is not null:
  *   history   int32 [rows][width], the row's first lens[r] tokens, of which the
- *             first prompt_lens[r] (null: none) were given and the others
- *             produced:
+ *             first prompt_lens[r] (null: none; below 0 none, beyond lens[r] all)
+ *             were given and the others produced:
  *     x = x > 0 ? x / repetition[r] : x * repetition[r]  if t is in it;
  *     x = x - frequency[r] * n;  x = x - presence[r]     if t was produced n > 0 times;
  *   bias      x = x + bias[r][i] for the last i with bias_tokens[r][i] = t
@@ -267,7 +267,7 @@ QG_API int qgbeam_select(const void* logits, int type, const float* cum, int req
  * Tokens outside [0, vocab) in history and bias_tokens are passed over.  out: of
  * `type` or fp32, rows out_stride elements apart; it may be `logits` itself (of
  * the same type and stride), and then, without a temperature, only the logits that
- * change are touched.  A length outside [0, width] is cut to it, and a mask
+ * change are touched.  A lens[r] outside [0, width] is cut to it, and a mask
  * number outside [-1, masks) counts as -1 (QG_EBOUNDS). */
 QG_API int qglogits_adjust(const void* logits, int type, int64_t rows, int64_t vocab, int64_t row_stride, void* out,
                            int out_type, int64_t out_stride, const int32_t* history, int64_t width,
